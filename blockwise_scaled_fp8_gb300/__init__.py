@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -28,6 +29,8 @@ EXPORTS = [
     "bfp8_quant_dual_weight", "bfp8_mx_cast", "bfp8_linear_step_host_workspace_size",
     "bfp8_linear_step_host", "bfp8_moe_step_host_workspace_size", "bfp8_moe_step_host",
     "bfp8_gemm_1x128_128x128_xq", "bfp8_gemm_1x128_128x1_xq",
+    "bfp8_moe_route", "bfp8_moe_route_bwd", "bfp8_moe_plan_rows", "bfp8_moe_plan", "bfp8_moe_dispatch",
+    "bfp8_moe_combine", "bfp8_moe_combine_bwd", "bfp8_gemm_routed_1x128_128x128",
 ]
 
 _lib = None
@@ -91,10 +94,22 @@ def lib() -> ctypes.CDLL:
     L.bfp8_gemm_grouped_1x128_128x1.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64,
                                                 i64, i64, i64, vp]
     L.bfp8_debug_gemm_stall.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, vp]
+    f32 = ctypes.c_float
+    L.bfp8_moe_route.argtypes = [vp, i32, i64, i64, i64, vp, i64, i32, i64, i64, i32, i32, f32, vp, vp, vp]
+    L.bfp8_moe_route_bwd.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, i64, i32, i32, f32, vp, i64, vp]
+    L.bfp8_moe_plan_rows.argtypes = [i64, i64, i64, i64]
+    L.bfp8_moe_plan.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, i64, vp, vp]
+    L.bfp8_moe_dispatch.argtypes = [vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.bfp8_moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, vp, i64, vp]
+    L.bfp8_moe_combine_bwd.argtypes = [vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp]
+    L.bfp8_gemm_routed_1x128_128x128.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                                 i64, i64, i64, vp]
     for name in EXPORTS:
         if name not in ("bfp8_last_error", "bfp8_linear_workspace_size", "bfp8_linear_train_workspace_size",
-                        "bfp8_linear_step_host_workspace_size", "bfp8_moe_step_host_workspace_size"):
+                        "bfp8_linear_step_host_workspace_size", "bfp8_moe_step_host_workspace_size",
+                        "bfp8_moe_plan_rows"):
             getattr(L, name).restype = ctypes.c_int
+    L.bfp8_moe_plan_rows.restype = i64
     _lib = L
     return L
 
@@ -403,6 +418,207 @@ def moe_linear_bwd(dy, saved, offs, dx=None, dw=None):
     dx = gemm_grouped_1x128_128x128(qdy, sdy, qwt, sw, offs, K, N, sb_transposed=True, out=dx)
     dw = gemm_grouped_1x128_128x1(qdyt, sdyt, qxt, sxt, offs, M_total, out=dw)
     return dx, dw
+
+
+# ---------------------------------------------------------------------------
+# Routing to the experts.  A slot is a (token t, choice j) pair, flat index
+# t*k + j; sorted buffers have R rows, row[t, j] is a slot's row and src[r] a
+# row's slot (-1: none)
+# ---------------------------------------------------------------------------
+
+class MoePlan(NamedTuple):
+    """The slots sorted by expert (int32 device tensors): expert e owns rows
+    offs[e] .. offs[e+1], its counts[e] slots in slot order, then padding."""
+    offs: "torch.Tensor"    # [E+1]
+    row: "torch.Tensor"     # [T, k]
+    src: "torch.Tensor"     # [R]
+    counts: "torch.Tensor"  # [E]
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return _SCORES[score]
+
+
+def _need(t, name, dtype, shape):
+    """A contiguous CUDA tensor of that type and shape."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _need_logits(logits):
+    torch = _torch()
+    if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or not logits.is_cuda or \
+            (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be a 2-D CUDA bf16 or float32 tensor with unit column stride")
+    return logits.dtype == torch.float32
+
+
+def _ld(t):
+    """Row stride; of a single row the width (torch may report any stride there)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups=None, group_top: int = 1,
+              renormalize: bool = True, scale: float = 1.0):
+    """Each token's k experts and their weights: logits [T, E] bf16 or fp32 ->
+    (idx [T, k] int32, w [T, k] fp32); see bfp8_moe_route.  ``bias`` [E] fp32
+    joins the choice, not the weights; ``groups`` > 1 limits the choice to the
+    ``top_groups`` (default: all) groups whose ``group_top`` largest values sum
+    highest.  A logit of -inf, of its type's lowest value or NaN masks an
+    expert; idx is -1 (w 0) where none is left."""
+    torch = _torch()
+    f32 = _need_logits(logits)
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+    idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _check(lib().bfp8_moe_route(_p(logits), f32, T, E, _ld(logits), _p(bias), k, _score(score), groups,
+                                groups if top_groups is None else top_groups, group_top, renormalize, scale,
+                                _p(idx), _p(w), _stream()))
+    return idx, w
+
+
+def moe_route_bwd(logits, idx, w, dw, score: str = "softmax", renormalize: bool = True, scale: float = 1.0):
+    """Gradient of moe_route's weights: dw [T, k] fp32 -> dlogits [T, E] (the
+    logits' type), from the forward's logits, idx and w."""
+    torch = _torch()
+    f32 = _need_logits(logits)
+    T, E = logits.shape
+    k = idx.shape[-1]
+    _need(idx, "idx", torch.int32, (T, k))
+    _need(w, "w", torch.float32, (T, k))
+    _need(dw, "dw", torch.float32, (T, k))
+    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _check(lib().bfp8_moe_route_bwd(_p(logits), f32, T, E, _ld(logits), _p(idx), _p(w), _p(dw), k, _score(score),
+                                    renormalize, scale, _p(out), E, _stream()))
+    return out
+
+
+def moe_plan_rows(T: int, k: int, E: int, align: int = BLOCK) -> int:
+    """Rows that sorted buffers need for any choice of k experts by T tokens."""
+    rows = int(lib().bfp8_moe_plan_rows(T, k, E, align))
+    if rows < 0:
+        raise ValueError(f"moe_plan_rows: sizes out of range (T={T}, k={k}, E={E}, align={align})")
+    return rows
+
+
+def moe_plan(idx, E: int, align: int = BLOCK) -> MoePlan:
+    """Sorts the slots of idx [T, k] int32 by expert: each expert's rows start
+    on a multiple of ``align`` (128 for training, 1 for the routed product)."""
+    torch = _torch()
+    if idx.dim() != 2:
+        raise ValueError("idx must be a [T, k] tensor")
+    T, k = idx.shape
+    _need(idx, "idx", torch.int32, (T, k))
+    R = moe_plan_rows(T, k, E, align)
+    e = lambda *shape: torch.empty(shape, dtype=torch.int32, device=idx.device)
+    plan = MoePlan(offs=e(E + 1), row=e(T, k), src=e(R), counts=e(E))
+    _check(lib().bfp8_moe_plan(_p(idx), T, k, E, align, _p(plan.offs), _p(plan.row), _p(plan.src), R,
+                               _p(plan.counts), _stream()))
+    return plan
+
+
+def _need_plan(plan, T):
+    torch = _torch()
+    k = plan.row.shape[-1]
+    _need(plan.row, "plan.row", torch.int32, (T, k))
+    _need(plan.src, "plan.src", torch.int32, (plan.src.numel(),))
+    return k, plan.src.numel()
+
+
+def moe_dispatch(x, plan: MoePlan, weight=None, cols: bool = True):
+    """Gathers x [T, K] bf16 into the plan's rows, scaled by weight [T, k] fp32
+    where given, and quantises them in one pass: (q_row [R, ldq], s_row [Kb,
+    R], q_col [K, ldq'], s_col [Rb, lds]) as quant_dual of the gathered tensor
+    (q_col, s_col None without ``cols``).  Padding rows are zeros."""
+    torch = _torch()
+    _need_bf16_2d(x, "x")
+    T, K = x.shape
+    k, R = _need_plan(plan, T)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, (T, k))
+    dev = x.device
+    q = torch.empty((R, _rup(max(K, 1), 16)), dtype=torch.uint8, device=dev)
+    s = torch.empty((_cdiv(K, BLOCK), max(R, 1)), dtype=torch.float32, device=dev)
+    qc = sc = None
+    if cols:
+        qc = torch.empty((K, _rup(max(R, 1), 16)), dtype=torch.uint8, device=dev)
+        sc = torch.empty((_cdiv(R, BLOCK), _rup(max(K, 1), 4)), dtype=torch.float32, device=dev)
+    _check(lib().bfp8_moe_dispatch(_p(x), T, K, _ld(x), _p(plan.src), R, k, _p(weight), _p(q), _rup(max(K, 1), 16), _p(s),
+                                   max(R, 1), _p(qc), _rup(max(R, 1), 16) if cols else 0, _p(sc),
+                                   _rup(max(K, 1), 4) if cols else 0, _stream()))
+    return q, s, qc, sc
+
+
+def moe_combine(ye, plan: MoePlan, w=None, y=None):
+    """y[t] = sum_j w[t, j] ye[row[t, j]] (w None: 1, the gradient of the
+    dispatch): ye [R, N] bf16 -> y [T, N] bf16."""
+    torch = _torch()
+    _need_bf16_2d(ye, "ye")
+    T = plan.row.shape[0]
+    k, R = _need_plan(plan, T)
+    N = ye.shape[1]
+    if ye.shape[0] != R:
+        raise ValueError(f"ye has {ye.shape[0]} rows, the plan {R}")
+    if w is not None:
+        _need(w, "w", torch.float32, (T, k))
+    if y is None:
+        y = torch.empty((T, N), dtype=torch.bfloat16, device=ye.device)
+    else:
+        _need_bf16_2d(y, "y")
+        if tuple(y.shape) != (T, N):
+            raise ValueError(f"y must be {(T, N)}, got {tuple(y.shape)}")
+    _check(lib().bfp8_moe_combine(_p(ye), _ld(ye), R, _p(plan.row), _p(w), T, k, N, _p(y), _ld(y), _stream()))
+    return y
+
+
+def moe_combine_bwd(dy, ye, plan: MoePlan, w, with_dye: bool = True):
+    """Gradient of moe_combine: (dye [R, N] bf16 or None, dw [T, k] fp32).
+    Without ``with_dye`` only dw is formed (the FP8 path forms dye's codes with
+    moe_dispatch(dy, plan, weight=w))."""
+    torch = _torch()
+    _need_bf16_2d(dy, "dy")
+    _need_bf16_2d(ye, "ye")
+    T, N = dy.shape
+    k, R = _need_plan(plan, T)
+    if tuple(ye.shape) != (R, N):
+        raise ValueError(f"ye must be {(R, N)}, got {tuple(ye.shape)}")
+    _need(w, "w", torch.float32, (T, k))
+    dye = torch.empty((R, N), dtype=torch.bfloat16, device=dy.device) if with_dye else None
+    dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    _check(lib().bfp8_moe_combine_bwd(_p(dy), _ld(dy), _p(ye), _ld(ye), R, _p(plan.row), _p(plan.src), _p(w), T, k, N,
+                                      _p(dye), N, _p(dw), _stream()))
+    return dye, dw
+
+
+def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gathered: bool = True, out=None):
+    """C[r] = A[token of row r] W_e^T for the plan's rows (decode: few rows an
+    expert).  qa [T, lda], sa [Kb, ldsa] = quant_lhs(x), one row a token
+    (``gathered`` False: one row a plan row); qb [E*N, ldb], sb [E*Nb, ldsb]
+    the stacked weights.  Returns C [R, N] bf16 (rows past offs[E] are left as
+    they were in ``out``)."""
+    torch = _torch()
+    offs = _offs(plan.offs)
+    k, R = _need_plan(plan, plan.row.shape[0])
+    T = qa.shape[0]
+    if T != (plan.row.shape[0] if gathered else R):
+        raise ValueError(f"qa has {T} rows, the plan {plan.row.shape[0] if gathered else R}")
+    if qb.shape[0] != (offs.numel() - 1) * N:
+        raise ValueError(f"qb has {qb.shape[0]} rows, {offs.numel() - 1} experts of {N} need {(offs.numel() - 1) * N}")
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=qa.device)
+    _check(lib().bfp8_gemm_routed_1x128_128x128(_p(qa), _ld(qa), _p(sa), sa.stride(0), T, _p(qb), _ld(qb), _p(sb),
+                                                _ld(sb), _p(offs), offs.numel() - 1,
+                                                _p(plan.src if gathered else None), k, _p(out), _ld(out), R, N, K,
+                                                _stream()))
+    return out
 
 
 # ---------------------------------------------------------------------------

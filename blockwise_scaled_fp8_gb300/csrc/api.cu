@@ -501,6 +501,201 @@ bfp8_status bfp8_gemm_grouped_1x128_128x1(const void* qa, int64_t lda, const flo
   return grouped_common("bfp8_gemm_grouped_1x128_128x1", ga, stream);
 }
 
+// ---------------------------------------------------------------------------
+// Mixture-of-experts operators
+// ---------------------------------------------------------------------------
+
+static bfp8_status check_slots(const char* fn, int64_t T, int64_t k) {
+  CHECK_ARG(T >= 0, "%s: negative dimension", fn);
+  CHECK_ARG(k >= 1 && k <= BFP8_MOE_MAX_K, "%s: k=%lld must be in [1, %d]", fn, (long long)k, BFP8_MOE_MAX_K);
+  CHECK_ARG(T < kMaxDim && T * k < kMaxDim, "%s: T * k must stay below 2^31", fn);
+  return BFP8_OK;
+}
+
+bfp8_status bfp8_moe_route(const void* logits, int logits_f32, int64_t T, int64_t E, int64_t ldl, const float* bias,
+                           int64_t k, int score, int64_t groups, int64_t top_groups, int group_top, int renormalize,
+                           float scale, int32_t* idx, float* w, bfp8_stream_t stream) {
+  const char* fn = "bfp8_moe_route";
+  bfp8_status st = check_slots(fn, T, k);
+  if (st != BFP8_OK) return st;
+  CHECK_ARG(E >= 1 && E <= kMaxGroups, "%s: E=%lld must be in [1, %d]", fn, (long long)E, kMaxGroups);
+  CHECK_ARG(k <= E, "%s: k=%lld > E=%lld", fn, (long long)k, (long long)E);
+  CHECK_ARG(score == BFP8_MOE_SOFTMAX || score == BFP8_MOE_SIGMOID, "%s: unknown score %d", fn, score);
+  CHECK_ARG(groups >= 1 && groups <= 32 && E % groups == 0, "%s: groups=%lld must be in [1, 32] and divide E=%lld", fn,
+            (long long)groups, (long long)E);
+  CHECK_ARG(top_groups >= 1 && top_groups <= groups, "%s: top_groups=%lld must be in [1, groups]", fn,
+            (long long)top_groups);
+  CHECK_ARG(group_top == 1 || group_top == 2, "%s: group_top must be 1 or 2", fn);
+  CHECK_ARG(k <= top_groups * (E / groups), "%s: k=%lld exceeds the experts of %lld groups", fn, (long long)k,
+            (long long)top_groups);
+  CHECK_ARG(ldl >= E, "%s: ldl=%lld < E=%lld", fn, (long long)ldl, (long long)E);
+  if (T == 0) return BFP8_OK;
+  CHECK_ARG(logits && idx && w, "%s: null pointer", fn);
+  CHECK_ARG((logits_f32 ? al4(logits) : al2(logits)) && al4(bias) && al4(idx) && al4(w), "%s: misaligned pointer", fn);
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const cudaError_t e =
+      launch_moe_route(RouteArgs{logits, logits_f32 != 0, T, E, ldl, bias, (int)k, score == BFP8_MOE_SIGMOID,
+                                 (int)groups, (int)top_groups, group_top, renormalize != 0, scale, idx, w, 0},
+                       (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+
+bfp8_status bfp8_moe_route_bwd(const void* logits, int logits_f32, int64_t T, int64_t E, int64_t ldl,
+                               const int32_t* idx, const float* w, const float* dw, int64_t k, int score,
+                               int renormalize, float scale, void* dlogits, int64_t ldd, bfp8_stream_t stream) {
+  const char* fn = "bfp8_moe_route_bwd";
+  bfp8_status st = check_slots(fn, T, k);
+  if (st != BFP8_OK) return st;
+  CHECK_ARG(E >= 1 && E <= kMaxGroups, "%s: E=%lld must be in [1, %d]", fn, (long long)E, kMaxGroups);
+  CHECK_ARG(score == BFP8_MOE_SOFTMAX || score == BFP8_MOE_SIGMOID, "%s: unknown score %d", fn, score);
+  CHECK_ARG(ldl >= E && ldd >= E, "%s: ldl=%lld / ldd=%lld < E=%lld", fn, (long long)ldl, (long long)ldd, (long long)E);
+  if (T == 0) return BFP8_OK;
+  CHECK_ARG(logits && idx && w && dw && dlogits, "%s: null pointer", fn);
+  CHECK_ARG((logits_f32 ? al4(logits) && al4(dlogits) : al2(logits) && al2(dlogits)) && al4(idx) && al4(w) && al4(dw),
+            "%s: misaligned pointer", fn);
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const cudaError_t e =
+      launch_moe_route_bwd(RouteBwdArgs{logits, logits_f32 != 0, T, E, ldl, idx, w, dw, (int)k,
+                                        score == BFP8_MOE_SIGMOID, renormalize != 0, scale, dlogits, ldd},
+                           (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+
+int64_t bfp8_moe_plan_rows(int64_t T, int64_t k, int64_t E, int64_t align) {
+  if (T < 0 || k < 1 || E < 1 || align < 1 || T >= kMaxDim || k >= kMaxDim || E >= kMaxDim || align >= kMaxDim)
+    return -1;
+  if (T > ((int64_t)1 << 62) / k) return -1;
+  const int64_t n = T * k, reach = n < E ? n : E;
+  if (n >= kMaxDim) return -1;
+  // each reached expert adds at most align - 1 rows of padding, and the total is a multiple of align
+  const int64_t rows = (n + reach * (align - 1)) / align * align;
+  return rows < kMaxDim ? rows : -1;
+}
+
+bfp8_status bfp8_moe_plan(const int32_t* idx, int64_t T, int64_t k, int64_t E, int64_t align, int32_t* offs,
+                          int32_t* row, int32_t* src, int64_t R, int32_t* counts, bfp8_stream_t stream) {
+  const char* fn = "bfp8_moe_plan";
+  bfp8_status st = check_slots(fn, T, k);
+  if (st != BFP8_OK) return st;
+  CHECK_ARG(E >= 1 && E <= kMaxGroups, "%s: E=%lld must be in [1, %d]", fn, (long long)E, kMaxGroups);
+  CHECK_ARG(align >= 1 && align <= 4096, "%s: align=%lld must be in [1, 4096]", fn, (long long)align);
+  const int64_t need = bfp8_moe_plan_rows(T, k, E, align);
+  CHECK_ARG(need >= 0, "%s: more than 2^31 rows", fn);
+  CHECK_ARG(R >= need && R < kMaxDim, "%s: R=%lld < bfp8_moe_plan_rows=%lld (or not below 2^31)", fn, (long long)R,
+            (long long)need);
+  CHECK_ARG(offs && counts && (T == 0 || (idx && row)) && (R == 0 || src), "%s: null pointer", fn);
+  CHECK_ARG(al4(idx) && al4(offs) && al4(row) && al4(src) && al4(counts), "%s: misaligned pointer", fn);
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const cudaError_t e = launch_moe_plan(PlanArgs{idx, T * k, E, align, offs, row, src, R, counts}, (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+
+bfp8_status bfp8_moe_dispatch(const void* x, int64_t T, int64_t K, int64_t ldx, const int32_t* src, int64_t R,
+                              int64_t k, const float* weight, void* q_row, int64_t ldq_row, float* s_row,
+                              int64_t lds_row, void* q_col, int64_t ldq_col, float* s_col, int64_t lds_col,
+                              bfp8_stream_t stream) {
+  const char* fn = "bfp8_moe_dispatch";
+  bfp8_status st = check_slots(fn, T, k);
+  if (st != BFP8_OK) return st;
+  if ((st = check_dims(fn, R, K)) != BFP8_OK) return st;
+  CHECK_ARG(!q_col == !s_col, "%s: the transposed output needs its codes and its scales", fn);
+  if (R == 0 || K == 0) return BFP8_OK;
+  CHECK_ARG(src && q_row && s_row && (T == 0 || x), "%s: null pointer", fn);
+  CHECK_ARG(al2(x) && al4(src) && al4(weight) && al16(q_row) && al16(q_col) && al4(s_row) && al4(s_col),
+            "%s: x must be 2-byte, codes 16-byte, the rest 4-byte aligned", fn);
+  CHECK_ARG(ldx >= K, "%s: ldx=%lld < K=%lld", fn, (long long)ldx, (long long)K);
+  CHECK_ARG(ldq_row >= K && ldq_row % 16 == 0, "%s: ldq_row=%lld must be >= K=%lld and a multiple of 16", fn,
+            (long long)ldq_row, (long long)K);
+  CHECK_ARG(lds_row >= R, "%s: lds_row=%lld < R=%lld", fn, (long long)lds_row, (long long)R);
+  if (q_col) {
+    CHECK_ARG(ldq_col >= R && ldq_col % 16 == 0, "%s: ldq_col=%lld must be >= R=%lld and a multiple of 16", fn,
+              (long long)ldq_col, (long long)R);
+    CHECK_ARG(lds_col >= K, "%s: lds_col=%lld < K=%lld", fn, (long long)lds_col, (long long)K);
+  }
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const char* msg = nullptr;
+  const cudaError_t e = launch_moe_dispatch(
+      DispatchArgs{(const uint16_t*)x, T, K, ldx, src, R, (int)k, weight, (uint8_t*)q_row, ldq_row, s_row, lds_row,
+                   (uint8_t*)q_col, ldq_col, s_col, lds_col},
+      sms, (cudaStream_t)stream, &msg);
+  if (e != cudaSuccess) return msg ? fail(BFP8_ERR_INVALID_ARG, "%s: %s", fn, msg) : cuda_fail(e, fn);
+  return BFP8_OK;
+}
+
+bfp8_status bfp8_moe_combine(const void* ye, int64_t ldye, int64_t R, const int32_t* row, const float* w, int64_t T,
+                             int64_t k, int64_t N, void* y, int64_t ldy, bfp8_stream_t stream) {
+  const char* fn = "bfp8_moe_combine";
+  bfp8_status st = check_slots(fn, T, k);
+  if (st != BFP8_OK) return st;
+  if ((st = check_dims(fn, R, N)) != BFP8_OK) return st;
+  CHECK_ARG(T * cdiv(N, kCombineThreads) < kMaxDim, "%s: T * N too large for one launch", fn);
+  if (T == 0 || N == 0) return BFP8_OK;
+  CHECK_ARG(row && y && (R == 0 || ye), "%s: null pointer", fn);
+  CHECK_ARG(al2(ye) && al2(y) && al4(row) && al4(w), "%s: misaligned pointer", fn);
+  CHECK_ARG(ldye >= N && ldy >= N, "%s: ldye=%lld / ldy=%lld < N=%lld", fn, (long long)ldye, (long long)ldy,
+            (long long)N);
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const cudaError_t e = launch_moe_combine(
+      CombineArgs{(const uint16_t*)ye, ldye, R, row, w, T, (int)k, N, (uint16_t*)y, ldy, 0}, (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+
+bfp8_status bfp8_moe_combine_bwd(const void* dy, int64_t lddy, const void* ye, int64_t ldye, int64_t R,
+                                 const int32_t* row, const int32_t* src, const float* w, int64_t T, int64_t k,
+                                 int64_t N, void* dye, int64_t lddye, float* dw, bfp8_stream_t stream) {
+  const char* fn = "bfp8_moe_combine_bwd";
+  bfp8_status st = check_slots(fn, T, k);
+  if (st != BFP8_OK) return st;
+  if ((st = check_dims(fn, R, N)) != BFP8_OK) return st;
+  CHECK_ARG(lddy >= N && ldye >= N && (!dye || lddye >= N), "%s: a row stride is below N=%lld", fn, (long long)N);
+  CHECK_ARG((T == 0 || (row && dw && (N == 0 || dy))) && (R == 0 || N == 0 || (ye && (!dye || src))),
+            "%s: null pointer", fn);
+  CHECK_ARG(al2(dy) && al2(ye) && al2(dye) && al4(row) && al4(src) && al4(w) && al4(dw), "%s: misaligned pointer", fn);
+  if (T == 0 && (!dye || R == 0 || N == 0)) return BFP8_OK;
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const cudaError_t e =
+      launch_moe_combine_bwd(CombineBwdArgs{(const uint16_t*)dy, lddy, (const uint16_t*)ye, ldye, R, row, src, w, T,
+                                            (int)k, N, (uint16_t*)dye, lddye, dw},
+                             sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+
+bfp8_status bfp8_gemm_routed_1x128_128x128(const void* qa, int64_t lda, const float* sa, int64_t ldsa, int64_t T,
+                                           const void* qb, int64_t ldb, const float* sb, int64_t ldsb,
+                                           const int32_t* offs, int64_t E, const int32_t* src, int64_t k, void* c,
+                                           int64_t ldc, int64_t R, int64_t N, int64_t K, bfp8_stream_t stream) {
+  const char* fn = "bfp8_gemm_routed_1x128_128x128";
+  bfp8_status st = check_slots(fn, T, src ? k : 1);
+  if (st != BFP8_OK) return st;
+  if ((st = check_dims(fn, R, N, K)) != BFP8_OK) return st;
+  CHECK_ARG(E >= 1 && E <= kMaxGroups, "%s: E=%lld must be in [1, %d]", fn, (long long)E, kMaxGroups);
+  if (R == 0 || N == 0) return BFP8_OK;
+  CHECK_ARG(offs && c && (K == 0 || (qb && sb && (T == 0 || (qa && sa)))), "%s: null pointer", fn);
+  CHECK_ARG(al16(qa) && al16(qb), "%s: qa and qb must be 16-byte aligned", fn);
+  CHECK_ARG(al4(sa) && al4(sb) && al4(offs) && al4(src) && al2(c), "%s: misaligned pointer", fn);
+  CHECK_ARG(lda >= K && lda % 16 == 0, "%s: lda=%lld must be >= K=%lld and a multiple of 16", fn, (long long)lda,
+            (long long)K);
+  CHECK_ARG(ldb >= K && ldb % 16 == 0, "%s: ldb=%lld must be >= K=%lld and a multiple of 16", fn, (long long)ldb,
+            (long long)K);
+  CHECK_ARG(ldsa >= T, "%s: ldsa=%lld < T=%lld", fn, (long long)ldsa, (long long)T);
+  CHECK_ARG(ldsb >= cdiv(K, kBlock), "%s: ldsb=%lld < ceil(K/128)=%lld", fn, (long long)ldsb,
+            (long long)cdiv(K, kBlock));
+  CHECK_ARG(ldc >= N, "%s: ldc=%lld < N=%lld", fn, (long long)ldc, (long long)N);
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const cudaError_t e = launch_gemm_routed(
+      GemmRoutedArgs{(const uint8_t*)qa, lda, sa, ldsa, T, (const uint8_t*)qb, ldb, sb, ldsb, offs, E, src, (int)k,
+                     (uint16_t*)c, ldc, R, N, K},
+      sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+
 bfp8_status bfp8_debug_gemm_stall(const void* qa, int64_t lda, const float* sa, int64_t ldsa, const void* qb,
                                   int64_t ldb, const float* sb, int64_t ldsb, void* c, int64_t ldc, int64_t M,
                                   int64_t N, int64_t K, int64_t wait_limit_us, bfp8_stream_t stream) {

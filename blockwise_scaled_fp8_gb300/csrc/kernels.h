@@ -131,6 +131,114 @@ struct GemmWxqArgs {
 };
 cudaError_t launch_gemm_wgrad_xq(const GemmWxqArgs& a, int num_sms, cudaStream_t st, const char** msg);
 
+// Mixture-of-experts operators (moe.cu, moe_dispatch.cu, moe_gemm.cu); the
+// arguments are those of the ABI's entries (bfp8.h).
+constexpr int kRouteThreads = 128;
+constexpr int kPlanThreads = 1024;
+constexpr int kCombineThreads = 256;
+constexpr float kRouteSumFloor = 1e-20f;  // of the chosen scores' sum that weights are renormalised by
+
+struct RouteArgs {
+  const void* logits;
+  int f32;
+  int64_t T, E, ldl;
+  const float* bias;
+  int k, sigmoid, groups, top_groups, group_top, renormalize;
+  float scale;
+  int32_t* idx;
+  float* w;
+  int group_lanes;  // set by the launcher
+};
+cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t st);
+
+struct RouteBwdArgs {
+  const void* logits;
+  int f32;
+  int64_t T, E, ldl;
+  const int32_t* idx;
+  const float *w, *dw;
+  int k, sigmoid, renormalize;
+  float scale;
+  void* dlogits;
+  int64_t ldd;
+};
+cudaError_t launch_moe_route_bwd(const RouteBwdArgs& a, cudaStream_t st);
+
+struct PlanArgs {
+  const int32_t* idx;
+  int64_t n, E, align;  // n slots
+  int32_t *offs, *row, *src;
+  int64_t R;
+  int32_t* counts;
+};
+cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st);
+
+struct DispatchArgs {
+  const uint16_t* x;
+  int64_t T, C, ldx;
+  const int32_t* src;
+  int64_t R;
+  int k;
+  const float* weight;  // by slot, or null
+  uint8_t* q_row;
+  int64_t ldq_row;
+  float* s_row;
+  int64_t lds_row;
+  uint8_t* q_col;  // null: 1x128 groups only
+  int64_t ldq_col;
+  float* s_col;
+  int64_t lds_col;
+};
+cudaError_t launch_moe_dispatch(const DispatchArgs& a, int num_sms, cudaStream_t st, const char** msg);
+
+struct CombineArgs {
+  const uint16_t* ye;
+  int64_t ldye, R;
+  const int32_t* row;
+  const float* w;  // null: 1
+  int64_t T;
+  int k;
+  int64_t N;
+  uint16_t* y;
+  int64_t ldy;
+  int col_blocks;  // set by the launcher
+};
+cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t st);
+
+struct CombineBwdArgs {
+  const uint16_t* dy;
+  int64_t lddy;
+  const uint16_t* ye;
+  int64_t ldye, R;
+  const int32_t *row, *src;
+  const float* w;
+  int64_t T;
+  int k;
+  int64_t N;
+  uint16_t* dye;  // null: dw only
+  int64_t lddye;
+  float* dw;
+};
+cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& a, int num_sms, cudaStream_t st);
+
+struct GemmRoutedArgs {
+  const uint8_t* qa;
+  int64_t lda;
+  const float* sa;
+  int64_t ldsa, T;
+  const uint8_t* qb;
+  int64_t ldb;
+  const float* sb;
+  int64_t ldsb;
+  const int32_t* offs;
+  int64_t E;
+  const int32_t* src;  // null: row r of A is row r of C
+  int k;
+  uint16_t* c;
+  int64_t ldc, R, N, K;
+};
+cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_t st);
+
 // Reads and clears the device error word of the GEMM kernels (synchronous).
 cudaError_t gemm_read_errors(uint32_t* out);
 

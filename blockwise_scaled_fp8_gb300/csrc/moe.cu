@@ -1,0 +1,593 @@
+// Mixture-of-experts operators around the experts' products: the router and
+// its gradient, the plan that sorts the routed slots by expert, and the
+// combine of the experts' outputs with its gradient.
+//
+// A slot is a (token t, choice j) pair, flat index t*k + j; a row is a place
+// of the sorted buffers.  row[slot] is a slot's row, src[row] a row's slot;
+// -1 marks a slot that goes nowhere and a row that holds padding.
+#include <float.h>
+
+#include <mutex>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace bfp8 {
+
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+
+__device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ uint16_t f32_to_bf16(float v) { return (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// A 32-bit key with the order of the floats (no NaN), equal for the two zeros; every float's key is above 0.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 + 0 = +0
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float load_logit(const void* p, int f32, int64_t i) {
+  return f32 ? __ldg(static_cast<const float*>(p) + i)
+             : bf16_to_f32(__ldg(static_cast<const uint16_t*>(p) + i));
+}
+
+// The lowest finite value of the logits' type: it, -inf and NaN mask an expert.
+__device__ __forceinline__ float lowest_of(int f32) { return f32 ? -FLT_MAX : __uint_as_float(0xFF7F0000u); }
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Router
+// ---------------------------------------------------------------------------
+//
+// One warp a token, lane l the experts l, l + 32, ..  Scores in fp32: sigmoid
+// 1 / (1 + exp(-l)), or softmax exp(l - max) / sum over the eligible experts.
+// The choice compares c: score + bias, or for a softmax without bias the logit
+// itself (the softmax keeps its order, and no rounding of the denominator can
+// change a choice).  c lives in registers as an order-preserving integer key
+// (0: not eligible or already taken), so that one redux over the warp finds
+// the best key and a second one the lowest expert that holds it.
+template <int VPL>
+__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArgs a) {
+  extern __shared__ float s_route[];  // groups > 1: per warp E + 32 group-scored values
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
+  const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + warp;
+  if (t >= a.T) return;
+  const int E = (int)a.E;
+  const float low = lowest_of(a.f32);
+  const int64_t at = t * a.ldl;
+  float s[VPL];       // logit, then score
+  uint32_t key[VPL];  // of the choice value
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 32 + lane;
+    float l = e < E ? load_logit(a.logits, a.f32, at + e) : -INFINITY;
+    l = l > low ? fminf(l, FLT_MAX) : -INFINITY;  // NaN compares false
+    s[i] = l;
+    top = fmaxf(top, l);
+  }
+  float gv[VPL];  // what a group's score sums the largest of
+  if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool ok = s[i] > -INFINITY;
+      s[i] = 1.0f / (1.0f + expf(-s[i]));
+      const float c = a.bias && ok ? s[i] + __ldg(a.bias + i * 32 + lane) : s[i];
+      gv[i] = ok && c > -INFINITY ? c : -INFINITY;
+      key[i] = gv[i] > -INFINITY ? order_key(c) : 0u;
+    }
+  } else {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool ok = s[i] > -INFINITY;
+      key[i] = ok ? order_key(s[i]) : 0u;
+      s[i] = ok ? expf(s[i] - top) : 0.0f;
+      gv[i] = ok ? s[i] : -INFINITY;
+      sum += s[i];
+    }
+    sum = fmaxf(warp_sum(sum), FLT_MIN);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      s[i] = s[i] / sum;
+      if (a.bias && key[i]) {
+        gv[i] = s[i] + __ldg(a.bias + i * 32 + lane);
+        if (!(gv[i] > -INFINITY)) gv[i] = -INFINITY;
+        key[i] = gv[i] > -INFINITY ? order_key(gv[i]) : 0u;
+      }
+    }
+  }
+  if (a.groups > 1) {
+    // L lanes a group (a power of two), each the two largest of its share; a
+    // group's experts sit 32 values apart in the register layout, so they
+    // pass through shared memory, padded so that the groups' lanes meet
+    // different banks
+    const int S = E / a.groups, L = a.group_lanes;
+    float* buf = s_route + warp * (E + 32);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 32 + lane;
+      if (e < E) buf[e + e / S * L] = gv[i];
+    }
+    __syncwarp();
+    const int g = lane / L;
+    float m1 = -INFINITY, m2 = -INFINITY;
+    if (g < a.groups)
+      for (int i = lane % L; i < S; i += L) {
+        const float v = buf[g * (S + L) + i];
+        m2 = fmaxf(m2, fminf(m1, v));
+        m1 = fmaxf(m1, v);
+      }
+    for (int o = L >> 1; o >= 1; o >>= 1) {
+      const float n1 = __shfl_xor_sync(kFull, m1, o), n2 = __shfl_xor_sync(kFull, m2, o);
+      m2 = fmaxf(fmaxf(m2, n2), fminf(m1, n1));
+      m1 = fmaxf(m1, n1);
+    }
+    const float gs = a.group_top == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+    uint32_t gkey = lane % L == 0 && g < a.groups && m1 > -INFINITY ? order_key(gs) : 0u;
+    uint32_t kept = 0;  // bit g: group g stays
+    for (int j = 0; j < a.top_groups; ++j) {
+      const uint32_t best = __reduce_max_sync(kFull, gkey);
+      if (best == 0) break;
+      const int win = __ffs(__ballot_sync(kFull, gkey == best)) - 1;  // lowest lane = lowest group
+      kept |= 1u << (win / L);
+      if (lane == win) gkey = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (!((kept >> min((i * 32 + lane) / S, 31)) & 1u)) key[i] = 0;
+  }
+  // k choices
+  int my_e = -1;
+  float my_s = 0.0f;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
+    const uint32_t best = __reduce_max_sync(kFull, m);
+    if (best == 0) break;
+    uint32_t e = 0xffffffffu;
+    float sc = 0.0f;
+#pragma unroll
+    for (int i = VPL - 1; i >= 0; --i)
+      if (key[i] == best) {
+        e = (uint32_t)(i * 32 + lane);
+        sc = s[i];
+      }
+    const uint32_t win = __reduce_min_sync(kFull, e);
+    sc = __shfl_sync(kFull, sc, (int)(win & 31u));
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (win == (uint32_t)(i * 32 + lane)) key[i] = 0;
+    if (lane == j) {
+      my_e = (int)win;
+      my_s = sc;
+    }
+  }
+  const float total = a.renormalize ? fmaxf(warp_sum(my_s), kRouteSumFloor) : 1.0f;
+  if (lane < a.k) {
+    a.idx[t * a.k + lane] = my_e;
+    a.w[t * a.k + lane] = a.scale * (my_s / total);
+  }
+}
+
+// The router's gradient.  With p the scores, S = max(sum of the chosen p,
+// floor) and the chosen j:
+//   ds_j = (scale dw_j - sum_i dw_i w_i) / S   (renormalised),  scale dw_j  (not)
+//   sigmoid:  dl_j = ds_j p_j (1 - p_j), zero elsewhere
+//   softmax:  dl_e = p_e (ds_e - sum_i ds_i p_i), ds_e = 0 where not chosen
+// One warp a token; lane j < k handles choice j, every lane the experts
+// l, l + 32, .. of the dense row, over which the chosen values go last.
+template <int VPL>
+__global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const RouteBwdArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = (int)(threadIdx.x & 31);
+  const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const int E = (int)a.E;
+  const float low = lowest_of(a.f32);
+  const int64_t at = t * a.ldl, out = t * a.ldd;
+  int e_j = lane < a.k ? a.idx[t * a.k + lane] : -1;
+  if (e_j >= E) e_j = -1;
+  const float dw = e_j >= 0 ? a.dw[t * a.k + lane] : 0.0f, w = e_j >= 0 ? a.w[t * a.k + lane] : 0.0f;
+  float l_j = e_j >= 0 ? load_logit(a.logits, a.f32, at + e_j) : -INFINITY;
+  l_j = l_j > low ? fminf(l_j, FLT_MAX) : -INFINITY;
+  float s[VPL], p_j, dot = 0.0f;
+  if (a.sigmoid) {
+    p_j = 1.0f / (1.0f + expf(-l_j));
+  } else {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 32 + lane;
+      float l = e < E ? load_logit(a.logits, a.f32, at + e) : -INFINITY;
+      l = l > low ? fminf(l, FLT_MAX) : -INFINITY;
+      s[i] = l;
+      top = fmaxf(top, l);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      s[i] = s[i] > -INFINITY ? expf(s[i] - top) : 0.0f;
+      sum += s[i];
+    }
+    sum = fmaxf(warp_sum(sum), FLT_MIN);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = s[i] / sum;
+    p_j = l_j > -INFINITY ? expf(l_j - top) / sum : 0.0f;
+  }
+  float ds = a.scale * dw;
+  if (a.renormalize) {
+    const float S = fmaxf(warp_sum(p_j), kRouteSumFloor);
+    ds = (ds - warp_sum(dw * w)) / S;
+  }
+  if (e_j < 0) ds = 0.0f;
+  if (!a.sigmoid) dot = warp_sum(ds * p_j);
+  const float dl_j = a.sigmoid ? ds * p_j * (1.0f - p_j) : p_j * (ds - dot);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 32 + lane;
+    const float dl = a.sigmoid ? 0.0f : -s[i] * dot;
+    if (e < E) {
+      if (a.f32) static_cast<float*>(a.dlogits)[out + e] = dl;
+      else static_cast<uint16_t*>(a.dlogits)[out + e] = f32_to_bf16(dl);
+    }
+  }
+  __syncwarp();  // orders the dense row before the chosen values
+  if (e_j >= 0) {
+    if (a.f32) static_cast<float*>(a.dlogits)[out + e_j] = dl_j;
+    else static_cast<uint16_t*>(a.dlogits)[out + e_j] = f32_to_bf16(dl_j);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Plan: a stable counting sort of the slots by expert
+// ---------------------------------------------------------------------------
+//
+// One launch of one cluster.  Warp w of the cluster takes a contiguous run of
+// slots, 32 at a time: match_any groups the lanes of one expert, whose rank
+// among them follows the lane, so the order within an expert is the slots'
+// order and every run gives the same plan.  Counts a warp, then prefix sums:
+// over the warps of a CTA, over the CTAs of the cluster through distributed
+// shared memory, over the experts' aligned counts.  A second walk places the
+// slots.
+__global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
+  extern __shared__ uint32_t s_cnt[];  // [32 warps][E] counts, then first ranks; [E] CTA totals; [E + 1] offsets
+  __shared__ uint32_t s_scan[32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int E = (int)a.E, tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;  // the grid is one cluster
+  uint32_t* mine = s_cnt + warp * E;
+  uint32_t* s_tot = s_cnt + 32 * E;
+  uint32_t* s_off = s_tot + E;
+  for (int i = tid; i < 32 * E; i += kPlanThreads) s_cnt[i] = 0;
+  __syncthreads();
+  const int64_t n = a.n;
+  const int64_t run = cdiv(cdiv(n, (int64_t)ctas * 32), 32) * 32;  // slots a warp, a multiple of 32
+  const int64_t lo = ((int64_t)rank * 32 + warp) * run, hi = lo + run < n ? lo + run : n;
+  for (int64_t i = lo; i < hi; i += 32) {
+    const int64_t slot = i + lane;
+    const int e = slot < hi ? a.idx[slot] : -1;
+    const bool ok = e >= 0 && e < E;
+    const uint32_t peers = __match_any_sync(kFull, ok ? e : -1);
+    if (ok && lane == __ffs(peers) - 1) mine[e] += (uint32_t)__popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  if (tid < E) {  // counts of the warps -> first ranks within the CTA
+    uint32_t sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < 32; ++w) {
+      const uint32_t c = s_cnt[w * E + tid];
+      s_cnt[w * E + tid] = sum;
+      sum += c;
+    }
+    s_tot[tid] = sum;
+  }
+  uint32_t before = 0, total = 0;  // of expert tid: slots in the CTAs before this one, in all
+  if (ctas > 1) {
+    cluster_sync_all();
+    if (tid < E)
+      for (int c = 0; c < ctas; ++c) {
+        uint32_t v;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                     : "=r"(v)
+                     : "r"(mapa_shared(smem_u32(s_tot + tid), (uint32_t)c))
+                     : "memory");
+        if (c < rank) before += v;
+        total += v;
+      }
+  } else if (tid < E) {
+    total = s_tot[tid];
+  }
+  // the experts' first rows: exclusive prefix of the aligned counts
+  const uint32_t al = (uint32_t)a.align;
+  const uint32_t rows = (total + al - 1) / al * al;
+  uint32_t inc = rows;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(kFull, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) s_scan[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t v = s_scan[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v += u;
+    }
+    s_scan[lane] = v;
+  }
+  __syncthreads();
+  const uint32_t first = inc - rows + (warp ? s_scan[warp - 1] : 0u);
+  if (tid < E) {
+    s_off[tid] = first + before;  // of this CTA's first slot of the expert
+    if (rank == 0) {
+      a.offs[tid] = (int32_t)first;
+      a.counts[tid] = (int32_t)total;
+      if (tid == E - 1) a.offs[E] = (int32_t)(first + rows);
+    }
+  }
+  __syncthreads();
+  // padding rows: within the experts (split over the CTAs), and past the last one
+  if (tid < E)
+    for (uint32_t r = first + total + (uint32_t)rank; r < first + rows; r += (uint32_t)ctas) a.src[r] = -1;
+  const int64_t end = s_scan[31];
+  for (int64_t r = end + (int64_t)rank * kPlanThreads + tid; r < a.R; r += (int64_t)ctas * kPlanThreads) a.src[r] = -1;
+  for (int64_t i = lo; i < hi; i += 32) {
+    const int64_t slot = i + lane;
+    const int e = slot < hi ? a.idx[slot] : -1;
+    const bool ok = e >= 0 && e < E;
+    const uint32_t peers = __match_any_sync(kFull, ok ? e : -1);
+    int r = -1;
+    if (ok) r = (int)(s_off[e] + mine[e] + (uint32_t)__popc(peers & ((1u << lane) - 1u)));
+    __syncwarp();
+    if (ok && lane == __ffs(peers) - 1) mine[e] += (uint32_t)__popc(peers);
+    __syncwarp();
+    if (slot < hi) a.row[slot] = r;
+    if (ok) a.src[r] = (int32_t)slot;
+  }
+  if (ctas > 1) cluster_sync_all();  // no CTA leaves while a peer reads its totals
+}
+
+// ---------------------------------------------------------------------------
+// Combine: y[t] = sum_j w[t,j] ye[row[t,j]], and its gradient
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// VEC consecutive bf16 values as fp32
+template <int VEC>
+struct Bf16s {
+  uint32_t v[VEC == 1 ? 1 : VEC / 2];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    if constexpr (VEC == 8) {
+      const uint4 q = ld_nc_v4(p);
+      v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+      v[0] = __ldg(p);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (VEC == 1 ? 1 : VEC / 2); ++i) v[i] = 0;
+  }
+  __device__ __forceinline__ float get(int i) const { return (i & 1) ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]); }
+};
+
+template <int VEC>
+__device__ __forceinline__ void store_bf16s(uint16_t* p, const float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  } else {
+    *p = f32_to_bf16(f[0]);
+  }
+}
+
+constexpr int kCombineBatch = 8;  // rows of ye in flight a thread
+
+}  // namespace
+
+// One thread VEC columns of one token; the token's rows are read eight at a
+// time before the first is used.
+template <int VEC>
+__global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const CombineArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t t = blockIdx.x / a.col_blocks;
+  const int64_t n = ((int64_t)(blockIdx.x % a.col_blocks) * kCombineThreads + threadIdx.x) * VEC;
+  if (n >= a.N) return;
+  float acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+  for (int j0 = 0; j0 < a.k; j0 += kCombineBatch) {
+    Bf16s<VEC> v[kCombineBatch];
+    float w[kCombineBatch];
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j) {
+      const int64_t slot = t * a.k + j0 + j;
+      const int r = j0 + j < a.k ? __ldg(a.row + slot) : -1;
+      const bool ok = r >= 0 && r < a.R;
+      w[j] = ok ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
+      if (ok) v[j].load(a.ye + (int64_t)r * a.ldye + n);
+      else v[j].zero();
+    }
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w[j], v[j].get(i), acc[i]);
+  }
+  store_bf16s<VEC>(a.y + t * a.ldy + n, acc);
+}
+
+// One CTA a token: dw[t,j] = dy[t] . ye[row[t,j]], and with dye the rows
+// dye[row[t,j]] = w[t,j] dy[t] from the same read of dy.  The CTAs past the
+// tokens write the zeros of dye's padding rows.
+template <int VEC, bool DYE>
+__global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const CombineBwdArgs a) {
+  __shared__ float s_part[kCombineThreads / 32][kCombineBatch];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if ((int64_t)blockIdx.x >= a.T) {
+    if constexpr (DYE) {
+      float z[VEC] = {};
+      const int64_t step = (int64_t)gridDim.x - a.T;
+      for (int64_t r = (int64_t)blockIdx.x - a.T; r < a.R; r += step) {
+        if (__ldg(a.src + r) >= 0) continue;
+        for (int64_t n = (int64_t)tid * VEC; n < a.N; n += kCombineThreads * VEC) store_bf16s<VEC>(a.dye + r * a.lddye + n, z);
+      }
+    }
+    return;
+  }
+  const int64_t t = blockIdx.x;
+  for (int j0 = 0; j0 < a.k; j0 += kCombineBatch) {
+    int r[kCombineBatch];
+    float w[kCombineBatch], dot[kCombineBatch];
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j) {
+      const int64_t slot = t * a.k + j0 + j;
+      r[j] = j0 + j < a.k ? __ldg(a.row + slot) : -1;
+      if (r[j] >= a.R) r[j] = -1;
+      w[j] = r[j] >= 0 ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
+      dot[j] = 0.0f;
+    }
+    for (int64_t n = (int64_t)tid * VEC; n < a.N; n += kCombineThreads * VEC) {
+      Bf16s<VEC> d, v[kCombineBatch];
+      d.load(a.dy + t * a.lddy + n);
+#pragma unroll
+      for (int j = 0; j < kCombineBatch; ++j) {
+        if (r[j] >= 0) v[j].load(a.ye + (int64_t)r[j] * a.ldye + n);
+        else v[j].zero();
+      }
+#pragma unroll
+      for (int j = 0; j < kCombineBatch; ++j) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dot[j] = fmaf(d.get(i), v[j].get(i), dot[j]);
+        if (DYE && r[j] >= 0) {
+          float o[VEC];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) o[i] = w[j] * d.get(i);
+          store_bf16s<VEC>(a.dye + (int64_t)r[j] * a.lddye + n, o);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j) {
+      dot[j] = warp_sum(dot[j]);
+      if (lane == 0) s_part[warp][j] = dot[j];
+    }
+    __syncthreads();
+    if (tid < kCombineBatch && j0 + tid < a.k) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kCombineThreads / 32; ++q) sum += s_part[q][tid];
+      a.dw[t * a.k + j0 + tid] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Experts a lane of the router's warps: the next power of two of E / 32.
+template <typename F>
+static cudaError_t by_vpl(int64_t E, F&& f) {
+  if (E <= 32) return f(std::integral_constant<int, 1>{});
+  if (E <= 64) return f(std::integral_constant<int, 2>{});
+  if (E <= 128) return f(std::integral_constant<int, 4>{});
+  if (E <= 256) return f(std::integral_constant<int, 8>{});
+  if (E <= 512) return f(std::integral_constant<int, 16>{});
+  return f(std::integral_constant<int, 32>{});
+}
+
+cudaError_t launch_moe_route(const RouteArgs& args, cudaStream_t st) {
+  RouteArgs a = args;
+  a.group_lanes = 1;
+  while (a.groups > 1 && a.group_lanes * 2 * a.groups <= 32) a.group_lanes *= 2;
+  const size_t smem = a.groups > 1 ? (size_t)(kRouteThreads / 32) * (a.E + 32) * 4 : 0;
+  return by_vpl(a.E, [&](auto v) {
+    return launch_pdl(moe_route_kernel<decltype(v)::value>, (unsigned)cdiv(a.T, kRouteThreads / 32), kRouteThreads,
+                      smem, st, a);
+  });
+}
+
+cudaError_t launch_moe_route_bwd(const RouteBwdArgs& a, cudaStream_t st) {
+  return by_vpl(a.E, [&](auto v) {
+    return launch_pdl(moe_route_bwd_kernel<decltype(v)::value>, (unsigned)cdiv(a.T, kRouteThreads / 32), kRouteThreads,
+                      0, st, a);
+  });
+}
+
+cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
+  const size_t smem = (size_t)(34 * a.E + 1) * 4;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (34 * kMaxGroups + 1) * 4);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  int ctas = 1;
+  while (ctas < 8 && (int64_t)ctas * kPlanThreads < a.n) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, moe_plan_kernel, a);
+}
+
+static bool rows16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
+
+cudaError_t launch_moe_combine(const CombineArgs& args, cudaStream_t st) {
+  CombineArgs a = args;
+  const bool vec = a.N % 8 == 0 && rows16(a.ye, a.ldye) && rows16(a.y, a.ldy);
+  a.col_blocks = (int)cdiv(a.N, kCombineThreads * (vec ? 8 : 1));
+  const unsigned grid = (unsigned)(a.T * a.col_blocks);
+  return vec ? launch_pdl(moe_combine_kernel<8>, grid, kCombineThreads, 0, st, a)
+             : launch_pdl(moe_combine_kernel<1>, grid, kCombineThreads, 0, st, a);
+}
+
+cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& a, int num_sms, cudaStream_t st) {
+  const bool vec = a.N % 8 == 0 && rows16(a.dy, a.lddy) && rows16(a.ye, a.ldye) && (!a.dye || rows16(a.dye, a.lddye));
+  const unsigned grid = (unsigned)(a.T + (a.dye ? (a.R < num_sms ? a.R : num_sms) : 0));
+  if (a.dye)
+    return vec ? launch_pdl(moe_combine_bwd_kernel<8, true>, grid, kCombineThreads, 0, st, a)
+               : launch_pdl(moe_combine_bwd_kernel<1, true>, grid, kCombineThreads, 0, st, a);
+  return vec ? launch_pdl(moe_combine_bwd_kernel<8, false>, grid, kCombineThreads, 0, st, a)
+             : launch_pdl(moe_combine_bwd_kernel<1, false>, grid, kCombineThreads, 0, st, a);
+}
+
+}  // namespace bfp8

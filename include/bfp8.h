@@ -246,6 +246,138 @@ BFP8_API bfp8_status bfp8_gemm_grouped_1x128_128x1(const void *qa, int64_t lda, 
                                     bfp8_stream_t stream);
 
 /*
+ * Mixture-of-experts operators around the grouped GEMMs (no counterpart on the
+ * pages, which name an MoE path and leave its routing to the model).
+ *
+ * A slot is a (token t, choice j) pair, flat index t*k + j.  Sorted buffers
+ * (the grouped GEMMs' token rows) have R rows; row[t*k + j] is a slot's row
+ * (-1: the slot goes nowhere) and src[r] a row's slot (-1: padding).
+ * 1 <= k <= BFP8_MOE_MAX_K, 1 <= E <= 1024, T*k and R below 2^31.  Index
+ * values outside their range are taken as -1; none leads to an access outside
+ * a buffer.
+ */
+#define BFP8_MOE_MAX_K 32
+#define BFP8_MOE_SOFTMAX 0
+#define BFP8_MOE_SIGMOID 1
+
+/*
+ * Router: each token's k experts and their weights, from logits [T,E].
+ *   p = softmax over the token's eligible experts, or sigmoid, in fp32.
+ *   An expert is eligible where its logit is above the lowest finite value of
+ *   the logits' type (that value, -inf and NaN mask it; +inf counts as the
+ *   largest finite value) and its bias is above -inf.
+ *   c = p + bias[e]; without a bias c = p, which a softmax compares by the
+ *   logits (the same order, with no rounding between equal candidates).
+ *   groups > 1: the experts are groups of E / groups consecutive ones; a
+ *   group's score is the sum of its group_top (1 or 2) largest c (of the
+ *   softmax's unnormalised terms where it has no bias), and the choice is
+ *   among the top_groups best groups.
+ *   idx[t*k + j] = the experts with the k largest c in falling order, of equal
+ *   ones the lowest index first; -1 where no eligible expert is left (a token
+ *   whose experts are all masked is routed nowhere).
+ *   w[t*k + j] = scale * p[idx] (0 at -1), with renormalize divided by
+ *   max(sum of the token's chosen p, 1e-20).  The bias is not part of w.
+ * logits device bf16, or fp32 (logits_f32 != 0), row stride ldl >= E; bias
+ * device fp32 [E] or NULL; idx device int32 [T,k], w device fp32 [T,k].
+ */
+BFP8_API bfp8_status bfp8_moe_route(const void *logits, int logits_f32, int64_t T, int64_t E, int64_t ldl,
+                                    const float *bias, int64_t k, int score, int64_t groups, int64_t top_groups,
+                                    int group_top, int renormalize, float scale, int32_t *idx, float *w,
+                                    bfp8_stream_t stream);
+
+/*
+ * The router's gradient: dlogits [T,E] (the logits' type, row stride ldd >= E,
+ * every element written) from dw [T,k] fp32, given the forward's logits, idx,
+ * w, score, renormalize and scale.  The choice itself has no gradient, nor has
+ * the bias.
+ */
+BFP8_API bfp8_status bfp8_moe_route_bwd(const void *logits, int logits_f32, int64_t T, int64_t E, int64_t ldl,
+                                        const int32_t *idx, const float *w, const float *dw, int64_t k, int score,
+                                        int renormalize, float scale, void *dlogits, int64_t ldd,
+                                        bfp8_stream_t stream);
+
+/*
+ * Plan: sorts the slots by expert, on the device.  Expert e owns the rows
+ * offs[e] .. offs[e+1] (what the grouped GEMMs take): its counts[e] slots in
+ * slot order, then padding up to a multiple of align (128 for the weight
+ * gradient's form, 1 for the routed product).  R >= bfp8_moe_plan_rows(T, k,
+ * E, align), the rows that any choice of experts fits in (host arithmetic; -1
+ * for sizes out of range); rows past offs[E] are padding.
+ *   idx device int32 [T,k]; offs device int32 [E+1], row [T,k], src [R],
+ *   counts [E], all written whole.  1 <= align <= 4096.  One launch; the same
+ *   inputs give the same plan.
+ */
+BFP8_API int64_t bfp8_moe_plan_rows(int64_t T, int64_t k, int64_t E, int64_t align);
+BFP8_API bfp8_status bfp8_moe_plan(const int32_t *idx, int64_t T, int64_t k, int64_t E, int64_t align,
+                                   int32_t *offs, int32_t *row, int32_t *src, int64_t R, int32_t *counts,
+                                   bfp8_stream_t stream);
+
+/*
+ * Dispatch: gathers tokens into sorted rows and quantises them, in one pass.
+ * With X[r] = weight[src[r]] * x[src[r] / k] (weight 1 where NULL; formed in
+ * fp32 and not rounded before quantisation), zero where src[r] is -1:
+ *   q_row, s_row as bfp8_quant_lhs(X): q_row[r*ldq_row + c],
+ *                s_row[(c/128)*lds_row + r];
+ *   q_col, s_col as bfp8_quant_rhs(X) (both NULL: not formed):
+ *                q_col[c*ldq_col + r], s_col[(r/128)*lds_col + c].
+ * Without weights the bytes and scales equal those of the quantisation entries
+ * on the gathered tensor.  The forward dispatches x; the backward dispatches
+ * dy with the routing weights, which is the gradient of the experts' outputs.
+ *   x device bf16 [T,K], ldx >= K (16-byte aligned rows, ldx % 8 == 0, are
+ *   copied asynchronously; others element by element); src device int32 [R];
+ *   weight device fp32 [T*k] or NULL; codes 16-byte aligned with row strides
+ *   that are multiples of 16, ldq_row >= K, ldq_col >= R, lds_row >= R,
+ *   lds_col >= K.
+ */
+BFP8_API bfp8_status bfp8_moe_dispatch(const void *x, int64_t T, int64_t K, int64_t ldx, const int32_t *src,
+                                       int64_t R, int64_t k, const float *weight, void *q_row, int64_t ldq_row,
+                                       float *s_row, int64_t lds_row, void *q_col, int64_t ldq_col, float *s_col,
+                                       int64_t lds_col, bfp8_stream_t stream);
+
+/*
+ * Combine: y[t] = sum over j of w[t,j] * ye[row[t,j]] (w NULL: 1), fp32 sums
+ * in the order of j, stored as bf16; a slot with row -1 adds nothing.  With
+ * w NULL it is the gradient of the dispatch (dx from the experts' dx).
+ *   ye device bf16 [R,N], ldye >= N; row device int32 [T,k]; w device fp32
+ *   [T,k] or NULL; y device bf16 [T,N], ldy >= N.
+ */
+BFP8_API bfp8_status bfp8_moe_combine(const void *ye, int64_t ldye, int64_t R, const int32_t *row, const float *w,
+                                      int64_t T, int64_t k, int64_t N, void *y, int64_t ldy, bfp8_stream_t stream);
+
+/*
+ * The combine's gradient: dw[t,j] = dy[t] . ye[row[t,j]] (fp32, 0 where row is
+ * -1) and, where dye is not NULL, dye[r] = w[src[r]] * dy[src[r] / k], zero on
+ * padding rows (bf16 [R,N], lddye >= N, every row written).  (The FP8 path
+ * takes dw alone and forms dye's codes with bfp8_moe_dispatch.)  row and src
+ * are one plan's; src may be NULL without dye.
+ */
+BFP8_API bfp8_status bfp8_moe_combine_bwd(const void *dy, int64_t lddy, const void *ye, int64_t ldye, int64_t R,
+                                          const int32_t *row, const int32_t *src, const float *w, int64_t T,
+                                          int64_t k, int64_t N, void *dye, int64_t lddye, float *dw,
+                                          bfp8_stream_t stream);
+
+/*
+ * Routed product, for batches that give an expert few rows (decoding): C[r]
+ * for the rows offs[e] .. offs[e+1] of each expert e is A's row src[r] / k (src
+ * NULL: r) against W_e, in the method of bfp8_gemm_1x128_128x128.  Same sources
+ * and reading as the grouped GEMM (bfp8_gemm_grouped_1x128_128x128, forward),
+ * which gives the same values up to the order of its fp32 sums and is the
+ * faster one for many rows an expert.
+ *   qa device e4m3 [T, lda], sa[kb*ldsa + t] (bfp8_quant_lhs's outputs, one row
+ *      a token), lda >= K, lda % 16 == 0, 16-byte aligned, ldsa >= T;
+ *   qb, sb the experts' stacked weights, as the grouped forward's;
+ *   offs device int32 [E+1], src device int32 [R] (a plan's);
+ *   c  device bf16 [R, ldc], ldc >= N.  Padding rows inside an expert's range
+ *      get zeros; rows outside [offs[0], offs[E]) are not written.
+ * K == 0 gives zeros.  Offsets outside [0, R] are clamped.
+ */
+BFP8_API bfp8_status bfp8_gemm_routed_1x128_128x128(const void *qa, int64_t lda, const float *sa, int64_t ldsa,
+                                                    int64_t T, const void *qb, int64_t ldb, const float *sb,
+                                                    int64_t ldsb, const int32_t *offs, int64_t E,
+                                                    const int32_t *src, int64_t k, void *c, int64_t ldc, int64_t R,
+                                                    int64_t N, int64_t K, bfp8_stream_t stream);
+
+/*
  * Blockwise-FP8 linear layer (the Float8BlockwiseLinear computation of the
  * ROCm enablement page: quantise, then the blockwise GEMMs), y = x W^T.
  *   x  device bf16 [M,K] contiguous;  w  device bf16 [N,K] contiguous;
