@@ -729,6 +729,9 @@ bfp8_status bfp8_check_device_errors(bfp8_stream_t stream) {
   e = quant_read_errors(&qbits);
   if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: read flag");
   if (qbits) return fail(BFP8_ERR_TIMEOUT, "quantisation kernel gave up waiting for its TMA tile loads");
+  e = dispatch_read_errors(&qbits);
+  if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: read flag");
+  if (qbits) return fail(BFP8_ERR_TIMEOUT, "dispatch kernel gave up waiting for its gathered rows");
   if (bits & 64u)  // kErrGroupOffsets
     return fail(BFP8_ERR_INVALID_ARG,
                 "grouped GEMM: expert offsets decreasing, outside [0, total tokens], or (weight gradient) "

@@ -190,6 +190,7 @@ struct DispatchArgs {
   int64_t lds_col;
 };
 cudaError_t launch_moe_dispatch(const DispatchArgs& a, int num_sms, cudaStream_t st, const char** msg);
+cudaError_t dispatch_read_errors(uint32_t* out);  // reads and clears the kernel's error word (synchronous)
 
 struct CombineArgs {
   const uint16_t* ye;

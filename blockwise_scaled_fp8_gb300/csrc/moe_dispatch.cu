@@ -6,18 +6,18 @@
 // ever being written: with X[r] = w[src[r]] x[src[r] / k] (zero where src[r]
 // is -1), the outputs are those of quantising X both ways.
 //
-// Persistent CTAs (two per SM, 16 warps each) over 128 x 128 tiles:
-//   1. cp.async gathers the tile's 128 rows (256 bytes each; zero-filled on
-//      padding and past the last column) into one of two stages, swizzled as a
-//      128-byte-swizzled TMA box would be.  The rows' slots were read one tile
-//      earlier, so that no copy waits for its own address.
-//   2. Warp w takes the 8-column chunk w, lane l the rows 4l .. 4l+3.  A
-//      column's 128 rows are one warp's, so its maximum, its scale and its
-//      codes need no CTA barrier: a halving exchange leaves each lane with one
-//      column's maximum over all rows.  A row's 16 chunk maxima meet in shared
-//      memory.
+// Persistent CTAs (two per SM: eight quantising warps and two that gather)
+// over 128 x 128 tiles:
+//   1. The gathering warps bring the tile's 128 rows into one of two stages,
+//      four rows of 64 columns a TMA gather, 128-byte swizzled; rows past the
+//      tensor (padding) and columns past C arrive as zeros.
+//   2. Quantising warp w takes the 16 columns 16w .., lane l the rows 4l ..
+//      4l+3.  A column's 128 rows are one warp's, so its maximum, its scale and
+//      its codes need no CTA barrier: a halving exchange leaves each lane with
+//      one column's maximum over all rows.  A row's eight partial maxima meet
+//      in shared memory.
 //   3. The codes go to a staging tile (row-major and transposed) and leave by
-//      one TMA store per output; the stage is free for the tile after the next
+//      one TMA store per output; a stage is free for the tile after the next
 //      as soon as its values are in registers.
 // The tiles are walked in bands of kBand column blocks, all rows of a band
 // before the next band: a token's rows (one per chosen expert) then read the
@@ -33,25 +33,35 @@
 
 namespace bfp8 {
 
+static __device__ uint32_t g_dispatch_error;
+
 namespace {
 
-constexpr int kDsThreads = 512;
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kDsConsumers = 256;                 // 8 warps that quantise, and two that gather
+constexpr int kDsProducers = 64;
+constexpr int kDsThreads = kDsConsumers + kDsProducers;
 constexpr int kDsCtasPerSm = 2;
 constexpr int kBand = 4;                          // column blocks of a band
 constexpr int kDsBoxBytes = 128 * 128;            // 64 bf16 columns x 128 rows
 constexpr int kDsStageBytes = 2 * kDsBoxBytes;
 constexpr int kDsOffRow = 2 * kDsStageBytes;      // q_row tile: 128 rows x 128 B, 128-byte swizzled
 constexpr int kDsOffCol = kDsOffRow + 128 * 128;  // q_col tile: 128 columns x 128 B
-constexpr int kDsOffRed = kDsOffCol + 128 * 128;  // [16 chunks][128 rows] bf16x2 row maxima
-constexpr int kDsOffSc = kDsOffRed + 16 * 128 * 4;  // [128 rows] (s, -1/s)
-constexpr int kDsOffW = kDsOffSc + 128 * 8;       // [2 stages][128 rows] weights
-constexpr int kDsSmemBytes = kDsOffW + 2 * 128 * 4 + 1024;  // + alignment slack
+constexpr int kDsOffRed = kDsOffCol + 128 * 128;  // [8 warps][128 rows] bf16x2 row maxima
+constexpr int kDsOffSc = kDsOffRed + 8 * 128 * 4;  // [128 rows] (hi, lo) of 1/s
+constexpr int kDsOffCsc = kDsOffSc + 128 * 8;     // [8 warps][8 column pairs] (hi, hi', lo, lo') of 1/s
+constexpr int kDsOffW = kDsOffCsc + 8 * 8 * 16;  // [2 stages][128 rows] weights
+constexpr int kDsOffBar = kDsOffW + 2 * 128 * 4;  // full[2], empty[2], the abort flag, a word that stays zero
+constexpr int kDsSmemBytes = kDsOffBar + 48 + 1024;  // + alignment slack
 static_assert(2 * (kDsSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 
 struct DispatchParams {
   DispatchArgs a;
-  int64_t C_al, R_al;  // C & ~15, R & ~15: extents of the two store maps
+  int C_al, R_al;  // C & ~15, R & ~15: extents of the two store maps
   int tiles_c, tiles_t, num_tiles;
+  // quotients by kBand tiles_t and by k (see magic)
+  uint32_t band_mul, k_mul;
+  int band_shift, k_shift;
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -62,244 +72,391 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+// Barriers of the quantising warps alone.
+__device__ __forceinline__ void bar_sync_consumers() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kDsConsumers) : "memory"); }
+__device__ __forceinline__ bool bar_sync_and(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "n"(kDsConsumers)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int q) {
   return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
 }
 
-// The e4m3 codes of -(x w / s) for the bf16 pair x, w2 = (w, w): neg_codes2 with the product formed first.
-__device__ __forceinline__ uint32_t neg_codes2_w(uint32_t x, uint64_t w2, uint64_t s2, uint64_t ny2) {
-  const uint64_t x2 = f2_mul(f2_pack(bf16_lo(x), bf16_hi(x)), w2);
-  const uint64_t q0 = f2_mul(x2, ny2);
-  const uint64_t r = f2_fma(s2, q0, x2);
-  const uint64_t q1 = f2_fma(r, ny2, q0);
-  return cvt_e4m3x2(__uint_as_float((uint32_t)q1), __uint_as_float((uint32_t)(q1 >> 32)));
+// Four e4m3 codes (RNE, saturating): bytes a.lo, a.hi, b.lo, b.hi.
+__device__ __forceinline__ uint32_t cvt4(uint64_t a, uint64_t b) {
+  float a0, a1, b0, b1;
+  f2_unpack(a, a0, a1);
+  f2_unpack(b, b0, b1);
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+  return r;
+}
+// Four rows y0 .. y3 x 64 columns from column x on, 128 bytes each, one after
+// the other at dst; rows past the tensor's are filled with zeros.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y0,
+                                            int32_t y1, int32_t y2, int32_t y3) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 1/s as hi + lo with lo >= 0: hi the hardware's approximation, two ulps down
+// where it is above 1/s, lo what it lacks.  RN(x hi + RN(x lo)) rounds to the
+// e4m3 code of the IEEE quotient x/s for every bf16 x with |x| <= 448 s, sign
+// of zero included (checked exhaustively on the CPU).
+__device__ __forceinline__ float2 recip_hi_lo(float s) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  if (__fmaf_rn(-s, y, 1.0f) < 0.0f) y = __uint_as_float(__float_as_uint(y) - 2u);
+  return make_float2(y, __fmul_rn(__fmaf_rn(-s, y, 1.0f), y));
 }
 
 struct TilePos {
-  int t, c;
+  int t, c;  // row and column block
 };
-__device__ __forceinline__ TilePos tile_pos(int tile, int tiles_t, int tiles_c) {
-  const int band = tile / (kBand * tiles_t), c0 = band * kBand;
-  const int width = min(kBand, tiles_c - c0), rem = tile - band * kBand * tiles_t;
+__device__ __forceinline__ TilePos tile_pos(int tile, const DispatchParams& p) {
+  const int band = (int)__umulhi((uint32_t)tile, p.band_mul) >> p.band_shift;  // tile / (kBand tiles_t)
+  const int c0 = band * kBand, rem = tile - band * kBand * p.tiles_t;
+  const int width = p.tiles_c - c0;
+  if (width >= kBand) return TilePos{rem / kBand, c0 + rem % kBand};
   return TilePos{rem / width, c0 + rem % width};
 }
 
 }  // namespace
 
-template <bool COL, bool WEIGHTED, bool VEC>
+// Position of row r of a tile in the per-row arrays, which hold a lane's four
+// rows in the order the lane reads them: 4l + ((i + rot) & 3), rot = (l >> 1) & 3
+// (so that the 16-byte reads of a quarter-warp fall into eight bank groups).
+__device__ __forceinline__ int row_pos(int r) { return (r & ~3) | ((r - (r >> 3)) & 3); }
+
+template <bool COL, bool WEIGHTED, bool TMA>
 __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
-    moe_dispatch_kernel(const __grid_constant__ CUtensorMap tmap_qrow, const __grid_constant__ CUtensorMap tmap_qcol,
-                        const DispatchParams p) {
+    moe_dispatch_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_qrow,
+                        const __grid_constant__ CUtensorMap tmap_qcol, const DispatchParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t outr = sbase + kDsOffRow, outc = sbase + kDsOffCol, red = sbase + kDsOffRed;
+  const uint32_t full0 = sbase + kDsOffBar, empty0 = full0 + 16;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDsOffBar + 32);
+  volatile int* never = abort_flag + 1;
   float* s_w = reinterpret_cast<float*>(smem + kDsOffW);
-  const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t C = p.a.C, R = p.a.R;
+  const int tid = (int)threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
+  const int C = (int)p.a.C, R = (int)p.a.R, step = (int)gridDim.x;
   pdl_launch_dependents();
   if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(full0 + 8 * s, TMA ? kDsProducers / 32 : kDsProducers);
+      mbar_init(empty0 + 8 * s, kDsConsumers / 32);
+    }
+    *abort_flag = 0;
+    *never = 0;
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    if (TMA) tma_prefetch_desc(&tmap_x);
     if (p.C_al > 0) tma_prefetch_desc(&tmap_qrow);
     if (COL && p.R_al > 0) tma_prefetch_desc(&tmap_qcol);
   }
+  __syncthreads();
   pdl_wait();
 
-  const int rot = (lane >> 1) & 3;  // the order a lane reads its rows in: 4l + ((i + rot) & 3)
-  uint32_t sel_e = 0, sel_o = 0;    // byte selectors of the transposed words (rows in order)
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = (k - rot) & 3;
-    sel_e |= (uint32_t)((i & 1) + 4 * (i >> 1)) << (4 * k);
-    sel_o |= (uint32_t)(2 + (i & 1) + 4 * (i >> 1)) << (4 * k);
-  }
-  // gather role: thread tid copies 16-byte chunk tid % 16 of rows tid / 16 + 32 i
-  const int gc = tid & 15, gr = tid >> 4;
-  int slot[4];  // of the rows of the tile that is copied next
-  auto fetch_slots = [&](int tile) {
-    const int64_t t0 = tile < p.num_tiles ? (int64_t)tile_pos(tile, p.tiles_t, p.tiles_c).t * 128 : R;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) slot[i] = t0 + gr + 32 * i < R ? __ldg(p.a.src + t0 + gr + 32 * i) : -1;
-  };
-  auto issue = [&](int tile, int s) {
-    if (tile < p.num_tiles) {
-      const int64_t c = (int64_t)tile_pos(tile, p.tiles_t, p.tiles_c).c * 128 + gc * 8;
-      const int cols = C - c >= 8 ? 8 : C - c > 0 ? (int)(C - c) : 0;
+  if (warp >= kDsConsumers / 32) {
+    // ------------------------------------------------------------ producers
+    // Warp w gathers the rows 64w .. 64w + 63, lane l the four rows 4 (l & 15) ..
+    // of them and the 64-column half l >> 4; their slots and weights are read
+    // one tile ahead, so that no copy waits for its own address.
+    const int r4 = 64 * (warp - kDsConsumers / 32) + 4 * (lane & 15), half = lane >> 4;
+    const int rot = (lane >> 1) & 3;  // of rows r4 ..
+    int tok[4];
+    float wgt[4];
+    auto fetch = [&](int tile) {
+      const int64_t r0 = tile < p.num_tiles ? (int64_t)tile_pos(tile, p).t * 128 + r4 : R;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = gr + 32 * i;
-        const int64_t tok = slot[i] >= 0 ? (int64_t)((uint32_t)slot[i] / (uint32_t)p.a.k) : p.a.T;
-        const bool ok = tok < p.a.T;
-        const uint32_t dst = sbase + (uint32_t)(s * kDsStageBytes + (gc >> 3) * kDsBoxBytes + r * 128 +
-                                                (((gc & 7) ^ (r & 7)) << 4));
-        const uint16_t* from = p.a.x + (ok ? tok * p.a.ldx + c : 0);
-        if constexpr (VEC) {
-          cp_async_16(dst, ok && cols > 0 ? from : p.a.x, ok ? 2u * cols : 0u);
-        } else {
-          uint32_t v[4] = {};
-          if (ok)
-            for (int j = 0; j < cols; ++j) v[j >> 1] |= (uint32_t)__ldg(from + j) << (16 * (j & 1));
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                       : "memory");
-        }
-        if (WEIGHTED && gc == 0) s_w[s * 128 + r] = ok ? __ldg(p.a.weight + slot[i]) : 0.0f;
+        const int slot = r0 + i < R ? __ldg(p.a.src + r0 + i) : -1;
+        const uint32_t t = p.k_mul ? __umulhi((uint32_t)slot, p.k_mul) >> p.k_shift : (uint32_t)slot;
+        const bool ok = slot >= 0 && (int64_t)t < p.a.T;
+        tok[i] = ok ? (int)t : (int)p.a.T;  // past the tensor: zeros
+        if constexpr (WEIGHTED) wgt[i] = ok ? __ldg(p.a.weight + slot) : 0.0f;
       }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  const int step = (int)gridDim.x;
-  fetch_slots((int)blockIdx.x);
-  issue((int)blockIdx.x, 0);
-  fetch_slots((int)blockIdx.x + step);
-  issue((int)blockIdx.x + step, 1);
-  fetch_slots((int)blockIdx.x + 2 * step);
-
-  int it = 0;
-  for (int tile = (int)blockIdx.x; tile < p.num_tiles; tile += step, ++it) {
-    const int s = it & 1;
-    const uint32_t stage = sbase + (uint32_t)(s * kDsStageBytes);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();  // the tile has landed
-    const TilePos pos = tile_pos(tile, p.tiles_t, p.tiles_c);
-    const int64_t t0 = (int64_t)pos.t * 128, c0 = (int64_t)pos.c * 128;
-
-    // ------------------------------------------------ values and maxima
-    uint4 v[4];
-    float w[4];
+    };
+    fetch((int)blockIdx.x);
+    int it = 0;
+    bool ok = true;
+    for (int tile = (int)blockIdx.x; tile < p.num_tiles; tile += step, ++it) {
+      const int s = it & 1;
+      ok = mbar_wait_bounded(empty0 + 8 * s, (uint32_t)((it >> 1) & 1) ^ 1u, kWaitLimitNs, abort_flag);
+      if (!__all_sync(kAll, ok)) {
+        if (lane == 0 && !*abort_flag) atomicOr(&g_dispatch_error, 1u);
+        *abort_flag = 1;
+        ok = false;
+        break;
+      }
+      const uint32_t stage = sbase + (uint32_t)(s * kDsStageBytes);
+      const int c0 = tile_pos(tile, p).c * 128;
+      if constexpr (WEIGHTED) {  // in the order of row_pos
+        const bool r1 = rot & 1, r2 = rot & 2;
+        const float a0 = r1 ? wgt[1] : wgt[0], a1 = r1 ? wgt[2] : wgt[1], a2 = r1 ? wgt[3] : wgt[2],
+                    a3 = r1 ? wgt[0] : wgt[3];
+        if (half == 0)
+          *reinterpret_cast<float4*>(s_w + s * 128 + r4) = r2 ? make_float4(a2, a3, a0, a1) : make_float4(a0, a1, a2, a3);
+      }
+      if constexpr (TMA) {
+        __syncwarp();  // the weights, before the arrival that publishes them
+        if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(kDsStageBytes / (kDsProducers / 32)));
+        __syncwarp();
+        tma_gather4(stage + (uint32_t)(half * kDsBoxBytes + r4 * 128), &tmap_x, full0 + 8 * s, c0 + 64 * half, tok[0],
+                    tok[1], tok[2], tok[3]);
+      } else {
+        // rows that TMA cannot read: element by element
+        for (int i = 0; i < 4; ++i) {
+          const int r = r4 + i;
+          for (int ch = 8 * half; ch < 8 * half + 8; ++ch) {
+            const int cols = min(C - (c0 + 8 * ch), 8);
+            uint32_t v[4] = {};
+            if (tok[i] < p.a.T) {
+              const uint16_t* from = p.a.x + (int64_t)tok[i] * p.a.ldx + c0 + 8 * ch;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * lane + ((i + rot) & 3);
-      v[i] = lds128(stage + (uint32_t)((warp >> 3) * kDsBoxBytes + r * 128 + (((warp & 7) ^ (r & 7)) << 4)));
-      w[i] = WEIGHTED ? s_w[s * 128 + r] : 1.0f;
-      sts32(red + 4u * (uint32_t)(warp * 128 + r), amax2(amax2(v[i].x, v[i].y), amax2(v[i].z, v[i].w)));
+              for (int j = 0; j < 8; ++j)
+                if (j < cols) v[j >> 1] |= (uint32_t)__ldg(from + j) << (16 * (j & 1));
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             stage + (uint32_t)((ch >> 3) * kDsBoxBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4))),
+                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                         : "memory");
+          }
+        }
+        mbar_arrive(full0 + 8 * s);
+      }
+      fetch(tile + step);
     }
-    const float wrow = WEIGHTED ? fabsf(s_w[s * 128 + (tid >> 2)]) : 1.0f;  // of the row whose scale this thread joins
-    float csc = 0.0f, cny = 0.0f;  // lane l: scale and -1/scale of column 8 warp + (l >> 2)
-    if constexpr (COL) {
-      float m[8];
+    if (TMA && !ok && lane == 0)  // copies already issued land before this CTA's shared memory goes away
+      for (int i = it > 2 ? it - 2 : 0; i < it; ++i)
+        mbar_wait_bounded(full0 + 8 * (i & 1), (uint32_t)((i >> 1) & 1), kWaitLimitNs, never);
+  } else {
+    // ------------------------------------------------------------ quantisers
+    // Warp w takes the 16 columns 16w .. of the tile, lane l the rows 4l .. 4l+3.
+    const uint32_t outr = sbase + kDsOffRow, outc = sbase + kDsOffCol;
+    const int rot = (lane >> 1) & 3;
+    uint32_t sel_e = 0, sel_o = 0;  // byte selectors of the transposed words (rows in order)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t i = (uint32_t)((k - rot) & 3);
+      sel_e |= (2 * i) << (4 * k);
+      sel_o |= (2 * i + 1) << (4 * k);
+    }
+    uint32_t* s_red = reinterpret_cast<uint32_t*>(smem + kDsOffRed);
+    float* s_csc = reinterpret_cast<float*>(smem + kDsOffCsc) + 32 * warp;
+    const int g = tid >> 1, gpos = row_pos(g);  // the row whose scale this thread and its neighbour form
+    int it = 0;
+    for (int tile = (int)blockIdx.x; tile < p.num_tiles; tile += step, ++it) {
+      const int s = it & 1;
+      const uint32_t stage = sbase + (uint32_t)(s * kDsStageBytes);
+      const TilePos pos = tile_pos(tile, p);
+      const int t0 = pos.t * 128, c0 = pos.c * 128;
+      const bool landed = mbar_wait_bounded(full0 + 8 * s, (uint32_t)((it >> 1) & 1), kWaitLimitNs, abort_flag);
+
+      // ---------------------------------------------- values and maxima
+      // Weighted values are unpacked and multiplied once and stay in registers
+      // as fp32 products; the others stay packed.
+      uint4 v[4][2];
+      uint64_t x2[WEIGHTED ? 4 : 1][8];  // products of row i, column pair q
+      float w[4];
       if constexpr (WEIGHTED) {
+        const float4 w4 = *reinterpret_cast<const float4*>(s_w + s * 128 + 4 * lane);
+        w[0] = w4.x, w[1] = w4.y, w[2] = w4.z, w[3] = w4.w;
+      }
+      uint32_t rm[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float lo = 0.0f, hi = 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * lane + ((i + rot) & 3);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[i][h] = lds128(stage + (uint32_t)((warp >> 2) * kDsBoxBytes + r * 128 +
+                                              ((((2 * warp + h) & 7) ^ (r & 7)) << 4)));
+        rm[i] = amax2(amax2(amax2(v[i][0].x, v[i][0].y), amax2(v[i][0].z, v[i][0].w)),
+                      amax2(amax2(v[i][1].x, v[i][1].y), amax2(v[i][1].z, v[i][1].w)));
+        if constexpr (WEIGHTED) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t x = word_of(v[i][q >> 2], q & 3);
+            x2[i][q] = f2_mul(f2_pack(bf16_lo(x), bf16_hi(x)), f2_pack(w[i], w[i]));
+          }
+        }
+      }
+      *reinterpret_cast<uint4*>(s_red + warp * 128 + 4 * lane) = make_uint4(rm[0], rm[1], rm[2], rm[3]);
+      const float wrow = WEIGHTED ? fabsf(s_w[s * 128 + gpos]) : 1.0f;
+      if constexpr (COL) {
+        // Halving exchange over the lanes: each step keeps half of the columns
+        // (bits 4, 3, .. of the lane choose it), then the lanes that are left
+        // with the same columns combine.
+        float cmax;  // of column 16 warp + (lane >> 1)
+        if constexpr (WEIGHTED) {
+          float m[16];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f2_unpack(x2[i][q], lo[i], hi[i]);
+            m[2 * q] = fmaxf(max3_abs(lo[0], lo[1], lo[2]), fabsf(lo[3]));
+            m[2 * q + 1] = fmaxf(max3_abs(hi[0], hi[1], hi[2]), fabsf(hi[3]));
+          }
+#pragma unroll
+          for (int h = 8; h >= 1; h >>= 1) {
+            const bool up = (lane & (2 * h)) != 0;
+#pragma unroll
+            for (int i = 0; i < h; ++i) {
+              const float give = up ? m[i] : m[i + h], keep = up ? m[i + h] : m[i];
+              m[i] = fmaxf(keep, __shfl_xor_sync(kAll, give, 2 * h));
+            }
+          }
+          cmax = fmaxf(m[0], __shfl_xor_sync(kAll, m[0], 1));
+        } else {
+          uint32_t m[8];  // packed column pairs
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            m[q] = amax2(amax2(word_of(v[0][q >> 2], q & 3), word_of(v[1][q >> 2], q & 3)),
+                         amax2(word_of(v[2][q >> 2], q & 3), word_of(v[3][q >> 2], q & 3)));
+#pragma unroll
+          for (int h = 4; h >= 1; h >>= 1) {
+            const bool up = (lane & (4 * h)) != 0;
+#pragma unroll
+            for (int i = 0; i < h; ++i) {
+              const uint32_t give = up ? m[i] : m[i + h], keep = up ? m[i + h] : m[i];
+              m[i] = amax2(keep, __shfl_xor_sync(kAll, give, 4 * h));
+            }
+          }
+          m[0] = amax2(m[0], __shfl_xor_sync(kAll, m[0], 1));
+          m[0] = amax2(m[0], __shfl_xor_sync(kAll, m[0], 2));
+          cmax = __uint_as_float((lane & 2 ? m[0] : m[0] << 16) & 0x7FFF0000u);
+        }
+        if ((lane & 1) == 0) {
+          const float sc = scale_of(cmax);
+          const float2 y = recip_hi_lo(sc);
+          const int j = lane >> 1, c = c0 + 16 * warp + j;
+          float* dst = s_csc + (j >> 1) * 4 + (j & 1);
+          dst[0] = y.x;
+          dst[2] = y.y;
+          if (c < C) p.a.s_col[(int64_t)pos.t * p.a.lds_col + c] = sc;
+        }
+      }
+      if (tid == 0) bulk_wait_read_all();  // the last tile's stores have read the staging tiles
+      // row maxima visible; every warp knows whether the tile had landed
+      if (!bar_sync_and(landed)) {
+        if (tid == 0) {
+          if (!*abort_flag) atomicOr(&g_dispatch_error, 1u);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      if (lane == 0) mbar_arrive(empty0 + 8 * s);  // the stage is in registers
+
+      // ---------------------------------------------- row scales: two threads a row
+      {
+        uint32_t m = amax2(amax2(s_red[(4 * (tid & 1)) * 128 + gpos], s_red[(4 * (tid & 1) + 1) * 128 + gpos]),
+                           amax2(s_red[(4 * (tid & 1) + 2) * 128 + gpos], s_red[(4 * (tid & 1) + 3) * 128 + gpos]));
+        m = amax2(m, __shfl_xor_sync(kAll, m, 1));
+        m = amax2(m, __byte_perm(m, 0, 0x1032));
+        // rounding is monotonic: the largest |x w| of the row is |w| times its largest |x|
+        const float sc = scale_of(__uint_as_float(m & 0x7FFF0000u) * wrow);
+        if ((tid & 1) == 0) {
+          *reinterpret_cast<float2*>(smem + kDsOffSc + 8 * gpos) = recip_hi_lo(sc);
+          if (t0 + g < R) p.a.s_row[(int64_t)pos.c * p.a.lds_row + t0 + g] = sc;
+        }
+      }
+      bar_sync_consumers();  // row scales visible
+      // ---------------------------------------------- codes
+      // One unpacking for both forms.  Without weights x/s is RN(x hi + RN(x lo)),
+      // the IEEE quotient's code; with them RN(RN(x w) hi), within three
+      // roundings of the quotient (the product x w has no ties to keep).
+      float rhi[4], rlo[4];
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const float4 y = *reinterpret_cast<const float4*>(smem + kDsOffSc + 8 * (4 * lane + i));
+        rhi[i] = y.x, rlo[i] = y.y, rhi[i + 1] = y.z, rlo[i + 1] = y.w;
+      }
+      uint32_t rc[4][4];  // row codes: the thread's 16 columns of row i
+#pragma unroll
+      for (int q2 = 0; q2 < 4; ++q2) {
+        uint64_t rv[4][2];
+#pragma unroll
+        for (int q1 = 0; q1 < 2; ++q1) {
+          const int q = 2 * q2 + q1;
+          uint64_t chi = 0, clo = 0, cv[4];  // columns 16 warp + 2q, + 1
+          if constexpr (COL) {
+            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(s_csc + 4 * q);
+            chi = y.x, clo = y.y;
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            lo = fmaxf(lo, fabsf(bf16_lo(word_of(v[i], q)) * w[i]));
-            hi = fmaxf(hi, fabsf(bf16_hi(word_of(v[i], q)) * w[i]));
+            if constexpr (WEIGHTED) {
+              cv[i] = f2_mul(x2[i][q], chi);
+              rv[i][q1] = f2_mul(x2[i][q], f2_pack(rhi[i], rhi[i]));
+            } else {
+              const uint32_t x1 = word_of(v[i][q >> 2], q & 3);
+              const uint64_t x = f2_pack(bf16_lo(x1), bf16_hi(x1));
+              cv[i] = f2_fma(x, chi, f2_mul(x, clo));
+              rv[i][q1] = f2_fma(x, f2_pack(rhi[i], rhi[i]), f2_mul(x, f2_pack(rlo[i], rlo[i])));
+            }
           }
-          m[2 * q] = lo, m[2 * q + 1] = hi;
+          if constexpr (COL) {
+            const uint32_t dst = outc + (uint32_t)((16 * warp + 2 * q) * 128 + 4 * lane);
+            const uint32_t lo = cvt4(cv[0], cv[1]), hi = cvt4(cv[2], cv[3]);
+            sts32(dst, __byte_perm(lo, hi, sel_e));
+            sts32(dst + 128u, __byte_perm(lo, hi, sel_o));
+          }
         }
-      } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t c2 = amax2(amax2(word_of(v[0], q), word_of(v[1], q)), amax2(word_of(v[2], q), word_of(v[3], q)));
-          m[2 * q] = __uint_as_float((c2 << 16) & 0x7FFF0000u);
-          m[2 * q + 1] = __uint_as_float(c2 & 0x7FFF0000u);
-        }
+        for (int i = 0; i < 4; ++i) rc[i][q2] = cvt4(rv[i][0], rv[i][1]);
       }
-      // halving exchange: after it lane l holds column l >> 2 (bits 4, 3, 2 of the lane choose the half kept)
 #pragma unroll
-      for (int h = 4; h >= 1; h >>= 1) {
-        const bool up = (lane & (4 * h)) != 0;
-#pragma unroll
-        for (int i = 0; i < h; ++i) {
-          const float give = up ? m[i] : m[i + h], keep = up ? m[i + h] : m[i];
-          m[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 4 * h));
-        }
-      }
-      m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
-      m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 2));
-      csc = WEIGHTED ? group_scale(m[0]) : scale_of(m[0]);
-      cny = neg_rcp(csc);
-      const int64_t c = c0 + 8 * warp + (lane >> 2);
-      if ((lane & 3) == 0 && c < C) p.a.s_col[(t0 / 128) * p.a.lds_col + c] = csc;
-    }
-    if (tid == 0) bulk_wait_read_all();  // the last tile's stores have read the staging tiles
-    __syncthreads();  // row maxima visible; the stage is in registers
-    // ------------------------------------------------ the copy after the next
-    issue(tile + 2 * step, s);
-    fetch_slots(tile + 3 * step);
-
-    // ------------------------------------------------ row scales: four threads a row
-    {
-      const int g = tid >> 2, qd = tid & 3;
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t x;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(red + 4u * (uint32_t)((4 * qd + j) * 128 + g)));
-        m = amax2(m, x);
-      }
-      m = amax2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = amax2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      m = amax2(m, __byte_perm(m, 0, 0x1032));
-      const float amax = __uint_as_float(m & 0x7FFF0000u);
-      // rounding is monotonic: the largest |x w| of the row is |w| times its largest |x|
-      if (qd == 0) {
-        const float sc = WEIGHTED ? group_scale(amax * wrow) : scale_of(amax);
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sbase + kDsOffSc + 8u * g), "f"(sc), "f"(neg_rcp(sc))
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * lane + ((i + rot) & 3);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(outr + (uint32_t)(r * 128 + ((warp ^ (r & 7)) << 4))),
+                     "r"(rc[i][0]), "r"(rc[i][1]), "r"(rc[i][2]), "r"(rc[i][3])
                      : "memory");
-        if (t0 + g < R) p.a.s_row[(c0 / 128) * p.a.lds_row + t0 + g] = sc;
+      }
+      fence_proxy_async_shared();
+      bar_sync_consumers();  // the output tiles are complete
+      if (tid == 0) {
+        if (c0 < p.C_al) tma_store_2d(&tmap_qrow, outr, c0, t0);
+        if (COL && t0 < p.R_al) tma_store_2d(&tmap_qcol, outc, t0, c0);
+        bulk_commit();
+      }
+      // the last C % 16 (R % 16) bytes of a row, past the maps' extents
+      if (p.C_al < C && c0 + 128 > p.C_al && t0 + g < R) {
+        for (int c = p.C_al + (tid & 1); c < C; c += 2)
+          p.a.q_row[(int64_t)(t0 + g) * p.a.ldq_row + c] =
+              smem[kDsOffRow + g * 128 + (((((c - c0) >> 4) ^ (g & 7)) << 4) | ((c - c0) & 15))];
+      }
+      if (COL && p.R_al < R && t0 + 128 > p.R_al && c0 + g < C) {
+        for (int r = p.R_al + (tid & 1); r < R; r += 2)
+          p.a.q_col[(int64_t)(c0 + g) * p.a.ldq_col + r] = smem[kDsOffCol + g * 128 + (r - t0)];
       }
     }
-    // ------------------------------------------------ transposed codes
-    if constexpr (COL) {
-      const uint32_t dst = outc + (uint32_t)(8 * warp * 128 + 4 * lane);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint64_t s2 = f2_pack(__shfl_sync(0xffffffffu, csc, 8 * q), __shfl_sync(0xffffffffu, csc, 8 * q + 4));
-        const uint64_t ny2 = f2_pack(__shfl_sync(0xffffffffu, cny, 8 * q), __shfl_sync(0xffffffffu, cny, 8 * q + 4));
-        uint32_t cc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          cc[i] = WEIGHTED ? neg_codes2_w(word_of(v[i], q), f2_pack(w[i], w[i]), s2, ny2)
-                           : neg_codes2(word_of(v[i], q), s2, ny2);
-        const uint32_t X = __byte_perm(cc[0], cc[1], 0x5140), Y = __byte_perm(cc[2], cc[3], 0x5140);
-        sts32(dst + (uint32_t)((2 * q) * 128), __byte_perm(X, Y, sel_e) ^ 0x80808080u);
-        sts32(dst + (uint32_t)((2 * q + 1) * 128), __byte_perm(X, Y, sel_o) ^ 0x80808080u);
-      }
-    }
-    __syncthreads();  // row scales visible
-    // ------------------------------------------------ row-major codes
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * lane + ((i + rot) & 3);
-      float rs, rny;
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(rs), "=f"(rny) : "r"(sbase + kDsOffSc + 8u * r));
-      const uint64_t s2 = f2_pack(rs, rs), ny2 = f2_pack(rny, rny), w2 = f2_pack(w[i], w[i]);
-      uint32_t cd[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        cd[q] = WEIGHTED ? neg_codes2_w(word_of(v[i], q), w2, s2, ny2) : neg_codes2(word_of(v[i], q), s2, ny2);
-      sts64(outr + (uint32_t)(r * 128 + ((((warp >> 1) ^ (r & 7)) << 4) | ((warp & 1) << 3))),
-            __byte_perm(cd[0], cd[1], 0x5410) ^ 0x80808080u, __byte_perm(cd[2], cd[3], 0x5410) ^ 0x80808080u);
-    }
-    fence_proxy_async_shared();
-    __syncthreads();  // the output tiles are complete
-    if (tid == 0) {
-      if (c0 < p.C_al) tma_store_2d(&tmap_qrow, outr, (int32_t)c0, (int32_t)t0);
-      if (COL && t0 < p.R_al) tma_store_2d(&tmap_qcol, outc, (int32_t)t0, (int32_t)c0);
-      bulk_commit();
-    }
-    // the last C % 16 (R % 16) bytes of a row, past the maps' extents
-    const int g = tid >> 2, b0 = 4 * (tid & 3);
-    if (c0 + 128 > p.C_al && p.C_al < C && t0 + g < R) {
-      for (int b = b0; b < b0 + 4; ++b)
-        if (p.C_al + b < C) {
-          const int cl = (int)(p.C_al + b - c0);
-          p.a.q_row[(t0 + g) * p.a.ldq_row + p.C_al + b] =
-              smem[kDsOffRow + g * 128 + ((((cl >> 4) ^ (g & 7)) << 4) | (cl & 15))];
-        }
-    }
-    if (COL && t0 + 128 > p.R_al && p.R_al < R && c0 + g < C) {
-      for (int b = b0; b < b0 + 4; ++b)
-        if (p.R_al + b < R) p.a.q_col[(c0 + g) * p.a.ldq_col + p.R_al + b] = smem[kDsOffCol + g * 128 + (p.R_al + b - t0)];
-    }
+    if (tid == 0) bulk_wait_all();  // stores complete before the CTA exits
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  if (tid == 0) bulk_wait_all();  // stores complete before the CTA exits
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
@@ -332,26 +489,48 @@ static bool ds_store_map(CUtensorMap* m, void* base, int64_t inner, int64_t rows
                         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool COL, bool WEIGHTED, bool VEC>
-static cudaError_t run_dispatch(const CUtensorMap& mr, const CUtensorMap& mc, const DispatchParams& p, int num_sms,
+// x bf16 [T, C], gathered by rows of 64 columns, 128-byte swizzled.
+static bool ds_gather_map(CUtensorMap* m, const uint16_t* x, int64_t C, int64_t T, int64_t ldx) {
+  cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)T};
+  cuuint64_t strides[1] = {(cuuint64_t)ldx * 2};
+  cuuint32_t box[2] = {64, 1};
+  cuuint32_t elem[2] = {1, 1};
+  return ds_encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(x), dims, strides, box, elem,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// n / d = umulhi(n, mul) >> shift for 0 <= n < 2^31 and d >= 2: with 2^(shift
+// + 1) >= d, mul = floor(2^(32 + shift) / d) + 1 is 2^(32 + shift) / d + e, 0 <
+// e <= 1, which adds at most n e / 2^(32 + shift) < 2^-(shift + 1) <= 1/d to the
+// quotient: not enough to reach the next whole number.  d = 1: mul = 0.
+static void magic(uint32_t d, uint32_t* mul, int* shift) {
+  int sh = 0;
+  while (((uint64_t)2 << sh) < d) ++sh;
+  *mul = d == 1 ? 0u : (uint32_t)((((uint64_t)1 << (32 + sh)) / d) + 1);
+  *shift = sh;
+}
+
+template <bool COL, bool WEIGHTED, bool TMA>
+static cudaError_t run_dispatch(const CUtensorMap& mx, const CUtensorMap& mr, const CUtensorMap& mc, const DispatchParams& p, int num_sms,
                                 cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(moe_dispatch_kernel<COL, WEIGHTED, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    attr = cudaFuncSetAttribute(moe_dispatch_kernel<COL, WEIGHTED, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kDsSmemBytes);
   });
   if (attr != cudaSuccess) return attr;
   const int cap = kDsCtasPerSm * num_sms;
-  return launch_pdl(moe_dispatch_kernel<COL, WEIGHTED, VEC>, (unsigned)(p.num_tiles < cap ? p.num_tiles : cap),
-                    kDsThreads, kDsSmemBytes, st, mr, mc, p);
+  return launch_pdl(moe_dispatch_kernel<COL, WEIGHTED, TMA>, (unsigned)(p.num_tiles < cap ? p.num_tiles : cap),
+                    kDsThreads, kDsSmemBytes, st, mx, mr, mc, p);
 }
 
 cudaError_t launch_moe_dispatch(const DispatchArgs& a, int num_sms, cudaStream_t st, const char** msg) {
   DispatchParams p;
   p.a = a;
-  p.C_al = a.C & ~(int64_t)15;
-  p.R_al = a.R & ~(int64_t)15;
+  p.C_al = (int)(a.C & ~(int64_t)15);
+  p.R_al = (int)(a.R & ~(int64_t)15);
   const int64_t tc = cdiv(a.C, 128), tt = cdiv(a.R, 128);
   if (tc * tt >= ((int64_t)1 << 30)) {
     *msg = "too many 128x128 tiles (2^30 at most)";
@@ -360,25 +539,35 @@ cudaError_t launch_moe_dispatch(const DispatchArgs& a, int num_sms, cudaStream_t
   p.tiles_c = (int)tc;
   p.tiles_t = (int)tt;
   p.num_tiles = (int)(tc * tt);
-  CUtensorMap mr, mc;
+  magic((uint32_t)(kBand * tt), &p.band_mul, &p.band_shift);
+  magic((uint32_t)a.k, &p.k_mul, &p.k_shift);
+  CUtensorMap mx, mr, mc;
+  memset(&mx, 0, sizeof(mx));
   memset(&mr, 0, sizeof(mr));
   memset(&mc, 0, sizeof(mc));
-  if (ds_encode_fn() == nullptr ||
+  const bool tma = a.T > 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx % 8 == 0;
+  if (ds_encode_fn() == nullptr || (tma && !ds_gather_map(&mx, a.x, a.C, a.T, a.ldx)) ||
       (p.C_al > 0 && !ds_store_map(&mr, a.q_row, p.C_al, a.R, a.ldq_row, true)) ||
       (a.q_col && p.R_al > 0 && !ds_store_map(&mc, a.q_col, p.R_al, a.C, a.ldq_col, false))) {
-    *msg = "cuTensorMapEncodeTiled failed for an output (alignment, stride or size out of range)";
+    *msg = "cuTensorMapEncodeTiled failed for an operand (alignment, stride or size out of range)";
     return cudaErrorInvalidValue;
   }
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx % 8 == 0;
   auto pick = [&](auto col, auto weighted) {
     constexpr bool kCol = decltype(col)::value, kW = decltype(weighted)::value;
-    return vec ? run_dispatch<kCol, kW, true>(mr, mc, p, num_sms, st)
-               : run_dispatch<kCol, kW, false>(mr, mc, p, num_sms, st);
+    return tma ? run_dispatch<kCol, kW, true>(mx, mr, mc, p, num_sms, st)
+               : run_dispatch<kCol, kW, false>(mx, mr, mc, p, num_sms, st);
   };
   using T = std::true_type;
   using F = std::false_type;
   if (a.q_col) return a.weight ? pick(T{}, T{}) : pick(T{}, F{});
   return a.weight ? pick(F{}, T{}) : pick(F{}, F{});
+}
+
+cudaError_t dispatch_read_errors(uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_dispatch_error, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_dispatch_error, &zero, sizeof(uint32_t));
 }
 
 }  // namespace bfp8
