@@ -127,17 +127,27 @@ def _rup(a: int, b: int) -> int:
     return _cdiv(a, b) * b
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream():
-    return ctypes.c_void_p(_torch().cuda.current_stream().cuda_stream)
+    """The current stream's handle.  torch's raw getter, where it has one:
+    building a Stream object takes 3 us of host time, more than the launch."""
+    C = _torch()._C
+    raw = getattr(C, "_cuda_getCurrentRawStream", None)
+    return raw(C._cuda_getDevice()) if raw is not None else _torch().cuda.current_stream().cuda_stream
 
 
-def _p(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(None)
+def _p(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _need_bf16_2d(t, name):
@@ -446,7 +456,7 @@ def _score(score):
 
 def _need(t, name, dtype, shape):
     """A contiguous CUDA tensor of that type and shape."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
 

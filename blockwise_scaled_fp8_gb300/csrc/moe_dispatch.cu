@@ -19,9 +19,10 @@
 //   3. The codes go to a staging tile (row-major and transposed) and leave by
 //      one TMA store per output; a stage is free for the tile after the next
 //      as soon as its values are in registers.
-// The tiles are walked in bands of kBand column blocks, all rows of a band
-// before the next band: a token's rows (one per chosen expert) then read the
-// same few hundred bytes of it within a short time, from L2 after the first.
+// The tiles are walked down the rows of a column block before the next block:
+// a token's rows (one per chosen expert) then read the same 256 bytes of it
+// within a short time, from L2 after the first (16384 tokens x 4096, eight
+// experts each: 342 us; blocks of four columns at a time 348, all 32 of them 383).
 #include <cudaTypedefs.h>
 #include <string.h>
 
@@ -42,7 +43,6 @@ constexpr int kDsConsumers = 256;                 // 8 warps that quantise, and 
 constexpr int kDsProducers = 64;
 constexpr int kDsThreads = kDsConsumers + kDsProducers;
 constexpr int kDsCtasPerSm = 2;
-constexpr int kBand = 4;                          // column blocks of a band
 constexpr int kDsBoxBytes = 128 * 128;            // 64 bf16 columns x 128 rows
 constexpr int kDsStageBytes = 2 * kDsBoxBytes;
 constexpr int kDsOffRow = 2 * kDsStageBytes;      // q_row tile: 128 rows x 128 B, 128-byte swizzled
@@ -59,9 +59,9 @@ struct DispatchParams {
   DispatchArgs a;
   int C_al, R_al;  // C & ~15, R & ~15: extents of the two store maps
   int tiles_c, tiles_t, num_tiles;
-  // quotients by kBand tiles_t and by k (see magic)
-  uint32_t band_mul, k_mul;
-  int band_shift, k_shift;
+  // quotients by tiles_t and by k (see magic)
+  uint32_t t_mul, k_mul;
+  int t_shift, k_shift;
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -135,11 +135,8 @@ struct TilePos {
   int t, c;  // row and column block
 };
 __device__ __forceinline__ TilePos tile_pos(int tile, const DispatchParams& p) {
-  const int band = (int)__umulhi((uint32_t)tile, p.band_mul) >> p.band_shift;  // tile / (kBand tiles_t)
-  const int c0 = band * kBand, rem = tile - band * kBand * p.tiles_t;
-  const int width = p.tiles_c - c0;
-  if (width >= kBand) return TilePos{rem / kBand, c0 + rem % kBand};
-  return TilePos{rem / width, c0 + rem % width};
+  const int c = p.tiles_t > 1 ? (int)__umulhi((uint32_t)tile, p.t_mul) >> p.t_shift : tile;  // tile / tiles_t
+  return TilePos{tile - c * p.tiles_t, c};
 }
 
 }  // namespace
@@ -539,7 +536,7 @@ cudaError_t launch_moe_dispatch(const DispatchArgs& a, int num_sms, cudaStream_t
   p.tiles_c = (int)tc;
   p.tiles_t = (int)tt;
   p.num_tiles = (int)(tc * tt);
-  magic((uint32_t)(kBand * tt), &p.band_mul, &p.band_shift);
+  magic((uint32_t)tt, &p.t_mul, &p.t_shift);
   magic((uint32_t)a.k, &p.k_mul, &p.k_shift);
   CUtensorMap mx, mr, mc;
   memset(&mx, 0, sizeof(mx));
