@@ -536,7 +536,7 @@ bfp8_status bfp8_moe_route(const void* logits, int logits_f32, int64_t T, int64_
   if ((st = check_device(&sms)) != BFP8_OK) return st;
   const cudaError_t e =
       launch_moe_route(RouteArgs{logits, logits_f32 != 0, T, E, ldl, bias, (int)k, score == BFP8_MOE_SIGMOID,
-                                 (int)groups, (int)top_groups, group_top, renormalize != 0, scale, idx, w, 0},
+                                 (int)groups, (int)top_groups, group_top, renormalize != 0, scale, idx, w, 0, 0, 0, 0},
                        (cudaStream_t)stream);
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
 }
@@ -558,7 +558,7 @@ bfp8_status bfp8_moe_route_bwd(const void* logits, int logits_f32, int64_t T, in
   if ((st = check_device(&sms)) != BFP8_OK) return st;
   const cudaError_t e =
       launch_moe_route_bwd(RouteBwdArgs{logits, logits_f32 != 0, T, E, ldl, idx, w, dw, (int)k,
-                                        score == BFP8_MOE_SIGMOID, renormalize != 0, scale, dlogits, ldd},
+                                        score == BFP8_MOE_SIGMOID, renormalize != 0, scale, dlogits, ldd, 0},
                            (cudaStream_t)stream);
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
 }

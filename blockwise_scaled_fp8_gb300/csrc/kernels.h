@@ -147,7 +147,7 @@ struct RouteArgs {
   float scale;
   int32_t* idx;
   float* w;
-  int group_lanes;  // set by the launcher
+  int vec, bias_vec, group_lanes, group_whole;  // set by the launcher
 };
 cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t st);
 
@@ -161,6 +161,7 @@ struct RouteBwdArgs {
   float scale;
   void* dlogits;
   int64_t ldd;
+  int vec;  // set by the launcher
 };
 cudaError_t launch_moe_route_bwd(const RouteBwdArgs& a, cudaStream_t st);
 

@@ -47,90 +47,170 @@ __device__ __forceinline__ float lowest_of(int f32) { return f32 ? -FLT_MAX : __
 // ---------------------------------------------------------------------------
 // Router
 // ---------------------------------------------------------------------------
-//
-// One warp a token, lane l the experts l, l + 32, ..  Scores in fp32: sigmoid
-// 1 / (1 + exp(-l)), or softmax exp(l - max) / sum over the eligible experts.
-// The choice compares c: score + bias, or for a softmax without bias the logit
-// itself (the softmax keeps its order, and no rounding of the denominator can
-// change a choice).  c lives in registers as an order-preserving integer key
-// (0: not eligible or already taken), so that one redux over the warp finds
-// the best key and a second one the lowest expert that holds it.
-template <int VPL>
+
+namespace {
+
+template <int X, int Y, int N, typename K>
+__device__ __forceinline__ void order_pair(K (&v)[N]) {
+  const K hi = v[X] > v[Y] ? v[X] : v[Y], lo = v[X] > v[Y] ? v[Y] : v[X];
+  v[X] = hi;
+  v[Y] = lo;
+}
+
+// Sorts 1 .. 6 or 8 values, largest first (networks of the fewest exchanges).
+template <int N, typename K>
+__device__ __forceinline__ void sort_down(K (&v)[N]) {
+  static_assert(N <= 6 || N == 8, "a network for N values");
+  if constexpr (N == 2) {
+    order_pair<0, 1>(v);
+  } else if constexpr (N == 3) {
+    order_pair<1, 2>(v); order_pair<0, 2>(v); order_pair<0, 1>(v);
+  } else if constexpr (N == 4) {
+    order_pair<0, 1>(v); order_pair<2, 3>(v); order_pair<0, 2>(v); order_pair<1, 3>(v); order_pair<1, 2>(v);
+  } else if constexpr (N == 5) {
+    order_pair<0, 1>(v); order_pair<3, 4>(v); order_pair<2, 4>(v); order_pair<2, 3>(v); order_pair<1, 4>(v);
+    order_pair<0, 3>(v); order_pair<0, 2>(v); order_pair<1, 3>(v); order_pair<1, 2>(v);
+  } else if constexpr (N == 6) {
+    order_pair<1, 2>(v); order_pair<4, 5>(v); order_pair<0, 2>(v); order_pair<3, 5>(v); order_pair<0, 1>(v);
+    order_pair<3, 4>(v); order_pair<2, 5>(v); order_pair<0, 3>(v); order_pair<1, 4>(v); order_pair<2, 4>(v);
+    order_pair<1, 3>(v); order_pair<2, 3>(v);
+  } else if constexpr (N == 8) {
+    order_pair<0, 1>(v); order_pair<2, 3>(v); order_pair<4, 5>(v); order_pair<6, 7>(v); order_pair<0, 2>(v);
+    order_pair<1, 3>(v); order_pair<4, 6>(v); order_pair<5, 7>(v); order_pair<1, 2>(v); order_pair<5, 6>(v);
+    order_pair<0, 4>(v); order_pair<1, 5>(v); order_pair<2, 6>(v); order_pair<3, 7>(v); order_pair<2, 4>(v);
+    order_pair<3, 5>(v); order_pair<1, 2>(v); order_pair<3, 4>(v); order_pair<5, 6>(v);
+  }
+}
+
+// N logits of a row from element i on as fp32, -inf past the row's end and where the expert is masked.
+template <int N, bool F32>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t at, int e0, float (&l)[N]) {
+  const float low = lowest_of(F32);
+  if (N % 4 == 0 && a.vec && e0 + N <= (int)a.E) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i + 3 < N; i += 4) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + e0 + i));
+        l[i] = q.x, l[i + 1] = q.y, l[i + 2] = q.z, l[i + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i + 3 < N; i += 4) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + at + e0 + i));
+        l[i] = bf16_lo(q.x), l[i + 1] = bf16_hi(q.x), l[i + 2] = bf16_lo(q.y), l[i + 3] = bf16_hi(q.y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = e0 + i < (int)a.E ? load_logit(a.logits, F32, at + e0 + i) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) l[i] = l[i] > low ? fminf(l[i], FLT_MAX) : -INFINITY;  // NaN compares false
+}
+
+__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+}  // namespace
+
+// One warp a token, lane l the VPL consecutive experts from l VPL on.  Scores
+// in fp32: sigmoid 1 / (1 + exp(-l)), or softmax exp(l - max) / sum over the
+// eligible experts.  The choice compares c: score + bias, or for a softmax
+// without bias the logit itself (the softmax keeps its order, and no rounding
+// of the denominator can change a choice), as an order-preserving integer key
+// (0: not eligible).  What bounds it is instructions, so:
+//   - each lane sorts its keys once (VPL <= 8), each with its place in the low
+//     word so that equal ones keep their order; a choice is then one redux
+//     over the lanes' first keys, a ballot for the lowest lane that holds it
+//     (whose experts are the lowest), and a shift of the winner's list;
+//   - bf16 logits of a softmax without bias are 16-bit keys: they share a
+//     32-bit word with the expert's complement, and the redux names the winner;
+//   - with more experts a lane (VPL > 8) sorting costs more than k scans;
+//   - scores of the chosen are formed again from their logits, by k lanes.
+// 16384 tokens, 256 experts in 8 groups, sigmoid, k = 8: see the launcher.
+template <int VPL, bool F32, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArgs a) {
-  extern __shared__ float s_route[];  // groups > 1: per warp E + 32 group-scored values
+  // per warp: E + 32 values of groups that are not whole powers of two of lanes, later the sorted lists (VPL <= 8)
+  extern __shared__ __align__(16) float s_route[];
+  constexpr bool kByLogit = !SIGMOID && !BIAS, kPacked = kByLogit && !F32 && VPL <= 8;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
   const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + warp;
   if (t >= a.T) return;
-  const int E = (int)a.E;
-  const float low = lowest_of(a.f32);
+  const int E = (int)a.E, e0 = lane * VPL;
+  float* mine_s = s_route + warp * (VPL <= 8 ? VPL * 64 : E + 32);
   const int64_t at = t * a.ldl;
-  float s[VPL];       // logit, then score
-  uint32_t key[VPL];  // of the choice value
-  float top = -INFINITY;
+  float c[VPL];  // logit, then the choice value (-inf: not eligible)
+  load_logits<VPL, F32>(a, at, e0, c);
+  float top = 0.0f, sum = 1.0f;  // softmax: p = exp(l - top) / sum
+  float gv[VPL];                 // what a group's score sums the largest of (softmax without bias)
+  if constexpr (!SIGMOID) {
+    top = c[0];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    float l = e < E ? load_logit(a.logits, a.f32, at + e) : -INFINITY;
-    l = l > low ? fminf(l, FLT_MAX) : -INFINITY;  // NaN compares false
-    s[i] = l;
-    top = fmaxf(top, l);
-  }
-  float gv[VPL];  // what a group's score sums the largest of
-  if (a.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const bool ok = s[i] > -INFINITY;
-      s[i] = 1.0f / (1.0f + expf(-s[i]));
-      const float c = a.bias && ok ? s[i] + __ldg(a.bias + i * 32 + lane) : s[i];
-      gv[i] = ok && c > -INFINITY ? c : -INFINITY;
-      key[i] = gv[i] > -INFINITY ? order_key(c) : 0u;
-    }
-  } else {
+    for (int i = 1; i < VPL; ++i) top = fmaxf(top, c[i]);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    float sum = 0.0f;
+    sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const bool ok = s[i] > -INFINITY;
-      key[i] = ok ? order_key(s[i]) : 0u;
-      s[i] = ok ? expf(s[i] - top) : 0.0f;
-      gv[i] = ok ? s[i] : -INFINITY;
-      sum += s[i];
+      gv[i] = c[i] > -INFINITY ? expf(c[i] - top) : 0.0f;
+      sum += gv[i];
     }
     sum = fmaxf(warp_sum(sum), FLT_MIN);
+  }
+  if constexpr (!kByLogit) {
+    float b[VPL] = {};
+    if constexpr (BIAS) {
+      if (VPL % 4 == 0 && a.bias_vec && e0 + VPL <= E) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      s[i] = s[i] / sum;
-      if (a.bias && key[i]) {
-        gv[i] = s[i] + __ldg(a.bias + i * 32 + lane);
-        if (!(gv[i] > -INFINITY)) gv[i] = -INFINITY;
-        key[i] = gv[i] > -INFINITY ? order_key(gv[i]) : 0u;
+        for (int i = 0; i + 3 < VPL; i += 4) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(a.bias + e0 + i));
+          b[i] = q.x, b[i + 1] = q.y, b[i + 2] = q.z, b[i + 3] = q.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (e0 + i < E) b[i] = __ldg(a.bias + e0 + i);
       }
     }
-  }
-  if (a.groups > 1) {
-    // L lanes a group (a power of two), each the two largest of its share; a
-    // group's experts sit 32 values apart in the register layout, so they
-    // pass through shared memory, padded so that the groups' lanes meet
-    // different banks
-    const int S = E / a.groups, L = a.group_lanes;
-    float* buf = s_route + warp * (E + 32);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = i * 32 + lane;
-      if (e < E) buf[e + e / S * L] = gv[i];
+      const bool ok = c[i] > -INFINITY;
+      float v = SIGMOID ? sigmoid(c[i]) : gv[i] / sum;
+      if (BIAS) v += b[i];
+      c[i] = ok && v > -INFINITY ? v : -INFINITY;
     }
-    __syncwarp();
-    const int g = lane / L;
-    float m1 = -INFINITY, m2 = -INFINITY;
-    if (g < a.groups)
-      for (int i = lane % L; i < S; i += L) {
-        const float v = buf[g * (S + L) + i];
+  }
+  uint32_t kept = 0xffffffffu;  // bit g: group g stays
+  const int S = a.groups > 1 ? E / a.groups : E;
+  if (a.groups > 1) {
+    auto value = [&](int i) { return kByLogit ? (c[i] > -INFINITY ? gv[i] : -INFINITY) : c[i]; };
+    float m1 = -INFINITY, m2 = -INFINITY;  // the two largest of this lane's share of a group
+    int L = a.group_lanes, g;              // lanes a group
+    if (a.group_whole) {
+      // a lane's experts lie in one group, of L consecutive lanes
+      g = lane / L;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float v = value(i);
         m2 = fmaxf(m2, fminf(m1, v));
         m1 = fmaxf(m1, v);
       }
+    } else {
+      // through shared memory, padded so that the groups' lanes meet different banks
+      float* buf = mine_s;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (e0 + i < E) buf[e0 + i + (e0 + i) / S * L] = value(i);
+      __syncwarp();
+      g = lane / L;
+      if (g < a.groups)
+        for (int i = lane % L; i < S; i += L) {
+          const float v = buf[g * (S + L) + i];
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
+        }
+    }
     for (int o = L >> 1; o >= 1; o >>= 1) {
       const float n1 = __shfl_xor_sync(kFull, m1, o), n2 = __shfl_xor_sync(kFull, m2, o);
       m2 = fmaxf(fmaxf(m2, n2), fminf(m1, n1));
@@ -138,7 +218,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
     }
     const float gs = a.group_top == 2 && m2 > -INFINITY ? m1 + m2 : m1;
     uint32_t gkey = lane % L == 0 && g < a.groups && m1 > -INFINITY ? order_key(gs) : 0u;
-    uint32_t kept = 0;  // bit g: group g stays
+    kept = 0;
     for (int j = 0; j < a.top_groups; ++j) {
       const uint32_t best = __reduce_max_sync(kFull, gkey);
       if (best == 0) break;
@@ -146,41 +226,95 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
       kept |= 1u << (win / L);
       if (lane == win) gkey = 0;
     }
+    if (a.group_whole) {
+      if (!((kept >> min(g, 31)) & 1u)) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (!((kept >> min((i * 32 + lane) / S, 31)) & 1u)) key[i] = 0;
-  }
-  // k choices
-  int my_e = -1;
-  float my_s = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t m = key[0];
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
-    const uint32_t best = __reduce_max_sync(kFull, m);
-    if (best == 0) break;
-    uint32_t e = 0xffffffffu;
-    float sc = 0.0f;
-#pragma unroll
-    for (int i = VPL - 1; i >= 0; --i)
-      if (key[i] == best) {
-        e = (uint32_t)(i * 32 + lane);
-        sc = s[i];
+        for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
       }
-    const uint32_t win = __reduce_min_sync(kFull, e);
-    sc = __shfl_sync(kFull, sc, (int)(win & 31u));
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (win == (uint32_t)(i * 32 + lane)) key[i] = 0;
-    if (lane == j) {
-      my_e = (int)win;
-      my_s = sc;
+      for (int i = 0; i < VPL; ++i)
+        if (!((kept >> min((e0 + i) / S, 31)) & 1u)) c[i] = -INFINITY;
     }
   }
-  const float total = a.renormalize ? fmaxf(warp_sum(my_s), kRouteSumFloor) : 1.0f;
+  // k choices: lane j keeps choice j
+  int my_e = -1;
+  if constexpr (kPacked) {
+    uint32_t key[VPL];  // 16 bits of the logit's order, then the expert's complement: every key differs
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      key[i] = c[i] > -INFINITY ? (order_key(c[i]) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e0 - i) : 0u;
+    sort_down(key);
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t best = __reduce_max_sync(kFull, key[0]);
+      if (best == 0) break;
+      if (lane == j) my_e = 0xFFFF - (int)(best & 0xFFFFu);
+      const bool mine = key[0] == best;
+#pragma unroll
+      for (int i = 0; i + 1 < VPL; ++i) key[i] = mine ? key[i + 1] : key[i];
+      if (mine) key[VPL - 1] = 0;
+    }
+  } else if constexpr (VPL <= 8) {
+    uint64_t key[VPL];  // the value's order, then the complement of the place in the lane
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      key[i] = c[i] > -INFINITY ? ((uint64_t)order_key(c[i]) << 32) | (uint32_t)(VPL - 1 - i) : 0u;
+    sort_down(key);
+    // the rest of the list, [place][lane]: the winner fetches its next key
+    uint64_t* list = reinterpret_cast<uint64_t*>(mine_s) + lane;
+    uint64_t head = key[0];
+    if constexpr (VPL > 1) {
+      __syncwarp();  // the groups' values, which lay here, have been read
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) list[32 * (i - 1)] = key[i];
+      list[32 * (VPL - 1)] = 0;
+    }
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t hi = (uint32_t)(head >> 32), best = __reduce_max_sync(kFull, hi);
+      if (best == 0) break;
+      const int win = __ffs(__ballot_sync(kFull, hi == best)) - 1;
+      const int e = __shfl_sync(kFull, e0 + VPL - 1 - (int)(uint32_t)head, win);
+      if (lane == j) my_e = e;
+      if (lane == win) {
+        if constexpr (VPL > 1) {
+          head = *list;
+          if (head) list += 32;
+        } else {
+          head = 0;
+        }
+      }
+    }
+  } else {
+    uint32_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = c[i] > -INFINITY ? order_key(c[i]) : 0u;
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
+      const uint32_t best = __reduce_max_sync(kFull, m);
+      if (best == 0) break;
+      const int win = __ffs(__ballot_sync(kFull, m == best)) - 1;
+      int at_i = 0;
+#pragma unroll
+      for (int i = VPL - 1; i >= 0; --i)
+        if (key[i] == best) at_i = i;
+      const int e = __shfl_sync(kFull, e0 + at_i, win);
+      if (lane == j) my_e = e;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (e == e0 + i) key[i] = 0;
+    }
+  }
+  float p = 0.0f;
+  if (my_e >= 0) {
+    const float l = fminf(load_logit(a.logits, F32, at + my_e), FLT_MAX);
+    p = SIGMOID ? sigmoid(l) : expf(l - top) / sum;
+  }
+  const float total = a.renormalize ? fmaxf(warp_sum(p), kRouteSumFloor) : 1.0f;
   if (lane < a.k) {
     a.idx[t * a.k + lane] = my_e;
-    a.w[t * a.k + lane] = a.scale * (my_s / total);
+    a.w[t * a.k + lane] = a.scale * (p / total);
   }
 }
 
@@ -189,9 +323,10 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
 //   ds_j = (scale dw_j - sum_i dw_i w_i) / S   (renormalised),  scale dw_j  (not)
 //   sigmoid:  dl_j = ds_j p_j (1 - p_j), zero elsewhere
 //   softmax:  dl_e = p_e (ds_e - sum_i ds_i p_i), ds_e = 0 where not chosen
-// One warp a token; lane j < k handles choice j, every lane the experts
-// l, l + 32, .. of the dense row, over which the chosen values go last.
-template <int VPL>
+// One warp a token; lane j < k handles choice j.  Of the dense row lane l
+// takes the pairs 2l, 2l + 64, .. (one load and one store a pair where the row
+// is aligned for it), over which the chosen values go last.
+template <int PAIRS, bool F32, bool SIGMOID>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const RouteBwdArgs a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -199,38 +334,50 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
   const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
   if (t >= a.T) return;
   const int E = (int)a.E;
-  const float low = lowest_of(a.f32);
+  const float low = lowest_of(F32);
   const int64_t at = t * a.ldl, out = t * a.ldd;
-  int e_j = lane < a.k ? a.idx[t * a.k + lane] : -1;
+  int e_j = lane < a.k ? __ldg(a.idx + t * a.k + lane) : -1;
   if (e_j >= E) e_j = -1;
-  const float dw = e_j >= 0 ? a.dw[t * a.k + lane] : 0.0f, w = e_j >= 0 ? a.w[t * a.k + lane] : 0.0f;
-  float l_j = e_j >= 0 ? load_logit(a.logits, a.f32, at + e_j) : -INFINITY;
+  const float dw = e_j >= 0 ? __ldg(a.dw + t * a.k + lane) : 0.0f, w = e_j >= 0 ? __ldg(a.w + t * a.k + lane) : 0.0f;
+  float l_j = e_j >= 0 ? load_logit(a.logits, F32, at + e_j) : -INFINITY;
   l_j = l_j > low ? fminf(l_j, FLT_MAX) : -INFINITY;
-  float s[VPL], p_j, dot = 0.0f;
-  if (a.sigmoid) {
-    p_j = 1.0f / (1.0f + expf(-l_j));
+  float s[2 * PAIRS], p_j, dot = 0.0f;
+  if constexpr (SIGMOID) {
+    p_j = sigmoid(l_j);
   } else {
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * 32 + lane;
-      float l = e < E ? load_logit(a.logits, a.f32, at + e) : -INFINITY;
-      l = l > low ? fminf(l, FLT_MAX) : -INFINITY;
-      s[i] = l;
-      top = fmaxf(top, l);
+    for (int i = 0; i < PAIRS; ++i) {
+      const int e = 64 * i + 2 * lane;
+      float l0 = -INFINITY, l1 = -INFINITY;
+      if (a.vec && e + 1 < E) {
+        if constexpr (F32) {
+          const float2 q = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.logits) + at + e));
+          l0 = q.x, l1 = q.y;
+        } else {
+          const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.logits) + at + e));
+          l0 = bf16_lo(q), l1 = bf16_hi(q);
+        }
+      } else {
+        if (e < E) l0 = load_logit(a.logits, F32, at + e);
+        if (e + 1 < E) l1 = load_logit(a.logits, F32, at + e + 1);
+      }
+      s[2 * i] = l0 > low ? fminf(l0, FLT_MAX) : -INFINITY;
+      s[2 * i + 1] = l1 > low ? fminf(l1, FLT_MAX) : -INFINITY;
+      top = fmaxf(top, fmaxf(s[2 * i], s[2 * i + 1]));
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
+    for (int i = 0; i < 2 * PAIRS; ++i) {
       s[i] = s[i] > -INFINITY ? expf(s[i] - top) : 0.0f;
       sum += s[i];
     }
-    sum = fmaxf(warp_sum(sum), FLT_MIN);
+    const float inv = 1.0f / fmaxf(warp_sum(sum), FLT_MIN);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = s[i] / sum;
-    p_j = l_j > -INFINITY ? expf(l_j - top) / sum : 0.0f;
+    for (int i = 0; i < 2 * PAIRS; ++i) s[i] *= inv;
+    p_j = l_j > -INFINITY ? expf(l_j - top) * inv : 0.0f;
   }
   float ds = a.scale * dw;
   if (a.renormalize) {
@@ -238,20 +385,33 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
     ds = (ds - warp_sum(dw * w)) / S;
   }
   if (e_j < 0) ds = 0.0f;
-  if (!a.sigmoid) dot = warp_sum(ds * p_j);
-  const float dl_j = a.sigmoid ? ds * p_j * (1.0f - p_j) : p_j * (ds - dot);
+  if constexpr (!SIGMOID) dot = warp_sum(ds * p_j);
+  const float dl_j = SIGMOID ? ds * p_j * (1.0f - p_j) : p_j * (ds - dot);
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = i * 32 + lane;
-    const float dl = a.sigmoid ? 0.0f : -s[i] * dot;
-    if (e < E) {
-      if (a.f32) static_cast<float*>(a.dlogits)[out + e] = dl;
-      else static_cast<uint16_t*>(a.dlogits)[out + e] = f32_to_bf16(dl);
+  for (int i = 0; i < PAIRS; ++i) {
+    const int e = 64 * i + 2 * lane;
+    const float d0 = SIGMOID ? 0.0f : -s[2 * i] * dot, d1 = SIGMOID ? 0.0f : -s[2 * i + 1] * dot;
+    if constexpr (F32) {
+      float* to = static_cast<float*>(a.dlogits) + out + e;
+      if (a.vec && e + 1 < E) {
+        *reinterpret_cast<float2*>(to) = make_float2(d0, d1);
+      } else {
+        if (e < E) to[0] = d0;
+        if (e + 1 < E) to[1] = d1;
+      }
+    } else {
+      uint16_t* to = static_cast<uint16_t*>(a.dlogits) + out + e;
+      if (a.vec && e + 1 < E) {
+        *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(d0, d1);
+      } else {
+        if (e < E) to[0] = f32_to_bf16(d0);
+        if (e + 1 < E) to[1] = f32_to_bf16(d1);
+      }
     }
   }
   __syncwarp();  // orders the dense row before the chosen values
   if (e_j >= 0) {
-    if (a.f32) static_cast<float*>(a.dlogits)[out + e_j] = dl_j;
+    if constexpr (F32) static_cast<float*>(a.dlogits)[out + e_j] = dl_j;
     else static_cast<uint16_t*>(a.dlogits)[out + e_j] = f32_to_bf16(dl_j);
   }
 }
@@ -512,33 +672,81 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const 
 // Host side
 // ---------------------------------------------------------------------------
 
-// Experts a lane of the router's warps: the next power of two of E / 32.
+// f with the experts a lane takes as a compile-time number: E / 32 rounded up to one of these.
 template <typename F>
 static cudaError_t by_vpl(int64_t E, F&& f) {
-  if (E <= 32) return f(std::integral_constant<int, 1>{});
-  if (E <= 64) return f(std::integral_constant<int, 2>{});
-  if (E <= 128) return f(std::integral_constant<int, 4>{});
-  if (E <= 256) return f(std::integral_constant<int, 8>{});
-  if (E <= 512) return f(std::integral_constant<int, 16>{});
+  const int64_t n = cdiv(E, 32);
+  if (n <= 1) return f(std::integral_constant<int, 1>{});
+  if (n <= 2) return f(std::integral_constant<int, 2>{});
+  if (n <= 3) return f(std::integral_constant<int, 3>{});
+  if (n <= 4) return f(std::integral_constant<int, 4>{});
+  if (n <= 5) return f(std::integral_constant<int, 5>{});
+  if (n <= 6) return f(std::integral_constant<int, 6>{});
+  if (n <= 8) return f(std::integral_constant<int, 8>{});
+  if (n <= 16) return f(std::integral_constant<int, 16>{});
   return f(std::integral_constant<int, 32>{});
+}
+
+template <typename F>
+static cudaError_t by_bool(bool v, F&& f) {
+  return v ? f(std::true_type{}) : f(std::false_type{});
+}
+
+static bool aligned_to(const void* p, int64_t ld_bytes, int64_t n) {
+  return reinterpret_cast<uintptr_t>(p) % n == 0 && ld_bytes % n == 0;
 }
 
 cudaError_t launch_moe_route(const RouteArgs& args, cudaStream_t st) {
   RouteArgs a = args;
-  a.group_lanes = 1;
-  while (a.groups > 1 && a.group_lanes * 2 * a.groups <= 32) a.group_lanes *= 2;
-  const size_t smem = a.groups > 1 ? (size_t)(kRouteThreads / 32) * (a.E + 32) * 4 : 0;
-  return by_vpl(a.E, [&](auto v) {
-    return launch_pdl(moe_route_kernel<decltype(v)::value>, (unsigned)cdiv(a.T, kRouteThreads / 32), kRouteThreads,
-                      smem, st, a);
+  const int el = a.f32 ? 4 : 2;
+  a.vec = aligned_to(a.logits, a.ldl * el, 4 * el);
+  a.bias_vec = aligned_to(a.bias, 0, 16);
+  return by_vpl(a.E, [&](auto vpl) {
+    constexpr int kVpl = decltype(vpl)::value;
+    if (a.groups > 1) {
+      // a power of two of lanes a group, whole lanes where the groups' size allows it
+      const int64_t S = a.E / a.groups, lanes = S / kVpl;
+      a.group_whole = S % kVpl == 0 && (lanes & (lanes - 1)) == 0;
+      a.group_lanes = 1;
+      if (a.group_whole) a.group_lanes = (int)lanes;
+      else
+        while (a.group_lanes * 2 * a.groups <= 32) a.group_lanes *= 2;
+    }
+    // (VPL <= 8: E + 32 <= 64 VPL)
+    const size_t smem = kVpl <= 8 ? (size_t)(kRouteThreads / 32) * kVpl * 64 * 4
+                        : a.groups > 1 ? (size_t)(kRouteThreads / 32) * (a.E + 32) * 4 : 0;
+    return by_bool(a.f32, [&](auto f32) {
+      return by_bool(a.sigmoid, [&](auto sig) {
+        return by_bool(a.bias != nullptr, [&](auto bias) {
+          return launch_pdl(moe_route_kernel<kVpl, decltype(f32)::value, decltype(sig)::value, decltype(bias)::value>,
+                            (unsigned)cdiv(a.T, kRouteThreads / 32), kRouteThreads, smem, st, a);
+        });
+      });
+    });
   });
 }
 
-cudaError_t launch_moe_route_bwd(const RouteBwdArgs& a, cudaStream_t st) {
-  return by_vpl(a.E, [&](auto v) {
-    return launch_pdl(moe_route_bwd_kernel<decltype(v)::value>, (unsigned)cdiv(a.T, kRouteThreads / 32), kRouteThreads,
-                      0, st, a);
-  });
+cudaError_t launch_moe_route_bwd(const RouteBwdArgs& args, cudaStream_t st) {
+  RouteBwdArgs a = args;
+  const int el = a.f32 ? 4 : 2;
+  a.vec = aligned_to(a.logits, a.ldl * el, 2 * el) && aligned_to(a.dlogits, a.ldd * el, 2 * el);
+  const unsigned grid = (unsigned)cdiv(a.T, kRouteThreads / 32);
+  auto go = [&](auto pairs) {
+    constexpr int kPairs = decltype(pairs)::value;
+    return by_bool(a.f32, [&](auto f32) {
+      return by_bool(a.sigmoid, [&](auto sig) {
+        return launch_pdl(moe_route_bwd_kernel<kPairs, decltype(f32)::value, decltype(sig)::value>, grid, kRouteThreads,
+                          0, st, a);
+      });
+    });
+  };
+  const int64_t n = cdiv(a.E, 64);
+  if (n <= 1) return go(std::integral_constant<int, 1>{});
+  if (n <= 2) return go(std::integral_constant<int, 2>{});
+  if (n <= 3) return go(std::integral_constant<int, 3>{});
+  if (n <= 4) return go(std::integral_constant<int, 4>{});
+  if (n <= 8) return go(std::integral_constant<int, 8>{});
+  return go(std::integral_constant<int, 16>{});
 }
 
 cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
