@@ -675,8 +675,10 @@ bfp8_status bfp8_gemm_routed_1x128_128x128(const void* qa, int64_t lda, const fl
   if (st != BFP8_OK) return st;
   if ((st = check_dims(fn, R, N, K)) != BFP8_OK) return st;
   CHECK_ARG(E >= 1 && E <= kMaxGroups, "%s: E=%lld must be in [1, %d]", fn, (long long)E, kMaxGroups);
+  CHECK_ARG(E * N < kMaxDim, "%s: E * N must stay below 2^31", fn);
   if (R == 0 || N == 0) return BFP8_OK;
-  CHECK_ARG(offs && c && (K == 0 || (qb && sb && (T == 0 || (qa && sa)))), "%s: null pointer", fn);
+  CHECK_ARG(T > 0, "%s: rows without tokens (T=0, R=%lld)", fn, (long long)R);
+  CHECK_ARG(offs && c && (K == 0 || (qb && sb && qa && sa)), "%s: null pointer", fn);
   CHECK_ARG(al16(qa) && al16(qb), "%s: qa and qb must be 16-byte aligned", fn);
   CHECK_ARG(al4(sa) && al4(sb) && al4(offs) && al4(src) && al2(c), "%s: misaligned pointer", fn);
   CHECK_ARG(lda >= K && lda % 16 == 0, "%s: lda=%lld must be >= K=%lld and a multiple of 16", fn, (long long)lda,
@@ -689,11 +691,13 @@ bfp8_status bfp8_gemm_routed_1x128_128x128(const void* qa, int64_t lda, const fl
   CHECK_ARG(ldc >= N, "%s: ldc=%lld < N=%lld", fn, (long long)ldc, (long long)N);
   int sms = 0;
   if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const char* msg = nullptr;
   const cudaError_t e = launch_gemm_routed(
       GemmRoutedArgs{(const uint8_t*)qa, lda, sa, ldsa, T, (const uint8_t*)qb, ldb, sb, ldsb, offs, E, src, (int)k,
                      (uint16_t*)c, ldc, R, N, K},
-      sms, (cudaStream_t)stream);
-  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+      sms, (cudaStream_t)stream, &msg);
+  if (e != cudaSuccess) return msg ? fail(BFP8_ERR_INVALID_ARG, "%s: %s", fn, msg) : cuda_fail(e, fn);
+  return BFP8_OK;
 }
 
 bfp8_status bfp8_debug_gemm_stall(const void* qa, int64_t lda, const float* sa, int64_t ldsa, const void* qb,
@@ -723,15 +727,15 @@ bfp8_status bfp8_check_device_errors(bfp8_stream_t stream) {
   if (st != BFP8_OK) return st;
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: stream synchronize");
-  uint32_t bits = 0, qbits = 0;
+  uint32_t bits = 0, qbits = 0, dbits = 0, rbits = 0;
   e = gemm_read_errors(&bits);
-  if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: read flag");
-  e = quant_read_errors(&qbits);
+  if (e == cudaSuccess) e = quant_read_errors(&qbits);
+  if (e == cudaSuccess) e = dispatch_read_errors(&dbits);
+  if (e == cudaSuccess) e = routed_read_errors(&rbits);
   if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: read flag");
   if (qbits) return fail(BFP8_ERR_TIMEOUT, "quantisation kernel gave up waiting for its TMA tile loads");
-  e = dispatch_read_errors(&qbits);
-  if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: read flag");
-  if (qbits) return fail(BFP8_ERR_TIMEOUT, "dispatch kernel gave up waiting for its gathered rows");
+  if (dbits) return fail(BFP8_ERR_TIMEOUT, "dispatch kernel gave up waiting for its gathered rows");
+  if (rbits) return fail(BFP8_ERR_TIMEOUT, "routed product gave up waiting for its weights");
   if (bits & 64u)  // kErrGroupOffsets
     return fail(BFP8_ERR_INVALID_ARG,
                 "grouped GEMM: expert offsets decreasing, outside [0, total tokens], or (weight gradient) "

@@ -239,7 +239,8 @@ struct GemmRoutedArgs {
   uint16_t* c;
   int64_t ldc, R, N, K;
 };
-cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_t st, const char** msg);
+cudaError_t routed_read_errors(uint32_t* out);  // reads and clears the kernel's error word (synchronous)
 
 // Reads and clears the device error word of the GEMM kernels (synchronous).
 cudaError_t gemm_read_errors(uint32_t* out);

@@ -421,14 +421,15 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
 // ---------------------------------------------------------------------------
 //
 // One launch of one cluster.  Warp w of the cluster takes a contiguous run of
-// slots, 32 at a time: match_any groups the lanes of one expert, whose rank
-// among them follows the lane, so the order within an expert is the slots'
-// order and every run gives the same plan.  Counts a warp, then prefix sums:
-// over the warps of a CTA, over the CTAs of the cluster through distributed
-// shared memory, over the experts' aligned counts.  A second walk places the
-// slots.
+// slots, 32 at a time: the lanes of one expert find each other by ballots over
+// the bits of its number (a match instruction is several times slower here),
+// and their rank among them follows the lane, so the order within an expert is
+// the slots' order and every launch gives the same plan.  A slot's rank within
+// its warp's run waits in row.  Then prefix sums of the counts: over the warps
+// of a CTA, over the CTAs of the cluster through distributed shared memory,
+// over the experts' aligned counts; and the slots' rows follow.
 __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
-  extern __shared__ uint32_t s_cnt[];  // [32 warps][E] counts, then first ranks; [E] CTA totals; [E + 1] offsets
+  extern __shared__ uint32_t s_cnt[];  // [32 warps][E] counts, then first rows; [E] CTA totals
   __shared__ uint32_t s_scan[32];
   pdl_launch_dependents();
   pdl_wait();
@@ -436,19 +437,38 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
   const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;  // the grid is one cluster
   uint32_t* mine = s_cnt + warp * E;
   uint32_t* s_tot = s_cnt + 32 * E;
-  uint32_t* s_off = s_tot + E;
-  for (int i = tid; i < 32 * E; i += kPlanThreads) s_cnt[i] = 0;
-  __syncthreads();
   const int64_t n = a.n;
   const int64_t run = cdiv(cdiv(n, (int64_t)ctas * 32), 32) * 32;  // slots a warp, a multiple of 32
   const int64_t lo = ((int64_t)rank * 32 + warp) * run, hi = lo + run < n ? lo + run : n;
-  for (int64_t i = lo; i < hi; i += 32) {
-    const int64_t slot = i + lane;
-    const int e = slot < hi ? a.idx[slot] : -1;
-    const bool ok = e >= 0 && e < E;
-    const uint32_t peers = __match_any_sync(kFull, ok ? e : -1);
-    if (ok && lane == __ffs(peers) - 1) mine[e] += (uint32_t)__popc(peers);
-    __syncwarp();
+  for (int i = lane; i < E; i += 32) mine[i] = 0;
+  // padding everywhere; the barriers below come before the slots' own entries
+  for (int64_t r = (int64_t)rank * kPlanThreads + tid; r < a.R; r += (int64_t)ctas * kPlanThreads) a.src[r] = -1;
+  __syncwarp();
+  const int bits = 32 - __clz(E);  // E itself stands for "nowhere"
+  constexpr int kAhead = 4;        // groups of 32 slots whose experts are read at once
+  for (int64_t i0 = lo; i0 < hi; i0 += 32 * kAhead) {
+    int e[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t slot = i0 + 32 * u + lane;
+      e[u] = slot < hi ? __ldg(a.idx + slot) : -1;
+      if ((uint32_t)e[u] >= (uint32_t)E) e[u] = E;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t slot = i0 + 32 * u + lane;
+      uint32_t peers = kFull;
+      for (int b = 0; b < bits; ++b) {
+        const uint32_t vote = __ballot_sync(kFull, (e[u] >> b) & 1);
+        peers &= (e[u] >> b) & 1 ? vote : ~vote;
+      }
+      const bool ok = e[u] < E;
+      const uint32_t base = ok ? mine[e[u]] : 0u, lower = (uint32_t)__popc(peers & ((1u << lane) - 1u));
+      __syncwarp();
+      if (ok && lower == 0) mine[e[u]] = base + (uint32_t)__popc(peers);
+      __syncwarp();
+      if (slot < hi) a.row[slot] = (int32_t)(base + lower);
+    }
   }
   __syncthreads();
   if (tid < E) {  // counts of the warps -> first ranks within the CTA
@@ -474,6 +494,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
         if (c < rank) before += v;
         total += v;
       }
+    cluster_sync_all();  // every CTA has read the totals: they may be replaced, and a CTA may leave
   } else if (tid < E) {
     total = s_tot[tid];
   }
@@ -500,7 +521,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
   __syncthreads();
   const uint32_t first = inc - rows + (warp ? s_scan[warp - 1] : 0u);
   if (tid < E) {
-    s_off[tid] = first + before;  // of this CTA's first slot of the expert
+    s_tot[tid] = first + before;  // row of this CTA's first slot of the expert
     if (rank == 0) {
       a.offs[tid] = (int32_t)first;
       a.counts[tid] = (int32_t)total;
@@ -508,25 +529,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
     }
   }
   __syncthreads();
-  // padding rows: within the experts (split over the CTAs), and past the last one
-  if (tid < E)
-    for (uint32_t r = first + total + (uint32_t)rank; r < first + rows; r += (uint32_t)ctas) a.src[r] = -1;
-  const int64_t end = s_scan[31];
-  for (int64_t r = end + (int64_t)rank * kPlanThreads + tid; r < a.R; r += (int64_t)ctas * kPlanThreads) a.src[r] = -1;
-  for (int64_t i = lo; i < hi; i += 32) {
-    const int64_t slot = i + lane;
-    const int e = slot < hi ? a.idx[slot] : -1;
-    const bool ok = e >= 0 && e < E;
-    const uint32_t peers = __match_any_sync(kFull, ok ? e : -1);
-    int r = -1;
-    if (ok) r = (int)(s_off[e] + mine[e] + (uint32_t)__popc(peers & ((1u << lane) - 1u)));
-    __syncwarp();
-    if (ok && lane == __ffs(peers) - 1) mine[e] += (uint32_t)__popc(peers);
-    __syncwarp();
-    if (slot < hi) a.row[slot] = r;
+#pragma unroll 4
+  for (int64_t slot = lo + lane; slot < hi; slot += 32) {
+    const int e = __ldg(a.idx + slot);
+    const bool ok = (uint32_t)e < (uint32_t)E;
+    const int r = ok ? a.row[slot] + (int)(mine[e] + s_tot[e]) : -1;
+    a.row[slot] = r;
     if (ok) a.src[r] = (int32_t)slot;
   }
-  if (ctas > 1) cluster_sync_all();  // no CTA leaves while a peer reads its totals
 }
 
 // ---------------------------------------------------------------------------
@@ -750,12 +760,12 @@ cudaError_t launch_moe_route_bwd(const RouteBwdArgs& args, cudaStream_t st) {
 }
 
 cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
-  const size_t smem = (size_t)(34 * a.E + 1) * 4;
+  const size_t smem = (size_t)(33 * a.E) * 4;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
     attr_err = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (34 * kMaxGroups + 1) * 4);
+                                    33 * kMaxGroups * 4);
   });
   if (attr_err != cudaSuccess) return attr_err;
   int ctas = 1;

@@ -7,203 +7,516 @@
 // P_kb the e4m3 x e4m3 partial product, promoted per K-block into fp32.
 //
 // Each reached expert's weight is read once from memory, which is what bounds
-// the product here.  So nothing is staged: a warp's matrix instruction takes
-// 16 rows of W (its A) and 8 tokens (its B) straight from the registers that
-// the loads filled.  A lane holds 16 consecutive bytes of a row per load and
-// uses them as the k-slices of two instructions: the sum over k does not care
-// which k a slice holds as long as both operands agree, so no byte moves
-// between lanes.  The warps of a CTA split a 16-row block's K-blocks and add
-// their fp32 sums in warp order through shared memory.
+// the product; so the operands swap places in the MMA, as in the dense GEMM
+// for few rows: 128 rows of W are the instruction's A, streamed by TMA through
+// a ring that holds most of an SM's shared memory, and R = 16, 32 or 64 tokens
+// its B, gathered by TMA from the tokens' codes (four rows a gather; past the
+// expert's last row zeros).  A persistent CTA per SM walks a contiguous run of
+// 128-row tiles over all reached experts without draining the ring in between;
+// an expert with more than R rows walks its weight again for the next R, from
+// L2.  Where the batch is so small that the tiles leave SMs idle (and its rows
+// are few enough for one walk), each tile's K-blocks are split over a cluster
+// instead and the partial sums added in rank order through distributed shared
+// memory.
+//
+//   warp 0      producer: lane 0 W's tile, lanes l < R/4 four tokens each
+//   warps 1, 3  MMA issuers (M = 128, N = R) on alternate K-blocks
+//   warp 2      a_s of the tokens and b_s of the tile, per K-block
+//   warps 4-7   promotion (lane n: column n of the tile, its R tokens), stores
+// Every mbarrier wait is bounded; a role that gives up sets the abort flag, the
+// others leave their loops, and copies and MMAs in flight finish before the
+// CTA exits.
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include <mutex>
+
 #include "common.cuh"
 #include "kernels.h"
 
 namespace bfp8 {
 
+static __device__ uint32_t g_routed_error;
+
 namespace {
 
+constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kRpThreads = 256;
-constexpr int kRpWarps = kRpThreads / 32;
-constexpr int kRpRows = 16;   // rows of W an item
-constexpr int kRpUnroll = 2;  // K-blocks in flight a warp
+constexpr int kRpTile = 128;  // rows of W a tile
 
-// D (16 x 8, fp32) += A (16 x 32 e4m3, row) B (32 x 8 e4m3, column)
-__device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1) {
+template <int R>
+struct RpCfg {
+  static_assert(R == 16 || R == 32 || R == 64, "tokens of one walk");
+  static constexpr int kStages = R == 16 ? 11 : R == 32 ? 10 : 8;
+  static constexpr int kBufs = R == 64 ? 4 : 8;             // R-column partial products in tensor memory
+  static constexpr int kTmemCols = kBufs * R;               // 128 or 256
+  static constexpr int kWBytes = kRpTile * kBlock;          // 16 KiB
+  static constexpr int kXBytes = R * kBlock;
+  static constexpr int kSlotBytes = (4 * R + 16 + 127) / 128 * 128;  // a_s[R], then b_s at byte 4R
+  static constexpr int kOffX = kStages * kWBytes;
+  static constexpr int kOffSlot = kOffX + kStages * kXBytes;
+  static constexpr int kOffExpert = kOffSlot + kStages * kSlotBytes;
+  static constexpr int kOffBar = kOffExpert + kMaxGroups * 4;
+  // full[S] empty[S] sfull[S] sempty[S] tfull[T] tempty[T] drain
+  static constexpr int kNumBars = 4 * kStages + 2 * kBufs + 1;
+  static constexpr int kOffMisc = kOffBar + (kNumBars + 1) / 2 * 16;  // tensor memory's address, abort flag, a zero
+  static constexpr int kOffCount = kOffMisc + 16;
+  static constexpr int kSmemBytes = kOffCount + 4 * (kRpThreads / 32) + 1024;
+  static_assert(kRpTile * R * 4 <= kStages * kWBytes, "the partial sums of a split tile fit in the W stages");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+};
+
+// Four rows y0 .. y3 x 128 bytes from byte x on, one after the other at dst; rows past the tensor's are zeros.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y0,
+                                            int32_t y1, int32_t y2, int32_t y3) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
+      : "memory");
 }
 
-// The first n (0 .. 16) bytes of v, the others zero.
-__device__ __forceinline__ uint4 first_bytes(uint4 v, int n) {
-  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int b = n - 4 * i;
-    if (b < 4) w[i] &= b <= 0 ? 0u : (1u << (8 * b)) - 1u;
-  }
+__device__ __forceinline__ float lds32_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
+}
+
+// The A row of sorted row m (before r1): its slot's token, or m itself; a.T (past A, read as zeros) where there is none.
+__device__ __forceinline__ int token_of(const GemmRoutedArgs& a, int64_t m, int64_t r1) {
+  if (m >= r1) return (int)a.T;
+  int64_t t = m;
+  if (a.src) {
+    const int slot = __ldg(a.src + m);
+    t = slot >= 0 ? (int64_t)((uint32_t)slot / (uint32_t)a.k) : a.T;
+  }
+  return (int)(t < a.T ? t : a.T);
 }
 
 }  // namespace
 
-// TN: 8-token blocks an item holds at once; an expert with more rows walks W
-// again for the next 8 TN.
-template <int TN>
-__global__ void __launch_bounds__(kRpThreads, 2) gemm_routed_kernel(const GemmRoutedArgs a) {
-  __shared__ int s_expert[kMaxGroups];
-  __shared__ int s_count[kRpWarps];
-  __shared__ float s_part[kRpWarps][kRpRows][8 * TN + 1];
-  __shared__ int s_tok[8 * TN];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+template <int R>
+__global__ void __launch_bounds__(kRpThreads, 1)
+    gemm_routed_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUtensorMap tma_x,
+                       const GemmRoutedArgs a, const int splits) {
+  using Cfg = RpCfg<R>;
+  constexpr int ST = Cfg::kStages, NT = Cfg::kBufs;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem), sX = sbase + Cfg::kOffX, sSlot = sbase + Cfg::kOffSlot;
+  const uint32_t full0 = sbase + Cfg::kOffBar, empty0 = full0 + 8 * ST, sfull0 = empty0 + 8 * ST,
+                 sempty0 = sfull0 + 8 * ST, tfull0 = sempty0 + 8 * ST, tempty0 = tfull0 + 8 * NT,
+                 drain = tempty0 + 8 * NT;
+  int* s_expert = reinterpret_cast<int*>(smem + Cfg::kOffExpert);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
+  volatile int* never = abort_flag + 1;
+  int* s_count = reinterpret_cast<int*>(smem + Cfg::kOffCount);
+  const int tid = (int)threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
   const int E = (int)a.E;
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 1);
+      mbar_init(sfull0 + 8 * i, 32);  // one cp.async arrival per loader lane
+      mbar_init(sempty0 + 8 * i, 4);  // the promotion warps
+    }
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(tfull0 + 8 * i, 1);
+      mbar_init(tempty0 + 8 * i, 4);
+    }
+    mbar_init(drain, 2);  // one commit per issuer
+    *abort_flag = 0;
+    *never = 0;
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    if (a.K > 0) {
+      tma_prefetch_desc(&tma_w);
+      tma_prefetch_desc(&tma_x);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_wait();
   // the experts that hold rows, in order
   int reached = 0;
   for (int e0 = 0; e0 < E; e0 += kRpThreads) {
     const int e = e0 + tid;
     const bool on = e < E && __ldg(a.offs + e + 1) > __ldg(a.offs + e);
-    const uint32_t vote = __ballot_sync(0xffffffffu, on);
+    const uint32_t vote = __ballot_sync(kAll, on);
     if (lane == 0) s_count[warp] = __popc(vote);
     __syncthreads();
     int at = reached;
-    for (int w = 0; w < kRpWarps; ++w) {
+#pragma unroll
+    for (int w = 0; w < kRpThreads / 32; ++w) {
       if (w < warp) at += s_count[w];
       reached += s_count[w];
     }
     if (on) s_expert[at + __popc(vote & ((1u << lane) - 1u))] = e;
     __syncthreads();
   }
-  const int64_t Kb = cdiv(a.K, kBlock), Nb = cdiv(a.N, kBlock);
-  const int blocks = (int)cdiv(a.N, kRpRows);
-  const int64_t items = (int64_t)reached * blocks;
-  const int g = lane >> 2, q = lane & 3;
-  const bool k_tail = a.K % kBlock != 0;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int e = s_expert[item / blocks];
-    const int64_t n0 = (item % blocks) * kRpRows;
-    int64_t r0 = __ldg(a.offs + e), r1 = __ldg(a.offs + e + 1);
-    r0 = r0 < 0 ? 0 : r0;
-    r1 = r1 > a.R ? a.R : r1;
-    const int64_t na = n0 + g < a.N ? n0 + g : a.N - 1, nb = n0 + g + 8 < a.N ? n0 + g + 8 : a.N - 1;
-    const uint8_t* wa = a.qb + (e * a.N + na) * a.ldb + q * 16;
-    const uint8_t* wb = a.qb + (e * a.N + nb) * a.ldb + q * 16;
-    const float* sb = a.sb + (e * Nb + n0 / kBlock) * a.ldsb;
-    for (int64_t m0 = r0; m0 < r1; m0 += 8 * TN) {
-      // the A row of each of the item's tokens (-1: zeros)
-      if (tid < 8 * TN) {
-        int64_t tok = -1;
-        if (m0 + tid < r1) {
-          tok = m0 + tid;
-          if (a.src) {
-            const int slot = __ldg(a.src + m0 + tid);
-            tok = slot >= 0 ? (int64_t)((uint32_t)slot / (uint32_t)a.k) : -1;
-          }
-          if (tok >= a.T) tok = -1;
-        }
-        s_tok[tid] = (int)tok;
-      }
-      __syncthreads();
-      const uint8_t* xp[TN];
-      int tok[TN];
-      const float* sa0[TN];
-      const float* sa1[TN];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        tok[j] = s_tok[8 * j + g];
-        xp[j] = a.qa + (int64_t)max(tok[j], 0) * a.lda + q * 16;
-        sa0[j] = a.sa + max(s_tok[8 * j + 2 * q], 0);
-        sa1[j] = a.sa + max(s_tok[8 * j + 2 * q + 1], 0);
-      }
-      float acc[TN][4];
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-      for (int64_t kb0 = warp; kb0 < Kb; kb0 += kRpWarps * kRpUnroll) {
-        uint4 w[kRpUnroll][4], x[kRpUnroll][TN][2];
-        float s0[kRpUnroll][TN], s1[kRpUnroll][TN];
-#pragma unroll
-        for (int u = 0; u < kRpUnroll; ++u) {
-          const int64_t kb = kb0 + u * kRpWarps;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int64_t k = kb * kBlock + h * 64;
-            const bool in = k + q * 16 < a.K;
-            w[u][2 * h] = in ? ld_nc_v4(wa + k) : make_uint4(0, 0, 0, 0);
-            w[u][2 * h + 1] = in ? ld_nc_v4(wb + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-              x[u][j][h] = in && tok[j] >= 0 ? __ldg(reinterpret_cast<const uint4*>(xp[j] + k)) : make_uint4(0, 0, 0, 0);
-          }
-          const float b = kb < Kb ? __ldg(sb + kb) : 0.0f;
-#pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            s0[u][j] = kb < Kb ? __ldg(sa0[j] + kb * a.ldsa) * b : 0.0f;
-            s1[u][j] = kb < Kb ? __ldg(sa1[j] + kb * a.ldsa) * b : 0.0f;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kRpUnroll; ++u) {
-          const int64_t kb = kb0 + u * kRpWarps;
-          if (k_tail && kb >= Kb - 1) {  // the bytes past K are not data
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int64_t left = a.K - (kb * kBlock + h * 64 + q * 16);
-              const int n = left < 0 ? 0 : left > 16 ? 16 : (int)left;
-              w[u][2 * h] = first_bytes(w[u][2 * h], n);
-              w[u][2 * h + 1] = first_bytes(w[u][2 * h + 1], n);
-#pragma unroll
-              for (int j = 0; j < TN; ++j) x[u][j][h] = first_bytes(x[u][j][h], n);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < TN; ++j) {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 A = w[u][2 * h], B = w[u][2 * h + 1], X = x[u][j][h];
-              mma_16x8x32(d, A.x, B.x, A.y, B.y, X.x, X.y);
-              mma_16x8x32(d, A.z, B.z, A.w, B.w, X.z, X.w);
-            }
-            acc[j][0] = fmaf(s0[u][j], d[0], acc[j][0]);
-            acc[j][1] = fmaf(s1[u][j], d[1], acc[j][1]);
-            acc[j][2] = fmaf(s0[u][j], d[2], acc[j][2]);
-            acc[j][3] = fmaf(s1[u][j], d[3], acc[j][3]);
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        s_part[warp][g][8 * j + 2 * q] = acc[j][0];
-        s_part[warp][g][8 * j + 2 * q + 1] = acc[j][1];
-        s_part[warp][g + 8][8 * j + 2 * q] = acc[j][2];
-        s_part[warp][g + 8][8 * j + 2 * q + 1] = acc[j][3];
-      }
-      __syncthreads();
-      for (int i = tid; i < kRpRows * 8 * TN; i += kRpThreads) {
-        const int nl = i % kRpRows, m = i / kRpRows;
-        float sum = s_part[0][nl][m];
-#pragma unroll
-        for (int v = 1; v < kRpWarps; ++v) sum += s_part[v][nl][m];
-        if (m0 + m < r1 && n0 + nl < a.N)
-          a.c[(m0 + m) * a.ldc + n0 + nl] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
-      }
-      __syncthreads();  // the sums and the token list are free again
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  const int Kb = (int)cdiv(a.K, kBlock), blocks = (int)cdiv(a.N, kRpTile);
+  const int64_t tiles = (int64_t)reached * blocks;
+  // this CTA's tiles, and its K-blocks of each (split = the rank in the cluster)
+  const int group = (int)blockIdx.x / splits, groups = (int)gridDim.x / splits, split = (int)blockIdx.x % splits;
+  const int64_t first = tiles * group / groups, last = tiles * (group + 1) / groups;
+  const int kb0 = smallm_kb_lo(split, splits, Kb), kbn = smallm_kb_lo(split + 1, splits, Kb) - kb0;
+
+  // One walk: R rows of an expert against a 128-row tile of its weight.  Every
+  // role goes through the same walks in the same order.
+  struct Walk {
+    int64_t tile, m0, r1;
+    int e, block;
+  };
+  auto enter = [&](Walk& w) {  // the first walk of tile w.tile (tiles of experts clamped to no rows are passed over)
+    for (; w.tile < last; ++w.tile) {
+      w.e = s_expert[w.tile / blocks];
+      w.block = (int)(w.tile % blocks);
+      w.m0 = max(__ldg(a.offs + w.e), 0);
+      w.r1 = min((int64_t)__ldg(a.offs + w.e + 1), a.R);
+      if (w.m0 < w.r1) return;
     }
+  };
+  auto next = [&](Walk& w) {
+    w.m0 += R;
+    if (w.m0 < w.r1) return;
+    ++w.tile;
+    enter(w);
+  };
+  auto fail = [&](uint32_t code) {
+    if (!*abort_flag) atomicOr(&g_routed_error, code);
+    *abort_flag = 1;
+  };
+  Walk w{first, 0, 0, 0, 0};
+  enter(w);
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    int n = 0;  // K-blocks issued
+    int at_e = -1;
+    int64_t at_m = -1;
+    int tok[4] = {};
+    for (; w.tile < last && ok; next(w)) {
+      if (w.e != at_e || w.m0 != at_m) {
+        at_e = w.e, at_m = w.m0;
+        if (lane < R / 4) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tok[i] = token_of(a, w.m0 + 4 * lane + i, w.r1);
+        }
+      }
+      const int row = w.e * (int)a.N + w.block * kRpTile;
+      for (int j = 0; j < kbn; ++j, ++n) {
+        const int st = n % ST;
+        ok = mbar_wait_bounded(empty0 + 8 * st, (uint32_t)((n / ST) & 1) ^ 1u, kWaitLimitNs, abort_flag);
+        if (!__all_sync(kAll, ok)) {
+          if (lane == 0) fail(1u);
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(Cfg::kWBytes + Cfg::kXBytes));
+          tma_load_2d(sbase + (uint32_t)(st * Cfg::kWBytes), &tma_w, full0 + 8 * st, (kb0 + j) * kBlock, row);
+        }
+        __syncwarp();
+        if (lane < R / 4)
+          tma_gather4(sX + (uint32_t)(st * Cfg::kXBytes + lane * 512), &tma_x, full0 + 8 * st, (kb0 + j) * kBlock, tok[0],
+                      tok[1], tok[2], tok[3]);
+      }
+    }
+    if (!ok && lane == 0)  // copies already issued land before this CTA's shared memory goes away
+      for (int i = n > ST ? n - ST : 0; i < n; ++i)
+        mbar_wait_bounded(full0 + 8 * (i % ST), (uint32_t)((i / ST) & 1), kWaitLimitNs, never);
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ MMA issuers (alternate K-blocks)
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(kRpTile, R);
+      int n = 0;
+      for (; w.tile < last && ok; next(w)) {
+        for (int j = 0; j < kbn && ok; ++j, ++n) {
+          if ((n & 1) != (warp == 1 ? 0 : 1)) continue;
+          const int st = n % ST, buf = n % NT;
+          ok = mbar_spin_bounded(tempty0 + 8 * buf, (uint32_t)((n / NT) & 1) ^ 1u, kWaitLimitNs, abort_flag) &&
+               mbar_spin_bounded(full0 + 8 * st, (uint32_t)((n / ST) & 1), kWaitLimitNs, abort_flag);
+          if (!ok) {
+            fail(2u);
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = desc_kmajor_sw128(sbase + (uint32_t)(st * Cfg::kWBytes));
+          const uint64_t db = desc_kmajor_sw128(sX + (uint32_t)(st * Cfg::kXBytes));
+#pragma unroll
+          for (int k = 0; k < kBlock / 32; ++k)
+            mma_e4m3(tmem_base + (uint32_t)(buf * R), da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), idesc,
+                     k > 0 ? 1u : 0u);
+          mma_commit(empty0 + 8 * st);
+          mma_commit(tfull0 + 8 * buf);
+        }
+      }
+      // every MMA issued completes before tensor memory is released
+      mma_commit(drain);
+      if (!mbar_wait_bounded(drain, 0, kWaitLimitNs, never)) fail(4u);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scale loader
+    const int Nb = (int)cdiv(a.N, kBlock);
+    constexpr int kPer = (R + 31) / 32;
+    int n = 0, at_e = -1;
+    int64_t at_m = -1;
+    int tok[kPer] = {};
+    for (; w.tile < last && ok; next(w)) {
+      if (w.e != at_e || w.m0 != at_m) {
+        at_e = w.e, at_m = w.m0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) tok[i] = lane + 32 * i < R ? token_of(a, w.m0 + lane + 32 * i, w.r1) : (int)a.T;
+      }
+      const float* sb = a.sb + ((int64_t)w.e * Nb + w.block) * a.ldsb;
+      for (int j = 0; j < kbn; ++j, ++n) {
+        const int st = n % ST, kb = kb0 + j;
+        ok = mbar_wait_bounded(sempty0 + 8 * st, (uint32_t)((n / ST) & 1) ^ 1u, kWaitLimitNs, abort_flag);
+        if (!__all_sync(kAll, ok)) {
+          if (lane == 0) fail(8u);
+          ok = false;
+          break;
+        }
+        const uint32_t slot = sSlot + (uint32_t)(st * Cfg::kSlotBytes);
+        const float* sa = a.sa + (int64_t)kb * a.ldsa;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const bool in = (int64_t)tok[i] < a.T;  // zeros for no token
+          if (lane + 32 * i < R) cp_async_4(slot + 4u * (uint32_t)(lane + 32 * i), in ? sa + tok[i] : sb, in ? 4u : 0u);
+        }
+        if (lane == 0) cp_async_4(slot + 4u * R, sb + kb, 4u);
+        cp_async_mbar_arrive(sfull0 + 8 * st);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // ------------------------------------------------------------ promotion
+    const int nl = 32 * (warp - 4) + lane;  // tensor-memory lane = column nl of the tile
+    const uint32_t lane_base = (uint32_t)(32 * (warp - 4)) << 16;
+    int n = 0;
+    for (; w.tile < last && ok; next(w)) {
+      float acc[R];
+#pragma unroll
+      for (int m = 0; m < R; ++m) acc[m] = 0.0f;
+      for (int j = 0; j < kbn; ++j, ++n) {
+        const int st = n % ST, buf = n % NT;
+        ok = mbar_wait_bounded(sfull0 + 8 * st, (uint32_t)((n / ST) & 1), kWaitLimitNs, abort_flag) &&
+             mbar_wait_bounded(tfull0 + 8 * buf, (uint32_t)((n / NT) & 1), kWaitLimitNs, abort_flag);
+        if (!__all_sync(kAll, ok)) {
+          if (lane == 0) fail(16u);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t slot = sSlot + (uint32_t)(st * Cfg::kSlotBytes);
+        float bsc;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(bsc) : "r"(slot + 4u * R));
+        const uint64_t b2 = f2_pack(bsc, bsc);
+        constexpr int CH = R < 32 ? R : 32;  // columns per tensor-memory load
+#pragma unroll
+        for (int c = 0; c < R / CH; ++c) {
+          uint32_t r[CH];
+          const uint32_t taddr = tmem_base + lane_base + (uint32_t)(buf * R + c * CH);
+          if constexpr (CH == 32) tmem_ld_32x32b_x32(taddr, r);
+          else tmem_ld_32x32b_x16(taddr, r);
+          tmem_ld_wait();
+          tmem_regs_after_wait(r);
+          // acc[m] += (a_s[m] * b_s) * P[m], two tokens per fp32x2 operation
+#pragma unroll
+          for (int q = 0; q < CH / 4; ++q) {
+            float4 a4;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(a4.x), "=f"(a4.y), "=f"(a4.z), "=f"(a4.w)
+                         : "r"(slot + 4u * (uint32_t)(c * CH + 4 * q)));
+            const int m = c * CH + 4 * q;
+            const uint64_t s01 = f2_mul(f2_pack(a4.x, a4.y), b2), s23 = f2_mul(f2_pack(a4.z, a4.w), b2);
+            f2_unpack(f2_fma(s01, f2_pack(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])),
+                             f2_pack(acc[m], acc[m + 1])),
+                      acc[m], acc[m + 1]);
+            f2_unpack(f2_fma(s23, f2_pack(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])),
+                             f2_pack(acc[m + 2], acc[m + 3])),
+                      acc[m + 2], acc[m + 3]);
+          }
+        }
+        // the partial and the scales have been read: release the buffer and the slot
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(tempty0 + 8 * buf);
+          mbar_arrive(sempty0 + 8 * st);
+        }
+      }
+      if (!ok) break;
+      const int64_t col = (int64_t)w.block * kRpTile + nl;
+      if (splits == 1) {
+        if (col < a.N) {
+          uint16_t* c = a.c + w.m0 * a.ldc + col;
+          const int rows = (int)min(w.r1 - w.m0, (int64_t)R);
+#pragma unroll
+          for (int m = 0; m < R; ++m)
+            if (m < rows) c[(int64_t)m * a.ldc] = (uint16_t)(pack_bf16x2(acc[m], 0.0f) & 0xFFFFu);
+        }
+      } else {
+        // the CTA's only walk (every MMA has completed, every copy has landed): the sums go into the W stages
+        float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int m = 0; m < R; ++m) part[m * kRpTile + nl] = acc[m];
+      }
+    }
+  }
+  __syncwarp();
+  if (splits > 1) {
+    // Every thread of every CTA of the cluster reaches both barriers (every
+    // wait before them is bounded): the first makes the partial sums visible,
+    // the second keeps each CTA resident until no peer reads them any more.
+    cluster_sync_all();
+    if (warp >= 4 && first < last) {
+      Walk f{first, 0, 0, 0, 0};
+      enter(f);
+      const int nl = 32 * (warp - 4) + lane, per = R / splits, m_lo = split * per;
+      const int64_t col = (int64_t)f.block * kRpTile + nl;
+      for (int m = m_lo; m < m_lo + per; ++m) {
+        float sum = 0.0f;
+        for (int s = 0; s < splits; ++s)
+          sum += lds32_cluster(mapa_shared(sbase + 4u * (uint32_t)(m * kRpTile + nl), (uint32_t)s));
+        if (f.tile < last && col < a.N && f.m0 + m < f.r1)
+          a.c[(f.m0 + m) * a.ldc + col] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Cfg::kTmemCols);
   }
 }
 
-cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_t st) {
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+static PFN_cuTensorMapEncodeTiled_v12000 rp_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// Row-major [rows, inner] bytes with row stride ld: boxes of 128 bytes x box_rows rows, 128-byte swizzled, zeros
+// outside.
+static bool rp_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t ld, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {kBlock, (cuuint32_t)box_rows};
+  cuuint32_t elem[2] = {1, 1};
+  return rp_encode_fn() != nullptr &&
+         rp_encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTAs a tile's K-blocks are split over: 8, 4 or 2, the most for which `tiles`
+// clusters are resident at once with at least four K-blocks a CTA (below that
+// the hand-over of the partial sums costs more than the K-blocks it spreads).
+template <int R>
+static int rp_splits(int64_t tiles, int Kb, int num_sms) {
+  static std::once_flag once;
+  static int max_clusters[9] = {};
+  std::call_once(once, [] {
+    for (int s = 2; s <= 8; s *= 2) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(s * 16));
+      cfg.blockDim = dim3(kRpThreads);
+      cfg.dynamicSmemBytes = RpCfg<R>::kSmemBytes;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)s;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, gemm_routed_kernel<R>, &cfg) == cudaSuccess) max_clusters[s] = n;
+    }
+    (void)cudaGetLastError();  // a size the device refuses leaves no error behind
+  });
+  for (int s = 8; s >= 2; s /= 2)
+    if (s <= Kb / 4 && tiles * s <= num_sms && tiles <= max_clusters[s]) return s;
+  return 1;
+}
+
+template <int R>
+static cudaError_t run_routed(const CUtensorMap& mw, const CUtensorMap& mx, const GemmRoutedArgs& a, int num_sms,
+                              cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(gemm_routed_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    RpCfg<R>::kSmemBytes);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
   const int64_t reach = a.E < a.R ? a.E : a.R;  // experts that can hold rows
-  const int64_t items = reach * cdiv(a.N, kRpRows), cap = 2 * (int64_t)num_sms;
-  const unsigned grid = (unsigned)(items < cap ? items : cap);
+  const int64_t tiles = reach * cdiv(a.N, kRpTile);
+  // a split tile has one walk: only where every row fits in it
+  const int splits = a.R <= R ? rp_splits<R>(tiles, (int)cdiv(a.K, kBlock), num_sms) : 1;
+  const int64_t groups = splits > 1 || tiles < num_sms ? tiles : num_sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * splits));
+  cfg.blockDim = dim3(kRpThreads);
+  cfg.dynamicSmemBytes = RpCfg<R>::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, gemm_routed_kernel<R>, mw, mx, a, splits);
+}
+
+cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_t st, const char** msg) {
+  CUtensorMap mw, mx;
+  memset(&mw, 0, sizeof(mw));
+  memset(&mx, 0, sizeof(mx));
+  if (a.K > 0 && a.T > 0 && (!rp_map(&mw, a.qb, a.K, a.E * a.N, a.ldb, kRpTile) || !rp_map(&mx, a.qa, a.K, a.T, a.lda, 1))) {
+    *msg = "cuTensorMapEncodeTiled failed for an operand (alignment, stride or size out of range)";
+    return cudaErrorInvalidValue;
+  }
   const int64_t rows = cdiv(a.R, a.E);  // rows an expert, spread evenly
-  if (rows <= 4) return launch_pdl(gemm_routed_kernel<1>, grid, kRpThreads, 0, st, a);
-  if (rows <= 12) return launch_pdl(gemm_routed_kernel<2>, grid, kRpThreads, 0, st, a);
-  return launch_pdl(gemm_routed_kernel<4>, grid, kRpThreads, 0, st, a);
+  if (rows <= 8) return run_routed<16>(mw, mx, a, num_sms, st);
+  if (rows <= 16) return run_routed<32>(mw, mx, a, num_sms, st);
+  return run_routed<64>(mw, mx, a, num_sms, st);
+}
+
+cudaError_t routed_read_errors(uint32_t* out) {
+  uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_routed_error, sizeof(uint32_t));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_routed_error, &zero, sizeof(uint32_t));
 }
 
 }  // namespace bfp8

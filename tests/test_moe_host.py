@@ -109,7 +109,8 @@ def test_routed_product_argument_validation():
                         R=8, N=64, K=256, st=NULL))
     for bad in (dict(E=0), dict(E=1025), dict(k=0), dict(T=-1), dict(R=-1), dict(lda=240), dict(lda=260), dict(ldb=264),
                 dict(ldsa=3), dict(ldsb=1), dict(ldc=63), dict(qa=NULL), dict(sa=NULL), dict(qb=NULL), dict(sb=NULL),
-                dict(offs=NULL), dict(c=NULL), dict(qa=ODD), dict(qb=ODD), dict(src=ODD)):
+                dict(offs=NULL), dict(c=NULL), dict(qa=ODD), dict(qb=ODD), dict(src=ODD), dict(T=0),
+                dict(E=1024, N=1 << 22, ldc=1 << 22)):
         assert call(**bad) == BAD, bad
     assert call(R=0) == B.BFP8_OK
     assert call(N=0) == B.BFP8_OK
