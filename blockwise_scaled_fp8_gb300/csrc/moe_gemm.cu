@@ -11,10 +11,10 @@
 // for few rows: 128 rows of W are the instruction's A, streamed by TMA through
 // a ring that holds most of an SM's shared memory, and R = 16, 32 or 64 tokens
 // its B, gathered by TMA from the tokens' codes (four rows a gather; past the
-// expert's last row zeros).  A persistent CTA per SM walks a contiguous run of
-// 128-row tiles over all reached experts without draining the ring in between;
-// an expert with more than R rows walks its weight again for the next R, from
-// L2.  Where the batch is so small that the tiles leave SMs idle (and its rows
+// expert's last row zeros).  A persistent CTA per SM goes through a contiguous
+// run of (128-row tile, R tokens) walks over all reached experts without
+// draining the ring in between; a tile is walked again for the next R rows of
+// its expert, from L2.  Where the batch is so small that the tiles leave SMs idle (and its rows
 // are few enough for one walk), each tile's K-blocks are split over a cluster
 // instead and the partial sums added in rank order through distributed shared
 // memory.
@@ -56,12 +56,13 @@ struct RpCfg {
   static constexpr int kOffX = kStages * kWBytes;
   static constexpr int kOffSlot = kOffX + kStages * kXBytes;
   static constexpr int kOffExpert = kOffSlot + kStages * kSlotBytes;
-  static constexpr int kOffBar = kOffExpert + kMaxGroups * 4;
+  static constexpr int kOffWalk = kOffExpert + kMaxGroups * 4;      // walks before each reached expert
+  static constexpr int kOffBar = kOffWalk + (kMaxGroups + 4) * 4;
   // full[S] empty[S] sfull[S] sempty[S] tfull[T] tempty[T] drain
   static constexpr int kNumBars = 4 * kStages + 2 * kBufs + 1;
   static constexpr int kOffMisc = kOffBar + (kNumBars + 1) / 2 * 16;  // tensor memory's address, abort flag, a zero
   static constexpr int kOffCount = kOffMisc + 16;
-  static constexpr int kSmemBytes = kOffCount + 4 * (kRpThreads / 32) + 1024;
+  static constexpr int kSmemBytes = kOffCount + 2 * 4 * (kRpThreads / 32) + 1024;
   static_assert(kRpTile * R * 4 <= kStages * kWBytes, "the partial sums of a split tile fit in the W stages");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(kRpThreads, 1)
                  sempty0 = sfull0 + 8 * ST, tfull0 = sempty0 + 8 * ST, tempty0 = tfull0 + 8 * NT,
                  drain = tempty0 + 8 * NT;
   int* s_expert = reinterpret_cast<int*>(smem + Cfg::kOffExpert);
+  int* s_walk = reinterpret_cast<int*>(smem + Cfg::kOffWalk);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Cfg::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffMisc + 4);
   volatile int* never = abort_flag + 1;
@@ -142,62 +144,89 @@ __global__ void __launch_bounds__(kRpThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  // the experts that hold rows, in order
-  int reached = 0;
+  // the experts that hold rows, in order, and the walks (of R rows) before each
+  int reached = 0, walks = 0;
   for (int e0 = 0; e0 < E; e0 += kRpThreads) {
     const int e = e0 + tid;
-    const bool on = e < E && __ldg(a.offs + e + 1) > __ldg(a.offs + e);
-    const uint32_t vote = __ballot_sync(kAll, on);
-    if (lane == 0) s_count[warp] = __popc(vote);
+    int64_t rows = 0;
+    if (e < E) rows = min((int64_t)__ldg(a.offs + e + 1), a.R) - max(__ldg(a.offs + e), 0);
+    const int mine = rows > 0 ? (int)((rows + R - 1) / R) : 0;
+    const uint32_t vote = __ballot_sync(kAll, mine > 0);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) {
+      s_count[warp] = __popc(vote);
+      s_count[kRpThreads / 32 + warp] = inc;
+    }
     __syncthreads();
-    int at = reached;
+    int at = reached, before = walks;
 #pragma unroll
     for (int w = 0; w < kRpThreads / 32; ++w) {
-      if (w < warp) at += s_count[w];
+      if (w < warp) at += s_count[w], before += s_count[kRpThreads / 32 + w];
       reached += s_count[w];
+      walks += s_count[kRpThreads / 32 + w];
     }
-    if (on) s_expert[at + __popc(vote & ((1u << lane) - 1u))] = e;
+    if (mine > 0) {
+      at += __popc(vote & ((1u << lane) - 1u));
+      s_expert[at] = e;
+      s_walk[at] = before + inc - mine;
+    }
     __syncthreads();
   }
+  if (tid == 0) s_walk[reached] = walks;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
   const int Kb = (int)cdiv(a.K, kBlock), blocks = (int)cdiv(a.N, kRpTile);
-  const int64_t tiles = (int64_t)reached * blocks;
-  // this CTA's tiles, and its K-blocks of each (split = the rank in the cluster)
+  // Work: walks, each R rows of an expert against a 128-row tile of its weight;
+  // expert by expert, tile by tile, the walks of one tile side by side (they
+  // share it through L2).  Walk x of the launch belongs to the last reached
+  // expert i with s_walk[i] * blocks <= x.  This CTA takes a contiguous run of
+  // them, and its share of each one's K-blocks (split = the rank in the cluster);
+  // every role goes through the same walks in the same order.
+  // (The launcher keeps the number of walks below 2^31.)
+  const int all = walks * blocks;
   const int group = (int)blockIdx.x / splits, groups = (int)gridDim.x / splits, split = (int)blockIdx.x % splits;
-  const int64_t first = tiles * group / groups, last = tiles * (group + 1) / groups;
+  const int first = (int)((int64_t)all * group / groups), last = (int)((int64_t)all * (group + 1) / groups);
   const int kb0 = smallm_kb_lo(split, splits, Kb), kbn = smallm_kb_lo(split + 1, splits, Kb) - kb0;
-
-  // One walk: R rows of an expert against a 128-row tile of its weight.  Every
-  // role goes through the same walks in the same order.
   struct Walk {
-    int64_t tile, m0, r1;
-    int e, block;
+    int x;
+    int i, e, block;  // reached expert, expert, tile
+    int64_t m0, r1;   // first row, end of the expert's rows
   };
-  auto enter = [&](Walk& w) {  // the first walk of tile w.tile (tiles of experts clamped to no rows are passed over)
-    for (; w.tile < last; ++w.tile) {
-      w.e = s_expert[w.tile / blocks];
-      w.block = (int)(w.tile % blocks);
-      w.m0 = max(__ldg(a.offs + w.e), 0);
-      w.r1 = min((int64_t)__ldg(a.offs + w.e + 1), a.R);
-      if (w.m0 < w.r1) return;
-    }
+  auto enter = [&](Walk& w) {
+    while (w.i + 1 < reached && s_walk[w.i + 1] * blocks <= w.x) ++w.i;
+    const int in = w.x - s_walk[w.i] * blocks, per = s_walk[w.i + 1] - s_walk[w.i];
+    w.e = s_expert[w.i];
+    w.block = per == 1 ? in : in / per;
+    w.m0 = max(__ldg(a.offs + w.e), 0) + (int64_t)(in - w.block * per) * R;
+    w.r1 = min((int64_t)__ldg(a.offs + w.e + 1), a.R);
+    if (w.m0 < 0) w.m0 = w.r1 = 0;  // (offsets of overlapping experts can overflow the count of walks)
   };
   auto next = [&](Walk& w) {
-    w.m0 += R;
-    if (w.m0 < w.r1) return;
-    ++w.tile;
-    enter(w);
+    if (++w.x < last) enter(w);
   };
   auto fail = [&](uint32_t code) {
     if (!*abort_flag) atomicOr(&g_routed_error, code);
     *abort_flag = 1;
   };
-  Walk w{first, 0, 0, 0, 0};
-  enter(w);
+  Walk w{first, 0, 0, 0, 0, 0};
+  if (first < last) {
+    int hi = reached;  // s_walk[w.i] * blocks <= first < s_walk[hi] * blocks
+    while (hi - w.i > 1) {
+      const int mid = (w.i + hi) >> 1;
+      if (s_walk[mid] * blocks <= first) w.i = mid;
+      else hi = mid;
+    }
+    enter(w);
+  }
+  const Walk w_first = w;
   bool ok = true;
 
   if (warp == 0) {
@@ -206,7 +235,15 @@ __global__ void __launch_bounds__(kRpThreads, 1)
     int at_e = -1;
     int64_t at_m = -1;
     int tok[4] = {};
-    for (; w.tile < last && ok; next(w)) {
+    auto issue_w = [&](int j, int st, int row) {  // lane 0
+      mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(Cfg::kWBytes + Cfg::kXBytes));
+      tma_load_2d(sbase + (uint32_t)(st * Cfg::kWBytes), &tma_w, full0 + 8 * st, (kb0 + j) * kBlock, row);
+    };
+    // the first stages' weights go out before the tokens are known
+    const int ahead = w.x < last ? min(ST, kbn) : 0;
+    if (lane == 0)
+      for (int j = 0; j < ahead; ++j) issue_w(j, j, w.e * (int)a.N + w.block * kRpTile);
+    for (; w.x < last && ok; next(w)) {
       if (w.e != at_e || w.m0 != at_m) {
         at_e = w.e, at_m = w.m0;
         if (lane < R / 4) {
@@ -217,15 +254,14 @@ __global__ void __launch_bounds__(kRpThreads, 1)
       const int row = w.e * (int)a.N + w.block * kRpTile;
       for (int j = 0; j < kbn; ++j, ++n) {
         const int st = n % ST;
-        ok = mbar_wait_bounded(empty0 + 8 * st, (uint32_t)((n / ST) & 1) ^ 1u, kWaitLimitNs, abort_flag);
-        if (!__all_sync(kAll, ok)) {
-          if (lane == 0) fail(1u);
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(Cfg::kWBytes + Cfg::kXBytes));
-          tma_load_2d(sbase + (uint32_t)(st * Cfg::kWBytes), &tma_w, full0 + 8 * st, (kb0 + j) * kBlock, row);
+        if (n >= ahead) {
+          ok = mbar_wait_bounded(empty0 + 8 * st, (uint32_t)((n / ST) & 1) ^ 1u, kWaitLimitNs, abort_flag);
+          if (!__all_sync(kAll, ok)) {
+            if (lane == 0) fail(1u);
+            ok = false;
+            break;
+          }
+          if (lane == 0) issue_w(j, st, row);
         }
         __syncwarp();
         if (lane < R / 4)
@@ -234,14 +270,14 @@ __global__ void __launch_bounds__(kRpThreads, 1)
       }
     }
     if (!ok && lane == 0)  // copies already issued land before this CTA's shared memory goes away
-      for (int i = n > ST ? n - ST : 0; i < n; ++i)
+      for (int i = n > ST ? n - ST : 0; i < max(n, ahead); ++i)
         mbar_wait_bounded(full0 + 8 * (i % ST), (uint32_t)((i / ST) & 1), kWaitLimitNs, never);
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA issuers (alternate K-blocks)
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(kRpTile, R);
       int n = 0;
-      for (; w.tile < last && ok; next(w)) {
+      for (; w.x < last && ok; next(w)) {
         for (int j = 0; j < kbn && ok; ++j, ++n) {
           if ((n & 1) != (warp == 1 ? 0 : 1)) continue;
           const int st = n % ST, buf = n % NT;
@@ -273,7 +309,7 @@ __global__ void __launch_bounds__(kRpThreads, 1)
     int n = 0, at_e = -1;
     int64_t at_m = -1;
     int tok[kPer] = {};
-    for (; w.tile < last && ok; next(w)) {
+    for (; w.x < last && ok; next(w)) {
       if (w.e != at_e || w.m0 != at_m) {
         at_e = w.e, at_m = w.m0;
 #pragma unroll
@@ -305,7 +341,7 @@ __global__ void __launch_bounds__(kRpThreads, 1)
     const int nl = 32 * (warp - 4) + lane;  // tensor-memory lane = column nl of the tile
     const uint32_t lane_base = (uint32_t)(32 * (warp - 4)) << 16;
     int n = 0;
-    for (; w.tile < last && ok; next(w)) {
+    for (; w.x < last && ok; next(w)) {
       float acc[R];
 #pragma unroll
       for (int m = 0; m < R; ++m) acc[m] = 0.0f;
@@ -382,15 +418,14 @@ __global__ void __launch_bounds__(kRpThreads, 1)
     // the second keeps each CTA resident until no peer reads them any more.
     cluster_sync_all();
     if (warp >= 4 && first < last) {
-      Walk f{first, 0, 0, 0, 0};
-      enter(f);
+      const Walk& f = w_first;
       const int nl = 32 * (warp - 4) + lane, per = R / splits, m_lo = split * per;
       const int64_t col = (int64_t)f.block * kRpTile + nl;
       for (int m = m_lo; m < m_lo + per; ++m) {
         float sum = 0.0f;
         for (int s = 0; s < splits; ++s)
           sum += lds32_cluster(mapa_shared(sbase + 4u * (uint32_t)(m * kRpTile + nl), (uint32_t)s));
-        if (f.tile < last && col < a.N && f.m0 + m < f.r1)
+        if (col < a.N && f.m0 + m < f.r1)
           a.c[(f.m0 + m) * a.ldc + col] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
       }
     }
@@ -480,7 +515,8 @@ static cudaError_t run_routed(const CUtensorMap& mw, const CUtensorMap& mx, cons
   const int64_t tiles = reach * cdiv(a.N, kRpTile);
   // a split tile has one walk: only where every row fits in it
   const int splits = a.R <= R ? rp_splits<R>(tiles, (int)cdiv(a.K, kBlock), num_sms) : 1;
-  const int64_t groups = splits > 1 || tiles < num_sms ? tiles : num_sms;
+  const int64_t walks = (reach + a.R / R) * cdiv(a.N, kRpTile);  // at most
+  const int64_t groups = splits > 1 ? tiles : walks < num_sms ? walks : num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * splits));
   cfg.blockDim = dim3(kRpThreads);
@@ -506,10 +542,17 @@ cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_
     *msg = "cuTensorMapEncodeTiled failed for an operand (alignment, stride or size out of range)";
     return cudaErrorInvalidValue;
   }
-  const int64_t rows = cdiv(a.R, a.E);  // rows an expert, spread evenly
-  if (rows <= 8) return run_routed<16>(mw, mx, a, num_sms, st);
-  if (rows <= 16) return run_routed<32>(mw, mx, a, num_sms, st);
-  return run_routed<64>(mw, mx, a, num_sms, st);
+  // R: enough for the rows of an expert were they spread evenly, with room for
+  // twice that, as long as the walks still cover the SMs
+  const int64_t reach = a.E < a.R ? a.E : a.R, rows = cdiv(a.R, a.E), tiles = reach * cdiv(a.N, kRpTile);
+  if ((reach + a.R / 16) * cdiv(a.N, kRpTile) >= (int64_t)1 << 31) {
+    *msg = "too many rows and columns: (experts + R/16) * ceil(N/128) must stay below 2^31";
+    return cudaErrorInvalidValue;
+  }
+  auto walks = [&](int r) { return tiles * cdiv(rows, r); };
+  if (rows > 16 && walks(64) >= num_sms) return run_routed<64>(mw, mx, a, num_sms, st);
+  if (rows > 8 && (rows <= 16 || walks(32) >= num_sms / 2)) return run_routed<32>(mw, mx, a, num_sms, st);
+  return run_routed<16>(mw, mx, a, num_sms, st);
 }
 
 cudaError_t routed_read_errors(uint32_t* out) {
