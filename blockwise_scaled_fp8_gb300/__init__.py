@@ -631,6 +631,47 @@ def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gat
     return out
 
 
+def moe_experts_fwd(x, w, plan: MoePlan, weight):
+    """Routed experts, training forward: y[t] = sum_j weight[t, j] W_e x[t] over
+    the token's experts e, each product in blockwise FP8 (x [T, K], w [E, N, K]
+    bf16, N % 128 == 0, the plan's align 128, weight [T, k] fp32).  Returns
+    (y [T, N], saved); ``saved`` holds the quantised operands, the experts'
+    outputs and what the backward needs of the plan."""
+    E, N, K = w.shape
+    if N % BLOCK:
+        raise ValueError("moe_experts_fwd: the experts' output features must be a multiple of 128")
+    if plan.offs.numel() != E + 1:
+        raise ValueError(f"moe_experts_fwd: the plan has {plan.offs.numel() - 1} experts, w {E}")
+    qx, sx, qxt, sxt = moe_dispatch(x, plan)
+    qw, qwt, sw = quant_weight(w.reshape(E * N, K), with_t=True)
+    ye = gemm_grouped_1x128_128x128(qx, sx, qw, sw, plan.offs, N, K)
+    return moe_combine(ye, plan, weight), (qxt, sxt, qwt, sw, ye, plan, weight)
+
+
+def moe_experts_bwd(dy, saved):
+    """Backward of moe_experts_fwd from what it saved: (dx [T, K], dW [E, N,
+    K], dweight [T, k] fp32)."""
+    torch = _torch()
+    qxt, sxt, qwt, sw, ye, plan, weight = saved
+    N, K, R = dy.shape[1], qxt.shape[0], plan.src.numel()
+    if R == 0:  # no tokens
+        dw = torch.zeros((plan.offs.numel() - 1, N, K), dtype=torch.bfloat16, device=dy.device)
+        return torch.empty((0, K), dtype=torch.bfloat16, device=dy.device), dw, torch.empty_like(weight)
+    _, dweight = moe_combine_bwd(dy, ye, plan, weight, with_dye=False)
+    qd, sd, qdt, sdt = moe_dispatch(dy, plan, weight=weight)
+    dxe = gemm_grouped_1x128_128x128(qd, sd, qwt, sw, plan.offs, K, N, sb_transposed=True)
+    dw = gemm_grouped_1x128_128x1(qdt, sdt, qxt, sxt, plan.offs, R)
+    return moe_combine(dxe, plan), dw, dweight
+
+
+def moe_experts_decode(x, qw, sw, plan: MoePlan, weight, N: int):
+    """Routed experts for a few tokens (serving): y [T, N] from x [T, K] bf16 and
+    the experts' weights quantised once, (qw, _, sw) = quant_weight(w.reshape(
+    E * N, K)); the plan's align is 1."""
+    q, s = quant_lhs(x)
+    return moe_combine(gemm_routed_1x128_128x128(q, s, qw, sw, plan, N, x.shape[1]), plan, weight)
+
+
 # ---------------------------------------------------------------------------
 # Linear layer
 # ---------------------------------------------------------------------------
@@ -834,7 +875,7 @@ def debug_write_counts(kind: int, M: int, N: int, K: int, flag: int = 0):
 
 def __getattr__(name):
     # the autograd wrapper lives in its own module (it imports torch at load)
-    if name in ("Float8BlockwiseLinear", "blockwise_fp8_linear"):
+    if name in ("Float8BlockwiseLinear", "blockwise_fp8_linear", "Float8RoutedExperts", "blockwise_fp8_experts"):
         from . import module
         return getattr(module, name)
     raise AttributeError(name)

@@ -601,8 +601,8 @@ bfp8_status bfp8_moe_dispatch(const void* x, int64_t T, int64_t K, int64_t ldx, 
   bfp8_status st = check_slots(fn, T, k);
   if (st != BFP8_OK) return st;
   if ((st = check_dims(fn, R, K)) != BFP8_OK) return st;
-  CHECK_ARG(!q_col == !s_col, "%s: the transposed output needs its codes and its scales", fn);
   if (R == 0 || K == 0) return BFP8_OK;
+  CHECK_ARG(!q_col == !s_col, "%s: the transposed output needs its codes and its scales", fn);
   CHECK_ARG(src && q_row && s_row && (T == 0 || x), "%s: null pointer", fn);
   CHECK_ARG(al2(x) && al4(src) && al4(weight) && al16(q_row) && al16(q_col) && al4(s_row) && al4(s_col),
             "%s: x must be 2-byte, codes 16-byte, the rest 4-byte aligned", fn);
