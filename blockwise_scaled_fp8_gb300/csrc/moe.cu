@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
 // its warp's run waits in row.  Then prefix sums of the counts: over the warps
 // of a CTA, over the CTAs of the cluster through distributed shared memory,
 // over the experts' aligned counts; and the slots' rows follow.
+template <int BITS>  // of the experts' numbers, E (nowhere) among them
 __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [32 warps][E] counts, then first rows; [E] CTA totals
   __shared__ uint32_t s_scan[32];
@@ -445,7 +446,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
   // padding everywhere; the barriers below come before the slots' own entries
   for (int64_t r = (int64_t)rank * kPlanThreads + tid; r < a.R; r += (int64_t)ctas * kPlanThreads) a.src[r] = -1;
   __syncwarp();
-  const int bits = 32 - __clz(E);  // E itself stands for "nowhere"
   constexpr int kAhead = 4;        // groups of 32 slots whose experts are read at once
   for (int64_t i0 = lo; i0 < hi; i0 += 32 * kAhead) {
     int e[kAhead];
@@ -459,9 +459,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
     for (int u = 0; u < kAhead; ++u) {
       const int64_t slot = i0 + 32 * u + lane;
       uint32_t peers = kFull;
-      for (int b = 0; b < bits; ++b) {
-        const uint32_t vote = __ballot_sync(kFull, (e[u] >> b) & 1);
-        peers &= (e[u] >> b) & 1 ? vote : ~vote;
+#pragma unroll
+      for (int b = 0; b < BITS; ++b) {
+        const bool set = (e[u] >> b) & 1;
+        const uint32_t vote = __ballot_sync(kFull, set);
+        peers &= set ? vote : ~vote;
       }
       const bool ok = e[u] < E;
       const uint32_t base = ok ? mine[e[u]] : 0u, lower = (uint32_t)__popc(peers & ((1u << lane) - 1u));
@@ -838,17 +840,36 @@ cudaError_t launch_moe_route_bwd(const RouteBwdArgs& args, cudaStream_t st) {
   return go(std::integral_constant<int, 16>{});
 }
 
-cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
+template <int BITS>
+static cudaError_t run_plan(const PlanArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(33 * a.E) * 4;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
+  static int most = 8;  // CTAs of the cluster: 16 where the device can hold one, else the portable 8
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    33 * kMaxGroups * 4);
+    const int max_smem = 33 * kMaxGroups * 4;
+    attr_err = cudaFuncSetAttribute(moe_plan_kernel<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+    if (attr_err != cudaSuccess) return;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = max_smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(moe_plan_kernel<BITS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, moe_plan_kernel<BITS>, &cfg) == cudaSuccess && n >= 1)
+      most = 16;
+    (void)cudaGetLastError();  // a size the device refuses leaves no error behind
   });
   if (attr_err != cudaSuccess) return attr_err;
   int ctas = 1;
-  while (ctas < 8 && (int64_t)ctas * kPlanThreads < a.n) ctas *= 2;
+  while (ctas < most && (int64_t)ctas * kPlanThreads < a.n) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kPlanThreads);
@@ -863,7 +884,14 @@ cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, moe_plan_kernel, a);
+  return cudaLaunchKernelEx(&cfg, moe_plan_kernel<BITS>, a);
+}
+
+cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
+  if (a.E < 1 << 5) return run_plan<5>(a, st);
+  if (a.E < 1 << 7) return run_plan<7>(a, st);
+  if (a.E < 1 << 9) return run_plan<9>(a, st);
+  return run_plan<11>(a, st);
 }
 
 static bool rows16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
