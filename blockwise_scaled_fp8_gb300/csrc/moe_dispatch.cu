@@ -12,17 +12,25 @@
 //      four rows of 64 columns a TMA gather, 128-byte swizzled; rows past the
 //      tensor (padding) and columns past C arrive as zeros.
 //   2. Quantising warp w takes the 16 columns 16w .., lane l the rows 4l ..
-//      4l+3.  A column's 128 rows are one warp's, so its maximum, its scale and
-//      its codes need no CTA barrier: a halving exchange leaves each lane with
-//      one column's maximum over all rows.  A row's eight partial maxima meet
-//      in shared memory.
+//      4l+3, in fp32 registers.  A column's 128 rows are one warp's, so its
+//      maximum, its scale and its codes need no other warp: a halving exchange
+//      leaves each lane with one column's maximum over all rows.  A row's eight
+//      partial maxima meet in shared memory.
 //   3. The codes go to a staging tile (row-major and transposed) and leave by
 //      one TMA store per output; a stage is free for the tile after the next
 //      as soon as its values are in registers.
+// What bounds it: 131072 routed rows x 4096 (16384 tokens, 64 experts, 8 each)
+// write 1.12 GB and read 0.18 (x nearly once) in 318 us with weights, 315
+// without; a plain fill of the same bytes takes 283 us on this memory, the
+// instructions of the two quantisations about 230.  Steps that led here:
+// gathering by cp.async from the quantising warps 675 us; by TMA from two warps
+// of their own, 16 columns a warp 349; the warps' barriers split into arrival
+// and wait 318.  (cp.async from the two gathering warps: 340 and 348, since the
+// copies share the quantisers' path to shared memory.)
 // The tiles are walked down the rows of a column block before the next block:
 // a token's rows (one per chosen expert) then read the same 256 bytes of it
 // within a short time, from L2 after the first (16384 tokens x 4096, eight
-// experts each: 342 us; blocks of four columns at a time 348, all 32 of them 383).
+// experts each: 342 us at the time; four column blocks at once 348, all 32 of them 383).
 #include <cudaTypedefs.h>
 #include <string.h>
 
@@ -51,8 +59,8 @@ constexpr int kDsOffRed = kDsOffCol + 128 * 128;  // [8 warps][128 rows] bf16x2 
 constexpr int kDsOffSc = kDsOffRed + 8 * 128 * 4;  // [128 rows] (hi, lo) of 1/s
 constexpr int kDsOffCsc = kDsOffSc + 128 * 8;     // [8 warps][8 column pairs] (hi, hi', lo, lo') of 1/s
 constexpr int kDsOffW = kDsOffCsc + 8 * 8 * 16;  // [2 stages][128 rows] weights
-constexpr int kDsOffBar = kDsOffW + 2 * 128 * 4;  // full[2], empty[2], the abort flag, a word that stays zero
-constexpr int kDsSmemBytes = kDsOffBar + 48 + 1024;  // + alignment slack
+constexpr int kDsOffBar = kDsOffW + 2 * 128 * 4;  // full[2], empty[2], rows, scales, codes ready; the abort flag, a zero
+constexpr int kDsSmemBytes = kDsOffBar + 64 + 1024;  // + alignment slack
 static_assert(2 * (kDsSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 
 struct DispatchParams {
@@ -71,20 +79,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 }
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-// Barriers of the quantising warps alone.
-__device__ __forceinline__ void bar_sync_consumers() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kDsConsumers) : "memory"); }
-__device__ __forceinline__ bool bar_sync_and(bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)v), "n"(kDsConsumers)
-      : "memory");
-  return r != 0;
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int q) {
   return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
@@ -155,7 +149,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t full0 = sbase + kDsOffBar, empty0 = full0 + 16;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDsOffBar + 32);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kDsOffBar + 56);
   volatile int* never = abort_flag + 1;
   float* s_w = reinterpret_cast<float*>(smem + kDsOffW);
   const int tid = (int)threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31;
@@ -166,6 +160,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
       mbar_init(full0 + 8 * s, TMA ? kDsProducers / 32 : kDsProducers);
       mbar_init(empty0 + 8 * s, kDsConsumers / 32);
     }
+    for (int i = 0; i < 3; ++i) mbar_init(full0 + 32 + 8 * i, kDsConsumers / 32);  // rows, scales, codes ready
     *abort_flag = 0;
     *never = 0;
     fence_barrier_init();
@@ -180,24 +175,28 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
   if (warp >= kDsConsumers / 32) {
     // ------------------------------------------------------------ producers
     // Warp w gathers the rows 64w .. 64w + 63, lane l the four rows 4 (l & 15) ..
-    // of them and the 64-column half l >> 4; their slots and weights are read
-    // one tile ahead, so that no copy waits for its own address.
+    // of them and the 64-column half l >> 4.  Their slots are read two tiles
+    // ahead, their weights one, so that no copy waits for its own address.
     const int r4 = 64 * (warp - kDsConsumers / 32) + 4 * (lane & 15), half = lane >> 4;
-    const int rot = (lane >> 1) & 3;  // of rows r4 ..
-    int tok[4];
+    int slot[4], tok[4];  // of the tile after next, of the next
     float wgt[4];
-    auto fetch = [&](int tile) {
-      const int64_t r0 = tile < p.num_tiles ? (int64_t)tile_pos(tile, p).t * 128 + r4 : R;
+    auto read_slots = [&](int tile) {
+      const int64_t at = tile < p.num_tiles ? (int64_t)tile_pos(tile, p).t * 128 + r4 : R;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) slot[i] = at + i < R ? __ldg(p.a.src + at + i) : -1;
+    };
+    auto read_weights = [&]() {  // and the tokens, from the slots
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int slot = r0 + i < R ? __ldg(p.a.src + r0 + i) : -1;
-        const uint32_t t = p.k_mul ? __umulhi((uint32_t)slot, p.k_mul) >> p.k_shift : (uint32_t)slot;
-        const bool ok = slot >= 0 && (int64_t)t < p.a.T;
+        const uint32_t t = p.k_mul ? __umulhi((uint32_t)slot[i], p.k_mul) >> p.k_shift : (uint32_t)slot[i];
+        const bool ok = slot[i] >= 0 && (int64_t)t < p.a.T;
         tok[i] = ok ? (int)t : (int)p.a.T;  // past the tensor: zeros
-        if constexpr (WEIGHTED) wgt[i] = ok ? __ldg(p.a.weight + slot) : 0.0f;
+        if constexpr (WEIGHTED) wgt[i] = ok ? __ldg(p.a.weight + slot[i]) : 0.0f;
       }
     };
-    fetch((int)blockIdx.x);
+    read_slots((int)blockIdx.x);
+    read_weights();
+    read_slots((int)blockIdx.x + step);
     int it = 0;
     bool ok = true;
     for (int tile = (int)blockIdx.x; tile < p.num_tiles; tile += step, ++it) {
@@ -211,12 +210,10 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
       }
       const uint32_t stage = sbase + (uint32_t)(s * kDsStageBytes);
       const int c0 = tile_pos(tile, p).c * 128;
-      if constexpr (WEIGHTED) {  // in the order of row_pos
-        const bool r1 = rot & 1, r2 = rot & 2;
-        const float a0 = r1 ? wgt[1] : wgt[0], a1 = r1 ? wgt[2] : wgt[1], a2 = r1 ? wgt[3] : wgt[2],
-                    a3 = r1 ? wgt[0] : wgt[3];
-        if (half == 0)
-          *reinterpret_cast<float4*>(s_w + s * 128 + r4) = r2 ? make_float4(a2, a3, a0, a1) : make_float4(a0, a1, a2, a3);
+      if constexpr (WEIGHTED) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (half == 0) s_w[s * 128 + row_pos(r4 + i)] = wgt[i];
       }
       if constexpr (TMA) {
         __syncwarp();  // the weights, before the arrival that publishes them
@@ -245,7 +242,8 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
         }
         mbar_arrive(full0 + 8 * s);
       }
-      fetch(tile + step);
+      read_weights();
+      read_slots(tile + 2 * step);
     }
     if (TMA && !ok && lane == 0)  // copies already issued land before this CTA's shared memory goes away
       for (int i = it > 2 ? it - 2 : 0; i < it; ++i)
@@ -253,7 +251,13 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
   } else {
     // ------------------------------------------------------------ quantisers
     // Warp w takes the 16 columns 16w .. of the tile, lane l the rows 4l .. 4l+3.
+    // The warps meet twice a tile, by arriving early and waiting late:
+    //   rows ready   the row maxima (and the stage and the staging tiles free)
+    //   scales ready the row scales, while each warp forms its columns' codes
+    // A warp goes on to the next tile without waiting for the others' codes;
+    // thread 0 alone waits for them, to store the tile.
     const uint32_t outr = sbase + kDsOffRow, outc = sbase + kDsOffCol;
+    const uint32_t rows_ready = full0 + 32, scales_ready = full0 + 40, codes_ready = full0 + 48;
     const int rot = (lane >> 1) & 3;
     uint32_t sel_e = 0, sel_o = 0;  // byte selectors of the transposed words (rows in order)
 #pragma unroll
@@ -265,88 +269,78 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
     uint32_t* s_red = reinterpret_cast<uint32_t*>(smem + kDsOffRed);
     float* s_csc = reinterpret_cast<float*>(smem + kDsOffCsc) + 32 * warp;
     const int g = tid >> 1, gpos = row_pos(g);  // the row whose scale this thread and its neighbour form
+    const bool ragged = p.C_al < C || (COL && p.R_al < R);
+    auto arrive = [&](uint32_t bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto wait = [&](uint32_t bar, int phase) {
+      const bool ok = mbar_wait_bounded(bar, (uint32_t)phase, kWaitLimitNs, abort_flag);
+      if (__all_sync(kAll, ok)) return true;
+      if (lane == 0 && !*abort_flag) atomicOr(&g_dispatch_error, 1u);
+      *abort_flag = 1;
+      return false;
+    };
     int it = 0;
     for (int tile = (int)blockIdx.x; tile < p.num_tiles; tile += step, ++it) {
-      const int s = it & 1;
+      const int s = it & 1, phase = it & 1;
       const uint32_t stage = sbase + (uint32_t)(s * kDsStageBytes);
       const TilePos pos = tile_pos(tile, p);
       const int t0 = pos.t * 128, c0 = pos.c * 128;
-      const bool landed = mbar_wait_bounded(full0 + 8 * s, (uint32_t)((it >> 1) & 1), kWaitLimitNs, abort_flag);
+      if (!wait(full0 + 8 * s, (it >> 1) & 1)) break;
 
-      // ---------------------------------------------- values and maxima
-      // Weighted values are unpacked and multiplied once and stay in registers
-      // as fp32 products; the others stay packed.
-      uint4 v[4][2];
-      uint64_t x2[WEIGHTED ? 4 : 1][8];  // products of row i, column pair q
+      // ---------------------------------------------- values (times the rows' weights) in fp32, row maxima
+      uint64_t x2[4][8];  // row i, column pair q
+      uint32_t rm[4];
       float w[4];
       if constexpr (WEIGHTED) {
         const float4 w4 = *reinterpret_cast<const float4*>(s_w + s * 128 + 4 * lane);
         w[0] = w4.x, w[1] = w4.y, w[2] = w4.z, w[3] = w4.w;
       }
-      uint32_t rm[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * lane + ((i + rot) & 3);
+        uint4 v[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          v[i][h] = lds128(stage + (uint32_t)((warp >> 2) * kDsBoxBytes + r * 128 +
-                                              ((((2 * warp + h) & 7) ^ (r & 7)) << 4)));
-        rm[i] = amax2(amax2(amax2(v[i][0].x, v[i][0].y), amax2(v[i][0].z, v[i][0].w)),
-                      amax2(amax2(v[i][1].x, v[i][1].y), amax2(v[i][1].z, v[i][1].w)));
-        if constexpr (WEIGHTED) {
+          v[h] = lds128(stage + (uint32_t)((warp >> 2) * kDsBoxBytes + r * 128 + ((((2 * warp + h) & 7) ^ (r & 7)) << 4)));
+        rm[i] = amax2(amax2(amax2(v[0].x, v[0].y), amax2(v[0].z, v[0].w)),
+                      amax2(amax2(v[1].x, v[1].y), amax2(v[1].z, v[1].w)));
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t x = word_of(v[i][q >> 2], q & 3);
-            x2[i][q] = f2_mul(f2_pack(bf16_lo(x), bf16_hi(x)), f2_pack(w[i], w[i]));
-          }
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t x = word_of(v[q >> 2], q & 3);
+          x2[i][q] = f2_pack(bf16_lo(x), bf16_hi(x));
+          if constexpr (WEIGHTED) x2[i][q] = f2_mul(x2[i][q], f2_pack(w[i], w[i]));
         }
       }
       *reinterpret_cast<uint4*>(s_red + warp * 128 + 4 * lane) = make_uint4(rm[0], rm[1], rm[2], rm[3]);
       const float wrow = WEIGHTED ? fabsf(s_w[s * 128 + gpos]) : 1.0f;
+      if (tid == 0) bulk_wait_read_all();  // the last tile's stores have read the staging tiles
+      arrive(rows_ready);
+
+      // ---------------------------------------------- column maxima and scales: the warp's own
       if constexpr (COL) {
         // Halving exchange over the lanes: each step keeps half of the columns
-        // (bits 4, 3, .. of the lane choose it), then the lanes that are left
-        // with the same columns combine.
-        float cmax;  // of column 16 warp + (lane >> 1)
-        if constexpr (WEIGHTED) {
-          float m[16];
+        // (bits 4, 3, .. of the lane choose it): lane l ends with column l >> 1.
+        float m[16];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float lo[4], hi[4];
+        for (int q = 0; q < 8; ++q) {
+          float lo[4], hi[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f2_unpack(x2[i][q], lo[i], hi[i]);
-            m[2 * q] = fmaxf(max3_abs(lo[0], lo[1], lo[2]), fabsf(lo[3]));
-            m[2 * q + 1] = fmaxf(max3_abs(hi[0], hi[1], hi[2]), fabsf(hi[3]));
-          }
-#pragma unroll
-          for (int h = 8; h >= 1; h >>= 1) {
-            const bool up = (lane & (2 * h)) != 0;
-#pragma unroll
-            for (int i = 0; i < h; ++i) {
-              const float give = up ? m[i] : m[i + h], keep = up ? m[i + h] : m[i];
-              m[i] = fmaxf(keep, __shfl_xor_sync(kAll, give, 2 * h));
-            }
-          }
-          cmax = fmaxf(m[0], __shfl_xor_sync(kAll, m[0], 1));
-        } else {
-          uint32_t m[8];  // packed column pairs
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            m[q] = amax2(amax2(word_of(v[0][q >> 2], q & 3), word_of(v[1][q >> 2], q & 3)),
-                         amax2(word_of(v[2][q >> 2], q & 3), word_of(v[3][q >> 2], q & 3)));
-#pragma unroll
-          for (int h = 4; h >= 1; h >>= 1) {
-            const bool up = (lane & (4 * h)) != 0;
-#pragma unroll
-            for (int i = 0; i < h; ++i) {
-              const uint32_t give = up ? m[i] : m[i + h], keep = up ? m[i + h] : m[i];
-              m[i] = amax2(keep, __shfl_xor_sync(kAll, give, 4 * h));
-            }
-          }
-          m[0] = amax2(m[0], __shfl_xor_sync(kAll, m[0], 1));
-          m[0] = amax2(m[0], __shfl_xor_sync(kAll, m[0], 2));
-          cmax = __uint_as_float((lane & 2 ? m[0] : m[0] << 16) & 0x7FFF0000u);
+          for (int i = 0; i < 4; ++i) f2_unpack(x2[i][q], lo[i], hi[i]);
+          m[2 * q] = fmaxf(max3_abs(lo[0], lo[1], lo[2]), fabsf(lo[3]));
+          m[2 * q + 1] = fmaxf(max3_abs(hi[0], hi[1], hi[2]), fabsf(hi[3]));
         }
+#pragma unroll
+        for (int h = 8; h >= 1; h >>= 1) {
+          const bool up = (lane & (2 * h)) != 0;
+#pragma unroll
+          for (int i = 0; i < h; ++i) {
+            const float give = up ? m[i] : m[i + h], keep = up ? m[i + h] : m[i];
+            m[i] = fmaxf(keep, __shfl_xor_sync(kAll, give, 2 * h));
+          }
+        }
+        const float cmax = fmaxf(m[0], __shfl_xor_sync(kAll, m[0], 1));
         if ((lane & 1) == 0) {
           const float sc = scale_of(cmax);
           const float2 y = recip_hi_lo(sc);
@@ -356,16 +350,9 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
           dst[2] = y.y;
           if (c < C) p.a.s_col[(int64_t)pos.t * p.a.lds_col + c] = sc;
         }
+        __syncwarp();
       }
-      if (tid == 0) bulk_wait_read_all();  // the last tile's stores have read the staging tiles
-      // row maxima visible; every warp knows whether the tile had landed
-      if (!bar_sync_and(landed)) {
-        if (tid == 0) {
-          if (!*abort_flag) atomicOr(&g_dispatch_error, 1u);
-          *abort_flag = 1;
-        }
-        break;
-      }
+      if (!wait(rows_ready, phase)) break;
       if (lane == 0) mbar_arrive(empty0 + 8 * s);  // the stage is in registers
 
       // ---------------------------------------------- row scales: two threads a row
@@ -381,64 +368,51 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
           if (t0 + g < R) p.a.s_row[(int64_t)pos.c * p.a.lds_row + t0 + g] = sc;
         }
       }
-      bar_sync_consumers();  // row scales visible
+      arrive(scales_ready);
       // ---------------------------------------------- codes
-      // One unpacking for both forms.  Without weights x/s is RN(x hi + RN(x lo)),
-      // the IEEE quotient's code; with them RN(RN(x w) hi), within three
-      // roundings of the quotient (the product x w has no ties to keep).
-      float rhi[4], rlo[4];
+      // Without weights x/s is RN(x hi + RN(x lo)), the IEEE quotient's code;
+      // with them RN(RN(x w) hi), within three roundings of the quotient (the
+      // product x w has no ties to keep).
+      if constexpr (COL) {
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const float4 y = *reinterpret_cast<const float4*>(smem + kDsOffSc + 8 * (4 * lane + i));
-        rhi[i] = y.x, rlo[i] = y.y, rhi[i + 1] = y.z, rlo[i + 1] = y.w;
-      }
-      uint32_t rc[4][4];  // row codes: the thread's 16 columns of row i
+        for (int q = 0; q < 8; ++q) {  // columns 16 warp + 2q, + 1
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(s_csc + 4 * q);
+          uint64_t cv[4];
 #pragma unroll
-      for (int q2 = 0; q2 < 4; ++q2) {
-        uint64_t rv[4][2];
-#pragma unroll
-        for (int q1 = 0; q1 < 2; ++q1) {
-          const int q = 2 * q2 + q1;
-          uint64_t chi = 0, clo = 0, cv[4];  // columns 16 warp + 2q, + 1
-          if constexpr (COL) {
-            const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(s_csc + 4 * q);
-            chi = y.x, clo = y.y;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (WEIGHTED) {
-              cv[i] = f2_mul(x2[i][q], chi);
-              rv[i][q1] = f2_mul(x2[i][q], f2_pack(rhi[i], rhi[i]));
-            } else {
-              const uint32_t x1 = word_of(v[i][q >> 2], q & 3);
-              const uint64_t x = f2_pack(bf16_lo(x1), bf16_hi(x1));
-              cv[i] = f2_fma(x, chi, f2_mul(x, clo));
-              rv[i][q1] = f2_fma(x, f2_pack(rhi[i], rhi[i]), f2_mul(x, f2_pack(rlo[i], rlo[i])));
-            }
-          }
-          if constexpr (COL) {
-            const uint32_t dst = outc + (uint32_t)((16 * warp + 2 * q) * 128 + 4 * lane);
-            const uint32_t lo = cvt4(cv[0], cv[1]), hi = cvt4(cv[2], cv[3]);
-            sts32(dst, __byte_perm(lo, hi, sel_e));
-            sts32(dst + 128u, __byte_perm(lo, hi, sel_o));
-          }
+          for (int i = 0; i < 4; ++i)
+            cv[i] = WEIGHTED ? f2_mul(x2[i][q], y.x) : f2_fma(x2[i][q], y.x, f2_mul(x2[i][q], y.y));
+          const uint32_t dst = outc + (uint32_t)((16 * warp + 2 * q) * 128 + 4 * lane);
+          const uint32_t lo = cvt4(cv[0], cv[1]), hi = cvt4(cv[2], cv[3]);
+          sts32(dst, __byte_perm(lo, hi, sel_e));
+          sts32(dst + 128u, __byte_perm(lo, hi, sel_o));
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rc[i][q2] = cvt4(rv[i][0], rv[i][1]);
       }
+      if (!wait(scales_ready, phase)) break;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const float2 y = *reinterpret_cast<const float2*>(smem + kDsOffSc + 8 * (4 * lane + i));
+        const uint64_t hi = f2_pack(y.x, y.x), lo = f2_pack(y.y, y.y);
+        uint32_t rc[4];
+#pragma unroll
+        for (int q = 0; q < 8; q += 2) {
+          const uint64_t a = WEIGHTED ? f2_mul(x2[i][q], hi) : f2_fma(x2[i][q], hi, f2_mul(x2[i][q], lo));
+          const uint64_t b = WEIGHTED ? f2_mul(x2[i][q + 1], hi) : f2_fma(x2[i][q + 1], hi, f2_mul(x2[i][q + 1], lo));
+          rc[q >> 1] = cvt4(a, b);
+        }
         const int r = 4 * lane + ((i + rot) & 3);
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(outr + (uint32_t)(r * 128 + ((warp ^ (r & 7)) << 4))),
-                     "r"(rc[i][0]), "r"(rc[i][1]), "r"(rc[i][2]), "r"(rc[i][3])
+                     "r"(rc[0]), "r"(rc[1]), "r"(rc[2]), "r"(rc[3])
                      : "memory");
       }
       fence_proxy_async_shared();
-      bar_sync_consumers();  // the output tiles are complete
-      if (tid == 0) {
-        if (c0 < p.C_al) tma_store_2d(&tmap_qrow, outr, c0, t0);
-        if (COL && t0 < p.R_al) tma_store_2d(&tmap_qcol, outc, t0, c0);
-        bulk_commit();
+      arrive(codes_ready);
+      if (warp == 0 || ragged) {
+        if (!wait(codes_ready, phase)) break;
+        if (tid == 0) {
+          if (c0 < p.C_al) tma_store_2d(&tmap_qrow, outr, c0, t0);
+          if (COL && t0 < p.R_al) tma_store_2d(&tmap_qcol, outc, t0, c0);
+          bulk_commit();
+        }
       }
       // the last C % 16 (R % 16) bytes of a row, past the maps' extents
       if (p.C_al < C && c0 + 128 > p.C_al && t0 + g < R) {
