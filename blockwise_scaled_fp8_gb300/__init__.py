@@ -590,8 +590,8 @@ def moe_combine(ye, plan: MoePlan, w=None, y=None):
 
 
 def moe_combine_bwd(dy, ye, plan: MoePlan, w, with_dye: bool = True):
-    """Gradient of moe_combine: (dye [R, N] bf16 or None, dw [T, k] fp32).
-    Without ``with_dye`` only dw is formed (the FP8 path forms dye's codes with
+    """Gradient of moe_combine: (dye [R, N] bf16 or None, dw [T, k] fp32); w
+    None stands for 1.  Without ``with_dye`` only dw is formed (the FP8 path forms dye's codes with
     moe_dispatch(dy, plan, weight=w))."""
     torch = _torch()
     _need_bf16_2d(dy, "dy")
@@ -600,7 +600,8 @@ def moe_combine_bwd(dy, ye, plan: MoePlan, w, with_dye: bool = True):
     k, R = _need_plan(plan, T)
     if tuple(ye.shape) != (R, N):
         raise ValueError(f"ye must be {(R, N)}, got {tuple(ye.shape)}")
-    _need(w, "w", torch.float32, (T, k))
+    if w is not None:
+        _need(w, "w", torch.float32, (T, k))
     dye = torch.empty((R, N), dtype=torch.bfloat16, device=dy.device) if with_dye else None
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
     _check(lib().bfp8_moe_combine_bwd(_p(dy), _ld(dy), _p(ye), _ld(ye), R, _p(plan.row), _p(plan.src), _p(w), T, k, N,
@@ -620,12 +621,14 @@ def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gat
     T = qa.shape[0]
     if T != (plan.row.shape[0] if gathered else R):
         raise ValueError(f"qa has {T} rows, the plan {plan.row.shape[0] if gathered else R}")
-    if qb.shape[0] != (offs.numel() - 1) * N:
-        raise ValueError(f"qb has {qb.shape[0]} rows, {offs.numel() - 1} experts of {N} need {(offs.numel() - 1) * N}")
+    E = offs.numel() - 1
+    if qb.shape[0] != E * N or sb.shape[0] < E * _cdiv(N, BLOCK) or sa.shape[0] < _cdiv(K, BLOCK):
+        raise ValueError(f"{E} experts of {N} x {K} need qb, sb, sa of {E * N}, {E * _cdiv(N, BLOCK)}, {_cdiv(K, BLOCK)} "
+                         f"rows, got {qb.shape[0]}, {sb.shape[0]}, {sa.shape[0]}")
     if out is None:
         out = torch.empty((R, N), dtype=torch.bfloat16, device=qa.device)
     _check(lib().bfp8_gemm_routed_1x128_128x128(_p(qa), _ld(qa), _p(sa), sa.stride(0), T, _p(qb), _ld(qb), _p(sb),
-                                                _ld(sb), _p(offs), offs.numel() - 1,
+                                                _ld(sb), _p(offs), E,
                                                 _p(plan.src if gathered else None), k, _p(out), _ld(out), R, N, K,
                                                 _stream()))
     return out

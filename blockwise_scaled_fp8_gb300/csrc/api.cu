@@ -653,8 +653,7 @@ bfp8_status bfp8_moe_combine_bwd(const void* dy, int64_t lddy, const void* ye, i
   if (st != BFP8_OK) return st;
   if ((st = check_dims(fn, R, N)) != BFP8_OK) return st;
   CHECK_ARG(lddy >= N && ldye >= N && (!dye || lddye >= N), "%s: a row stride is below N=%lld", fn, (long long)N);
-  CHECK_ARG((T == 0 || (row && dw && (N == 0 || dy))) && (R == 0 || (src && (N == 0 || ye))) && (!dye || T == 0 || w),
-            "%s: null pointer", fn);
+  CHECK_ARG((T == 0 || (row && dw && (N == 0 || dy))) && (R == 0 || (src && (N == 0 || ye))), "%s: null pointer", fn);
   CHECK_ARG(al2(dy) && al2(ye) && al2(dye) && al4(row) && al4(src) && al4(w) && al4(dw), "%s: misaligned pointer", fn);
   if (T == 0 && (!dye || R == 0 || N == 0)) return BFP8_OK;
   int sms = 0;

@@ -127,7 +127,10 @@ __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-
 //     32-bit word with the expert's complement, and the redux names the winner;
 //   - with more experts a lane (VPL > 8) sorting costs more than k scans;
 //   - scores of the chosen are formed again from their logits, by k lanes.
-// 16384 tokens, 256 experts in 8 groups, sigmoid, k = 8: see the launcher.
+// 16384 tokens x 256 fp32, 8 groups, sigmoid with bias, k = 8: 19.6 us, 1076
+// warp-instructions a token, half of them the 256 scores (the first form, k
+// scans of every lane's keys, took 1737 and 32.8 us); 50021 x 160 bf16, softmax,
+// k = 6: 19 us, 421; one token 1.8 us.
 template <int VPL, bool F32, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArgs a) {
   // per warp: E + 32 values of groups that are not whole powers of two of lanes, later the sorted lists (VPL <= 8)
@@ -326,7 +329,9 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
 //   softmax:  dl_e = p_e (ds_e - sum_i ds_i p_i), ds_e = 0 where not chosen
 // One warp a token; lane j < k handles choice j.  Of the dense row lane l
 // takes the pairs 2l, 2l + 64, .. (one load and one store a pair where the row
-// is aligned for it), over which the chosen values go last.
+// is aligned for it), over which the chosen values go last.  Bound by
+// instructions as the router is: 50021 tokens x 160 bf16, softmax, 19 us, 365
+// warp-instructions a token.
 template <int PAIRS, bool F32, bool SIGMOID>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const RouteBwdArgs a) {
   pdl_launch_dependents();
@@ -428,7 +433,9 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
 // the slots' order and every launch gives the same plan.  A slot's rank within
 // its warp's run waits in row.  Then prefix sums of the counts: over the warps
 // of a CTA, over the CTAs of the cluster through distributed shared memory,
-// over the experts' aligned counts; and the slots' rows follow.
+// over the experts' aligned counts; and the slots' rows follow.  131072 slots,
+// 256 experts: 15.0 us, a chain of latencies (24.0 with a cluster of 8 CTAs,
+// 36.0 with matches); 384 slots, one CTA: 3.9 us.
 template <int BITS>  // of the experts' numbers, E (nowhere) among them
 __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [32 warps][E] counts, then first rows; [E] CTA totals
@@ -608,7 +615,8 @@ constexpr int kCombineBatch = 8;  // rows of ye in flight a thread
 }  // namespace
 
 // One thread VEC columns of one token; the token's rows are read eight at a
-// time before the first is used.
+// time before the first is used.  Bound by memory: 16384 tokens x 4096, eight
+// experts each, 1.21 GB in 182-192 us (0.93-0.98 of the copy rate).
 template <int VEC>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const CombineArgs a) {
   pdl_launch_dependents();
@@ -718,7 +726,7 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const 
   const int64_t t = slot >= 0 ? (int64_t)((uint32_t)slot / (uint32_t)a.k) : a.T;
   const uint64_t once = evict_first_policy();
   const bool live = t < a.T;  // not padding
-  const float w = live ? __ldg(a.w + slot) : 0.0f;
+  const float w = live ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
   const uint16_t *dy = a.dy + (live ? t : 0) * a.lddy, *ye = a.ye + r * a.ldye;
   uint16_t* dye = a.dye + r * a.lddye;
   float dot[kClasses];

@@ -349,7 +349,7 @@ BFP8_API bfp8_status bfp8_moe_combine(const void *ye, int64_t ldye, int64_t R, c
  * -1) and, where dye is not NULL, dye[r] = w[src[r]] * dy[src[r] / k], zero on
  * padding rows (bf16 [R,N], lddye >= N, every row written).  (The FP8 path
  * takes dw alone and forms dye's codes with bfp8_moe_dispatch.)  row and src
- * are one plan's; w may be NULL without dye.
+ * are one plan's; w NULL: 1.
  */
 BFP8_API bfp8_status bfp8_moe_combine_bwd(const void *dy, int64_t lddy, const void *ye, int64_t ldye, int64_t R,
                                           const int32_t *row, const int32_t *src, const float *w, int64_t T,

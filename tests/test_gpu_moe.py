@@ -426,3 +426,74 @@ def test_operators_repeat_bit_for_bit():
                 *B.moe_combine_bwd(x, ye, plan, w)]
     for a, b in zip(once(), once()):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_combine_gradient_without_weights_is_the_dispatch():
+    plan = _routed(3, 30, 2, 4, 128)
+    g = _gen(4)
+    ye, dy = _randn(g, plan.src.numel(), 96, dtype=torch.bfloat16), _randn(g, 30, 96, dtype=torch.bfloat16)
+    dye, dw = B.moe_combine_bwd(dy, ye, plan, None)
+    one = torch.ones(30, 2, device="cuda")
+    dye1, dw1 = B.moe_combine_bwd(dy, ye, plan, one)
+    assert torch.equal(dye, dye1) and torch.equal(dw, dw1)
+    src = plan.src.long()
+    want = torch.where((src >= 0)[:, None], dy[src.clamp_min(0) // 2], torch.zeros((), dtype=dy.dtype, device="cuda"))
+    assert torch.equal(dye, want)
+
+
+def test_routed_product_refuses_wrong_sizes():
+    plan = _routed(1, 4, 2, 3, 1, empty=0.0)
+    e8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
+    f = lambda *s: torch.zeros(s, device="cuda")
+    ok = dict(qa=e8(4, 256), sa=f(2, 4), qb=e8(3 * 8, 256), sb=f(3, 2), plan=plan, N=8, K=256)
+    B.gemm_routed_1x128_128x128(**ok)
+    for bad in (dict(qa=e8(5, 256)), dict(qb=e8(23, 256)), dict(sb=f(2, 2)), dict(sa=f(1, 4)), dict(gathered=False)):
+        with pytest.raises(ValueError):
+            B.gemm_routed_1x128_128x128(**{**ok, **bad})
+    for bad in (dict(K=272), dict(qa=e8(4, 264)), dict(sb=f(3, 1))):
+        with pytest.raises((B.Bfp8Error, ValueError)):
+            B.gemm_routed_1x128_128x128(**{**ok, **bad})
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def test_more_than_2_31_elements():
+    """Sorted buffers and logits of more than 2^32 bytes and 2^31 elements: their last rows are right."""
+    T, k, E, K = 70000, 8, 64, 4096                  # 560000 rows and more: 2.3e9 elements
+    g = _gen(31)
+    logits = _randn(g, T, E)
+    idx, w = B.moe_route(logits, k, score="sigmoid")
+    plan = B.moe_plan(idx, E)
+    R = plan.src.numel()
+    assert R * K > 1 << 31
+    x = _randn(g, T, K, dtype=torch.bfloat16)
+    q, s, qc, sc = B.moe_dispatch(x, plan)
+    end = int(plan.offs[E])
+    rows = torch.arange(end - 128, end, device="cuda")          # the last expert's last block
+    src = plan.src[rows].long()
+    xg = torch.where((src >= 0)[:, None], x[src.clamp_min(0) // k], torch.zeros((), dtype=x.dtype, device="cuda"))
+    q2, s2, qc2, sc2 = B.quant_dual(xg)
+    assert torch.equal(q[rows], q2) and torch.equal(s[:, rows], s2)
+    assert torch.equal(qc[:, end - 128:end], qc2) and torch.equal(sc[end // 128 - 1], sc2[0])
+    assert not q[end:].any() and not qc[:, end:].any()          # rows of no expert
+    del q, s, qc, sc
+    ye = torch.empty(R, K, dtype=torch.bfloat16, device="cuda")
+    ye.copy_(torch.arange(R, device="cuda")[:, None] % 251)
+    y = B.moe_combine(ye, plan, w)
+    dye, dw = B.moe_combine_bwd(x, ye, plan, w)
+    t = torch.tensor([0, 1, T // 2, T - 2, T - 1], device="cuda")
+    at = plan.row[t].long()
+    want = (ye[at].double() * w[t].double()[:, :, None]).sum(1)
+    assert float((y[t].double() - want).abs().max()) <= 2.0 ** -8 * float(want.abs().max()) + 1e-3
+    dref = x[t].double()[:, None, :] * w[t].double()[:, :, None]
+    assert float((dye[at].double() - dref).abs().max()) <= 2.0 ** -8 * float(dref.abs().max()) + 1e-6
+    assert not dye[end:].any()
+    dwref = (x[t].double()[:, None, :] * ye[at].double()).sum(2)
+    size = (x[t].double()[:, None, :] * ye[at].double()).abs().sum(2)
+    assert bool(((dw[t].double() - dwref).abs() <= (K / 32 + 24) * EPS * size).all())
+    del ye, dye, y
+    wide = torch.zeros(2200000, 1024, dtype=torch.bfloat16, device="cuda")
+    wide[-1] = _randn(g, 1024, dtype=torch.bfloat16)
+    i1, w1 = B.moe_route(wide, 4)
+    i2, w2 = B.moe_route(wide[-1:], 4)
+    assert torch.equal(i1[-1:], i2) and torch.equal(w1[-1:], w2) and bool((i1[0] == torch.arange(4, device="cuda")).all())
