@@ -463,16 +463,20 @@ def _need(t, name, dtype, shape):
 
 def _need_logits(logits):
     torch = _torch()
-    if logits.dtype not in (torch.bfloat16, torch.float32) or logits.dim() != 2 or not logits.is_cuda or \
+    dt = logits.dtype
+    if (dt is not torch.bfloat16 and dt is not torch.float32) or logits.dim() != 2 or not logits.is_cuda or \
             (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be a 2-D CUDA bf16 or float32 tensor with unit column stride")
-    return logits.dtype == torch.float32
+    return dt is torch.float32
 
 
 def _ld(t):
     """Row stride; of a single row the width (torch may report any stride there)."""
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
+
+# (The calls below are short on the device: each of them avoids what host time
+# it can, a helper call a tensor included.)
 
 def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups=None, group_top: int = 1,
               renormalize: bool = True, scale: float = 1.0):
@@ -485,13 +489,18 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     torch = _torch()
     f32 = _need_logits(logits)
     T, E = logits.shape
+    at_bias = None
     if bias is not None:
         _need(bias, "bias", torch.float32, (E,))
-    idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _check(lib().bfp8_moe_route(_p(logits), f32, T, E, _ld(logits), _p(bias), k, _score(score), groups,
-                                groups if top_groups is None else top_groups, group_top, renormalize, scale,
-                                _p(idx), _p(w), _stream()))
+        at_bias = bias.data_ptr()
+    dev = logits.device
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    st = lib().bfp8_moe_route(logits.data_ptr(), f32, T, E, logits.stride(0) if T > 1 else E, at_bias, k, _score(score),
+                              groups, groups if top_groups is None else top_groups, group_top, renormalize, scale,
+                              idx.data_ptr(), w.data_ptr(), _stream())
+    if st:
+        _check(st)
     return idx, w
 
 
@@ -502,45 +511,59 @@ def moe_route_bwd(logits, idx, w, dw, score: str = "softmax", renormalize: bool 
     f32 = _need_logits(logits)
     T, E = logits.shape
     k = idx.shape[-1]
-    _need(idx, "idx", torch.int32, (T, k))
-    _need(w, "w", torch.float32, (T, k))
-    _need(dw, "dw", torch.float32, (T, k))
+    shape = (T, k)
+    _need(idx, "idx", torch.int32, shape)
+    _need(w, "w", torch.float32, shape)
+    _need(dw, "dw", torch.float32, shape)
     out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _check(lib().bfp8_moe_route_bwd(_p(logits), f32, T, E, _ld(logits), _p(idx), _p(w), _p(dw), k, _score(score),
-                                    renormalize, scale, _p(out), E, _stream()))
+    st = lib().bfp8_moe_route_bwd(logits.data_ptr(), f32, T, E, logits.stride(0) if T > 1 else E, idx.data_ptr(),
+                                  w.data_ptr(), dw.data_ptr(), k, _score(score), renormalize, scale, out.data_ptr(), E,
+                                  _stream())
+    if st:
+        _check(st)
     return out
 
 
 def moe_plan_rows(T: int, k: int, E: int, align: int = BLOCK) -> int:
-    """Rows that sorted buffers need for any choice of k experts by T tokens."""
-    rows = int(lib().bfp8_moe_plan_rows(T, k, E, align))
-    if rows < 0:
+    """Rows that sorted buffers need for any choice of k experts by T tokens
+    (bfp8_moe_plan_rows; the plan's entry holds R against it)."""
+    n = T * k
+    if T < 0 or k < 1 or E < 1 or align < 1 or max(n, E, align) >= 1 << 31:
         raise ValueError(f"moe_plan_rows: sizes out of range (T={T}, k={k}, E={E}, align={align})")
-    return rows
+    return (n + min(n, E) * (align - 1)) // align * align
 
 
 def moe_plan(idx, E: int, align: int = BLOCK) -> MoePlan:
     """Sorts the slots of idx [T, k] int32 by expert: each expert's rows start
     on a multiple of ``align`` (128 for training, 1 for the routed product)."""
     torch = _torch()
+    i32 = torch.int32
     if idx.dim() != 2:
         raise ValueError("idx must be a [T, k] tensor")
     T, k = idx.shape
-    _need(idx, "idx", torch.int32, (T, k))
+    _need(idx, "idx", i32, (T, k))
     R = moe_plan_rows(T, k, E, align)
-    e = lambda *shape: torch.empty(shape, dtype=torch.int32, device=idx.device)
-    plan = MoePlan(offs=e(E + 1), row=e(T, k), src=e(R), counts=e(E))
-    _check(lib().bfp8_moe_plan(_p(idx), T, k, E, align, _p(plan.offs), _p(plan.row), _p(plan.src), R,
-                               _p(plan.counts), _stream()))
-    return plan
+    dev = idx.device
+    offs = torch.empty(E + 1, dtype=i32, device=dev)
+    row = torch.empty((T, k), dtype=i32, device=dev)
+    src = torch.empty(R, dtype=i32, device=dev)
+    counts = torch.empty(E, dtype=i32, device=dev)
+    st = lib().bfp8_moe_plan(idx.data_ptr(), T, k, E, align, offs.data_ptr(), row.data_ptr(), src.data_ptr(), R,
+                             counts.data_ptr(), _stream())
+    if st:
+        _check(st)
+    return MoePlan(offs, row, src, counts)
 
 
 def _need_plan(plan, T):
-    torch = _torch()
-    k = plan.row.shape[-1]
-    _need(plan.row, "plan.row", torch.int32, (T, k))
-    _need(plan.src, "plan.src", torch.int32, (plan.src.numel(),))
-    return k, plan.src.numel()
+    """k and the rows R of a plan for T tokens."""
+    i32 = _torch().int32
+    row, src = plan.row, plan.src
+    if row.dtype is not i32 or src.dtype is not i32 or row.dim() != 2 or row.shape[0] != T or src.dim() != 1 or \
+            not (row.is_contiguous() and src.is_contiguous() and row.is_cuda and src.is_cuda):
+        raise ValueError(f"the plan must be one of moe_plan's for {T} tokens: contiguous CUDA int32 row [{T}, k] and "
+                         f"src [R], got {tuple(row.shape)} and {tuple(src.shape)}")
+    return row.shape[1], src.shape[0]
 
 
 def moe_dispatch(x, plan: MoePlan, weight=None, cols: bool = True):
@@ -552,18 +575,25 @@ def moe_dispatch(x, plan: MoePlan, weight=None, cols: bool = True):
     _need_bf16_2d(x, "x")
     T, K = x.shape
     k, R = _need_plan(plan, T)
+    at_weight = None
     if weight is not None:
         _need(weight, "weight", torch.float32, (T, k))
-    dev = x.device
-    q = torch.empty((R, _rup(max(K, 1), 16)), dtype=torch.uint8, device=dev)
-    s = torch.empty((_cdiv(K, BLOCK), max(R, 1)), dtype=torch.float32, device=dev)
-    qc = sc = None
+        at_weight = weight.data_ptr()
+    dev, u8, f32 = x.device, torch.uint8, torch.float32
+    ldq, lds = (max(K, 1) + 15) // 16 * 16, max(R, 1)
+    q = torch.empty((R, ldq), dtype=u8, device=dev)
+    s = torch.empty(((K + BLOCK - 1) // BLOCK, lds), dtype=f32, device=dev)
+    qc = sc = at_qc = at_sc = None
+    ldqc = ldsc = 0
     if cols:
-        qc = torch.empty((K, _rup(max(R, 1), 16)), dtype=torch.uint8, device=dev)
-        sc = torch.empty((_cdiv(R, BLOCK), _rup(max(K, 1), 4)), dtype=torch.float32, device=dev)
-    _check(lib().bfp8_moe_dispatch(_p(x), T, K, _ld(x), _p(plan.src), R, k, _p(weight), _p(q), _rup(max(K, 1), 16), _p(s),
-                                   max(R, 1), _p(qc), _rup(max(R, 1), 16) if cols else 0, _p(sc),
-                                   _rup(max(K, 1), 4) if cols else 0, _stream()))
+        ldqc, ldsc = (lds + 15) // 16 * 16, (max(K, 1) + 3) // 4 * 4
+        qc = torch.empty((K, ldqc), dtype=u8, device=dev)
+        sc = torch.empty(((R + BLOCK - 1) // BLOCK, ldsc), dtype=f32, device=dev)
+        at_qc, at_sc = qc.data_ptr(), sc.data_ptr()
+    st = lib().bfp8_moe_dispatch(x.data_ptr(), T, K, _ld(x), plan.src.data_ptr(), R, k, at_weight, q.data_ptr(), ldq,
+                                 s.data_ptr(), lds, at_qc, ldqc, at_sc, ldsc, _stream())
+    if st:
+        _check(st)
     return q, s, qc, sc
 
 
@@ -574,38 +604,46 @@ def moe_combine(ye, plan: MoePlan, w=None, y=None):
     _need_bf16_2d(ye, "ye")
     T = plan.row.shape[0]
     k, R = _need_plan(plan, T)
-    N = ye.shape[1]
-    if ye.shape[0] != R:
-        raise ValueError(f"ye has {ye.shape[0]} rows, the plan {R}")
+    rows, N = ye.shape
+    if rows != R:
+        raise ValueError(f"ye has {rows} rows, the plan {R}")
+    at_w = None
     if w is not None:
         _need(w, "w", torch.float32, (T, k))
+        at_w = w.data_ptr()
+    ldy = N
     if y is None:
         y = torch.empty((T, N), dtype=torch.bfloat16, device=ye.device)
     else:
         _need_bf16_2d(y, "y")
-        if tuple(y.shape) != (T, N):
+        if y.shape != (T, N):
             raise ValueError(f"y must be {(T, N)}, got {tuple(y.shape)}")
-    _check(lib().bfp8_moe_combine(_p(ye), _ld(ye), R, _p(plan.row), _p(w), T, k, N, _p(y), _ld(y), _stream()))
+        ldy = _ld(y)
+    st = lib().bfp8_moe_combine(ye.data_ptr(), _ld(ye), R, plan.row.data_ptr(), at_w, T, k, N, y.data_ptr(), ldy, _stream())
+    if st:
+        _check(st)
     return y
 
 
 def moe_combine_bwd(dy, ye, plan: MoePlan, w, with_dye: bool = True):
     """Gradient of moe_combine: (dye [R, N] bf16 or None, dw [T, k] fp32); w
-    None stands for 1.  Without ``with_dye`` only dw is formed (the FP8 path forms dye's codes with
-    moe_dispatch(dy, plan, weight=w))."""
+    None stands for 1.  Without ``with_dye`` only dw is formed (the FP8 path
+    forms dye's codes with moe_dispatch(dy, plan, weight=w))."""
     torch = _torch()
     _need_bf16_2d(dy, "dy")
     _need_bf16_2d(ye, "ye")
     T, N = dy.shape
     k, R = _need_plan(plan, T)
-    if tuple(ye.shape) != (R, N):
+    if ye.shape != (R, N):
         raise ValueError(f"ye must be {(R, N)}, got {tuple(ye.shape)}")
     if w is not None:
         _need(w, "w", torch.float32, (T, k))
     dye = torch.empty((R, N), dtype=torch.bfloat16, device=dy.device) if with_dye else None
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
-    _check(lib().bfp8_moe_combine_bwd(_p(dy), _ld(dy), _p(ye), _ld(ye), R, _p(plan.row), _p(plan.src), _p(w), T, k, N,
-                                      _p(dye), N, _p(dw), _stream()))
+    st = lib().bfp8_moe_combine_bwd(dy.data_ptr(), _ld(dy), ye.data_ptr(), _ld(ye), R, plan.row.data_ptr(),
+                                    plan.src.data_ptr(), _p(w), T, k, N, _p(dye), N, dw.data_ptr(), _stream())
+    if st:
+        _check(st)
     return dye, dw
 
 
@@ -617,20 +655,25 @@ def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gat
     they were in ``out``)."""
     torch = _torch()
     offs = _offs(plan.offs)
-    k, R = _need_plan(plan, plan.row.shape[0])
-    T = qa.shape[0]
-    if T != (plan.row.shape[0] if gathered else R):
-        raise ValueError(f"qa has {T} rows, the plan {plan.row.shape[0] if gathered else R}")
-    E = offs.numel() - 1
+    tokens = plan.row.shape[0]
+    k, R = _need_plan(plan, tokens)
+    T, E = qa.shape[0], offs.shape[0] - 1
+    if T != (tokens if gathered else R):
+        raise ValueError(f"qa has {T} rows, the plan {tokens if gathered else R}")
     if qb.shape[0] != E * N or sb.shape[0] < E * _cdiv(N, BLOCK) or sa.shape[0] < _cdiv(K, BLOCK):
         raise ValueError(f"{E} experts of {N} x {K} need qb, sb, sa of {E * N}, {E * _cdiv(N, BLOCK)}, {_cdiv(K, BLOCK)} "
                          f"rows, got {qb.shape[0]}, {sb.shape[0]}, {sa.shape[0]}")
+    ldc = N
     if out is None:
         out = torch.empty((R, N), dtype=torch.bfloat16, device=qa.device)
-    _check(lib().bfp8_gemm_routed_1x128_128x128(_p(qa), _ld(qa), _p(sa), sa.stride(0), T, _p(qb), _ld(qb), _p(sb),
-                                                _ld(sb), _p(offs), E,
-                                                _p(plan.src if gathered else None), k, _p(out), _ld(out), R, N, K,
-                                                _stream()))
+    else:
+        ldc = _ld(out)
+    st = lib().bfp8_gemm_routed_1x128_128x128(qa.data_ptr(), _ld(qa), sa.data_ptr(), sa.stride(0), T, qb.data_ptr(),
+                                              _ld(qb), sb.data_ptr(), _ld(sb), offs.data_ptr(), E,
+                                              plan.src.data_ptr() if gathered else None, k, out.data_ptr(), ldc, R, N, K,
+                                              _stream())
+    if st:
+        _check(st)
     return out
 
 

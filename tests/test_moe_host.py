@@ -68,6 +68,7 @@ def test_plan_rows_hold_every_choice():
         idx = rng.integers(-1, E, size=(T, k)).astype(np.int32)
         offs, row, src, counts = ref.plan(idx, E, align, R)
         assert offs[-1] <= R and R % align == 0
+        assert R == B.lib().bfp8_moe_plan_rows(T, k, E, align)
         assert np.array_equal(np.sort(src[src >= 0]), np.flatnonzero(idx.reshape(-1) >= 0))
     # the bound is reached: each slot its own expert
     assert B.moe_plan_rows(3, 1, 8, 128) == 3 * 128
@@ -75,6 +76,7 @@ def test_plan_rows_hold_every_choice():
     for bad in ((-1, 1, 1, 1), (1, 0, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0), (1 << 31, 1, 1, 1), (1 << 28, 8, 1, 1)):
         with pytest.raises(ValueError, match="out of range"):
             B.moe_plan_rows(*bad)
+        assert B.lib().bfp8_moe_plan_rows(*bad) == -1
 
 
 def test_dispatch_argument_validation():
