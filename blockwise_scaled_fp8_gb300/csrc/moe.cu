@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
+// The float whose key it is (+0 for both zeros).
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+}
+constexpr uint32_t kNoKey = 0x007FFFFFu;  // the key of -inf: not eligible
+
 __device__ __forceinline__ float load_logit(const void* p, int f32, int64_t i) {
   return f32 ? __ldg(static_cast<const float*>(p) + i)
              : bf16_to_f32(__ldg(static_cast<const uint16_t*>(p) + i));
@@ -127,10 +133,10 @@ __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-
 //     32-bit word with the expert's complement, and the redux names the winner;
 //   - with more experts a lane (VPL > 8) sorting costs more than k scans;
 //   - scores of the chosen are formed again from their logits, by k lanes.
-// 16384 tokens x 256 fp32, 8 groups, sigmoid with bias, k = 8: 19.6 us, 1076
+// 16384 tokens x 256 fp32, 8 groups, sigmoid with bias, k = 8: 18.6 us, 994
 // warp-instructions a token, half of them the 256 scores (the first form, k
 // scans of every lane's keys, took 1737 and 32.8 us); 50021 x 160 bf16, softmax,
-// k = 6: 19 us, 421; one token 1.8 us.
+// k = 6: 19 us, 411; one token 2.0 us.
 template <int VPL, bool F32, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArgs a) {
   // per warp: E + 32 values of groups that are not whole powers of two of lanes, later the sorted lists (VPL <= 8)
@@ -149,11 +155,10 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
   float top = 0.0f, sum = 1.0f;  // softmax: p = exp(l - top) / sum
   float gv[VPL];                 // what a group's score sums the largest of (softmax without bias)
   if constexpr (!SIGMOID) {
-    top = c[0];
+    float m = c[0];
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) top = fmaxf(top, c[i]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, c[i]);
+    top = key_value(__reduce_max_sync(kFull, order_key(m)));
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -247,11 +252,11 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
     uint32_t key[VPL];  // 16 bits of the logit's order, then the expert's complement: every key differs
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      key[i] = c[i] > -INFINITY ? (order_key(c[i]) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e0 - i) : 0u;
+      key[i] = (order_key(c[i]) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e0 - i);
     sort_down(key);
     for (int j = 0; j < a.k; ++j) {
       const uint32_t best = __reduce_max_sync(kFull, key[0]);
-      if (best == 0) break;
+      if (best <= (kNoKey | 0xFFFFu)) break;
       if (lane == j) my_e = 0xFFFF - (int)(best & 0xFFFFu);
       const bool mine = key[0] == best;
 #pragma unroll
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
     uint64_t key[VPL];  // the value's order, then the complement of the place in the lane
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      key[i] = c[i] > -INFINITY ? ((uint64_t)order_key(c[i]) << 32) | (uint32_t)(VPL - 1 - i) : 0u;
+      key[i] = ((uint64_t)order_key(c[i]) << 32) | (uint32_t)(VPL - 1 - i);
     sort_down(key);
     // the rest of the list, [place][lane]: the winner fetches its next key
     uint64_t* list = reinterpret_cast<uint64_t*>(mine_s) + lane;
@@ -275,14 +280,14 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
     }
     for (int j = 0; j < a.k; ++j) {
       const uint32_t hi = (uint32_t)(head >> 32), best = __reduce_max_sync(kFull, hi);
-      if (best == 0) break;
+      if (best <= kNoKey) break;
       const int win = __ffs(__ballot_sync(kFull, hi == best)) - 1;
       const int e = __shfl_sync(kFull, e0 + VPL - 1 - (int)(uint32_t)head, win);
       if (lane == j) my_e = e;
-      if (lane == win) {
+      if (lane == win) {  // (the list ends with a key of 0, which never wins: nothing is read past it)
         if constexpr (VPL > 1) {
           head = *list;
-          if (head) list += 32;
+          list += 32;
         } else {
           head = 0;
         }
@@ -291,13 +296,13 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
   } else {
     uint32_t key[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = c[i] > -INFINITY ? order_key(c[i]) : 0u;
+    for (int i = 0; i < VPL; ++i) key[i] = order_key(c[i]);
     for (int j = 0; j < a.k; ++j) {
       uint32_t m = key[0];
 #pragma unroll
       for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
       const uint32_t best = __reduce_max_sync(kFull, m);
-      if (best == 0) break;
+      if (best <= kNoKey) break;
       const int win = __ffs(__ballot_sync(kFull, m == best)) - 1;
       int at_i = 0;
 #pragma unroll
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
 // One warp a token; lane j < k handles choice j.  Of the dense row lane l
 // takes the pairs 2l, 2l + 64, .. (one load and one store a pair where the row
 // is aligned for it), over which the chosen values go last.  Bound by
-// instructions as the router is: 50021 tokens x 160 bf16, softmax, 19 us, 365
+// instructions as the router is: 50021 tokens x 160 bf16, softmax, 16 us, 295
 // warp-instructions a token.
 template <int PAIRS, bool F32, bool SIGMOID>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const RouteBwdArgs a) {
@@ -351,7 +356,6 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
   if constexpr (SIGMOID) {
     p_j = sigmoid(l_j);
   } else {
-    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
       const int e = 64 * i + 2 * lane;
@@ -370,20 +374,30 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
       }
       s[2 * i] = l0 > low ? fminf(l0, FLT_MAX) : -INFINITY;
       s[2 * i + 1] = l1 > low ? fminf(l1, FLT_MAX) : -INFINITY;
-      top = fmaxf(top, fmaxf(s[2 * i], s[2 * i + 1]));
     }
+    // p = exp(l - ref) * mult: by the first choice where its weight gives its p
+    // (no renormalisation, and p not so small that it has lost bits), else by
+    // the largest logit and the sum over the row
+    float ref = __shfl_sync(kFull, l_j, 0), mult = __shfl_sync(kFull, w, 0) / a.scale;
+    if (!a.renormalize && mult > 1e-20f && mult < 2.0f) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    float sum = 0.0f;
+      for (int i = 0; i < 2 * PAIRS; ++i) s[i] = expf(s[i] - ref) * mult;
+    } else {
+      ref = s[0];
 #pragma unroll
-    for (int i = 0; i < 2 * PAIRS; ++i) {
-      s[i] = s[i] > -INFINITY ? expf(s[i] - top) : 0.0f;
-      sum += s[i];
+      for (int i = 1; i < 2 * PAIRS; ++i) ref = fmaxf(ref, s[i]);
+      ref = fmaxf(key_value(__reduce_max_sync(kFull, order_key(ref))), -FLT_MAX);  // finite where all are masked
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2 * PAIRS; ++i) {
+        s[i] = expf(s[i] - ref);
+        sum += s[i];
+      }
+      mult = 1.0f / fmaxf(warp_sum(sum), FLT_MIN);
+#pragma unroll
+      for (int i = 0; i < 2 * PAIRS; ++i) s[i] *= mult;
     }
-    const float inv = 1.0f / fmaxf(warp_sum(sum), FLT_MIN);
-#pragma unroll
-    for (int i = 0; i < 2 * PAIRS; ++i) s[i] *= inv;
-    p_j = l_j > -INFINITY ? expf(l_j - top) * inv : 0.0f;
+    p_j = expf(l_j - ref) * mult;  // -inf: 0
   }
   float ds = a.scale * dw;
   if (a.renormalize) {
