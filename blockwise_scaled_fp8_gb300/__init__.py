@@ -663,12 +663,14 @@ def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gat
     if qb.shape[0] != E * N or sb.shape[0] < E * _cdiv(N, BLOCK) or sa.shape[0] < _cdiv(K, BLOCK):
         raise ValueError(f"{E} experts of {N} x {K} need qb, sb, sa of {E * N}, {E * _cdiv(N, BLOCK)}, {_cdiv(K, BLOCK)} "
                          f"rows, got {qb.shape[0]}, {sb.shape[0]}, {sa.shape[0]}")
+    if qa.stride(1) != 1 or qb.stride(1) != 1 or (sa.stride(1) != 1 and T > 1) or (sb.stride(1) != 1 and K > BLOCK):
+        raise ValueError("qa, sa, qb and sb must have unit column strides")
     ldc = N
     if out is None:
         out = torch.empty((R, N), dtype=torch.bfloat16, device=qa.device)
     else:
         ldc = _ld(out)
-    st = lib().bfp8_gemm_routed_1x128_128x128(qa.data_ptr(), _ld(qa), sa.data_ptr(), sa.stride(0), T, qb.data_ptr(),
+    st = lib().bfp8_gemm_routed_1x128_128x128(qa.data_ptr(), _ld(qa), sa.data_ptr(), _ld(sa), T, qb.data_ptr(),
                                               _ld(qb), sb.data_ptr(), _ld(sb), offs.data_ptr(), E,
                                               plan.src.data_ptr() if gathered else None, k, out.data_ptr(), ldc, R, N, K,
                                               _stream())

@@ -455,6 +455,20 @@ def test_routed_product_refuses_wrong_sizes():
             B.gemm_routed_1x128_128x128(**{**ok, **bad})
 
 
+def test_routed_product_of_one_k_block_takes_any_stride_of_its_single_row_of_scales():
+    plan = _routed(1, 4, 2, 3, 1, empty=0.0)
+    g = _gen(2)
+    qa, qb = (torch.randint(0, 120, (n, 128), generator=g, device="cuda", dtype=torch.uint8) for n in (4, 24))
+    sa, sb = torch.rand(4, 1, generator=g, device="cuda"), torch.rand(3, 1, generator=g, device="cuda")
+    one = sa.t()                                     # [1, 4], row stride 1
+    assert one.stride(0) == 1
+    got = B.gemm_routed_1x128_128x128(qa, one, qb, sb, plan, 8, 128)
+    want = B.gemm_routed_1x128_128x128(qa, sa.reshape(1, 4).clone(), qb, sb, plan, 8, 128)
+    assert torch.equal(got, want)
+    with pytest.raises(ValueError, match="unit column"):
+        B.gemm_routed_1x128_128x128(qa, torch.rand(4, 2, device="cuda").t(), qb, sb, plan, 8, 128)
+
+
 # ------------------------------------------------------------------ offsets past 32 bits
 
 def test_more_than_2_31_elements():
