@@ -101,7 +101,7 @@ def lib() -> ctypes.CDLL:
     L.bfp8_moe_plan.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, i64, vp, vp]
     L.bfp8_moe_dispatch.argtypes = [vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp]
     L.bfp8_moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i64, i64, vp, i64, vp]
-    L.bfp8_moe_combine_bwd.argtypes = [vp, i64, vp, i64, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp]
+    L.bfp8_moe_combine_bwd.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp]
     L.bfp8_gemm_routed_1x128_128x128.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
                                                  i64, i64, i64, vp]
     for name in EXPORTS:
@@ -640,8 +640,10 @@ def moe_combine_bwd(dy, ye, plan: MoePlan, w, with_dye: bool = True):
         _need(w, "w", torch.float32, (T, k))
     dye = torch.empty((R, N), dtype=torch.bfloat16, device=dy.device) if with_dye else None
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
-    st = lib().bfp8_moe_combine_bwd(dy.data_ptr(), _ld(dy), ye.data_ptr(), _ld(ye), R, plan.row.data_ptr(),
-                                    plan.src.data_ptr(), _p(w), T, k, N, _p(dye), N, dw.data_ptr(), _stream())
+    offs = _offs(plan.offs)
+    st = lib().bfp8_moe_combine_bwd(dy.data_ptr(), _ld(dy), ye.data_ptr(), _ld(ye), R, offs.data_ptr(),
+                                    offs.shape[0] - 1, plan.row.data_ptr(), plan.src.data_ptr(), _p(w), T, k, N, _p(dye),
+                                    N, dw.data_ptr(), _stream())
     if st:
         _check(st)
     return dye, dw

@@ -646,21 +646,25 @@ bfp8_status bfp8_moe_combine(const void* ye, int64_t ldye, int64_t R, const int3
 }
 
 bfp8_status bfp8_moe_combine_bwd(const void* dy, int64_t lddy, const void* ye, int64_t ldye, int64_t R,
-                                 const int32_t* row, const int32_t* src, const float* w, int64_t T, int64_t k,
-                                 int64_t N, void* dye, int64_t lddye, float* dw, bfp8_stream_t stream) {
+                                 const int32_t* offs, int64_t E, const int32_t* row, const int32_t* src,
+                                 const float* w, int64_t T, int64_t k, int64_t N, void* dye, int64_t lddye, float* dw,
+                                 bfp8_stream_t stream) {
   const char* fn = "bfp8_moe_combine_bwd";
   bfp8_status st = check_slots(fn, T, k);
   if (st != BFP8_OK) return st;
   if ((st = check_dims(fn, R, N)) != BFP8_OK) return st;
   CHECK_ARG(lddy >= N && ldye >= N && (!dye || lddye >= N), "%s: a row stride is below N=%lld", fn, (long long)N);
-  CHECK_ARG((T == 0 || (row && dw && (N == 0 || dy))) && (R == 0 || (src && (N == 0 || ye))), "%s: null pointer", fn);
-  CHECK_ARG(al2(dy) && al2(ye) && al2(dye) && al4(row) && al4(src) && al4(w) && al4(dw), "%s: misaligned pointer", fn);
+  CHECK_ARG(E >= 1 && E <= kMaxGroups, "%s: E=%lld must be in [1, %d]", fn, (long long)E, kMaxGroups);
+  CHECK_ARG((T == 0 || (row && dw && (N == 0 || dy))) && (R == 0 || (src && (N == 0 || ye))) && (!dye || offs),
+            "%s: null pointer", fn);
+  CHECK_ARG(al2(dy) && al2(ye) && al2(dye) && al4(offs) && al4(row) && al4(src) && al4(w) && al4(dw),
+            "%s: misaligned pointer", fn);
   if (T == 0 && (!dye || R == 0 || N == 0)) return BFP8_OK;
   int sms = 0;
   if ((st = check_device(&sms)) != BFP8_OK) return st;
   const cudaError_t e =
-      launch_moe_combine_bwd(CombineBwdArgs{(const uint16_t*)dy, lddy, (const uint16_t*)ye, ldye, R, row, src, w, T,
-                                            (int)k, N, (uint16_t*)dye, lddye, dw},
+      launch_moe_combine_bwd(CombineBwdArgs{(const uint16_t*)dy, lddy, (const uint16_t*)ye, ldye, R, offs, E, row, src, w,
+                                            T, (int)k, N, (uint16_t*)dye, lddye, dw, 0},
                              sms, (cudaStream_t)stream);
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
 }

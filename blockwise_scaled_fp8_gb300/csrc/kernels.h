@@ -212,6 +212,8 @@ struct CombineBwdArgs {
   int64_t lddy;
   const uint16_t* ye;
   int64_t ldye, R;
+  const int32_t* offs;
+  int64_t E;
   const int32_t *row, *src;
   const float* w;
   int64_t T;
@@ -220,6 +222,7 @@ struct CombineBwdArgs {
   uint16_t* dye;  // null: dw only
   int64_t lddye;
   float* dw;
+  int64_t pieces;  // set by the launcher
 };
 cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& a, int num_sms, cudaStream_t st);
 

@@ -624,7 +624,8 @@ __device__ __forceinline__ uint64_t evict_first_policy() {
   return p;
 }
 
-constexpr int kCombineBatch = 8;  // rows of ye in flight a thread
+constexpr int kCombineBatch = 8;   // rows of ye in flight a thread
+constexpr int kCombinePiece = 16;  // rows of an expert that a CTA of the gradient takes, on average
 
 }  // namespace
 
@@ -713,72 +714,89 @@ __global__ void __launch_bounds__(kCombineThreads, 3) moe_combine_dw_kernel(cons
   }
 }
 
-// dw and dye: one warp a sorted row r of slot (t, j), dye[r] = w[t,j] dy[t]
-// from the same read of dy.  Row by row, so that ye is read and dye written
-// from one end to the other: written token by token, rows scattered over
-// memory, the same traffic took 655 us (16384 tokens x 4096, 8 experts; so 465).
-// ye and dye, touched once, are marked to leave L2 first, which leaves it to
-// dy, read for each of a token's k rows (without the marks 494 us with the same
-// kernel; dy in two or four column bands, a launch each: 455 and 453).  The
-// warps past the rows write the zeros of slots without a row.
+// dw and dye: a warp takes sorted rows r of slots (t, j), dye[r] = w[t,j] dy[t]
+// from the same read of dy.  By rows, because dye scattered over memory, row by
+// row of each token, was written at half the rate of a copy (655 us for 16384
+// tokens x 4096, 8 experts each).  A CTA takes one of `pieces` equal pieces of
+// one expert's rows, the CTAs piece by piece over all experts: the slots of an
+// expert are sorted by token, so the rows of one piece belong to neighbouring
+// tokens in every expert, and a token's dy is read from memory for one of them
+// and from L2 for most others (in the order of the rows it was read 7 of 8
+// times: 2.1 GB in, 1.1 out, 465 us, the memory's limit).  ye and dye, touched
+// once, are marked to leave L2 first.  With less to read it is a matter of
+// loads in flight: 16 a lane 397 us, 8 of them 482.  Pieces of 8 / 16 / 32 rows:
+// 401 / 397 / 430.  The last CTAs write the zeros of rows past the experts and
+// of slots without a row.
 template <int VEC>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const CombineBwdArgs a) {
-  constexpr int kClasses = kCombineThreads / 32, U = 4;  // U loads of each input in flight a lane
+  constexpr int kClasses = kCombineThreads / 32;
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = (int)(threadIdx.x & 31);
-  const int64_t r = (int64_t)blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5);
-  if (r >= a.R) {
-    const int64_t warps = (int64_t)gridDim.x * (kCombineThreads / 32);
-    for (int64_t i = (r - a.R) * 32 + lane; i < a.T * a.k; i += (warps - a.R) * 32) {
-      const int at = __ldg(a.row + i);
-      if (at < 0 || at >= a.R) a.dw[i] = 0.0f;
+  const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
+  const uint64_t once = evict_first_policy();
+  const int64_t blocks = a.E * a.pieces;
+  int64_t r = 0, end = 0;
+  if ((int64_t)blockIdx.x < blocks) {
+    const int64_t e = blockIdx.x % a.E, piece = blockIdx.x / a.E;
+    const int64_t lo = max(__ldg(a.offs + e), 0), n = min((int64_t)__ldg(a.offs + e + 1), a.R) - lo;
+    if (n <= 0) return;
+    r = lo + n * piece / a.pieces + warp;
+    end = lo + n * (piece + 1) / a.pieces;
+  } else {
+    const int64_t at = (blockIdx.x - blocks) * kClasses + warp, warps = (gridDim.x - blocks) * kClasses;
+    for (int64_t i = at * 32 + lane; i < a.T * a.k; i += warps * 32) {
+      const int row = __ldg(a.row + i);
+      if (row < 0 || row >= a.R) a.dw[i] = 0.0f;
     }
+    float z[VEC] = {};
+    for (int64_t q = max((int64_t)__ldg(a.offs + a.E), (int64_t)0) + at; q < a.R; q += warps)
+      for (int64_t n = (int64_t)lane * VEC; n < a.N; n += 32 * VEC) store_bf16s<VEC>(a.dye + q * a.lddye + n, z, once);
     return;
   }
-  const int slot = __ldg(a.src + r);
-  const int64_t t = slot >= 0 ? (int64_t)((uint32_t)slot / (uint32_t)a.k) : a.T;
-  const uint64_t once = evict_first_policy();
-  const bool live = t < a.T;  // not padding
-  const float w = live ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
-  const uint16_t *dy = a.dy + (live ? t : 0) * a.lddy, *ye = a.ye + r * a.ldye;
-  uint16_t* dye = a.dye + r * a.lddye;
-  float dot[kClasses];
+  int slot = r < end ? __ldg(a.src + r) : -1;
+  for (; r < end; r += kClasses) {
+    const int64_t t = slot >= 0 ? (int64_t)((uint32_t)slot / (uint32_t)a.k) : a.T;
+    const bool live = t < a.T;  // not padding
+    const float w = live ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
+    const int slot_next = r + kClasses < end ? __ldg(a.src + r + kClasses) : -1;
+    const uint16_t *dy = a.dy + (live ? t : 0) * a.lddy, *ye = a.ye + r * a.ldye;
+    uint16_t* dye = a.dye + r * a.lddye;
+    float dot[kClasses];
 #pragma unroll
-  for (int c = 0; c < kClasses; ++c) dot[c] = 0.0f;
-  for (int64_t base = (int64_t)lane * VEC; base < a.N; base += kCombineThreads * VEC) {
+    for (int c = 0; c < kClasses; ++c) dot[c] = 0.0f;
+    for (int64_t base = (int64_t)lane * VEC; base < a.N; base += kCombineThreads * VEC) {
+      Bf16s<VEC> d[kClasses], v[kClasses];
 #pragma unroll
-    for (int c0 = 0; c0 < kClasses; c0 += U) {
-      Bf16s<VEC> d[U], v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t n = base + (c0 + u) * 32 * VEC;
+      for (int c = 0; c < kClasses; ++c) {
+        const int64_t n = base + c * 32 * VEC;
         if (live && n < a.N) {
-          v[u].load(ye + n, once);
-          d[u].load(dy + n);
+          v[c].load(ye + n, once);
+          d[c].load(dy + n);
         } else {
-          v[u].zero();
-          d[u].zero();
+          v[c].zero();
+          d[c].zero();
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t n = base + (c0 + u) * 32 * VEC;
+      for (int c = 0; c < kClasses; ++c) {
+        const int64_t n = base + c * 32 * VEC;
         float o[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          dot[c0 + u] = fmaf(d[u].get(i), v[u].get(i), dot[c0 + u]);
-          o[i] = w * d[u].get(i);
+          dot[c] = fmaf(d[c].get(i), v[c].get(i), dot[c]);
+          o[i] = w * d[c].get(i);
         }
         if (n < a.N) store_bf16s<VEC>(dye + n, o, once);
       }
     }
-  }
-  if (!live) return;
-  float sum = 0.0f;
+    if (live) {
+      float sum = 0.0f;
 #pragma unroll
-  for (int c = 0; c < kClasses; ++c) sum += warp_sum(dot[c]);
-  if (lane == 0) a.dw[slot] = sum;
+      for (int c = 0; c < kClasses; ++c) sum += warp_sum(dot[c]);
+      if (lane == 0) a.dw[slot] = sum;
+    }
+    slot = slot_next;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -927,16 +945,19 @@ cudaError_t launch_moe_combine(const CombineArgs& args, cudaStream_t st) {
              : launch_pdl(moe_combine_kernel<1>, grid, kCombineThreads, 0, st, a);
 }
 
-cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& a, int num_sms, cudaStream_t st) {
-  const bool vec = a.N % 8 == 0 && rows16(a.dy, a.lddy) && rows16(a.ye, a.ldye) && (!a.dye || rows16(a.dye, a.lddye));
-  if (!a.dye) {
-    if (a.T == 0) return cudaSuccess;
-    return vec ? launch_pdl(moe_combine_dw_kernel<8>, (unsigned)a.T, kCombineThreads, 0, st, a)
-               : launch_pdl(moe_combine_dw_kernel<1>, (unsigned)a.T, kCombineThreads, 0, st, a);
+cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& args, int num_sms, cudaStream_t st) {
+  const bool vec = args.N % 8 == 0 && rows16(args.dy, args.lddy) && rows16(args.ye, args.ldye) && (!args.dye || rows16(args.dye, args.lddye));
+  if (!args.dye) {
+    if (args.T == 0) return cudaSuccess;
+    return vec ? launch_pdl(moe_combine_dw_kernel<8>, (unsigned)args.T, kCombineThreads, 0, st, args)
+               : launch_pdl(moe_combine_dw_kernel<1>, (unsigned)args.T, kCombineThreads, 0, st, args);
   }
-  // a warp a row, and some for the slots without one
-  const int64_t zero_warps = std::min<int64_t>(cdiv(a.T * a.k, 32), 8 * num_sms);
-  const unsigned grid = (unsigned)cdiv(a.R + zero_warps, kCombineThreads / 32);
+  CombineBwdArgs a = args;
+  a.pieces = cdiv(a.R, a.E * kCombinePiece);
+  if (a.pieces < 1) a.pieces = 1;
+  // and CTAs for the zeros
+  const int64_t zeros = std::min<int64_t>(cdiv(std::max(cdiv(a.T * a.k, 32), a.R), kCombineThreads / 32), 2 * num_sms);
+  const unsigned grid = (unsigned)(a.E * a.pieces + zeros);
   return vec ? launch_pdl(moe_combine_bwd_kernel<8>, grid, kCombineThreads, 0, st, a)
              : launch_pdl(moe_combine_bwd_kernel<1>, grid, kCombineThreads, 0, st, a);
 }

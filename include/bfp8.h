@@ -348,13 +348,13 @@ BFP8_API bfp8_status bfp8_moe_combine(const void *ye, int64_t ldye, int64_t R, c
  * The combine's gradient: dw[t,j] = dy[t] . ye[row[t,j]] (fp32, 0 where row is
  * -1) and, where dye is not NULL, dye[r] = w[src[r]] * dy[src[r] / k], zero on
  * padding rows (bf16 [R,N], lddye >= N, every row written).  (The FP8 path
- * takes dw alone and forms dye's codes with bfp8_moe_dispatch.)  row and src
- * are one plan's; w NULL: 1.
+ * takes dw alone and forms dye's codes with bfp8_moe_dispatch.)  offs [E+1],
+ * row and src are one plan's (offs may be NULL without dye); w NULL: 1.
  */
 BFP8_API bfp8_status bfp8_moe_combine_bwd(const void *dy, int64_t lddy, const void *ye, int64_t ldye, int64_t R,
-                                          const int32_t *row, const int32_t *src, const float *w, int64_t T,
-                                          int64_t k, int64_t N, void *dye, int64_t lddye, float *dw,
-                                          bfp8_stream_t stream);
+                                          const int32_t *offs, int64_t E, const int32_t *row, const int32_t *src,
+                                          const float *w, int64_t T, int64_t k, int64_t N, void *dye, int64_t lddye,
+                                          float *dw, bfp8_stream_t stream);
 
 /*
  * Routed product, for batches that give an expert few rows (decoding): C[r]

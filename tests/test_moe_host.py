@@ -97,10 +97,10 @@ def test_combine_argument_validation():
         assert call(**bad) == BAD, bad
     assert call(T=0) == B.BFP8_OK
     assert call(N=0) == B.BFP8_OK
-    call = _caller("bfp8_moe_combine_bwd", dict(dy=P, lddy=64, ye=P, ldye=64, R=8, row=P, src=P, w=P, T=4, k=2, N=64,
+    call = _caller("bfp8_moe_combine_bwd", dict(dy=P, lddy=64, ye=P, ldye=64, R=8, offs=P, E=8, row=P, src=P, w=P, T=4, k=2, N=64,
                                                 dye=P, lddye=64, dw=P, st=NULL))
     for bad in (dict(T=-1), dict(k=40), dict(dy=NULL), dict(ye=NULL), dict(row=NULL), dict(src=NULL), dict(dw=NULL),
-                dict(lddy=63), dict(lddye=63), dict(ldye=1), dict(dye=ODD), dict(dw=ODD)):
+                dict(offs=NULL), dict(E=0), dict(E=1025), dict(lddy=63), dict(lddye=63), dict(ldye=1), dict(dye=ODD), dict(dw=ODD)):
         assert call(**bad) == BAD, bad
     assert call(T=0, dye=NULL) == B.BFP8_OK
 
