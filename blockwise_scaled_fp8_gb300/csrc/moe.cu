@@ -139,16 +139,18 @@ __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-
 // k = 6: 19 us, 411; one token 2.0 us.
 template <int VPL, bool F32, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArgs a) {
-  // per warp: E + 32 values of groups that are not whole powers of two of lanes, later the sorted lists (VPL <= 8)
+  // per warp: E + 32 values of groups that are not whole powers of two of lanes, later the sorted lists
   extern __shared__ __align__(16) float s_route[];
-  constexpr bool kByLogit = !SIGMOID && !BIAS, kPacked = kByLogit && !F32 && VPL <= 8;
+  constexpr bool kByLogit = !SIGMOID && !BIAS, kPacked = kByLogit && !F32;
+  constexpr int kLists = (VPL + 7) / 8, kLen = VPL / kLists;  // sorted lists a lane
+  static_assert(kLists * kLen == VPL, "lists of one length");
   pdl_launch_dependents();
   pdl_wait();
   const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
   const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + warp;
   if (t >= a.T) return;
   const int E = (int)a.E, e0 = lane * VPL;
-  float* mine_s = s_route + warp * (VPL <= 8 ? VPL * 64 : E + 32);
+  float* mine_s = s_route + warp * (VPL * 64);  // (E + 32 <= 64 VPL)
   const int64_t at = t * a.ldl;
   float c[VPL];  // logit, then the choice value (-inf: not eligible)
   load_logits<VPL, F32>(a, at, e0, c);
@@ -246,73 +248,55 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
         if (!((kept >> min((e0 + i) / S, 31)) & 1u)) c[i] = -INFINITY;
     }
   }
-  // k choices: lane j keeps choice j
+  // k choices: lane j keeps choice j.  A key is the value's order with the
+  // expert's complement below it (kPacked) or the complement of its place in
+  // the lane, so that of equal values the lowest expert comes first.
+  using Key = std::conditional_t<kPacked, uint32_t, uint64_t>;
+  Key head[kLists];
+  Key* list = reinterpret_cast<Key*>(mine_s) + lane;  // the rest, [list][place][lane]: a winner fetches its next key
+  int next[kLists];                                   // where a list's next key lies
+  __syncwarp();  // the groups' values, which lay here, have been read
+#pragma unroll
+  for (int l = 0; l < kLists; ++l) {
+    Key key[kLen];
+#pragma unroll
+    for (int i = 0; i < kLen; ++i) {
+      const int at_i = l * kLen + i;
+      if constexpr (kPacked) key[i] = (order_key(c[at_i]) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e0 - at_i);
+      else key[i] = ((uint64_t)order_key(c[at_i]) << 32) | (uint32_t)(VPL - 1 - at_i);
+    }
+    sort_down(key);
+    head[l] = key[0];
+    next[l] = 32 * l * kLen;
+#pragma unroll
+    for (int i = 1; i < kLen; ++i) list[32 * (l * kLen + i - 1)] = key[i];
+    list[32 * (l * kLen + kLen - 1)] = 0;  // never wins: nothing is read past it
+  }
   int my_e = -1;
-  if constexpr (kPacked) {
-    uint32_t key[VPL];  // 16 bits of the logit's order, then the expert's complement: every key differs
+  for (int j = 0; j < a.k; ++j) {
+    Key my = head[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      key[i] = (order_key(c[i]) & 0xFFFF0000u) | (uint32_t)(0xFFFF - e0 - i);
-    sort_down(key);
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t best = __reduce_max_sync(kFull, key[0]);
-      if (best <= (kNoKey | 0xFFFFu)) break;
-      if (lane == j) my_e = 0xFFFF - (int)(best & 0xFFFFu);
-      const bool mine = key[0] == best;
-#pragma unroll
-      for (int i = 0; i + 1 < VPL; ++i) key[i] = mine ? key[i + 1] : key[i];
-      if (mine) key[VPL - 1] = 0;
+    for (int l = 1; l < kLists; ++l) my = my > head[l] ? my : head[l];
+    const uint32_t hi = (uint32_t)(kPacked ? my : my >> (kPacked ? 0 : 32)), best = __reduce_max_sync(kFull, hi);
+    if (best <= kNoKey) break;
+    int e;
+    bool mine;
+    if constexpr (kPacked) {
+      e = 0xFFFF - (int)(best & 0xFFFFu);
+      mine = hi == best;
+    } else {
+      const int win = __ffs(__ballot_sync(kFull, hi == best)) - 1;  // lowest lane = lowest experts
+      e = __shfl_sync(kFull, e0 + VPL - 1 - (int)(uint32_t)my, win);
+      mine = lane == win;
     }
-  } else if constexpr (VPL <= 8) {
-    uint64_t key[VPL];  // the value's order, then the complement of the place in the lane
+    if (lane == j) my_e = e;
+    if (mine) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      key[i] = ((uint64_t)order_key(c[i]) << 32) | (uint32_t)(VPL - 1 - i);
-    sort_down(key);
-    // the rest of the list, [place][lane]: the winner fetches its next key
-    uint64_t* list = reinterpret_cast<uint64_t*>(mine_s) + lane;
-    uint64_t head = key[0];
-    if constexpr (VPL > 1) {
-      __syncwarp();  // the groups' values, which lay here, have been read
-#pragma unroll
-      for (int i = 1; i < VPL; ++i) list[32 * (i - 1)] = key[i];
-      list[32 * (VPL - 1)] = 0;
-    }
-    for (int j = 0; j < a.k; ++j) {
-      const uint32_t hi = (uint32_t)(head >> 32), best = __reduce_max_sync(kFull, hi);
-      if (best <= kNoKey) break;
-      const int win = __ffs(__ballot_sync(kFull, hi == best)) - 1;
-      const int e = __shfl_sync(kFull, e0 + VPL - 1 - (int)(uint32_t)head, win);
-      if (lane == j) my_e = e;
-      if (lane == win) {  // (the list ends with a key of 0, which never wins: nothing is read past it)
-        if constexpr (VPL > 1) {
-          head = *list;
-          list += 32;
-        } else {
-          head = 0;
+      for (int l = 0; l < kLists; ++l)
+        if (kLists == 1 || head[l] == my) {
+          head[l] = list[next[l]];
+          next[l] += 32;
         }
-      }
-    }
-  } else {
-    uint32_t key[VPL];
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = order_key(c[i]);
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t m = key[0];
-#pragma unroll
-      for (int i = 1; i < VPL; ++i) m = max(m, key[i]);
-      const uint32_t best = __reduce_max_sync(kFull, m);
-      if (best <= kNoKey) break;
-      const int win = __ffs(__ballot_sync(kFull, m == best)) - 1;
-      int at_i = 0;
-#pragma unroll
-      for (int i = VPL - 1; i >= 0; --i)
-        if (key[i] == best) at_i = i;
-      const int e = __shfl_sync(kFull, e0 + at_i, win);
-      if (lane == j) my_e = e;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (e == e0 + i) key[i] = 0;
     }
   }
   float p = 0.0f;
@@ -572,11 +556,17 @@ namespace {
 // VEC consecutive bf16 values as fp32
 template <int VEC>
 struct Bf16s {
+  static_assert(VEC == 8 || VEC == 4 || VEC == 2 || VEC == 1, "one access of 16, 8, 4 or 2 bytes");
   uint32_t v[VEC == 1 ? 1 : VEC / 2];
   __device__ __forceinline__ void load(const uint16_t* p) {
     if constexpr (VEC == 8) {
       const uint4 q = ld_nc_v4(p);
       v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else if constexpr (VEC == 4) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+      v[0] = q.x, v[1] = q.y;
+    } else if constexpr (VEC == 2) {
+      v[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
     } else {
       v[0] = __ldg(p);
     }
@@ -587,7 +577,7 @@ struct Bf16s {
                    : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                    : "l"(p), "l"(policy));
     } else {
-      v[0] = __ldg(p);
+      load(p);
     }
   }
   __device__ __forceinline__ void zero() {
@@ -602,6 +592,10 @@ __device__ __forceinline__ void store_bf16s(uint16_t* p, const float (&f)[VEC]) 
   if constexpr (VEC == 8) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+  } else if constexpr (VEC == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
   } else {
     *p = f32_to_bf16(f[0]);
   }
@@ -614,7 +608,7 @@ __device__ __forceinline__ void store_bf16s(uint16_t* p, const float (&f)[VEC], 
                  "r"(pack_bf16x2(f[2], f[3])), "r"(pack_bf16x2(f[4], f[5])), "r"(pack_bf16x2(f[6], f[7])), "l"(policy)
                  : "memory");
   } else {
-    *p = f32_to_bf16(f[0]);
+    store_bf16s<VEC>(p, f);
   }
 }
 // L2 policy of data that is touched once: it is the first to leave.
@@ -814,7 +808,10 @@ static cudaError_t by_vpl(int64_t E, F&& f) {
   if (n <= 5) return f(std::integral_constant<int, 5>{});
   if (n <= 6) return f(std::integral_constant<int, 6>{});
   if (n <= 8) return f(std::integral_constant<int, 8>{});
+  if (n <= 10) return f(std::integral_constant<int, 10>{});
+  if (n <= 12) return f(std::integral_constant<int, 12>{});
   if (n <= 16) return f(std::integral_constant<int, 16>{});
+  if (n <= 24) return f(std::integral_constant<int, 24>{});
   return f(std::integral_constant<int, 32>{});
 }
 
@@ -843,9 +840,8 @@ cudaError_t launch_moe_route(const RouteArgs& args, cudaStream_t st) {
       else
         while (a.group_lanes * 2 * a.groups <= 32) a.group_lanes *= 2;
     }
-    // (VPL <= 8: E + 32 <= 64 VPL)
-    const size_t smem = kVpl <= 8 ? (size_t)(kRouteThreads / 32) * kVpl * 64 * 4
-                        : a.groups > 1 ? (size_t)(kRouteThreads / 32) * (a.E + 32) * 4 : 0;
+    constexpr size_t smem = (size_t)(kRouteThreads / 32) * kVpl * 64 * 4;
+    static_assert(smem <= 48 * 1024, "no opt-in needed");
     return by_bool(a.f32, [&](auto f32) {
       return by_bool(a.sigmoid, [&](auto sig) {
         return by_bool(a.bias != nullptr, [&](auto bias) {
@@ -934,23 +930,42 @@ cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
   return run_plan<11>(a, st);
 }
 
-static bool rows16(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; }
+// Columns an access takes: 8, 4, 2 or 1, the most that the width, the rows'
+// strides and their bases allow (one access then stays within a row, aligned).
+// 8192 tokens, eight rows each: 95 us at 4000 columns (8), 106 at 4004 (4), 143
+// at 4002 (2), 333 at 4001 (1).
+struct RowAlign {
+  int64_t bits;
+  explicit RowAlign(int64_t N) : bits(N) {}
+  RowAlign& row(const void* p, int64_t ld) {
+    bits |= (int64_t)(reinterpret_cast<uintptr_t>(p) / 2) | ld;
+    return *this;
+  }
+  template <typename F>
+  cudaError_t go(F&& f) const {
+    if (bits % 8 == 0) return f(std::integral_constant<int, 8>{});
+    if (bits % 4 == 0) return f(std::integral_constant<int, 4>{});
+    if (bits % 2 == 0) return f(std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 1>{});
+  }
+};
 
 cudaError_t launch_moe_combine(const CombineArgs& args, cudaStream_t st) {
-  CombineArgs a = args;
-  const bool vec = a.N % 8 == 0 && rows16(a.ye, a.ldye) && rows16(a.y, a.ldy);
-  a.col_blocks = (int)cdiv(a.N, kCombineThreads * (vec ? 8 : 1));
-  const unsigned grid = (unsigned)(a.T * a.col_blocks);
-  return vec ? launch_pdl(moe_combine_kernel<8>, grid, kCombineThreads, 0, st, a)
-             : launch_pdl(moe_combine_kernel<1>, grid, kCombineThreads, 0, st, a);
+  return RowAlign(args.N).row(args.ye, args.ldye).row(args.y, args.ldy).go([&](auto vec) {
+    constexpr int kVec = decltype(vec)::value;
+    CombineArgs a = args;
+    a.col_blocks = (int)cdiv(a.N, kCombineThreads * kVec);
+    return launch_pdl(moe_combine_kernel<kVec>, (unsigned)(a.T * a.col_blocks), kCombineThreads, 0, st, a);
+  });
 }
 
 cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& args, int num_sms, cudaStream_t st) {
-  const bool vec = args.N % 8 == 0 && rows16(args.dy, args.lddy) && rows16(args.ye, args.ldye) && (!args.dye || rows16(args.dye, args.lddye));
+  const RowAlign rows = RowAlign(args.N).row(args.dy, args.lddy).row(args.ye, args.ldye);
   if (!args.dye) {
     if (args.T == 0) return cudaSuccess;
-    return vec ? launch_pdl(moe_combine_dw_kernel<8>, (unsigned)args.T, kCombineThreads, 0, st, args)
-               : launch_pdl(moe_combine_dw_kernel<1>, (unsigned)args.T, kCombineThreads, 0, st, args);
+    return rows.go([&](auto vec) {
+      return launch_pdl(moe_combine_dw_kernel<decltype(vec)::value>, (unsigned)args.T, kCombineThreads, 0, st, args);
+    });
   }
   CombineBwdArgs a = args;
   a.pieces = cdiv(a.R, a.E * kCombinePiece);
@@ -958,8 +973,9 @@ cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& args, int num_sms, cuda
   // and CTAs for the zeros
   const int64_t zeros = std::min<int64_t>(cdiv(std::max(cdiv(a.T * a.k, 32), a.R), kCombineThreads / 32), 2 * num_sms);
   const unsigned grid = (unsigned)(a.E * a.pieces + zeros);
-  return vec ? launch_pdl(moe_combine_bwd_kernel<8>, grid, kCombineThreads, 0, st, a)
-             : launch_pdl(moe_combine_bwd_kernel<1>, grid, kCombineThreads, 0, st, a);
+  return RowAlign(rows).row(a.dye, a.lddye).go([&](auto vec) {
+    return launch_pdl(moe_combine_bwd_kernel<decltype(vec)::value>, grid, kCombineThreads, 0, st, a);
+  });
 }
 
 }  // namespace bfp8

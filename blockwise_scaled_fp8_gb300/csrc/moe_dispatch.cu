@@ -222,22 +222,29 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
         tma_gather4(stage + (uint32_t)(half * kDsBoxBytes + r4 * 128), &tmap_x, full0 + 8 * s, c0 + 64 * half, tok[0],
                     tok[1], tok[2], tok[3]);
       } else {
-        // rows that TMA cannot read: element by element
-        for (int i = 0; i < 4; ++i) {
-          const int r = r4 + i;
-          for (int ch = 8 * half; ch < 8 * half + 8; ++ch) {
-            const int cols = min(C - (c0 + 8 * ch), 8);
-            uint32_t v[4] = {};
-            if (tok[i] < p.a.T) {
-              const uint16_t* from = p.a.x + (int64_t)tok[i] * p.a.ldx + c0 + 8 * ch;
+        // rows that TMA cannot read, element by element: lane l columns l, l + 32, ..
+        const int r0 = 64 * (warp - kDsConsumers / 32);
+        constexpr int kRows = 8;  // in flight
+        for (int i0 = 0; i0 < 64; i0 += kRows) {
+          uint16_t v[kRows][4];
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (j < cols) v[j >> 1] |= (uint32_t)__ldg(from + j) << (16 * (j & 1));
+          for (int i = 0; i < kRows; ++i) {
+            const int t = __shfl_sync(kAll, tok[i & 3], (i0 + i) >> 2);
+            const uint16_t* from = p.a.x + (int64_t)t * p.a.ldx + c0 + lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = t < p.a.T && c0 + lane + 32 * j < C ? __ldg(from + 32 * j) : (uint16_t)0;
+          }
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i0 + i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int c = lane + 32 * j;
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + (uint32_t)((c >> 6) * kDsBoxBytes + r * 128 +
+                                                                              ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2)),
+                           "h"(v[i][j])
+                           : "memory");
             }
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             stage + (uint32_t)((ch >> 3) * kDsBoxBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4))),
-                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                         : "memory");
           }
         }
         mbar_arrive(full0 + 8 * s);
