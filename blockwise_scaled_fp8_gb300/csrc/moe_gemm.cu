@@ -10,19 +10,19 @@
 // the product; so the operands swap places in the MMA, as in the dense GEMM
 // for few rows: 128 rows of W are the instruction's A, streamed by TMA through
 // a ring that holds most of an SM's shared memory, and R = 16, 32 or 64 tokens
-// its B, gathered by TMA from the tokens' codes (four rows a gather; past the
-// expert's last row zeros).  A persistent CTA per SM goes through a contiguous
+// its B, gathered by TMA from the tokens' codes (four rows a gather; gathers past
+// the expert's last row are left out).  A persistent CTA per SM goes through a contiguous
 // run of (128-row tile, R tokens) walks over all reached experts without
 // draining the ring in between; a tile is walked again for the next R rows of
-// its expert, from L2.  Where the batch is so small that the tiles leave SMs idle (and its rows
-// are few enough for one walk), each tile's K-blocks are split over a cluster
-// instead and the partial sums added in rank order through distributed shared
-// memory.
+// its expert, from L2.  Where the batch is so small that the tiles leave SMs idle
+// (and its rows are few enough for one walk), each tile's K-blocks are split over
+// a cluster instead and the partial sums added in rank order through distributed
+// shared memory.
 //
-//   warp 0      producer: lane 0 W's tile, lanes l < R/4 four tokens each
-//   warps 1, 3  MMA issuers (M = 128, N = R) on alternate K-blocks
-//   warp 2      a_s of the tokens and b_s of the tile, per K-block
-//   warps 4-7   promotion (lane n: column n of the tile, its R tokens), stores
+//   warps 0, 8..  producers: warp 0 W's tile, each of them 16 tokens
+//   warps 1, 3    MMA issuers (M = 128, N = R) on alternate K-blocks
+//   warp 2        a_s of the tokens and b_s of the tile, per K-block
+//   warps 4-7     promotion (lane n: column n of the tile, its R tokens), stores
 // Every mbarrier wait is bounded; a role that gives up sets the abort flag, the
 // others leave their loops, and copies and MMAs in flight finish before the
 // CTA exits.
@@ -41,12 +41,15 @@ static __device__ uint32_t g_routed_error;
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kRpThreads = 256;
 constexpr int kRpTile = 128;  // rows of W a tile
 
 template <int R>
 struct RpCfg {
   static_assert(R == 16 || R == 32 || R == 64, "tokens of one walk");
+  // one producer warp for each 16 tokens: a warp issues a gather of four every 84
+  // cycles or so, and a K-block's weights arrive every 700
+  static constexpr int kProducers = R / 16;
+  static constexpr int kThreads = 256 + 32 * (kProducers - 1);
   static constexpr int kStages = R == 16 ? 11 : R == 32 ? 10 : 8;
   static constexpr int kBufs = R == 64 ? 4 : 8;             // R-column partial products in tensor memory
   static constexpr int kTmemCols = kBufs * R;               // 128 or 256
@@ -62,7 +65,7 @@ struct RpCfg {
   static constexpr int kNumBars = 4 * kStages + 2 * kBufs + 1;
   static constexpr int kOffMisc = kOffBar + (kNumBars + 1) / 2 * 16;  // tensor memory's address, abort flag, a zero
   static constexpr int kOffCount = kOffMisc + 16;
-  static constexpr int kSmemBytes = kOffCount + 2 * 4 * (kRpThreads / 32) + 1024;
+  static constexpr int kSmemBytes = kOffCount + 2 * 4 * (kThreads / 32) + 1024;
   static_assert(kRpTile * R * 4 <= kStages * kWBytes, "the partial sums of a split tile fit in the W stages");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -83,7 +86,8 @@ __device__ __forceinline__ float lds32_cluster(uint32_t addr) {
   return v;
 }
 
-// The A row of sorted row m (before r1): its slot's token, or m itself; a.T (past A, read as zeros) where there is none.
+// The A row that is gathered for sorted row m of an expert whose rows end at r1: its
+// slot's token, or m itself; a.T (past A, read as zeros) where there is none.
 __device__ __forceinline__ int token_of(const GemmRoutedArgs& a, int64_t m, int64_t r1) {
   if (m >= r1) return (int)a.T;
   int64_t t = m;
@@ -97,11 +101,11 @@ __device__ __forceinline__ int token_of(const GemmRoutedArgs& a, int64_t m, int6
 }  // namespace
 
 template <int R>
-__global__ void __launch_bounds__(kRpThreads, 1)
+__global__ void __launch_bounds__(RpCfg<R>::kThreads, 1)
     gemm_routed_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUtensorMap tma_x,
                        const GemmRoutedArgs a, const int splits) {
   using Cfg = RpCfg<R>;
-  constexpr int ST = Cfg::kStages, NT = Cfg::kBufs;
+  constexpr int ST = Cfg::kStages, NT = Cfg::kBufs, kWarps = Cfg::kThreads / 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -120,7 +124,7 @@ __global__ void __launch_bounds__(kRpThreads, 1)
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(full0 + 8 * i, 1);
+      mbar_init(full0 + 8 * i, Cfg::kProducers);
       mbar_init(empty0 + 8 * i, 1);
       mbar_init(sfull0 + 8 * i, 32);  // one cp.async arrival per loader lane
       mbar_init(sempty0 + 8 * i, 4);  // the promotion warps
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kRpThreads, 1)
   pdl_wait();
   // the experts that hold rows, in order, and the walks (of R rows) before each
   int reached = 0, walks = 0;
-  for (int e0 = 0; e0 < E; e0 += kRpThreads) {
+  for (int e0 = 0; e0 < E; e0 += Cfg::kThreads) {
     const int e = e0 + tid;
     int64_t rows = 0;
     if (e < E) rows = min((int64_t)__ldg(a.offs + e + 1), a.R) - max(__ldg(a.offs + e), 0);
@@ -160,15 +164,15 @@ __global__ void __launch_bounds__(kRpThreads, 1)
     }
     if (lane == 31) {
       s_count[warp] = __popc(vote);
-      s_count[kRpThreads / 32 + warp] = inc;
+      s_count[kWarps + warp] = inc;
     }
     __syncthreads();
     int at = reached, before = walks;
 #pragma unroll
-    for (int w = 0; w < kRpThreads / 32; ++w) {
-      if (w < warp) at += s_count[w], before += s_count[kRpThreads / 32 + w];
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += s_count[w], before += s_count[kWarps + w];
       reached += s_count[w];
-      walks += s_count[kRpThreads / 32 + w];
+      walks += s_count[kWarps + w];
     }
     if (mine > 0) {
       at += __popc(vote & ((1u << lane) - 1u));
@@ -229,29 +233,34 @@ __global__ void __launch_bounds__(kRpThreads, 1)
   const Walk w_first = w;
   bool ok = true;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    int n = 0;  // K-blocks issued
+  if (warp == 0 || warp >= 8) {
+    // ------------------------------------------------------------ producers: tokens 16 q .. 16 q + 15, q = 0 also W
+    const int q = warp == 0 ? 0 : warp - 7;
+    constexpr uint32_t kPart = 16 * kBlock;  // bytes of a producer's tokens
+    // Gathers of four rows that hold a row of the walk; the others are left out:
+    // what their rows of the stage hold feeds columns that are not stored.
+    auto gathers = [&]() { return (int)((min(max(w.r1 - w.m0 - 16 * q, (int64_t)0), (int64_t)16) + 3) / 4); };
+    int n = 0;                               // K-blocks issued
     int at_e = -1;
     int64_t at_m = -1;
     int tok[4] = {};
-    auto issue_w = [&](int j, int st, int row) {  // lane 0
-      mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(Cfg::kWBytes + Cfg::kXBytes));
+    auto issue_w = [&](int j, int st, int row) {  // lane 0 of producer 0
+      mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(Cfg::kWBytes + 512 * gathers()));
       tma_load_2d(sbase + (uint32_t)(st * Cfg::kWBytes), &tma_w, full0 + 8 * st, (kb0 + j) * kBlock, row);
     };
     // the first stages' weights go out before the tokens are known
     const int ahead = w.x < last ? min(ST, kbn) : 0;
-    if (lane == 0)
+    if (q == 0 && lane == 0)
       for (int j = 0; j < ahead; ++j) issue_w(j, j, w.e * (int)a.N + w.block * kRpTile);
     for (; w.x < last && ok; next(w)) {
       if (w.e != at_e || w.m0 != at_m) {
         at_e = w.e, at_m = w.m0;
-        if (lane < R / 4) {
+        if (lane < 4) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tok[i] = token_of(a, w.m0 + 4 * lane + i, w.r1);
+          for (int i = 0; i < 4; ++i) tok[i] = token_of(a, w.m0 + 16 * q + 4 * lane + i, w.r1);
         }
       }
-      const int row = w.e * (int)a.N + w.block * kRpTile;
+      const int row = w.e * (int)a.N + w.block * kRpTile, live = gathers();
       for (int j = 0; j < kbn; ++j, ++n) {
         const int st = n % ST;
         if (n >= ahead) {
@@ -261,12 +270,13 @@ __global__ void __launch_bounds__(kRpThreads, 1)
             ok = false;
             break;
           }
-          if (lane == 0) issue_w(j, st, row);
+          if (q == 0 && lane == 0) issue_w(j, st, row);
         }
+        if (q > 0 && lane == 0) mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(512 * live));
         __syncwarp();
-        if (lane < R / 4)
-          tma_gather4(sX + (uint32_t)(st * Cfg::kXBytes + lane * 512), &tma_x, full0 + 8 * st, (kb0 + j) * kBlock, tok[0],
-                      tok[1], tok[2], tok[3]);
+        if (lane < live)
+          tma_gather4(sX + (uint32_t)(st * Cfg::kXBytes) + q * kPart + lane * 512, &tma_x, full0 + 8 * st,
+                      (kb0 + j) * kBlock, tok[0], tok[1], tok[2], tok[3]);
       }
     }
     if (!ok && lane == 0)  // copies already issued land before this CTA's shared memory goes away
@@ -417,16 +427,30 @@ __global__ void __launch_bounds__(kRpThreads, 1)
     // wait before them is bounded): the first makes the partial sums visible,
     // the second keeps each CTA resident until no peer reads them any more.
     cluster_sync_all();
-    if (warp >= 4 && first < last) {
+    if (warp >= 4 && warp < 8 && first < last) {
       const Walk& f = w_first;
-      const int nl = 32 * (warp - 4) + lane, per = R / splits, m_lo = split * per;
+      // Row m of the walk's rows is rank m % splits' to join; the loads of four
+      // rows are in flight at once (one after another, a pair of CTAs took 3 us
+      // for 16 rows).
+      const int nl = 32 * (warp - 4) + lane, live = (int)min(f.r1 - f.m0, (int64_t)R);
       const int64_t col = (int64_t)f.block * kRpTile + nl;
-      for (int m = m_lo; m < m_lo + per; ++m) {
-        float sum = 0.0f;
-        for (int s = 0; s < splits; ++s)
-          sum += lds32_cluster(mapa_shared(sbase + 4u * (uint32_t)(m * kRpTile + nl), (uint32_t)s));
-        if (col < a.N && f.m0 + m < f.r1)
-          a.c[(f.m0 + m) * a.ldc + col] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
+      for (int m0 = split; m0 < live; m0 += 4 * splits) {
+        float v[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            if (m0 + i * splits < live && s < splits)
+              v[i][s] = lds32_cluster(mapa_shared(sbase + 4u * (uint32_t)((m0 + i * splits) * kRpTile + nl), (uint32_t)s));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = m0 + i * splits;
+          float sum = 0.0f;
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            if (m < live && s < splits) sum += v[i][s];
+          if (m < live && col < a.N) a.c[(f.m0 + m) * a.ldc + col] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
+        }
       }
     }
     __syncwarp();
@@ -472,8 +496,14 @@ static bool rp_map(CUtensorMap* m, const void* base, int64_t inner, int64_t rows
 }
 
 // CTAs a tile's K-blocks are split over: 8, 4 or 2, the most for which `tiles`
-// clusters are resident at once with at least four K-blocks a CTA (below that
-// the hand-over of the partial sums costs more than the K-blocks it spreads).
+// clusters are resident at once, from 8 K-blocks on.  The hand-over of the sums
+// takes about 1 us, a K-block 0.2.  Measured with a split / with one CTA a tile,
+// in us, tokens in brackets:
+//   4 K-blocks, 16 experts of 512 columns [1]: over 4 CTAs 5.7 / 5.3;
+//   6, 256 columns [1]: over 4, 5.8 / 5.6;   8, 8 experts of 128 [1]: over 8, 5.5 / 6.2;
+//   8, 512 columns [1]: over 4, 5.9 / 6.2;   8, 8 experts of 1024 [1 / 4]: over 2, 6.4 / 6.2, 6.9 / 6.5;
+//   16, 8 experts of 1000 [8]: over 2, 8.2 / 9.3;   16, 256 experts of 512 [1]: over 4, 6.8 / 8.3;
+//   32, 16 experts of 256 [1 / 4]: over 8, 6.2 / 11.7, over 4, 7.4 / 11.7.
 template <int R>
 static int rp_splits(int64_t tiles, int Kb, int num_sms) {
   static std::once_flag once;
@@ -482,7 +512,7 @@ static int rp_splits(int64_t tiles, int Kb, int num_sms) {
     for (int s = 2; s <= 8; s *= 2) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3((unsigned)(s * 16));
-      cfg.blockDim = dim3(kRpThreads);
+      cfg.blockDim = dim3(RpCfg<R>::kThreads);
       cfg.dynamicSmemBytes = RpCfg<R>::kSmemBytes;
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -497,7 +527,7 @@ static int rp_splits(int64_t tiles, int Kb, int num_sms) {
     (void)cudaGetLastError();  // a size the device refuses leaves no error behind
   });
   for (int s = 8; s >= 2; s /= 2)
-    if (s <= Kb / 4 && tiles * s <= num_sms && tiles <= max_clusters[s]) return s;
+    if (Kb >= 8 && tiles * s <= num_sms && tiles <= max_clusters[s]) return s;
   return 1;
 }
 
@@ -519,7 +549,7 @@ static cudaError_t run_routed(const CUtensorMap& mw, const CUtensorMap& mx, cons
   const int64_t groups = splits > 1 ? tiles : walks < num_sms ? walks : num_sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * splits));
-  cfg.blockDim = dim3(kRpThreads);
+  cfg.blockDim = dim3(RpCfg<R>::kThreads);
   cfg.dynamicSmemBytes = RpCfg<R>::kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -542,17 +572,21 @@ cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_
     *msg = "cuTensorMapEncodeTiled failed for an operand (alignment, stride or size out of range)";
     return cudaErrorInvalidValue;
   }
-  // R: enough for the rows of an expert were they spread evenly, with room for
-  // twice that, as long as the walks still cover the SMs
+  // R, by the rows of an expert were they spread evenly: room for twice that, as
+  // a walk less is a pass less over the tile.  Measured with R = 16 / 32 / 64, in us, at
+  //   64 experts of 2048 x 4096:  1 row 58.8 / 58.5 / 60.5 (8 rows in all 12.4 / 13.0 / 14.5),
+  //     8 rows 88.8 / 87.9 / 88.6, 16 rows 99.9 / 88.9 / 90.6, 32 rows 168 / 107 / 91.4, 64 rows 301 / 183 / 120;
+  //   256 experts of 512 x 2048:  1 row (one token) 7.7 / 8.9 / 11.3, 16 rows 54.2 / 48.1 / 49.9.
+  // Where walks of 64 are fewer than half the SMs, more of 32 share the work better:
+  //   8 experts of 1000 x 2000:   38 rows (64 walks) 15.0 / 10.8 / 11.4, 100 rows (128 walks) 20.3 / 16.7 / 12.0.
   const int64_t reach = a.E < a.R ? a.E : a.R, rows = cdiv(a.R, a.E), tiles = reach * cdiv(a.N, kRpTile);
   if ((reach + a.R / 16) * cdiv(a.N, kRpTile) >= (int64_t)1 << 31) {
     *msg = "too many rows and columns: (experts + R/16) * ceil(N/128) must stay below 2^31";
     return cudaErrorInvalidValue;
   }
-  auto walks = [&](int r) { return tiles * cdiv(rows, r); };
-  if (rows > 16 && walks(64) >= num_sms) return run_routed<64>(mw, mx, a, num_sms, st);
-  if (rows > 8 && (rows <= 16 || walks(32) >= num_sms / 2)) return run_routed<32>(mw, mx, a, num_sms, st);
-  return run_routed<16>(mw, mx, a, num_sms, st);
+  if (rows <= 8) return run_routed<16>(mw, mx, a, num_sms, st);
+  if (rows <= 16 || tiles * cdiv(rows, 64) < num_sms / 2) return run_routed<32>(mw, mx, a, num_sms, st);
+  return run_routed<64>(mw, mx, a, num_sms, st);
 }
 
 cudaError_t routed_read_errors(uint32_t* out) {
