@@ -797,7 +797,10 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const 
 // Host side
 // ---------------------------------------------------------------------------
 
-// f with the experts a lane takes as a compile-time number: E / 32 rounded up to one of these.
+// f with the experts a lane takes as a compile-time number, so that they stay in
+// registers: E / 32 rounded up to one of these.  The nearest against the next
+// one up, 32768 tokens, k 8: 64 experts 10.9 / 11.8 us, 128 12.8 / 15.5, 160
+// 14.4 / 15.4, 256 17.3 / 22.7 (in groups 34.1 / 65.2), 384 24.0 / 31.6.
 template <typename F>
 static cudaError_t by_vpl(int64_t E, F&& f) {
   const int64_t n = cdiv(E, 32);
@@ -827,12 +830,16 @@ static bool aligned_to(const void* p, int64_t ld_bytes, int64_t n) {
 cudaError_t launch_moe_route(const RouteArgs& args, cudaStream_t st) {
   RouteArgs a = args;
   const int el = a.f32 ? 4 : 2;
+  // four logits, four biases a load where they are aligned: 32768 x 256 17.3 us against
+  // 18.0 with an odd row stride, with a bias 24.9 against 26.1
   a.vec = aligned_to(a.logits, a.ldl * el, 4 * el);
   a.bias_vec = aligned_to(a.bias, 0, 16);
   return by_vpl(a.E, [&](auto vpl) {
     constexpr int kVpl = decltype(vpl)::value;
     if (a.groups > 1) {
-      // a power of two of lanes a group, whole lanes where the groups' size allows it
+      // a power of two of lanes a group, whole lanes where the groups' size allows it (no
+      // exchange of the values then: 32768 x 192, sigmoid, 4 groups 27.5 us; 6 groups, which
+      // do not fit lanes, 40.8)
       const int64_t S = a.E / a.groups, lanes = S / kVpl;
       a.group_whole = S % kVpl == 0 && (lanes & (lanes - 1)) == 0;
       a.group_lanes = 1;
@@ -856,6 +863,7 @@ cudaError_t launch_moe_route(const RouteArgs& args, cudaStream_t st) {
 cudaError_t launch_moe_route_bwd(const RouteBwdArgs& args, cudaStream_t st) {
   RouteBwdArgs a = args;
   const int el = a.f32 ? 4 : 2;
+  // pairs of experts a load and a store: 32768 x 256 15.5 us against 17.1 with an odd row stride
   a.vec = aligned_to(a.logits, a.ldl * el, 2 * el) && aligned_to(a.dlogits, a.ldd * el, 2 * el);
   const unsigned grid = (unsigned)cdiv(a.T, kRouteThreads / 32);
   auto go = [&](auto pairs) {
@@ -867,6 +875,8 @@ cudaError_t launch_moe_route_bwd(const RouteBwdArgs& args, cudaStream_t st) {
       });
     });
   };
+  // pairs a lane, a compile-time number as in the forward; the nearest against the next one up,
+  // 32768 tokens: 64 experts 10.6 / 11.6 us, 160 13.4 / 22.9 (8 pairs for 3), 256 15.5 / 22.7
   const int64_t n = cdiv(a.E, 64);
   if (n <= 1) return go(std::integral_constant<int, 1>{});
   if (n <= 2) return go(std::integral_constant<int, 2>{});
@@ -904,6 +914,9 @@ static cudaError_t run_plan(const PlanArgs& a, cudaStream_t st) {
     (void)cudaGetLastError();  // a size the device refuses leaves no error behind
   });
   if (attr_err != cudaSuccess) return attr_err;
+  // A CTA for every 1024 slots: fewer leave a warp more steps, more pay the cluster's barriers
+  // (about 1 us).  With 512 / 1024 / 2048 / 8192 slots a CTA, 64 experts, in us: 1024 slots
+  // 6.2 / 5.3 / 5.3 / 5.2, 4096 6.6 / 6.3 / 7.1 / 7.0, 16384 6.9 / 6.9 / 7.3 / 12.3.
   int ctas = 1;
   while (ctas < most && (int64_t)ctas * kPlanThreads < a.n) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -923,6 +936,8 @@ static cudaError_t run_plan(const PlanArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, moe_plan_kernel<BITS>, a);
 }
 
+// A ballot a bit of the experts' numbers: the fewest bits against 11, 131072 slots: 64 experts
+// 13.3 / 14.7 us, 200 14.8 / 15.6; 8192 slots, 8 experts 5.9 / 6.9.
 cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
   if (a.E < 1 << 5) return run_plan<5>(a, st);
   if (a.E < 1 << 7) return run_plan<7>(a, st);

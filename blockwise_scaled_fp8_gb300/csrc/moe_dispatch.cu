@@ -523,6 +523,8 @@ cudaError_t launch_moe_dispatch(const DispatchArgs& a, int num_sms, cudaStream_t
   memset(&mx, 0, sizeof(mx));
   memset(&mr, 0, sizeof(mr));
   memset(&mc, 0, sizeof(mc));
+  // TMA gathers need 16-byte aligned rows; others are gathered by the elements (8192 tokens to
+  // eight experts each: 2000 columns 90 us, 1999 190)
   const bool tma = a.T > 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ldx % 8 == 0;
   if (ds_encode_fn() == nullptr || (tma && !ds_gather_map(&mx, a.x, a.C, a.T, a.ldx)) ||
       (p.C_al > 0 && !ds_store_map(&mr, a.q_row, p.C_al, a.R, a.ldq_row, true)) ||

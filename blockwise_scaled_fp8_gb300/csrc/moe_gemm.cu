@@ -18,6 +18,10 @@
 // (and its rows are few enough for one walk), each tile's K-blocks are split over
 // a cluster instead and the partial sums added in rank order through distributed
 // shared memory.
+// 64 experts of 2048 x 4096, eight a token: 64 tokens (every expert reached, 537 MB
+// of weights) 87.4 us, 6.1 TB/s, 0.91 of the copy rate; 512 tokens 120; one token
+// with the weights in memory 15.2 us, in L2 12.1.  (The codes straight into the
+// registers of an 8-bit mma.sync: 116 us for 32 tokens, against 86.)
 //
 //   warps 0, 8..  producers: warp 0 W's tile, each of them 16 tokens
 //   warps 1, 3    MMA issuers (M = 128, N = R) on alternate K-blocks
