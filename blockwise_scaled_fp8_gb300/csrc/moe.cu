@@ -133,10 +133,11 @@ __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-
 //     32-bit word with the expert's complement, and the redux names the winner;
 //   - with more experts a lane (VPL > 8) sorting costs more than k scans;
 //   - scores of the chosen are formed again from their logits, by k lanes.
-// 16384 tokens x 256 fp32, 8 groups, sigmoid with bias, k = 8: 18.6 us, 994
-// warp-instructions a token, half of them the 256 scores (the first form, k
-// scans of every lane's keys, took 1737 and 32.8 us); 50021 x 160 bf16, softmax,
-// k = 6: 19 us, 411; one token 2.0 us.
+// 16384 tokens x 256 fp32, 8 groups, sigmoid with bias, k = 8: 18.6 us, 1002
+// warp-instructions a token (the first form, k scans of every lane's keys, took
+// 1737 and 32.8 us; scores by __expf and an approximate quotient 16.9, but then
+// near-equal experts are not chosen as the plain fp32 form chooses); 50021 x 160
+// bf16, softmax, k = 6: 17 us, 411; one token 2.0 us.
 template <int VPL, bool F32, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArgs a) {
   // per warp: E + 32 values of groups that are not whole powers of two of lanes, later the sorted lists
@@ -162,10 +163,18 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
     for (int i = 1; i < VPL; ++i) m = fmaxf(m, c[i]);
     top = key_value(__reduce_max_sync(kFull, order_key(m)));
     sum = 0.0f;
+    if (!kByLogit || a.groups > 1) {  // the terms are compared
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      gv[i] = c[i] > -INFINITY ? expf(c[i] - top) : 0.0f;
-      sum += gv[i];
+      for (int i = 0; i < VPL; ++i) {
+        gv[i] = c[i] > -INFINITY ? expf(c[i] - top) : 0.0f;
+        sum += gv[i];
+      }
+    } else {
+      // only their sum is used: __expf, off by 2 ulp and |x| 2^-24 of a term exp(x),
+      // keeps it to 2^-21 (x exp(x) is at most 1 / e for x < 0); masked: exp(-inf) = 0
+      top = fmaxf(top, -FLT_MAX);  // finite where all are masked
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sum += __expf(c[i] - top);
     }
     sum = fmaxf(warp_sum(sum), FLT_MIN);
   }
@@ -311,6 +320,14 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
   }
 }
 
+// exp(x), x <= 0, of the gradient's dense row: in bf16 by __expf, whose error (2
+// ulp and |x| 2^-24, at most 2^-17 where the result is a normal number) is far
+// below the output's rounding of 2^-9.
+template <bool F32>
+__device__ __forceinline__ float dense_exp(float x) {
+  return F32 ? expf(x) : __expf(x);
+}
+
 // The router's gradient.  With p the scores, S = max(sum of the chosen p,
 // floor) and the chosen j:
 //   ds_j = (scale dw_j - sum_i dw_i w_i) / S   (renormalised),  scale dw_j  (not)
@@ -365,7 +382,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
     float ref = __shfl_sync(kFull, l_j, 0), mult = __shfl_sync(kFull, w, 0) / a.scale;
     if (!a.renormalize && mult > 1e-20f && mult < 2.0f) {
 #pragma unroll
-      for (int i = 0; i < 2 * PAIRS; ++i) s[i] = expf(s[i] - ref) * mult;
+      for (int i = 0; i < 2 * PAIRS; ++i) s[i] = dense_exp<F32>(s[i] - ref) * mult;
     } else {
       ref = s[0];
 #pragma unroll
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 2 * PAIRS; ++i) {
-        s[i] = expf(s[i] - ref);
+        s[i] = dense_exp<F32>(s[i] - ref);
         sum += s[i];
       }
       mult = 1.0f / fmaxf(warp_sum(sum), FLT_MIN);
