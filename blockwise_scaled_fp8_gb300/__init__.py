@@ -566,6 +566,16 @@ def _need_plan(plan, T):
     return row.shape[1], src.shape[0]
 
 
+def _need_plan_offs(plan):
+    """The plan's offsets and its experts."""
+    offs = plan.offs
+    if offs.dtype is not _torch().int32 or offs.dim() != 1 or offs.shape[0] < 2 or not offs.is_cuda or \
+            not offs.is_contiguous():
+        raise ValueError(f"the plan's offs must be a contiguous CUDA int32 tensor of E+1 offsets, got {offs.dtype} "
+                         f"{tuple(offs.shape)} on {offs.device}")
+    return offs, offs.shape[0] - 1
+
+
 def moe_dispatch(x, plan: MoePlan, weight=None, cols: bool = True):
     """Gathers x [T, K] bf16 into the plan's rows, scaled by weight [T, k] fp32
     where given, and quantises them in one pass: (q_row [R, ldq], s_row [Kb,
@@ -640,10 +650,10 @@ def moe_combine_bwd(dy, ye, plan: MoePlan, w, with_dye: bool = True):
         _need(w, "w", torch.float32, (T, k))
     dye = torch.empty((R, N), dtype=torch.bfloat16, device=dy.device) if with_dye else None
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
-    offs = _offs(plan.offs)
-    st = lib().bfp8_moe_combine_bwd(dy.data_ptr(), _ld(dy), ye.data_ptr(), _ld(ye), R, offs.data_ptr(),
-                                    offs.shape[0] - 1, plan.row.data_ptr(), plan.src.data_ptr(), _p(w), T, k, N, _p(dye),
-                                    N, dw.data_ptr(), _stream())
+    offs, E = _need_plan_offs(plan)
+    st = lib().bfp8_moe_combine_bwd(dy.data_ptr(), _ld(dy), ye.data_ptr(), _ld(ye), R, offs.data_ptr(), E,
+                                    plan.row.data_ptr(), plan.src.data_ptr(), _p(w), T, k, N, _p(dye), N, dw.data_ptr(),
+                                    _stream())
     if st:
         _check(st)
     return dye, dw
@@ -656,10 +666,14 @@ def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gat
     the stacked weights.  Returns C [R, N] bf16 (rows past offs[E] are left as
     they were in ``out``)."""
     torch = _torch()
-    offs = _offs(plan.offs)
+    offs, E = _need_plan_offs(plan)
     tokens = plan.row.shape[0]
     k, R = _need_plan(plan, tokens)
-    T, E = qa.shape[0], offs.shape[0] - 1
+    T = qa.shape[0]
+    u8, f8, f32 = torch.uint8, torch.float8_e4m3fn, torch.float32
+    if not (qa.dtype in (u8, f8) and qb.dtype in (u8, f8) and sa.dtype is f32 and sb.dtype is f32 and qa.is_cuda and
+            qb.is_cuda and sa.is_cuda and sb.is_cuda):
+        raise ValueError("qa, qb must be CUDA uint8 or float8_e4m3fn codes and sa, sb CUDA float32 scales")
     if T != (tokens if gathered else R):
         raise ValueError(f"qa has {T} rows, the plan {tokens if gathered else R}")
     if qb.shape[0] != E * N or sb.shape[0] < E * _cdiv(N, BLOCK) or sa.shape[0] < _cdiv(K, BLOCK):
@@ -671,6 +685,9 @@ def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gat
     if out is None:
         out = torch.empty((R, N), dtype=torch.bfloat16, device=qa.device)
     else:
+        _need_bf16_2d(out, "out")
+        if out.shape[0] < R or out.shape[1] < N:
+            raise ValueError(f"out must hold {(R, N)}, got {tuple(out.shape)}")
         ldc = _ld(out)
     st = lib().bfp8_gemm_routed_1x128_128x128(qa.data_ptr(), _ld(qa), sa.data_ptr(), _ld(sa), T, qb.data_ptr(),
                                               _ld(qb), sb.data_ptr(), _ld(sb), offs.data_ptr(), E,
@@ -692,6 +709,8 @@ def moe_experts_fwd(x, w, plan: MoePlan, weight):
         raise ValueError("moe_experts_fwd: the experts' output features must be a multiple of 128")
     if plan.offs.numel() != E + 1:
         raise ValueError(f"moe_experts_fwd: the plan has {plan.offs.numel() - 1} experts, w {E}")
+    if plan.src.numel() % BLOCK:
+        raise ValueError(f"moe_experts_fwd: the plan's rows must start on multiples of {BLOCK} (moe_plan's align)")
     qx, sx, qxt, sxt = moe_dispatch(x, plan)
     qw, qwt, sw = quant_weight(w.reshape(E * N, K), with_t=True)
     ye = gemm_grouped_1x128_128x128(qx, sx, qw, sw, plan.offs, N, K)

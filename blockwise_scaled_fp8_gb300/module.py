@@ -118,7 +118,7 @@ def blockwise_fp8_experts(x: torch.Tensor, weight: torch.Tensor, logits: torch.T
         raise ValueError(f"blockwise_fp8_experts: x is {tuple(x.shape)}, weight {tuple(weight.shape)}, logits "
                          f"{tuple(logits.shape)}")
     route = {"score": "softmax", "renormalize": True, "scale": 1.0, **route}
-    return _BlockwiseFp8Experts.apply(x.contiguous(), weight.contiguous(), logits, k, bias, route)
+    return _BlockwiseFp8Experts.apply(x.contiguous(), weight.contiguous(), logits.contiguous(), k, bias, route)
 
 
 class Float8RoutedExperts(torch.nn.Module):
@@ -161,8 +161,9 @@ class Float8RoutedExperts(torch.nn.Module):
         if self._codes is None:
             raise RuntimeError("Float8RoutedExperts.decode: call quantize() first")
         lead = x.shape[:-1]
-        idx, w = moe_route(logits.reshape(-1, self.experts), self.k, bias=self.choice_bias, **self.route)
-        y = moe_experts_decode(x.reshape(-1, self.in_features), *self._codes, moe_plan(idx, self.experts, align=1), w,
+        logits, x = logits.reshape(-1, self.experts).contiguous(), x.reshape(-1, self.in_features).contiguous()
+        idx, w = moe_route(logits, self.k, bias=self.choice_bias, **self.route)
+        y = moe_experts_decode(x, *self._codes, moe_plan(idx, self.experts, align=1), w,
                                self.out_features)
         return y.reshape(*lead, self.out_features)
 

@@ -406,6 +406,37 @@ def test_routed_product(T, k, E, align, N, K, gathered):
     assert np.all(body[end:] == sent)
 
 
+# Batches whose tiles are few, split over 8, 4 and 2 CTAs with 16, 32 and 64 tokens a walk, and
+# experts of several walks of 32 and 64 (the same check as above)
+@pytest.mark.parametrize("gathered", [True, False])
+@pytest.mark.parametrize("T,k,E,align,N,K", [
+    (3, 1, 2, 1, 100, 1024), (4, 2, 8, 1, 500, 1100), (8, 2, 8, 1, 1000, 2000), (14, 1, 1, 1, 257, 1024),
+    (30, 1, 2, 1, 300, 1100), (60, 1, 1, 1, 9728, 1024), (33, 1, 2, 1, 136, 2048), (300, 2, 4, 1, 2500, 272),
+    (150, 3, 6, 16, 640, 400)])
+def test_routed_product_splits_and_walks(T, k, E, align, N, K, gathered):
+    test_routed_product(T, k, E, align, N, K, gathered)
+
+
+def test_routed_product_refuses_wrong_types_and_outputs():
+    plan = _routed(1, 4, 2, 3, 1, empty=0.0)
+    e8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
+    f = lambda *s: torch.zeros(s, device="cuda")
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    ok = dict(qa=e8(4, 256), sa=f(2, 4), qb=e8(3 * 8, 256), sb=f(3, 2), plan=plan, N=8, K=256)
+    f8 = torch.float8_e4m3fn
+    B.gemm_routed_1x128_128x128(**{**ok, "qa": ok["qa"].view(f8), "qb": ok["qb"].view(f8)}, out=bf(9, 24))
+    for name, bad in (("codes", dict(qa=bf(4, 256))), ("codes", dict(qb=bf(24, 256))), ("scales", dict(sa=bf(2, 4))),
+                      ("scales", dict(sb=f(3, 2).double())), ("CUDA", dict(sa=torch.zeros(2, 4))),
+                      ("out", dict(out=f(8, 8))), ("out", dict(out=bf(7, 8))), ("out", dict(out=bf(8, 7))),
+                      ("out", dict(out=bf(8, 8).t())), ("offs", dict(plan=plan._replace(offs=plan.offs.cpu()))),
+                      ("offs", dict(plan=plan._replace(offs=plan.offs.long())))):
+        with pytest.raises(ValueError, match=name):
+            B.gemm_routed_1x128_128x128(**{**ok, **bad})
+    ye, dy = bf(8, 16), bf(4, 16)
+    with pytest.raises(ValueError, match="offs"):
+        B.moe_combine_bwd(dy, ye, plan._replace(offs=plan.offs.cpu()), None)
+
+
 def test_routed_product_of_no_reduction_is_zero():
     plan = _routed(1, 4, 2, 3, 1, empty=0.0)
     e8 = lambda *s: torch.empty(s, dtype=torch.uint8, device="cuda")

@@ -108,6 +108,36 @@ def test_layer_refuses_wrong_types_and_shapes():
         B.Float8RoutedExperts(128, 100, 8, 2)
 
 
+def test_training_forward_refuses_a_plan_of_unaligned_rows():
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(8, 128, 128, dtype=torch.bfloat16, device="cuda")
+    idx, weight = B.moe_route(torch.zeros(4, 8, device="cuda"), 2)
+    with pytest.raises(ValueError, match="multiples of 128"):
+        B.moe_experts_fwd(x, w, B.moe_plan(idx, 8, align=1), weight)
+
+
+def test_layer_takes_broadcast_and_strided_inputs():
+    """One row of logits for every token, and a token broadcast: the same as their copies, gradients summed."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = torch.randn(4, 128, 256, generator=g, device="cuda").bfloat16()
+    row, x = torch.randn(1, 4, generator=g, device="cuda"), torch.randn(6, 256, generator=g, device="cuda").bfloat16()
+    def grads(l, x1):
+        l, x1 = l.clone().requires_grad_(), x1.clone().requires_grad_()
+        y, _ = B.blockwise_fp8_experts(x1.expand(6, 256), w, l.expand(6, 4), 2)
+        y.float().sum().backward()
+        return y, l.grad, x1.grad
+    y0, l0, x0 = grads(row.expand(6, 4).contiguous(), x)
+    y1, l1, _ = grads(row, x)
+    assert torch.equal(y0, y1) and float((l1 - l0.sum(0, keepdim=True)).abs().max()) <= 8 * 2.0 ** -24 * float(l0.abs().sum())
+    y2, _, x2 = grads(row, x[:1])
+    assert torch.equal(y2, y1[:1].expand(6, 128)) and x2.shape == (1, 256)
+    layer = B.Float8RoutedExperts(256, 128, 4, 2, device="cuda")
+    with torch.no_grad():
+        layer.weight.copy_(w)
+    layer.quantize()
+    assert torch.equal(layer.decode(x[:1].expand(6, 256), row.expand(6, 4)), layer.decode(x[:1].repeat(6, 1), row.repeat(6, 1)))
+
+
 def test_layer_in_a_cuda_graph_and_on_a_side_stream():
     g = torch.Generator(device="cuda").manual_seed(2)
     layer = B.Float8RoutedExperts(256, 128, 8, 2, device="cuda")
