@@ -449,8 +449,10 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
 // its warp's run waits in row.  Then prefix sums of the counts: over the warps
 // of a CTA, over the CTAs of the cluster through distributed shared memory,
 // over the experts' aligned counts; and the slots' rows follow.  131072 slots,
-// 256 experts: 15.0 us, a chain of latencies (24.0 with a cluster of 8 CTAs,
-// 36.0 with matches); 384 slots, one CTA: 3.9 us.
+// 256 experts: 14.8 us, a chain of latencies and, on 16 SMs, the 32 scattered
+// stores of each warp's src (24.0 with a cluster of 8 CTAs, 36.0 with matches);
+// 384 slots, one CTA: 3.6 us.
+constexpr int kPlanCtas = 16;  // of the cluster, at most
 template <int BITS>  // of the experts' numbers, E (nowhere) among them
 __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
   extern __shared__ uint32_t s_cnt[];  // [32 warps][E] counts, then first rows; [E] CTA totals
@@ -468,7 +470,23 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
   // padding everywhere; the barriers below come before the slots' own entries
   for (int64_t r = (int64_t)rank * kPlanThreads + tid; r < a.R; r += (int64_t)ctas * kPlanThreads) a.src[r] = -1;
   __syncwarp();
-  constexpr int kAhead = 4;        // groups of 32 slots whose experts are read at once
+  // ranks of the 32 slots from i0 on, of expert e (E: none) in this lane
+  auto rank_slots = [&](int64_t i0, int e) {
+    uint32_t peers = kFull;
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
+      const bool set = (e >> b) & 1;
+      const uint32_t vote = __ballot_sync(kFull, set);
+      peers &= set ? vote : ~vote;
+    }
+    const bool ok = e < E;
+    const uint32_t base = ok ? mine[e] : 0u, lower = (uint32_t)__popc(peers & ((1u << lane) - 1u));
+    __syncwarp();
+    if (ok && lower == 0) mine[e] = base + (uint32_t)__popc(peers);
+    __syncwarp();
+    if (i0 + lane < hi) a.row[i0 + lane] = (int32_t)(base + lower);
+  };
+  constexpr int kAhead = 4;  // groups of 32 slots whose experts are read at once
   for (int64_t i0 = lo; i0 < hi; i0 += 32 * kAhead) {
     int e[kAhead];
 #pragma unroll
@@ -477,22 +495,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
       e[u] = slot < hi ? __ldg(a.idx + slot) : -1;
       if ((uint32_t)e[u] >= (uint32_t)E) e[u] = E;
     }
+    if (i0 + 32 * kAhead <= hi) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int64_t slot = i0 + 32 * u + lane;
-      uint32_t peers = kFull;
+      for (int u = 0; u < kAhead; ++u) rank_slots(i0 + 32 * u, e[u]);
+    } else {  // not all of them: a group takes 0.25 us (4096 slots 6.3 us with empty ones, 5.6 without)
 #pragma unroll
-      for (int b = 0; b < BITS; ++b) {
-        const bool set = (e[u] >> b) & 1;
-        const uint32_t vote = __ballot_sync(kFull, set);
-        peers &= set ? vote : ~vote;
-      }
-      const bool ok = e[u] < E;
-      const uint32_t base = ok ? mine[e[u]] : 0u, lower = (uint32_t)__popc(peers & ((1u << lane) - 1u));
-      __syncwarp();
-      if (ok && lower == 0) mine[e[u]] = base + (uint32_t)__popc(peers);
-      __syncwarp();
-      if (slot < hi) a.row[slot] = (int32_t)(base + lower);
+      for (int u = 0; u < kAhead; ++u)
+        if (i0 + 32 * u < hi) rank_slots(i0 + 32 * u, e[u]);
     }
   }
   __syncthreads();
@@ -509,16 +518,23 @@ __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArg
   uint32_t before = 0, total = 0;  // of expert tid: slots in the CTAs before this one, in all
   if (ctas > 1) {
     cluster_sync_all();
-    if (tid < E)
-      for (int c = 0; c < ctas; ++c) {
-        uint32_t v;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                     : "=r"(v)
-                     : "r"(mapa_shared(smem_u32(s_tot + tid), (uint32_t)c))
-                     : "memory");
-        if (c < rank) before += v;
-        total += v;
+    if (tid < E) {
+      uint32_t v[kPlanCtas];  // all in flight at once
+#pragma unroll
+      for (int c = 0; c < kPlanCtas; ++c) {
+        v[c] = 0;
+        if (c < ctas)
+          asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                       : "=r"(v[c])
+                       : "r"(mapa_shared(smem_u32(s_tot + tid), (uint32_t)c))
+                       : "memory");
       }
+#pragma unroll
+      for (int c = 0; c < kPlanCtas; ++c) {
+        if (c < rank) before += v[c];
+        total += v[c];
+      }
+    }
     cluster_sync_all();  // every CTA has read the totals: they may be replaced, and a CTA may leave
   } else if (tid < E) {
     total = s_tot[tid];
@@ -908,18 +924,18 @@ static cudaError_t run_plan(const PlanArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(33 * a.E) * 4;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
-  static int most = 8;  // CTAs of the cluster: 16 where the device can hold one, else the portable 8
+  static int most = 8;  // CTAs of the cluster: kPlanCtas where the device can hold one, else the portable 8
   std::call_once(once, [] {
     const int max_smem = 33 * kMaxGroups * 4;
     attr_err = cudaFuncSetAttribute(moe_plan_kernel<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
     if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(16);
+    cfg.gridDim = dim3(kPlanCtas);
     cfg.blockDim = dim3(kPlanThreads);
     cfg.dynamicSmemBytes = max_smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.x = kPlanCtas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -927,13 +943,13 @@ static cudaError_t run_plan(const PlanArgs& a, cudaStream_t st) {
     int n = 0;
     if (cudaFuncSetAttribute(moe_plan_kernel<BITS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
         cudaOccupancyMaxActiveClusters(&n, moe_plan_kernel<BITS>, &cfg) == cudaSuccess && n >= 1)
-      most = 16;
+      most = kPlanCtas;
     (void)cudaGetLastError();  // a size the device refuses leaves no error behind
   });
   if (attr_err != cudaSuccess) return attr_err;
   // A CTA for every 1024 slots: fewer leave a warp more steps, more pay the cluster's barriers
   // (about 1 us).  With 512 / 1024 / 2048 / 8192 slots a CTA, 64 experts, in us: 1024 slots
-  // 6.2 / 5.3 / 5.3 / 5.2, 4096 6.6 / 6.3 / 7.1 / 7.0, 16384 6.9 / 6.9 / 7.3 / 12.3.
+  // 5.4 / 4.5 / 4.6 / 4.6, 4096 5.5 / 5.6 / 6.7 / 7.4, 16384 5.7 / 5.7 / 6.8 / 12.7.
   int ctas = 1;
   while (ctas < most && (int64_t)ctas * kPlanThreads < a.n) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
