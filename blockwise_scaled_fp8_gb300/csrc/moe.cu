@@ -137,7 +137,7 @@ __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-
 // warp-instructions a token (the first form, k scans of every lane's keys, took
 // 1737 and 32.8 us; scores by __expf and an approximate quotient 16.9, but then
 // near-equal experts are not chosen as the plain fp32 form chooses); 50021 x 160
-// bf16, softmax, k = 6: 17 us, 411; one token 2.0 us.
+// bf16, softmax, k = 6: 17 us, 347; one token 2.0 us.
 template <int VPL, bool F32, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArgs a) {
   // per warp: E + 32 values of groups that are not whole powers of two of lanes, later the sorted lists
@@ -336,7 +336,7 @@ __device__ __forceinline__ float dense_exp(float x) {
 // One warp a token; lane j < k handles choice j.  Of the dense row lane l
 // takes the pairs 2l, 2l + 64, .. (one load and one store a pair where the row
 // is aligned for it), over which the chosen values go last.  Bound by
-// instructions as the router is: 50021 tokens x 160 bf16, softmax, 16 us, 295
+// instructions as the router is: 50021 tokens x 160 bf16, softmax, 15 us, 275
 // warp-instructions a token.
 template <int PAIRS, bool F32, bool SIGMOID>
 __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const RouteBwdArgs a) {
@@ -449,9 +449,9 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const Rout
 // its warp's run waits in row.  Then prefix sums of the counts: over the warps
 // of a CTA, over the CTAs of the cluster through distributed shared memory,
 // over the experts' aligned counts; and the slots' rows follow.  131072 slots,
-// 256 experts: 14.8 us, a chain of latencies and, on 16 SMs, the 32 scattered
-// stores of each warp's src (24.0 with a cluster of 8 CTAs, 36.0 with matches);
-// 384 slots, one CTA: 3.6 us.
+// 256 experts: 14.9 us, a chain of latencies, of which the scattered stores of
+// src from 16 SMs are 3.6 and the padding's 0.8 (24.0 us with a cluster of 8
+// CTAs, 36.0 with matches); 384 slots, one CTA: 3.6 us.
 constexpr int kPlanCtas = 16;  // of the cluster, at most
 template <int BITS>  // of the experts' numbers, E (nowhere) among them
 __global__ void __launch_bounds__(kPlanThreads, 1) moe_plan_kernel(const PlanArgs a) {
