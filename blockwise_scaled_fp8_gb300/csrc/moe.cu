@@ -338,12 +338,20 @@ __device__ __forceinline__ float dense_exp(float x) {
 // is aligned for it), over which the chosen values go last.  Bound by
 // instructions as the router is: 50021 tokens x 160 bf16, softmax, 15 us, 275
 // warp-instructions a token.
+//
+// Tokens with little work are bound by the start of CTAs, about one a
+// nanosecond: twice the warps a CTA for them (32768 x 256 sigmoid 9.6 -> 8.6
+// us, x 64 softmax 10.7 -> 9.7; more pairs of a softmax 14.8 -> 15.1 at 256,
+// 23.7 -> 25.5 at 384 experts).
+template <int PAIRS, bool SIGMOID>
+constexpr int kRouteBwdThreads = SIGMOID || PAIRS == 1 ? 2 * kRouteThreads : kRouteThreads;
+
 template <int PAIRS, bool F32, bool SIGMOID>
-__global__ void __launch_bounds__(kRouteThreads) moe_route_bwd_kernel(const RouteBwdArgs a) {
+__global__ void __launch_bounds__(kRouteBwdThreads<PAIRS, SIGMOID>) moe_route_bwd_kernel(const RouteBwdArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = (int)(threadIdx.x & 31);
-  const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = (int64_t)blockIdx.x * (kRouteBwdThreads<PAIRS, SIGMOID> / 32) + (threadIdx.x >> 5);
   if (t >= a.T) return;
   const int E = (int)a.E;
   const float low = lowest_of(F32);
@@ -898,13 +906,13 @@ cudaError_t launch_moe_route_bwd(const RouteBwdArgs& args, cudaStream_t st) {
   const int el = a.f32 ? 4 : 2;
   // pairs of experts a load and a store: 32768 x 256 15.5 us against 17.1 with an odd row stride
   a.vec = aligned_to(a.logits, a.ldl * el, 2 * el) && aligned_to(a.dlogits, a.ldd * el, 2 * el);
-  const unsigned grid = (unsigned)cdiv(a.T, kRouteThreads / 32);
   auto go = [&](auto pairs) {
     constexpr int kPairs = decltype(pairs)::value;
     return by_bool(a.f32, [&](auto f32) {
       return by_bool(a.sigmoid, [&](auto sig) {
-        return launch_pdl(moe_route_bwd_kernel<kPairs, decltype(f32)::value, decltype(sig)::value>, grid, kRouteThreads,
-                          0, st, a);
+        constexpr int threads = kRouteBwdThreads<kPairs, decltype(sig)::value>;
+        return launch_pdl(moe_route_bwd_kernel<kPairs, decltype(f32)::value, decltype(sig)::value>,
+                          (unsigned)cdiv(a.T, threads / 32), threads, 0, st, a);
       });
     });
   };

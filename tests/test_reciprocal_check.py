@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 
 
 @pytest.fixture(scope="module")
-def checker(tmp_path_factory):
+def program(tmp_path_factory):
     exe = str(tmp_path_factory.mktemp("rc") / "reciprocal_check")
     cmd = ["gcc", "-O2", "-std=c11", "-ffp-contract=off", "-fno-fast-math", "-fopenmp",
            os.path.join(HERE, "reciprocal_check.c"), os.path.join(ROOT, "oracle", "bfp8_oracle.c"), "-lm", "-o", exe]
@@ -26,12 +26,12 @@ def _run(exe, stride):
     return int(fields["tot"]), int(fields["bad"])
 
 
-def test_quotient_strided(checker):
-    tot, bad = _run(checker, 97)
+def test_quotient_strided(program):
+    tot, bad = _run(program, 97)
     assert tot > 5_000_000 and bad == 0
 
 
 @pytest.mark.slow
-def test_quotient_exhaustive(checker):
-    tot, bad = _run(checker, 1)
+def test_quotient_exhaustive(program):
+    tot, bad = _run(program, 1)
     assert tot == 1_065_402_240 and bad == 0
