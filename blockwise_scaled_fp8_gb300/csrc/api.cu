@@ -641,7 +641,7 @@ bfp8_status bfp8_moe_combine(const void* ye, int64_t ldye, int64_t R, const int3
   int sms = 0;
   if ((st = check_device(&sms)) != BFP8_OK) return st;
   const cudaError_t e = launch_moe_combine(
-      CombineArgs{(const uint16_t*)ye, ldye, R, row, w, T, (int)k, N, (uint16_t*)y, ldy, 0}, (cudaStream_t)stream);
+      CombineArgs{(const uint16_t*)ye, ldye, R, row, w, T, (int)k, N, (uint16_t*)y, ldy, 0, 0, 0}, (cudaStream_t)stream);
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
 }
 

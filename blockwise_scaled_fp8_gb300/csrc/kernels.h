@@ -203,7 +203,7 @@ struct CombineArgs {
   int64_t N;
   uint16_t* y;
   int64_t ldy;
-  int col_blocks;  // set by the launcher
+  int col_blocks, cols, sides;  // set by the launcher: CTAs a row, threads a row of a CTA, rows side by side
 };
 cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t st);
 

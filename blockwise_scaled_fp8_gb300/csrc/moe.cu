@@ -664,37 +664,43 @@ constexpr int kCombinePiece = 16;  // rows of an expert that a CTA of the gradie
 
 }  // namespace
 
-// One thread VEC columns of one token; the token's rows are read eight at a
-// time before the first is used.  Bound by memory: 16384 tokens x 4096, eight
-// experts each, 1.21 GB in 182-192 us (0.93-0.98 of the copy rate).
-template <int VEC>
-__global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const CombineArgs a) {
+// One thread VEC columns of a token, or of the tokens whose rows make eight:
+// eight rows are read before the first is used (KB of each token; one token at
+// a time 8192 tokens x 4096, two experts each, took 60 us, so 33).  Narrow rows
+// share a CTA (32768 tokens x 256, eight experts: 39 us, so 25).  Bound by
+// memory: 16384 tokens x 4096, eight experts each, 1.21 GB in 179 us, the copy
+// rate.  Four CTAs an SM: with more or fewer loads in flight than theirs the
+// memory is slower (three 210 us, five 198).
+template <int VEC, int KB>
+__global__ void __launch_bounds__(kCombineThreads, 4) moe_combine_kernel(const CombineArgs a) {
+  constexpr int kTokens = kCombineBatch / KB;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t t = blockIdx.x / a.col_blocks;
-  const int64_t n = ((int64_t)(blockIdx.x % a.col_blocks) * kCombineThreads + threadIdx.x) * VEC;
-  if (n >= a.N) return;
-  float acc[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-  for (int j0 = 0; j0 < a.k; j0 += kCombineBatch) {
+  const int side = KB == kCombineBatch && a.sides == 1 ? 0 : (int)threadIdx.x / a.cols;
+  const int64_t t0 = ((int64_t)(blockIdx.x / a.col_blocks) * a.sides + side) * kTokens;
+  const int64_t n = ((int64_t)(blockIdx.x % a.col_blocks) * a.cols + ((int)threadIdx.x - side * a.cols)) * VEC;
+  if (n >= a.N || (int)threadIdx.x >= a.sides * a.cols) return;
+  float acc[VEC] = {};
+  for (int j0 = 0; j0 < a.k; j0 += KB) {  // (once where KB < 8, as k is at most KB)
     Bf16s<VEC> v[kCombineBatch];
     float w[kCombineBatch];
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j) {
-      const int64_t slot = t * a.k + j0 + j;
-      const int r = j0 + j < a.k ? __ldg(a.row + slot) : -1;
+    for (int i = 0; i < kCombineBatch; ++i) {
+      const int64_t t = t0 + i / KB, slot = t * a.k + j0 + i % KB;
+      const int r = (kTokens == 1 || t < a.T) && j0 + i % KB < a.k ? __ldg(a.row + slot) : -1;
       const bool ok = r >= 0 && r < a.R;
-      w[j] = ok ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
-      if (ok) v[j].load(a.ye + (int64_t)r * a.ldye + n);
-      else v[j].zero();
+      w[i] = ok ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
+      if (ok) v[i].load(a.ye + (int64_t)r * a.ldye + n);
+      else v[i].zero();
     }
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j)
+    for (int i = 0; i < kCombineBatch; ++i) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w[j], v[j].get(i), acc[i]);
+      for (int c = 0; c < VEC; ++c) acc[c] = fmaf(w[i], v[i].get(c), kTokens > 1 && i % KB == 0 ? 0.0f : acc[c]);
+      if (kTokens > 1 && i % KB == KB - 1 && t0 + i / KB < a.T) store_bf16s<VEC>(a.y + (t0 + i / KB) * a.ldy + n, acc);
+    }
   }
-  store_bf16s<VEC>(a.y + t * a.ldy + n, acc);
+  if (kTokens == 1) store_bf16s<VEC>(a.y + t0 * a.ldy + n, acc);
 }
 
 // The gradient comes in two forms that give the same bits: a dot product dw is
@@ -702,50 +708,73 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_kernel(const Comb
 // VEC .. of every 256 VEC (lane l), each class a chain a lane and a tree over
 // the lanes.
 //
-// dw alone: one CTA a token, whose warps are the classes; dy is read once and
-// the token's rows together (16384 tokens x 4096, 8 experts: 167 us, 1.2 GB).
-template <int VEC>
+// dw alone: one CTA a token (or the tokens whose rows make eight, KB each),
+// whose warps are the classes; dy is read once and the rows together (16384
+// tokens x 4096, 8 experts: 167 us, 1.2 GB).  WARP: narrow rows, a warp for all
+// classes of its tokens (rows of 1024 values 51 us against 71, 1536 73 against
+// 80, 2048 95 against 91; 16384 tokens, 8 experts).
+template <int VEC, int KB, bool WARP>
 __global__ void __launch_bounds__(kCombineThreads, 3) moe_combine_dw_kernel(const CombineBwdArgs a) {
-  __shared__ float s_part[kCombineThreads / 32][kCombineBatch];
+  constexpr int kClasses = kCombineThreads / 32, kTokens = kCombineBatch / KB;
+  __shared__ float s_part[kClasses][kCombineBatch];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t t = blockIdx.x;
-  for (int j0 = 0; j0 < a.k; j0 += kCombineBatch) {
+  const int64_t t0 = (WARP ? (int64_t)blockIdx.x * kClasses + warp : (int64_t)blockIdx.x) * kTokens;
+  for (int j0 = 0; j0 < a.k; j0 += KB) {
     int r[kCombineBatch];
-    float dot[kCombineBatch];
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j) {
-      r[j] = j0 + j < a.k ? __ldg(a.row + t * a.k + j0 + j) : -1;
-      if (r[j] >= a.R) r[j] = -1;
-      dot[j] = 0.0f;
+    for (int i = 0; i < kCombineBatch; ++i) {
+      const int64_t t = t0 + i / KB;
+      r[i] = t < a.T && j0 + i % KB < a.k ? __ldg(a.row + t * a.k + j0 + i % KB) : -1;
+      if (r[i] >= a.R) r[i] = -1;
     }
-    for (int64_t n = (int64_t)tid * VEC; n < a.N; n += kCombineThreads * VEC) {
-      Bf16s<VEC> d, v[kCombineBatch];
-      d.load(a.dy + t * a.lddy + n);
+    // the dots of class c, over all lanes
+    auto dots = [&](int c, float (&dot)[kCombineBatch]) {
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j) {
-        if (r[j] >= 0) v[j].load(a.ye + (int64_t)r[j] * a.ldye + n);
-        else v[j].zero();
+      for (int i = 0; i < kCombineBatch; ++i) dot[i] = 0.0f;
+      for (int64_t n = (int64_t)(32 * c + lane) * VEC; n < a.N; n += kCombineThreads * VEC) {
+        Bf16s<VEC> d[kTokens], v[kCombineBatch];
+#pragma unroll
+        for (int m = 0; m < kTokens; ++m) {
+          if (t0 + m < a.T) d[m].load(a.dy + (t0 + m) * a.lddy + n);
+          else d[m].zero();
+        }
+#pragma unroll
+        for (int i = 0; i < kCombineBatch; ++i) {
+          if (r[i] >= 0) v[i].load(a.ye + (int64_t)r[i] * a.ldye + n);
+          else v[i].zero();
+        }
+#pragma unroll
+        for (int i = 0; i < kCombineBatch; ++i)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) dot[i] = fmaf(d[i / KB].get(e), v[i].get(e), dot[i]);
       }
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j)
+      for (int i = 0; i < kCombineBatch; ++i) dot[i] = warp_sum(dot[i]);
+    };
+    float dot[kCombineBatch], sum = 0.0f;  // sum: of dot `lane` (WARP), of dot `tid`
+    if constexpr (WARP) {
+      for (int c = 0; c < kClasses && c * 32 * VEC < a.N; ++c) {
+        dots(c, dot);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) dot[j] = fmaf(d.get(i), v[j].get(i), dot[j]);
-    }
+        for (int i = 0; i < kCombineBatch; ++i)
+          if (lane == i) sum += dot[i];
+      }
+    } else {
+      dots(warp, dot);
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j) {
-      dot[j] = warp_sum(dot[j]);
-      if (lane == 0) s_part[warp][j] = dot[j];
-    }
-    __syncthreads();
-    if (tid < kCombineBatch && j0 + tid < a.k) {
-      float sum = 0.0f;
+      for (int i = 0; i < kCombineBatch; ++i)
+        if (lane == 0) s_part[warp][i] = dot[i];
+      __syncthreads();
+      if (tid < kCombineBatch) {
 #pragma unroll
-      for (int q = 0; q < kCombineThreads / 32; ++q) sum += s_part[q][tid];
-      a.dw[t * a.k + j0 + tid] = sum;
+        for (int c = 0; c < kClasses; ++c) sum += s_part[c][tid];
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    const int i = WARP ? lane : tid;
+    if (i < kCombineBatch && t0 + i / KB < a.T && j0 + i % KB < a.k) a.dw[(t0 + i / KB) * a.k + j0 + i % KB] = sum;
   }
 }
 
@@ -762,9 +791,13 @@ __global__ void __launch_bounds__(kCombineThreads, 3) moe_combine_dw_kernel(cons
 // loads in flight: 16 a lane 397 us, 8 of them 482.  Pieces of 8 / 16 / 32 rows:
 // 401 / 397 / 430.  The last CTAs write the zeros of rows past the experts and
 // of slots without a row.
-template <int VEC>
+//
+// CL: column classes of a row, all eight or fewer of narrow rows, of which a
+// warp then takes 8 / CL at once and a CTA as many times the rows (32768 x 256,
+// 8 experts: 60 us, row by row 216; 16384 x 1024: 99 and 134).
+template <int VEC, int CL>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const CombineBwdArgs a) {
-  constexpr int kClasses = kCombineThreads / 32;
+  constexpr int kClasses = kCombineThreads / 32, kRows = kClasses / CL;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
@@ -775,7 +808,7 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const 
     const int64_t e = blockIdx.x % a.E, piece = blockIdx.x / a.E;
     const int64_t lo = max(__ldg(a.offs + e), 0), n = min((int64_t)__ldg(a.offs + e + 1), a.R) - lo;
     if (n <= 0) return;
-    r = lo + n * piece / a.pieces + warp;
+    r = lo + n * piece / a.pieces + warp * kRows;
     end = lo + n * (piece + 1) / a.pieces;
   } else {
     const int64_t at = (blockIdx.x - blocks) * kClasses + warp, warps = (gridDim.x - blocks) * kClasses;
@@ -788,48 +821,58 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const 
       for (int64_t n = (int64_t)lane * VEC; n < a.N; n += 32 * VEC) store_bf16s<VEC>(a.dye + q * a.lddye + n, z, once);
     return;
   }
-  int slot = r < end ? __ldg(a.src + r) : -1;
-  for (; r < end; r += kClasses) {
-    const int64_t t = slot >= 0 ? (int64_t)((uint32_t)slot / (uint32_t)a.k) : a.T;
-    const bool live = t < a.T;  // not padding
-    const float w = live ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
-    const int slot_next = r + kClasses < end ? __ldg(a.src + r + kClasses) : -1;
-    const uint16_t *dy = a.dy + (live ? t : 0) * a.lddy, *ye = a.ye + r * a.ldye;
-    uint16_t* dye = a.dye + r * a.lddye;
-    float dot[kClasses];
+  auto read_slot = [&](int64_t r0) { return lane < kRows && r0 + lane < end ? __ldg(a.src + r0 + lane) : -1; };
+  int slot = read_slot(r);  // of lane g: row r + g's
+  for (; r < end; r += kClasses * kRows) {
+    const int t_of = slot >= 0 ? (int)min((int64_t)((uint32_t)slot / (uint32_t)a.k), a.T) : (int)a.T;
+    const float w_of = t_of < a.T ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
+    const int slot_next = read_slot(r + kClasses * kRows);
+    float dot[kClasses], w[kRows];
+    int t[kRows];  // a.T: padding
+#pragma unroll
+    for (int g = 0; g < kRows; ++g) {
+      t[g] = __shfl_sync(kFull, t_of, g);
+      w[g] = __shfl_sync(kFull, w_of, g);
+    }
 #pragma unroll
     for (int c = 0; c < kClasses; ++c) dot[c] = 0.0f;
     for (int64_t base = (int64_t)lane * VEC; base < a.N; base += kCombineThreads * VEC) {
       Bf16s<VEC> d[kClasses], v[kClasses];
 #pragma unroll
-      for (int c = 0; c < kClasses; ++c) {
-        const int64_t n = base + c * 32 * VEC;
-        if (live && n < a.N) {
-          v[c].load(ye + n, once);
-          d[c].load(dy + n);
+      for (int i = 0; i < kClasses; ++i) {
+        const int g = i / CL;
+        const int64_t n = base + i % CL * 32 * VEC;
+        if (t[g] < a.T && n < a.N) {
+          v[i].load(a.ye + (r + g) * a.ldye + n, once);
+          d[i].load(a.dy + t[g] * a.lddy + n);
         } else {
-          v[c].zero();
-          d[c].zero();
+          v[i].zero();
+          d[i].zero();
         }
       }
 #pragma unroll
-      for (int c = 0; c < kClasses; ++c) {
-        const int64_t n = base + c * 32 * VEC;
+      for (int i = 0; i < kClasses; ++i) {
+        const int g = i / CL;
+        const int64_t n = base + i % CL * 32 * VEC;
         float o[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          dot[c] = fmaf(d[c].get(i), v[c].get(i), dot[c]);
-          o[i] = w * d[c].get(i);
+        for (int e = 0; e < VEC; ++e) {
+          dot[i] = fmaf(d[i].get(e), v[i].get(e), dot[i]);
+          o[e] = w[g] * d[i].get(e);
         }
-        if (n < a.N) store_bf16s<VEC>(dye + n, o, once);
+        if (n < a.N && r + g < end) store_bf16s<VEC>(a.dye + (r + g) * a.lddye + n, o, once);
       }
+      if constexpr (CL < kClasses) break;  // (N is at most CL classes)
     }
-    if (live) {
-      float sum = 0.0f;
+    float sum = 0.0f;  // of lane g: row r + g's
 #pragma unroll
-      for (int c = 0; c < kClasses; ++c) sum += warp_sum(dot[c]);
-      if (lane == 0) a.dw[slot] = sum;
+    for (int g = 0; g < kRows; ++g) {
+      float of_row = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CL; ++c) of_row += warp_sum(dot[g * CL + c]);
+      if (lane == g) sum = of_row;
     }
+    if (lane < kRows && t_of < a.T) a.dw[slot] = sum;
     slot = slot_next;
   }
 }
@@ -1006,12 +1049,29 @@ struct RowAlign {
   }
 };
 
+// f with the rows of a token that are read at once: k rounded up to a power of two, at most eight.
+template <typename F>
+static cudaError_t by_batch(int k, F&& f) {
+  if (k <= 1) return f(std::integral_constant<int, 1>{});
+  if (k <= 2) return f(std::integral_constant<int, 2>{});
+  if (k <= 4) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 8>{});
+}
+
 cudaError_t launch_moe_combine(const CombineArgs& args, cudaStream_t st) {
   return RowAlign(args.N).row(args.ye, args.ldye).row(args.y, args.ldy).go([&](auto vec) {
-    constexpr int kVec = decltype(vec)::value;
-    CombineArgs a = args;
-    a.col_blocks = (int)cdiv(a.N, kCombineThreads * kVec);
-    return launch_pdl(moe_combine_kernel<kVec>, (unsigned)(a.T * a.col_blocks), kCombineThreads, 0, st, a);
+    return by_batch(args.k, [&](auto batch) {
+      constexpr int kVec = decltype(vec)::value, kBatch = decltype(batch)::value;
+      CombineArgs a = args;
+      // as many CTAs a row as it needs, of equal parts; as many rows a CTA as fit
+      const int64_t accesses = cdiv(a.N, kVec);
+      a.col_blocks = (int)cdiv(accesses, kCombineThreads);
+      a.cols = (int)cdiv(accesses, a.col_blocks);
+      a.sides = kCombineThreads / a.cols;
+      const int64_t ctas = cdiv(a.T, a.sides * (kCombineBatch / kBatch)) * a.col_blocks;
+      return launch_pdl(moe_combine_kernel<kVec, kBatch>, (unsigned)ctas, (unsigned)(cdiv(a.sides * a.cols, 32) * 32), 0,
+                        st, a);
+    });
   });
 }
 
@@ -1020,17 +1080,32 @@ cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& args, int num_sms, cuda
   if (!args.dye) {
     if (args.T == 0) return cudaSuccess;
     return rows.go([&](auto vec) {
-      return launch_pdl(moe_combine_dw_kernel<decltype(vec)::value>, (unsigned)args.T, kCombineThreads, 0, st, args);
+      return by_batch(args.k, [&](auto batch) {
+        constexpr int kVec = decltype(vec)::value, kBatch = decltype(batch)::value;
+        const int64_t groups = cdiv(args.T, kCombineBatch / kBatch);
+        if (args.N <= 6 * 32 * kVec)
+          return launch_pdl(moe_combine_dw_kernel<kVec, kBatch, true>, (unsigned)cdiv(groups, kCombineThreads / 32),
+                            kCombineThreads, 0, st, args);
+        return launch_pdl(moe_combine_dw_kernel<kVec, kBatch, false>, (unsigned)groups, kCombineThreads, 0, st, args);
+      });
     });
   }
-  CombineBwdArgs a = args;
-  a.pieces = cdiv(a.R, a.E * kCombinePiece);
-  if (a.pieces < 1) a.pieces = 1;
-  // and CTAs for the zeros
-  const int64_t zeros = std::min<int64_t>(cdiv(std::max(cdiv(a.T * a.k, 32), a.R), kCombineThreads / 32), 2 * num_sms);
-  const unsigned grid = (unsigned)(a.E * a.pieces + zeros);
-  return RowAlign(rows).row(a.dye, a.lddye).go([&](auto vec) {
-    return launch_pdl(moe_combine_bwd_kernel<decltype(vec)::value>, grid, kCombineThreads, 0, st, a);
+  return RowAlign(rows).row(args.dye, args.lddye).go([&](auto vec) {
+    constexpr int kVec = decltype(vec)::value;
+    auto run = [&](auto classes) {
+      constexpr int kCl = decltype(classes)::value;
+      CombineBwdArgs a = args;
+      a.pieces = std::max<int64_t>(cdiv(a.R, a.E * kCombinePiece * (8 / kCl)), 1);
+      // and CTAs for the zeros
+      const int64_t zeros =
+          std::min<int64_t>(cdiv(std::max(cdiv(a.T * a.k, 32), a.R), kCombineThreads / 32), 2 * num_sms);
+      return launch_pdl(moe_combine_bwd_kernel<kVec, kCl>, (unsigned)(a.E * a.pieces + zeros), kCombineThreads, 0, st, a);
+    };
+    const int64_t classes = cdiv(args.N, 32 * kVec);
+    if (classes <= 1) return run(std::integral_constant<int, 1>{});
+    if (classes <= 2) return run(std::integral_constant<int, 2>{});
+    if (classes <= 4) return run(std::integral_constant<int, 4>{});
+    return run(std::integral_constant<int, 8>{});
   });
 }
 

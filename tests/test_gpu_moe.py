@@ -318,6 +318,13 @@ def test_combine_and_gradient(T, k, E, align, N):
     assert np.all(np.abs(_f64(dw) - dw_ref) <= chain * EPS * size + 1e-38)
 
 
+# Rows of one to eight column classes and more, shared CTAs, one to several tokens a thread, k past eight
+@pytest.mark.parametrize("N", [1, 8, 24, 256, 264, 500, 1024, 1026, 1536, 1544, 2304])
+@pytest.mark.parametrize("T,k,E,align", [(1, 1, 3, 1), (33, 2, 5, 128), (70, 3, 8, 1), (19, 4, 6, 16), (40, 9, 12, 1)])
+def test_combine_narrow_rows_and_batches(T, k, E, align, N):
+    test_combine_and_gradient(T, k, E, align, N)
+
+
 def test_combine_gradients_against_differences():
     """The combine is linear in ye and in w, so a whole unit step is its derivative."""
     T, k, E, N = 6, 2, 3, 16
