@@ -660,6 +660,15 @@ __device__ __forceinline__ uint64_t evict_first_policy() {
 }
 
 constexpr int kCombineBatch = 8;   // rows of ye in flight a thread
+// CTAs an SM that the registers leave room for, by the columns an access takes:
+// narrow accesses need more warps for the same bytes in flight; a few registers
+// spill for it.  8192 tokens, 8 experts each, in us, at 4001 / 4002 / 4004
+// columns (1 / 2 / 4): y 272 / 114 / 98 (430 / 170 / 117 with four CTAs and a
+// CTA for 256 accesses), dw 190 / 100 / 90 (334 / 134 / 102 with three), dw
+// with dye 467 / 216 / 193 (642 / 230 / 224 with two).
+constexpr int combine_ctas(int vec) { return vec == 1 ? 8 : 4; }
+constexpr int combine_dw_ctas(int vec) { return vec <= 2 ? 6 : vec == 4 ? 5 : 3; }
+constexpr int combine_bwd_ctas(int vec) { return vec == 1 ? 5 : vec == 2 ? 4 : vec == 4 ? 3 : 2; }
 constexpr int kCombinePiece = 16;  // rows of an expert that a CTA of the gradient takes, on average
 
 }  // namespace
@@ -672,35 +681,51 @@ constexpr int kCombinePiece = 16;  // rows of an expert that a CTA of the gradie
 // rate.  Four CTAs an SM: with more or fewer loads in flight than theirs the
 // memory is slower (three 210 us, five 198).
 template <int VEC, int KB>
-__global__ void __launch_bounds__(kCombineThreads, 4) moe_combine_kernel(const CombineArgs a) {
+__global__ void __launch_bounds__(kCombineThreads, combine_ctas(VEC)) moe_combine_kernel(const CombineArgs a) {
   constexpr int kTokens = kCombineBatch / KB;
   pdl_launch_dependents();
   pdl_wait();
   const int side = KB == kCombineBatch && a.sides == 1 ? 0 : (int)threadIdx.x / a.cols;
   const int64_t t0 = ((int64_t)(blockIdx.x / a.col_blocks) * a.sides + side) * kTokens;
-  const int64_t n = ((int64_t)(blockIdx.x % a.col_blocks) * a.cols + ((int)threadIdx.x - side * a.cols)) * VEC;
-  if (n >= a.N || (int)threadIdx.x >= a.sides * a.cols) return;
-  float acc[VEC] = {};
-  for (int j0 = 0; j0 < a.k; j0 += KB) {  // (once where KB < 8, as k is at most KB)
-    Bf16s<VEC> v[kCombineBatch];
-    float w[kCombineBatch];
+  const int64_t n0 = ((int64_t)(blockIdx.x % a.col_blocks) * a.cols + ((int)threadIdx.x - side * a.cols)) * VEC;
+  if (n0 >= a.N || (int)threadIdx.x >= a.sides * a.cols) return;
+  constexpr int U = VEC == 2 ? 2 : 1;  // accesses of a row at once
+  const int64_t step = (int64_t)a.cols * VEC;
+  for (int64_t nb = n0; nb < a.N; nb += U * step) {
+    float acc[U][VEC] = {};
+    for (int j0 = 0; j0 < a.k; j0 += KB) {  // (once where KB < 8, as k is at most KB)
+      Bf16s<VEC> v[U][kCombineBatch];
+      float w[kCombineBatch];
 #pragma unroll
-    for (int i = 0; i < kCombineBatch; ++i) {
-      const int64_t t = t0 + i / KB, slot = t * a.k + j0 + i % KB;
-      const int r = (kTokens == 1 || t < a.T) && j0 + i % KB < a.k ? __ldg(a.row + slot) : -1;
-      const bool ok = r >= 0 && r < a.R;
-      w[i] = ok ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
-      if (ok) v[i].load(a.ye + (int64_t)r * a.ldye + n);
-      else v[i].zero();
+      for (int i = 0; i < kCombineBatch; ++i) {
+        const int64_t t = t0 + i / KB, slot = t * a.k + j0 + i % KB;
+        const int r = (kTokens == 1 || t < a.T) && j0 + i % KB < a.k ? __ldg(a.row + slot) : -1;
+        const bool ok = r >= 0 && r < a.R;
+        w[i] = ok ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (ok && (u == 0 || nb + u * step < a.N)) v[u][i].load(a.ye + (int64_t)r * a.ldye + nb + u * step);
+          else v[u][i].zero();
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kCombineBatch; ++i)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t n = nb + u * step;
+#pragma unroll
+          for (int c = 0; c < VEC; ++c)
+            acc[u][c] = fmaf(w[i], v[u][i].get(c), kTokens > 1 && i % KB == 0 ? 0.0f : acc[u][c]);
+          if (kTokens > 1 && i % KB == KB - 1 && t0 + i / KB < a.T && (u == 0 || n < a.N))
+            store_bf16s<VEC>(a.y + (t0 + i / KB) * a.ldy + n, acc[u]);
+        }
     }
+    if (kTokens == 1)
 #pragma unroll
-    for (int i = 0; i < kCombineBatch; ++i) {
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) acc[c] = fmaf(w[i], v[i].get(c), kTokens > 1 && i % KB == 0 ? 0.0f : acc[c]);
-      if (kTokens > 1 && i % KB == KB - 1 && t0 + i / KB < a.T) store_bf16s<VEC>(a.y + (t0 + i / KB) * a.ldy + n, acc);
-    }
+      for (int u = 0; u < U; ++u)
+        if (u == 0 || nb + u * step < a.N) store_bf16s<VEC>(a.y + t0 * a.ldy + nb + u * step, acc[u]);
+    if (VEC == 8) break;
   }
-  if (kTokens == 1) store_bf16s<VEC>(a.y + t0 * a.ldy + n, acc);
 }
 
 // The gradient comes in two forms that give the same bits: a dot product dw is
@@ -714,7 +739,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) moe_combine_kernel(const C
 // classes of its tokens (rows of 1024 values 51 us against 71, 1536 73 against
 // 80, 2048 95 against 91; 16384 tokens, 8 experts).
 template <int VEC, int KB, bool WARP>
-__global__ void __launch_bounds__(kCombineThreads, 3) moe_combine_dw_kernel(const CombineBwdArgs a) {
+__global__ void __launch_bounds__(kCombineThreads, combine_dw_ctas(VEC)) moe_combine_dw_kernel(const CombineBwdArgs a) {
   constexpr int kClasses = kCombineThreads / 32, kTokens = kCombineBatch / KB;
   __shared__ float s_part[kClasses][kCombineBatch];
   pdl_launch_dependents();
@@ -796,7 +821,8 @@ __global__ void __launch_bounds__(kCombineThreads, 3) moe_combine_dw_kernel(cons
 // warp then takes 8 / CL at once and a CTA as many times the rows (32768 x 256,
 // 8 experts: 60 us, row by row 216; 16384 x 1024: 99 and 134).
 template <int VEC, int CL>
-__global__ void __launch_bounds__(kCombineThreads) moe_combine_bwd_kernel(const CombineBwdArgs a) {
+__global__ void __launch_bounds__(kCombineThreads, combine_bwd_ctas(VEC))
+    moe_combine_bwd_kernel(const CombineBwdArgs a) {
   constexpr int kClasses = kCombineThreads / 32, kRows = kClasses / CL;
   pdl_launch_dependents();
   pdl_wait();
@@ -1031,8 +1057,8 @@ cudaError_t launch_moe_plan(const PlanArgs& a, cudaStream_t st) {
 
 // Columns an access takes: 8, 4, 2 or 1, the most that the width, the rows'
 // strides and their bases allow (one access then stays within a row, aligned).
-// 8192 tokens, eight rows each: 95 us at 4000 columns (8), 106 at 4004 (4), 143
-// at 4002 (2), 333 at 4001 (1).
+// 8192 tokens, eight rows each: 90 us at 4000 columns (8), 98 at 4004 (4), 114
+// at 4002 (2), 272 at 4001 (1).
 struct RowAlign {
   int64_t bits;
   explicit RowAlign(int64_t N) : bits(N) {}
@@ -1063,14 +1089,15 @@ cudaError_t launch_moe_combine(const CombineArgs& args, cudaStream_t st) {
     return by_batch(args.k, [&](auto batch) {
       constexpr int kVec = decltype(vec)::value, kBatch = decltype(batch)::value;
       CombineArgs a = args;
-      // as many CTAs a row as it needs, of equal parts; as many rows a CTA as fit
+      // as many CTAs a row as it needs, of equal parts, and one that loops where an access is
+      // narrow (starting CTAs would take longer); as many rows a CTA as fit
       const int64_t accesses = cdiv(a.N, kVec);
-      a.col_blocks = (int)cdiv(accesses, kCombineThreads);
-      a.cols = (int)cdiv(accesses, a.col_blocks);
+      a.col_blocks = kVec < 8 ? 1 : (int)cdiv(accesses, kCombineThreads);
+      a.cols = (int)std::min<int64_t>(cdiv(accesses, a.col_blocks), kCombineThreads);
       a.sides = kCombineThreads / a.cols;
       const int64_t ctas = cdiv(a.T, a.sides * (kCombineBatch / kBatch)) * a.col_blocks;
-      return launch_pdl(moe_combine_kernel<kVec, kBatch>, (unsigned)ctas, (unsigned)(cdiv(a.sides * a.cols, 32) * 32), 0,
-                        st, a);
+      const unsigned threads = (unsigned)(cdiv(a.sides * a.cols, 32) * 32);
+      return launch_pdl(moe_combine_kernel<kVec, kBatch>, (unsigned)ctas, threads, 0, st, a);
     });
   });
 }
@@ -1099,7 +1126,8 @@ cudaError_t launch_moe_combine_bwd(const CombineBwdArgs& args, int num_sms, cuda
       // and CTAs for the zeros
       const int64_t zeros =
           std::min<int64_t>(cdiv(std::max(cdiv(a.T * a.k, 32), a.R), kCombineThreads / 32), 2 * num_sms);
-      return launch_pdl(moe_combine_bwd_kernel<kVec, kCl>, (unsigned)(a.E * a.pieces + zeros), kCombineThreads, 0, st, a);
+      const unsigned ctas = (unsigned)(a.E * a.pieces + zeros);
+      return launch_pdl(moe_combine_bwd_kernel<kVec, kCl>, ctas, kCombineThreads, 0, st, a);
     };
     const int64_t classes = cdiv(args.N, 32 * kVec);
     if (classes <= 1) return run(std::integral_constant<int, 1>{});
