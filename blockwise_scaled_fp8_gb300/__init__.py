@@ -929,11 +929,11 @@ def check_device_errors() -> None:
 def debug_write_counts(kind: int, M: int, N: int, K: int, flag: int = 0):
     """Per-element write counts a launch would produce.  Returns
     (counts [rows, cols], scale_counts or None, out_of_range_writes)."""
-    shapes = {0: (M, K), 1: (N, K), 2: (N, K), 3: (M, N), 4: (K, N), 5: (M, K), 6: (K, M)}
+    shapes = {0: (M, K), 1: (N, K), 2: (N, K), 3: (M, N), 4: (K, N), 5: (M, K), 6: (K, M), 7: (M, N)}
     rows, cols = shapes[kind]
     counts = np.zeros((rows, cols), dtype=np.uint32)
     sshape = {0: (_cdiv(K, BLOCK), M), 1: (_cdiv(K, BLOCK), N), 2: (_cdiv(N, BLOCK), _cdiv(K, BLOCK)),
-              5: (_cdiv(K, BLOCK), M), 6: (_cdiv(M, BLOCK), K)}.get(kind)
+              5: (_cdiv(K, BLOCK), M), 6: (_cdiv(M, BLOCK), K), 7: (M, K)}.get(kind)
     scounts = np.zeros(sshape, dtype=np.uint32) if sshape else None
     oob = ctypes.c_int64(0)
     _check(lib().bfp8_debug_write_counts(kind, M, N, K, flag, counts.ctypes.data_as(ctypes.c_void_p),

@@ -641,7 +641,7 @@ bfp8_status bfp8_moe_combine(const void* ye, int64_t ldye, int64_t R, const int3
   int sms = 0;
   if ((st = check_device(&sms)) != BFP8_OK) return st;
   const cudaError_t e = launch_moe_combine(
-      CombineArgs{(const uint16_t*)ye, ldye, R, row, w, T, (int)k, N, (uint16_t*)y, ldy, 0, 0, 0}, (cudaStream_t)stream);
+      CombineArgs{(const uint16_t*)ye, ldye, R, row, w, T, (int)k, N, (uint16_t*)y, ldy, {}}, (cudaStream_t)stream);
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
 }
 
@@ -1478,6 +1478,24 @@ bfp8_status bfp8_debug_write_counts(int kind, int64_t M, int64_t N, int64_t K, i
                 for (int b = 0; b < 8; ++b)
                   if (n0 + b < N) hit(counts, m, n0 + b, M, N);
               }
+      }
+    return BFP8_OK;
+  }
+  if (kind == 7) {  // moe_combine y [M tokens, N], and the slots [M, K choices] that the threads read
+    const int vec = 1 << ((flag >> 4) & 3), batch = combine_batch((int)K), tokens = kCombineBatch / batch;
+    CHECK_ARG(K >= 1 && K <= BFP8_MOE_MAX_K && N % vec == 0, "bfp8_debug_write_counts: k or N out of range");
+    if (M == 0 || N == 0) return BFP8_OK;
+    const CombineGeom g = combine_geom(N, vec);
+    for (int64_t blk = 0; blk < combine_ctas(M, g, batch); ++blk)
+      for (int th = 0; th < combine_threads(g); ++th) {
+        const CombineThread c = combine_thread((uint32_t)blk, th, g, M, N, vec, batch);
+        if (!c.on) continue;
+        for (int64_t t = c.t0; t < c.t0 + tokens; ++t) {
+          if (tokens > 1 && t >= M) continue;  // (with one token a thread, only `on` bounds it)
+          for (int64_t j = 0; j < K; ++j) hit(scale_counts, t, j, M, K);
+          for (int64_t n = c.n0; n < N; n += vec < 8 ? (int64_t)g.cols * vec : N)
+            for (int b = 0; b < vec; ++b) hit(counts, t, n + b, M, N);
+        }
       }
     return BFP8_OK;
   }

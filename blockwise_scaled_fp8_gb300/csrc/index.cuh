@@ -212,4 +212,50 @@ BFP8_HD int epi_store_col(int e, int lane, int sg, int G, int bn, int ew) {
   return epi_col0(e, bn, ew) + 8 * (G * sg + lane % G);
 }
 
+// ---------------------------------------------------------------------------
+// Combine of routed experts: a CTA holds `sides` groups of `cols` threads; a
+// group takes kCombineBatch / batch consecutive tokens (batch: the rows of a
+// token that are read at once, a power of two), a thread `vec` columns of each
+// and, with vec < 8, every cols * vec further on.  With vec = 8 a row may need
+// col_blocks CTAs.  N is a multiple of vec.
+// ---------------------------------------------------------------------------
+constexpr int kCombineThreads = 256;
+constexpr int kCombineBatch = 8;  // rows of the experts' outputs in flight a thread
+
+struct CombineGeom {
+  int col_blocks, cols, sides;
+};
+// As many CTAs a row as it needs, of equal parts, and one that loops where an
+// access is narrow (starting CTAs would take longer); as many rows a CTA as fit.
+BFP8_HD CombineGeom combine_geom(int64_t N, int vec) {
+  const int64_t accesses = cdiv(N, vec);
+  CombineGeom g;
+  g.col_blocks = vec < 8 ? 1 : (int)cdiv(accesses, kCombineThreads);
+  const int64_t cols = cdiv(accesses, g.col_blocks);
+  g.cols = (int)(cols < kCombineThreads ? cols : kCombineThreads);
+  g.sides = kCombineThreads / g.cols;
+  return g;
+}
+BFP8_HD int64_t combine_ctas(int64_t T, const CombineGeom& g, int batch) {
+  return cdiv(T, g.sides * (kCombineBatch / batch)) * g.col_blocks;
+}
+BFP8_HD int combine_threads(const CombineGeom& g) { return (int)cdiv(g.sides * g.cols, 32) * 32; }
+
+struct CombineThread {
+  int64_t t0, n0;  // first token, first column
+  bool on;         // it has a token and a column
+};
+BFP8_HD CombineThread combine_thread(uint32_t block, int thread, const CombineGeom& g, int64_t T, int64_t N, int vec,
+                                     int batch) {
+  const uint32_t blocks = (uint32_t)g.col_blocks;
+  const int side = batch == kCombineBatch && g.sides == 1 ? 0 : thread / g.cols;
+  CombineThread c;
+  c.t0 = ((int64_t)(block / blocks) * g.sides + side) * (kCombineBatch / batch);
+  c.n0 = ((int64_t)(block % blocks) * g.cols + (thread - side * g.cols)) * vec;
+  c.on = thread < g.sides * g.cols && c.n0 < N && c.t0 < T;
+  return c;
+}
+// Rows of a token that are read at once: k rounded up to a power of two, at most kCombineBatch.
+BFP8_HD int combine_batch(int k) { return k <= 1 ? 1 : k <= 2 ? 2 : k <= 4 ? 4 : kCombineBatch; }
+
 }  // namespace bfp8

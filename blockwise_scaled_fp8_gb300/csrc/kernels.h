@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/bfp8.h"
+#include "index.cuh"
 
 namespace bfp8 {
 
@@ -135,7 +136,6 @@ cudaError_t launch_gemm_wgrad_xq(const GemmWxqArgs& a, int num_sms, cudaStream_t
 // arguments are those of the ABI's entries (bfp8.h).
 constexpr int kRouteThreads = 128;
 constexpr int kPlanThreads = 1024;
-constexpr int kCombineThreads = 256;
 constexpr float kRouteSumFloor = 1e-20f;  // of the chosen scores' sum that weights are renormalised by
 
 struct RouteArgs {
@@ -203,7 +203,7 @@ struct CombineArgs {
   int64_t N;
   uint16_t* y;
   int64_t ldy;
-  int col_blocks, cols, sides;  // set by the launcher: CTAs a row, threads a row of a CTA, rows side by side
+  CombineGeom geom;  // set by the launcher
 };
 cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t st);
 

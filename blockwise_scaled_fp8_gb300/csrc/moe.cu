@@ -659,14 +659,13 @@ __device__ __forceinline__ uint64_t evict_first_policy() {
   return p;
 }
 
-constexpr int kCombineBatch = 8;   // rows of ye in flight a thread
 // CTAs an SM that the registers leave room for, by the columns an access takes:
 // narrow accesses need more warps for the same bytes in flight; a few registers
 // spill for it.  8192 tokens, 8 experts each, in us, at 4001 / 4002 / 4004
 // columns (1 / 2 / 4): y 272 / 114 / 98 (430 / 170 / 117 with four CTAs and a
 // CTA for 256 accesses), dw 190 / 100 / 90 (334 / 134 / 102 with three), dw
 // with dye 467 / 216 / 193 (642 / 230 / 224 with two).
-constexpr int combine_ctas(int vec) { return vec == 1 ? 8 : 4; }
+constexpr int combine_ctas_sm(int vec) { return vec == 1 ? 8 : 4; }
 constexpr int combine_dw_ctas(int vec) { return vec <= 2 ? 6 : vec == 4 ? 5 : 3; }
 constexpr int combine_bwd_ctas(int vec) { return vec == 1 ? 5 : vec == 2 ? 4 : vec == 4 ? 3 : 2; }
 constexpr int kCombinePiece = 16;  // rows of an expert that a CTA of the gradient takes, on average
@@ -681,17 +680,16 @@ constexpr int kCombinePiece = 16;  // rows of an expert that a CTA of the gradie
 // rate.  Four CTAs an SM: with more or fewer loads in flight than theirs the
 // memory is slower (three 210 us, five 198).
 template <int VEC, int KB>
-__global__ void __launch_bounds__(kCombineThreads, combine_ctas(VEC)) moe_combine_kernel(const CombineArgs a) {
+__global__ void __launch_bounds__(kCombineThreads, combine_ctas_sm(VEC)) moe_combine_kernel(const CombineArgs a) {
   constexpr int kTokens = kCombineBatch / KB;
   pdl_launch_dependents();
   pdl_wait();
-  const int side = KB == kCombineBatch && a.sides == 1 ? 0 : (int)threadIdx.x / a.cols;
-  const int64_t t0 = ((int64_t)(blockIdx.x / a.col_blocks) * a.sides + side) * kTokens;
-  const int64_t n0 = ((int64_t)(blockIdx.x % a.col_blocks) * a.cols + ((int)threadIdx.x - side * a.cols)) * VEC;
-  if (n0 >= a.N || (int)threadIdx.x >= a.sides * a.cols) return;
+  const CombineThread me = combine_thread(blockIdx.x, (int)threadIdx.x, a.geom, a.T, a.N, VEC, KB);
+  const int64_t t0 = me.t0;
+  if (!me.on) return;
   constexpr int U = VEC == 2 ? 2 : 1;  // accesses of a row at once
-  const int64_t step = (int64_t)a.cols * VEC;
-  for (int64_t nb = n0; nb < a.N; nb += U * step) {
+  const int64_t step = (int64_t)a.geom.cols * VEC;
+  for (int64_t nb = me.n0; nb < a.N; nb += U * step) {
     float acc[U][VEC] = {};
     for (int j0 = 0; j0 < a.k; j0 += KB) {  // (once where KB < 8, as k is at most KB)
       Bf16s<VEC> v[U][kCombineBatch];
@@ -699,7 +697,7 @@ __global__ void __launch_bounds__(kCombineThreads, combine_ctas(VEC)) moe_combin
 #pragma unroll
       for (int i = 0; i < kCombineBatch; ++i) {
         const int64_t t = t0 + i / KB, slot = t * a.k + j0 + i % KB;
-        const int r = (kTokens == 1 || t < a.T) && j0 + i % KB < a.k ? __ldg(a.row + slot) : -1;
+        const int r = t < a.T && j0 + i % KB < a.k ? __ldg(a.row + slot) : -1;
         const bool ok = r >= 0 && r < a.R;
         w[i] = ok ? (a.w ? __ldg(a.w + slot) : 1.0f) : 0.0f;
 #pragma unroll
@@ -1075,13 +1073,15 @@ struct RowAlign {
   }
 };
 
-// f with the rows of a token that are read at once: k rounded up to a power of two, at most eight.
+// f with combine_batch(k) as a compile-time number.
 template <typename F>
 static cudaError_t by_batch(int k, F&& f) {
-  if (k <= 1) return f(std::integral_constant<int, 1>{});
-  if (k <= 2) return f(std::integral_constant<int, 2>{});
-  if (k <= 4) return f(std::integral_constant<int, 4>{});
-  return f(std::integral_constant<int, 8>{});
+  switch (combine_batch(k)) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    default: return f(std::integral_constant<int, kCombineBatch>{});
+  }
 }
 
 cudaError_t launch_moe_combine(const CombineArgs& args, cudaStream_t st) {
@@ -1089,15 +1089,9 @@ cudaError_t launch_moe_combine(const CombineArgs& args, cudaStream_t st) {
     return by_batch(args.k, [&](auto batch) {
       constexpr int kVec = decltype(vec)::value, kBatch = decltype(batch)::value;
       CombineArgs a = args;
-      // as many CTAs a row as it needs, of equal parts, and one that loops where an access is
-      // narrow (starting CTAs would take longer); as many rows a CTA as fit
-      const int64_t accesses = cdiv(a.N, kVec);
-      a.col_blocks = kVec < 8 ? 1 : (int)cdiv(accesses, kCombineThreads);
-      a.cols = (int)std::min<int64_t>(cdiv(accesses, a.col_blocks), kCombineThreads);
-      a.sides = kCombineThreads / a.cols;
-      const int64_t ctas = cdiv(a.T, a.sides * (kCombineBatch / kBatch)) * a.col_blocks;
-      const unsigned threads = (unsigned)(cdiv(a.sides * a.cols, 32) * 32);
-      return launch_pdl(moe_combine_kernel<kVec, kBatch>, (unsigned)ctas, threads, 0, st, a);
+      a.geom = combine_geom(a.N, kVec);
+      return launch_pdl(moe_combine_kernel<kVec, kBatch>, (unsigned)combine_ctas(a.T, a.geom, kBatch),
+                        (unsigned)combine_threads(a.geom), 0, st, a);
     });
   });
 }

@@ -605,6 +605,9 @@ BFP8_API bfp8_status bfp8_debug_gemm_stall(const void *qa, int64_t lda, const fl
  *   kind 4: bfp8_quant_weight qt       (rows = K, cols = N)
  *   kind 5: bfp8_quant_dual q_row      (rows = M, cols = K), scales [Kb, M]  (T = M, C = K)
  *   kind 6: bfp8_quant_dual q_col      (rows = K, cols = M), scales [Mb, K]
+ *   kind 7: bfp8_moe_combine y         (rows = M tokens, cols = N), K choices a
+ *           token; flag bits 4-5: log2 of the columns an access takes (N is a
+ *           multiple of them); scale_counts counts the reads of row and w [M, K]
  * counts is host uint32 [rows*cols] (incremented); *oob receives the number
  * of writes that would land outside the logical tensor.  Scale writes are
  * counted in scale_counts (host uint32 [scale_rows*scale_cols], may be NULL).
