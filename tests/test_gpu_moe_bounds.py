@@ -75,3 +75,67 @@ def test_combine_stays_inside_its_output(N, k):
         want, size = ref.combine(f(ye), row, f(w)), ref.combine(abs(f(ye)), row, abs(f(w)))
         # k fused products in fp32, one rounding to bf16
         assert (abs(f(y.out) - want) <= 2.0 ** -8 * abs(want) + (k + 1) * 2 * EPS * size + 1e-38).all()
+
+
+def _call(fn, *args):
+    """An entry of the ABI: tensors by their addresses, the current stream."""
+    a = [x.data_ptr() if isinstance(x, torch.Tensor) else x for x in args]
+    assert getattr(B.lib(), fn)(*a, torch.cuda.current_stream().cuda_stream) == B.BFP8_OK
+
+
+@pytest.mark.parametrize("with_dye", [True, False])
+@pytest.mark.parametrize("N", [1, 24, 101, 128, 258, 260, 1000, 1536, 1544, 4104])
+@pytest.mark.parametrize("k", [1, 2, 3, 6, 9, 32])
+def test_combine_gradient_stays_inside_its_outputs(N, k, with_dye):
+    for T in (1, 37, 70):
+        g = torch.Generator(device="cuda").manual_seed(1000 * N + 10 * k + T)
+        plan = _plan(g, T, k, 40, 16)
+        R = plan.src.numel()
+        ye, dy = (torch.randn(n, N, generator=g, device="cuda").bfloat16() for n in (R, T))
+        w = torch.randn(T, k, generator=g, device="cuda")
+        more = torch.arange(300 * k, device="cuda") % R
+        row, src = _behind(plan.row, more), _behind(plan.src, more % (T * k))
+        dye, dw = Guarded(R, N, N + 8, torch.bfloat16), Guarded(T, k, k, torch.float32)
+        _call("bfp8_moe_combine_bwd", dy, N, ye, N, R, plan.offs, 40, row, src, _behind(w, torch.ones(300 * k, device="cuda")),
+              T, k, N, dye.out if with_dye else None, N + 8, dw.out)
+        dye.check()
+        dw.check()
+        want_dye, want_dw = B.moe_combine_bwd(dy, ye, plan, w, with_dye=with_dye)
+        assert torch.equal(dw.out, want_dw) and (not with_dye or torch.equal(dye.out, want_dye))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 2), (37, 32), (64, 6), (160, 8), (256, 8), (500, 3), (1024, 32)])
+def test_router_stays_inside_its_outputs(E, k, score, dtype):
+    f32 = int(dtype == torch.float32)
+    for T in (1, 5, 34):
+        g = torch.Generator(device="cuda").manual_seed(E + T)
+        logits = torch.randn(T, E, generator=g, device="cuda").to(dtype)
+        wide = torch.full((T + 8, E + 3), 100.0, dtype=dtype, device="cuda")  # what is beside would be chosen
+        wide[:T, :E] = logits
+        idx, w = Guarded(T, k, k, torch.int32), Guarded(T, k, k, torch.float32)
+        _call("bfp8_moe_route", wide, f32, T, E, E + 3, None, k, score, 1, 1, 1, 1, 1.0, idx.out, w.out)
+        idx.check()
+        w.check()
+        i1, w1 = B.moe_route(logits, k, score="sigmoid" if score else "softmax")
+        assert torch.equal(idx.out, i1) and torch.equal(w.out, w1)
+        dw, dl = torch.randn(T, k, generator=g, device="cuda"), Guarded(T, E, E + 3, dtype)
+        _call("bfp8_moe_route_bwd", wide, f32, T, E, E + 3, i1, w1, dw, k, score, 1, 1.0, dl.out, E + 3)
+        dl.check()
+        assert torch.equal(dl.out, B.moe_route_bwd(logits, i1, w1, dw, score="sigmoid" if score else "softmax"))
+
+
+@pytest.mark.parametrize("T,k,E,align", [(1, 1, 1, 1), (1, 8, 64, 1), (33, 3, 7, 128), (150, 7, 160, 16), (4100, 2, 8, 16),
+                                         (5000, 8, 1024, 128)])
+def test_plan_stays_inside_its_outputs(T, k, E, align):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    idx = torch.randint(-1, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    R = B.moe_plan_rows(T, k, E, align)
+    offs, row, src, counts = (Guarded(n, 1, 1, torch.int32) for n in (E + 1, T * k, R, E))
+    _call("bfp8_moe_plan", _behind(idx, torch.zeros(4096, device="cuda")), T, k, E, align, offs.out, row.out, src.out, R,
+          counts.out)
+    want = B.moe_plan(idx, E, align=align)
+    for got, part in ((offs, want.offs), (row, want.row), (src, want.src), (counts, want.counts)):
+        got.check()
+        assert torch.equal(got.out.reshape(-1), part.reshape(-1))
