@@ -328,9 +328,11 @@ __device__ __forceinline__ float dense_exp(float x) {
   return F32 ? expf(x) : __expf(x);
 }
 
-// The router's gradient.  With p the scores, S = max(sum of the chosen p,
-// floor) and the chosen j:
+// The router's gradient.  With p the scores, S the sum of the chosen p and the
+// chosen j:
 //   ds_j = (scale dw_j - sum_i dw_i w_i) / S   (renormalised),  scale dw_j  (not)
+//   (where S is not above the floor the weights are scale p / floor, whose
+//   denominator is a constant: ds_j = scale dw_j / floor)
 //   sigmoid:  dl_j = ds_j p_j (1 - p_j), zero elsewhere
 //   softmax:  dl_e = p_e (ds_e - sum_i ds_i p_i), ds_e = 0 where not chosen
 // One warp a token; lane j < k handles choice j.  Of the dense row lane l
@@ -410,8 +412,8 @@ __global__ void __launch_bounds__(kRouteBwdThreads<PAIRS, SIGMOID>) moe_route_bw
   }
   float ds = a.scale * dw;
   if (a.renormalize) {
-    const float S = fmaxf(warp_sum(p_j), kRouteSumFloor);
-    ds = (ds - warp_sum(dw * w)) / S;
+    const float S = warp_sum(p_j), back = warp_sum(dw * w);
+    ds = S > kRouteSumFloor ? (ds - back) / S : ds / kRouteSumFloor;
   }
   if (e_j < 0) ds = 0.0f;
   if constexpr (!SIGMOID) dot = warp_sum(ds * p_j);
