@@ -387,10 +387,12 @@ __global__ void __launch_bounds__(kRouteBwdThreads<PAIRS, SIGMOID>) moe_route_bw
       s[2 * i + 1] = l1 > low ? fminf(l1, FLT_MAX) : -INFINITY;
     }
     // p = exp(l - ref) * mult: by the first choice where its weight gives its p
-    // (no renormalisation, and p not so small that it has lost bits), else by
-    // the largest logit and the sum over the row
-    float ref = __shfl_sync(kFull, l_j, 0), mult = __shfl_sync(kFull, w, 0) / a.scale;
-    if (!a.renormalize && mult > 1e-20f && mult < 2.0f) {
+    // (no renormalisation, and neither p nor the weight, scale p, so small that
+    // it has lost bits), else by the largest logit and the sum over the row
+    float ref = __shfl_sync(kFull, l_j, 0);
+    const float w_0 = __shfl_sync(kFull, w, 0);
+    float mult = w_0 / a.scale;
+    if (!a.renormalize && mult > 1e-20f && mult < 2.0f && fabsf(w_0) >= FLT_MIN) {
 #pragma unroll
       for (int i = 0; i < 2 * PAIRS; ++i) s[i] = dense_exp<F32>(s[i] - ref) * mult;
     } else {

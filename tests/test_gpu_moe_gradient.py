@@ -47,3 +47,20 @@ def test_gradient_at_the_sum_floor(score, renorm):
     pe = np.take_along_axis(p, ix, 1)
     size = scale * np.abs(_f64(dw)).max(1) * (pe.max(1) / np.maximum(pe.sum(1), ref.SUM_FLOOR) if renorm else pe.max(1))
     assert np.all(np.abs(got - want) <= 4 * tol * size[:, None] + 1e-37)
+
+
+def test_gradient_of_weights_below_the_normal_range():
+    """A scale so small that the weights lose bits, dw as large: the scores come from the logits, not from the weights."""
+    T, E, k, scale = 16, 512, 4, 2.0 ** -140
+    g = torch.Generator(device="cuda").manual_seed(1)
+    logits = 0.3 * torch.randn(T, E, generator=g, device="cuda")
+    dw = 2.0 ** 100 * torch.randn(T, k, generator=g, device="cuda")
+    idx, w = B.moe_route(logits, k, renormalize=False, scale=scale)
+    got = _f64(B.moe_route_bwd(logits, idx, w, dw, renormalize=False, scale=scale))
+    ix = idx.cpu().numpy()
+    p, _ = ref.scores(_f64(logits), "softmax", F32_LOWEST)
+    want = gref.route_grad(p, ix, _f64(dw), "softmax", False, scale)
+    # scores: exp of arguments below 4, a sum of E / 32 + 5 additions, a quotient, products
+    tol = (4 + 2 * 2 + E / 32 + 5 + 8) * EPS
+    size = scale * np.abs(_f64(dw)).max(1) * np.take_along_axis(p, ix, 1).max(1)
+    assert np.all(np.abs(got - want) <= 4 * tol * size[:, None] + 1e-37)
