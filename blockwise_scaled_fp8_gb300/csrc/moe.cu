@@ -47,6 +47,7 @@ __device__ __forceinline__ float load_logit(const void* p, int f32, int64_t i) {
 }
 
 // The lowest finite value of the logits' type: it, -inf and NaN mask an expert.
+// Its negative is the largest, which +inf counts as.
 __device__ __forceinline__ float lowest_of(int f32) { return f32 ? -FLT_MAX : __uint_as_float(0xFF7F0000u); }
 
 }  // namespace
@@ -112,7 +113,7 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t at, int 
     for (int i = 0; i < N; ++i) l[i] = e0 + i < (int)a.E ? load_logit(a.logits, F32, at + e0 + i) : -INFINITY;
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) l[i] = l[i] > low ? fminf(l[i], FLT_MAX) : -INFINITY;  // NaN compares false
+  for (int i = 0; i < N; ++i) l[i] = l[i] > low ? fminf(l[i], -low) : -INFINITY;  // NaN compares false
 }
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
   }
   float p = 0.0f;
   if (my_e >= 0) {
-    const float l = fminf(load_logit(a.logits, F32, at + my_e), FLT_MAX);
+    const float l = fminf(load_logit(a.logits, F32, at + my_e), -lowest_of(F32));
     p = SIGMOID ? sigmoid(l) : expf(l - top) / sum;
   }
   const float total = a.renormalize ? fmaxf(warp_sum(p), kRouteSumFloor) : 1.0f;
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kRouteBwdThreads<PAIRS, SIGMOID>) moe_route_bw
   if (e_j >= E) e_j = -1;
   const float dw = e_j >= 0 ? __ldg(a.dw + t * a.k + lane) : 0.0f, w = e_j >= 0 ? __ldg(a.w + t * a.k + lane) : 0.0f;
   float l_j = e_j >= 0 ? load_logit(a.logits, F32, at + e_j) : -INFINITY;
-  l_j = l_j > low ? fminf(l_j, FLT_MAX) : -INFINITY;
+  l_j = l_j > low ? fminf(l_j, -low) : -INFINITY;
   float s[2 * PAIRS], p_j, dot = 0.0f;
   if constexpr (SIGMOID) {
     p_j = sigmoid(l_j);
@@ -383,8 +384,8 @@ __global__ void __launch_bounds__(kRouteBwdThreads<PAIRS, SIGMOID>) moe_route_bw
         if (e < E) l0 = load_logit(a.logits, F32, at + e);
         if (e + 1 < E) l1 = load_logit(a.logits, F32, at + e + 1);
       }
-      s[2 * i] = l0 > low ? fminf(l0, FLT_MAX) : -INFINITY;
-      s[2 * i + 1] = l1 > low ? fminf(l1, FLT_MAX) : -INFINITY;
+      s[2 * i] = l0 > low ? fminf(l0, -low) : -INFINITY;
+      s[2 * i + 1] = l1 > low ? fminf(l1, -low) : -INFINITY;
     }
     // p = exp(l - ref) * mult: by the first choice where its weight gives its p
     // (no renormalisation, and neither p nor the weight, scale p, so small that

@@ -1,0 +1,43 @@
+"""Values of the routed experts' operators at the edges of their types, and to
+the last bit where the method fixes it."""
+import pytest
+
+from gpu_util import torch
+
+import blockwise_scaled_fp8_gb300 as B
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    B.build()
+    yield
+    B.check_device_errors()
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ------------------------------------------------------------------ router
+
+@pytest.mark.parametrize("E", [8, 64, 300])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_route_infinity_counts_as_the_types_largest_value(E, dtype):
+    big = torch.finfo(dtype).max
+    logits = torch.zeros(3, E, dtype=dtype, device="cuda")
+    logits[0, 3], logits[0, 5] = float("inf"), big
+    logits[1, 2], logits[1, 6] = big, float("inf")
+    logits[2, 1] = logits[2, 4] = float("inf")
+    at = torch.tensor([[3, 5], [2, 6], [1, 4]], device="cuda")
+    idx, w = B.moe_route(logits, 2, renormalize=False)
+    assert torch.equal(idx.long(), at) and bool((w == 0.5).all())
+    dw = torch.tensor([[1.0, 3.0]], device="cuda").repeat(3, 1)
+    for renorm in (False, True):
+        idx, w = B.moe_route(logits, 2, renormalize=renorm)
+        dl = B.moe_route_bwd(logits, idx, w, dw, renormalize=renorm).float()
+        want = torch.zeros(3, E, device="cuda").scatter_(1, at, torch.tensor([[-0.5, 0.5]], device="cuda").repeat(3, 1))
+        assert torch.equal(dl, want)
