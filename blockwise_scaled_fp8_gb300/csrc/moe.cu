@@ -118,6 +118,17 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t at, int 
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
+// exp(x) of terms that are not compared.  Of bf16 logits by __expf, off by 2 ulp
+// and |x| 2^-24 (at most 2^-17 where the result is a normal number):
+//   - a softmax's denominator keeps it to 2^-21, since x exp(x) is at most 1 / e
+//     for x < 0 (a logit's own rounding moves it by up to 2^-9 of the logit);
+//   - the gradient's dense row is rounded to bf16, 2^-9.
+// Of fp32 logits by expf.
+template <bool F32>
+__device__ __forceinline__ float dense_exp(float x) {
+  return F32 ? expf(x) : __expf(x);
+}
+
 }  // namespace
 
 // One warp a token, lane l the VPL consecutive experts from l VPL on.  Scores
@@ -171,11 +182,10 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
         sum += gv[i];
       }
     } else {
-      // only their sum is used: __expf, off by 2 ulp and |x| 2^-24 of a term exp(x),
-      // keeps it to 2^-21 (x exp(x) is at most 1 / e for x < 0); masked: exp(-inf) = 0
+      // only their sum is used; masked: exp(-inf) = 0
       top = fmaxf(top, -FLT_MAX);  // finite where all are masked
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) sum += __expf(c[i] - top);
+      for (int i = 0; i < VPL; ++i) sum += dense_exp<F32>(c[i] - top);
     }
     sum = fmaxf(warp_sum(sum), FLT_MIN);
   }
@@ -319,14 +329,6 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
     a.idx[t * a.k + lane] = my_e;
     a.w[t * a.k + lane] = a.scale * (p / total);
   }
-}
-
-// exp(x), x <= 0, of the gradient's dense row: in bf16 by __expf, whose error (2
-// ulp and |x| 2^-24, at most 2^-17 where the result is a normal number) is far
-// below the output's rounding of 2^-9.
-template <bool F32>
-__device__ __forceinline__ float dense_exp(float x) {
-  return F32 ? expf(x) : __expf(x);
 }
 
 // The router's gradient.  With p the scores, S the sum of the chosen p and the

@@ -277,6 +277,8 @@ BFP8_API bfp8_status bfp8_gemm_grouped_1x128_128x1(const void *qa, int64_t lda, 
  *   whose experts are all masked is routed nowhere).
  *   w[t*k + j] = scale * p[idx] (0 at -1), with renormalize divided by
  *   max(sum of the token's chosen p, 1e-20).  The bias is not part of w.
+ *   Scores are within a few fp32 roundings; a softmax's denominator of bf16
+ *   logits (without bias or groups) is within 2^-20 of its value.
  * logits device bf16, or fp32 (logits_f32 != 0), row stride ldl >= E; bias
  * device fp32 [E] or NULL; idx device int32 [T,k], w device fp32 [T,k].
  */

@@ -41,3 +41,22 @@ def test_route_infinity_counts_as_the_types_largest_value(E, dtype):
         dl = B.moe_route_bwd(logits, idx, w, dw, renormalize=renorm).float()
         want = torch.zeros(3, E, device="cuda").scatter_(1, at, torch.tensor([[-0.5, 0.5]], device="cuda").repeat(3, 1))
         assert torch.equal(dl, want)
+
+
+@pytest.mark.parametrize("E", [32, 20, 128])
+def test_route_softmax_of_fp32_logits_by_the_full_exponential(E):
+    """Weights that are not renormalised, bit for bit: exp(l - max) / sum, the sum lane by lane and over the lanes in
+    pairs."""
+    g = _gen(E)
+    logits = 3 * torch.randn(2000, E, generator=g, device="cuda")
+    idx, w = B.moe_route(logits, 4, renormalize=False)
+    e = torch.exp(logits - logits.amax(1, keepdim=True))
+    lanes = torch.zeros(2000, -(-E // 32) * 32, device="cuda")
+    lanes[:, :E] = e
+    lanes = lanes.view(2000, 32, -1)
+    s = torch.zeros(2000, 32, device="cuda")
+    for i in range(lanes.shape[2]):
+        s = s + lanes[:, :, i]
+    for o in (16, 8, 4, 2, 1):
+        s = s + s[:, torch.arange(32, device="cuda") ^ o]
+    assert torch.equal(w, e.gather(1, idx.long()) / s[:, :1])
