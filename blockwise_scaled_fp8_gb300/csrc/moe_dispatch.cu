@@ -20,12 +20,12 @@
 //      one TMA store per output; a stage is free for the tile after the next
 //      as soon as its values are in registers.
 // What bounds it: 131072 routed rows x 4096 (16384 tokens, 64 experts, 8 each)
-// write 1.12 GB and read 0.18 (x nearly once) in 318 us with weights, 315
+// write 1.12 GB and read 0.18 (x nearly once) in 329 us with weights, 315
 // without; a plain fill of the same bytes takes 283 us on this memory, the
 // instructions of the two quantisations about 230.  Steps that led here:
 // gathering by cp.async from the quantising warps 675 us; by TMA from two warps
 // of their own, 16 columns a warp 349; the warps' barriers split into arrival
-// and wait 318.  (cp.async from the two gathering warps: 340 and 348, since the
+// and wait 318 (with one product a code; the quotient's codes take the 11 us).  (cp.async from the two gathering warps: 340 and 348, since the
 // copies share the quantisers' path to shared memory.)
 // The tiles are walked down the rows of a column block before the next block:
 // a token's rows (one per chosen expert) then read the same 256 bytes of it
@@ -117,7 +117,12 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // 1/s as hi + lo with lo >= 0: hi the hardware's approximation, two ulps down
 // where it is above 1/s, lo what it lacks.  RN(x hi + RN(x lo)) rounds to the
 // e4m3 code of the IEEE quotient x/s for every bf16 x with |x| <= 448 s, sign
-// of zero included (checked exhaustively on the CPU).
+// of zero included (checked exhaustively on the CPU).  Of products x = RN(x' w)
+// it is x/s to within 2^-43 before its rounding, so the quotient unless that
+// lies as near to halfway between two floats (no code differs in 6e9 products
+// checked on the CPU).  One product x hi would not do: with a weight that a
+// whole row shares, x/s is 448 x'/max|x'| but for roundings, which are often
+// within an ulp of a tie of the codes (1.3 in a thousand differ).
 __device__ __forceinline__ float2 recip_hi_lo(float s) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
@@ -377,9 +382,6 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
       }
       arrive(scales_ready);
       // ---------------------------------------------- codes
-      // Without weights x/s is RN(x hi + RN(x lo)), the IEEE quotient's code;
-      // with them RN(RN(x w) hi), within three roundings of the quotient (the
-      // product x w has no ties to keep).
       if constexpr (COL) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {  // columns 16 warp + 2q, + 1
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
           uint64_t cv[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            cv[i] = WEIGHTED ? f2_mul(x2[i][q], y.x) : f2_fma(x2[i][q], y.x, f2_mul(x2[i][q], y.y));
+            cv[i] = f2_fma(x2[i][q], y.x, f2_mul(x2[i][q], y.y));
           const uint32_t dst = outc + (uint32_t)((16 * warp + 2 * q) * 128 + 4 * lane);
           const uint32_t lo = cvt4(cv[0], cv[1]), hi = cvt4(cv[2], cv[3]);
           sts32(dst, __byte_perm(lo, hi, sel_e));
@@ -402,8 +404,8 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
         uint32_t rc[4];
 #pragma unroll
         for (int q = 0; q < 8; q += 2) {
-          const uint64_t a = WEIGHTED ? f2_mul(x2[i][q], hi) : f2_fma(x2[i][q], hi, f2_mul(x2[i][q], lo));
-          const uint64_t b = WEIGHTED ? f2_mul(x2[i][q + 1], hi) : f2_fma(x2[i][q + 1], hi, f2_mul(x2[i][q + 1], lo));
+          const uint64_t a = f2_fma(x2[i][q], hi, f2_mul(x2[i][q], lo));
+          const uint64_t b = f2_fma(x2[i][q + 1], hi, f2_mul(x2[i][q + 1], lo));
           rc[q >> 1] = cvt4(a, b);
         }
         const int r = 4 * lane + ((i + rot) & 3);

@@ -60,3 +60,39 @@ def test_route_softmax_of_fp32_logits_by_the_full_exponential(E):
     for o in (16, 8, 4, 2, 1):
         s = s + s[:, torch.arange(32, device="cuda") ^ o]
     assert torch.equal(w, e.gather(1, idx.long()) / s[:, :1])
+
+
+# ------------------------------------------------------------------ dispatch
+
+def _plan(g, T, k, E, align=128, empty=0.1):
+    idx = torch.argsort(torch.rand(T, E, generator=g, device="cuda"), dim=1)[:, :k].to(torch.int32)
+    idx[torch.rand(T, generator=g, device="cuda") < empty] = -1
+    return B.moe_plan(idx.contiguous(), E, align=align)
+
+
+def _codes(X):
+    """Codes and scales of the 1x128 groups of X [A, C], fp32, by IEEE quotients (C a multiple of 128)."""
+    v = X.view(X.shape[0], -1, 128)
+    amax = v.abs().amax(2)
+    s = amax.clamp_min(1e-12) / torch.full_like(amax, 448.0)
+    q = (v / s[:, :, None].expand_as(v)).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    return q.view(X.shape).view(torch.uint8), s.t()
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_dispatch_codes_are_those_of_the_quotient(weighted):
+    g = _gen(3)
+    T, k, E, K = 2048, 4, 16, 1024
+    plan = _plan(g, T, k, E)
+    x = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    w = torch.rand(T, k, generator=g, device="cuda") + 0.05 if weighted else None
+    q, s, qc, sc = B.moe_dispatch(x, plan, weight=w)
+    src = plan.src.long()
+    X = x.float()[src.clamp_min(0) // k]
+    if weighted:
+        X = X * w.reshape(-1)[src.clamp_min(0)][:, None]
+    X = torch.where((src >= 0)[:, None], X, torch.zeros((), device="cuda"))
+    R = src.numel()
+    for codes, scales, (want_q, want_s) in ((q[:, :K], s[:, :R], _codes(X)), (qc[:, :R], sc[:, :K], _codes(X.t().contiguous()))):
+        assert torch.equal(scales, want_s)
+        assert torch.equal(codes, want_q), f"{int((codes != want_q).sum())} of {codes.numel()} codes differ"
