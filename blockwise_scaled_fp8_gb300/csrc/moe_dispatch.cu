@@ -25,12 +25,15 @@
 // instructions of the two quantisations about 230.  Steps that led here:
 // gathering by cp.async from the quantising warps 675 us; by TMA from two warps
 // of their own, 16 columns a warp 349; the warps' barriers split into arrival
-// and wait 318 (with one product a code; the quotient's codes take the 11 us).  (cp.async from the two gathering warps: 340 and 348, since the
-// copies share the quantisers' path to shared memory.)
+// and wait 318 (with one product a code of weighted rows, whose quotients take
+// the other 11 us).  (cp.async from the two gathering warps: 340 and 348, since
+// the copies share the quantisers' path to shared memory.)
 // The tiles are walked down the rows of a column block before the next block:
 // a token's rows (one per chosen expert) then read the same 256 bytes of it
 // within a short time, from L2 after the first (16384 tokens x 4096, eight
 // experts each: 342 us at the time; four column blocks at once 348, all 32 of them 383).
+// A NaN's code is 0x7F, where the quantisation entries, which form the codes of
+// -x/s and turn their signs, give 0xFF (that way here: 327 us without weights).
 #include <cudaTypedefs.h>
 #include <string.h>
 

@@ -323,8 +323,10 @@ BFP8_API bfp8_status bfp8_moe_plan(const int32_t *idx, int64_t T, int64_t k, int
  *   q_col, s_col as bfp8_quant_rhs(X) (both NULL: not formed):
  *                q_col[c*ldq_col + r], s_col[(r/128)*lds_col + c].
  * Without weights the bytes and scales equal those of the quantisation entries
- * on the gathered tensor.  The forward dispatches x; the backward dispatches
- * dy with the routing weights, which is the gradient of the experts' outputs.
+ * on the gathered tensor, but for the sign bit of NaN codes (groups that hold
+ * an infinity, NaN values); with them X/s is formed to 2^-43 before it is
+ * rounded to a code.  The forward dispatches x; the backward dispatches dy with
+ * the routing weights, which is the gradient of the experts' outputs.
  *   x device bf16 [T,K], ldx >= K (16-byte aligned rows, ldx % 8 == 0, are
  *   copied asynchronously; others element by element); src device int32 [R];
  *   weight device fp32 [T*k] or NULL; codes 16-byte aligned with row strides

@@ -96,3 +96,24 @@ def test_dispatch_codes_are_those_of_the_quotient(weighted):
     for codes, scales, (want_q, want_s) in ((q[:, :K], s[:, :R], _codes(X)), (qc[:, :R], sc[:, :K], _codes(X.t().contiguous()))):
         assert torch.equal(scales, want_s)
         assert torch.equal(codes, want_q), f"{int((codes != want_q).sum())} of {codes.numel()} codes differ"
+
+
+def test_dispatch_of_values_that_are_not_finite():
+    """The same bytes as quantising the gathered rows, but for the sign of NaN codes, where a group holds infinities or
+    NaN."""
+    g = _gen(4)
+    T, k, E, K = 200, 2, 4, 384
+    plan = _plan(g, T, k, E)
+    x = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    x[3, 5], x[7, 130], x[9, 200], x[20, :128] = float("inf"), -float("inf"), float("nan"), float("nan")
+    x[30], x[40, ::2] = float("inf"), -float("nan")
+    src = plan.src.long()
+    xg = torch.where((src >= 0)[:, None], x[src.clamp_min(0) // k], torch.zeros((), dtype=x.dtype, device="cuda"))
+    for got, want in zip(B.moe_dispatch(x, plan), B.quant_dual(xg.contiguous())):
+        if got.dtype == torch.uint8:
+            n = K if got.shape[0] == src.numel() else src.numel()
+            a, b = (torch.where((t[:, :n] & 0x7F) == 0x7F, 0x7F, t[:, :n]) for t in (got, want))
+            assert torch.equal(a, b) and bool((a == 0x7F).any()) and not bool((a == 0x7F).all())
+        else:
+            a, b = got[:want.shape[0], :want.shape[1]], want
+            assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
