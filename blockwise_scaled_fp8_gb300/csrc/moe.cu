@@ -804,6 +804,9 @@ __global__ void __launch_bounds__(kCombineThreads, combine_dw_ctas(VEC)) moe_com
       __syncthreads();
     }
     const int i = WARP ? lane : tid;
+#pragma unroll
+    for (int u = 0; u < kCombineBatch; ++u)
+      if (i == u && r[u] < 0) sum = 0.0f;  // (dy may hold an infinity, times the zeros read for no row)
     if (i < kCombineBatch && t0 + i / KB < a.T && j0 + i % KB < a.k) a.dw[(t0 + i / KB) * a.k + j0 + i % KB] = sum;
   }
 }

@@ -117,3 +117,32 @@ def test_dispatch_of_values_that_are_not_finite():
         else:
             a, b = got[:want.shape[0], :want.shape[1]], want
             assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
+# ------------------------------------------------------------------ combine
+
+@pytest.mark.parametrize("N", [64, 1000, 4096])
+@pytest.mark.parametrize("k", [1, 2, 3, 6, 9])
+def test_combine_gradient_of_slots_without_a_row_is_zero(N, k):
+    """Whatever dy and the weight hold there."""
+    g = _gen(N + k)
+    T, E = 33, 12
+    idx = torch.argsort(torch.rand(T, E, generator=g, device="cuda"), dim=1)[:, :k].to(torch.int32)
+    idx[torch.rand(T, k, generator=g, device="cuda") < 0.3] = -1
+    idx[5] = idx[6] = idx[7] = -1
+    plan = B.moe_plan(idx.contiguous(), E, align=16)
+    ye, dy = (torch.randn(n, N, generator=g, device="cuda").bfloat16() for n in (plan.src.numel(), T))
+    dy[5], dy[6, 0], dy[8, 1] = float("inf"), float("nan"), -float("inf")
+    w = torch.randn(T, k, generator=g, device="cuda")
+    w[idx < 0] = float("nan")
+    none = plan.row < 0
+    y = B.moe_combine(ye, plan, w)
+    assert bool(y.isfinite().all()) and not y[5].any()
+    results = [B.moe_combine_bwd(dy, ye, plan, w, with_dye=d) for d in (True, False)]
+    for dye, dw in results:
+        assert not dw[none].any()
+        assert not dw[none].isnan().any()
+        if dye is not None:
+            assert not dye[plan.src < 0].any()
+    a, b = results[0][1], results[1][1]
+    assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
