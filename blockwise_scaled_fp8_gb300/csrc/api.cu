@@ -738,6 +738,7 @@ bfp8_status bfp8_check_device_errors(bfp8_stream_t stream) {
   if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: read flag");
   if (qbits) return fail(BFP8_ERR_TIMEOUT, "quantisation kernel gave up waiting for its TMA tile loads");
   if (dbits) return fail(BFP8_ERR_TIMEOUT, "dispatch kernel gave up waiting for its gathered rows");
+  if (rbits & kRoutedOffsets) return fail(BFP8_ERR_INVALID_ARG, "routed product: expert offsets decreasing");
   if (rbits) return fail(BFP8_ERR_TIMEOUT, "routed product gave up waiting for its weights");
   if (bits & 64u)  // kErrGroupOffsets
     return fail(BFP8_ERR_INVALID_ARG,

@@ -243,6 +243,7 @@ struct GemmRoutedArgs {
   int64_t ldc, R, N, K;
 };
 cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_t st, const char** msg);
+constexpr uint32_t kRoutedOffsets = 32u;  // error bit: decreasing offsets (the others: a wait that gave up)
 cudaError_t routed_read_errors(uint32_t* out);  // reads and clears the kernel's error word (synchronous)
 
 // Reads and clears the device error word of the GEMM kernels (synchronous).

@@ -154,12 +154,19 @@ __global__ void __launch_bounds__(RpCfg<R>::kThreads, 1)
   pdl_wait();
   // the experts that hold rows, in order, and the walks (of R rows) before each
   int reached = 0, walks = 0;
+  constexpr int kFell = 1 << 16;  // added to the count for a warp whose experts' offsets decrease
   for (int e0 = 0; e0 < E; e0 += Cfg::kThreads) {
     const int e = e0 + tid;
     int64_t rows = 0;
-    if (e < E) rows = min((int64_t)__ldg(a.offs + e + 1), a.R) - max(__ldg(a.offs + e), 0);
+    bool falls = false;
+    if (e < E) {
+      const int o0 = __ldg(a.offs + e), o1 = __ldg(a.offs + e + 1);
+      rows = min((int64_t)o1, a.R) - max(o0, 0);
+      falls = o1 < o0;
+    }
     const int mine = rows > 0 ? (int)((rows + R - 1) / R) : 0;
     const uint32_t vote = __ballot_sync(kAll, mine > 0);
+    const int fell = __any_sync(kAll, falls) ? kFell : 0;
     int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(RpCfg<R>::kThreads, 1)
       if (lane >= o) inc += v;
     }
     if (lane == 31) {
-      s_count[warp] = __popc(vote);
+      s_count[warp] = __popc(vote) + fell;
       s_count[kWarps + warp] = inc;
     }
     __syncthreads();
@@ -179,11 +186,16 @@ __global__ void __launch_bounds__(RpCfg<R>::kThreads, 1)
       walks += s_count[kWarps + w];
     }
     if (mine > 0) {
-      at += __popc(vote & ((1u << lane) - 1u));
+      at = (at & (kFell - 1)) + __popc(vote & ((1u << lane) - 1u));
       s_expert[at] = e;
       s_walk[at] = before + inc - mine;
     }
     __syncthreads();
+  }
+  if (reached >= kFell) {
+    // decreasing offsets are no plan's: experts may overlap, and their walks pass the launcher's bound
+    reached = walks = 0;
+    if (blockIdx.x == 0 && tid == 0) atomicOr(&g_routed_error, kRoutedOffsets);
   }
   if (tid == 0) s_walk[reached] = walks;
   tc_fence_before();
@@ -215,7 +227,6 @@ __global__ void __launch_bounds__(RpCfg<R>::kThreads, 1)
     w.block = per == 1 ? in : in / per;
     w.m0 = max(__ldg(a.offs + w.e), 0) + (int64_t)(in - w.block * per) * R;
     w.r1 = min((int64_t)__ldg(a.offs + w.e + 1), a.R);
-    if (w.m0 < 0) w.m0 = w.r1 = 0;  // (offsets of overlapping experts can overflow the count of walks)
   };
   auto next = [&](Walk& w) {
     if (++w.x < last) enter(w);

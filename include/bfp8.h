@@ -373,7 +373,9 @@ BFP8_API bfp8_status bfp8_moe_combine_bwd(const void *dy, int64_t lddy, const vo
  *   offs device int32 [E+1], src device int32 [R] (a plan's);
  *   c  device bf16 [R, ldc], ldc >= N.  Padding rows inside an expert's range
  *      get zeros; rows outside [offs[0], offs[E]) are not written.
- * K == 0 gives zeros.  Offsets outside [0, R] are clamped.
+ * K == 0 gives zeros.  Offsets outside [0, R] are clamped; where offsets
+ * decrease nothing is written, and bfp8_check_device_errors reports
+ * BFP8_ERR_INVALID_ARG.
  */
 BFP8_API bfp8_status bfp8_gemm_routed_1x128_128x128(const void *qa, int64_t lda, const float *sa, int64_t ldsa,
                                                     int64_t T, const void *qb, int64_t ldb, const float *sb,
