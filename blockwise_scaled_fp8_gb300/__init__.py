@@ -736,7 +736,10 @@ def moe_experts_bwd(dy, saved):
 def moe_experts_decode(x, qw, sw, plan: MoePlan, weight, N: int):
     """Routed experts for a few tokens (serving): y [T, N] from x [T, K] bf16 and
     the experts' weights quantised once, (qw, _, sw) = quant_weight(w.reshape(
-    E * N, K)); the plan's align is 1."""
+    E * N, K)); the plan's align is 1.  N % 128 == 0 unless there is one expert,
+    so that the stacked weight's tiles stay inside an expert."""
+    if N % BLOCK and plan.offs.numel() > 2:
+        raise ValueError("moe_experts_decode: the experts' output features must be a multiple of 128")
     q, s = quant_lhs(x)
     return moe_combine(gemm_routed_1x128_128x128(q, s, qw, sw, plan, N, x.shape[1]), plan, weight)
 
