@@ -709,6 +709,8 @@ def moe_experts_fwd(x, w, plan: MoePlan, weight):
         raise ValueError("moe_experts_fwd: the experts' output features must be a multiple of 128")
     if plan.offs.numel() != E + 1:
         raise ValueError(f"moe_experts_fwd: the plan has {plan.offs.numel() - 1} experts, w {E}")
+    if x.shape[1] != K:
+        raise ValueError(f"moe_experts_fwd: w is {tuple(w.shape)}, x has {x.shape[1]} features")
     if plan.src.numel() % BLOCK:
         raise ValueError(f"moe_experts_fwd: the plan's rows must start on multiples of {BLOCK} (moe_plan's align)")
     qx, sx, qxt, sxt = moe_dispatch(x, plan)
@@ -740,8 +742,11 @@ def moe_experts_decode(x, qw, sw, plan: MoePlan, weight, N: int):
     so that the stacked weight's tiles stay inside an expert."""
     if N % BLOCK and plan.offs.numel() > 2:
         raise ValueError("moe_experts_decode: the experts' output features must be a multiple of 128")
+    K = x.shape[1]
+    if qw.shape[1] != _rup(K, 16) and sw.shape[1] != _cdiv(K, BLOCK):  # (either may be a padded buffer)
+        raise ValueError(f"moe_experts_decode: qw is {tuple(qw.shape)}, sw {tuple(sw.shape)}, x has {K} features")
     q, s = quant_lhs(x)
-    return moe_combine(gemm_routed_1x128_128x128(q, s, qw, sw, plan, N, x.shape[1]), plan, weight)
+    return moe_combine(gemm_routed_1x128_128x128(q, s, qw, sw, plan, N, K), plan, weight)
 
 
 # ---------------------------------------------------------------------------

@@ -29,3 +29,26 @@ def test_decoding_refuses_tiles_that_straddle_experts(E, N):
     qw, sw = _quantised(E, N, 256)
     with pytest.raises(ValueError, match="multiple of 128"):
         B.moe_experts_decode(torch.zeros(4, 256, dtype=torch.bfloat16), qw, sw, _plan(4, 2, E, 1), torch.zeros(4, 2), N)
+
+
+@pytest.mark.parametrize("columns", [120, 250, 304])
+def test_training_forward_refuses_another_width_of_tokens(columns):
+    """Fewer columns than the weights' (their codes' padding would be read) and more."""
+    w = torch.zeros(4, 128, 256 if columns > 128 else 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match=f"x has {columns} features"):
+        B.moe_experts_fwd(torch.zeros(8, columns, dtype=torch.bfloat16), w, _plan(8, 2, 4, 128), torch.zeros(8, 2))
+
+
+@pytest.mark.parametrize("columns,K", [(128, 256), (256, 512), (300, 256), (1024, 896)])
+def test_decoding_refuses_another_width_of_tokens(columns, K):
+    qw, sw = _quantised(4, 128, K)
+    with pytest.raises(ValueError, match=f"x has {columns} features"):
+        B.moe_experts_decode(torch.zeros(8, columns, dtype=torch.bfloat16), qw, sw, _plan(8, 2, 4, 1), torch.zeros(8, 2), 128)
+
+
+def test_decoding_takes_padded_codes_or_scales():
+    """Row strides beyond the weight's width are no other width: these fail at the tensors' device only."""
+    qw, sw = _quantised(4, 128, 200)
+    for q, s in ((torch.zeros(512, 256, dtype=torch.uint8), sw), (qw, torch.zeros(4, 5))):
+        with pytest.raises(ValueError, match="x must be"):
+            B.moe_experts_decode(torch.zeros(8, 200, dtype=torch.bfloat16), q, s, _plan(8, 2, 4, 1), torch.zeros(8, 2), 128)
