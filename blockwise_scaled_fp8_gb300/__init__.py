@@ -669,16 +669,20 @@ def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gat
     offs, E = _need_plan_offs(plan)
     tokens = plan.row.shape[0]
     k, R = _need_plan(plan, tokens)
-    T = qa.shape[0]
+    (T, na), (rows_b, nb), (rows_sa, nsa), (rows_sb, nsb) = qa.shape, qb.shape, sa.shape, sb.shape
+    Kb, Nb = (K + BLOCK - 1) // BLOCK, (N + BLOCK - 1) // BLOCK
     u8, f8, f32 = torch.uint8, torch.float8_e4m3fn, torch.float32
     if not (qa.dtype in (u8, f8) and qb.dtype in (u8, f8) and sa.dtype is f32 and sb.dtype is f32 and qa.is_cuda and
             qb.is_cuda and sa.is_cuda and sb.is_cuda):
         raise ValueError("qa, qb must be CUDA uint8 or float8_e4m3fn codes and sa, sb CUDA float32 scales")
     if T != (tokens if gathered else R):
         raise ValueError(f"qa has {T} rows, the plan {tokens if gathered else R}")
-    if qb.shape[0] != E * N or sb.shape[0] < E * _cdiv(N, BLOCK) or sa.shape[0] < _cdiv(K, BLOCK):
-        raise ValueError(f"{E} experts of {N} x {K} need qb, sb, sa of {E * N}, {E * _cdiv(N, BLOCK)}, {_cdiv(K, BLOCK)} "
-                         f"rows, got {qb.shape[0]}, {sb.shape[0]}, {sa.shape[0]}")
+    if rows_b != E * N or rows_sb < E * Nb or rows_sa < Kb:
+        raise ValueError(f"{E} experts of {N} x {K} need qb, sb, sa of {E * N}, {E * Nb}, {Kb} rows, got {rows_b}, "
+                         f"{rows_sb}, {rows_sa}")
+    if na < K or nb < K or nsa < T or nsb < Kb:
+        raise ValueError(f"{T} rows and {K} features need qa, qb, sa, sb of {K}, {K}, {T}, {Kb} columns, got {na}, {nb}, "
+                         f"{nsa}, {nsb}")
     if qa.stride(1) != 1 or qb.stride(1) != 1 or (sa.stride(1) != 1 and T > 1) or (sb.stride(1) != 1 and K > BLOCK):
         raise ValueError("qa, sa, qb and sb must have unit column strides")
     ldc = N
@@ -689,8 +693,11 @@ def gemm_routed_1x128_128x128(qa, sa, qb, sb, plan: MoePlan, N: int, K: int, gat
         if out.shape[0] < R or out.shape[1] < N:
             raise ValueError(f"out must hold {(R, N)}, got {tuple(out.shape)}")
         ldc = _ld(out)
-    st = lib().bfp8_gemm_routed_1x128_128x128(qa.data_ptr(), _ld(qa), sa.data_ptr(), _ld(sa), T, qb.data_ptr(),
-                                              _ld(qb), sb.data_ptr(), _ld(sb), offs.data_ptr(), E,
+    # row strides as _ld's
+    st = lib().bfp8_gemm_routed_1x128_128x128(qa.data_ptr(), qa.stride(0) if T > 1 else na, sa.data_ptr(),
+                                              sa.stride(0) if rows_sa > 1 else nsa, T, qb.data_ptr(),
+                                              qb.stride(0) if rows_b > 1 else nb, sb.data_ptr(),
+                                              sb.stride(0) if rows_sb > 1 else nsb, offs.data_ptr(), E,
                                               plan.src.data_ptr() if gathered else None, k, out.data_ptr(), ldc, R, N, K,
                                               _stream())
     if st:

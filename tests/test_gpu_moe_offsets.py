@@ -45,3 +45,16 @@ def test_routed_product_refuses_decreasing_offsets(R, N, K, offs):
     want = B.gemm_routed_1x128_128x128(qa, sa, qb, sb, plan._replace(offs=whole), N, K)
     assert torch.equal(out, want)
     assert bool((flat[:R * N] == 0x7FC1).all()) and bool((flat[2 * R * N:] == 0x7FC1).all())
+
+
+def test_routed_product_refuses_operands_narrower_than_the_product():
+    """Views whose rows lie far enough apart but do not hold the columns: they would be read beyond their width."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    plan = B.MoePlan(torch.tensor([0, 4, 8, 8], dtype=torch.int32, device="cuda"), i(4, 2), i(8), i(3))
+    e8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
+    f = lambda *s: torch.zeros(s, device="cuda")
+    ok = dict(qa=e8(4, 256), sa=f(2, 4), qb=e8(3 * 8, 256), sb=f(3, 2), plan=plan, N=8, K=256)
+    B.gemm_routed_1x128_128x128(**ok)
+    for bad in (dict(qa=e8(4, 256)[:, :240]), dict(qb=e8(24, 256)[:, :128]), dict(sa=f(2, 8)[:, :3]), dict(sb=f(3, 4)[:, :1])):
+        with pytest.raises(ValueError, match="columns"):
+            B.gemm_routed_1x128_128x128(**{**ok, **bad})
