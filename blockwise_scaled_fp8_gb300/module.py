@@ -142,7 +142,7 @@ class Float8RoutedExperts(torch.nn.Module):
         for w in self.weight:
             torch.nn.init.kaiming_uniform_(w, a=5 ** 0.5)
         self.register_buffer("choice_bias", torch.zeros(experts, device=device) if choice_bias else None)
-        self._codes = None
+        self._codes = self._codes_of = None
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor):
         lead = x.shape[:-1]
@@ -150,16 +150,25 @@ class Float8RoutedExperts(torch.nn.Module):
                                           logits.reshape(-1, self.experts), self.k, bias=self.choice_bias, **self.route)
         return y.reshape(*lead, self.out_features), counts
 
+    def _weight_state(self):
+        """What changes with the weights: their storage, and torch's count of writes in place."""
+        w = self.weight
+        return w.data_ptr(), w.device, None if w.is_inference() else w._version
+
     @torch.no_grad()
     def quantize(self) -> None:
-        """Quantises the experts' weights for decode(); call it again after they change."""
+        """Quantises the experts' weights for decode(); call it again after they change (decode() refuses codes of
+        weights that were replaced, moved or written since; writes through weight.data or in inference mode leave no
+        trace that it could see).  The codes are not part of the layer's state."""
         qw, _, sw = quant_weight(self.weight.reshape(self.experts * self.out_features, self.in_features))
-        self._codes = (qw, sw)
+        self._codes, self._codes_of = (qw, sw), self._weight_state()
 
     @torch.no_grad()
     def decode(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         if self._codes is None:
             raise RuntimeError("Float8RoutedExperts.decode: call quantize() first")
+        if self._codes_of != self._weight_state():
+            raise RuntimeError("Float8RoutedExperts.decode: the weights have changed since quantize(); call it again")
         lead = x.shape[:-1]
         logits, x = logits.reshape(-1, self.experts).contiguous(), x.reshape(-1, self.in_features).contiguous()
         idx, w = moe_route(logits, self.k, bias=self.choice_bias, **self.route)

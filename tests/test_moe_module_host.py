@@ -1,0 +1,55 @@
+"""Host logic of the routed layer (no GPU: the kernels' entries are stood in for)."""
+import copy
+
+import pytest
+import torch
+
+from blockwise_scaled_fp8_gb300 import module as M
+
+
+@pytest.fixture
+def layer(monkeypatch):
+    """A layer on the CPU whose decode() gives the sum of the weights that were quantised."""
+    monkeypatch.setattr(M, "quant_weight", lambda w: (w.detach().float().sum(), None, None))
+    monkeypatch.setattr(M, "moe_route", lambda logits, k, **_: (None, None))
+    monkeypatch.setattr(M, "moe_plan", lambda *_, **__: None)
+    monkeypatch.setattr(M, "moe_experts_decode", lambda x, qw, sw, plan, w, N: qw.expand(x.shape[0], N))
+    return M.Float8RoutedExperts(16, 128, 4, 2)
+
+
+def _decode(layer):
+    return float(layer.decode(torch.zeros(1, 16, dtype=torch.bfloat16), torch.zeros(1, 4))[0, 0])
+
+
+def test_decode_refuses_codes_of_other_weights(layer):
+    with pytest.raises(RuntimeError, match="quantize"):
+        _decode(layer)
+
+    def step():
+        opt = torch.optim.SGD(layer.parameters(), lr=1.0)
+        layer.weight.grad = torch.ones_like(layer.weight)
+        opt.step()
+
+    def swap():
+        layer.weight = torch.nn.Parameter(layer.weight.detach() + 1)
+
+    def data():
+        layer.weight.data = layer.weight.data.clone()
+
+    state = copy.deepcopy(layer.state_dict())
+    for change in (step, lambda: layer.load_state_dict(state), lambda: layer.to(torch.float32).to(torch.bfloat16), swap, data,
+                   lambda: torch.nn.init.ones_(layer.weight)):
+        layer.quantize()
+        assert _decode(layer) == float(layer.weight.detach().float().sum())
+        change()
+        with pytest.raises(RuntimeError, match="changed since quantize"):
+            _decode(layer)
+
+
+def test_decode_keeps_codes_of_unchanged_weights(layer):
+    layer.quantize()
+    want = _decode(layer)
+    layer.eval().train().requires_grad_(False)
+    layer.to(torch.device("cpu"))
+    layer.weight.grad = None
+    assert _decode(layer) == want
