@@ -98,6 +98,7 @@ class _BlockwiseFp8Experts(torch.autograd.Function):
         return y, plan.counts
 
     @staticmethod
+    @torch.autograd.function.once_differentiable  # the kernels' gradients carry no graph
     def backward(ctx, dy, _):
         qxt, sxt, qwt, sw, ye, offs, row, src, counts, w, logits, idx = ctx.saved_tensors
         plan = MoePlan(offs, row, src, counts)

@@ -53,3 +53,33 @@ def test_decode_keeps_codes_of_unchanged_weights(layer):
     layer.to(torch.device("cpu"))
     layer.weight.grad = None
     assert _decode(layer) == want
+
+
+@pytest.fixture
+def experts(monkeypatch):
+    """blockwise_fp8_experts on the CPU whose entries compute y = 2 x and dx = 2 dy."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    monkeypatch.setattr(M, "moe_route", lambda logits, k, **_: (i(logits.shape[0], k), torch.zeros(logits.shape[0], k)))
+    monkeypatch.setattr(M, "moe_plan", lambda idx, E: M.MoePlan(i(E + 1), idx, i(128), i(E)))
+    monkeypatch.setattr(M, "moe_experts_fwd", lambda x, w, plan, wt: (2 * x, (x, x, x, x, x, plan, wt)))
+    monkeypatch.setattr(M, "moe_experts_bwd", lambda dy, saved: (2 * dy.detach(), torch.zeros(4, 128, 128), saved[-1]))
+    monkeypatch.setattr(M, "moe_route_bwd", lambda logits, *_, **__: torch.zeros_like(logits))
+    return M.blockwise_fp8_experts
+
+
+def test_a_second_derivative_is_refused(experts):
+    """The kernels' gradients have none: without a refusal its terms would be left out of the sum."""
+    x = torch.randn(3, 128).bfloat16().requires_grad_()
+    w = torch.zeros(4, 128, 128, dtype=torch.bfloat16, requires_grad=True)
+    y, _ = experts(x, w, torch.zeros(3, 4, requires_grad=True), 2)
+    (g,) = torch.autograd.grad(y.float().square().sum() + x.float().pow(3).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="twice"):
+        g.float().sum().backward()
+
+
+def test_a_first_derivative_with_its_graph_is_served(experts):
+    x = torch.ones(3, 128).bfloat16().requires_grad_()
+    w = torch.zeros(4, 128, 128, dtype=torch.bfloat16, requires_grad=True)
+    y, _ = experts(x, w, torch.zeros(3, 4, requires_grad=True), 2)
+    (g,) = torch.autograd.grad(y.float().sum(), x, create_graph=True)
+    assert bool((g == 2).all())
