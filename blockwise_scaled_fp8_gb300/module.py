@@ -92,7 +92,8 @@ class _BlockwiseFp8Experts(torch.autograd.Function):
         plan = moe_plan(idx, weight.shape[0])
         y, saved = moe_experts_fwd(x, weight, plan, w)
         qxt, sxt, qwt, sw, ye, plan, w = saved
-        ctx.save_for_backward(qxt, sxt, qwt, sw, ye, *plan, w, logits, idx)
+        # (not the counts: they are the caller's to write, and the gradients do without)
+        ctx.save_for_backward(qxt, sxt, qwt, sw, ye, plan.offs, plan.row, plan.src, w, logits, idx)
         ctx.how = how
         ctx.mark_non_differentiable(plan.counts)
         return y, plan.counts
@@ -100,8 +101,8 @@ class _BlockwiseFp8Experts(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable  # the kernels' gradients carry no graph
     def backward(ctx, dy, _):
-        qxt, sxt, qwt, sw, ye, offs, row, src, counts, w, logits, idx = ctx.saved_tensors
-        plan = MoePlan(offs, row, src, counts)
+        qxt, sxt, qwt, sw, ye, offs, row, src, w, logits, idx = ctx.saved_tensors
+        plan = MoePlan(offs, row, src, None)
         dx, dw, dweight = moe_experts_bwd(dy.to(torch.bfloat16).contiguous(), (qxt, sxt, qwt, sw, ye, plan, w))
         dlogits = moe_route_bwd(logits, idx, w, dweight, **ctx.how) if ctx.needs_input_grad[2] else None
         return dx, dw, dlogits, None, None, None

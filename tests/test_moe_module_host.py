@@ -83,3 +83,13 @@ def test_a_first_derivative_with_its_graph_is_served(experts):
     y, _ = experts(x, w, torch.zeros(3, 4, requires_grad=True), 2)
     (g,) = torch.autograd.grad(y.float().sum(), x, create_graph=True)
     assert bool((g == 2).all())
+
+
+def test_the_returned_counts_may_be_written(experts):
+    """Summed over processes in place, say, before the backward pass."""
+    x = torch.ones(3, 128).bfloat16().requires_grad_()
+    w = torch.zeros(4, 128, 128, dtype=torch.bfloat16, requires_grad=True)
+    y, counts = experts(x, w, torch.zeros(3, 4, requires_grad=True), 2)
+    counts.add_(1)
+    y.float().sum().backward()
+    assert bool((x.grad == 2).all())
