@@ -1824,7 +1824,11 @@ __global__ void __launch_bounds__(WxqCfg::kThreads, 1)
                        : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
                        : "r"(box + (uint32_t)((8 * g + ph) * 128) + (uint32_t)((jb ^ ph) << 4)));
         }
-        // the values are in registers: the raw slot can be refilled
+        // The raw slot can be refilled once the values are in registers.  The
+        // fence orders these reads before the refill, which TMA writes through
+        // the other proxy; without it the last reads in flight got tokens of
+        // K-block it + kRawSlots in 3 of 100 calls (4096 x 4096 over 8192 tokens).
+        fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(rempty_bar(r));
         // |x| maxima of the 8 features (packed bf16 pairs) over the 128 tokens
