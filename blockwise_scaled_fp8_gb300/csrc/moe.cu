@@ -804,10 +804,11 @@ __global__ void __launch_bounds__(kCombineThreads, combine_dw_ctas(VEC)) moe_com
       __syncthreads();
     }
     const int i = WARP ? lane : tid;
-#pragma unroll
-    for (int u = 0; u < kCombineBatch; ++u)
-      if (i == u && r[u] < 0) sum = 0.0f;  // (dy may hold an infinity, times the zeros read for no row)
-    if (i < kCombineBatch && t0 + i / KB < a.T && j0 + i % KB < a.k) a.dw[(t0 + i / KB) * a.k + j0 + i % KB] = sum;
+    if (i < kCombineBatch && t0 + i / KB < a.T && j0 + i % KB < a.k) {
+      const int64_t slot = (t0 + i / KB) * a.k + j0 + i % KB;
+      const int row = __ldg(a.row + slot);
+      a.dw[slot] = row >= 0 && row < a.R ? sum : 0.0f;  // (dy may hold an infinity, times the zeros read for no row)
+    }
   }
 }
 
