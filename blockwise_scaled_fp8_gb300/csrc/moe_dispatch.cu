@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(kDsThreads, kDsCtasPerSm)
         __syncwarp();
       }
       if (!wait(rows_ready, phase)) break;
-      if (lane == 0) mbar_arrive(empty0 + 8 * s);  // the stage is in registers
+      // the stage is in registers: the row maxima, stored before the wait above, were formed from every value read
+      if (lane == 0) mbar_arrive(empty0 + 8 * s);
 
       // ---------------------------------------------- row scales: two threads a row
       {

@@ -262,10 +262,11 @@ BFP8_API bfp8_status bfp8_gemm_grouped_1x128_128x1(const void *qa, int64_t lda, 
 
 /*
  * Router: each token's k experts and their weights, from logits [T,E].
- *   p = softmax over the token's eligible experts, or sigmoid, in fp32.
- *   An expert is eligible where its logit is above the lowest finite value of
- *   the logits' type (that value, -inf and NaN mask it; +inf counts as the
- *   largest finite value) and its bias is above -inf.
+ *   p = softmax over the token's experts that are not masked, or sigmoid, in fp32.
+ *   An expert is masked where its logit is -inf, NaN or the lowest finite value
+ *   of the logits' type (+inf counts as the largest), and eligible where it is
+ *   not masked and its bias is above -inf (a bias joins the choice alone: the
+ *   softmax still counts an expert that its bias switches off).
  *   c = p + bias[e]; without a bias c = p, which a softmax compares by the
  *   logits (the same order, with no rounding between equal candidates).
  *   groups > 1: the experts are groups of E / groups consecutive ones; a
@@ -291,7 +292,8 @@ BFP8_API bfp8_status bfp8_moe_route(const void *logits, int logits_f32, int64_t 
  * The router's gradient: dlogits [T,E] (the logits' type, row stride ldd >= E,
  * every element written) from dw [T,k] fp32, given the forward's logits, idx,
  * w, score, renormalize and scale.  The choice itself has no gradient, nor has
- * the bias.
+ * the bias.  Where renormalised weights have the floor of 1e-20 as their
+ * denominator it is a constant.
  */
 BFP8_API bfp8_status bfp8_moe_route_bwd(const void *logits, int logits_f32, int64_t T, int64_t E, int64_t ldl,
                                         const int32_t *idx, const float *w, const float *dw, int64_t k, int score,
@@ -372,7 +374,8 @@ BFP8_API bfp8_status bfp8_moe_combine_bwd(const void *dy, int64_t lddy, const vo
  *   qb, sb the experts' stacked weights, as the grouped forward's;
  *   offs device int32 [E+1], src device int32 [R] (a plan's);
  *   c  device bf16 [R, ldc], ldc >= N.  Padding rows inside an expert's range
- *      get zeros; rows outside [offs[0], offs[E]) are not written.
+ *      get zeros (NaN where the expert's codes or scales are not finite); rows
+ *      outside [offs[0], offs[E]) are not written.
  * K == 0 gives zeros.  Offsets outside [0, R] are clamped; where offsets
  * decrease nothing is written, and bfp8_check_device_errors reports
  * BFP8_ERR_INVALID_ARG.
