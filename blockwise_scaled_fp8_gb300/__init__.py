@@ -718,7 +718,8 @@ def moe_experts_fwd(x, w, plan: MoePlan, weight):
         raise ValueError(f"moe_experts_fwd: the plan has {plan.offs.numel() - 1} experts, w {E}")
     if x.shape[1] != K:
         raise ValueError(f"moe_experts_fwd: w is {tuple(w.shape)}, x has {x.shape[1]} features")
-    if plan.src.numel() % BLOCK:
+    R = plan.src.numel()  # (fewer rows than any choice needs with align 128: a plan of a smaller one)
+    if R % BLOCK or R < moe_plan_rows(*plan.row.shape, E):
         raise ValueError(f"moe_experts_fwd: the plan's rows must start on multiples of {BLOCK} (moe_plan's align)")
     qx, sx, qxt, sxt = moe_dispatch(x, plan)
     qw, qwt, sw = quant_weight(w.reshape(E * N, K), with_t=True)

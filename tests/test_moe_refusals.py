@@ -52,3 +52,19 @@ def test_decoding_takes_padded_codes_or_scales():
     for q, s in ((torch.zeros(512, 256, dtype=torch.uint8), sw), (qw, torch.zeros(4, 5))):
         with pytest.raises(ValueError, match="x must be"):
             B.moe_experts_decode(torch.zeros(8, 200, dtype=torch.bfloat16), q, s, _plan(8, 2, 4, 1), torch.zeros(8, 2), 128)
+
+
+@pytest.mark.parametrize("T,k,E,align", [(64, 2, 8, 1), (256, 4, 8, 1), (128, 1, 2, 64), (130, 3, 16, 32), (512, 2, 4, 8)])
+def test_training_forward_refuses_plans_whose_experts_start_off_a_block(T, k, E, align):
+    """Also where the rows in all happen to be a multiple of 128."""
+    w = torch.zeros(E, 128, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="multiples of 128"):
+        B.moe_experts_fwd(torch.zeros(T, 128, dtype=torch.bfloat16), w, _plan(T, k, E, align), torch.zeros(T, k))
+
+
+@pytest.mark.parametrize("T,k,E,align", [(64, 2, 8, 128), (1, 1, 1, 128), (300, 2, 4, 256), (128, 1, 1, 1), (3, 2, 1024, 128)])
+def test_training_forward_takes_every_plan_on_blocks(T, k, E, align):
+    """One expert starts on a block whatever the alignment; these fail at the tensors' device only."""
+    w = torch.zeros(E, 128, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="x must be"):
+        B.moe_experts_fwd(torch.zeros(T, 128, dtype=torch.bfloat16), w, _plan(T, k, E, align), torch.zeros(T, k))
