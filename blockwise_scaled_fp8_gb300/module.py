@@ -149,8 +149,12 @@ class Float8RoutedExperts(torch.nn.Module):
     def forward(self, x: torch.Tensor, logits: torch.Tensor):
         lead = x.shape[:-1]
         y, counts = blockwise_fp8_experts(x.reshape(-1, self.in_features), self.weight,
-                                          logits.reshape(-1, self.experts), self.k, bias=self.choice_bias, **self.route)
+                                          logits.reshape(-1, self.experts), self.k, bias=self._bias(), **self.route)
         return y.reshape(*lead, self.out_features), counts
+
+    def _bias(self):
+        """The choice bias in the router's fp32 (a cast of the whole model casts the buffer)."""
+        return None if self.choice_bias is None else self.choice_bias.float()
 
     def _weight_state(self):
         """What changes with the weights: their storage, and torch's count of writes in place."""
@@ -173,7 +177,7 @@ class Float8RoutedExperts(torch.nn.Module):
             raise RuntimeError("Float8RoutedExperts.decode: the weights have changed since quantize(); call it again")
         lead = x.shape[:-1]
         logits, x = logits.reshape(-1, self.experts).contiguous(), x.reshape(-1, self.in_features).contiguous()
-        idx, w = moe_route(logits, self.k, bias=self.choice_bias, **self.route)
+        idx, w = moe_route(logits, self.k, bias=self._bias(), **self.route)
         y = moe_experts_decode(x, *self._codes, moe_plan(idx, self.experts, align=1), w,
                                self.out_features)
         return y.reshape(*lead, self.out_features)

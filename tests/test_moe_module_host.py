@@ -93,3 +93,22 @@ def test_the_returned_counts_may_be_written(experts):
     counts.add_(1)
     y.float().sum().backward()
     assert bool((x.grad == 2).all())
+
+
+def test_choice_bias_joins_in_fp32_after_the_layer_is_cast(monkeypatch):
+    """Casting a whole model to bf16 casts the buffer too."""
+    seen = []
+    monkeypatch.setattr(M, "moe_route", lambda logits, k, bias=None, **_: seen.append(bias) or (None, None))
+    monkeypatch.setattr(M, "moe_plan", lambda *_, **__: None)
+    monkeypatch.setattr(M, "quant_weight", lambda w: (w, None, w))
+    monkeypatch.setattr(M, "moe_experts_decode", lambda x, qw, sw, plan, w, N: x.new_zeros(x.shape[0], N))
+    layer = M.Float8RoutedExperts(16, 128, 4, 2, choice_bias=True)
+    layer.choice_bias += 0.5
+    for cast in (False, True):
+        if cast:
+            layer.to(torch.bfloat16)
+        layer.quantize()
+        layer.decode(torch.zeros(1, 16, dtype=torch.bfloat16), torch.zeros(1, 4))
+        with pytest.raises(AttributeError):  # the forward stops at what stands in for the plan
+            layer(torch.zeros(1, 16, dtype=torch.bfloat16), torch.zeros(1, 4))
+    assert len(seen) == 4 and all(b.dtype == torch.float32 and bool((b == 0.5).all()) for b in seen)
