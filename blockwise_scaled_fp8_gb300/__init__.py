@@ -31,6 +31,8 @@ EXPORTS = [
     "bfp8_gemm_1x128_128x128_xq", "bfp8_gemm_1x128_128x1_xq",
     "bfp8_moe_route", "bfp8_moe_route_bwd", "bfp8_moe_plan_rows", "bfp8_moe_plan", "bfp8_moe_dispatch",
     "bfp8_moe_combine", "bfp8_moe_combine_bwd", "bfp8_gemm_routed_1x128_128x128",
+    "bfp8_rms_norm_quant", "bfp8_rms_norm_bwd_workspace_size", "bfp8_rms_norm_bwd",
+    "bfp8_grad_workspace_size", "bfp8_grad_norm", "bfp8_clip_grads",
 ]
 
 _lib = None
@@ -104,8 +106,18 @@ def lib() -> ctypes.CDLL:
     L.bfp8_moe_combine_bwd.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp]
     L.bfp8_gemm_routed_1x128_128x128.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64,
                                                  i64, i64, i64, vp]
+    L.bfp8_rms_norm_quant.argtypes = [vp, i64, i64, i64, vp, i64, vp, i32, f32, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp,
+                                      i64, vp, i64, vp]
+    L.bfp8_rms_norm_bwd_workspace_size.argtypes = [i64, i64]
+    L.bfp8_rms_norm_bwd.argtypes = [vp, i64, i64, i64, vp, i64, vp, i32, vp, vp, i64, vp, i64, vp, vp, sz, vp]
+    L.bfp8_grad_workspace_size.argtypes = [i64]
+    L.bfp8_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
+    L.bfp8_clip_grads.argtypes = [vp, vp, vp, i64, f32, vp, vp, vp, vp, sz, vp]
+    sizes = ("bfp8_rms_norm_bwd_workspace_size", "bfp8_grad_workspace_size")
+    for name in sizes:
+        getattr(L, name).restype = sz
     for name in EXPORTS:
-        if name not in ("bfp8_last_error", "bfp8_linear_workspace_size", "bfp8_linear_train_workspace_size",
+        if name not in sizes + ("bfp8_last_error", "bfp8_linear_workspace_size", "bfp8_linear_train_workspace_size",
                         "bfp8_linear_step_host_workspace_size", "bfp8_moe_step_host_workspace_size",
                         "bfp8_moe_plan_rows"):
             getattr(L, name).restype = ctypes.c_int
@@ -755,6 +767,191 @@ def moe_experts_decode(x, qw, sw, plan: MoePlan, weight, N: int):
         raise ValueError(f"moe_experts_decode: qw is {tuple(qw.shape)}, sw {tuple(sw.shape)}, x has {K} features")
     q, s = quant_lhs(x)
     return moe_combine(gemm_routed_1x128_128x128(q, s, qw, sw, plan, N, K), plan, weight)
+
+
+# ---------------------------------------------------------------------------
+# Root-mean-square norm with the residual's addition and quantised outputs
+# ---------------------------------------------------------------------------
+
+class NormOut(NamedTuple):
+    """What rms_norm_quant formed; None for what was not asked for."""
+    h: "torch.Tensor"      # [T, K] bf16, x + residual (x itself without one)
+    rstd: "torch.Tensor"   # [T] fp32
+    q_row: "torch.Tensor"  # [T, ldq], s_row [Kb, lds]: as quant_lhs of the normed rows
+    s_row: "torch.Tensor"
+    q_col: "torch.Tensor"  # [K, ldq'], s_col [Tb, lds']: as quant_rhs of them
+    s_col: "torch.Tensor"
+    y: "torch.Tensor"      # [T, K] bf16
+
+
+def _need_here(*tensors):
+    """The tensors must be on the current device: the launch goes to its stream."""
+    here = _torch()._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+def _need_norm_weight(weight, K):
+    torch = _torch()
+    f32 = weight.dtype is torch.float32
+    if not (f32 or weight.dtype is torch.bfloat16) or weight.shape != (K,) or not weight.is_cuda or \
+            not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous CUDA bf16 or float32 tensor of shape {(K,)}, got {weight.dtype} "
+                         f"{tuple(weight.shape)} on {weight.device}")
+    return f32
+
+
+def _need_rows(t, name, shape):
+    _need_bf16_2d(t, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows (stride {t.stride(0)} of {t.shape[1]} columns)")
+
+
+def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, rows: bool = True, cols: bool = False, out: bool = False,
+                   h=None) -> NormOut:
+    """y = h rsqrt(mean(h^2) + eps) weight of each row of h = x + residual (x
+    [T, K], residual bf16, weight [K] bf16 or fp32), quantised in 1x128 groups
+    (``rows``) and 128x1 groups (``cols``), or in bf16 (``out``), from one pass;
+    y is not rounded before its quantisation.  ``h`` (default: a new tensor) takes
+    the sum; it may be x or residual.  See bfp8_rms_norm_quant."""
+    torch = _torch()
+    _need_bf16_2d(x, "x")
+    T, K = x.shape
+    _need_rows(x, "x", (T, K))
+    f32 = _need_norm_weight(weight, K)
+    dev, u8, fp = x.device, torch.uint8, torch.float32
+    if residual is not None:
+        _need_rows(residual, "residual", (T, K))
+        if h is None:
+            h = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+        else:
+            _need_rows(h, "h", (T, K))
+    elif h is not None:
+        raise ValueError("h takes x + residual: it needs a residual")
+    _need_here(x, weight, residual, h)
+    rstd = torch.empty(T, dtype=fp, device=dev)
+    q = s = qc = sc = y = None
+    if rows:
+        q = torch.empty((T, (max(K, 1) + 15) // 16 * 16), dtype=u8, device=dev)
+        s = torch.empty(((K + BLOCK - 1) // BLOCK, max(T, 1)), dtype=fp, device=dev)
+    if cols:
+        qc = torch.empty((K, (max(T, 1) + 15) // 16 * 16), dtype=u8, device=dev)
+        sc = torch.empty(((T + BLOCK - 1) // BLOCK, (max(K, 1) + 3) // 4 * 4), dtype=fp, device=dev)
+    if out:
+        y = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+    st = lib().bfp8_rms_norm_quant(
+        x.data_ptr(), T, K, _ld(x), _p(residual), _ld(residual) if residual is not None else 0, weight.data_ptr(), f32, eps,
+        _p(h), _ld(h) if h is not None else 0, rstd.data_ptr(), _p(q), q.stride(0) if rows else 0, _p(s),
+        max(T, 1), _p(qc), qc.stride(0) if cols else 0, _p(sc), sc.stride(0) if cols else 0, _p(y), K, _stream())
+    if st:
+        _check(st)
+    return NormOut(x if h is None else h, rstd, q, s, qc, sc, y)
+
+
+def rms_norm_bwd(dy, h, weight, rstd, dh=None):
+    """Gradient of rms_norm_quant from its h and rstd: dy [T, K] bf16 (of the
+    normed rows), dh [T, K] bf16 or None (of h, by the stream itself) -> (dx [T,
+    K] bf16, the gradient of x and of the residual, dweight [K] fp32)."""
+    torch = _torch()
+    _need_bf16_2d(dy, "dy")
+    T, K = dy.shape
+    _need_rows(dy, "dy", (T, K))
+    _need_rows(h, "h", (T, K))
+    f32 = _need_norm_weight(weight, K)
+    _need(rstd, "rstd", torch.float32, (T,))
+    if dh is not None:
+        _need_rows(dh, "dh", (T, K))
+    _need_here(dy, h, weight, rstd, dh)
+    dev = dy.device
+    dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+    dw = torch.empty(K, dtype=torch.float32, device=dev)
+    L = lib()
+    ws = torch.empty(max(L.bfp8_rms_norm_bwd_workspace_size(T, K), 16), dtype=torch.uint8, device=dev)
+    st = L.bfp8_rms_norm_bwd(dy.data_ptr(), T, K, _ld(dy), h.data_ptr(), _ld(h), weight.data_ptr(), f32, rstd.data_ptr(),
+                             _p(dh), _ld(dh) if dh is not None else 0, dx.data_ptr(), max(K, 1), dw.data_ptr(),
+                             ws.data_ptr(), ws.numel(), _stream())
+    if st:
+        _check(st)
+    return dx, dw
+
+
+# ---------------------------------------------------------------------------
+# The norm of many tensors, and clipping
+# ---------------------------------------------------------------------------
+
+_grad_types = None
+
+
+def _grad_list(tensors, name):
+    """Addresses, sizes and types of a list of tensors, for the ABI."""
+    global _grad_types
+    torch = _torch()
+    if _grad_types is None:
+        _grad_types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    n = len(tensors)
+    ptr, numel, kind = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
+    here = torch._C._cuda_getDevice() if n else None
+    for i, t in enumerate(tensors):
+        code = _grad_types.get(t.dtype)
+        if code is None or not t.is_cuda or t.device.index != here:
+            raise ValueError(f"{name}[{i}] must be a bf16, fp16 or float32 tensor on the current CUDA device, got {t.dtype} "
+                             f"on {t.device}")
+        if not (t.is_contiguous() or _dense(t)):
+            raise ValueError(f"{name}[{i}] has gaps or repeats (shape {tuple(t.shape)}, strides {t.stride()})")
+        ptr[i], numel[i], kind[i] = t.data_ptr(), t.numel(), code
+    return ptr, numel, kind
+
+
+def _dense(t):
+    """Whether the tensor's elements fill its memory, each once, in some order of its dimensions."""
+    order = sorted(range(t.dim()), key=lambda d: (t.stride(d), t.shape[d]), reverse=True)
+    return t.permute(order).is_contiguous()
+
+
+def _grad_scratch(n, device):
+    torch = _torch()
+    ws = torch.empty(max(lib().bfp8_grad_workspace_size(n), 16), dtype=torch.uint8, device=device)
+    return torch.empty((), dtype=torch.float32, device=device), ws
+
+
+def grad_norm(tensors):
+    """The norm of all the tensors' elements as one vector: a list of CUDA
+    tensors (bf16, fp16, fp32 in any mixture) -> fp32 scalar on the device."""
+    tensors = list(tensors)
+    ptr, numel, kind = _grad_list(tensors, "tensors")
+    norm, ws = _grad_scratch(len(tensors), tensors[0].device if tensors else "cuda")
+    st = lib().bfp8_grad_norm(ptr, numel, kind, len(tensors), norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream())
+    if st:
+        _check(st)
+    return norm
+
+
+def clip_grads(tensors, max_norm: float, out=None):
+    """Scales the tensors by min(1, max_norm / (norm + 1e-6)) with their
+    grad_norm, in place or into the tensors ``out`` (bf16, fp16 or fp32, of the
+    same shapes and strides: an optimizer's own buffers).  Returns the norm
+    before, an fp32 scalar on the device; nothing waits for it."""
+    tensors = list(tensors)
+    ptr, numel, kind = _grad_list(tensors, "tensors")
+    optr, okind = ptr, kind
+    if out is not None:
+        out = list(out)
+        if len(out) != len(tensors):
+            raise ValueError(f"{len(tensors)} tensors, {len(out)} outputs")
+        for i, (t, o) in enumerate(zip(tensors, out)):
+            if t.shape != o.shape or (t.stride() != o.stride() and not (t.is_contiguous() and o.is_contiguous())):
+                raise ValueError(f"out[{i}] must have the shape and strides of tensors[{i}], {tuple(t.shape)} {t.stride()}, "
+                                 f"got {tuple(o.shape)} {o.stride()}")
+        optr, _, okind = _grad_list(out, "out")
+    norm, ws = _grad_scratch(len(tensors), tensors[0].device if tensors else "cuda")
+    st = lib().bfp8_clip_grads(ptr, numel, kind, len(tensors), max_norm, optr, okind, norm.data_ptr(), ws.data_ptr(),
+                               ws.numel(), _stream())
+    if st:
+        _check(st)
+    return norm
 
 
 # ---------------------------------------------------------------------------

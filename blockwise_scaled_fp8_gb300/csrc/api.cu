@@ -2,8 +2,10 @@
 // device checks, the linear-layer composition and the host-side index replay.
 #include <stdarg.h>
 #include <stdio.h>
+#include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 #include <vector>
 
@@ -722,6 +724,179 @@ bfp8_status bfp8_cast_e4m3(const float* x, int64_t n, void* q, bfp8_stream_t str
   if (st != BFP8_OK) return st;
   cudaError_t e = launch_cast(x, n, (uint8_t*)q, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, "bfp8_cast_e4m3 launch");
+}
+
+bfp8_status bfp8_rms_norm_quant(const void* x, int64_t T, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
+                                const void* weight, int weight_f32, float eps, void* h, int64_t ldh, float* rstd,
+                                void* q_row, int64_t ldq_row, float* s_row, int64_t lds_row, void* q_col,
+                                int64_t ldq_col, float* s_col, int64_t lds_col, void* y, int64_t ldy,
+                                bfp8_stream_t stream) {
+  const char* fn = "bfp8_rms_norm_quant";
+  bfp8_status st = check_dims(fn, T, K);
+  if (st != BFP8_OK) return st;
+  CHECK_ARG(K <= kNormMaxK, "%s: K=%lld > %lld", fn, (long long)K, (long long)kNormMaxK);
+  CHECK_ARG(eps > 0.0f && eps < INFINITY, "%s: eps must be positive and finite", fn);
+  CHECK_ARG(!residual == !h, "%s: a residual and the sum h come together", fn);
+  CHECK_ARG(!q_row == !s_row && !q_col == !s_col, "%s: codes and scales come together", fn);
+  if (T == 0 || K == 0) return BFP8_OK;
+  CHECK_ARG(x && weight && rstd, "%s: null pointer", fn);
+  CHECK_ARG(al2(x) && al2(residual) && al2(h) && al2(y) && (weight_f32 ? al4(weight) : al2(weight)) && al4(rstd) &&
+                al16(q_row) && al16(q_col) && al4(s_row) && al4(s_col),
+            "%s: bf16 must be 2-byte, fp32 4-byte, codes 16-byte aligned", fn);
+  CHECK_ARG(ldx >= K && (!residual || (ldr >= K && ldh >= K)) && (!y || ldy >= K), "%s: a row stride is below K=%lld", fn,
+            (long long)K);
+  if (q_row)
+    CHECK_ARG(ldq_row >= K && ldq_row % 16 == 0 && lds_row >= T, "%s: ldq_row=%lld must be >= K=%lld and a multiple of 16, "
+              "lds_row=%lld >= T=%lld", fn, (long long)ldq_row, (long long)K, (long long)lds_row, (long long)T);
+  if (q_col)
+    CHECK_ARG(ldq_col >= T && ldq_col % 16 == 0 && lds_col >= K, "%s: ldq_col=%lld must be >= T=%lld and a multiple of 16, "
+              "lds_col=%lld >= K=%lld", fn, (long long)ldq_col, (long long)T, (long long)lds_col, (long long)K);
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const cudaError_t e = launch_rms_norm(
+      NormArgs{(const uint16_t*)x, ldx, (const uint16_t*)residual, ldr, T, K, weight, weight_f32 != 0, eps, (uint16_t*)h,
+               ldh, rstd, (uint8_t*)q_row, ldq_row, s_row, lds_row, (uint8_t*)q_col, ldq_col, s_col, lds_col,
+               (uint16_t*)y, ldy, 0, 0},
+      sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+
+size_t bfp8_rms_norm_bwd_workspace_size(int64_t T, int64_t K) {
+  if (T < 0 || K < 0 || T >= kMaxDim || K > kNormMaxK) return 0;
+  int sms = 0;
+  if (check_device(&sms) != BFP8_OK) sms = 1 << 10;  // (no device to ask: more than any has)
+  return (size_t)norm_bwd_geom(T, K, sms).teams * (size_t)K * 4;
+}
+
+bfp8_status bfp8_rms_norm_bwd(const void* dy, int64_t T, int64_t K, int64_t lddy, const void* h, int64_t ldh,
+                              const void* weight, int weight_f32, const float* rstd, const void* dh, int64_t lddh,
+                              void* dx, int64_t lddx, float* dweight, void* ws, size_t ws_bytes, bfp8_stream_t stream) {
+  const char* fn = "bfp8_rms_norm_bwd";
+  bfp8_status st = check_dims(fn, T, K);
+  if (st != BFP8_OK) return st;
+  CHECK_ARG(K <= kNormMaxK, "%s: K=%lld > %lld", fn, (long long)K, (long long)kNormMaxK);
+  if (K == 0) return BFP8_OK;
+  CHECK_ARG(dweight && (T == 0 || (dy && h && weight && rstd && dx && ws)), "%s: null pointer", fn);
+  CHECK_ARG(al2(dy) && al2(h) && al2(dh) && al2(dx) && (weight_f32 ? al4(weight) : al2(weight)) && al4(rstd) && al4(dweight) &&
+                al16(ws),
+            "%s: bf16 must be 2-byte, fp32 4-byte, the workspace 16-byte aligned", fn);
+  CHECK_ARG(T == 0 || (lddy >= K && ldh >= K && lddx >= K && (!dh || lddh >= K)), "%s: a row stride is below K=%lld", fn,
+            (long long)K);
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  const size_t need = bfp8_rms_norm_bwd_workspace_size(T, K);
+  CHECK_ARG(ws_bytes >= need, "%s: workspace of %zu bytes, needs %zu", fn, ws_bytes, need);
+  const cudaError_t e = launch_rms_norm_bwd(
+      NormBwdArgs{(const uint16_t*)dy, lddy, (const uint16_t*)h, ldh, T, K, weight, weight_f32 != 0, rstd,
+                  (const uint16_t*)dh, lddh, (uint16_t*)dx, lddx, dweight, (float*)ws, 0},
+      sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+
+size_t bfp8_grad_workspace_size(int64_t n) {
+  if (n < 0 || n >= kMaxDim) return 0;
+  int sms = 0;
+  if (check_device(&sms) != BFP8_OK) sms = 1 << 10;
+  return (size_t)grad_launches(n) * (size_t)grad_grid(sms) * 8;
+}
+
+}  // extern "C"
+
+namespace {
+// Checks of a list of tensors; *total gets the elements.
+bfp8_status check_grads(const char* fn, const char* what, const void* const* p, const int64_t* numel, const int32_t* type,
+                        int64_t n) {
+  CHECK_ARG(n >= 0 && n < ((int64_t)1 << 20), "%s: %lld tensors", fn, (long long)n);
+  CHECK_ARG(n == 0 || (p && numel && type), "%s: null list", fn);
+  int64_t total = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    CHECK_ARG(numel[i] >= 0 && numel[i] < ((int64_t)1 << 40), "%s: tensor %lld has %lld elements", fn, (long long)i,
+              (long long)numel[i]);
+    total += numel[i];
+    CHECK_ARG(total < ((int64_t)1 << 44), "%s: more than 2^44 elements", fn);
+    CHECK_ARG(type[i] >= kGradF32 && type[i] <= kGradF16, "%s: %s %lld has an unknown type %d", fn, what, (long long)i, type[i]);
+    if (numel[i] == 0) continue;
+    CHECK_ARG(p[i], "%s: %s %lld is null", fn, what, (long long)i);
+    CHECK_ARG(type[i] == kGradF32 ? al4(p[i]) : al2(p[i]), "%s: %s %lld is misaligned", fn, what, (long long)i);
+  }
+  return BFP8_OK;
+}
+
+struct Span {
+  uintptr_t from, to;
+  bool written;
+  int64_t i;
+};
+
+bfp8_status run_grads(const char* fn, const void* const* in, const int64_t* numel, const int32_t* in_type, int64_t n,
+                      void* const* out, const int32_t* out_type, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                      bfp8_stream_t stream) {
+  CHECK_ARG(norm && ws, "%s: null pointer", fn);
+  CHECK_ARG(al4(norm) && al16(ws), "%s: norm must be 4-byte, the workspace 16-byte aligned", fn);
+  int sms = 0;
+  bfp8_status st = check_device(&sms);
+  if (st != BFP8_OK) return st;
+  std::vector<int64_t> which;
+  which.reserve((size_t)n);
+  bool in_place = out != nullptr;
+  for (int64_t i = 0; i < n; ++i)
+    if (numel[i] > 0) {
+      which.push_back(i);
+      in_place = in_place && in[i] == out[i] && in_type[i] == out_type[i];
+    }
+  const size_t need = (size_t)grad_launches((int64_t)which.size()) * (size_t)grad_grid(sms) * 8;
+  CHECK_ARG(ws_bytes >= need, "%s: workspace of %zu bytes, needs %zu", fn, ws_bytes, need);
+  const cudaError_t e = launch_grads(GradArgs{in, numel, in_type, out, out_type, max_norm, in_place, norm, (double*)ws},
+                                     which.data(), (int64_t)which.size(), sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
+}
+}  // namespace
+
+extern "C" {
+
+bfp8_status bfp8_grad_norm(const void* const* tensors, const int64_t* numel, const int32_t* types, int64_t n, float* norm,
+                           void* ws, size_t ws_bytes, bfp8_stream_t stream) {
+  const char* fn = "bfp8_grad_norm";
+  const bfp8_status st = check_grads(fn, "tensor", tensors, numel, types, n);
+  if (st != BFP8_OK) return st;
+  try {
+    return run_grads(fn, tensors, numel, types, n, nullptr, nullptr, 0.0f, norm, ws, ws_bytes, stream);
+  } catch (...) {  // no memory for the host's lists
+    return fail(BFP8_ERR_CUDA, "%s: out of host memory", fn);
+  }
+}
+
+bfp8_status bfp8_clip_grads(const void* const* tensors, const int64_t* numel, const int32_t* types, int64_t n,
+                            float max_norm, void* const* out, const int32_t* out_types, float* norm, void* ws,
+                            size_t ws_bytes, bfp8_stream_t stream) {
+  const char* fn = "bfp8_clip_grads";
+  bfp8_status st = check_grads(fn, "tensor", tensors, numel, types, n);
+  if (st != BFP8_OK) return st;
+  if ((st = check_grads(fn, "output", out, numel, out_types, n)) != BFP8_OK) return st;
+  CHECK_ARG(max_norm >= 0.0f, "%s: max_norm must not be negative or NaN", fn);
+  try {
+    // No output may overlap another output, or an input but its own exactly: the CTAs go through them in no order.
+    std::vector<Span> spans;
+    spans.reserve(2 * (size_t)n);
+    for (int64_t i = 0; i < n; ++i) {
+      if (numel[i] == 0) continue;
+      const uintptr_t a = (uintptr_t)tensors[i], b = (uintptr_t)out[i];
+      const bool own = a == b && types[i] == out_types[i];
+      if (!own) spans.push_back(Span{a, a + (uintptr_t)numel[i] * (types[i] == kGradF32 ? 4 : 2), false, i});
+      spans.push_back(Span{b, b + (uintptr_t)numel[i] * (out_types[i] == kGradF32 ? 4 : 2), true, i});
+    }
+    std::sort(spans.begin(), spans.end(), [](const Span& p, const Span& q) { return p.from < q.from; });
+    uintptr_t end = 0, end_written = 0;  // of the spans before
+    for (const Span& s : spans) {
+      CHECK_ARG(s.from >= end_written && (!s.written || s.from >= end),
+                "%s: tensor %lld shares memory with another, or its output with an input", fn, (long long)s.i);
+      end = std::max(end, s.to);
+      if (s.written) end_written = std::max(end_written, s.to);
+    }
+    return run_grads(fn, tensors, numel, types, n, out, out_types, max_norm, norm, ws, ws_bytes, stream);
+  } catch (...) {
+    return fail(BFP8_ERR_CUDA, "%s: out of host memory", fn);
+  }
 }
 
 bfp8_status bfp8_check_device_errors(bfp8_stream_t stream) {

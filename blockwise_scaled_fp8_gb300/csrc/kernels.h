@@ -246,6 +246,78 @@ cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_
 constexpr uint32_t kRoutedOffsets = 32u;  // error bit: decreasing offsets (the others: a wait that gave up)
 cudaError_t routed_read_errors(uint32_t* out);  // reads and clears the kernel's error word (synchronous)
 
+// Root-mean-square norm with the residual's addition and quantised outputs, and its gradient (norm.cu); the
+// arguments are those of the ABI's entries (bfp8.h).
+constexpr int64_t kNormMaxK = 16384;
+struct NormArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* residual;  // null: h is x
+  int64_t ldr;
+  int64_t T, K;
+  const void* weight;
+  int weight_f32;
+  float eps;
+  uint16_t* h;
+  int64_t ldh;
+  float* rstd;
+  uint8_t* q_row;  // null: not formed
+  int64_t ldq_row;
+  float* s_row;
+  int64_t lds_row;
+  uint8_t* q_col;  // null: not formed
+  int64_t ldq_col;
+  float* s_col;
+  int64_t lds_col;
+  uint16_t* y;  // null: not formed
+  int64_t ldy;
+  int team, cluster;  // set by the launcher: threads a row, CTAs that share 128 rows
+};
+cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t st);
+struct NormBwdArgs {
+  const uint16_t* dy;
+  int64_t lddy;
+  const uint16_t* h;
+  int64_t ldh;
+  int64_t T, K;
+  const void* weight;
+  int weight_f32;
+  const float* rstd;
+  const uint16_t* dh;  // null: none
+  int64_t lddh;
+  uint16_t* dx;
+  int64_t lddx;
+  float* dweight;
+  float* partial;  // [teams][K]
+  int team;        // set by the launcher
+};
+struct NormBwdGeom {
+  int vpt, team;
+  int64_t grid, teams;  // teams: rows of partial sums
+};
+NormBwdGeom norm_bwd_geom(int64_t T, int64_t K, int num_sms);
+cudaError_t launch_rms_norm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t st);
+
+// The norm of many tensors and their clipping (grad.cu): tensor i has numel[i] elements of in_type[i] at in[i], and
+// goes to out[i] (out null: the norm alone).
+enum : int { kGradF32 = 0, kGradBf16 = 1, kGradF16 = 2 };
+constexpr int kGradCapSmall = 64, kGradCap = 640;  // tensors a launch
+struct GradArgs {
+  const void* const* in;
+  const int64_t* numel;
+  const int32_t* in_type;
+  void* const* out;
+  const int32_t* out_type;
+  float max_norm;
+  int in_place;  // every out[i] is in[i]
+  float* norm;
+  double* partial;  // grad_launches(n) * grad_grid(num_sms)
+};
+int grad_grid(int num_sms);
+int64_t grad_launches(int64_t n);
+// `which`: the n tensors that hold elements
+cudaError_t launch_grads(const GradArgs& a, const int64_t* which, int64_t n, int num_sms, cudaStream_t st);
+
 // Reads and clears the device error word of the GEMM kernels (synchronous).
 cudaError_t gemm_read_errors(uint32_t* out);
 

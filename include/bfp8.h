@@ -387,6 +387,73 @@ BFP8_API bfp8_status bfp8_gemm_routed_1x128_128x128(const void *qa, int64_t lda,
                                                     int64_t N, int64_t K, bfp8_stream_t stream);
 
 /*
+ * Root-mean-square norm of a residual stream, with the addition before it and
+ * quantised outputs after it (no counterpart on the pages, which quantise a
+ * linear layer's input; this forms that input's codes where it arises):
+ *   h = bf16(x + residual), x itself without a residual;
+ *   r = 1 / sqrt(mean over k of h^2 + eps),   y[t,k] = h r weight[k]
+ * and of y, which is not rounded before its quantisation, whichever of
+ *   q_row, s_row as bfp8_quant_lhs(y);  q_col, s_col as bfp8_quant_rhs(y);  y in bf16
+ * is not NULL.  Sums are fp32; a code is y/s to within a few fp32 roundings,
+ * rounded (y/s within those of a tie may go either way).  The squares of a row
+ * must fit fp32 (|h| up to about 1e18), and eps > 0.
+ *   x, residual device bf16 [T,K] (residual and h both NULL or both given); h
+ *   device bf16 [T,K], may be x or residual themselves (with that one's row
+ *   stride); weight device bf16 or fp32 (weight_f32 != 0) [K]; rstd device fp32
+ *   [T], gets r; codes, scales, strides as bfp8_quant_dual's; y device bf16
+ *   [T,K].  K <= 16384.  16-byte aligned rows (K and strides multiples of 8)
+ *   take wide accesses, others go element by element.
+ */
+BFP8_API bfp8_status bfp8_rms_norm_quant(const void *x, int64_t T, int64_t K, int64_t ldx, const void *residual,
+                                         int64_t ldr, const void *weight, int weight_f32, float eps, void *h,
+                                         int64_t ldh, float *rstd, void *q_row, int64_t ldq_row, float *s_row,
+                                         int64_t lds_row, void *q_col, int64_t ldq_col, float *s_col, int64_t lds_col,
+                                         void *y, int64_t ldy, bfp8_stream_t stream);
+
+/*
+ * The norm's gradient, from its h (x where there was no residual) and rstd:
+ * with n = h r and g = dy weight,
+ *   dx = r (g - n mean over k of g n) + dh      (bf16, the gradient of x and of the residual alike)
+ *   dweight[k] = sum over t of dy n             (fp32)
+ * dh (bf16 [T,K] or NULL) is the gradient that reaches h by the stream itself.
+ * dx may be dy, dh or h.  T == 0 gives dweight 0.  ws: at least
+ * bfp8_rms_norm_bwd_workspace_size(T, K) bytes of the device that is current
+ * in both calls, 16-byte aligned.  The same inputs give the same bits.
+ */
+BFP8_API size_t bfp8_rms_norm_bwd_workspace_size(int64_t T, int64_t K);
+BFP8_API bfp8_status bfp8_rms_norm_bwd(const void *dy, int64_t T, int64_t K, int64_t lddy, const void *h, int64_t ldh,
+                                       const void *weight, int weight_f32, const float *rstd, const void *dh,
+                                       int64_t lddh, void *dx, int64_t lddx, float *dweight, void *ws, size_t ws_bytes,
+                                       bfp8_stream_t stream);
+
+/*
+ * The norm of many tensors taken as one vector, and their clipping by it (the
+ * end of a training step):
+ *   norm = sqrt(sum of all elements' squares)              (fp32, on the device)
+ *   out_i = min(1, max_norm / (norm + 1e-6)) * tensor_i    (bfp8_clip_grads)
+ * tensors, numel, types, out, out_types are HOST arrays of n: tensor i has
+ * numel[i] contiguous elements of types[i] at the device address tensors[i],
+ * and is written to out[i] (itself with its own type: in place, and then not
+ * touched where the factor is 1) as out_types[i].  Sums are exact enough that
+ * the norm is that of the elements to fp32's rounding, whatever their size; a
+ * NaN or an infinity among them makes it one, and the outputs what the
+ * factor then gives.  The arrays are read before the call returns.
+ * Outputs must not overlap one another or other inputs (BFP8_ERR_INVALID_ARG).
+ * n < 2^20; empty tensors take part as nothing.  The same tensors in the same
+ * order give the same bits.  ws: at least bfp8_grad_workspace_size(n) bytes of
+ * the current device, 16-byte aligned.  Two launches for up to 640 tensors.
+ */
+#define BFP8_F32 0
+#define BFP8_BF16 1
+#define BFP8_F16 2
+BFP8_API size_t bfp8_grad_workspace_size(int64_t n);
+BFP8_API bfp8_status bfp8_grad_norm(const void *const *tensors, const int64_t *numel, const int32_t *types, int64_t n,
+                                    float *norm, void *ws, size_t ws_bytes, bfp8_stream_t stream);
+BFP8_API bfp8_status bfp8_clip_grads(const void *const *tensors, const int64_t *numel, const int32_t *types, int64_t n,
+                                     float max_norm, void *const *out, const int32_t *out_types, float *norm, void *ws,
+                                     size_t ws_bytes, bfp8_stream_t stream);
+
+/*
  * Blockwise-FP8 linear layer (the Float8BlockwiseLinear computation of the
  * ROCm enablement page: quantise, then the blockwise GEMMs), y = x W^T.
  *   x  device bf16 [M,K] contiguous;  w  device bf16 [N,K] contiguous;
