@@ -31,6 +31,7 @@ EXPORTS = [
     "bfp8_gemm_1x128_128x128_xq", "bfp8_gemm_1x128_128x1_xq",
     "bfp8_moe_route", "bfp8_moe_route_bwd", "bfp8_moe_plan_rows", "bfp8_moe_plan", "bfp8_moe_dispatch",
     "bfp8_moe_combine", "bfp8_moe_combine_bwd", "bfp8_gemm_routed_1x128_128x128",
+    "bfp8_moe_mlp_workspace_size", "bfp8_moe_mlp_decode",
     "bfp8_rms_norm_quant", "bfp8_rms_norm_bwd_workspace_size", "bfp8_rms_norm_bwd",
     "bfp8_grad_workspace_size", "bfp8_grad_norm", "bfp8_clip_grads",
 ]
@@ -113,7 +114,10 @@ def lib() -> ctypes.CDLL:
     L.bfp8_grad_workspace_size.argtypes = [i64]
     L.bfp8_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
     L.bfp8_clip_grads.argtypes = [vp, vp, vp, i64, f32, vp, vp, vp, vp, sz, vp]
-    sizes = ("bfp8_rms_norm_bwd_workspace_size", "bfp8_grad_workspace_size")
+    L.bfp8_moe_mlp_workspace_size.argtypes = [i64, i64, i64]
+    L.bfp8_moe_mlp_decode.argtypes = [vp, i64, i64, i64, vp, i32, i64, i64, vp, i64, i32, i64, i64, i32, i32, f32,
+                                      vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, vp, i64, vp, sz, vp]
+    sizes = ("bfp8_moe_mlp_workspace_size", "bfp8_rms_norm_bwd_workspace_size", "bfp8_grad_workspace_size")
     for name in sizes:
         getattr(L, name).restype = sz
     for name in EXPORTS:
@@ -767,6 +771,49 @@ def moe_experts_decode(x, qw, sw, plan: MoePlan, weight, N: int):
         raise ValueError(f"moe_experts_decode: qw is {tuple(qw.shape)}, sw {tuple(sw.shape)}, x has {K} features")
     q, s = quant_lhs(x)
     return moe_combine(gemm_routed_1x128_128x128(q, s, qw, sw, plan, N, K), plan, weight)
+
+
+def moe_mlp_decode(x, logits, k: int, qgu, sgu, qd, sd, I: int, N: int, bias=None, score: str = "softmax",
+                   groups: int = 1, top_groups=None, group_top: int = 1, renormalize: bool = True, scale: float = 1.0):
+    """A whole layer of gated experts for at most 16 tokens (serving), in two
+    launches: the router's choices by logits [T, E] (arguments as moe_route's),
+    then y[t] = sum_j w_j D_e q(silu(G_e q(x[t])) * (U_e q(x[t]))) over them.  x
+    [T, K] bf16; (qgu, _, sgu) = quant_weight of the experts' stacked [2I, K]
+    weights (gate rows, then up rows), (qd, _, sd) of their [N, I] ones.  Returns
+    y [T, N] bf16; see bfp8_moe_mlp_decode."""
+    torch = _torch()
+    f32 = _need_logits(logits)
+    T, E = logits.shape
+    _need_bf16_2d(x, "x")
+    K = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} tokens, the logits {T}")
+    at_bias = None
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,))
+        at_bias = bias.data_ptr()
+    u8, f8, fp = torch.uint8, torch.float8_e4m3fn, torch.float32
+    for name, q, s, rows, cols in (("gu", qgu, sgu, 2 * I, K), ("d", qd, sd, N, I)):
+        if q.dtype not in (u8, f8) or s.dtype is not fp or q.dim() != 2 or s.dim() != 2 or not (q.is_cuda and s.is_cuda):
+            raise ValueError(f"q{name} must be 2-D CUDA uint8 or float8_e4m3fn codes and s{name} their CUDA float32 scales")
+        if q.shape[0] != E * rows or q.shape[1] < cols or s.shape[0] < E * _cdiv(rows, BLOCK) or \
+                s.shape[1] < _cdiv(cols, BLOCK):
+            raise ValueError(f"{E} experts of {rows} x {cols} need q{name} of {E * rows} rows and {cols} columns and s{name} "
+                             f"of {E * _cdiv(rows, BLOCK)} x {_cdiv(cols, BLOCK)}, got {tuple(q.shape)} and {tuple(s.shape)}")
+        if q.stride(1) != 1 or (s.stride(1) != 1 and s.shape[1] > 1):
+            raise ValueError(f"q{name} and s{name} must have unit column strides")
+    _need_here(x, logits, bias, qgu, sgu, qd, sd)
+    dev = x.device
+    L = lib()
+    y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    ws = torch.empty(max(L.bfp8_moe_mlp_workspace_size(T, k, I), 16), dtype=u8, device=dev)
+    st = L.bfp8_moe_mlp_decode(x.data_ptr(), T, K, _ld(x), logits.data_ptr(), f32, E, logits.stride(0) if T > 1 else E,
+                               at_bias, k, _score(score), groups, groups if top_groups is None else top_groups, group_top,
+                               renormalize, scale, qgu.data_ptr(), _ld(qgu), sgu.data_ptr(), _ld(sgu), qd.data_ptr(),
+                               _ld(qd), sd.data_ptr(), _ld(sd), I, N, y.data_ptr(), N, ws.data_ptr(), ws.numel(), _stream())
+    if st:
+        _check(st)
+    return y
 
 
 # ---------------------------------------------------------------------------

@@ -514,10 +514,12 @@ static bfp8_status check_slots(const char* fn, int64_t T, int64_t k) {
   return BFP8_OK;
 }
 
-bfp8_status bfp8_moe_route(const void* logits, int logits_f32, int64_t T, int64_t E, int64_t ldl, const float* bias,
-                           int64_t k, int score, int64_t groups, int64_t top_groups, int group_top, int renormalize,
-                           float scale, int32_t* idx, float* w, bfp8_stream_t stream) {
-  const char* fn = "bfp8_moe_route";
+}  // extern "C"
+
+namespace {
+// What bfp8_moe_route asks of its arguments (T > 0: of the pointers too).
+bfp8_status check_route(const char* fn, const void* logits, int logits_f32, int64_t T, int64_t E, int64_t ldl,
+                        const float* bias, int64_t k, int score, int64_t groups, int64_t top_groups, int group_top) {
   bfp8_status st = check_slots(fn, T, k);
   if (st != BFP8_OK) return st;
   CHECK_ARG(E >= 1 && E <= kMaxGroups, "%s: E=%lld must be in [1, %d]", fn, (long long)E, kMaxGroups);
@@ -532,13 +534,27 @@ bfp8_status bfp8_moe_route(const void* logits, int logits_f32, int64_t T, int64_
             (long long)top_groups);
   CHECK_ARG(ldl >= E, "%s: ldl=%lld < E=%lld", fn, (long long)ldl, (long long)E);
   if (T == 0) return BFP8_OK;
-  CHECK_ARG(logits && idx && w, "%s: null pointer", fn);
-  CHECK_ARG((logits_f32 ? al4(logits) : al2(logits)) && al4(bias) && al4(idx) && al4(w), "%s: misaligned pointer", fn);
+  CHECK_ARG(logits, "%s: null pointer", fn);
+  CHECK_ARG((logits_f32 ? al4(logits) : al2(logits)) && al4(bias), "%s: misaligned pointer", fn);
+  return BFP8_OK;
+}
+}  // namespace
+
+extern "C" {
+
+bfp8_status bfp8_moe_route(const void* logits, int logits_f32, int64_t T, int64_t E, int64_t ldl, const float* bias,
+                           int64_t k, int score, int64_t groups, int64_t top_groups, int group_top, int renormalize,
+                           float scale, int32_t* idx, float* w, bfp8_stream_t stream) {
+  const char* fn = "bfp8_moe_route";
+  bfp8_status st = check_route(fn, logits, logits_f32, T, E, ldl, bias, k, score, groups, top_groups, group_top);
+  if (st != BFP8_OK || T == 0) return st;
+  CHECK_ARG(idx && w, "%s: null pointer", fn);
+  CHECK_ARG(al4(idx) && al4(w), "%s: misaligned pointer", fn);
   int sms = 0;
   if ((st = check_device(&sms)) != BFP8_OK) return st;
   const cudaError_t e =
       launch_moe_route(RouteArgs{logits, logits_f32 != 0, T, E, ldl, bias, (int)k, score == BFP8_MOE_SIGMOID,
-                                 (int)groups, (int)top_groups, group_top, renormalize != 0, scale, idx, w, 0, 0, 0, 0},
+                                 (int)groups, (int)top_groups, group_top, renormalize != 0, scale, idx, w, 0, 0, 0, 0, nullptr},
                        (cudaStream_t)stream);
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
 }
@@ -726,6 +742,85 @@ bfp8_status bfp8_cast_e4m3(const float* x, int64_t n, void* q, bfp8_stream_t str
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, "bfp8_cast_e4m3 launch");
 }
 
+}  // extern "C"
+
+namespace {
+// Workspace of the few-token layer: the count of CTAs that have arrived, the choices, their weights, the activations.
+struct MlpLayout {
+  size_t idx, w, act, total;
+};
+MlpLayout mlp_layout(int64_t T, int64_t k, int64_t I) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  MlpLayout L;
+  L.idx = 256;
+  L.w = up(L.idx + (size_t)(T * k) * 4);
+  L.act = up(L.w + (size_t)(T * k) * 4);
+  L.total = L.act + (size_t)(T * k) * (size_t)I * 4;
+  return L;
+}
+}  // namespace
+
+extern "C" {
+
+size_t bfp8_moe_mlp_workspace_size(int64_t T, int64_t k, int64_t I) {
+  if (T < 0 || T > kMlpMaxTokens || k < 1 || k > BFP8_MOE_MAX_K || I < 0 || I >= kMaxDim) return 0;
+  return mlp_layout(T, k, I).total;
+}
+
+bfp8_status bfp8_moe_mlp_decode(const void* x, int64_t T, int64_t K, int64_t ldx, const void* logits, int logits_f32,
+                                int64_t E, int64_t ldl, const float* bias, int64_t k, int score, int64_t groups,
+                                int64_t top_groups, int group_top, int renormalize, float scale, const void* qgu,
+                                int64_t ldgu, const float* sgu, int64_t ldsgu, const void* qd, int64_t ldd,
+                                const float* sd, int64_t ldsd, int64_t I, int64_t N, void* y, int64_t ldy, void* ws,
+                                size_t ws_bytes, bfp8_stream_t stream) {
+  const char* fn = "bfp8_moe_mlp_decode";
+  bfp8_status st = check_route(fn, logits, logits_f32, T, E, ldl, bias, k, score, groups, top_groups, group_top);
+  if (st != BFP8_OK) return st;
+  if ((st = check_dims(fn, K, I, N)) != BFP8_OK) return st;
+  CHECK_ARG(T <= kMlpMaxTokens, "%s: T=%lld > %d tokens", fn, (long long)T, kMlpMaxTokens);
+  CHECK_ARG(K >= 1 && I >= 1 && N >= 1, "%s: K, I and N must be positive", fn);
+  CHECK_ARG(I % 64 == 0, "%s: I=%lld must be a multiple of 64", fn, (long long)I);
+  CHECK_ARG(E == 1 || N % kBlock == 0, "%s: N=%lld must be a multiple of 128 (of several experts)", fn, (long long)N);
+  CHECK_ARG(E * 2 * I < kMaxDim && E * N < kMaxDim, "%s: the stacked weights pass 2^31 rows", fn);
+  if (T == 0) return BFP8_OK;
+  CHECK_ARG(x && qgu && sgu && qd && sd && y && ws, "%s: null pointer", fn);
+  CHECK_ARG(al2(x) && al16(qgu) && al16(qd) && al4(sgu) && al4(sd) && al2(y) && al16(ws),
+            "%s: x, y must be 2-byte, scales 4-byte, codes and the workspace 16-byte aligned", fn);
+  CHECK_ARG(ldx >= K && ldy >= N, "%s: ldx=%lld / ldy=%lld below K=%lld / N=%lld", fn, (long long)ldx, (long long)ldy,
+            (long long)K, (long long)N);
+  CHECK_ARG(ldgu >= K && ldgu % 16 == 0 && ldd >= I && ldd % 16 == 0,
+            "%s: ldgu=%lld, ldd=%lld must be multiples of 16 and >= K=%lld, I=%lld", fn, (long long)ldgu, (long long)ldd,
+            (long long)K, (long long)I);
+  CHECK_ARG(ldsgu >= cdiv(K, kBlock) && ldsd >= cdiv(I, kBlock), "%s: ldsgu=%lld / ldsd=%lld below the K-blocks", fn,
+            (long long)ldsgu, (long long)ldsd);
+  const MlpLayout L = mlp_layout(T, k, I);
+  CHECK_ARG(ws_bytes >= L.total, "%s: workspace of %zu bytes, needs %zu", fn, ws_bytes, L.total);
+  int sms = 0;
+  if ((st = check_device(&sms)) != BFP8_OK) return st;
+  CHECK_ARG(mlp_geom(T, K, I, N, sms).stages >= 2,
+            "%s: K, I <= 16384 (8192 for more than 8 tokens) and N <= 128 a multiprocessor; got K=%lld, I=%lld, N=%lld", fn,
+            (long long)K, (long long)I, (long long)N);
+  uint8_t* base = (uint8_t*)ws;
+  uint32_t* arrived = (uint32_t*)base;
+  int32_t* idx = (int32_t*)(base + L.idx);
+  float* w = (float*)(base + L.w);
+  cudaError_t e =
+      launch_moe_route(RouteArgs{logits, logits_f32 != 0, T, E, ldl, bias, (int)k, score == BFP8_MOE_SIGMOID,
+                                 (int)groups, (int)top_groups, group_top, renormalize != 0, scale, idx, w, 0, 0, 0, 0, arrived},
+                       (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  MlpArgs a = {};
+  a.x = (const uint16_t*)x, a.ldx = ldx;
+  a.T = (int)T, a.K = (int)K, a.E = (int)E, a.k = (int)k, a.I = (int)I, a.N = (int)N;
+  a.idx = idx, a.w = w, a.sgu = sgu, a.ldsgu = ldsgu, a.sd = sd, a.ldsd = ldsd;
+  a.act = (float*)(base + L.act), a.arrived = arrived;
+  a.y = (uint16_t*)y, a.ldy = ldy;
+  const char* msg = nullptr;
+  e = launch_moe_mlp(a, (const uint8_t*)qgu, ldgu, (const uint8_t*)qd, ldd, sms, (cudaStream_t)stream, &msg);
+  if (e != cudaSuccess) return msg ? fail(BFP8_ERR_CUDA, "%s: %s", fn, msg) : cuda_fail(e, fn);
+  return BFP8_OK;
+}
+
 bfp8_status bfp8_rms_norm_quant(const void* x, int64_t T, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
                                 const void* weight, int weight_f32, float eps, void* h, int64_t ldh, float* rstd,
                                 void* q_row, int64_t ldq_row, float* s_row, int64_t lds_row, void* q_col,
@@ -905,15 +1000,17 @@ bfp8_status bfp8_check_device_errors(bfp8_stream_t stream) {
   if (st != BFP8_OK) return st;
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: stream synchronize");
-  uint32_t bits = 0, qbits = 0, dbits = 0, rbits = 0;
+  uint32_t bits = 0, qbits = 0, dbits = 0, rbits = 0, mbits = 0;
   e = gemm_read_errors(&bits);
   if (e == cudaSuccess) e = quant_read_errors(&qbits);
   if (e == cudaSuccess) e = dispatch_read_errors(&dbits);
   if (e == cudaSuccess) e = routed_read_errors(&rbits);
+  if (e == cudaSuccess) e = mlp_read_errors(&mbits);
   if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: read flag");
   if (qbits) return fail(BFP8_ERR_TIMEOUT, "quantisation kernel gave up waiting for its TMA tile loads");
   if (dbits) return fail(BFP8_ERR_TIMEOUT, "dispatch kernel gave up waiting for its gathered rows");
   if (rbits & kRoutedOffsets) return fail(BFP8_ERR_INVALID_ARG, "routed product: expert offsets decreasing");
+  if (mbits) return fail(BFP8_ERR_TIMEOUT, "few-token experts layer gave up on a wait (flags 0x%x)", mbits);
   if (rbits) return fail(BFP8_ERR_TIMEOUT, "routed product gave up waiting for its weights");
   if (bits & 64u)  // kErrGroupOffsets
     return fail(BFP8_ERR_INVALID_ARG,

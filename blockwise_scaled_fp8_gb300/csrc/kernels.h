@@ -148,6 +148,7 @@ struct RouteArgs {
   int32_t* idx;
   float* w;
   int vec, bias_vec, group_lanes, group_whole;  // set by the launcher
+  uint32_t* zero;  // set to 0, or null
 };
 cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t st);
 
@@ -245,6 +246,34 @@ struct GemmRoutedArgs {
 cudaError_t launch_gemm_routed(const GemmRoutedArgs& a, int num_sms, cudaStream_t st, const char** msg);
 constexpr uint32_t kRoutedOffsets = 32u;  // error bit: decreasing offsets (the others: a wait that gave up)
 cudaError_t routed_read_errors(uint32_t* out);  // reads and clears the kernel's error word (synchronous)
+
+// A layer of gated experts for a few tokens (moe_mlp.cu), behind its router's launch.
+constexpr int kMlpMaxTokens = 16, kMlpMaxSlots = kMlpMaxTokens * BFP8_MOE_MAX_K;
+constexpr int kMlpCodeBytes = 128 * 1024;  // of a CTA's codes of the tokens, or of an expert's activations
+struct MlpArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  int T, K, E, k, I, N;
+  const int32_t* idx;  // the router's, [T, k]
+  const float* w;
+  const float* sgu;
+  int64_t ldsgu;
+  const float* sd;
+  int64_t ldsd;
+  float* act;         // [T*k, I]
+  uint32_t* arrived;  // 0 at the start
+  uint16_t* y;
+  int64_t ldy;
+  // set by the launcher: rows of D a CTA, its 16-row tiles, K-blocks of a stage, buffers of activations, stages, ..
+  int rows, mtiles, blocks, buffers, stages, off_scale, off_misc, vec;
+};
+struct MlpGeom {
+  int rows, mtiles, blocks, buffers, stages, off_scale, off_misc, smem;  // stages 0: sizes out of range
+};
+MlpGeom mlp_geom(int64_t T, int64_t K, int64_t I, int64_t N, int num_sms);
+cudaError_t launch_moe_mlp(const MlpArgs& a, const uint8_t* qgu, int64_t ldgu, const uint8_t* qd, int64_t ldd, int num_sms,
+                           cudaStream_t st, const char** msg);
+cudaError_t mlp_read_errors(uint32_t* out);  // reads and clears the kernel's error word (synchronous)
 
 // Root-mean-square norm with the residual's addition and quantised outputs, and its gradient (norm.cu); the
 // arguments are those of the ABI's entries (bfp8.h).

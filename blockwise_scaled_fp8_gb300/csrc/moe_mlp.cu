@@ -107,6 +107,12 @@ __device__ __forceinline__ void mma_16x8x32(float (&d)[4], const uint32_t (&a)[4
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// max(amax, 1e-12) / 448 as one product with 1/448: within an ulp of group_scale's quotient.
+__device__ __forceinline__ float scale_near(float amax) { return __fmul_rn(fmaxf(amax, kAmaxFloor), 1.0f / kE4m3Max); }
+// The codes of two bf16 values over s (IEEE quotients).
+__device__ __forceinline__ uint32_t codes2(uint32_t w, float s) {
+  return cvt_e4m3x2(__fdiv_rn(bf16_lo(w), s), __fdiv_rn(bf16_hi(w), s));
+}
 // The 16 x 8 NT partial product of one K-block: A's 16 rows, whose first eight lie at lines a0 .. and the others at
 // a1 .. of 128 bytes (swizzled by their address), against the codes of 8 NT tokens at b.
 template <int NT>
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
     return;
   }
 
-  // ------------------------------------------------------------ the tokens' codes (bfp8_quant_lhs's), by all other warps
+  // ------------------------------------------------------------ the tokens' codes, by all other warps
   {
     const int half = (tid - 32) >> 4, halves = (kMlpThreads - 32) >> 4, l16 = lane & 15;
     const int groups = a.T * Kb;
@@ -322,10 +328,8 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
         m = amax2(m, __byte_perm(m, 0, 0x1032));
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) m = amax2(m, __shfl_xor_sync(kAll, m, o));
-        const float s = scale_of(__uint_as_float(m & 0x7FFF0000u)), ny = neg_rcp(s);
-        const uint64_t s2 = f2_pack(s, s), ny2 = f2_pack(ny, ny);
-        const uint32_t lo = (neg_codes2(v[i].x, s2, ny2) | neg_codes2(v[i].y, s2, ny2) << 16) ^ 0x80808080u;
-        const uint32_t hi = (neg_codes2(v[i].z, s2, ny2) | neg_codes2(v[i].w, s2, ny2) << 16) ^ 0x80808080u;
+        const float s = scale_near(__uint_as_float(m & 0x7FFF0000u));
+        const uint32_t lo = codes2(v[i].x, s) | codes2(v[i].y, s) << 16, hi = codes2(v[i].z, s) | codes2(v[i].w, s) << 16;
         if (g < groups) {
           const uint32_t at = area + (uint32_t)((kb * NT + (t >> 3)) * kAtom + (t & 7) * 128 +
                                                 (((l16 >> 1) ^ (t & 7)) << 4) + 8 * (l16 & 1));
@@ -369,14 +373,15 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
     };
     float sg, su, sg_next, su_next;
     unit_scales(u0, 0, sg_next, su_next);
-    for (int u = u0; u < u1 && ok; ++u) {
+    // (a warp whose wait gave up goes on through the units without their stages, so that the barriers between them match)
+    for (int u = u0; u < u1; ++u) {
       sg = sg_next, su = su_next;
       unit_scales(u + 1, 0, sg_next, su_next);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[i][q] = 0.0f;
-      for (int j = 0; j < items1; ++j) {
+      for (int j = 0; j < items1 && ok; ++j) {
         if (j > 0 && (j & 31) == 0) unit_scales(u, j, sg, su);
         if (!(ok = wait_full())) break;
         const bool tail = j * kUnitBlocks >= Kf;
@@ -397,7 +402,6 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
         }
         release();
       }
-      if (!ok) break;
       float* red = s_red + turn * (kMmaWarps * 16 * NC);
       turn ^= 1;
 #pragma unroll
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
             up += red[(w * 16 + 8 + i) * NC + t];
           }
           const int slot = s_slot[s_start[r] + __popc(mask & ((1u << t) - 1u))];
-          a.act[(int64_t)slot * a.I + i0 + i] = gate / (1.0f + __expf(-gate)) * up;
+          a.act[(int64_t)slot * a.I + i0 + i] = gate / (1.0f + expf(-gate)) * up;
         }
       }
     }
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
                           fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w))));
 #pragma unroll
           for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-          const float s = group_scale(m), y = recip_rn(s);
+          const float s = scale_near(m), y = recip_rn(s);
           const uint32_t lo = cvt_e4m3x2(p.x * y, p.y * y) | cvt_e4m3x2(p.z * y, p.w * y) << 16;
           const uint32_t hi = cvt_e4m3x2(q.x * y, q.y * y) | cvt_e4m3x2(q.z * y, q.w * y) << 16;
           if (g0 + half + i * kHalves < groups) {

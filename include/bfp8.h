@@ -387,6 +387,38 @@ BFP8_API bfp8_status bfp8_gemm_routed_1x128_128x128(const void *qa, int64_t lda,
                                                     int64_t N, int64_t K, bfp8_stream_t stream);
 
 /*
+ * A whole layer of gated experts for a few tokens (decoding), in two launches:
+ * bfp8_moe_route's, and one that does the rest.  With (idx, w) the router's
+ * choices and weights (arguments and rules of bfp8_moe_route),
+ *   a[t,j] = silu(G_e q(x[t])) * (U_e q(x[t]))       e = idx[t,j], fp32
+ *   y[t]   = sum over j of w[t,j] D_e q(a[t,j])      (a slot with idx -1 adds nothing)
+ * q quantises in 1x128 groups, q(a) from fp32 values that were not rounded
+ * before; its scale is the product max(amax, 1e-12) * fl(1/448), within an ulp
+ * of bfp8_quant_lhs's quotient (codes of x/s that lie at a tie of two codes for
+ * one of the two scales may differ), its codes RNE_e4m3(x/s).  The products are those of
+ * bfp8_gemm_1x128_128x128 with fp32 results, and y is rounded once.  The same
+ * inputs give the same bits.
+ *   x   device bf16 [T,K], 0 <= T <= 16, ldx >= K;  y device bf16 [T,N], ldy >= N
+ *   qgu device e4m3 [E*2I, ldgu]: each expert's I gate rows, then its I up rows
+ *       (bfp8_quant_weight of the stacked weights); sgu their tile scales
+ *       [E*2I/128, ldsgu]; ldgu >= K, ldgu % 16 == 0, 16-byte aligned
+ *   qd  device e4m3 [E*N, ldd], sd [E*ceil(N/128), ldsd]: the ways down; ldd >= I
+ *   I % 64 == 0; N % 128 == 0 unless E == 1; K, I <= 16384 (8192 for T > 8),
+ *   N <= 128 times the device's multiprocessors
+ *   ws  device, bfp8_moe_mlp_workspace_size(T, k, I) bytes, 16-byte aligned:
+ *       one call's at a time
+ * The second launch is a cooperative one: its CTAs, one a multiprocessor, wait
+ * for one another once.  The wait is bounded (bfp8_check_device_errors).
+ */
+BFP8_API size_t bfp8_moe_mlp_workspace_size(int64_t T, int64_t k, int64_t I);
+BFP8_API bfp8_status bfp8_moe_mlp_decode(const void *x, int64_t T, int64_t K, int64_t ldx, const void *logits,
+                                         int logits_f32, int64_t E, int64_t ldl, const float *bias, int64_t k, int score,
+                                         int64_t groups, int64_t top_groups, int group_top, int renormalize, float scale,
+                                         const void *qgu, int64_t ldgu, const float *sgu, int64_t ldsgu, const void *qd,
+                                         int64_t ldd, const float *sd, int64_t ldsd, int64_t I, int64_t N, void *y,
+                                         int64_t ldy, void *ws, size_t ws_bytes, bfp8_stream_t stream);
+
+/*
  * Root-mean-square norm of a residual stream, with the addition before it and
  * quantised outputs after it (no counterpart on the pages, which quantise a
  * linear layer's input; this forms that input's codes where it arises):
