@@ -797,7 +797,7 @@ bfp8_status bfp8_moe_mlp_decode(const void* x, int64_t T, int64_t K, int64_t ldx
   CHECK_ARG(ws_bytes >= L.total, "%s: workspace of %zu bytes, needs %zu", fn, ws_bytes, L.total);
   int sms = 0;
   if ((st = check_device(&sms)) != BFP8_OK) return st;
-  CHECK_ARG(mlp_geom(T, K, I, N, sms).stages >= 2,
+  CHECK_ARG(mlp_geom(T, K, I, N, sms).stages >= 4,
             "%s: K, I <= 16384 (8192 for more than 8 tokens) and N <= 128 a multiprocessor; got K=%lld, I=%lld, N=%lld", fn,
             (long long)K, (long long)I, (long long)N);
   uint8_t* base = (uint8_t*)ws;

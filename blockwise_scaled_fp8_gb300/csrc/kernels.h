@@ -249,6 +249,7 @@ cudaError_t routed_read_errors(uint32_t* out);  // reads and clears the kernel's
 
 // A layer of gated experts for a few tokens (moe_mlp.cu), behind its router's launch.
 constexpr int kMlpMaxTokens = 16, kMlpMaxSlots = kMlpMaxTokens * BFP8_MOE_MAX_K;
+constexpr int kMlpMaxBuffers = 8;  // of an expert's activations
 constexpr int kMlpCodeBytes = 128 * 1024;  // of a CTA's codes of the tokens, or of an expert's activations
 struct MlpArgs {
   const uint16_t* x;
@@ -264,11 +265,11 @@ struct MlpArgs {
   uint32_t* arrived;  // 0 at the start
   uint16_t* y;
   int64_t ldy;
-  // set by the launcher: rows of D a CTA, its 16-row tiles, K-blocks of a stage, buffers of activations, stages, ..
-  int rows, mtiles, blocks, buffers, stages, off_scale, off_misc, vec;
+  // set by the launcher: rows of D a CTA, the power of two that holds them, buffers of activations, stages of the ring, ..
+  int rows, group, buffers, stages, off_scale, off_misc, vec;
 };
 struct MlpGeom {
-  int rows, mtiles, blocks, buffers, stages, off_scale, off_misc, smem;  // stages 0: sizes out of range
+  int rows, group, buffers, stages, off_scale, off_misc, smem;  // stages 0: sizes out of range
 };
 MlpGeom mlp_geom(int64_t T, int64_t K, int64_t I, int64_t N, int num_sms);
 cudaError_t launch_moe_mlp(const MlpArgs& a, const uint8_t* qgu, int64_t ldgu, const uint8_t* qd, int64_t ldd, int num_sms,

@@ -15,23 +15,30 @@
 //     them) is a barrier over the grid that only the warps behind the ring wait
 //     for: the down weights do not depend on it and fill the ring meanwhile.
 //
-//   warp 0       producer
-//   warps 1-8    products: a stage's K-blocks are split over them, their sums meet
-//                in shared memory at the end of a unit
-//   warps 9-12   the activations' codes, an expert ahead of the products
-//
-// First part: a unit is 8 gate rows and the 8 up rows of the same features; the
+// First part: a unit is 16 gate rows and the 16 up rows of the same features; the
 // units of all reached experts are shared evenly.  Second part: CTA c takes the
-// rows [c R, c R + R) of D of every reached expert, so y's sums over experts
-// never leave its registers.  Both give every CTA the same bytes to within a few
-// percent, where tiles of 128 rows (the operand of tcgen05.mma, in the routed
-// product) would give some of them two and some one: 256 tiles of one token's
-// eight experts of 2 x 2048 rows over 152 SMs.  16 rows and up to 16 tokens are the
-// shape of an 8-bit mma.sync, whose rate does not matter here: a CTA needs one
-// in about 40 cycles to keep up with its share of the memory.
+// rows [c R, c R + R) of D of every reached expert, R = N over the CTAs, so y's
+// sums over experts never leave its registers.  Tiles of 128 rows of W, the usual
+// operand of tcgen05.mma, would give some CTAs two and some one (one token's eight
+// experts of 2 x 2048 rows are 256 of them for 152 SMs).  So the instruction's 128
+// rows are 32 rows of W (or 16, 64, 128: the power of two that holds R) of four
+// K-blocks, one below the other, and its columns the tokens' codes of the same
+// four K-blocks side by side.  Of the product only the blocks where the two
+// K-blocks are the same are read; the others cost tensor-core time that nothing
+// else wants (128 x 32 x 128 a stage: a tenth of the time that its bytes take).
+// (mma.sync on 16 rows instead, which needs no such blocks: 59 us for one token,
+// 399 for 16, as its 8-bit form takes 250 issued instructions a warp and stage.)
+//
+//   warp 0         producer
+//   warps 1, 3     MMA issuers, on alternate stages
+//   warp 2         the weights' scales, into slots ahead of the products (loaded where
+//                  they are used they cost a trip to L2 a stage)
+//   warps 4-7      promotion: lane l of warp w is row 32 w + l of the 128
+//   warps 8-13     the activations' codes, experts ahead of the products: one or two
+//                  warps an expert, three or six experts at once
 //
 // Waits are bounded; a role that gives up sets the abort flag, the others leave
-// their loops, and copies in flight land before the CTA exits.
+// their loops, and copies and MMAs in flight finish before the CTA exits.
 #include <cudaTypedefs.h>
 #include <string.h>
 
@@ -47,35 +54,32 @@ static __device__ uint32_t g_mlp_error;
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kMmaWarps = 8, kQuantWarps = 4;
-constexpr int kMlpThreads = 32 * (1 + kMmaWarps + kQuantWarps);
-constexpr int kStageBytes = 16384;
-constexpr int kUnit = 8;            // gate (and up) rows of a unit
-constexpr int kUnitBlocks = 8;      // K-blocks of a stage of the first part: 2 x 8 rows x 128 B each
+constexpr int kMlpThreads = 448;
+constexpr int kIssuers = 2;         // warps 1, 3
+constexpr int kCoders = 6;          // warps 8-13
+constexpr int kActBatch = 8;        // groups of 128 activations that half a warp of them loads at once
+constexpr int kStageBytes = 128 * kBlock;
+constexpr int kPairs = 16;          // gate (and up) rows of a unit
+constexpr int kUnitRows = 2 * kPairs, kUnitBlocks = 128 / kUnitRows;  // K-blocks of a stage of the first part
 constexpr int kMlpMaxStages = 12;
 constexpr int kAtom = 1024;         // 8 rows x 128 B, 128-byte swizzled
-static_assert(kUnitBlocks == kMmaWarps && 2 * kUnit * kBlock * kUnitBlocks == kStageBytes, "a K-block a warp");
+constexpr int kTmemCols = 512, kMaxBufs = 8;
+constexpr int kSlots = 8;  // slots of the scales of a few stages: 32 of them
 
-// Shared memory after the ring and the codes (offsets from MlpArgs::off_misc).
-constexpr int kOffRed = 0;                                           // two sets of [8 warps][16 rows][8 NT tokens] sums
-constexpr int kRedBytes = 2 * kMmaWarps * 16 * kMlpMaxTokens * 4;
-constexpr int kOffMask = kOffRed + kRedBytes;                        // [E] tokens of an expert; [E] its rank from the plan's end on
+// Shared memory after the ring, the codes and their scales (offsets from MlpArgs::off_misc).
+constexpr int kOffRed = 0;                                           // two sets of [128 rows][8 NT tokens] sums
+constexpr int kRedBytes = 2 * 128 * kMlpMaxTokens * 4;
+constexpr int kOffMask = kOffRed + kRedBytes;                        // [E] the tokens of an expert, and the first of its slots
 constexpr int kOffExpert = kOffMask + kMaxGroups * 4;                // [reached] expert | mask << 16
 constexpr int kOffStart = kOffExpert + kMlpMaxSlots * 4;             // [reached] first of its slots
-constexpr int kOffSlot = kOffStart + kMlpMaxSlots * 4;               // slots by expert, in token order
-constexpr int kOffWeight = kOffSlot + kMlpMaxSlots * 4;              // [slots] routing weights, by slot
-constexpr int kOffBars = kOffWeight + kMlpMaxSlots * 4;              // full[12] empty[12] hfull[2] hempty[2]
-constexpr int kOffFlag = kOffBars + 8 * (2 * kMlpMaxStages + 4);     // abort flag, a zero, scan[16]
-constexpr int kMiscBytes = kOffFlag + 8 + 4 * 16;
+constexpr int kOffSlot = kOffStart + kMlpMaxSlots * 4;               // slots by expert, in token order: slot | token << 16
+constexpr int kOffWeight = kOffSlot + kMlpMaxSlots * 4;              // routing weights, by slot
+constexpr int kOffWsc = kOffWeight + kMlpMaxSlots * 4;               // [8 slots][stages][K-blocks][gate, up; or the two tiles of a CTA's rows]
+constexpr int kOffBars = kOffWsc + kSlots * 32 * 4;
+// full[12] empty[12] tfull[8] tempty[8] hfull[8] hempty[8] sfull[8] sempty[8], x ready, drain
+constexpr int kOffFlag = kOffBars + 8 * (2 * kMlpMaxStages + 2 * kMaxBufs + 2 * kMlpMaxBuffers + 2 * kSlots + 2);
+constexpr int kMiscBytes = kOffFlag + 16 + 4 * 16;                   // abort flag, a zero, tensor memory's address; scan[16]
 
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
-                                            int c3, int c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
-          dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
                                             int c3) {
   asm volatile(
@@ -91,51 +95,40 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// d[16 x 8] += a[16 x 32] b[32 x 8], e4m3 into fp32: thread 4g + t holds rows g, g + 8 and columns 2t, 2t + 1 of d.
-__device__ __forceinline__ void mma_16x8x32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // max(amax, 1e-12) / 448 as one product with 1/448: within an ulp of group_scale's quotient.
 __device__ __forceinline__ float scale_near(float amax) { return __fmul_rn(fmaxf(amax, kAmaxFloor), 1.0f / kE4m3Max); }
-// The codes of two bf16 values over s (IEEE quotients).
-__device__ __forceinline__ uint32_t codes2(uint32_t w, float s) {
-  return cvt_e4m3x2(__fdiv_rn(bf16_lo(w), s), __fdiv_rn(bf16_hi(w), s));
+// Place n of a ring of `size`, by steps of at most its size, and the parity of its turn.
+struct Ring {
+  int at;
+  uint32_t parity;
+  __device__ __forceinline__ void step(int by, int size) {
+    at += by;
+    if (at >= size) at -= size, parity ^= 1u;
+  }
+};
+
+// C consecutive 32-bit columns of this warp's 32 lanes of tensor memory.
+template <int C>
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, uint32_t (&r)[C]) {
+  if constexpr (C == 8) tmem_ld_32x32b_x8(taddr, r);
+  else if constexpr (C == 16) tmem_ld_32x32b_x16(taddr, r);
+  else tmem_ld_32x32b_x32(taddr, r);
+  tmem_ld_wait();
+  tmem_regs_after_wait(r);
 }
-// The 16 x 8 NT partial product of one K-block: A's 16 rows, whose first eight lie at lines a0 .. and the others at
-// a1 .. of 128 bytes (swizzled by their address), against the codes of 8 NT tokens at b.
-template <int NT>
-__device__ __forceinline__ void block_product(float (&p)[NT][4], uint32_t stage, int a0, int a1, uint32_t b, int lane) {
-  const int line = (lane & 8 ? a1 : a0) + (lane & 7);
-  const uint32_t row = stage + (uint32_t)line * 128u;
+// acc[t] += (xs[t] b) P[t]; `mask`: the tokens that take part (the others' columns hold anything).
+template <int NC, bool MASKED>
+__device__ __forceinline__ void promote(float (&acc)[NC], const uint32_t (&p)[NC], const float* xs, float b, uint32_t mask) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int t = 0; t < NC; t += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(xs + t);
+    const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[n][i] = 0.0f;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t bv[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      ldmatrix_x4(b + (uint32_t)(n * kAtom + (lane & 7) * 128 + (((4 * half + (lane >> 3)) ^ (lane & 7)) << 4)), bv[n]);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t av[4];
-      ldmatrix_x4(row + (uint32_t)(((4 * half + 2 * s + (lane >> 4)) ^ (line & 7)) << 4), av);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mma_16x8x32(p[n], av, bv[n][2 * s], bv[n][2 * s + 1]);
-    }
+    for (int i = 0; i < 4; ++i)
+      if (!MASKED || (mask >> (t + i) & 1u)) acc[t + i] = fmaf(v[i] * b, __uint_as_float(p[t + i]), acc[t + i]);
   }
 }
 
@@ -143,19 +136,24 @@ __device__ __forceinline__ void block_product(float (&p)[NT][4], uint32_t stage,
 
 template <int NT>
 __global__ void __launch_bounds__(kMlpThreads, 1)
-    moe_mlp_kernel(const __grid_constant__ CUtensorMap map_gu, const __grid_constant__ CUtensorMap map_gu_tail,
-                   const __grid_constant__ CUtensorMap map_d, const __grid_constant__ CUtensorMap map_d_tail,
-                   const MlpArgs a) {
+    moe_mlp_kernel(const __grid_constant__ CUtensorMap map_gu, const __grid_constant__ CUtensorMap map_d, const MlpArgs a) {
   constexpr int NC = 8 * NT;  // token columns
+  // partial products in tensor memory: at most eight K-blocks side by side
+  constexpr int kBufCols = 8 * NC, kBufs = kTmemCols / kBufCols;
+  static_assert(kBufs <= kMaxBufs, "their barriers");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
   const uint32_t ring = smem_u32(smem);
   const uint32_t area = ring + (uint32_t)a.stages * kStageBytes;
   uint8_t* misc = smem + a.off_misc;
-  const uint32_t full0 = smem_u32(misc + kOffBars), empty0 = full0 + 8 * kMlpMaxStages, hfull0 = empty0 + 8 * kMlpMaxStages,
-                 hempty0 = hfull0 + 16;
-  float* s_scale = reinterpret_cast<float*>(smem + a.off_scale);  // of the codes: [block][NC], each buffer of the second part
+  const uint32_t full0 = smem_u32(misc + kOffBars), empty0 = full0 + 8 * kMlpMaxStages, tfull0 = empty0 + 8 * kMlpMaxStages,
+                 tempty0 = tfull0 + 8 * kMaxBufs, hfull0 = tempty0 + 8 * kMaxBufs, hempty0 = hfull0 + 8 * kMlpMaxBuffers,
+                 sfull0 = hempty0 + 8 * kMlpMaxBuffers, sempty0 = sfull0 + 8 * kSlots, xready = sempty0 + 8 * kSlots,
+                 drain = xready + 8;
+  // scales of the codes, [block][NC]; in the second part each buffer's
+  float* s_scale = reinterpret_cast<float*>(smem + a.off_scale);
+  float* s_wsc = reinterpret_cast<float*>(misc + kOffWsc);
   float* s_red = reinterpret_cast<float*>(misc + kOffRed);
   uint32_t* s_mask = reinterpret_cast<uint32_t*>(misc + kOffMask);
   uint32_t* s_expert = reinterpret_cast<uint32_t*>(misc + kOffExpert);
@@ -164,29 +162,73 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
   float* s_weight = reinterpret_cast<float*>(misc + kOffWeight);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + kOffFlag);
   volatile int* never = abort_flag + 1;
-  int* s_scan = reinterpret_cast<int*>(misc + kOffFlag + 8);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc + kOffFlag + 8);
+  int* s_scan = reinterpret_cast<int*>(misc + kOffFlag + 16);
   const int tid = (int)threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
   const int ST = a.stages, slots = a.T * a.k;
+  pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, kMmaWarps);
+      mbar_init(empty0 + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(hfull0 + 8 * i, kQuantWarps);
-      mbar_init(hempty0 + 8 * i, kMmaWarps);
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(tfull0 + 8 * i, 1);
+      mbar_init(tempty0 + 8 * i, 4);
     }
+    for (int i = 0; i < kMlpMaxBuffers; ++i) {
+      mbar_init(hfull0 + 8 * i, kCoders);
+      mbar_init(hempty0 + 8 * i, 4);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(sfull0 + 8 * i, 32);  // one cp.async arrival a lane
+      mbar_init(sempty0 + 8 * i, 4);
+    }
+    mbar_init(xready, kMlpThreads / 32 - 1 - kIssuers);
+    mbar_init(drain, kIssuers);
     *abort_flag = 0;
     *never = 0;
     fence_barrier_init();
     fence_proxy_async_shared();
     tma_prefetch_desc(&map_gu);
     tma_prefetch_desc(&map_d);
-    if (a.K % kBlock) tma_prefetch_desc(&map_gu_tail);
-    if (a.I % kBlock) tma_prefetch_desc(&map_d_tail);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+    tmem_relinquish();
   }
   for (int e = tid; e < a.E; e += kMlpThreads) s_mask[e] = 0;
   pdl_wait();
+  // The first of the tokens' values are on their way while the plan is made (half h of warps 2, 4, 5, .. takes the groups h,
+  // h + kHalves, ..; later they would wait behind the weights).
+  const int Kb = (int)cdiv(a.K, kBlock), Ib = (int)cdiv(a.I, kBlock);
+  const int l16 = lane & 15, half = 2 * (warp == 2 ? 0 : warp - 3) + (lane >> 4), groups = a.T * Kb;
+  constexpr int kHalves = 2 * (kMlpThreads / 32 - 1 - kIssuers), kBatch = 6;
+  uint4 xv[kBatch];
+  int x_t = half / Kb, x_kb = half - x_t * Kb;  // token and K-block of the half's next group
+  auto load_tokens = [&](int g0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (g0 + i * kHalves >= groups) break;
+      const int k = x_kb * kBlock + 8 * l16;
+      xv[i] = make_uint4(0, 0, 0, 0);
+      if (x_t < a.T && k < a.K) {
+        const uint16_t* p = a.x + (int64_t)x_t * a.ldx + k;
+        if (a.vec) {
+          xv[i] = __ldg(reinterpret_cast<const uint4*>(p));
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w[q] = (k + 2 * q < a.K ? (uint32_t)__ldg(p + 2 * q) : 0u) |
+                   (k + 2 * q + 1 < a.K ? (uint32_t)__ldg(p + 2 * q + 1) : 0u) << 16;
+          xv[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      for (x_kb += kHalves; x_kb >= Kb; x_kb -= Kb) ++x_t;
+    }
+  };
+  if (warp == 2 || warp >= 4) load_tokens(0);
   __syncthreads();
   // ------------------------------------------------------------ plan: the reached experts in order, their slots by token
   for (int s = tid; s < slots; s += kMlpThreads) {
@@ -226,7 +268,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
         const int at = before >> 16;
         s_expert[at] = (uint32_t)(4 * tid + i) | m[i] << 16;
         s_start[at] = before & 0xFFFF;
-        s_mask[4 * tid + i] = (uint32_t)(before & 0xFFFF) << 16 | m[i];  // (the slots' pass needs both)
+        s_mask[4 * tid + i] = (uint32_t)(before & 0xFFFF) << 16 | m[i];
         before += (1 << 16) + __popc(m[i]);
       }
     __syncthreads();
@@ -234,21 +276,23 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
       const int e = __ldg(a.idx + s);
       if (e < 0 || e >= a.E) continue;
       const uint32_t v = s_mask[e];
-      s_slot[(v >> 16) + __popc(v & ((1u << (s / a.k)) - 1u))] = s;
+      const int t = s / a.k;
+      s_slot[(v >> 16) + __popc(v & ((1u << t) - 1u))] = s | t << 16;
     }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
   }
+  const uint32_t tmem_base = *tmem_holder;
 
   const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
-  const int Kf = a.K / kBlock, If = a.I / kBlock;                           // whole K-blocks
-  const int Kb = (int)cdiv(a.K, kBlock), Ib = (int)cdiv(a.I, kBlock);
-  const int items1 = (int)cdiv(Kf, kUnitBlocks) + (Kb > Kf ? 1 : 0);        // stages of a unit
-  const int per_expert = a.I / kUnit, units = reached * per_expert;
+  const int items1 = (int)cdiv(Kb, kUnitBlocks);                            // stages of a unit
+  const int per_expert = a.I / kPairs, units = reached * per_expert;
   const int u0 = (int)((int64_t)units * cta / grid), u1 = (int)((int64_t)units * (cta + 1) / grid);
-  const int n0 = cta * a.rows;                                              // second part: rows of D
-  const int blocks2 = a.blocks;                                             // K-blocks of a stage of the second part
-  const int items2 = (int)cdiv(If, blocks2) + (Ib > If ? 1 : 0);
-  const bool second = n0 < a.N;
+  const int n0 = cta * a.rows;                                              // second part: rows of D, in groups of
+  const int group = a.group, blocks2 = 128 / group;                         // `group` rows of `blocks2` K-blocks a stage
+  const int items2 = (int)cdiv(Ib, blocks2);
+  const int experts2 = n0 < a.N ? reached : 0;
   auto fail = [&](uint32_t code) {
     if (!*abort_flag) atomicOr(&g_mlp_error, code);
     *abort_flag = 1;
@@ -257,330 +301,384 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int n = 0;
+      Ring at{0, 0};
+      int issued = 0;
       bool ok = true;
       auto stage = [&](uint32_t bytes) {  // the next stage, free; its barrier expects `bytes`
-        const int st = n % ST;
-        ok = mbar_wait_bounded(empty0 + 8 * st, (uint32_t)((n / ST) & 1) ^ 1u, kWaitLimitNs, abort_flag);
+        const int st = at.at;
+        ok = mbar_wait_bounded(empty0 + 8 * st, at.parity ^ 1u, kWaitLimitNs, abort_flag);
         if (!ok) {
           fail(1u);
           return -1;
         }
         mbar_arrive_expect_tx(full0 + 8 * st, bytes);
-        ++n;
+        at.step(1, ST);
+        ++issued;
         return st;
       };
       for (int u = u0; u < u1 && ok; ++u) {
-        const int r = u / per_expert, i0 = (u - r * per_expert) * kUnit, e = (int)(s_expert[r] & 0xFFFFu);
-        for (int j = 0; j < items1 && ok; ++j) {
-          const bool tail = j * kUnitBlocks >= Kf;
-          const int st = stage(tail ? 2 * kAtom : kStageBytes);
+        const int r = u / per_expert, i0 = (u - r * per_expert) * kPairs, e = (int)(s_expert[r] & 0xFFFFu);
+        for (int kb0 = 0; kb0 < Kb; kb0 += kUnitBlocks) {
+          const int blocks = min(kUnitBlocks, Kb - kb0);
+          const int st = stage((uint32_t)(blocks * kUnitRows * kBlock));
           if (st < 0) break;
-          if (!tail) tma_load_5d(ring + st * kStageBytes, &map_gu, full0 + 8 * st, 0, i0, j * kUnitBlocks, 0, e);
-          else tma_load_4d(ring + st * kStageBytes, &map_gu_tail, full0 + 8 * st, Kf * kBlock, i0, 0, e);
+          for (int b = 0; b < blocks; ++b)
+            tma_load_4d(ring + st * kStageBytes + b * kUnitRows * kBlock, &map_gu, full0 + 8 * st, (kb0 + b) * kBlock, i0, 0, e);
         }
       }
-      for (int r = 0; second && r < reached && ok; ++r) {
+      for (int r = 0; r < experts2 && ok; ++r) {
         const int e = (int)(s_expert[r] & 0xFFFFu);
-        for (int j = 0; j < items2 && ok; ++j) {
-          const bool tail = j * blocks2 >= If;
-          const int st = stage((uint32_t)((tail ? 1 : blocks2) * a.rows * kBlock));
+        for (int kb0 = 0; kb0 < Ib; kb0 += blocks2) {
+          const int blocks = min(blocks2, Ib - kb0);
+          const int st = stage((uint32_t)(blocks * a.rows * kBlock));
           if (st < 0) break;
-          if (!tail) tma_load_4d(ring + st * kStageBytes, &map_d, full0 + 8 * st, 0, n0, j * blocks2, e);
-          else tma_load_3d(ring + st * kStageBytes, &map_d_tail, full0 + 8 * st, If * kBlock, n0, e);
+          for (int b = 0; b < blocks; ++b)
+            tma_load_3d(ring + st * kStageBytes + b * group * kBlock, &map_d, full0 + 8 * st, (kb0 + b) * kBlock, n0, e);
         }
       }
       if (!ok)  // copies already issued land before this CTA's shared memory goes away
-        for (int i = n > ST ? n - ST : 0; i < n; ++i)
+        for (int i = issued > ST ? issued - ST : 0; i < issued; ++i)
           mbar_wait_bounded(full0 + 8 * (i % ST), (uint32_t)((i / ST) & 1), kWaitLimitNs, never);
     }
-    return;
-  }
-
-  // ------------------------------------------------------------ the tokens' codes, by all other warps
-  {
-    const int half = (tid - 32) >> 4, halves = (kMlpThreads - 32) >> 4, l16 = lane & 15;
-    const int groups = a.T * Kb;
-    for (int g0 = 0; g0 < groups; g0 += 2 * halves) {
-      uint4 v[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int g = g0 + half + i * halves, t = g / Kb, k = (g - t * Kb) * kBlock + 8 * l16;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (g < groups && k < a.K) {
-          const uint16_t* p = a.x + (int64_t)t * a.ldx + k;
-          if (a.vec) {
-            v[i] = __ldg(reinterpret_cast<const uint4*>(p));
-          } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              w[q] = (k + 2 * q < a.K ? (uint32_t)__ldg(p + 2 * q) : 0u) |
-                     (k + 2 * q + 1 < a.K ? (uint32_t)__ldg(p + 2 * q + 1) : 0u) << 16;
-            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ MMA issuers
+    if (lane == 0) {
+      const int me = warp >> 1;
+      Ring at{me, 0}, buf{me, 0};  // (both rings have a place an issuer at least)
+      int n = 0;                   // stages of all issuers
+      bool ok = true;
+      auto issue = [&](uint32_t codes, uint32_t idesc) {
+        ok = mbar_spin_bounded(tempty0 + 8 * buf.at, buf.parity ^ 1u, kWaitLimitNs, abort_flag) &&
+             mbar_spin_bounded(full0 + 8 * at.at, at.parity, kWaitLimitNs, abort_flag);
+        if (!ok) {
+          fail(2u);
+          return;
         }
-      }
+        tc_fence_after();
+        const uint64_t da = desc_kmajor_sw128(ring + (uint32_t)(at.at * kStageBytes)), db = desc_kmajor_sw128(codes);
+        const uint32_t d = tmem_base + (uint32_t)(buf.at * kBufCols);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int g = g0 + half + i * halves, t = g / Kb, kb = g - t * Kb;
+        for (int k = 0; k < kBlock / 32; ++k) mma_e4m3(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), idesc, k > 0 ? 1u : 0u);
+        mma_commit(empty0 + 8 * at.at);
+        mma_commit(tfull0 + 8 * buf.at);
+        at.step(kIssuers, ST);
+        buf.step(kIssuers, kBufs);
+      };
+      ok = mbar_wait_bounded(xready, 0, kWaitLimitNs, abort_flag);
+      if (!ok) fail(2u);
+      constexpr uint32_t idesc1 = idesc_e4m3_f32(128, kUnitBlocks * NC);
+      for (int u = u0; u < u1 && ok; ++u)
+        for (int j = 0; j < items1 && ok; ++j, ++n)
+          if (n % kIssuers == me) issue(area + (uint32_t)(j * kUnitBlocks * NT * kAtom), idesc1);
+      const uint32_t idesc2 = idesc_e4m3_f32(128, max(blocks2 * NC, 16));
+      Ring h{0, 0};
+      for (int r = 0; r < experts2 && ok; ++r) {
+        ok = mbar_wait_bounded(hfull0 + 8 * h.at, h.parity, 2 * kWaitLimitNs, abort_flag);
+        if (!ok) fail(4u);
+        for (int j = 0; j < items2 && ok; ++j, ++n)
+          if (n % kIssuers == me) issue(area + (uint32_t)((h.at * Ib + j * blocks2) * NT * kAtom), idesc2);
+        h.step(1, a.buffers);
+      }
+      // every MMA issued completes before tensor memory is released
+      mma_commit(drain);
+      if (!mbar_wait_bounded(drain, 0, kWaitLimitNs, never)) fail(32u);
+    }
+  } else {
+    // ------------------------------------------------------------ the tokens' codes, by all of these warps
+    int t = half / Kb, kb = half - t * Kb;
+    for (int g0 = 0; g0 < groups; g0 += kBatch * kHalves) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) v[i] = xv[i];
+      if (g0 + kBatch * kHalves < groups) load_tokens(g0 + kBatch * kHalves);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (g0 + i * kHalves >= groups) break;
         uint32_t m = amax2(amax2(v[i].x, v[i].y), amax2(v[i].z, v[i].w));
         m = amax2(m, __byte_perm(m, 0, 0x1032));
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) m = amax2(m, __shfl_xor_sync(kAll, m, o));
-        const float s = scale_near(__uint_as_float(m & 0x7FFF0000u));
-        const uint32_t lo = codes2(v[i].x, s) | codes2(v[i].y, s) << 16, hi = codes2(v[i].z, s) | codes2(v[i].w, s) << 16;
-        if (g < groups) {
+        // (neg_codes2 gives the codes of the IEEE quotient for this scale too: checked exhaustively on the CPU)
+        const float s = scale_near(__uint_as_float(m & 0x7FFF0000u)), ny = neg_rcp(s);
+        const uint64_t s2 = f2_pack(s, s), ny2 = f2_pack(ny, ny);
+        const uint32_t lo = (neg_codes2(v[i].x, s2, ny2) | neg_codes2(v[i].y, s2, ny2) << 16) ^ 0x80808080u;
+        const uint32_t hi = (neg_codes2(v[i].z, s2, ny2) | neg_codes2(v[i].w, s2, ny2) << 16) ^ 0x80808080u;
+        if (t < a.T) {
           const uint32_t at = area + (uint32_t)((kb * NT + (t >> 3)) * kAtom + (t & 7) * 128 +
                                                 (((l16 >> 1) ^ (t & 7)) << 4) + 8 * (l16 & 1));
           asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(lo), "r"(hi) : "memory");
           if (l16 == 0) s_scale[kb * NC + t] = s;
         }
+        for (kb += kHalves; kb >= Kb; kb -= Kb) ++t;
       }
     }
-  }
-  named_sync(1, kMlpThreads - 32);
+    fence_proxy_async_shared();  // the MMA reads the codes
+    __syncwarp();
+    if (lane == 0) mbar_arrive(xready);
 
-  if (warp <= kMmaWarps) {
-    // ------------------------------------------------------------ products
-    const int cw = warp - 1, ct = tid - 32, g = lane >> 2, t2 = 2 * (lane & 3);
-    int n = 0, turn = 0;
-    bool ok = true;
-    auto wait_full = [&]() {
-      const int st = n % ST;
-      const bool in = mbar_wait_bounded(full0 + 8 * st, (uint32_t)((n / ST) & 1), kWaitLimitNs, abort_flag);
-      if (__all_sync(kAll, in)) return true;
-      if (lane == 0) fail(2u);
-      return false;
-    };
-    auto release = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8 * (n % ST));
-      ++n;
-    };
-    float acc[NT][4];
-    // the scales of 32 stages of a unit, stage l's in lane l, fetched a unit ahead
-    const int Nb1 = (int)cdiv(2 * a.I, kBlock);
-    auto unit_scales = [&](int u, int j0, float& sg, float& su) {
-      sg = su = 0.0f;
-      if (u >= u1) return;
-      const int r = u / per_expert, i0 = (u - r * per_expert) * kUnit, e = (int)(s_expert[r] & 0xFFFFu);
-      const int j = j0 + lane, kb = j * kUnitBlocks >= Kf ? Kf : j * kUnitBlocks + cw;
-      if (j < items1 && kb < Kb) {
-        sg = __ldg(a.sgu + ((int64_t)e * Nb1 + i0 / kBlock) * a.ldsgu + kb);
-        su = __ldg(a.sgu + ((int64_t)e * Nb1 + (a.I + i0) / kBlock) * a.ldsgu + kb);
-      }
-    };
-    float sg, su, sg_next, su_next;
-    unit_scales(u0, 0, sg_next, su_next);
-    // (a warp whose wait gave up goes on through the units without their stages, so that the barriers between them match)
-    for (int u = u0; u < u1; ++u) {
-      sg = sg_next, su = su_next;
-      unit_scales(u + 1, 0, sg_next, su_next);
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][q] = 0.0f;
-      for (int j = 0; j < items1 && ok; ++j) {
-        if (j > 0 && (j & 31) == 0) unit_scales(u, j, sg, su);
-        if (!(ok = wait_full())) break;
-        const bool tail = j * kUnitBlocks >= Kf;
-        const int kb = tail ? Kf : j * kUnitBlocks + cw;
-        const float bg = __shfl_sync(kAll, sg, j & 31), bu = __shfl_sync(kAll, su, j & 31);
-        if (tail ? cw == 0 : kb < Kf) {
-          float p[NT][4];
-          const int at = tail ? 0 : cw, up = tail ? 1 : kUnitBlocks;
-          block_product<NT>(p, ring + (n % ST) * kStageBytes, 8 * at, 8 * (up + at), area + (uint32_t)(kb * NT * kAtom), lane);
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const float2 xs = *reinterpret_cast<const float2*>(s_scale + kb * NC + 8 * i + t2);
-            acc[i][0] = fmaf(xs.x * bg, p[i][0], acc[i][0]);
-            acc[i][1] = fmaf(xs.y * bg, p[i][1], acc[i][1]);
-            acc[i][2] = fmaf(xs.x * bu, p[i][2], acc[i][2]);
-            acc[i][3] = fmaf(xs.y * bu, p[i][3], acc[i][3]);
+    if (warp == 2) {
+      // ------------------------------------------------------------ the weights' scales
+      Ring slot{0, 0};
+      const int Nb1 = 2 * a.I / kBlock, Nb2 = (int)cdiv(a.N, kBlock);
+      bool ok = true;
+      // `stages` stages of `per` scales, lane l of a slot the scale l % per of its stage l / per: at(stage, scale), null
+      // where there is none
+      auto run = [&](int stages, int per, auto&& address) {
+        for (int before = 0; before < stages && ok; before += 32 / per) {
+          const bool free = mbar_wait_bounded(sempty0 + 8 * slot.at, slot.parity ^ 1u, kWaitLimitNs, abort_flag);
+          if (!(ok = __all_sync(kAll, free))) {
+            if (lane == 0) fail(64u);
+            break;
           }
-        }
-        release();
-      }
-      float* red = s_red + turn * (kMmaWarps * 16 * NC);
-      turn ^= 1;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        *reinterpret_cast<float2*>(red + (cw * 16 + g) * NC + 8 * i + t2) = make_float2(acc[i][0], acc[i][1]);
-        *reinterpret_cast<float2*>(red + (cw * 16 + g + 8) * NC + 8 * i + t2) = make_float2(acc[i][2], acc[i][3]);
-      }
-      named_sync(2, 32 * kMmaWarps);
-      if (ct < kUnit * NC) {
-        const int t = ct / kUnit, i = ct % kUnit;
-        const int r = u / per_expert, i0 = (u - r * per_expert) * kUnit;
-        const uint32_t mask = s_expert[r] >> 16;
-        if (mask >> t & 1u) {
-          float gate = 0.0f, up = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kMmaWarps; ++w) {
-            gate += red[(w * 16 + i) * NC + t];
-            up += red[(w * 16 + 8 + i) * NC + t];
-          }
-          const int slot = s_slot[s_start[r] + __popc(mask & ((1u << t) - 1u))];
-          a.act[(int64_t)slot * a.I + i0 + i] = gate / (1.0f + expf(-gate)) * up;
-        }
-      }
-    }
-    // the activations of this CTA are written: one arrival a CTA (not where a wait gave up: the others' give up too)
-    named_sync(2, 32 * kMmaWarps);
-    if (ct == 0 && ok) {
-      __threadfence();
-      atomicAdd(a.arrived, 1u);
-    }
-
-    if (second) {
-      const int mt = cw % a.mtiles, split = cw / a.mtiles;  // 16 rows, K-block of a stage
-      const int Nb2 = (int)cdiv(a.N, kBlock);
-      const int row0 = min(n0 + 16 * mt, a.N - 1) / kBlock, row1 = min(n0 + 16 * mt + 15, a.N - 1) / kBlock;
-      const bool hi0 = min(n0 + 16 * mt + g, a.N - 1) / kBlock != row0, hi1 = min(n0 + 16 * mt + g + 8, a.N - 1) / kBlock != row0;
-      auto expert_scales = [&](int r, int j0, float& s0, float& s1) {
-        s0 = s1 = 0.0f;
-        if (r >= reached) return;
-        const int e = (int)(s_expert[r] & 0xFFFFu), j = j0 + lane;
-        const int kb = j * blocks2 >= If ? If : j * blocks2 + split;
-        if (j < items2 && kb < Ib) {
-          s0 = __ldg(a.sd + ((int64_t)e * Nb2 + row0) * a.ldsd + kb);
-          s1 = __ldg(a.sd + ((int64_t)e * Nb2 + row1) * a.ldsd + kb);
+          const int n = before + lane / per;
+          const float* from = n < stages ? address(n, lane % per) : nullptr;
+          if (from) cp_async_4(smem_u32(s_wsc + slot.at * 32 + lane), from, 4u);
+          cp_async_mbar_arrive(sfull0 + 8 * slot.at);
+          slot.step(1, kSlots);
         }
       };
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][q] = 0.0f;
-      float s0, s1, s0_next, s1_next;
-      expert_scales(0, 0, s0_next, s1_next);
-      for (int r = 0; r < reached && ok; ++r) {
-        s0 = s0_next, s1 = s1_next;
-        expert_scales(r + 1, 0, s0_next, s1_next);
-        const int buf = r % a.buffers;
-        const uint32_t codes = area + (uint32_t)(buf * Ib * NT * kAtom);
-        const float* scales = s_scale + buf * Ib * NC;
-        const uint32_t mask = s_expert[r] >> 16;
-        const bool there = mbar_wait_bounded(hfull0 + 8 * buf, (uint32_t)((r / a.buffers) & 1), 2 * kWaitLimitNs, abort_flag);
-        if (!(ok = __all_sync(kAll, there))) {
-          if (lane == 0) fail(4u);
-          break;
+      run((u1 - u0) * items1, 2 * kUnitBlocks, [&](int n, int i) -> const float* {
+        const int u = u0 + n / items1, r = u / per_expert, kb = (n % items1) * kUnitBlocks + (i >> 1);
+        const int row = (u - r * per_expert) * kPairs + (i & 1) * a.I;
+        return kb < Kb ? a.sgu + ((int64_t)(s_expert[r] & 0xFFFFu) * Nb1 + row / kBlock) * a.ldsgu + kb : nullptr;
+      });
+      run(experts2 * items2, 2 * blocks2, [&](int n, int i) -> const float* {
+        const int r = n / items2, kb = (n % items2) * blocks2 + (i >> 1), tile = n0 / kBlock + (i & 1);
+        return kb < Ib && tile < Nb2 ? a.sd + ((int64_t)(s_expert[r] & 0xFFFFu) * Nb2 + tile) * a.ldsd + kb : nullptr;
+      });
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= 4 && warp < 8) {
+      // ------------------------------------------------------------ promotion
+      const int w = warp - 4, ct = tid - 128;
+      const uint32_t lane_base = (uint32_t)(32 * w) << 16;
+      Ring at{0, 0}, slot{0, 0};
+      int in_slot = 0;
+      bool ok = mbar_wait_bounded(xready, 0, kWaitLimitNs, abort_flag);
+      ok = __all_sync(kAll, ok);
+      auto wait_product = [&]() {
+        const bool in = mbar_wait_bounded(tfull0 + 8 * at.at, at.parity, kWaitLimitNs, abort_flag);
+        if (__all_sync(kAll, in)) {
+          tc_fence_after();
+          return true;
         }
-        for (int j = 0; j < items2; ++j) {
-          if (j > 0 && (j & 31) == 0) expert_scales(r, j, s0, s1);
-          if (!(ok = wait_full())) break;
-          const bool tail = j * blocks2 >= If;
-          const int kb = tail ? If : j * blocks2 + split;
-          const float b0 = __shfl_sync(kAll, s0, j & 31), b1 = __shfl_sync(kAll, s1, j & 31);
-          if (tail ? split == 0 : kb < If) {
-            float p[NT][4];
-            const int line = (tail ? 0 : split) * a.rows + 16 * mt;
-            block_product<NT>(p, ring + (n % ST) * kStageBytes, line, line + 8, codes + (uint32_t)(kb * NT * kAtom), lane);
-            const float bl = hi0 ? b1 : b0, bh = hi1 ? b1 : b0;
+        if (lane == 0) fail(8u);
+        return false;
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty0 + 8 * at.at);
+        at.step(1, kBufs);
+      };
+      // this thread's scale in the stage, of `per` in the stage, slot by slot
+      auto next_scale = [&](int per, int which, float& b) {
+        if (in_slot == 0) {
+          const bool there = mbar_wait_bounded(sfull0 + 8 * slot.at, slot.parity, kWaitLimitNs, abort_flag);
+          if (!__all_sync(kAll, there)) {
+            if (lane == 0) fail(64u);
+            return false;
+          }
+        }
+        b = s_wsc[slot.at * 32 + in_slot + which];
+        in_slot += per;
+        return true;
+      };
+      auto leave_slot = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty0 + 8 * slot.at);
+        slot.step(1, kSlots);
+        in_slot = 0;
+      };
+      float acc[NC];
+      auto write_sums = [&](float* red) {  // this thread's row of the 128
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              // (columns of tokens that are not this expert's hold whatever was in the buffer)
-              const float2 hs = *reinterpret_cast<const float2*>(scales + kb * NC + 8 * i + t2);
-              if (mask >> (8 * i + t2) & 1u) {
-                acc[i][0] = fmaf(hs.x * bl, p[i][0], acc[i][0]);
-                acc[i][2] = fmaf(hs.x * bh, p[i][2], acc[i][2]);
-              }
-              if (mask >> (8 * i + t2 + 1) & 1u) {
-                acc[i][1] = fmaf(hs.y * bl, p[i][1], acc[i][1]);
-                acc[i][3] = fmaf(hs.y * bh, p[i][3], acc[i][3]);
-              }
-            }
+        for (int t = 0; t < NC; t += 4)
+          *reinterpret_cast<float4*>(red + ct * NC + ((t + 4 * (ct >> 1)) & (NC - 1))) =
+              make_float4(acc[t], acc[t + 1], acc[t + 2], acc[t + 3]);
+      };
+      auto sum_at = [&](const float* red, int row, int t) {  // (rows' tokens are rotated: fewer bank conflicts)
+        return red[row * NC + (((t & ~3) + 4 * (row >> 1)) & (NC - 1)) + (t & 3)];
+      };
+      // First part: lane's row is half (lane / 16: gate, up) of pair lane % 16, K-block w of the stage.
+      int turn = 0;
+      // (a warp whose wait gave up goes on through the units without their stages, so that the barriers between them match)
+      for (int u = u0; u < u1; ++u) {
+#pragma unroll
+        for (int t = 0; t < NC; ++t) acc[t] = 0.0f;
+        for (int j = 0; j < items1 && ok; ++j) {
+          float b;
+          if (!(ok = next_scale(2 * kUnitBlocks, 2 * w + (lane >> 4), b) && wait_product())) break;
+          if (in_slot == 32) leave_slot();
+          const int kb = j * kUnitBlocks + w;
+          if (kb < Kb) {
+            uint32_t p[NC];
+            tmem_cols<NC>(tmem_base + lane_base + (uint32_t)(at.at * kBufCols + w * NC), p);
+            promote<NC, false>(acc, p, s_scale + kb * NC, b, 0u);
           }
           release();
         }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(hempty0 + 8 * buf);
-      }
-      // sums of the splits; y (also where no expert was reached: zeros)
-      float* red = s_red + turn * (kMmaWarps * 16 * NC);
+        float* red = s_red + turn * (128 * NC);
+        turn ^= 1;
+        write_sums(red);
+        named_sync(2, 128);
+        const int r = u / per_expert, i0 = (u - r * per_expert) * kPairs;
+        const uint32_t mask = s_expert[r] >> 16;
+        for (int o = ct; o < kPairs * NC; o += 128) {
+          const int t = o / kPairs, i = o % kPairs;
+          if (mask >> t & 1u) {
+            float gate = 0.0f, up = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        *reinterpret_cast<float2*>(red + (cw * 16 + g) * NC + 8 * i + t2) = make_float2(acc[i][0], acc[i][1]);
-        *reinterpret_cast<float2*>(red + (cw * 16 + g + 8) * NC + 8 * i + t2) = make_float2(acc[i][2], acc[i][3]);
-      }
-      named_sync(2, 32 * kMmaWarps);
-      const int rows = min(a.rows, a.N - n0);
-      if (ok)
-        for (int i = ct; i < rows * a.T; i += 32 * kMmaWarps) {
-          const int t = i / rows, row = i - t * rows;
-          float sum = 0.0f;
-          for (int s = 0; s < kMmaWarps / a.mtiles; ++s)
-            sum += red[((s * a.mtiles + row / 16) * 16 + row % 16) * NC + t];
-          a.y[(int64_t)t * a.ldy + n0 + row] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
+            for (int b = 0; b < kUnitBlocks; ++b) {
+              gate += sum_at(red, b * kUnitRows + i, t);
+              up += sum_at(red, b * kUnitRows + kPairs + i, t);
+            }
+            const int slot = s_slot[s_start[r] + __popc(mask & ((1u << t) - 1u))] & 0xFFFF;
+            a.act[(int64_t)slot * a.I + i0 + i] = gate / (1.0f + expf(-gate)) * up;
+          }
         }
-    }
-  } else if (second && reached > 0) {
-    // ------------------------------------------------------------ the activations' codes
-    const int half = (tid - 32 * (1 + kMmaWarps)) >> 4, l16 = lane & 15;
-    constexpr int kHalves = 2 * kQuantWarps;
-    bool ok = true;
-    {
-      const uint64_t t0 = globaltimer_ns();
-      while (ld_acquire_gpu(a.arrived) < (uint32_t)grid)
-        if (*abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) {
-          ok = ld_acquire_gpu(a.arrived) >= (uint32_t)grid;
-          break;
-        }
-      ok = __all_sync(kAll, ok);
-      if (!ok && lane == 0) fail(8u);
-    }
-    for (int r = 0; r < reached && ok; ++r) {
-      const int buf = r % a.buffers;
-      const bool free = mbar_wait_bounded(hempty0 + 8 * buf, (uint32_t)((r / a.buffers) & 1) ^ 1u, kWaitLimitNs, abort_flag);
-      if (!(ok = __all_sync(kAll, free))) {
-        if (lane == 0) fail(16u);
-        break;
       }
-      const uint32_t mask = s_expert[r] >> 16, codes = area + (uint32_t)(buf * Ib * NT * kAtom);
-      float* scales = s_scale + buf * Ib * NC;
-      const int count = __popc(mask), groups = count * Ib;
-      for (int g0 = 0; g0 < groups; g0 += 2 * kHalves) {
-        float4 v[2][2];
-        int tok[2], blk[2], slot[2];
+      // The activations of this CTA are written: one arrival a CTA.  (Where a wait gave up there is none; the others'
+      // waits for it then give up too.)
+      named_sync(2, 128);
+      if (ct == 0 && ok) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.arrived) : "memory");
+
+      // Second part: row 32 w + lane is K-block (32 w + lane) / group of the stage, row (32 w + lane) % group of the CTA's.
+      if (n0 < a.N) {
+        const int block = ct / group, row = ct & (group - 1);
+        const int tile = (n0 % kBlock + row) / kBlock & 1;  // of the two that the CTA's rows may touch
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int g = g0 + half + i * kHalves, c = g / Ib;
-          blk[i] = g - c * Ib;
-          v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          slot[i] = tok[i] = 0;
-          if (g < groups) {
-            slot[i] = s_slot[s_start[r] + c];
-            tok[i] = slot[i] / a.k;
-            const int k = blk[i] * kBlock + 8 * l16;
-            if (k < a.I) {
-              const float4* p = reinterpret_cast<const float4*>(a.act + (int64_t)slot[i] * a.I + k);
-              v[i][0] = __ldcg(p);
-              v[i][1] = __ldcg(p + 1);
+        for (int t = 0; t < NC; ++t) acc[t] = 0.0f;
+        if (in_slot > 0) leave_slot();  // (the second part begins with a slot of its own)
+        Ring h{0, 0};
+        for (int r = 0; r < experts2 && ok; ++r, h.step(1, a.buffers)) {
+          const int buf = h.at;
+          const float* scales = s_scale + buf * Ib * NC;
+          const uint32_t mask = s_expert[r] >> 16;
+          const bool there = mbar_wait_bounded(hfull0 + 8 * buf, h.parity, 2 * kWaitLimitNs, abort_flag);
+          if (!(ok = __all_sync(kAll, there))) {
+            if (lane == 0) fail(4u);
+            break;
+          }
+          for (int j = 0; j < items2; ++j) {
+            float b;
+            if (!(ok = next_scale(2 * blocks2, 2 * block + tile, b) && wait_product())) break;
+            if (in_slot == 32) leave_slot();
+            const int kb = j * blocks2 + block;
+            const uint32_t from = tmem_base + lane_base + (uint32_t)(at.at * kBufCols);
+            uint32_t p[NC];
+            if (group == 16) {  // two K-blocks in a warp
+              uint32_t q[2 * NC];
+              tmem_cols<2 * NC>(from + (uint32_t)(2 * w * NC), q);
+#pragma unroll
+              for (int t = 0; t < NC; ++t) p[t] = lane < 16 ? q[t] : q[NC + t];
+            } else {
+              tmem_cols<NC>(from + (uint32_t)(32 * w / group * NC), p);
+            }
+            if (kb < Ib) promote<NC, true>(acc, p, scales + kb * NC, b, mask);
+            release();
+          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(hempty0 + 8 * buf);
+        }
+        // sums of the K-blocks; y (also where no expert was reached: zeros)
+        float* red = s_red + turn * (128 * NC);
+        write_sums(red);
+        named_sync(2, 128);
+        const int rows = min(a.rows, a.N - n0);
+        if (ok)
+          for (int o = ct; o < rows * a.T; o += 128) {
+            const int t = o / rows, i = o - t * rows;
+            float sum = 0.0f;
+            for (int b = 0; b < blocks2; ++b) sum += sum_at(red, b * group + i, t);
+            a.y[(int64_t)t * a.ldy + n0 + i] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
+          }
+      }
+    } else if (experts2 > 0) {
+      // ------------------------------------------------------------ the activations' codes
+      // Teams of the six warps take an expert each, in turn: six teams, three where an expert's tokens have more groups
+      // than a warp loads at once, and no more teams than buffers (a team that is a whole turn of the
+      // buffers ahead of another could not tell the phases of their barriers apart).
+      const int coder = warp - 8;
+      const int want = slots * Ib > 2 * kActBatch * reached ? 3 : 6, most = min(want, a.buffers);
+      const int teams = most >= 6 ? 6 : min(most, 3), size = kCoders / teams;
+      const int h = 2 * (coder % size) + (lane >> 4), halves = 2 * size;
+      bool ok = true;
+      if (coder == 0) {  // (one warp asks: more of them hold the arrivals up)
+        const uint64_t t0 = globaltimer_ns();
+        while (ok && ld_acquire_gpu(a.arrived) < (uint32_t)grid) ok = !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs;
+        if (!__all_sync(kAll, ok) && lane == 0) fail(16u);
+      }
+      named_sync(3, 32 * kCoders);
+      ok = !*abort_flag;
+      Ring at{0, 0};  // expert r's buffer
+      int r = coder / size;
+      for (int i = 0; i < r; ++i) at.step(1, a.buffers);
+      for (; r < experts2 && ok; r += teams) {
+        const uint32_t mask = s_expert[r] >> 16, codes = area + (uint32_t)(at.at * Ib * NT * kAtom);
+        float* scales = s_scale + at.at * Ib * NC;
+        const int first = s_start[r], of_expert = __popc(mask) * Ib;
+        int c = h / Ib, blk = h - c * Ib;  // of the half's next group: token of the expert, K-block
+        for (int g0 = 0; g0 < of_expert; g0 += kActBatch * halves) {
+          float4 v[kActBatch][2];
+          const int c0 = c, blk0 = blk;
+#pragma unroll
+          for (int i = 0; i < kActBatch; ++i) {
+            if (g0 + i * halves < of_expert) {  // (of some half of the team)
+              const int k = blk * kBlock + 8 * l16;
+              v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (g0 + i * halves + h < of_expert && k < a.I) {
+                const float4* p = reinterpret_cast<const float4*>(a.act + (int64_t)(s_slot[first + c] & 0xFFFF) * a.I + k);
+                v[i][0] = __ldcg(p);
+                v[i][1] = __ldcg(p + 1);
+              }
+              for (blk += halves; blk >= Ib; blk -= Ib) ++c;
+            }
+          }
+          if (g0 == 0) {  // the values are on their way when the buffer is asked for
+            const bool free = mbar_wait_bounded(hempty0 + 8 * at.at, at.parity ^ 1u, kWaitLimitNs, abort_flag);
+            if (!(ok = __all_sync(kAll, free))) {
+              if (lane == 0) fail(16u);
+              break;
+            }
+          }
+          c = c0, blk = blk0;
+#pragma unroll
+          for (int i = 0; i < kActBatch; ++i) {
+            if (g0 + i * halves < of_expert) {
+              const float4 p = v[i][0], q = v[i][1];
+              float m = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))),
+                              fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w))));
+#pragma unroll
+              for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+              const float s = scale_near(m), y = recip_rn(s);
+              const uint32_t lo = cvt_e4m3x2(p.x * y, p.y * y) | cvt_e4m3x2(p.z * y, p.w * y) << 16;
+              const uint32_t hi = cvt_e4m3x2(q.x * y, q.y * y) | cvt_e4m3x2(q.z * y, q.w * y) << 16;
+              if (g0 + i * halves + h < of_expert) {
+                const int slot = s_slot[first + c], t = slot >> 16;
+                const uint32_t to = codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 +
+                                                       (((l16 >> 1) ^ (t & 7)) << 4) + 8 * (l16 & 1));
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(lo), "r"(hi) : "memory");
+                if (l16 == 0) scales[blk * NC + t] = s * s_weight[slot & 0xFFFF];
+              }
+              for (blk += halves; blk >= Ib; blk -= Ib) ++c;
             }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 p = v[i][0], q = v[i][1];
-          float m = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))),
-                          fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w))));
-#pragma unroll
-          for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-          const float s = scale_near(m), y = recip_rn(s);
-          const uint32_t lo = cvt_e4m3x2(p.x * y, p.y * y) | cvt_e4m3x2(p.z * y, p.w * y) << 16;
-          const uint32_t hi = cvt_e4m3x2(q.x * y, q.y * y) | cvt_e4m3x2(q.z * y, q.w * y) << 16;
-          if (g0 + half + i * kHalves < groups) {
-            const int t = tok[i];
-            const uint32_t at = codes + (uint32_t)((blk[i] * NT + (t >> 3)) * kAtom + (t & 7) * 128 +
-                                                   (((l16 >> 1) ^ (t & 7)) << 4) + 8 * (l16 & 1));
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(lo), "r"(hi) : "memory");
-            if (l16 == 0) scales[blk[i] * NC + t] = s * s_weight[slot[i]];
-          }
-        }
+        if (!ok) break;
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane < kCoders / size) mbar_arrive(hfull0 + 8 * at.at);  // as many arrivals a team, whatever its size
+        for (int i = 0; i < teams; ++i) at.step(1, a.buffers);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(hfull0 + 8 * buf);
     }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
   }
 }
 
@@ -622,24 +720,28 @@ MlpGeom mlp_geom(int64_t T, int64_t K, int64_t I, int64_t N, int num_sms) {
   MlpGeom g = {};
   const int64_t nt = T <= 8 ? 1 : 2, Kb = cdiv(K, kBlock), Ib = cdiv(I, kBlock);
   const int64_t most = kMlpCodeBytes, x = Kb * nt * kAtom, h = Ib * nt * kAtom;
-  g.rows = (int)cdiv(N, num_sms);
-  if (x > most || h > most || g.rows > 128) return g;  // stages 0: out of range
-  g.buffers = 2 * h <= most ? 2 : 1;
+  const int64_t rows = cdiv(N, num_sms);
+  if (x > most || h > most || rows > 128) return g;  // stages 0: out of range
+  g.rows = (int)rows;
+  // Buffers of activations: two, or what the tokens' space (or 48 KB) holds; one where two pass the limit.  The ring gets
+  // what they leave.
+  int64_t room = x > 2 * h ? x : 2 * h;
+  room = room < (48 << 10) ? (48 << 10) : room < most ? room : most;
+  g.buffers = (int)(room / h < kMlpMaxBuffers ? room / h : kMlpMaxBuffers);
   const int64_t codes = x > g.buffers * h ? x : g.buffers * h;
   const int64_t scales = (Kb > g.buffers * Ib ? Kb : g.buffers * Ib) * 8 * nt * 4;
-  g.mtiles = g.rows <= 16 ? 1 : g.rows <= 32 ? 2 : g.rows <= 64 ? 4 : 8;
-  g.blocks = kMmaWarps / g.mtiles;
-  const int64_t rest = codes + (scales + 15) / 16 * 16 + kMiscBytes;
-  int64_t stages = ((int64_t)227 * 1024 - 1024 - rest) / kStageBytes;
+  g.group = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int64_t stages = ((int64_t)227 * 1024 - 1024 - codes - scales - kMiscBytes) / kStageBytes;
   g.stages = (int)(stages < kMlpMaxStages ? stages : kMlpMaxStages);
   g.off_scale = (int)(g.stages * kStageBytes + codes);
-  g.off_misc = (int)(g.off_scale + (scales + 15) / 16 * 16);
+  g.off_misc = (int)(g.off_scale + scales);
   g.smem = g.off_misc + kMiscBytes + 1024;
   return g;
 }
 
 template <int NT>
-static cudaError_t run_mlp(const CUtensorMap (&m)[4], const MlpArgs& a, int smem, int num_sms, cudaStream_t st) {
+static cudaError_t run_mlp(const CUtensorMap& gu, const CUtensorMap& d, const MlpArgs& a, int smem, int num_sms,
+                           cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
@@ -651,51 +753,37 @@ static cudaError_t run_mlp(const CUtensorMap (&m)[4], const MlpArgs& a, int smem
   cfg.blockDim = dim3(kMlpThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs wait for one another: all or none are resident
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_mlp_kernel<NT>, m[0], m[1], m[2], m[3], a);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, moe_mlp_kernel<NT>, gu, d, a);
 }
 
 cudaError_t launch_moe_mlp(const MlpArgs& args, const uint8_t* qgu, int64_t ldgu, const uint8_t* qd, int64_t ldd,
                            int num_sms, cudaStream_t st, const char** msg) {
   MlpArgs a = args;
   const MlpGeom g = mlp_geom(a.T, a.K, a.I, a.N, num_sms);
-  a.rows = g.rows, a.mtiles = g.mtiles, a.blocks = g.blocks, a.buffers = g.buffers, a.stages = g.stages;
+  a.rows = g.rows, a.group = g.group, a.buffers = g.buffers, a.stages = g.stages;
   a.off_scale = g.off_scale, a.off_misc = g.off_misc;
   a.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % 8 == 0 && a.K % 8 == 0;
-  CUtensorMap m[4];
-  memset(m, 0, sizeof(m));
-  const int64_t Kf = a.K / kBlock, If = a.I / kBlock, E = a.E, I = a.I, N = a.N, K = a.K;
-  bool ok = true;
-  // features, K-blocks, then gate / up, expert: a box is 8 K-blocks of 8 gate and 8 up rows, a K-block's 8 rows together
-  if (Kf) {
-    const int64_t dim[5] = {kBlock, I, Kf, 2, E}, stride[5] = {1, ldgu, kBlock, I * ldgu, 2 * I * ldgu};
-    const int box[5] = {kBlock, kUnit, kUnitBlocks, 2, 1};
-    ok = mlp_map(&m[0], qgu, 5, dim, stride, box);
-  }
-  if (ok && K % kBlock) {
-    const int64_t dim[4] = {K, I, 2, E}, stride[4] = {1, ldgu, I * ldgu, 2 * I * ldgu};
-    const int box[4] = {kBlock, kUnit, 2, 1};
-    ok = mlp_map(&m[1], qgu, 4, dim, stride, box);
-  }
-  if (ok && If) {
-    const int64_t dim[4] = {kBlock, N, If, E}, stride[4] = {1, ldd, kBlock, N * ldd};
-    const int box[4] = {kBlock, g.rows, g.blocks, 1};
-    ok = mlp_map(&m[2], qd, 4, dim, stride, box);
-  }
-  if (ok && I % kBlock) {
-    const int64_t dim[3] = {I, N, E}, stride[3] = {1, ldd, N * ldd};
-    const int box[3] = {kBlock, g.rows, 1};
-    ok = mlp_map(&m[3], qd, 3, dim, stride, box);
-  }
-  if (!ok) {
+  CUtensorMap gu, d;
+  memset(&gu, 0, sizeof(gu));
+  memset(&d, 0, sizeof(d));
+  const int64_t E = a.E, I = a.I, N = a.N, K = a.K;
+  // features, rows, gate / up, expert; features, rows, expert
+  const int64_t dim1[4] = {K, I, 2, E}, stride1[4] = {1, ldgu, I * ldgu, 2 * I * ldgu};
+  const int box1[4] = {kBlock, kPairs, 2, 1};
+  const int64_t dim2[3] = {I, N, E}, stride2[3] = {1, ldd, N * ldd};
+  const int box2[3] = {kBlock, g.rows, 1};
+  if (!mlp_map(&gu, qgu, 4, dim1, stride1, box1) || !mlp_map(&d, qd, 3, dim2, stride2, box2)) {
     *msg = "cuTensorMapEncodeTiled failed for a weight (alignment, stride or size out of range)";
     return cudaErrorInvalidValue;
   }
-  return a.T <= 8 ? run_mlp<1>(m, a, g.smem, num_sms, st) : run_mlp<2>(m, a, g.smem, num_sms, st);
+  return a.T <= 8 ? run_mlp<1>(gu, d, a, g.smem, num_sms, st) : run_mlp<2>(gu, d, a, g.smem, num_sms, st);
 }
 
 cudaError_t mlp_read_errors(uint32_t* out) {
