@@ -802,7 +802,9 @@ def moe_mlp_decode(x, logits, k: int, qgu, sgu, qd, sd, I: int, N: int, bias=Non
                              f"of {E * _cdiv(rows, BLOCK)} x {_cdiv(cols, BLOCK)}, got {tuple(q.shape)} and {tuple(s.shape)}")
         if q.stride(1) != 1 or (s.stride(1) != 1 and s.shape[1] > 1):
             raise ValueError(f"q{name} and s{name} must have unit column strides")
-    _need_here(x, logits, bias, qgu, sgu, qd, sd)
+    here = _here()
+    if any(t is not None and t.get_device() != here for t in (x, logits, bias, qgu, sgu, qd, sd)):
+        raise ValueError(f"every tensor must be on the current device, cuda:{here}")
     dev = x.device
     L = lib()
     y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
@@ -831,30 +833,32 @@ class NormOut(NamedTuple):
     y: "torch.Tensor"      # [T, K] bf16
 
 
-def _need_here(*tensors):
-    """The tensors must be on the current device: the launch goes to its stream."""
-    here = _torch()._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+def _here():
+    """The current device's index: launches go to its stream, so tensors must be on it."""
+    return _torch()._C._cuda_getDevice()
 
 
-def _need_norm_weight(weight, K):
+def _rows(t, name, shape, here):
+    """The row stride of a bf16 tensor of that shape on device `here`, rows apart from one another."""
+    n, k = shape
+    stride = t.stride()
+    if t.dtype is not _torch().bfloat16 or t.shape != shape or t.get_device() != here or (stride[1] != 1 and k > 1) or \
+            (n > 1 and stride[0] < k):
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} with unit column stride and rows that do not "
+                         f"overlap, on the current device cuda:{here}; got {t.dtype} {tuple(t.shape)}, strides {stride}, on "
+                         f"{t.device}")
+    return stride[0] if n > 1 else max(k, 1)
+
+
+def _norm_weight(weight, K, here):
+    """Whether the norm's weight is fp32 (else bf16)."""
     torch = _torch()
     f32 = weight.dtype is torch.float32
-    if not (f32 or weight.dtype is torch.bfloat16) or weight.shape != (K,) or not weight.is_cuda or \
-            not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous CUDA bf16 or float32 tensor of shape {(K,)}, got {weight.dtype} "
-                         f"{tuple(weight.shape)} on {weight.device}")
+    if not (f32 or weight.dtype is torch.bfloat16) or weight.shape != (K,) or weight.get_device() != here or \
+            (weight.stride(0) != 1 and K > 1):
+        raise ValueError(f"weight must be a contiguous bf16 or float32 tensor of shape {(K,)} on the current device "
+                         f"cuda:{here}, got {weight.dtype} {tuple(weight.shape)} on {weight.device}")
     return f32
-
-
-def _need_rows(t, name, shape):
-    _need_bf16_2d(t, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} must not have overlapping rows (stride {t.stride(0)} of {t.shape[1]} columns)")
 
 
 def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, rows: bool = True, cols: bool = False, out: bool = False,
@@ -865,37 +869,48 @@ def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, rows: bool = Tru
     y is not rounded before its quantisation.  ``h`` (default: a new tensor) takes
     the sum; it may be x or residual.  See bfp8_rms_norm_quant."""
     torch = _torch()
-    _need_bf16_2d(x, "x")
-    T, K = x.shape
-    _need_rows(x, "x", (T, K))
-    f32 = _need_norm_weight(weight, K)
-    dev, u8, fp = x.device, torch.uint8, torch.float32
+    if x.dim() != 2:
+        raise ValueError(f"x must be a 2-D tensor, got shape {tuple(x.shape)}")
+    shape = x.shape
+    T, K = shape
+    here = _here()
+    ldx = _rows(x, "x", shape, here)
+    f32 = _norm_weight(weight, K, here)
+    dev, u8, fp, bf = x.device, torch.uint8, torch.float32, torch.bfloat16
+    empty = torch.empty
+    at_r = at_h = at_q = at_s = at_qc = at_sc = at_y = None
+    ldr = ldh = ldq = ldqc = ldsc = 0
+    q = s = qc = sc = y = None
     if residual is not None:
-        _need_rows(residual, "residual", (T, K))
+        ldr, at_r = _rows(residual, "residual", shape, here), residual.data_ptr()
         if h is None:
-            h = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+            h, ldh = empty(shape, dtype=bf, device=dev), max(K, 1)
         else:
-            _need_rows(h, "h", (T, K))
+            ldh = _rows(h, "h", shape, here)
+        at_h = h.data_ptr()
     elif h is not None:
         raise ValueError("h takes x + residual: it needs a residual")
-    _need_here(x, weight, residual, h)
-    rstd = torch.empty(T, dtype=fp, device=dev)
-    q = s = qc = sc = y = None
+    else:
+        h = x
+    rstd = empty(T, dtype=fp, device=dev)
     if rows:
-        q = torch.empty((T, (max(K, 1) + 15) // 16 * 16), dtype=u8, device=dev)
-        s = torch.empty(((K + BLOCK - 1) // BLOCK, max(T, 1)), dtype=fp, device=dev)
+        ldq = (max(K, 1) + 15) // 16 * 16
+        q = empty((T, ldq), dtype=u8, device=dev)
+        s = empty(((K + BLOCK - 1) // BLOCK, max(T, 1)), dtype=fp, device=dev)
+        at_q, at_s = q.data_ptr(), s.data_ptr()
     if cols:
-        qc = torch.empty((K, (max(T, 1) + 15) // 16 * 16), dtype=u8, device=dev)
-        sc = torch.empty(((T + BLOCK - 1) // BLOCK, (max(K, 1) + 3) // 4 * 4), dtype=fp, device=dev)
+        ldqc, ldsc = (max(T, 1) + 15) // 16 * 16, (max(K, 1) + 3) // 4 * 4
+        qc = empty((K, ldqc), dtype=u8, device=dev)
+        sc = empty(((T + BLOCK - 1) // BLOCK, ldsc), dtype=fp, device=dev)
+        at_qc, at_sc = qc.data_ptr(), sc.data_ptr()
     if out:
-        y = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
-    st = lib().bfp8_rms_norm_quant(
-        x.data_ptr(), T, K, _ld(x), _p(residual), _ld(residual) if residual is not None else 0, weight.data_ptr(), f32, eps,
-        _p(h), _ld(h) if h is not None else 0, rstd.data_ptr(), _p(q), q.stride(0) if rows else 0, _p(s),
-        max(T, 1), _p(qc), qc.stride(0) if cols else 0, _p(sc), sc.stride(0) if cols else 0, _p(y), K, _stream())
+        y = empty(shape, dtype=bf, device=dev)
+        at_y = y.data_ptr()
+    st = lib().bfp8_rms_norm_quant(x.data_ptr(), T, K, ldx, at_r, ldr, weight.data_ptr(), f32, eps, at_h, ldh,
+                                   rstd.data_ptr(), at_q, ldq, at_s, max(T, 1), at_qc, ldqc, at_sc, ldsc, at_y, K, _stream())
     if st:
         _check(st)
-    return NormOut(x if h is None else h, rstd, q, s, qc, sc, y)
+    return NormOut(h, rstd, q, s, qc, sc, y)
 
 
 def rms_norm_bwd(dy, h, weight, rstd, dh=None):
@@ -903,23 +918,26 @@ def rms_norm_bwd(dy, h, weight, rstd, dh=None):
     normed rows), dh [T, K] bf16 or None (of h, by the stream itself) -> (dx [T,
     K] bf16, the gradient of x and of the residual, dweight [K] fp32)."""
     torch = _torch()
-    _need_bf16_2d(dy, "dy")
-    T, K = dy.shape
-    _need_rows(dy, "dy", (T, K))
-    _need_rows(h, "h", (T, K))
-    f32 = _need_norm_weight(weight, K)
-    _need(rstd, "rstd", torch.float32, (T,))
+    if dy.dim() != 2:
+        raise ValueError(f"dy must be a 2-D tensor, got shape {tuple(dy.shape)}")
+    shape = dy.shape
+    T, K = shape
+    here = _here()
+    lddy, ldh = _rows(dy, "dy", shape, here), _rows(h, "h", shape, here)
+    f32 = _norm_weight(weight, K, here)
+    if rstd.dtype is not torch.float32 or rstd.shape != (T,) or rstd.get_device() != here or (T > 1 and rstd.stride(0) != 1):
+        raise ValueError(f"rstd must be a contiguous float32 tensor of shape {(T,)} on the current device, got {rstd.dtype} "
+                         f"{tuple(rstd.shape)} on {rstd.device}")
+    at_dh, lddh = None, 0
     if dh is not None:
-        _need_rows(dh, "dh", (T, K))
-    _need_here(dy, h, weight, rstd, dh)
-    dev = dy.device
-    dx = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
-    dw = torch.empty(K, dtype=torch.float32, device=dev)
-    L = lib()
-    ws = torch.empty(max(L.bfp8_rms_norm_bwd_workspace_size(T, K), 16), dtype=torch.uint8, device=dev)
-    st = L.bfp8_rms_norm_bwd(dy.data_ptr(), T, K, _ld(dy), h.data_ptr(), _ld(h), weight.data_ptr(), f32, rstd.data_ptr(),
-                             _p(dh), _ld(dh) if dh is not None else 0, dx.data_ptr(), max(K, 1), dw.data_ptr(),
-                             ws.data_ptr(), ws.numel(), _stream())
+        lddh, at_dh = _rows(dh, "dh", shape, here), dh.data_ptr()
+    dev, empty, L = dy.device, torch.empty, lib()
+    dx = empty(shape, dtype=torch.bfloat16, device=dev)
+    dw = empty(K, dtype=torch.float32, device=dev)
+    ws_bytes = max(L.bfp8_rms_norm_bwd_workspace_size(T, K), 16)
+    ws = empty(ws_bytes, dtype=torch.uint8, device=dev)
+    st = L.bfp8_rms_norm_bwd(dy.data_ptr(), T, K, lddy, h.data_ptr(), ldh, weight.data_ptr(), f32, rstd.data_ptr(), at_dh,
+                             lddh, dx.data_ptr(), max(K, 1), dw.data_ptr(), ws.data_ptr(), ws_bytes, _stream())
     if st:
         _check(st)
     return dx, dw
@@ -939,17 +957,16 @@ def _grad_list(tensors, name):
     if _grad_types is None:
         _grad_types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     n = len(tensors)
-    ptr, numel, kind = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
-    here = torch._C._cuda_getDevice() if n else None
+    kinds = [_grad_types.get(t.dtype, -1) for t in tensors]
+    here = _here() if n else 0
     for i, t in enumerate(tensors):
-        code = _grad_types.get(t.dtype)
-        if code is None or not t.is_cuda or t.device.index != here:
-            raise ValueError(f"{name}[{i}] must be a bf16, fp16 or float32 tensor on the current CUDA device, got {t.dtype} "
-                             f"on {t.device}")
+        if kinds[i] < 0 or t.get_device() != here:
+            raise ValueError(f"{name}[{i}] must be a bf16, fp16 or float32 tensor on the current device cuda:{here}, got "
+                             f"{t.dtype} on {t.device}")
         if not (t.is_contiguous() or _dense(t)):
             raise ValueError(f"{name}[{i}] has gaps or repeats (shape {tuple(t.shape)}, strides {t.stride()})")
-        ptr[i], numel[i], kind[i] = t.data_ptr(), t.numel(), code
-    return ptr, numel, kind
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
+            (ctypes.c_int32 * n)(*kinds))
 
 
 def _dense(t):
@@ -989,7 +1006,7 @@ def clip_grads(tensors, max_norm: float, out=None):
         if len(out) != len(tensors):
             raise ValueError(f"{len(tensors)} tensors, {len(out)} outputs")
         for i, (t, o) in enumerate(zip(tensors, out)):
-            if t.shape != o.shape or (t.stride() != o.stride() and not (t.is_contiguous() and o.is_contiguous())):
+            if t.shape != o.shape or not (t.is_contiguous() and o.is_contiguous() or t.stride() == o.stride()):
                 raise ValueError(f"out[{i}] must have the shape and strides of tensors[{i}], {tuple(t.shape)} {t.stride()}, "
                                  f"got {tuple(o.shape)} {o.stride()}")
         optr, _, okind = _grad_list(out, "out")

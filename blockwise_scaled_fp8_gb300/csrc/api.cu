@@ -1000,16 +1000,18 @@ bfp8_status bfp8_check_device_errors(bfp8_stream_t stream) {
   if (st != BFP8_OK) return st;
   cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: stream synchronize");
-  uint32_t bits = 0, qbits = 0, dbits = 0, rbits = 0, mbits = 0;
+  uint32_t bits = 0, qbits = 0, dbits = 0, rbits = 0, mbits = 0, nbits = 0;
   e = gemm_read_errors(&bits);
   if (e == cudaSuccess) e = quant_read_errors(&qbits);
   if (e == cudaSuccess) e = dispatch_read_errors(&dbits);
   if (e == cudaSuccess) e = routed_read_errors(&rbits);
   if (e == cudaSuccess) e = mlp_read_errors(&mbits);
+  if (e == cudaSuccess) e = norm_read_errors(&nbits);
   if (e != cudaSuccess) return cuda_fail(e, "bfp8_check_device_errors: read flag");
   if (qbits) return fail(BFP8_ERR_TIMEOUT, "quantisation kernel gave up waiting for its TMA tile loads");
   if (dbits) return fail(BFP8_ERR_TIMEOUT, "dispatch kernel gave up waiting for its gathered rows");
   if (rbits & kRoutedOffsets) return fail(BFP8_ERR_INVALID_ARG, "routed product: expert offsets decreasing");
+  if (nbits) return fail(BFP8_ERR_TIMEOUT, "norm kernel gave up waiting for its rows");
   if (mbits) return fail(BFP8_ERR_TIMEOUT, "few-token experts layer gave up on a wait (flags 0x%x)", mbits);
   if (rbits) return fail(BFP8_ERR_TIMEOUT, "routed product gave up waiting for its weights");
   if (bits & 64u)  // kErrGroupOffsets

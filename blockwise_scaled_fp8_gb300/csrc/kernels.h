@@ -301,9 +301,10 @@ struct NormArgs {
   int64_t lds_col;
   uint16_t* y;  // null: not formed
   int64_t ldy;
-  int team, cluster;  // set by the launcher: threads a row, CTAs that share 128 rows
+  int team, slots;  // set by the launcher: threads a row; rows in flight in a CTA
 };
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t st);
+cudaError_t norm_read_errors(uint32_t* out);  // reads and clears the kernel's error word (synchronous)
 struct NormBwdArgs {
   const uint16_t* dy;
   int64_t lddy;
