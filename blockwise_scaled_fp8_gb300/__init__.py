@@ -1221,7 +1221,8 @@ def debug_write_counts(kind: int, M: int, N: int, K: int, flag: int = 0):
 
 def __getattr__(name):
     # the autograd wrapper lives in its own module (it imports torch at load)
-    if name in ("Float8BlockwiseLinear", "blockwise_fp8_linear", "Float8RoutedExperts", "blockwise_fp8_experts"):
+    if name in ("Float8BlockwiseLinear", "blockwise_fp8_linear", "Float8RoutedExperts", "blockwise_fp8_experts",
+                "Float8NormLinear", "blockwise_fp8_norm_linear"):
         from . import module
         return getattr(module, name)
     raise AttributeError(name)

@@ -883,7 +883,7 @@ bfp8_status bfp8_rms_norm_bwd(const void* dy, int64_t T, int64_t K, int64_t lddy
   CHECK_ARG(ws_bytes >= need, "%s: workspace of %zu bytes, needs %zu", fn, ws_bytes, need);
   const cudaError_t e = launch_rms_norm_bwd(
       NormBwdArgs{(const uint16_t*)dy, lddy, (const uint16_t*)h, ldh, T, K, weight, weight_f32 != 0, rstd,
-                  (const uint16_t*)dh, lddh, (uint16_t*)dx, lddx, dweight, (float*)ws, 0},
+                  (const uint16_t*)dh, lddh, (uint16_t*)dx, lddx, dweight, (float*)ws, 0, 0},
       sms, (cudaStream_t)stream);
   return e == cudaSuccess ? BFP8_OK : cuda_fail(e, fn);
 }

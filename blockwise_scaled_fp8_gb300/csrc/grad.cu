@@ -9,11 +9,13 @@
 // run of them.  Partial sums are one double a CTA and are added in a fixed
 // order: the same tensors give the same norm.
 //
-// Squares are summed in fp32 over the 32 elements that a thread takes of a
-// chunk and from there on in fp64.  A thread whose fp32 sum overflowed, or lies
-// so low that its squares may have lost bits below the normal range, forms it
-// again in fp64 (its elements are in L1), so the norm of any finite gradients
-// is finite as long as it fits fp32, and that of tiny ones is not 0.
+// Squares are summed in fp32 over the 32 elements that a thread takes of a chunk, in
+// small models over the 256 that a warp takes, and from there on in fp64 (which this
+// part is slow at: where a CTA has one chunk, fp64 sums over its lanes are a third
+// of the call).  Where an fp32 sum overflowed, or lies so low that its squares may
+// have lost bits below the normal range, it is formed again in fp64 (its elements
+// are in L1), so the norm of any finite gradients is finite as long as it fits fp32,
+// and that of tiny ones is not 0.
 //
 // What bounds it is memory: every element is read for the norm, and read again
 // and written for the clipping, since the norm has to be known first.  The
@@ -31,11 +33,10 @@ namespace {
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
 constexpr int kGradVec = 8;                            // elements a thread takes at once
-constexpr int kGradUnroll = 4;                         // of them from a chunk
-constexpr int kGradChunk = kGradThreads * kGradVec * kGradUnroll;
+constexpr int kGradUnroll = 4;                         // and how often in a chunk (once where there are few chunks)
 constexpr float kClipFloor = 1e-6f;
-// below this a thread's sum of 32 squares may hold ones that lost bits below 2^-126
-constexpr float kTinySum = 1e-30f;
+// below this a sum of up to 256 squares may hold ones that lost bits below 2^-126
+constexpr float kTinySum = 1e-28f;
 
 struct GradEntry {
   const void* in;
@@ -141,22 +142,38 @@ __device__ __forceinline__ int entry_of(const GradTable<CAP>& t, uint32_t c) {
   return lo;
 }
 
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
 
+// sqrt(v) rounded to fp32 (to within an ulp), without fp64's: the root of v scaled into [1, 4), one Newton step on its
+// remainder, scaled back.  Infinities, NaN and 0 are their own roots.
+__device__ __forceinline__ float root_of(double v) {
+  if (!(v > 0.0) || v > 1e300) return (float)v;  // (1e300: far above the square of any fp32)
+  const int e = (((int)(__double_as_longlong(v) >> 52) & 0x7FF) - 1023) & ~1;
+  const double m = v * __longlong_as_double((long long)(1023 - e) << 52);
+  const float y = __fsqrt_rn((float)m);
+  const float rest = (float)fma(-(double)y, (double)y, m);
+  return ldexpf(y + rest * __fdividef(0.5f, y), e / 2);
+}
+
 }  // namespace
 
-// Chunk c of a tensor is its vectors [c * kGradThreads * kGradUnroll, ..), thread
-// by thread; its first chunk also takes the elements before the first vector and
+// Chunk c of a tensor is its vectors [c * kGradThreads * U, ..), thread by thread; its first chunk also takes the elements before the first vector and
 // after the last one.  A tensor without vectors (vec 0: its output's alignment
 // differs from its input's) is taken element by element instead, a warp's lanes
 // side by side.
-template <int CAP>
+template <int CAP, int U>
 __global__ void __launch_bounds__(kGradThreads, 2)
     grad_norm_kernel(const __grid_constant__ GradTable<CAP> t, const GradParams p) {
+  constexpr bool kByWarp = U == 1;  // sums are a warp's, the same in its lanes (else a thread's)
   __shared__ double s_sum[kGradWarps];
   const int tid = (int)threadIdx.x;
   pdl_launch_dependents();
@@ -173,16 +190,16 @@ __global__ void __launch_bounds__(kGradThreads, 2)
     uint32_t any = 0;  // bits of the magnitudes: 0 where every element is 0
     if (e.vec) {
       const int64_t nv = (e.n - e.lead) / kGradVec;
-      const int64_t v0 = (int64_t)local * (kGradThreads * kGradUnroll) + tid;
-      Raw8 r[kGradUnroll];
+      const int64_t v0 = (int64_t)local * (kGradThreads * U) + tid;
+      Raw8 r[U];
 #pragma unroll
-      for (int u = 0; u < kGradUnroll; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int64_t v = v0 + u * kGradThreads;
         if (v < nv) r[u] = load8(e.in, e.in_type, e.lead + v * kGradVec);
         else r[u].a = r[u].b = make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int u = 0; u < kGradUnroll; ++u) {
+      for (int u = 0; u < U; ++u) {
         float v[8];
         values8(r[u], e.in_type, v);
 #pragma unroll
@@ -195,27 +212,28 @@ __global__ void __launch_bounds__(kGradThreads, 2)
         if (tid < e.lead) edge = tid;
         else if (tail + tid - e.lead < e.n) edge = tail + tid - e.lead;
       }
-      if (edge >= 0) {
-        const double v = load1(e.in, e.in_type, edge);
-        total += v * v;
+      if (local == 0 && tid < 32) {  // (at most 14 of them: warp 0's)
+        const double v = edge >= 0 ? (double)load1(e.in, e.in_type, edge) : 0.0;
+        total += kByWarp ? warp_sum(v * v) : v * v;
       }
-      if (!(sum < INFINITY) || (sum < kTinySum && any != 0)) {
+      const float part = kByWarp ? warp_sum(sum) : sum;
+      if (!(part < INFINITY) || (part < kTinySum && (kByWarp ? __any_sync(kAll, any != 0) : any != 0))) {
         double again = 0.0;
-        for (int u = 0; u < kGradUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
           const int64_t v = v0 + u * kGradThreads;
           for (int i = 0; v < nv && i < kGradVec; ++i) {
             const double x = load1(e.in, e.in_type, e.lead + v * kGradVec + i);
             again += x * x;
           }
         }
-        total += again;
+        total += kByWarp ? warp_sum(again) : again;
       } else {
-        total += (double)sum;
+        total += (double)part;
       }
     } else {
-      const int64_t e0 = (int64_t)local * kGradChunk;
+      const int64_t e0 = (int64_t)local * (kGradThreads * kGradVec * U);
 #pragma unroll 8
-      for (int u = 0; u < kGradVec * kGradUnroll; ++u) {
+      for (int u = 0; u < kGradVec * U; ++u) {
         const int64_t i = e0 + u * kGradThreads + tid;
         if (i < e.n) {
           const float v = load1(e.in, e.in_type, i);
@@ -223,22 +241,23 @@ __global__ void __launch_bounds__(kGradThreads, 2)
           any |= __float_as_uint(v) << 1;
         }
       }
-      if (!(sum < INFINITY) || (sum < kTinySum && any != 0)) {
+      const float part = kByWarp ? warp_sum(sum) : sum;
+      if (!(part < INFINITY) || (part < kTinySum && (kByWarp ? __any_sync(kAll, any != 0) : any != 0))) {
         double again = 0.0;
-        for (int u = 0; u < kGradVec * kGradUnroll; ++u) {
+        for (int u = 0; u < kGradVec * U; ++u) {
           const int64_t i = e0 + u * kGradThreads + tid;
           if (i < e.n) {
             const double x = load1(e.in, e.in_type, i);
             again += x * x;
           }
         }
-        total += again;
+        total += kByWarp ? warp_sum(again) : again;
       } else {
-        total += (double)sum;
+        total += (double)part;
       }
     }
   }
-  total = warp_sum(total);
+  if (!kByWarp) total = warp_sum(total);
   if ((tid & 31) == 0) s_sum[tid >> 5] = total;
   __syncthreads();
   if (tid < 32) {
@@ -248,22 +267,28 @@ __global__ void __launch_bounds__(kGradThreads, 2)
 }
 
 // The norm from the partial sums, by every CTA in the same order; then its run of chunks, scaled, last one first.
-template <int CAP>
+template <int CAP, int U>
 __global__ void __launch_bounds__(kGradThreads, 2)
     grad_scale_kernel(const __grid_constant__ GradTable<CAP> t, const GradParams p) {
-  __shared__ double s_sum[kGradWarps];
+  __shared__ float s_norm;
   const int tid = (int)threadIdx.x;
   pdl_launch_dependents();
   pdl_wait();
-  double total = 0.0;
-  for (int i = tid; i < p.partials; i += kGradThreads) total += p.partial[i];
-  total = warp_sum(total);
-  if ((tid & 31) == 0) s_sum[tid >> 5] = total;
-  __syncthreads();
-  total = 0.0;
+  if (tid < 32) {
+    double total = 0.0;
+    constexpr int kLoads = 10;  // in flight (two CTAs an SM on 152 SMs: all of one table's)
+    for (int i0 = 0; i0 < p.partials; i0 += 32 * kLoads) {
+      double v[kLoads];
 #pragma unroll
-  for (int w = 0; w < kGradWarps; ++w) total += s_sum[w];
-  const float norm = (float)sqrt(total);
+      for (int j = 0; j < kLoads; ++j) v[j] = i0 + 32 * j + tid < p.partials ? p.partial[i0 + 32 * j + tid] : 0.0;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) total += v[j];
+    }
+    total = warp_sum(total);
+    if (tid == 0) s_norm = root_of(total);
+  }
+  __syncthreads();
+  const float norm = s_norm;
   if (p.write_norm && blockIdx.x == 0 && tid == 0) *p.norm = norm;
   const float ratio = p.max_norm / (norm + kClipFloor);
   const float coef = ratio > 1.0f ? 1.0f : ratio;  // (a NaN stays one)
@@ -277,15 +302,15 @@ __global__ void __launch_bounds__(kGradThreads, 2)
     const uint32_t local = c - e.first;
     if (e.vec) {
       const int64_t nv = (e.n - e.lead) / kGradVec;
-      const int64_t v0 = (int64_t)local * (kGradThreads * kGradUnroll) + tid;
-      Raw8 r[kGradUnroll];
+      const int64_t v0 = (int64_t)local * (kGradThreads * U) + tid;
+      Raw8 r[U];
 #pragma unroll
-      for (int u = 0; u < kGradUnroll; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int64_t v = v0 + u * kGradThreads;
         if (v < nv) r[u] = load8(e.in, e.in_type, e.lead + v * kGradVec);
       }
 #pragma unroll
-      for (int u = 0; u < kGradUnroll; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int64_t at_v = v0 + u * kGradThreads;
         if (at_v < nv) {
           float v[8];
@@ -303,8 +328,8 @@ __global__ void __launch_bounds__(kGradThreads, 2)
         if (edge >= 0) store1(e.out, e.out_type, edge, load1(e.in, e.in_type, edge) * coef);
       }
     } else {
-      const int64_t e0 = (int64_t)local * kGradChunk + tid;
-      for (int u0 = 0; u0 < kGradVec * kGradUnroll; u0 += 8) {
+      const int64_t e0 = (int64_t)local * (kGradThreads * kGradVec * U) + tid;
+      for (int u0 = 0; u0 < kGradVec * U; u0 += 8) {
         float v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -328,7 +353,7 @@ __global__ void __launch_bounds__(kGradThreads, 2)
 static int size_of(int type) { return type == kGradF32 ? 4 : 2; }
 
 // Entry of tensor i, and its chunks.
-static uint32_t fill_entry(const GradArgs& a, int64_t i, GradEntry* e) {
+static uint32_t fill_entry(const GradArgs& a, int64_t i, int unroll, GradEntry* e) {
   memset(e, 0, sizeof(*e));
   e->in = a.in[i];
   e->out = a.out ? a.out[i] : nullptr;
@@ -340,11 +365,12 @@ static uint32_t fill_entry(const GradArgs& a, int64_t i, GradEntry* e) {
   if (lead > e->n) lead = e->n;
   e->lead = (uint8_t)lead;
   e->vec = !e->out || ((reinterpret_cast<uintptr_t>(e->out) + (uintptr_t)lead * size_of(e->out_type)) & 15) == 0;
-  const int64_t chunks = e->vec ? cdiv((e->n - lead) / kGradVec, kGradThreads * kGradUnroll) : cdiv(e->n, kGradChunk);
+  const int64_t chunk = (int64_t)kGradThreads * unroll;
+  const int64_t chunks = e->vec ? cdiv((e->n - lead) / kGradVec, chunk) : cdiv(e->n, chunk * kGradVec);
   return (uint32_t)(chunks > 0 ? chunks : 1);
 }
 
-template <int CAP>
+template <int CAP, int U>
 static cudaError_t run_grads(const GradArgs& a, const int64_t* which, int64_t n, int num_sms, cudaStream_t st) {
   const int64_t launches = n > 0 ? cdiv(n, CAP) : 1;
   const int grid = grad_grid(num_sms);
@@ -360,7 +386,7 @@ static cudaError_t run_grads(const GradArgs& a, const int64_t* which, int64_t n,
       memset(&t, 0, sizeof(t));
       for (int64_t i = l * CAP; i < n && i < (l + 1) * CAP; ++i) {
         t.e[t.count].first = 0;
-        const uint32_t chunks = fill_entry(a, which[i], &t.e[t.count]);
+        const uint32_t chunks = fill_entry(a, which[i], U, &t.e[t.count]);
         t.e[t.count++].first = t.chunks;
         t.chunks += chunks;
       }
@@ -368,10 +394,10 @@ static cudaError_t run_grads(const GradArgs& a, const int64_t* which, int64_t n,
       p.write_norm = l == 0;
       cudaError_t e;
       if (pass == 0) {
-        e = launch_pdl(grad_norm_kernel<CAP>, (unsigned)grid, kGradThreads, 0, st, t, p);
+        e = launch_pdl(grad_norm_kernel<CAP, U>, (unsigned)grid, kGradThreads, 0, st, t, p);
       } else {
         if (!a.out) t.count = 0, t.chunks = 0;  // the norm alone: one CTA adds the partial sums
-        e = launch_pdl(grad_scale_kernel<CAP>, a.out ? (unsigned)grid : 1u, kGradThreads, 0, st, t, p);
+        e = launch_pdl(grad_scale_kernel<CAP, U>, a.out ? (unsigned)grid : 1u, kGradThreads, 0, st, t, p);
       }
       if (e != cudaSuccess) return e;
       if (pass == 1 && !a.out) break;
@@ -384,11 +410,17 @@ int grad_grid(int num_sms) { return 2 * num_sms; }
 int64_t grad_launches(int64_t n) { return n <= kGradCapSmall ? 1 : cdiv(n, kGradCap); }
 
 // Tables of 64 and of 640 tensors: the parameters of a launch are copied by the
-// driver whatever their use, 2 KB against 20.
+// driver whatever their use, 2 KB against 20.  Chunks of 4096 elements where those
+// of 16384 would be fewer than the CTAs (2M elements in 40 tensors: 25 us with the
+// larger ones).
 cudaError_t launch_grads(const GradArgs& a, const int64_t* which, int64_t n, int num_sms, cudaStream_t st) {
   static_assert(sizeof(GradTable<kGradCap>) + sizeof(GradParams) <= 32764, "a launch's parameters");
-  return n <= kGradCapSmall ? run_grads<kGradCapSmall>(a, which, n, num_sms, st)
-                            : run_grads<kGradCap>(a, which, n, num_sms, st);
+  int64_t total = 0;
+  for (int64_t i = 0; i < n; ++i) total += a.numel[which[i]];
+  const bool few = total < (int64_t)grad_grid(num_sms) * kGradThreads * kGradVec * kGradUnroll;
+  if (n <= kGradCapSmall)
+    return few ? run_grads<kGradCapSmall, 1>(a, which, n, num_sms, st) : run_grads<kGradCapSmall, kGradUnroll>(a, which, n, num_sms, st);
+  return few ? run_grads<kGradCap, 1>(a, which, n, num_sms, st) : run_grads<kGradCap, kGradUnroll>(a, which, n, num_sms, st);
 }
 
 }  // namespace bfp8

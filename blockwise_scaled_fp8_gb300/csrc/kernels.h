@@ -301,7 +301,7 @@ struct NormArgs {
   int64_t lds_col;
   uint16_t* y;  // null: not formed
   int64_t ldy;
-  int team, slots;  // set by the launcher: threads a row; rows in flight in a CTA
+  int team, slots;  // set by the launcher: threads, or warps, a row; rows in flight in a CTA
 };
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t st);
 cudaError_t norm_read_errors(uint32_t* out);  // reads and clears the kernel's error word (synchronous)
@@ -319,8 +319,8 @@ struct NormBwdArgs {
   uint16_t* dx;
   int64_t lddx;
   float* dweight;
-  float* partial;  // [teams][K]
-  int team;        // set by the launcher
+  float* partial;    // [teams][K]
+  int team, stages;  // set by the launcher
 };
 struct NormBwdGeom {
   int vpt, team;

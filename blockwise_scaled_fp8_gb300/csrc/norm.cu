@@ -26,7 +26,8 @@ static __device__ uint32_t g_norm_error;
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kNormWarps = 12, kNormMaxSlots = 32;
+constexpr int kNormWarps = 16, kNormMaxSlots = 32;
+constexpr int kBwdMaxStages = 8;
 constexpr int kVec = 8;  // features a thread takes side by side: 16 bytes of bf16, 16 threads a group of 128
 
 struct Team {
@@ -43,26 +44,40 @@ __device__ __forceinline__ uint4 ld_v4(const void* p) {
   asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld_u16(const uint16_t* p) {
-  uint16_t v;
-  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
-  return v;
+// The four words that start `sh` (0 or 16) bits into the five.
+__device__ __forceinline__ uint4 shift_words(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t sh) {
+  return make_uint4(__funnelshift_r(a, b, sh), __funnelshift_r(b, c, sh), __funnelshift_r(c, d, sh), __funnelshift_r(d, e, sh));
 }
-
 // Eight bf16 of a row from feature k on, zeros past its end.
 template <bool VEC>
 __device__ __forceinline__ uint4 load_row8(const uint16_t* row, int k, int K) {
   if constexpr (VEC) {
     return k < K ? ld_v4(row + k) : make_uint4(0, 0, 0, 0);
   } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = k + 2 * i < K ? ld_u16(row + k + 2 * i) : 0u;
-      const uint32_t hi = k + 2 * i + 1 < K ? ld_u16(row + k + 2 * i + 1) : 0u;
-      w[i] = lo | hi << 16;
+    // the two aligned 16 bytes that hold them, shifted (each holds one of the row's elements at least, or is not read)
+    uint4 out = make_uint4(0, 0, 0, 0);
+    if (k >= K) return out;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + k);
+    const int off = (int)(at & 15);
+    const uint4* p = reinterpret_cast<const uint4*>(at - off);
+    const uint4 a = ld_v4(p);
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (k + (16 - off) / 2 < K) b = ld_v4(p + 1);
+    const uint32_t sh = 8u * (uint32_t)(off & 2);
+    switch (off >> 2) {  // (the same for a whole row)
+      case 0: out = shift_words(a.x, a.y, a.z, a.w, b.x, sh); break;
+      case 1: out = shift_words(a.y, a.z, a.w, b.x, b.y, sh); break;
+      case 2: out = shift_words(a.z, a.w, b.x, b.y, b.z, sh); break;
+      default: out = shift_words(a.w, b.x, b.y, b.z, b.w, sh);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    if (k + kVec > K) {  // zeros past the row's end
+      const int n = K - k;
+      out.x = n >= 2 ? out.x : n == 1 ? out.x & 0xFFFFu : 0u;
+      out.y = n >= 4 ? out.y : n == 3 ? out.y & 0xFFFFu : 0u;
+      out.z = n >= 6 ? out.z : n == 5 ? out.z & 0xFFFFu : 0u;
+      out.w = n == 7 ? out.w & 0xFFFFu : 0u;
+    }
+    return out;
   }
 }
 template <bool VEC>
@@ -71,14 +86,23 @@ __device__ __forceinline__ void store_row8(uint16_t* row, int k, int K, const ui
     if (k < K) *reinterpret_cast<uint4*>(row + k) = v;
     return;
   }
+  uint16_t* to = row + k;
+  if (k + kVec <= K) {  // 32 bits at a time where they are aligned
+    if ((reinterpret_cast<uintptr_t>(to) & 2) == 0) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(to);
+      p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+    } else {
+      uint32_t* p = reinterpret_cast<uint32_t*>(to + 1);
+      to[0] = (uint16_t)v.x;
+      p[0] = __funnelshift_r(v.x, v.y, 16), p[1] = __funnelshift_r(v.y, v.z, 16), p[2] = __funnelshift_r(v.z, v.w, 16);
+      to[7] = (uint16_t)(v.w >> 16);
+    }
+    return;
+  }
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (k + i < K) row[k + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-}
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
-  f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+  for (int i = 0; i < 7; ++i)
+    if (k + i < K) to[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
 }
 // Keeps the compiler from carrying what it derived from the values (their fp32 forms, twice the registers) past here.
 template <int N>
@@ -97,9 +121,6 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 __device__ __forceinline__ float weight_at(const void* w, int f32, int64_t k) {
   return f32 ? __ldg(static_cast<const float*>(w) + k)
@@ -218,6 +239,26 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
 __device__ __forceinline__ void lds_2x64(uint32_t addr, uint64_t& a, uint64_t& b) {
   asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
+// The weights of aligned rows, kept in shared memory as they come, and eight of them from feature k on (zeros past the end).
+__device__ __forceinline__ uint32_t stage_weights(const void* w, int f32, int K, uint32_t to) {
+  const uint32_t bytes = (uint32_t)K * (f32 ? 4u : 2u);
+  for (uint32_t i = 16u * threadIdx.x; i < bytes; i += 16u * blockDim.x) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w) + i));
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + i), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  }
+  return (bytes + 127u) / 128u * 128u;
+}
+__device__ __forceinline__ void staged_weight8(uint32_t from, int f32, int k, int K, uint64_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = 0;
+  if (k >= K) return;
+  if (f32) {
+    lds_2x64(from + 4u * (uint32_t)k, w[0], w[1]);
+    lds_2x64(from + 4u * (uint32_t)k + 16u, w[2], w[3]);
+  } else {
+    pairs8(lds_v4(from + 2u * (uint32_t)k), w);
+  }
+}
 // `bytes` (a multiple of 16, both addresses 16-byte aligned) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -301,24 +342,28 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
   finish_row<VPT, VEC>(a, team, t, live, hv, rstd_of(team_sum(f2_sum(sum2), team, s_slots), K, a.eps));
 }
 
-// Many aligned rows: one CTA an SM, a warp a row, and no barrier between warps.  Rows
+// Many aligned rows: one CTA an SM, a team of one, two or four warps a row (so that
+// the rows that fit keep every warp busy), and no barrier between teams.  Rows
 // arrive by bulk copies in slots that hold all of shared memory, whatever the
-// threads are waiting for; row i of a CTA is slot i % slots and warp i % warps, and
-// the warp that is done with a row asks for the one that takes its slot.  A row is
+// threads are waiting for; row i of a CTA is slot i % slots and team i % teams, and
+// the team that is done with a row asks for the one that takes its slot.  A row is
 // read twice from its slot (the sum of the residual goes back into it): once for its
 // squares, once for its codes, four chunks of 256 features at a time, whose eight
 // groups' maxima a halving exchange leaves in a lane each.
 __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const NormArgs a) {
   extern __shared__ __align__(128) uint8_t s_ring[];  // weights, then the slots: [x, residual][K]
   __shared__ uint64_t s_full[kNormMaxSlots];
+  __shared__ float s_sum[kNormWarps];
+  __shared__ int s_abort;
   const int K = (int)a.K, tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31, slots = a.slots;
-  const int warps = slots < kNormWarps ? slots : kNormWarps;  // that have rows
+  const int size = a.team, teams = min(slots, kNormWarps / size), team = warp / size, sub = warp % size;
   const uint32_t row_bytes = 2u * (uint32_t)K, slot_bytes = row_bytes * (a.residual ? 2u : 1u), weight_bytes = a.weight_f32 ? 2u * row_bytes : row_bytes;
   const uint32_t weights = smem_u32(s_ring), ring = weights + (weight_bytes + 127u) / 128u * 128u, full = smem_u32(s_full);
   const int64_t rows = a.T > blockIdx.x ? cdiv(a.T - blockIdx.x, (int64_t)gridDim.x) : 0;  // of this CTA: every grid-th
-  const volatile int never = 0;
+  volatile int* abort_flag = &s_abort;
   pdl_launch_dependents();
   if (tid == 0) {
+    s_abort = 0;
     for (int i = 0; i < slots; ++i) mbar_init(full + 8 * i, 1);
     fence_barrier_init();
     fence_proxy_async_shared();
@@ -334,24 +379,26 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
   };
   if (tid == 0)
     for (int i = 0; i < slots && i < rows; ++i) issue(i, i);
-  for (uint32_t i = 16u * (uint32_t)tid; i < weight_bytes; i += 16u * blockDim.x) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.weight) + i));
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(weights + i), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-  }
+  stage_weights(a.weight, a.weight_f32, K, weights);
   __syncthreads();
-  if (warp >= warps) return;
-  int slot = warp;  // warps <= slots
+  if (team >= teams) return;
+  auto team_sync = [&]() {
+    if (size > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * size) : "memory");
+    else __syncwarp();
+  };
+  int slot = team;  // teams <= slots
   uint32_t parity = 0;
-  for (int64_t i = warp; i < rows; i += warps) {
+  for (int64_t i = team; i < rows; i += teams) {
     const int64_t t = blockIdx.x + i * gridDim.x;
     const uint32_t from = ring + (uint32_t)slot * slot_bytes;
-    if (!__all_sync(kAll, mbar_wait_bounded(full + 8 * slot, parity, kWaitLimitNs, &never))) {
-      if (lane == 0) atomicOr(&g_norm_error, 1u);
-      break;  // (the copies have not landed after four seconds: nothing is left to wait for)
+    // (a wait that gives up leaves the error word set and wrong rows from there on, without further waits or copies)
+    if (!mbar_wait_bounded(full + 8 * slot, parity, kWaitLimitNs, abort_flag)) {
+      atomicOr(&g_norm_error, 1u);
+      *abort_flag = 1;
     }
     uint64_t sum2 = 0;
 #pragma unroll 4
-    for (int k = kVec * lane; k < K; k += 32 * kVec) {
+    for (int k = kVec * (32 * sub + lane); k < K; k += 32 * kVec * size) {
       uint4 h = lds_v4(from + 2u * (uint32_t)k);
       if (a.residual) {
         h = add8(h, lds_v4(from + row_bytes + 2u * (uint32_t)k));
@@ -365,27 +412,24 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
     float sum = f2_sum(sum2);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (size > 1) {
+      if (lane == 0) s_sum[warp] = sum;
+      team_sync();  // the sums, and the row's values in the slot
+      sum = s_sum[team * size];
+      for (int j = 1; j < size; ++j) sum += s_sum[team * size + j];
+    }
     const float r = rstd_of(sum, K, a.eps);
-    if (lane == 0) a.rstd[t] = r;
+    if (sub == 0 && lane == 0) a.rstd[t] = r;
     if (a.q_row || a.y) {
-      for (int k0 = 0; k0 < K; k0 += 4 * 32 * kVec) {
+      for (int k0 = 4 * 32 * kVec * sub; k0 < K; k0 += 4 * 32 * kVec * size) {
         uint64_t v[4][4];
         float am[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int k = k0 + kVec * (32 * u + lane);
           uint64_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[u][j] = w[j] = 0;
-          if (k < K) {
-            if (a.weight_f32) {
-              lds_2x64(weights + 4u * (uint32_t)k, w[0], w[1]);
-              lds_2x64(weights + 4u * (uint32_t)k + 16u, w[2], w[3]);
-            } else {
-              pairs8(lds_v4(weights + 2u * (uint32_t)k), w);
-            }
-            times8(lds_v4(from + 2u * (uint32_t)k), w, v[u]);
-          }
+          staged_weight8(weights, a.weight_f32, k, K, w);
+          times8(k < K ? lds_v4(from + 2u * (uint32_t)k) : make_uint4(0, 0, 0, 0), w, v[u]);
           am[u] = amax8(v[u]);
         }
         if (a.y) {
@@ -412,9 +456,9 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
       }
     }
     fence_proxy_async_shared();  // this row's reads and writes of the slot, before the copy that takes it
-    __syncwarp();
-    if (lane == 0 && i + slots < rows) issue(i + slots, slot);
-    slot += warps;
+    team_sync();
+    if (sub == 0 && lane == 0 && i + slots < rows && !*abort_flag) issue(i + slots, slot);
+    slot += teams;
     if (slot >= slots) slot -= slots, parity ^= 1u;
   }
 }
@@ -515,62 +559,132 @@ __global__ void __launch_bounds__(256, 4) rms_norm_cols_kernel(const NormArgs a)
   }
 }
 
-// Gradient of a run of rows a team; the teams' sums for the weight go to partial[team of the launch][K].
-template <int VPT, bool VEC>
+// Gradient of every teams-th row, by teams of threads (chunks as above); the teams'
+// sums for the weight go to partial[team of the launch][K].  With RING (aligned
+// rows) the rows of dy, h and dh arrive by bulk copies, iterations ahead, and the
+// weights lie in shared memory (loaded into registers where they are used: a training
+// step's norm, forward and backward, of 16384 x 4096 265 us, so 236).
+template <int VPT, bool RING>
 __global__ void __launch_bounds__(256, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
+  extern __shared__ __align__(128) uint8_t s_ring[];  // weights, then [stages][dy, h, dh][rows of an iteration][K]
   __shared__ float s_slots[2][8];
+  __shared__ uint64_t s_full[kBwdMaxStages];
+  __shared__ int s_abort;
   const Team team = team_of(a.team);
-  const int K = (int)a.K, lane = team.lane;
+  const int K = (int)a.K, lane = team.lane, tid = (int)threadIdx.x, stages = a.stages;
+  const uint32_t weights = smem_u32(s_ring), ring = weights + ((uint32_t)K * (a.weight_f32 ? 4u : 2u) + 127u) / 128u * 128u;
+  const uint32_t full = smem_u32(s_full), row_bytes = 2u * (uint32_t)K;
+  const uint32_t part_bytes = (uint32_t)team.count * row_bytes, parts = a.dh ? 3 : 2;
+  const int64_t iterations = cdiv(a.T, team.count);
+  volatile int* abort_flag = &s_abort;
   pdl_launch_dependents();
+  if (RING) {
+    if (tid == 0) {
+      s_abort = 0;
+      for (int i = 0; i < stages; ++i) mbar_init(full + 8 * i, 1);
+      fence_barrier_init();
+      fence_proxy_async_shared();
+    }
+    __syncthreads();
+  }
   pdl_wait();
+  auto issue = [&](int64_t it, int st) {  // by warp 0: the rows of an iteration, a lane a row
+    const int64_t t = it * team.count;
+    const int rows = (int)(a.T - t < team.count ? a.T - t : team.count);
+    if (tid == 0) mbar_arrive_expect_tx(full + 8 * st, (uint32_t)rows * row_bytes * parts);
+    __syncwarp();
+    if (tid < rows) {
+      const uint32_t to = ring + (uint32_t)st * parts * part_bytes + (uint32_t)tid * row_bytes;
+      bulk_load(to, a.dy + (t + tid) * a.lddy, row_bytes, full + 8 * st);
+      bulk_load(to + part_bytes, a.h + (t + tid) * a.ldh, row_bytes, full + 8 * st);
+      if (a.dh) bulk_load(to + 2 * part_bytes, a.dh + (t + tid) * a.lddh, row_bytes, full + 8 * st);
+    }
+  };
+  if (RING && tid < 32)
+    for (int i = 0; i < stages; ++i)
+      if ((int64_t)blockIdx.x + (int64_t)i * gridDim.x < iterations) issue((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
+  if (RING) {
+    stage_weights(a.weight, a.weight_f32, K, weights);
+    __syncthreads();
+  }
+  auto weight8 = [&](int k, uint64_t (&w)[4]) {
+    if (RING) staged_weight8(weights, a.weight_f32, k, K, w);
+    else load_weight8<false>(a.weight, a.weight_f32, k, K, w);
+  };
   float dw[VPT][8] = {};
-  int turn = 0;
-  const int64_t me = (int64_t)blockIdx.x * team.count + team.index, teams = (int64_t)gridDim.x * team.count;
-  for (int64_t first = (int64_t)blockIdx.x * team.count; first < a.T; first += teams, turn ^= 1) {
-    const int64_t t = first + team.index;
+  int turn = 0, st = 0;
+  uint32_t parity = 0;
+  const int64_t me = (int64_t)blockIdx.x * team.count + team.index;
+  for (int64_t it = blockIdx.x; it < iterations; it += gridDim.x, turn ^= 1) {
+    const int64_t t = it * team.count + team.index;
     const bool live = t < a.T;
-    uint4 hv[VPT], dv[VPT], rv[VPT];
-#pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-      const int k = kVec * (u * team.size + lane);
-      hv[u] = live ? load_row8<VEC>(a.h + t * a.ldh, k, K) : make_uint4(0, 0, 0, 0);
-      dv[u] = live ? load_row8<VEC>(a.dy + t * a.lddy, k, K) : make_uint4(0, 0, 0, 0);
-      rv[u] = live && a.dh ? load_row8<VEC>(a.dh + t * a.lddh, k, K) : make_uint4(0, 0, 0, 0);
-    }
     const float r = live ? a.rstd[t] : 0.0f;
-    float sum = 0.0f;
-#pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-      float n[8], d[8], w[8];
-      unpack8(hv[u], n);
-      unpack8(dv[u], d);
-      uint64_t w2[4];
-      load_weight8<VEC>(a.weight, a.weight_f32, kVec * (u * team.size + lane), K, w2);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f2_unpack(w2[i], w[2 * i], w[2 * i + 1]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        n[i] *= r;
-        dw[u][i] = fmaf(d[i], n[i], dw[u][i]);
-        sum = fmaf(d[i] * w[i], n[i], sum);
+    uint4 hv[VPT], dv[VPT], rv[VPT];
+    if (RING) {
+      // (a wait that gives up leaves the error word set and wrong rows from there on, without further waits or copies)
+      if (!mbar_wait_bounded(full + 8 * st, parity, kWaitLimitNs, abort_flag)) {
+        atomicOr(&g_norm_error, 1u);
+        *abort_flag = 1;
       }
-    }
-    const float mean = team_sum(sum, team, s_slots[turn]) / (float)K;
-    if (live) {
+      const uint32_t from = ring + (uint32_t)st * parts * part_bytes + (uint32_t)team.index * row_bytes;
 #pragma unroll
       for (int u = 0; u < VPT; ++u) {
         const int k = kVec * (u * team.size + lane);
-        float n[8], d[8], w[8], e[8];
-        unpack8(hv[u], n);
-        unpack8(dv[u], d);
-        unpack8(rv[u], e);
-        uint64_t w2[4];
-        load_weight8<VEC>(a.weight, a.weight_f32, k, K, w2);
+        hv[u] = dv[u] = rv[u] = make_uint4(0, 0, 0, 0);
+        if (live && k < K) {
+          dv[u] = lds_v4(from + 2u * (uint32_t)k);
+          hv[u] = lds_v4(from + part_bytes + 2u * (uint32_t)k);
+          if (a.dh) rv[u] = lds_v4(from + 2 * part_bytes + 2u * (uint32_t)k);
+        }
+      }
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f2_unpack(w2[i], w[2 * i], w[2 * i + 1]);
+      for (int u = 0; u < VPT; ++u) {
+        const int k = kVec * (u * team.size + lane);
+        hv[u] = live ? load_row8<false>(a.h + t * a.ldh, k, K) : make_uint4(0, 0, 0, 0);
+        dv[u] = live ? load_row8<false>(a.dy + t * a.lddy, k, K) : make_uint4(0, 0, 0, 0);
+        rv[u] = live && a.dh ? load_row8<false>(a.dh + t * a.lddh, k, K) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    uint64_t sum2 = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = fmaf(r, d[i] * w[i] - n[i] * r * mean, e[i]);
-        store_row8<VEC>(a.dx + t * a.lddx, k, K, pack8(e));
+    for (int u = 0; u < VPT; ++u) {
+      uint64_t n[4], d[4], w[4];
+      row_times(hv[u], r, n);
+      pairs8(dv[u], d);
+      weight8(kVec * (u * team.size + lane), w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f2_unpack(f2_fma(d[i], n[i], f2_pack(dw[u][2 * i], dw[u][2 * i + 1])), dw[u][2 * i], dw[u][2 * i + 1]);
+        sum2 = f2_fma(f2_mul(d[i], w[i]), n[i], sum2);
+      }
+    }
+    if (RING) fence_proxy_async_shared();  // these reads, before the copy that takes their place
+    const float mean = __fdiv_rn(team_sum(f2_sum(sum2), team, s_slots[turn]), (float)K);
+    if (RING) {
+      if (team.size <= 32) __syncthreads();  // (else it is in the sum)
+      const int64_t next = it + (int64_t)stages * gridDim.x;
+      if (tid < 32 && next < iterations && !__any_sync(kAll, *abort_flag)) issue(next, st);
+      if (++st == stages) st = 0, parity ^= 1u;
+    }
+    if (live) {
+      const uint64_t r2 = f2_pack(r, r), c2 = f2_pack(-r * mean, -r * mean);  // dx = r (d w) - (r mean) n + dh
+#pragma unroll
+      for (int u = 0; u < VPT; ++u) {
+        const int k = kVec * (u * team.size + lane);
+        uint64_t n[4], d[4], w[4], e[4];
+        row_times(hv[u], r, n);
+        pairs8(dv[u], d);
+        pairs8(rv[u], e);
+        weight8(k, w);
+        uint32_t out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          f2_unpack(f2_add(f2_fma(c2, n[i], f2_mul(r2, f2_mul(d[i], w[i]))), e[i]), lo, hi);
+          out[i] = pack_bf16x2(lo, hi);
+        }
+        store_row8<RING>(a.dx + t * a.lddx, k, K, make_uint4(out[0], out[1], out[2], out[3]));
       }
     }
   }
@@ -649,6 +763,7 @@ static cudaError_t run_norm_ring(NormArgs a, int num_sms, cudaStream_t st) {
   if (attr_err != cudaSuccess) return attr_err;
   const int64_t weights = cdiv(a.K * (a.weight_f32 ? 4 : 2), 128) * 128, slot = a.K * 2 * (a.residual ? 2 : 1);
   const int64_t fit = (most - weights) / slot;  // (two of the largest rows)
+  a.team = a.K <= 4096 ? 1 : a.K <= 8192 ? 2 : 4;
   a.slots = (int)(fit < kNormMaxSlots ? fit : kNormMaxSlots);
   return launch_pdl(rms_norm_ring_kernel, (unsigned)(a.T < num_sms ? a.T : num_sms), 32 * kNormWarps,
                     (size_t)(weights + a.slots * slot), st, a);
@@ -695,8 +810,8 @@ NormBwdGeom norm_bwd_geom(int64_t T, int64_t K, int num_sms) {
   NormBwdGeom g;
   g.vpt = K <= 2048 ? 1 : K <= 4096 ? 2 : K <= 8192 ? 4 : 8;
   g.team = team_size(K, g.vpt, 256);
-  const int64_t per = 256 / g.team, most = (int64_t)num_sms * 3;
-  const int64_t ctas = cdiv(T, per * 4);  // four rows a team at least: each writes a row of sums
+  const int64_t per = 256 / g.team, most = (int64_t)num_sms * (g.vpt <= 2 ? 3 : g.vpt <= 4 ? 2 : 1);
+  const int64_t ctas = cdiv(T, per * 8);  // eight rows a team at least: each writes a row of sums
   g.grid = ctas < most ? ctas : most;
   g.teams = g.grid * per;
   return g;
@@ -711,7 +826,19 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& args, int num_sms, cudaStream
                      vec_ok(a.dx, a.lddx) && vec_ok(a.weight, 0);
     auto go = [&](auto vpt) {
       constexpr int V = decltype(vpt)::value;
-      return launch_pdl(vec ? rms_norm_bwd_kernel<V, true> : rms_norm_bwd_kernel<V, false>, (unsigned)g.grid, 256, 0, st, a);
+      if (!vec) return launch_pdl(rms_norm_bwd_kernel<V, false>, (unsigned)g.grid, 256, 0, st, a);
+      // the ring: what the CTAs that an SM holds leave each other (one stage of the largest rows)
+      constexpr int64_t most = 220 * 1024 / (V <= 2 ? 3 : V <= 4 ? 2 : 1) - 1024;
+      static std::once_flag once;
+      static cudaError_t attr_err = cudaSuccess;
+      std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(rms_norm_bwd_kernel<V, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+      });
+      if (attr_err != cudaSuccess) return attr_err;
+      const int64_t weights = cdiv(a.K * (a.weight_f32 ? 4 : 2), 128) * 128;
+      const int64_t stage = 256 / g.team * a.K * 2 * (a.dh ? 3 : 2), fit = (most - weights) / stage;
+      a.stages = (int)(fit < kBwdMaxStages ? fit : kBwdMaxStages);
+      return launch_pdl(rms_norm_bwd_kernel<V, true>, (unsigned)g.grid, 256, (size_t)(weights + a.stages * stage), st, a);
     };
     const cudaError_t e = g.vpt == 1   ? go(std::integral_constant<int, 1>{})
                           : g.vpt == 2 ? go(std::integral_constant<int, 2>{})

@@ -10,6 +10,10 @@ GEMMs.  Every step runs in the library's kernels through the C ABI; this
 module only reshapes, allocates outputs with torch and keeps the workspace
 for the backward.  No bias: the method has none.
 
+Float8NormLinear is such a layer behind the root-mean-square norm of a residual
+stream: the norm hands the products their operands' codes, and its rows are never
+written in bf16.
+
 Float8RoutedExperts puts a mixture of such layers behind a router: the router's
 logits choose each token's experts, and the layer is the weighted sum of their
 outputs, differentiable in the tokens, the experts' weights and the logits.
@@ -18,8 +22,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (MoePlan, linear_bwd_saved, linear_fwd_train, linear_train_workspace, moe_experts_bwd, moe_experts_decode,
-               moe_experts_fwd, moe_plan, moe_route, moe_route_bwd, quant_weight)
+from . import (MoePlan, gemm_1x128_128x1, gemm_1x128_128x128, linear_bwd_saved, linear_fwd_train, linear_train_workspace,
+               moe_experts_bwd, moe_experts_decode, moe_experts_fwd, moe_plan, moe_route, moe_route_bwd, quant_dual,
+               quant_weight, rms_norm_bwd, rms_norm_quant)
 
 
 class _BlockwiseFp8Linear(torch.autograd.Function):
@@ -82,6 +87,67 @@ class Float8BlockwiseLinear(torch.nn.Module):
 
     def extra_repr(self) -> str:
         return f"in_features={self.in_features}, out_features={self.out_features}, bias=False"
+
+
+class _BlockwiseFp8NormLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, norm_weight, residual, eps):
+        o = rms_norm_quant(x, norm_weight, residual=residual, eps=eps, cols=True)
+        qw, qwt, sw = quant_weight(weight, with_t=True)
+        y = gemm_1x128_128x128(o.q_row, o.s_row, qw, sw, x.shape[1])
+        ctx.save_for_backward(o.q_col, o.s_col, qwt, sw, o.h, o.rstd, norm_weight)
+        ctx.streams = residual is not None
+        return (y, o.h) if ctx.streams else y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable  # the kernels' gradients carry no graph
+    def backward(ctx, dy, dh=None):
+        q_col, s_col, qwt, sw, h, rstd, norm_weight = ctx.saved_tensors
+        T, N = dy.shape
+        qd, sd, qdt, sdt = quant_dual(dy.to(torch.bfloat16).contiguous())
+        dn = gemm_1x128_128x128(qd, sd, qwt, sw, N, sb_transposed=True)
+        dw = gemm_1x128_128x1(qdt, sdt, q_col, s_col, T) if ctx.needs_input_grad[1] else None
+        dx, dnorm = rms_norm_bwd(dn, h, norm_weight, rstd, dh=None if dh is None else dh.to(torch.bfloat16).contiguous())
+        return dx, dw, dnorm.to(norm_weight.dtype), dx if ctx.streams else None, None
+
+
+def blockwise_fp8_norm_linear(x: torch.Tensor, weight: torch.Tensor, norm_weight: torch.Tensor, residual=None,
+                              eps: float = 1e-6):
+    """(y, h): h = x + residual (x itself without one) and y = rms_norm(h) W^T with blockwise-FP8
+    products forward and backward, the norm quantised where it arises (x, residual [..., K],
+    weight [N, K] bf16, norm_weight [K] bf16 or fp32)."""
+    if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise TypeError("blockwise_fp8_norm_linear: x and weight must be bfloat16")
+    K, lead = x.shape[-1], x.shape[:-1]
+    if weight.dim() != 2 or weight.shape[1] != K or norm_weight.shape != (K,) or \
+            (residual is not None and residual.shape != x.shape):
+        raise ValueError(f"blockwise_fp8_norm_linear: x is {tuple(x.shape)}, weight {tuple(weight.shape)}, norm_weight "
+                         f"{tuple(norm_weight.shape)}, residual {None if residual is None else tuple(residual.shape)}")
+    x2 = x.reshape(-1, K).contiguous()
+    if residual is None:
+        y = _BlockwiseFp8NormLinear.apply(x2, weight.contiguous(), norm_weight.contiguous(), None, eps)
+        return y.reshape(*lead, weight.shape[0]), x
+    y, h = _BlockwiseFp8NormLinear.apply(x2, weight.contiguous(), norm_weight.contiguous(),
+                                         residual.reshape(-1, K).contiguous(), eps)
+    return y.reshape(*lead, weight.shape[0]), h.reshape(x.shape)
+
+
+class Float8NormLinear(torch.nn.Module):
+    """A root-mean-square norm and the linear layer (no bias) that reads it: forward(x, residual)
+    -> (y [..., N], h = x + residual [..., K], the residual stream that goes on)."""
+
+    def __init__(self, in_features: int, out_features: int, eps: float = 1e-6, device=None):
+        super().__init__()
+        self.in_features, self.out_features, self.eps = in_features, out_features, eps
+        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, device=device, dtype=torch.bfloat16))
+        torch.nn.init.kaiming_uniform_(self.weight, a=5 ** 0.5)
+        self.norm_weight = torch.nn.Parameter(torch.ones(in_features, device=device))
+
+    def forward(self, x: torch.Tensor, residual=None):
+        return blockwise_fp8_norm_linear(x, self.weight, self.norm_weight, residual, self.eps)
+
+    def extra_repr(self) -> str:
+        return f"in_features={self.in_features}, out_features={self.out_features}, eps={self.eps}, bias=False"
 
 
 class _BlockwiseFp8Experts(torch.autograd.Function):
