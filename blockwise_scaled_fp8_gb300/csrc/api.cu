@@ -831,9 +831,9 @@ bfp8_status bfp8_rms_norm_quant(const void* x, int64_t T, int64_t K, int64_t ldx
   if (st != BFP8_OK) return st;
   CHECK_ARG(K <= kNormMaxK, "%s: K=%lld > %lld", fn, (long long)K, (long long)kNormMaxK);
   CHECK_ARG(eps > 0.0f && eps < INFINITY, "%s: eps must be positive and finite", fn);
+  if (T == 0 || K == 0) return BFP8_OK;
   CHECK_ARG(!residual == !h, "%s: a residual and the sum h come together", fn);
   CHECK_ARG(!q_row == !s_row && !q_col == !s_col, "%s: codes and scales come together", fn);
-  if (T == 0 || K == 0) return BFP8_OK;
   CHECK_ARG(x && weight && rstd, "%s: null pointer", fn);
   CHECK_ARG(al2(x) && al2(residual) && al2(h) && al2(y) && (weight_f32 ? al4(weight) : al2(weight)) && al4(rstd) &&
                 al16(q_row) && al16(q_col) && al4(s_row) && al4(s_col),

@@ -1,6 +1,5 @@
 """The RMS norm with the residual's addition and quantised outputs, and its
 gradient, against the definitions in 64 bits."""
-import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -98,19 +97,19 @@ def test_parts_of_larger_buffers(T, K, off, ld):
     _, r = part(rv)
     hbuf, h = part()
     o = B.rms_norm_quant(x, w, residual=r, h=h, cols=True, out=True)
-    p = B.rms_norm_quant(xv, w, residual=rv, cols=True, out=True)
-    assert o.h is h and torch.equal(h, p.h) and torch.equal(o.q_row[:, :K], p.q_row[:, :K]) and torch.equal(o.y, p.y)
-    assert torch.equal(o.q_col[:, :T], p.q_col[:, :T])
+    # (rows of another alignment are summed in another order: not the same bits as the packed tensors', but as near)
+    hv, rstd, y = definition(xv, rv, w)
+    assert o.h is h and torch.equal(h, hv)
+    check_codes(o.q_row[:, :K], o.s_row[:, :T], y, rstd_tol(K), "rows")
+    check_codes(o.q_col[:, :T], o.s_col[:, :K], y.t().contiguous(), rstd_tol(K), "columns")
+    assert bool(((o.y.to(f64) - y).abs() <= y.abs() * (2.0 ** -8 + rstd_tol(K) + 2.0 ** -22) + 1e-38).all())
     around = torch.ones(hbuf.numel(), dtype=torch.bool, device="cuda")
     around[off:off + T * ld].view(T, ld)[:, :K] = False
     assert bool(hbuf[around].isnan().all())
     dy, dh = (torch.randn(T, K, generator=g, device="cuda").to(bf16) for _ in range(2))
     _, dyp = part(dy)
     _, dhp = part(dh)
-    a = B.rms_norm_bwd(dyp, h, w, o.rstd, dh=dhp)
-    b = B.rms_norm_bwd(dy, p.h, w, p.rstd, dh=dh)
-    assert torch.equal(a[0], b[0])
-    assert bool(((a[1] - b[1]).abs() <= 2.0 ** -20 * (dy.float() * p.h.float() * p.rstd[:, None]).abs().sum(0)).all())
+    check_backward(dyp, h, w, o.rstd, dhp)
 
 
 @pytest.mark.parametrize("K", [1000, 1003])
@@ -137,7 +136,26 @@ def test_zeros_and_extremes():
     o = B.rms_norm_quant(x, w, cols=True, out=True)
     check_codes(o.q_row, o.s_row, y, rstd_tol(384), "rows")
     check_codes(o.q_col, o.s_col[:, :384], y.t().contiguous(), rstd_tol(384), "columns")
-    assert int(o.q_row[3:].max()) == 0 and float(o.y[3:].abs().max()) == 0
+    assert float(o.q_row[3:].view(F8).float().abs().max()) == 0 and float(o.y[3:].abs().max()) == 0
+
+
+def check_backward(dy, h, w, rstd, dh):
+    T, K = dy.shape
+    dx, dw = B.rms_norm_bwd(dy, h, w, rstd, dh=dh)
+    h64 = h.to(f64).requires_grad_()
+    w64 = w.to(f64).requires_grad_()
+    y = h64 * (h64.square().mean(1, keepdim=True) + EPS).rsqrt() * w64
+    y.backward(dy.to(f64))
+    ref = h64.grad if dh is None else h64.grad + dh.to(f64)
+    n = h.to(f64) * rstd.to(f64)[:, None]
+    gr = dy.to(f64) * w.to(f64)
+    # one rounding to bf16; before it fp32's: of each term, and of the mean (a thread adds up to K / 32 terms in turn)
+    size = rstd.to(f64)[:, None] * (gr.abs() + n.abs() * (gr * n).abs().mean(1, keepdim=True))
+    tol = ref.abs() * 2.0 ** -8 + size * (K / 32 + 24) * 2.0 ** -24
+    assert bool(((dx.to(f64) - ref).abs() <= tol).all())
+    # sums over T of fp32 products, at most T + 32 additions one after another
+    assert bool(((dw.to(f64) - w64.grad).abs() <= (T + 40) * 2.0 ** -24 * (dy.to(f64) * n).abs().sum(0) + 1e-30).all())
+    return dx, dw
 
 
 @pytest.mark.parametrize("T,K", [(1, 16), (7, 1), (64, 128), (300, 1000), (33, 4096), (2000, 72), (200, 8192), (150, 16384),
@@ -149,20 +167,7 @@ def test_backward(T, K, with_dh):
     dy = torch.randn(T, K, generator=g, device="cuda").to(bf16)
     dh = torch.randn(T, K, generator=g, device="cuda").to(bf16) if with_dh else None
     o = B.rms_norm_quant(x, w, residual=r)
-    dx, dw = B.rms_norm_bwd(dy, o.h, w, o.rstd, dh=dh)
-    h = o.h.to(f64).requires_grad_()
-    w64 = w.to(f64).requires_grad_()
-    y = h * (h.square().mean(1, keepdim=True) + EPS).rsqrt() * w64
-    y.backward(dy.to(f64))
-    ref = h.grad if dh is None else h.grad + dh.to(f64)
-    n = (o.h.to(f64) * o.rstd.to(f64)[:, None])
-    gr = dy.to(f64) * w.to(f64)
-    # one rounding to bf16; before it fp32's: of each term, and of the mean (a thread adds up to K / 32 terms in turn)
-    size = o.rstd.to(f64)[:, None] * (gr.abs() + n.abs() * (gr * n).abs().mean(1, keepdim=True))
-    tol = ref.abs() * 2.0 ** -8 + size * (K / 32 + 24) * 2.0 ** -24
-    assert bool(((dx.to(f64) - ref).abs() <= tol).all())
-    # sums over T of fp32 products, at most T + 32 additions one after another
-    assert bool(((dw.to(f64) - w64.grad).abs() <= (T + 40) * 2.0 ** -24 * (dy.to(f64) * n).abs().sum(0) + 1e-30).all())
+    dx, dw = check_backward(dy, o.h, w, o.rstd, dh)
     again = B.rms_norm_bwd(dy, o.h, w, o.rstd, dh=dh)
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
     B.check_device_errors()
@@ -278,4 +283,4 @@ def test_norm_linear_module(residual):
         y2, _ = layer(x, r)
         (g,) = torch.autograd.grad(y2.float().sum(), x, create_graph=True)
         g.float().sum().backward()
-    assert np.isfinite(float(y.float().sum()))
+    assert bool(torch.isfinite(y.detach()).all())
