@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import NamedTuple
 
 import numpy as np
@@ -951,22 +952,25 @@ _grad_types = None
 
 
 def _grad_list(tensors, name):
-    """Addresses, sizes and types of a list of tensors, for the ABI."""
+    """Types, addresses and (all contiguous or not) of a list of tensors.  (Whole lists at a time: a call's host time is
+    what its tensors' attributes cost.)"""
     global _grad_types
     torch = _torch()
     if _grad_types is None:
         _grad_types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    n = len(tensors)
+    here = _here() if tensors else 0
     kinds = [_grad_types.get(t.dtype, -1) for t in tensors]
-    here = _here() if n else 0
-    for i, t in enumerate(tensors):
-        if kinds[i] < 0 or t.get_device() != here:
-            raise ValueError(f"{name}[{i}] must be a bf16, fp16 or float32 tensor on the current device cuda:{here}, got "
-                             f"{t.dtype} on {t.device}")
-        if not (t.is_contiguous() or _dense(t)):
-            raise ValueError(f"{name}[{i}] has gaps or repeats (shape {tuple(t.shape)}, strides {t.stride()})")
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
-            (ctypes.c_int32 * n)(*kinds))
+    if -1 in kinds or {t.get_device() for t in tensors} - {here}:
+        for i, t in enumerate(tensors):
+            if kinds[i] < 0 or t.get_device() != here:
+                raise ValueError(f"{name}[{i}] must be a bf16, fp16 or float32 tensor on the current device cuda:{here}, got "
+                                 f"{t.dtype} on {t.device}")
+    packed = all([t.is_contiguous() for t in tensors])
+    if not packed:
+        for i, t in enumerate(tensors):
+            if not (t.is_contiguous() or _dense(t)):
+                raise ValueError(f"{name}[{i}] has gaps or repeats (shape {tuple(t.shape)}, strides {t.stride()})")
+    return array("i", kinds), array("q", [t.data_ptr() for t in tensors]), packed
 
 
 def _dense(t):
@@ -975,19 +979,25 @@ def _dense(t):
     return t.permute(order).is_contiguous()
 
 
+def _at(a):
+    return a.buffer_info()[0]
+
+
 def _grad_scratch(n, device):
     torch = _torch()
-    ws = torch.empty(max(lib().bfp8_grad_workspace_size(n), 16), dtype=torch.uint8, device=device)
-    return torch.empty((), dtype=torch.float32, device=device), ws
+    size = max(lib().bfp8_grad_workspace_size(n), 16)
+    return torch.empty((), dtype=torch.float32, device=device), torch.empty(size, dtype=torch.uint8, device=device), size
 
 
 def grad_norm(tensors):
     """The norm of all the tensors' elements as one vector: a list of CUDA
     tensors (bf16, fp16, fp32 in any mixture) -> fp32 scalar on the device."""
     tensors = list(tensors)
-    ptr, numel, kind = _grad_list(tensors, "tensors")
-    norm, ws = _grad_scratch(len(tensors), tensors[0].device if tensors else "cuda")
-    st = lib().bfp8_grad_norm(ptr, numel, kind, len(tensors), norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream())
+    n = len(tensors)
+    kinds, at, _ = _grad_list(tensors, "tensors")
+    numel = array("q", [t.numel() for t in tensors])
+    norm, ws, size = _grad_scratch(n, tensors[0].device if n else "cuda")
+    st = lib().bfp8_grad_norm(_at(at), _at(numel), _at(kinds), n, norm.data_ptr(), ws.data_ptr(), size, _stream())
     if st:
         _check(st)
     return norm
@@ -999,20 +1009,24 @@ def clip_grads(tensors, max_norm: float, out=None):
     same shapes and strides: an optimizer's own buffers).  Returns the norm
     before, an fp32 scalar on the device; nothing waits for it."""
     tensors = list(tensors)
-    ptr, numel, kind = _grad_list(tensors, "tensors")
-    optr, okind = ptr, kind
+    n = len(tensors)
+    kinds, at, packed = _grad_list(tensors, "tensors")
+    to_kinds, to = kinds, at
     if out is not None:
         out = list(out)
-        if len(out) != len(tensors):
-            raise ValueError(f"{len(tensors)} tensors, {len(out)} outputs")
-        for i, (t, o) in enumerate(zip(tensors, out)):
-            if t.shape != o.shape or not (t.is_contiguous() and o.is_contiguous() or t.stride() == o.stride()):
-                raise ValueError(f"out[{i}] must have the shape and strides of tensors[{i}], {tuple(t.shape)} {t.stride()}, "
-                                 f"got {tuple(o.shape)} {o.stride()}")
-        optr, _, okind = _grad_list(out, "out")
-    norm, ws = _grad_scratch(len(tensors), tensors[0].device if tensors else "cuda")
-    st = lib().bfp8_clip_grads(ptr, numel, kind, len(tensors), max_norm, optr, okind, norm.data_ptr(), ws.data_ptr(),
-                               ws.numel(), _stream())
+        if len(out) != n:
+            raise ValueError(f"{n} tensors, {len(out)} outputs")
+        to_kinds, to, to_packed = _grad_list(out, "out")
+        if [t.shape for t in tensors] != [o.shape for o in out] or \
+                not (packed and to_packed or [t.stride() for t in tensors] == [o.stride() for o in out]):
+            for i, (t, o) in enumerate(zip(tensors, out)):
+                if t.shape != o.shape or not (t.is_contiguous() and o.is_contiguous() or t.stride() == o.stride()):
+                    raise ValueError(f"out[{i}] must have the shape and strides of tensors[{i}], {tuple(t.shape)} "
+                                     f"{t.stride()}, got {tuple(o.shape)} {o.stride()}")
+    numel = array("q", [t.numel() for t in tensors])
+    norm, ws, size = _grad_scratch(n, tensors[0].device if n else "cuda")
+    st = lib().bfp8_clip_grads(_at(at), _at(numel), _at(kinds), n, max_norm, _at(to), _at(to_kinds), norm.data_ptr(),
+                               ws.data_ptr(), size, _stream())
     if st:
         _check(st)
     return norm
