@@ -29,7 +29,9 @@
 // (mma.sync on 16 rows instead, which needs no such blocks: 59 us for one token,
 // 399 for 16, as its 8-bit form takes 250 issued instructions a warp and stage.)
 //
-//   warp 0         producer
+//   warps 0, 14, 15  producers: each a third of a stage's boxes (one warp issues a box in
+//                  about 90 ns, whatever it holds: narrow experts' 13 rows of a K-block
+//                  are 1.7 KB)
 //   warps 1, 3     MMA issuers, on alternate stages
 //   warp 2         the weights' scales, into slots ahead of the products (loaded where
 //                  they are used they cost a trip to L2 a stage)
@@ -54,7 +56,8 @@ static __device__ uint32_t g_mlp_error;
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-constexpr int kMlpThreads = 448;
+constexpr int kMlpThreads = 512;
+constexpr int kProducers = 3;       // warps 0, 14, 15
 constexpr int kIssuers = 2;         // warps 1, 3
 constexpr int kCoders = 6;          // warps 8-13
 constexpr int kActBatch = 8;        // groups of 128 activations that half a warp of them loads at once
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
-      mbar_init(full0 + 8 * i, 1);
+      mbar_init(full0 + 8 * i, kProducers);
       mbar_init(empty0 + 8 * i, 1);
     }
     for (int i = 0; i < kBufs; ++i) {
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
       mbar_init(sfull0 + 8 * i, 32);  // one cp.async arrival a lane
       mbar_init(sempty0 + 8 * i, 4);
     }
-    mbar_init(xready, kMlpThreads / 32 - 1 - kIssuers);
+    mbar_init(xready, kMlpThreads / 32 - kProducers - kIssuers);
     mbar_init(drain, kIssuers);
     *abort_flag = 0;
     *never = 0;
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
   // h + kHalves, ..; later they would wait behind the weights).
   const int Kb = (int)cdiv(a.K, kBlock), Ib = (int)cdiv(a.I, kBlock);
   const int l16 = lane & 15, half = 2 * (warp == 2 ? 0 : warp - 3) + (lane >> 4), groups = a.T * Kb;
-  constexpr int kHalves = 2 * (kMlpThreads / 32 - 1 - kIssuers), kBatch = 6;
+  constexpr int kHalves = 2 * (kMlpThreads / 32 - kProducers - kIssuers), kBatch = 6;
   uint4 xv[kBatch];
   int x_t = half / Kb, x_kb = half - x_t * Kb;  // token and K-block of the half's next group
   auto load_tokens = [&](int g0) {
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
       for (x_kb += kHalves; x_kb >= Kb; x_kb -= Kb) ++x_t;
     }
   };
-  if (warp == 2 || warp >= 4) load_tokens(0);
+  if (warp == 2 || (warp >= 4 && warp < 14)) load_tokens(0);
   __syncthreads();
   // ------------------------------------------------------------ plan: the reached experts in order, their slots by token
   for (int s = tid; s < slots; s += kMlpThreads) {
@@ -298,47 +301,44 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
     *abort_flag = 1;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  if (warp == 0 || warp >= 14) {
+    // ------------------------------------------------------------ producers
     if (lane == 0) {
+      const int me = warp == 0 ? 0 : warp - 13;
       Ring at{0, 0};
       int issued = 0;
       bool ok = true;
-      auto stage = [&](uint32_t bytes) {  // the next stage, free; its barrier expects `bytes`
+      // the next stage, free, of `blocks` boxes of `bytes`; this producer's: me, me + kProducers, ..
+      auto stage = [&](int blocks, int bytes, auto&& box) {
         const int st = at.at;
         ok = mbar_wait_bounded(empty0 + 8 * st, at.parity ^ 1u, kWaitLimitNs, abort_flag);
         if (!ok) {
           fail(1u);
-          return -1;
+          return;
         }
-        mbar_arrive_expect_tx(full0 + 8 * st, bytes);
+        mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)((blocks + kProducers - 1 - me) / kProducers * bytes));
+        for (int b = me; b < blocks; b += kProducers) box(ring + st * kStageBytes, full0 + 8 * st, b);
         at.step(1, ST);
         ++issued;
-        return st;
       };
       for (int u = u0; u < u1 && ok; ++u) {
         const int r = u / per_expert, i0 = (u - r * per_expert) * kPairs, e = (int)(s_expert[r] & 0xFFFFu);
-        for (int kb0 = 0; kb0 < Kb; kb0 += kUnitBlocks) {
-          const int blocks = min(kUnitBlocks, Kb - kb0);
-          const int st = stage((uint32_t)(blocks * kUnitRows * kBlock));
-          if (st < 0) break;
-          for (int b = 0; b < blocks; ++b)
-            tma_load_4d(ring + st * kStageBytes + b * kUnitRows * kBlock, &map_gu, full0 + 8 * st, (kb0 + b) * kBlock, i0, 0, e);
-        }
+        for (int kb0 = 0; kb0 < Kb && ok; kb0 += kUnitBlocks)
+          stage(min(kUnitBlocks, Kb - kb0), kUnitRows * kBlock, [&](uint32_t to, uint32_t bar, int b) {
+            tma_load_4d(to + b * kUnitRows * kBlock, &map_gu, bar, (kb0 + b) * kBlock, i0, 0, e);
+          });
       }
       for (int r = 0; r < experts2 && ok; ++r) {
         const int e = (int)(s_expert[r] & 0xFFFFu);
-        for (int kb0 = 0; kb0 < Ib; kb0 += blocks2) {
-          const int blocks = min(blocks2, Ib - kb0);
-          const int st = stage((uint32_t)(blocks * a.rows * kBlock));
-          if (st < 0) break;
-          for (int b = 0; b < blocks; ++b)
-            tma_load_3d(ring + st * kStageBytes + b * group * kBlock, &map_d, full0 + 8 * st, (kb0 + b) * kBlock, n0, e);
-        }
+        for (int kb0 = 0; kb0 < Ib && ok; kb0 += blocks2)
+          stage(min(blocks2, Ib - kb0), a.rows * kBlock, [&](uint32_t to, uint32_t bar, int b) {
+            tma_load_3d(to + b * group * kBlock, &map_d, bar, (kb0 + b) * kBlock, n0, e);
+          });
       }
-      if (!ok)  // copies already issued land before this CTA's shared memory goes away
+      if (!ok) {  // copies already issued land before this CTA's shared memory goes away
         for (int i = issued > ST ? issued - ST : 0; i < issued; ++i)
           mbar_wait_bounded(full0 + 8 * (i % ST), (uint32_t)((i / ST) & 1), kWaitLimitNs, never);
+      }
     }
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA issuers
@@ -732,7 +732,9 @@ MlpGeom mlp_geom(int64_t T, int64_t K, int64_t I, int64_t N, int num_sms) {
   const int64_t scales = (Kb > g.buffers * Ib ? Kb : g.buffers * Ib) * 8 * nt * 4;
   g.group = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   const int64_t stages = ((int64_t)227 * 1024 - 1024 - codes - scales - kMiscBytes) / kStageBytes;
-  g.stages = (int)(stages < kMlpMaxStages ? stages : kMlpMaxStages);
+  // An even number of stages: the two issuers take alternate ones, and a place's next use must be the same issuer's, who
+  // has seen the one before (the other could take a phase that is two behind for the one it waits for).
+  g.stages = (int)(stages < kMlpMaxStages ? stages : kMlpMaxStages) & ~1;
   g.off_scale = (int)(g.stages * kStageBytes + codes);
   g.off_misc = (int)(g.off_scale + scales);
   g.smem = g.off_misc + kMiscBytes + 1024;
