@@ -101,6 +101,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 // max(amax, 1e-12) / 448 as one product with 1/448: within an ulp of group_scale's quotient.
 __device__ __forceinline__ float scale_near(float amax) { return __fmul_rn(fmaxf(amax, kAmaxFloor), 1.0f / kE4m3Max); }
 // Place n of a ring of `size`, by steps of at most its size, and the parity of its turn.
@@ -342,30 +347,36 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
     }
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA issuers
-    if (lane == 0) {
+    // (The whole warp goes through the loop and one elected lane issues: a lane by itself takes 326 cycles a stage, this way 252.)
+    {
       const int me = warp >> 1;
+      const bool lead = elect_one();
       Ring at{me, 0}, buf{me, 0};  // (both rings have a place an issuer at least)
       int n = 0;                   // stages of all issuers
       bool ok = true;
       auto issue = [&](uint32_t codes, uint32_t idesc) {
         ok = mbar_spin_bounded(tempty0 + 8 * buf.at, buf.parity ^ 1u, kWaitLimitNs, abort_flag) &&
              mbar_spin_bounded(full0 + 8 * at.at, at.parity, kWaitLimitNs, abort_flag);
+        ok = __all_sync(kAll, ok);
         if (!ok) {
-          fail(2u);
+          if (lane == 0) fail(2u);
           return;
         }
         tc_fence_after();
         const uint64_t da = desc_kmajor_sw128(ring + (uint32_t)(at.at * kStageBytes)), db = desc_kmajor_sw128(codes);
         const uint32_t d = tmem_base + (uint32_t)(buf.at * kBufCols);
+        if (lead) {
 #pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k) mma_e4m3(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), idesc, k > 0 ? 1u : 0u);
-        mma_commit(empty0 + 8 * at.at);
-        mma_commit(tfull0 + 8 * buf.at);
+          for (int k = 0; k < kBlock / 32; ++k) mma_e4m3(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), idesc, k > 0 ? 1u : 0u);
+          mma_commit(empty0 + 8 * at.at);
+          mma_commit(tfull0 + 8 * buf.at);
+        }
+        __syncwarp();
         at.step(kIssuers, ST);
         buf.step(kIssuers, kBufs);
       };
-      ok = mbar_wait_bounded(xready, 0, kWaitLimitNs, abort_flag);
-      if (!ok) fail(2u);
+      ok = __all_sync(kAll, mbar_wait_bounded(xready, 0, kWaitLimitNs, abort_flag));
+      if (!ok && lane == 0) fail(2u);
       constexpr uint32_t idesc1 = idesc_e4m3_f32(128, kUnitBlocks * NC);
       for (int u = u0; u < u1 && ok; ++u)
         for (int j = 0; j < items1 && ok; ++j, ++n)
@@ -373,15 +384,18 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
       const uint32_t idesc2 = idesc_e4m3_f32(128, max(blocks2 * NC, 16));
       Ring h{0, 0};
       for (int r = 0; r < experts2 && ok; ++r) {
-        ok = mbar_wait_bounded(hfull0 + 8 * h.at, h.parity, 2 * kWaitLimitNs, abort_flag);
-        if (!ok) fail(4u);
+        ok = __all_sync(kAll, mbar_wait_bounded(hfull0 + 8 * h.at, h.parity, 2 * kWaitLimitNs, abort_flag));
+        if (!ok && lane == 0) fail(4u);
         for (int j = 0; j < items2 && ok; ++j, ++n)
           if (n % kIssuers == me) issue(area + (uint32_t)((h.at * Ib + j * blocks2) * NT * kAtom), idesc2);
         h.step(1, a.buffers);
       }
       // every MMA issued completes before tensor memory is released
-      mma_commit(drain);
-      if (!mbar_wait_bounded(drain, 0, kWaitLimitNs, never)) fail(32u);
+      if (lead) {
+        mma_commit(drain);
+        if (!mbar_wait_bounded(drain, 0, kWaitLimitNs, never)) fail(32u);
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ the tokens' codes, by all of these warps
