@@ -307,22 +307,26 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
   };
 
   if (warp == 0 || warp >= 14) {
-    // ------------------------------------------------------------ producers
-    if (lane == 0) {
+    // ------------------------------------------------------------ producers (one elected lane of a warp that stays together)
+    {
       const int me = warp == 0 ? 0 : warp - 13;
+      const bool lead = elect_one();
       Ring at{0, 0};
       int issued = 0;
       bool ok = true;
       // the next stage, free, of `blocks` boxes of `bytes`; this producer's: me, me + kProducers, ..
       auto stage = [&](int blocks, int bytes, auto&& box) {
         const int st = at.at;
-        ok = mbar_wait_bounded(empty0 + 8 * st, at.parity ^ 1u, kWaitLimitNs, abort_flag);
+        ok = __all_sync(kAll, mbar_wait_bounded(empty0 + 8 * st, at.parity ^ 1u, kWaitLimitNs, abort_flag));
         if (!ok) {
-          fail(1u);
+          if (lane == 0) fail(1u);
           return;
         }
-        mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)((blocks + kProducers - 1 - me) / kProducers * bytes));
-        for (int b = me; b < blocks; b += kProducers) box(ring + st * kStageBytes, full0 + 8 * st, b);
+        if (lead) {
+          mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)((blocks + kProducers - 1 - me) / kProducers * bytes));
+          for (int b = me; b < blocks; b += kProducers) box(ring + st * kStageBytes, full0 + 8 * st, b);
+        }
+        __syncwarp();
         at.step(1, ST);
         ++issued;
       };
@@ -340,10 +344,11 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
             tma_load_3d(to + b * group * kBlock, &map_d, bar, (kb0 + b) * kBlock, n0, e);
           });
       }
-      if (!ok) {  // copies already issued land before this CTA's shared memory goes away
+      if (!ok && lead) {  // copies already issued land before this CTA's shared memory goes away
         for (int i = issued > ST ? issued - ST : 0; i < issued; ++i)
           mbar_wait_bounded(full0 + 8 * (i % ST), (uint32_t)((i / ST) & 1), kWaitLimitNs, never);
       }
+      __syncwarp();
     }
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA issuers
