@@ -745,9 +745,10 @@ bfp8_status bfp8_cast_e4m3(const float* x, int64_t n, void* q, bfp8_stream_t str
 }  // extern "C"
 
 namespace {
-// Workspace of the few-token layer: the count of CTAs that have arrived, the choices, their weights, the activations.
+// Workspace of the few-token layer: the counts of CTAs that have arrived, the choices, their weights, the activations,
+// their codes and scales.
 struct MlpLayout {
-  size_t idx, w, act, total;
+  size_t idx, w, act, codes, scales, total;
 };
 MlpLayout mlp_layout(int64_t T, int64_t k, int64_t I) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -755,7 +756,9 @@ MlpLayout mlp_layout(int64_t T, int64_t k, int64_t I) {
   L.idx = 256;
   L.w = up(L.idx + (size_t)(T * k) * 4);
   L.act = up(L.w + (size_t)(T * k) * 4);
-  L.total = L.act + (size_t)(T * k) * (size_t)I * 4;
+  L.codes = up(L.act + (size_t)(T * k) * (size_t)I * 4);
+  L.scales = L.codes + (size_t)(T * k) * (size_t)cdiv(I, kBlock) * kBlock;
+  L.total = L.scales + (size_t)(T * k) * (size_t)cdiv(I, kBlock) * 4;
   return L;
 }
 }  // namespace
@@ -813,7 +816,7 @@ bfp8_status bfp8_moe_mlp_decode(const void* x, int64_t T, int64_t K, int64_t ldx
   a.x = (const uint16_t*)x, a.ldx = ldx;
   a.T = (int)T, a.K = (int)K, a.E = (int)E, a.k = (int)k, a.I = (int)I, a.N = (int)N;
   a.idx = idx, a.w = w, a.sgu = sgu, a.ldsgu = ldsgu, a.sd = sd, a.ldsd = ldsd;
-  a.act = (float*)(base + L.act), a.arrived = arrived;
+  a.act = (float*)(base + L.act), a.codes = base + L.codes, a.scales = (float*)(base + L.scales), a.arrived = arrived;
   a.y = (uint16_t*)y, a.ldy = ldy;
   const char* msg = nullptr;
   e = launch_moe_mlp(a, (const uint8_t*)qgu, ldgu, (const uint8_t*)qd, ldd, sms, (cudaStream_t)stream, &msg);

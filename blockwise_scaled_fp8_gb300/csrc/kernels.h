@@ -148,7 +148,7 @@ struct RouteArgs {
   int32_t* idx;
   float* w;
   int vec, bias_vec, group_lanes, group_whole;  // set by the launcher
-  uint32_t* zero;  // set to 0, or null
+  uint32_t* zero;  // two words that are set to 0, or null
 };
 cudaError_t launch_moe_route(const RouteArgs& a, cudaStream_t st);
 
@@ -262,7 +262,9 @@ struct MlpArgs {
   const float* sd;
   int64_t ldsd;
   float* act;         // [T*k, I]
-  uint32_t* arrived;  // 0 at the start
+  uint8_t* codes;     // [T*k, Ib, 128] of them
+  float* scales;      // [T*k, Ib]
+  uint32_t* arrived;  // two counts, 0 at the start
   uint16_t* y;
   int64_t ldy;
   // set by the launcher: rows of D a CTA, the power of two that holds them, buffers of activations, stages of the ring, ..

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteArg
   pdl_wait();
   const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
   const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + warp;
-  if (a.zero && blockIdx.x == 0 && threadIdx.x == 0) *a.zero = 0;
+  if (a.zero && blockIdx.x == 0 && threadIdx.x == 0) a.zero[0] = a.zero[1] = 0;
   if (t >= a.T) return;
   const int E = (int)a.E, e0 = lane * VPL;
   float* mine_s = s_route + warp * (VPL * 64);  // (E + 32 <= 64 VPL)

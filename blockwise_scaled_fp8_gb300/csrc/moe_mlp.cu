@@ -13,7 +13,11 @@
 //     then of the down rows;
 //   - the exchange of the activations between the two (every CTA needs all of
 //     them) is a barrier over the grid that only the warps behind the ring wait
-//     for: the down weights do not depend on it and fill the ring meanwhile.
+//     for: the down weights do not depend on it and fill the ring meanwhile.  The
+//     activations pass in fp32 and each CTA codes them for itself; where they are
+//     many, each CTA codes its share, and a second barrier hands out the codes (16
+//     tokens, 8 of 64 experts: coding all of them took a CTA as long as reading its
+//     weights, 251 us in all).
 //
 // First part: a unit is 16 gate rows and the 16 up rows of the same features; the
 // units of all reached experts are shared evenly.  Second part: CTA c takes the
@@ -61,6 +65,7 @@ constexpr int kProducers = 3;       // warps 0, 14, 15
 constexpr int kIssuers = 2;         // warps 1, 3
 constexpr int kCoders = 6;          // warps 8-13
 constexpr int kActBatch = 8;        // groups of 128 activations that half a warp of them loads at once
+constexpr int kSharedGroups = 4;    // groups a CTA from which on the CTAs share the coding
 constexpr int kStageBytes = 128 * kBlock;
 constexpr int kPairs = 16;          // gate (and up) rows of a unit
 constexpr int kUnitRows = 2 * kPairs, kUnitBlocks = 128 / kUnitRows;  // K-blocks of a stage of the first part
@@ -118,6 +123,17 @@ struct Ring {
   }
 };
 
+// Eight values of a group of 16 lanes: their codes and the group's scale.
+__device__ __forceinline__ float code8(const float4& p, const float4& q, uint32_t& lo, uint32_t& hi) {
+  float m = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))),
+                  fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w))));
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  const float s = scale_near(m), y = recip_rn(s);
+  lo = cvt_e4m3x2(p.x * y, p.y * y) | cvt_e4m3x2(p.z * y, p.w * y) << 16;
+  hi = cvt_e4m3x2(q.x * y, q.y * y) | cvt_e4m3x2(q.z * y, q.w * y) << 16;
+  return s;
+}
 // C consecutive 32-bit columns of this warp's 32 lanes of tensor memory.
 template <int C>
 __device__ __forceinline__ void tmem_cols(uint32_t taddr, uint32_t (&r)[C]) {
@@ -301,6 +317,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
   const int group = a.group, blocks2 = 128 / group;                         // `group` rows of `blocks2` K-blocks a stage
   const int items2 = (int)cdiv(Ib, blocks2);
   const int experts2 = n0 < a.N ? reached : 0;
+  const bool shared_codes = slots * Ib >= kSharedGroups * grid;             // the CTAs share the activations' coding
   auto fail = [&](uint32_t code) {
     if (!*abort_flag) atomicOr(&g_mlp_error, code);
     *abort_flag = 1;
@@ -613,7 +630,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
             a.y[(int64_t)t * a.ldy + n0 + i] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
           }
       }
-    } else if (experts2 > 0) {
+    } else if (experts2 > 0 || (shared_codes && reached > 0)) {
       // ------------------------------------------------------------ the activations' codes
       // Teams of the six warps take an expert each, in turn: six teams, three where an expert's tokens have more groups
       // than a warp loads at once, and no more teams than buffers (a team that is a whole turn of the
@@ -623,64 +640,124 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
       const int teams = most >= 6 ? 6 : min(most, 3), size = kCoders / teams;
       const int h = 2 * (coder % size) + (lane >> 4), halves = 2 * size;
       bool ok = true;
-      if (coder == 0) {  // (one warp asks: more of them hold the arrivals up)
+      // until every CTA has arrived (one warp asks: more of them hold the arrivals up)
+      auto wait_arrived = [&](const uint32_t* count) {
         const uint64_t t0 = globaltimer_ns();
-        while (ok && ld_acquire_gpu(a.arrived) < (uint32_t)grid) ok = !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs;
-        if (!__all_sync(kAll, ok) && lane == 0) fail(16u);
-      }
+        bool in = true;
+        while (in && ld_acquire_gpu(count) < (uint32_t)grid) in = !*abort_flag && globaltimer_ns() - t0 < kWaitLimitNs;
+        return __all_sync(kAll, in) != 0;
+      };
+      if (coder == 0 && !wait_arrived(a.arrived) && lane == 0) fail(16u);
       named_sync(3, 32 * kCoders);
       ok = !*abort_flag;
+      if (shared_codes) {
+        // this CTA's share of the groups: every (grid x 2 kCoders)-th, half a warp each
+        for (int g0 = 0; g0 < slots * Ib; g0 += grid * 2 * kCoders) {
+          const int g = g0 + (2 * coder + (lane >> 4)) * grid + cta, slot = g / Ib, blk = g - slot * Ib, k = blk * kBlock + 8 * l16;
+          float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q = p;
+          const bool in = ok && g < slots * Ib;
+          if (in && k < a.I) {  // (a slot without an expert: whatever was there, and not read)
+            const float4* from = reinterpret_cast<const float4*>(a.act + (int64_t)slot * a.I + k);
+            p = __ldcg(from);
+            q = __ldcg(from + 1);
+          }
+          uint32_t lo, hi;
+          const float s = code8(p, q, lo, hi);
+          if (in) {
+            *reinterpret_cast<uint2*>(a.codes + (int64_t)g * kBlock + 8 * l16) = make_uint2(lo, hi);
+            if (l16 == 0) a.scales[g] = s;
+          }
+        }
+        named_sync(3, 32 * kCoders);
+        if (coder == 0) {
+          if (lane == 0 && ok) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.arrived + 1) : "memory");
+          if (!wait_arrived(a.arrived + 1) && lane == 0) fail(16u);
+        }
+        named_sync(3, 32 * kCoders);
+        ok = !*abort_flag;
+      }
       Ring at{0, 0};  // expert r's buffer
       int r = coder / size;
       for (int i = 0; i < r; ++i) at.step(1, a.buffers);
       for (; r < experts2 && ok; r += teams) {
         const uint32_t mask = s_expert[r] >> 16, codes = area + (uint32_t)(at.at * Ib * NT * kAtom);
         float* scales = s_scale + at.at * Ib * NC;
+        auto buffer_free = [&]() {
+          const bool in = mbar_wait_bounded(hempty0 + 8 * at.at, at.parity ^ 1u, kWaitLimitNs, abort_flag);
+          if (__all_sync(kAll, in)) return true;
+          if (lane == 0) fail(16u);
+          return false;
+        };
         const int first = s_start[r], of_expert = __popc(mask) * Ib;
-        int c = h / Ib, blk = h - c * Ib;  // of the half's next group: token of the expert, K-block
-        for (int g0 = 0; g0 < of_expert; g0 += kActBatch * halves) {
-          float4 v[kActBatch][2];
-          const int c0 = c, blk0 = blk;
+        const int turn0 = (coder % size) * 32 + lane;
+        if (shared_codes) {
+          // codes as they are: 16 bytes a lane, eight lanes a group
+          for (int i0 = 0; i0 < 8 * of_expert; i0 += kActBatch * 32 * size) {
+            uint4 v[kActBatch];
 #pragma unroll
-          for (int i = 0; i < kActBatch; ++i) {
-            if (g0 + i * halves < of_expert) {  // (of some half of the team)
-              const int k = blk * kBlock + 8 * l16;
-              v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (g0 + i * halves + h < of_expert && k < a.I) {
-                const float4* p = reinterpret_cast<const float4*>(a.act + (int64_t)(s_slot[first + c] & 0xFFFF) * a.I + k);
-                v[i][0] = __ldcg(p);
-                v[i][1] = __ldcg(p + 1);
-              }
-              for (blk += halves; blk >= Ib; blk -= Ib) ++c;
+            for (int i = 0; i < kActBatch; ++i) {
+              const int n = i0 + i * 32 * size + turn0, g = n >> 3, c = g / Ib;
+              if (g < of_expert)
+                v[i] = __ldcg(reinterpret_cast<const uint4*>(
+                    a.codes + ((int64_t)(s_slot[first + c] & 0xFFFF) * Ib + (g - c * Ib)) * kBlock + 16 * (n & 7)));
             }
-          }
-          if (g0 == 0) {  // the values are on their way when the buffer is asked for
-            const bool free = mbar_wait_bounded(hempty0 + 8 * at.at, at.parity ^ 1u, kWaitLimitNs, abort_flag);
-            if (!(ok = __all_sync(kAll, free))) {
-              if (lane == 0) fail(16u);
-              break;
+            // and a group's scale a lane: as many groups a batch as the team has lanes
+            static_assert(kActBatch == 8, "a lane a group");
+            const int gs = i0 / 8 + turn0, cs = gs / Ib;
+            float sc = 0.0f;
+            int slot_s = 0;
+            if (gs < of_expert) {
+              slot_s = s_slot[first + cs];
+              sc = __ldcg(a.scales + (int64_t)(slot_s & 0xFFFF) * Ib + (gs - cs * Ib)) * s_weight[slot_s & 0xFFFF];
             }
-          }
-          c = c0, blk = blk0;
+            if (i0 == 0 && !(ok = buffer_free())) break;
 #pragma unroll
-          for (int i = 0; i < kActBatch; ++i) {
-            if (g0 + i * halves < of_expert) {
-              const float4 p = v[i][0], q = v[i][1];
-              float m = fmaxf(fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(p.z), fabsf(p.w))),
-                              fmaxf(fmaxf(fabsf(q.x), fabsf(q.y)), fmaxf(fabsf(q.z), fabsf(q.w))));
-#pragma unroll
-              for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-              const float s = scale_near(m), y = recip_rn(s);
-              const uint32_t lo = cvt_e4m3x2(p.x * y, p.y * y) | cvt_e4m3x2(p.z * y, p.w * y) << 16;
-              const uint32_t hi = cvt_e4m3x2(q.x * y, q.y * y) | cvt_e4m3x2(q.z * y, q.w * y) << 16;
-              if (g0 + i * halves + h < of_expert) {
-                const int slot = s_slot[first + c], t = slot >> 16;
-                const uint32_t to = codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 +
-                                                       (((l16 >> 1) ^ (t & 7)) << 4) + 8 * (l16 & 1));
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(lo), "r"(hi) : "memory");
-                if (l16 == 0) scales[blk * NC + t] = s * s_weight[slot & 0xFFFF];
+            for (int i = 0; i < kActBatch; ++i) {
+              const int n = i0 + i * 32 * size + turn0, g = n >> 3, c = g / Ib, blk = g - c * Ib;
+              if (g < of_expert) {
+                const int t = s_slot[first + c] >> 16;
+                const uint32_t to = codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 + (((n & 7) ^ (t & 7)) << 4));
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                             : "memory");
               }
-              for (blk += halves; blk >= Ib; blk -= Ib) ++c;
+            }
+            if (gs < of_expert) scales[(gs - cs * Ib) * NC + (slot_s >> 16)] = sc;
+          }
+        } else {
+          int c = h / Ib, blk = h - c * Ib;  // of the half's next group: token of the expert, K-block
+          for (int g0 = 0; g0 < of_expert; g0 += kActBatch * halves) {
+            float4 v[kActBatch][2];
+            const int c0 = c, blk0 = blk;
+#pragma unroll
+            for (int i = 0; i < kActBatch; ++i) {
+              if (g0 + i * halves < of_expert) {  // (of some half of the team)
+                const int k = blk * kBlock + 8 * l16;
+                v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (g0 + i * halves + h < of_expert && k < a.I) {
+                  const float4* p = reinterpret_cast<const float4*>(a.act + (int64_t)(s_slot[first + c] & 0xFFFF) * a.I + k);
+                  v[i][0] = __ldcg(p);
+                  v[i][1] = __ldcg(p + 1);
+                }
+                for (blk += halves; blk >= Ib; blk -= Ib) ++c;
+              }
+            }
+            if (g0 == 0 && !(ok = buffer_free())) break;  // the values are on their way when the buffer is asked for
+            c = c0, blk = blk0;
+#pragma unroll
+            for (int i = 0; i < kActBatch; ++i) {
+              if (g0 + i * halves < of_expert) {
+                const float4 p = v[i][0], q = v[i][1];
+                uint32_t lo, hi;
+                const float s = code8(p, q, lo, hi);
+                if (g0 + i * halves + h < of_expert) {
+                  const int slot = s_slot[first + c], t = slot >> 16;
+                  const uint32_t to = codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 +
+                                                         (((l16 >> 1) ^ (t & 7)) << 4) + 8 * (l16 & 1));
+                  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(lo), "r"(hi) : "memory");
+                  if (l16 == 0) scales[blk * NC + t] = s * s_weight[slot & 0xFFFF];
+                }
+                for (blk += halves; blk >= Ib; blk -= Ib) ++c;
+              }
             }
           }
         }
