@@ -65,7 +65,10 @@ constexpr int kProducers = 3;       // warps 0, 14, 15
 constexpr int kIssuers = 2;         // warps 1, 3
 constexpr int kCoders = 6;          // warps 8-13
 constexpr int kActBatch = 8;        // groups of 128 activations that half a warp of them loads at once
-constexpr int kSharedGroups = 4;    // groups a CTA from which on the CTAs share the coding
+// Groups a CTA from which on the CTAs share the coding.  Shared / each for itself, us: 64 experts of 3 x 2048 x 4096, 8 a token:
+// 2 tokens (1.7 groups a CTA) 72.8 / 71.8, 3 tokens 91.3 / 93.2, 4 tokens 110.5 / 114.5, 8 tokens 151 / 175, 16 tokens 211 / 251;
+// 128 of 3 x 704 x 1920, 6 a token: 5 tokens (1.2) 36.1 / 38.0, 16 tokens 77 / 87.
+constexpr int kSharedGroups = 1;
 constexpr int kStageBytes = 128 * kBlock;
 constexpr int kPairs = 16;          // gate (and up) rows of a unit
 constexpr int kUnitRows = 2 * kPairs, kUnitBlocks = 128 / kUnitRows;  // K-blocks of a stage of the first part
