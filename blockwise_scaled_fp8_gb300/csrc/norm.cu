@@ -48,6 +48,24 @@ __device__ __forceinline__ uint4 ld_v4(const void* p) {
 __device__ __forceinline__ uint4 shift_words(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t sh) {
   return make_uint4(__funnelshift_r(a, b, sh), __funnelshift_r(b, c, sh), __funnelshift_r(c, d, sh), __funnelshift_r(d, e, sh));
 }
+// The eight bf16 that start `off` bytes (even) into the 32, zeros after the first n.
+__device__ __forceinline__ uint4 shifted8(const uint4& a, const uint4& b, int off, int n) {
+  const uint32_t sh = 8u * (uint32_t)(off & 2);
+  uint4 out;
+  switch (off >> 2) {  // (the same for a whole row)
+    case 0: out = shift_words(a.x, a.y, a.z, a.w, b.x, sh); break;
+    case 1: out = shift_words(a.y, a.z, a.w, b.x, b.y, sh); break;
+    case 2: out = shift_words(a.z, a.w, b.x, b.y, b.z, sh); break;
+    default: out = shift_words(a.w, b.x, b.y, b.z, b.w, sh);
+  }
+  if (n < kVec) {
+    out.x = n >= 2 ? out.x : n == 1 ? out.x & 0xFFFFu : 0u;
+    out.y = n >= 4 ? out.y : n == 3 ? out.y & 0xFFFFu : 0u;
+    out.z = n >= 6 ? out.z : n == 5 ? out.z & 0xFFFFu : 0u;
+    out.w = n == 7 ? out.w & 0xFFFFu : 0u;
+  }
+  return out;
+}
 // Eight bf16 of a row from feature k on, zeros past its end.
 template <bool VEC>
 __device__ __forceinline__ uint4 load_row8(const uint16_t* row, int k, int K) {
@@ -55,29 +73,14 @@ __device__ __forceinline__ uint4 load_row8(const uint16_t* row, int k, int K) {
     return k < K ? ld_v4(row + k) : make_uint4(0, 0, 0, 0);
   } else {
     // the two aligned 16 bytes that hold them, shifted (each holds one of the row's elements at least, or is not read)
-    uint4 out = make_uint4(0, 0, 0, 0);
-    if (k >= K) return out;
+    if (k >= K) return make_uint4(0, 0, 0, 0);
     const uintptr_t at = reinterpret_cast<uintptr_t>(row + k);
     const int off = (int)(at & 15);
     const uint4* p = reinterpret_cast<const uint4*>(at - off);
     const uint4 a = ld_v4(p);
     uint4 b = make_uint4(0, 0, 0, 0);
     if (k + (16 - off) / 2 < K) b = ld_v4(p + 1);
-    const uint32_t sh = 8u * (uint32_t)(off & 2);
-    switch (off >> 2) {  // (the same for a whole row)
-      case 0: out = shift_words(a.x, a.y, a.z, a.w, b.x, sh); break;
-      case 1: out = shift_words(a.y, a.z, a.w, b.x, b.y, sh); break;
-      case 2: out = shift_words(a.z, a.w, b.x, b.y, b.z, sh); break;
-      default: out = shift_words(a.w, b.x, b.y, b.z, b.w, sh);
-    }
-    if (k + kVec > K) {  // zeros past the row's end
-      const int n = K - k;
-      out.x = n >= 2 ? out.x : n == 1 ? out.x & 0xFFFFu : 0u;
-      out.y = n >= 4 ? out.y : n == 3 ? out.y & 0xFFFFu : 0u;
-      out.z = n >= 6 ? out.z : n == 5 ? out.z & 0xFFFFu : 0u;
-      out.w = n == 7 ? out.w & 0xFFFFu : 0u;
-    }
-    return out;
+    return shifted8(a, b, off, K - k);
   }
 }
 template <bool VEC>
@@ -239,14 +242,29 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
 __device__ __forceinline__ void lds_2x64(uint32_t addr, uint64_t& a, uint64_t& b) {
   asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
-// The weights of aligned rows, kept in shared memory as they come, and eight of them from feature k on (zeros past the end).
-__device__ __forceinline__ uint32_t stage_weights(const void* w, int f32, int K, uint32_t to) {
-  const uint32_t bytes = (uint32_t)K * (f32 ? 4u : 2u);
-  for (uint32_t i = 16u * threadIdx.x; i < bytes; i += 16u * blockDim.x) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w) + i));
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + i), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+// The weights, kept in shared memory as they come (zeros up to a whole chunk), and eight of them from feature k on (zeros
+// past the end).
+__host__ __device__ __forceinline__ uint32_t staged_bytes(int K, int f32) {
+  return ((uint32_t)(K + kVec - 1) / kVec * kVec * (f32 ? 4u : 2u) + 127u) / 128u * 128u;
+}
+__device__ __forceinline__ void stage_weights(const void* w, int f32, int K, uint32_t to) {
+  const int padded = (K + kVec - 1) / kVec * kVec;
+  if (K == padded && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+    for (uint32_t i = 16u * threadIdx.x; i < (uint32_t)K * (f32 ? 4u : 2u); i += 16u * blockDim.x) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w) + i));
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + i), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    }
+  } else {
+    for (int i = (int)threadIdx.x; i < padded; i += (int)blockDim.x) {
+      if (f32) {
+        const float v = i < K ? __ldg(static_cast<const float*>(w) + i) : 0.0f;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + 4u * (uint32_t)i), "f"(v) : "memory");
+      } else {
+        const uint16_t v = i < K ? __ldg(static_cast<const uint16_t*>(w) + i) : (uint16_t)0;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2u * (uint32_t)i), "h"(v) : "memory");
+      }
+    }
   }
-  return (bytes + 127u) / 128u * 128u;
 }
 __device__ __forceinline__ void staged_weight8(uint32_t from, int f32, int k, int K, uint64_t (&w)[4]) {
 #pragma unroll
@@ -258,6 +276,25 @@ __device__ __forceinline__ void staged_weight8(uint32_t from, int f32, int k, in
   } else {
     pairs8(lds_v4(from + 2u * (uint32_t)k), w);
   }
+}
+// A row in shared memory as bulk copies bring it: the 16-byte blocks that hold it, its first element `off` bytes into them
+// (0 where it is aligned).  Each block holds a byte of the row, so no copy leaves the tensor's own 16-byte blocks.
+__host__ __device__ __forceinline__ uint32_t row_space(int K, bool aligned) {
+  return aligned ? 2u * (uint32_t)K : (2u * (uint32_t)K + 15u) / 16u * 16u + 32u;
+}
+template <bool ALIGNED>
+__device__ __forceinline__ int row_off(const uint16_t* row) {
+  return ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(row) & 15);
+}
+template <bool ALIGNED>
+__device__ __forceinline__ uint32_t row_copied(const uint16_t* row, int K) {  // bytes
+  return ALIGNED ? 2u * (uint32_t)K : ((uint32_t)row_off<false>(row) + 2u * (uint32_t)K + 15u) / 16u * 16u;
+}
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 lds_row8(uint32_t from, int off, int k, int K) {
+  if (k >= K) return make_uint4(0, 0, 0, 0);
+  if constexpr (ALIGNED) return lds_v4(from + 2u * (uint32_t)k);
+  return shifted8(lds_v4(from + 2u * (uint32_t)k), lds_v4(from + 2u * (uint32_t)k + 16u), off, K - k);
 }
 // `bytes` (a multiple of 16, both addresses 16-byte aligned) from global to shared memory, counted on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -342,14 +379,16 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
   finish_row<VPT, VEC>(a, team, t, live, hv, rstd_of(team_sum(f2_sum(sum2), team, s_slots), K, a.eps));
 }
 
-// Many aligned rows: one CTA an SM, a team of one, two or four warps a row (so that
+// Many rows: one CTA an SM, a team of one, two or four warps a row (so that
 // the rows that fit keep every warp busy), and no barrier between teams.  Rows
 // arrive by bulk copies in slots that hold all of shared memory, whatever the
 // threads are waiting for; row i of a CTA is slot i % slots and team i % teams, and
 // the team that is done with a row asks for the one that takes its slot.  A row is
-// read twice from its slot (the sum of the residual goes back into it): once for its
+// read twice from its slot (the sum of the residual goes back into it where the row is
+// aligned, and is formed again where it is not): once for its
 // squares, once for its codes, four chunks of 256 features at a time, whose eight
 // groups' maxima a halving exchange leaves in a lane each.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const NormArgs a) {
   extern __shared__ __align__(128) uint8_t s_ring[];  // weights, then the slots: [x, residual][K]
   __shared__ uint64_t s_full[kNormMaxSlots];
@@ -357,8 +396,8 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
   __shared__ int s_abort;
   const int K = (int)a.K, tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31, slots = a.slots;
   const int size = a.team, teams = min(slots, kNormWarps / size), team = warp / size, sub = warp % size;
-  const uint32_t row_bytes = 2u * (uint32_t)K, slot_bytes = row_bytes * (a.residual ? 2u : 1u), weight_bytes = a.weight_f32 ? 2u * row_bytes : row_bytes;
-  const uint32_t weights = smem_u32(s_ring), ring = weights + (weight_bytes + 127u) / 128u * 128u, full = smem_u32(s_full);
+  const uint32_t space = row_space(K, ALIGNED), slot_bytes = space * (a.residual ? 2u : 1u);
+  const uint32_t weights = smem_u32(s_ring), ring = weights + staged_bytes(K, a.weight_f32), full = smem_u32(s_full);
   const int64_t rows = a.T > blockIdx.x ? cdiv(a.T - blockIdx.x, (int64_t)gridDim.x) : 0;  // of this CTA: every grid-th
   volatile int* abort_flag = &s_abort;
   pdl_launch_dependents();
@@ -373,9 +412,11 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
   auto issue = [&](int64_t i, int slot) {
     const int64_t t = blockIdx.x + i * gridDim.x;
     const uint32_t to = ring + (uint32_t)slot * slot_bytes;
-    mbar_arrive_expect_tx(full + 8 * slot, slot_bytes);
-    bulk_load(to, a.x + t * a.ldx, row_bytes, full + 8 * slot);
-    if (a.residual) bulk_load(to + row_bytes, a.residual + t * a.ldr, row_bytes, full + 8 * slot);
+    const uint16_t *x = a.x + t * a.ldx, *r = a.residual ? a.residual + t * a.ldr : nullptr;
+    const uint32_t x_bytes = row_copied<ALIGNED>(x, K), r_bytes = r ? row_copied<ALIGNED>(r, K) : 0u;
+    mbar_arrive_expect_tx(full + 8 * slot, x_bytes + r_bytes);
+    bulk_load(to, x - row_off<ALIGNED>(x) / 2, x_bytes, full + 8 * slot);
+    if (r) bulk_load(to + space, r - row_off<ALIGNED>(r) / 2, r_bytes, full + 8 * slot);
   };
   if (tid == 0)
     for (int i = 0; i < slots && i < rows; ++i) issue(i, i);
@@ -397,15 +438,17 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
       *abort_flag = 1;
     }
     uint64_t sum2 = 0;
+    const int off_x = row_off<ALIGNED>(a.x + t * a.ldx), off_r = a.residual ? row_off<ALIGNED>(a.residual + t * a.ldr) : 0;
 #pragma unroll 4
     for (int k = kVec * (32 * sub + lane); k < K; k += 32 * kVec * size) {
-      uint4 h = lds_v4(from + 2u * (uint32_t)k);
+      uint4 h = lds_row8<ALIGNED>(from, off_x, k, K);
       if (a.residual) {
-        h = add8(h, lds_v4(from + row_bytes + 2u * (uint32_t)k));
-        *reinterpret_cast<uint4*>(a.h + t * a.ldh + k) = h;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(from + 2u * (uint32_t)k), "r"(h.x), "r"(h.y), "r"(h.z),
-                     "r"(h.w)
-                     : "memory");
+        h = add8(h, lds_row8<ALIGNED>(from + space, off_r, k, K));
+        store_row8<ALIGNED>(a.h + t * a.ldh, k, K, h);
+        if (ALIGNED)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(from + 2u * (uint32_t)k), "r"(h.x), "r"(h.y), "r"(h.z),
+                       "r"(h.w)
+                       : "memory");
       }
       sum2 = squares8(h, sum2);
     }
@@ -429,12 +472,14 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
           const int k = k0 + kVec * (32 * u + lane);
           uint64_t w[4];
           staged_weight8(weights, a.weight_f32, k, K, w);
-          times8(k < K ? lds_v4(from + 2u * (uint32_t)k) : make_uint4(0, 0, 0, 0), w, v[u]);
+          uint4 h = lds_row8<ALIGNED>(from, off_x, k, K);
+          if (!ALIGNED && a.residual) h = add8(h, lds_row8<ALIGNED>(from + space, off_r, k, K));
+          times8(h, w, v[u]);
           am[u] = amax8(v[u]);
         }
         if (a.y) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) store_row8<true>(a.y + t * a.ldy, k0 + kVec * (32 * u + lane), K, scaled_bf16(v[u], r));
+          for (int u = 0; u < 4; ++u) store_row8<ALIGNED>(a.y + t * a.ldy, k0 + kVec * (32 * u + lane), K, scaled_bf16(v[u], r));
         }
         if (a.q_row) {
           // lane l: chunk u = (l & 8 ? 2 : 0) + (l & 4 ? 1 : 0), group l / 16 of it
@@ -560,11 +605,11 @@ __global__ void __launch_bounds__(256, 4) rms_norm_cols_kernel(const NormArgs a)
 }
 
 // Gradient of every teams-th row, by teams of threads (chunks as above); the teams'
-// sums for the weight go to partial[team of the launch][K].  With RING (aligned
-// rows) the rows of dy, h and dh arrive by bulk copies, iterations ahead, and the
-// weights lie in shared memory (loaded into registers where they are used: a training
-// step's norm, forward and backward, of 16384 x 4096 265 us, so 236).
-template <int VPT, bool RING>
+// sums for the weight go to partial[team of the launch][K].  The rows of dy, h and dh
+// arrive by bulk copies, iterations ahead, and the weights lie in shared memory
+// (rows loaded into registers where they are used: a training step's norm, forward
+// and backward, of 16384 x 4096 265 us, so 236).
+template <int VPT, bool ALIGNED>
 __global__ void __launch_bounds__(256, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
   extern __shared__ __align__(128) uint8_t s_ring[];  // weights, then [stages][dy, h, dh][rows of an iteration][K]
   __shared__ float s_slots[2][8];
@@ -572,45 +617,40 @@ __global__ void __launch_bounds__(256, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
   __shared__ int s_abort;
   const Team team = team_of(a.team);
   const int K = (int)a.K, lane = team.lane, tid = (int)threadIdx.x, stages = a.stages;
-  const uint32_t weights = smem_u32(s_ring), ring = weights + ((uint32_t)K * (a.weight_f32 ? 4u : 2u) + 127u) / 128u * 128u;
-  const uint32_t full = smem_u32(s_full), row_bytes = 2u * (uint32_t)K;
-  const uint32_t part_bytes = (uint32_t)team.count * row_bytes, parts = a.dh ? 3 : 2;
+  const uint32_t weights = smem_u32(s_ring), ring = weights + staged_bytes(K, a.weight_f32), full = smem_u32(s_full);
+  const uint32_t space = row_space(K, ALIGNED), part_bytes = (uint32_t)team.count * space, parts = a.dh ? 3 : 2;
   const int64_t iterations = cdiv(a.T, team.count);
   volatile int* abort_flag = &s_abort;
   pdl_launch_dependents();
-  if (RING) {
-    if (tid == 0) {
-      s_abort = 0;
-      for (int i = 0; i < stages; ++i) mbar_init(full + 8 * i, 1);
-      fence_barrier_init();
-      fence_proxy_async_shared();
-    }
-    __syncthreads();
+  if (tid == 0) {
+    s_abort = 0;
+    for (int i = 0; i < stages; ++i) mbar_init(full + 8 * i, 1);
+    fence_barrier_init();
+    fence_proxy_async_shared();
   }
+  __syncthreads();
   pdl_wait();
   auto issue = [&](int64_t it, int st) {  // by warp 0: the rows of an iteration, a lane a row
-    const int64_t t = it * team.count;
-    const int rows = (int)(a.T - t < team.count ? a.T - t : team.count);
-    if (tid == 0) mbar_arrive_expect_tx(full + 8 * st, (uint32_t)rows * row_bytes * parts);
+    const int64_t t = it * team.count + tid;
+    const bool in = tid < team.count && t < a.T;
+    const uint16_t *d = a.dy + t * a.lddy, *h = a.h + t * a.ldh, *e = a.dh ? a.dh + t * a.lddh : nullptr;
+    const uint32_t nd = in ? row_copied<ALIGNED>(d, K) : 0u, nh = in ? row_copied<ALIGNED>(h, K) : 0u,
+                   ne = in && e ? row_copied<ALIGNED>(e, K) : 0u;
+    const uint32_t bytes = __reduce_add_sync(kAll, nd + nh + ne);
+    if (tid == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
     __syncwarp();
-    if (tid < rows) {
-      const uint32_t to = ring + (uint32_t)st * parts * part_bytes + (uint32_t)tid * row_bytes;
-      bulk_load(to, a.dy + (t + tid) * a.lddy, row_bytes, full + 8 * st);
-      bulk_load(to + part_bytes, a.h + (t + tid) * a.ldh, row_bytes, full + 8 * st);
-      if (a.dh) bulk_load(to + 2 * part_bytes, a.dh + (t + tid) * a.lddh, row_bytes, full + 8 * st);
+    if (in) {
+      const uint32_t to = ring + (uint32_t)st * parts * part_bytes + (uint32_t)tid * space;
+      bulk_load(to, d - row_off<ALIGNED>(d) / 2, nd, full + 8 * st);
+      bulk_load(to + part_bytes, h - row_off<ALIGNED>(h) / 2, nh, full + 8 * st);
+      if (e) bulk_load(to + 2 * part_bytes, e - row_off<ALIGNED>(e) / 2, ne, full + 8 * st);
     }
   };
-  if (RING && tid < 32)
+  if (tid < 32)
     for (int i = 0; i < stages; ++i)
       if ((int64_t)blockIdx.x + (int64_t)i * gridDim.x < iterations) issue((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
-  if (RING) {
-    stage_weights(a.weight, a.weight_f32, K, weights);
-    __syncthreads();
-  }
-  auto weight8 = [&](int k, uint64_t (&w)[4]) {
-    if (RING) staged_weight8(weights, a.weight_f32, k, K, w);
-    else load_weight8<false>(a.weight, a.weight_f32, k, K, w);
-  };
+  stage_weights(a.weight, a.weight_f32, K, weights);
+  __syncthreads();
   float dw[VPT][8] = {};
   int turn = 0, st = 0;
   uint32_t parity = 0;
@@ -620,31 +660,20 @@ __global__ void __launch_bounds__(256, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
     const bool live = t < a.T;
     const float r = live ? a.rstd[t] : 0.0f;
     uint4 hv[VPT], dv[VPT], rv[VPT];
-    if (RING) {
-      // (a wait that gives up leaves the error word set and wrong rows from there on, without further waits or copies)
-      if (!mbar_wait_bounded(full + 8 * st, parity, kWaitLimitNs, abort_flag)) {
-        atomicOr(&g_norm_error, 1u);
-        *abort_flag = 1;
-      }
-      const uint32_t from = ring + (uint32_t)st * parts * part_bytes + (uint32_t)team.index * row_bytes;
+    // (a wait that gives up leaves the error word set and wrong rows from there on, without further waits or copies)
+    if (!mbar_wait_bounded(full + 8 * st, parity, kWaitLimitNs, abort_flag)) {
+      atomicOr(&g_norm_error, 1u);
+      *abort_flag = 1;
+    }
+    const uint32_t from = ring + (uint32_t)st * parts * part_bytes + (uint32_t)team.index * space;
+    const int off_d = row_off<ALIGNED>(a.dy + t * a.lddy), off_h = row_off<ALIGNED>(a.h + t * a.ldh),
+              off_e = row_off<ALIGNED>(a.dh + t * a.lddh);
 #pragma unroll
-      for (int u = 0; u < VPT; ++u) {
-        const int k = kVec * (u * team.size + lane);
-        hv[u] = dv[u] = rv[u] = make_uint4(0, 0, 0, 0);
-        if (live && k < K) {
-          dv[u] = lds_v4(from + 2u * (uint32_t)k);
-          hv[u] = lds_v4(from + part_bytes + 2u * (uint32_t)k);
-          if (a.dh) rv[u] = lds_v4(from + 2 * part_bytes + 2u * (uint32_t)k);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < VPT; ++u) {
-        const int k = kVec * (u * team.size + lane);
-        hv[u] = live ? load_row8<false>(a.h + t * a.ldh, k, K) : make_uint4(0, 0, 0, 0);
-        dv[u] = live ? load_row8<false>(a.dy + t * a.lddy, k, K) : make_uint4(0, 0, 0, 0);
-        rv[u] = live && a.dh ? load_row8<false>(a.dh + t * a.lddh, k, K) : make_uint4(0, 0, 0, 0);
-      }
+    for (int u = 0; u < VPT; ++u) {
+      const int k = live ? kVec * (u * team.size + lane) : K;
+      dv[u] = lds_row8<ALIGNED>(from, off_d, k, K);
+      hv[u] = lds_row8<ALIGNED>(from + part_bytes, off_h, k, K);
+      rv[u] = a.dh ? lds_row8<ALIGNED>(from + 2 * part_bytes, off_e, k, K) : make_uint4(0, 0, 0, 0);
     }
     uint64_t sum2 = 0;
 #pragma unroll
@@ -652,21 +681,19 @@ __global__ void __launch_bounds__(256, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
       uint64_t n[4], d[4], w[4];
       row_times(hv[u], r, n);
       pairs8(dv[u], d);
-      weight8(kVec * (u * team.size + lane), w);
+      staged_weight8(weights, a.weight_f32, kVec * (u * team.size + lane), K, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f2_unpack(f2_fma(d[i], n[i], f2_pack(dw[u][2 * i], dw[u][2 * i + 1])), dw[u][2 * i], dw[u][2 * i + 1]);
         sum2 = f2_fma(f2_mul(d[i], w[i]), n[i], sum2);
       }
     }
-    if (RING) fence_proxy_async_shared();  // these reads, before the copy that takes their place
+    fence_proxy_async_shared();  // these reads, before the copy that takes their place
     const float mean = __fdiv_rn(team_sum(f2_sum(sum2), team, s_slots[turn]), (float)K);
-    if (RING) {
-      if (team.size <= 32) __syncthreads();  // (else it is in the sum)
-      const int64_t next = it + (int64_t)stages * gridDim.x;
-      if (tid < 32 && next < iterations && !__any_sync(kAll, *abort_flag)) issue(next, st);
-      if (++st == stages) st = 0, parity ^= 1u;
-    }
+    if (team.size <= 32) __syncthreads();  // (else it is in the sum)
+    const int64_t next = it + (int64_t)stages * gridDim.x;
+    if (tid < 32 && next < iterations && !__any_sync(kAll, *abort_flag)) issue(next, st);
+    if (++st == stages) st = 0, parity ^= 1u;
     if (live) {
       const uint64_t r2 = f2_pack(r, r), c2 = f2_pack(-r * mean, -r * mean);  // dx = r (d w) - (r mean) n + dh
 #pragma unroll
@@ -676,7 +703,7 @@ __global__ void __launch_bounds__(256, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
         row_times(hv[u], r, n);
         pairs8(dv[u], d);
         pairs8(rv[u], e);
-        weight8(k, w);
+        staged_weight8(weights, a.weight_f32, k, K, w);
         uint32_t out[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -684,7 +711,7 @@ __global__ void __launch_bounds__(256, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
           f2_unpack(f2_add(f2_fma(c2, n[i], f2_mul(r2, f2_mul(d[i], w[i]))), e[i]), lo, hi);
           out[i] = pack_bf16x2(lo, hi);
         }
-        store_row8<RING>(a.dx + t * a.lddx, k, K, make_uint4(out[0], out[1], out[2], out[3]));
+        store_row8<ALIGNED>(a.dx + t * a.lddx, k, K, make_uint4(out[0], out[1], out[2], out[3]));
       }
     }
   }
@@ -753,19 +780,20 @@ static cudaError_t run_norm(const NormArgs& a, int64_t grid, cudaStream_t st) {
                     THREADS, 0, st, a);
 }
 
+template <bool ALIGNED>
 static cudaError_t run_norm_ring(NormArgs a, int num_sms, cudaStream_t st) {
   constexpr int64_t most = 220 * 1024;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(rms_norm_ring_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    attr_err = cudaFuncSetAttribute(rms_norm_ring_kernel<ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  const int64_t weights = cdiv(a.K * (a.weight_f32 ? 4 : 2), 128) * 128, slot = a.K * 2 * (a.residual ? 2 : 1);
+  const int64_t weights = staged_bytes((int)a.K, a.weight_f32), slot = (int64_t)row_space((int)a.K, ALIGNED) * (a.residual ? 2 : 1);
   const int64_t fit = (most - weights) / slot;  // (two of the largest rows)
   a.team = a.K <= 4096 ? 1 : a.K <= 8192 ? 2 : 4;
   a.slots = (int)(fit < kNormMaxSlots ? fit : kNormMaxSlots);
-  return launch_pdl(rms_norm_ring_kernel, (unsigned)(a.T < num_sms ? a.T : num_sms), 32 * kNormWarps,
+  return launch_pdl(rms_norm_ring_kernel<ALIGNED>, (unsigned)(a.T < num_sms ? a.T : num_sms), 32 * kNormWarps,
                     (size_t)(weights + a.slots * slot), st, a);
 }
 
@@ -779,7 +807,7 @@ static cudaError_t norm_rows(NormArgs a, int num_sms, cudaStream_t st) {
     a.team = 1024;
     return K <= 8192 ? run_norm<1024, 1>(a, a.T, st) : run_norm<1024, 2>(a, a.T, st);
   }
-  if (norm_vec(a) && K >= 512 && a.T > num_sms) return run_norm_ring(a, num_sms, st);
+  if (K >= 512 && a.T > num_sms) return norm_vec(a) ? run_norm_ring<true>(a, num_sms, st) : run_norm_ring<false>(a, num_sms, st);
   auto go = [&](auto threads, auto vpt) {
     constexpr int N = decltype(threads)::value, V = decltype(vpt)::value;
     a.team = team_size(K, V, N);
@@ -824,22 +852,23 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& args, int num_sms, cudaStream
   if (a.T > 0) {
     const bool vec = a.K % 8 == 0 && vec_ok(a.dy, a.lddy) && vec_ok(a.h, a.ldh) && vec_ok(a.dh, a.lddh) &&
                      vec_ok(a.dx, a.lddx) && vec_ok(a.weight, 0);
-    auto go = [&](auto vpt) {
+    auto run = [&](auto vpt, auto aligned) {
       constexpr int V = decltype(vpt)::value;
-      if (!vec) return launch_pdl(rms_norm_bwd_kernel<V, false>, (unsigned)g.grid, 256, 0, st, a);
+      constexpr bool A = decltype(aligned)::value;
       // the ring: what the CTAs that an SM holds leave each other (one stage of the largest rows)
       constexpr int64_t most = 220 * 1024 / (V <= 2 ? 3 : V <= 4 ? 2 : 1) - 1024;
       static std::once_flag once;
       static cudaError_t attr_err = cudaSuccess;
       std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(rms_norm_bwd_kernel<V, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        attr_err = cudaFuncSetAttribute(rms_norm_bwd_kernel<V, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
       });
       if (attr_err != cudaSuccess) return attr_err;
-      const int64_t weights = cdiv(a.K * (a.weight_f32 ? 4 : 2), 128) * 128;
-      const int64_t stage = 256 / g.team * a.K * 2 * (a.dh ? 3 : 2), fit = (most - weights) / stage;
+      const int64_t weights = staged_bytes((int)a.K, a.weight_f32);
+      const int64_t stage = 256 / g.team * (int64_t)row_space((int)a.K, A) * (a.dh ? 3 : 2), fit = (most - weights) / stage;
       a.stages = (int)(fit < kBwdMaxStages ? fit : kBwdMaxStages);
-      return launch_pdl(rms_norm_bwd_kernel<V, true>, (unsigned)g.grid, 256, (size_t)(weights + a.stages * stage), st, a);
+      return launch_pdl(rms_norm_bwd_kernel<V, A>, (unsigned)g.grid, 256, (size_t)(weights + a.stages * stage), st, a);
     };
+    auto go = [&](auto vpt) { return vec ? run(vpt, std::true_type{}) : run(vpt, std::false_type{}); };
     const cudaError_t e = g.vpt == 1   ? go(std::integral_constant<int, 1>{})
                           : g.vpt == 2 ? go(std::integral_constant<int, 2>{})
                           : g.vpt == 4 ? go(std::integral_constant<int, 4>{})
