@@ -8,7 +8,7 @@
 //
 // The reached experts' codes are read once, which is what bounds the layer; so
 // the kernel is one stream of them, that no part of the work interrupts:
-//   - one CTA an SM, whose producer brings 16 KB stages by TMA through a ring
+//   - one CTA an SM, whose producers bring 16 KB stages by TMA through a ring
 //     that holds most of shared memory, first its share of the gate and up rows,
 //     then of the down rows;
 //   - the exchange of the activations between the two (every CTA needs all of
@@ -33,15 +33,23 @@
 // (mma.sync on 16 rows instead, which needs no such blocks: 59 us for one token,
 // 399 for 16, as its 8-bit form takes 250 issued instructions a warp and stage.)
 //
-//   warps 0, 14, 15  producers: each a third of a stage's boxes (one warp issues a box in
-//                  about 90 ns, whatever it holds: narrow experts' 13 rows of a K-block
-//                  are 1.7 KB)
+//   warps 0, 14, 15  producers: each a third of a stage's boxes (one warp takes longer to
+//                  issue a box than memory to bring it where it is small: narrow experts'
+//                  13 rows of a K-block are 1.7 KB)
 //   warps 1, 3     MMA issuers, on alternate stages
 //   warp 2         the weights' scales, into slots ahead of the products (loaded where
 //                  they are used they cost a trip to L2 a stage)
 //   warps 4-7      promotion: lane l of warp w is row 32 w + l of the 128
-//   warps 8-13     the activations' codes, experts ahead of the products: one or two
-//                  warps an expert, three or six experts at once
+//   warps 8-13     the activations' codes, experts ahead of the products: one to six
+//                  warps an expert, as many experts at once as there are buffers
+// Producers and issuers are whole warps that stay together, of which an elected lane
+// issues: a lane that leaves the others issues an MMA or a copy a third slower.
+//
+// Measured (with the router's launch; the floor is the reached experts' codes at the
+// copy rate): 64 experts of 3 x 2048 x 4096, 8 a token: one token 44.4 us (floor 30),
+// 4 tokens 111 (99), 16 tokens 212 (212); 128 of 3 x 704 x 1920, 6 a token, 5 tokens
+// 35.9 (16.5).  What is left at few tokens is fixed: the router and its launch 6 us,
+// the plan and the tokens' codes 3.5, the barrier and the first codes behind it 4.
 //
 // Waits are bounded; a role that gives up sets the abort flag, the others leave
 // their loops, and copies and MMAs in flight finish before the CTA exits.

@@ -13,6 +13,14 @@
 //
 // Gradient, with n = h r and g = dy w:
 //   dx = r (g - n mean(g n)) + dh,   dw[k] = sum over t of dy n.
+//
+// What bounds them is memory: each input once and each output once, but for the
+// codes along the columns, which need 128 rows of h after every row's rstd is known:
+// a second pass reads h again (10 bytes an element for 8).  Both in one pass (a
+// cluster of CTAs holding 128 rows in registers, its sums of squares joined through
+// distributed shared memory) took 185 us where the two passes take 124.  16384 x 4096
+// with residual: row codes 84 us (5.6 TB/s of 470 MB), the columns' pass 38 (5.3), the
+// gradient 100 (5.4) and 7 for the sum of its partial sums; a copy moves 6.2-6.7 TB/s.
 #include <mutex>
 #include <type_traits>
 
@@ -608,9 +616,10 @@ __global__ void __launch_bounds__(256, 4) rms_norm_cols_kernel(const NormArgs a)
 // sums for the weight go to partial[team of the launch][K].  The rows of dy, h and dh
 // arrive by bulk copies, iterations ahead, and the weights lie in shared memory
 // (rows loaded into registers where they are used: a training step's norm, forward
-// and backward, of 16384 x 4096 265 us, so 236).
+// and backward, of 16384 x 4096 265 us, so 236; with two CTAs an SM for rows up to
+// 8192, where three spilled registers, 219).
 template <int VPT, bool ALIGNED>
-__global__ void __launch_bounds__(256, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
   extern __shared__ __align__(128) uint8_t s_ring[];  // weights, then [stages][dy, h, dh][rows of an iteration][K]
   __shared__ float s_slots[2][8];
   __shared__ uint64_t s_full[kBwdMaxStages];
@@ -838,7 +847,7 @@ NormBwdGeom norm_bwd_geom(int64_t T, int64_t K, int num_sms) {
   NormBwdGeom g;
   g.vpt = K <= 2048 ? 1 : K <= 4096 ? 2 : K <= 8192 ? 4 : 8;
   g.team = team_size(K, g.vpt, 256);
-  const int64_t per = 256 / g.team, most = (int64_t)num_sms * (g.vpt <= 2 ? 3 : g.vpt <= 4 ? 2 : 1);
+  const int64_t per = 256 / g.team, most = (int64_t)num_sms * (g.vpt <= 1 ? 3 : g.vpt <= 4 ? 2 : 1);
   const int64_t ctas = cdiv(T, per * 8);  // eight rows a team at least: each writes a row of sums
   g.grid = ctas < most ? ctas : most;
   g.teams = g.grid * per;
@@ -856,7 +865,7 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& args, int num_sms, cudaStream
       constexpr int V = decltype(vpt)::value;
       constexpr bool A = decltype(aligned)::value;
       // the ring: what the CTAs that an SM holds leave each other (one stage of the largest rows)
-      constexpr int64_t most = 220 * 1024 / (V <= 2 ? 3 : V <= 4 ? 2 : 1) - 1024;
+      constexpr int64_t most = 220 * 1024 / (V <= 1 ? 3 : V <= 4 ? 2 : 1) - 1024;
       static std::once_flag once;
       static cudaError_t attr_err = cudaSuccess;
       std::call_once(once, [] {
