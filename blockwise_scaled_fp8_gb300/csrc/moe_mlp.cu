@@ -43,13 +43,15 @@
 //   warps 8-13     the activations' codes, experts ahead of the products: one to six
 //                  warps an expert, as many experts at once as there are buffers
 // Producers and issuers are whole warps that stay together, of which an elected lane
-// issues: a lane that leaves the others issues an MMA or a copy a third slower.
+// issues: a lane that left the others took 326 cycles for the four MMAs and two commits
+// of a stage, an elected one 252.
 //
 // Measured (with the router's launch; the floor is the reached experts' codes at the
-// copy rate): 64 experts of 3 x 2048 x 4096, 8 a token: one token 44.4 us (floor 30),
-// 4 tokens 111 (99), 16 tokens 212 (212); 128 of 3 x 704 x 1920, 6 a token, 5 tokens
-// 35.9 (16.5).  What is left at few tokens is fixed: the router and its launch 6 us,
-// the plan and the tokens' codes 3.5, the barrier and the first codes behind it 4.
+// rate of a plain copy): 64 experts of 3 x 2048 x 4096, 8 a token: one token 45 us
+// (floor 30), 4 tokens 111 (99), 16 tokens 212 (212); 128 of 3 x 704 x 1920, 6 a
+// token, 5 tokens 36 (16.5).  What is left at few tokens does not grow with the
+// weights: the router's launch, the plan, the tokens' codes and the exchange of the
+// activations.
 //
 // Waits are bounded; a role that gives up sets the abort flag, the others leave
 // their loops, and copies and MMAs in flight finish before the CTA exits.

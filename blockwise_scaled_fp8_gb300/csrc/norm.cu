@@ -16,11 +16,12 @@
 //
 // What bounds them is memory: each input once and each output once, but for the
 // codes along the columns, which need 128 rows of h after every row's rstd is known:
-// a second pass reads h again (10 bytes an element for 8).  Both in one pass (a
-// cluster of CTAs holding 128 rows in registers, its sums of squares joined through
-// distributed shared memory) took 185 us where the two passes take 124.  16384 x 4096
-// with residual: row codes 84 us (5.6 TB/s of 470 MB), the columns' pass 38 (5.3), the
-// gradient 100 (5.4) and 7 for the sum of its partial sums; a copy moves 6.2-6.7 TB/s.
+// a second pass reads h again (10 bytes an element for 8).  One launch instead (a
+// cluster of CTAs for 128 rows, which reads them again from L2 once its sums of
+// squares are joined) took 203 us for both codes of 16384 x 4096 with residual; the
+// two passes take 122: the rows' codes 83 (5.6 TB/s), the columns' 38 (5.3).  The
+// gradient takes 100 (5.4 TB/s) and the sum of its partial dw 7; a plain copy of
+// such sizes moves 6.2-6.7 TB/s.
 #include <mutex>
 #include <type_traits>
 

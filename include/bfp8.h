@@ -408,7 +408,8 @@ BFP8_API bfp8_status bfp8_gemm_routed_1x128_128x128(const void *qa, int64_t lda,
  *   ws  device, bfp8_moe_mlp_workspace_size(T, k, I) bytes, 16-byte aligned:
  *       one call's at a time
  * The second launch is a cooperative one: its CTAs, one a multiprocessor, wait
- * for one another once.  The wait is bounded (bfp8_check_device_errors).
+ * for one another once, or twice where the activations are many.  Every wait is
+ * bounded (bfp8_check_device_errors).
  */
 BFP8_API size_t bfp8_moe_mlp_workspace_size(int64_t T, int64_t k, int64_t I);
 BFP8_API bfp8_status bfp8_moe_mlp_decode(const void *x, int64_t T, int64_t K, int64_t ldx, const void *logits,
@@ -433,8 +434,8 @@ BFP8_API bfp8_status bfp8_moe_mlp_decode(const void *x, int64_t T, int64_t K, in
  *   device bf16 [T,K], may be x or residual themselves (with that one's row
  *   stride); weight device bf16 or fp32 (weight_f32 != 0) [K]; rstd device fp32
  *   [T], gets r; codes, scales, strides as bfp8_quant_dual's; y device bf16
- *   [T,K].  K <= 16384.  16-byte aligned rows (K and strides multiples of 8)
- *   take wide accesses, others go element by element.
+ *   [T,K].  K <= 16384.  Rows that are 16-byte aligned (K and strides multiples
+ *   of 8) are fastest; any others are allowed.
  */
 BFP8_API bfp8_status bfp8_rms_norm_quant(const void *x, int64_t T, int64_t K, int64_t ldx, const void *residual,
                                          int64_t ldr, const void *weight, int weight_f32, float eps, void *h,
