@@ -824,6 +824,25 @@ bfp8_status bfp8_moe_mlp_decode(const void* x, int64_t T, int64_t K, int64_t ldx
   return BFP8_OK;
 }
 
+}  // extern "C"
+
+namespace {
+// Whether rows of K bf16 that are written at `out` share elements with the rows at `in` without being those rows.
+bool rows_clash(const void* out, int64_t ldo, const void* in, int64_t ldi, int64_t T, int64_t K) {
+  if (!out || !in || T == 0 || K == 0) return false;
+  if (T == 1) ldo = ldi = K;
+  if (out == in) return ldo != ldi;
+  const uintptr_t o = (uintptr_t)out, i = (uintptr_t)in;
+  const uintptr_t apart = (o > i ? o - i : i - o) / 2, lower = (uintptr_t)((T - 1) * (o > i ? ldi : ldo) + K);
+  if (apart >= lower) return false;
+  if (ldo != ldi) return true;  // (interleaved with another stride: not looked at more closely)
+  const uintptr_t at = apart % (uintptr_t)ldo;
+  return at < (uintptr_t)K || (uintptr_t)ldo - at < (uintptr_t)K;
+}
+}  // namespace
+
+extern "C" {
+
 bfp8_status bfp8_rms_norm_quant(const void* x, int64_t T, int64_t K, int64_t ldx, const void* residual, int64_t ldr,
                                 const void* weight, int weight_f32, float eps, void* h, int64_t ldh, float* rstd,
                                 void* q_row, int64_t ldq_row, float* s_row, int64_t lds_row, void* q_col,
@@ -843,6 +862,11 @@ bfp8_status bfp8_rms_norm_quant(const void* x, int64_t T, int64_t K, int64_t ldx
             "%s: bf16 must be 2-byte, fp32 4-byte, codes 16-byte aligned", fn);
   CHECK_ARG(ldx >= K && (!residual || (ldr >= K && ldh >= K)) && (!y || ldy >= K), "%s: a row stride is below K=%lld", fn,
             (long long)K);
+  CHECK_ARG(!rows_clash(h, ldh, x, ldx, T, K) && !rows_clash(h, ldh, residual, ldr, T, K),
+            "%s: h may be x or residual, but not share memory with them otherwise", fn);
+  CHECK_ARG(!rows_clash(y, ldy, x, ldx, T, K) && !rows_clash(y, ldy, residual, ldr, T, K) && !rows_clash(y, ldy, h, ldh, T, K) &&
+                (!y || (y != x && y != residual && y != h)),
+            "%s: y must not share memory with x, residual or h", fn);
   if (q_row)
     CHECK_ARG(ldq_row >= K && ldq_row % 16 == 0 && lds_row >= T, "%s: ldq_row=%lld must be >= K=%lld and a multiple of 16, "
               "lds_row=%lld >= T=%lld", fn, (long long)ldq_row, (long long)K, (long long)lds_row, (long long)T);
@@ -880,6 +904,8 @@ bfp8_status bfp8_rms_norm_bwd(const void* dy, int64_t T, int64_t K, int64_t lddy
             "%s: bf16 must be 2-byte, fp32 4-byte, the workspace 16-byte aligned", fn);
   CHECK_ARG(T == 0 || (lddy >= K && ldh >= K && lddx >= K && (!dh || lddh >= K)), "%s: a row stride is below K=%lld", fn,
             (long long)K);
+  CHECK_ARG(!rows_clash(dx, lddx, dy, lddy, T, K) && !rows_clash(dx, lddx, h, ldh, T, K) && !rows_clash(dx, lddx, dh, lddh, T, K),
+            "%s: dx may be dy, h or dh, but not share memory with them otherwise", fn);
   int sms = 0;
   if ((st = check_device(&sms)) != BFP8_OK) return st;
   const size_t need = bfp8_rms_norm_bwd_workspace_size(T, K);

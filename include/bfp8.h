@@ -432,10 +432,11 @@ BFP8_API bfp8_status bfp8_moe_mlp_decode(const void *x, int64_t T, int64_t K, in
  * must fit fp32 (|h| up to about 1e18), and eps > 0.
  *   x, residual device bf16 [T,K] (residual and h both NULL or both given); h
  *   device bf16 [T,K], may be x or residual themselves (with that one's row
- *   stride); weight device bf16 or fp32 (weight_f32 != 0) [K]; rstd device fp32
- *   [T], gets r; codes, scales, strides as bfp8_quant_dual's; y device bf16
- *   [T,K].  K <= 16384.  Rows that are 16-byte aligned (K and strides multiples
- *   of 8) are fastest; any others are allowed.
+ *   stride), and no other memory of theirs; weight device bf16 or fp32
+ *   (weight_f32 != 0) [K]; rstd device fp32 [T], gets r; codes, scales, strides
+ *   as bfp8_quant_dual's; y device bf16 [T,K], no memory of x, residual or h.
+ *   K <= 16384.  Rows that are 16-byte aligned (K and strides multiples of 8)
+ *   are fastest; any others are allowed.
  */
 BFP8_API bfp8_status bfp8_rms_norm_quant(const void *x, int64_t T, int64_t K, int64_t ldx, const void *residual,
                                          int64_t ldr, const void *weight, int weight_f32, float eps, void *h,
@@ -449,7 +450,7 @@ BFP8_API bfp8_status bfp8_rms_norm_quant(const void *x, int64_t T, int64_t K, in
  *   dx = r (g - n mean over k of g n) + dh      (bf16, the gradient of x and of the residual alike)
  *   dweight[k] = sum over t of dy n             (fp32)
  * dh (bf16 [T,K] or NULL) is the gradient that reaches h by the stream itself.
- * dx may be dy, dh or h.  T == 0 gives dweight 0.  ws: at least
+ * dx may be dy, dh or h, and no other memory of theirs.  T == 0 gives dweight 0.  ws: at least
  * bfp8_rms_norm_bwd_workspace_size(T, K) bytes of the device that is current
  * in both calls, 16-byte aligned.  The same inputs give the same bits.
  */

@@ -124,6 +124,19 @@ def test_sum_in_place(K, which):
     assert torch.equal(o.q_row[:, :K], ref.q_row[:, :K]) and torch.equal(o.q_col[:, :400], ref.q_col[:, :400])
 
 
+def test_halves_of_one_buffer():
+    """x and the sum as the left and right columns of the same rows: no element is shared."""
+    x, r, w = make(300, 520, 3, True)
+    ref = B.rms_norm_quant(x, w, residual=r, cols=True)
+    buf = torch.empty(300, 1040, device="cuda", dtype=bf16)
+    buf[:, :520] = x
+    o = B.rms_norm_quant(buf[:, :520], w, residual=r, cols=True, h=buf[:, 520:])
+    assert torch.equal(buf[:, :520], x) and torch.equal(buf[:, 520:], ref.h)
+    assert torch.equal(o.q_row[:, :520], ref.q_row[:, :520]) and torch.equal(o.q_col[:, :300], ref.q_col[:, :300])
+    with pytest.raises(B.Bfp8Error):
+        B.rms_norm_quant(buf[:, :520], w, residual=r, h=buf[:, 519:1039])
+
+
 def test_zeros_and_extremes():
     """Rows and columns of zeros have finite scales and zero codes; weights of 0 and below 0; rows of one large value."""
     x = torch.zeros(256, 384, device="cuda", dtype=bf16)

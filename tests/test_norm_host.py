@@ -13,6 +13,7 @@ from blockwise_scaled_fp8_gb300 import buildlib as bbuild
 
 NULL = ctypes.c_void_p(None)
 P = ctypes.c_void_p(0x10000)      # fake, aligned; never dereferenced
+Y = ctypes.c_void_p(0x20000)
 ODD = ctypes.c_void_p(0x10001)
 BAD = 1                           # BFP8_ERR_INVALID_ARG
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +35,7 @@ def _caller(fn, ok):
 
 def test_rms_norm_argument_validation():
     call = _caller("bfp8_rms_norm_quant", dict(x=P, T=4, K=256, ldx=256, r=P, ldr=256, w=P, f32=0, eps=1e-6, h=P, ldh=256,
-                                               rstd=P, q=P, ldq=256, s=P, lds=4, qc=P, ldqc=16, sc=P, ldsc=256, y=P, ldy=256,
+                                               rstd=P, q=P, ldq=256, s=P, lds=4, qc=P, ldqc=16, sc=P, ldsc=256, y=Y, ldy=256,
                                                st=NULL))
     for bad in (dict(T=-1), dict(K=-1), dict(K=16385, ldx=16385), dict(T=1 << 31), dict(eps=0.0), dict(eps=-1.0),
                 dict(eps=float("inf")), dict(eps=float("nan")), dict(r=NULL), dict(h=NULL), dict(s=NULL), dict(q=NULL),
@@ -45,6 +46,24 @@ def test_rms_norm_argument_validation():
         assert call(**bad) == BAD, bad
     assert call(T=0, x=NULL) == B.BFP8_OK
     assert call(K=0) == B.BFP8_OK
+
+
+def test_rows_that_share_memory_are_refused():
+    """An output may be an input's rows themselves and otherwise none of its elements."""
+    at = lambda element: ctypes.c_void_p(0x100000 + 2 * element)  # noqa: E731
+    call = _caller("bfp8_rms_norm_quant", dict(x=at(0), T=4, K=256, ldx=512, r=P, ldr=256, w=P, f32=0, eps=1e-6, h=at(0),
+                                               ldh=512, rstd=P, q=NULL, ldq=0, s=NULL, lds=0, qc=NULL, ldqc=0, sc=NULL, ldsc=0,
+                                               y=NULL, ldy=256, st=NULL))
+    for bad in (dict(ldh=520), dict(h=at(512)), dict(h=at(8)), dict(h=at(255)), dict(h=at(264)), dict(h=at(3 * 512 + 255)),
+                dict(x=at(512)), dict(x=at(1791)), dict(h=at(256), ldh=256), dict(T=1, h=at(255)), dict(y=at(0), ldy=512),
+                dict(y=at(1)), dict(y=P), dict(r=at(512), ldr=512), dict(h=P, ldh=264)):
+        assert call(**bad) == BAD, bad
+        assert b"share memory" in B.lib().bfp8_last_error(), bad
+    call = _caller("bfp8_rms_norm_bwd", dict(dy=at(0), T=4, K=256, lddy=512, h=P, ldh=256, w=P, f32=1, rstd=P, dh=NULL, lddh=0,
+                                             dx=at(0), lddx=512, dw=Y, ws=P, n=1 << 30, st=NULL))
+    for bad in (dict(lddx=520), dict(dx=at(512)), dict(dx=at(1)), dict(dx=P, lddx=264), dict(dh=at(255), lddh=512, dy=Y)):
+        assert call(**bad) == BAD, bad
+        assert b"share memory" in B.lib().bfp8_last_error(), bad
 
 
 def test_rms_norm_bwd_argument_validation():
