@@ -311,6 +311,22 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "r"(bytes), "r"(bar)
                : "memory");
 }
+// Until the slot was asked to take its `turn`-th row: then that row's phase of its barrier is the running one or the last
+// (a team ahead of the others could ask for a row whose slot still waits for the one before, and the parity of an older
+// phase would answer).
+__device__ __forceinline__ bool wait_asked(const volatile int* asked, int turn, const volatile int* abort) {
+  if (*asked > turn) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (*asked <= turn)
+    if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  return true;
+}
+// Behind a CTA's last barrier, where a wait gave up: copies that were asked for land before its shared memory goes away.
+__device__ __forceinline__ void drain(uint32_t full, const int* asked, int slots) {
+  const int never = 0;
+  for (int i = 0; i < slots; ++i)
+    if (asked[i] > 0) mbar_wait_bounded(full + 8 * i, (uint32_t)(asked[i] - 1) & 1u, kWaitLimitNs, &never);
+}
 
 // The sum of v over a team's threads, the same bits in each of them.  `slots`: one of
 // two sets of a float a warp, used in turn, so that one barrier a sum is enough.
@@ -402,7 +418,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
   extern __shared__ __align__(128) uint8_t s_ring[];  // weights, then the slots: [x, residual][K]
   __shared__ uint64_t s_full[kNormMaxSlots];
   __shared__ float s_sum[kNormWarps];
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_asked[kNormMaxSlots];  // rows that a slot was asked to take
   const int K = (int)a.K, tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31, slots = a.slots;
   const int size = a.team, teams = min(slots, kNormWarps / size), team = warp / size, sub = warp % size;
   const uint32_t space = row_space(K, ALIGNED), slot_bytes = space * (a.residual ? 2u : 1u);
@@ -412,7 +428,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
   pdl_launch_dependents();
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < slots; ++i) mbar_init(full + 8 * i, 1);
+    for (int i = 0; i < slots; ++i) mbar_init(full + 8 * i, 1), s_asked[i] = 0;
     fence_barrier_init();
     fence_proxy_async_shared();
   }
@@ -424,6 +440,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
     const uint16_t *x = a.x + t * a.ldx, *r = a.residual ? a.residual + t * a.ldr : nullptr;
     const uint32_t x_bytes = row_copied<ALIGNED>(x, K), r_bytes = r ? row_copied<ALIGNED>(r, K) : 0u;
     mbar_arrive_expect_tx(full + 8 * slot, x_bytes + r_bytes);
+    *(volatile int*)(s_asked + slot) = s_asked[slot] + 1;
     bulk_load(to, x - row_off<ALIGNED>(x) / 2, x_bytes, full + 8 * slot);
     if (r) bulk_load(to + space, r - row_off<ALIGNED>(r) / 2, r_bytes, full + 8 * slot);
   };
@@ -431,18 +448,17 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
     for (int i = 0; i < slots && i < rows; ++i) issue(i, i);
   stage_weights(a.weight, a.weight_f32, K, weights);
   __syncthreads();
-  if (team >= teams) return;
   auto team_sync = [&]() {
     if (size > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * size) : "memory");
     else __syncwarp();
   };
-  int slot = team;  // teams <= slots
-  uint32_t parity = 0;
-  for (int64_t i = team; i < rows; i += teams) {
+  int slot = team, turn = 0;  // teams <= slots
+  for (int64_t i = team < teams ? team : rows; i < rows; i += teams) {
     const int64_t t = blockIdx.x + i * gridDim.x;
     const uint32_t from = ring + (uint32_t)slot * slot_bytes;
     // (a wait that gives up leaves the error word set and wrong rows from there on, without further waits or copies)
-    if (!mbar_wait_bounded(full + 8 * slot, parity, kWaitLimitNs, abort_flag)) {
+    if (!wait_asked(s_asked + slot, turn, abort_flag) ||
+        !mbar_wait_bounded(full + 8 * slot, (uint32_t)turn & 1u, kWaitLimitNs, abort_flag)) {
       atomicOr(&g_norm_error, 1u);
       *abort_flag = 1;
     }
@@ -513,8 +529,10 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
     team_sync();
     if (sub == 0 && lane == 0 && i + slots < rows && !*abort_flag) issue(i + slots, slot);
     slot += teams;
-    if (slot >= slots) slot -= slots, parity ^= 1u;
+    if (slot >= slots) slot -= slots, ++turn;
   }
+  __syncthreads();
+  if (tid == 0 && *abort_flag) drain(full, s_asked, slots);
 }
 
 // Codes along the columns, from h and rstd: a CTA a 128 x 128 tile, a thread eight
@@ -624,7 +642,7 @@ __global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
   extern __shared__ __align__(128) uint8_t s_ring[];  // weights, then [stages][dy, h, dh][rows of an iteration][K]
   __shared__ float s_slots[2][8];
   __shared__ uint64_t s_full[kBwdMaxStages];
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_asked[kBwdMaxStages];  // iterations that a stage was asked to take
   const Team team = team_of(a.team);
   const int K = (int)a.K, lane = team.lane, tid = (int)threadIdx.x, stages = a.stages;
   const uint32_t weights = smem_u32(s_ring), ring = weights + staged_bytes(K, a.weight_f32), full = smem_u32(s_full);
@@ -634,7 +652,7 @@ __global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
   pdl_launch_dependents();
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < stages; ++i) mbar_init(full + 8 * i, 1);
+    for (int i = 0; i < stages; ++i) mbar_init(full + 8 * i, 1), s_asked[i] = 0;
     fence_barrier_init();
     fence_proxy_async_shared();
   }
@@ -647,7 +665,10 @@ __global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
     const uint32_t nd = in ? row_copied<ALIGNED>(d, K) : 0u, nh = in ? row_copied<ALIGNED>(h, K) : 0u,
                    ne = in && e ? row_copied<ALIGNED>(e, K) : 0u;
     const uint32_t bytes = __reduce_add_sync(kAll, nd + nh + ne);
-    if (tid == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
+    if (tid == 0) {
+      ++s_asked[st];
+      mbar_arrive_expect_tx(full + 8 * st, bytes);
+    }
     __syncwarp();
     if (in) {
       const uint32_t to = ring + (uint32_t)st * parts * part_bytes + (uint32_t)tid * space;
@@ -725,6 +746,7 @@ __global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
       }
     }
   }
+  if (tid == 0 && *abort_flag) drain(full, s_asked, stages);  // (all of its own asking)
   float* out = a.partial + me * K;
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {

@@ -137,6 +137,22 @@ def test_halves_of_one_buffer():
         B.rms_norm_quant(buf[:, :520], w, residual=r, h=buf[:, 519:1039])
 
 
+@pytest.mark.parametrize("T,K,residual", [(8192, 4096, False), (8192, 4096, True), (6000, 5120, True), (4000, 2001, True),
+                                          (4000, 16384, True)])
+def test_many_runs_of_many_rows(T, K, residual):
+    """Rows that take the places of rows before them, with another number of places than of rows at once."""
+    x, r, w = make(T, K, 5, residual)
+    first = B.rms_norm_quant(x, w, residual=r)
+    dx, dw = B.rms_norm_bwd(x, first.h, w, first.rstd)
+    for _ in range(20):
+        o = B.rms_norm_quant(x, w, residual=r)
+        assert torch.equal(o.h, first.h) and torch.equal(o.rstd, first.rstd)
+        assert torch.equal(o.q_row[:, :K], first.q_row[:, :K]) and torch.equal(o.s_row[:, :T], first.s_row[:, :T])
+        dx2, dw2 = B.rms_norm_bwd(x, first.h, w, first.rstd)
+        assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+    B.check_device_errors()
+
+
 def test_zeros_and_extremes():
     """Rows and columns of zeros have finite scales and zero codes; weights of 0 and below 0; rows of one large value."""
     x = torch.zeros(256, 384, device="cuda", dtype=bf16)
