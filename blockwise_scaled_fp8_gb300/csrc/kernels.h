@@ -325,7 +325,7 @@ struct NormBwdArgs {
   int team, stages;  // set by the launcher
 };
 struct NormBwdGeom {
-  int vpt, team;
+  int threads, vpt, team;
   int64_t grid, teams;  // teams: rows of partial sums
 };
 NormBwdGeom norm_bwd_geom(int64_t T, int64_t K, int num_sms);

@@ -116,6 +116,53 @@ __device__ __forceinline__ void store_row8(uint16_t* row, int k, int K, const ui
   for (int i = 0; i < 7; ++i)
     if (k + i < K) to[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
 }
+// A warp's eight elements a lane of N chunks of 256 side by side, chunk u's from feature k0 + 256 u on, to a row.  Where
+// the row is not aligned, a lane writes the 16-byte block that its elements share with the lane's before it (a
+// write of 4 bytes in each 16 of a row passes L2 four times), and only the run's two ends go element by element.
+template <bool VEC, int N>
+__device__ __forceinline__ void store_run(uint16_t* row, int k0, int K, const uint4 (&v)[N]) {
+  const int lane = (int)threadIdx.x & 31;
+  const int off = VEC ? 0 : (int)(reinterpret_cast<uintptr_t>(row + k0) & 15), head = off >> 1;  // (the same for a warp)
+  if (off == 0) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int k = k0 + kVec * (32 * u + lane);
+      if (VEC || k + kVec <= K) store_row8<true>(row, k, K, v[u]);
+      else store_row8<false>(row, k, K, v[u]);
+    }
+    return;
+  }
+  uint4 carry = make_uint4(0, 0, 0, 0);  // lane 0's: the last lane's elements of the chunk before
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int k = k0 + kVec * (32 * u + lane), from = (lane + 31) & 31;
+    uint4 p;
+    p.x = __shfl_sync(kAll, v[u].x, from);
+    p.y = __shfl_sync(kAll, v[u].y, from);
+    p.z = __shfl_sync(kAll, v[u].z, from);
+    p.w = __shfl_sync(kAll, v[u].w, from);
+    const uint4 before = lane == 0 ? carry : p;
+    carry = p;
+    // elements k - head .. k - head + 7, of which the run's first block holds 8 - head only
+    const uint4 block = shifted8(before, v[u], 16 - off, kVec);
+    const int first = u == 0 && lane == 0 ? k : k - head, last = min(k - head + kVec, K);
+    if (first == k - head && last == k - head + kVec) {
+      *reinterpret_cast<uint4*>(row + k - head) = block;
+    } else {
+      const uint32_t w[4] = {block.x, block.y, block.z, block.w};
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (k - head + i >= first && k - head + i < last) row[k - head + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+  if (lane == 0) {  // the last lane's last elements
+    const int k = k0 + 256 * N - head;
+    const uint32_t w[4] = {carry.x, carry.y, carry.z, carry.w};
+#pragma unroll
+    for (int i = 1; i < kVec; ++i)
+      if (i >= kVec - head && k + i - (kVec - head) < K) row[k + i - (kVec - head)] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
 // Keeps the compiler from carrying what it derived from the values (their fp32 forms, twice the registers) past here.
 template <int N>
 __device__ __forceinline__ void only_packed(uint4 (&v)[N]) {
@@ -409,8 +456,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ?
 // arrive by bulk copies in slots that hold all of shared memory, whatever the
 // threads are waiting for; row i of a CTA is slot i % slots and team i % teams, and
 // the team that is done with a row asks for the one that takes its slot.  A row is
-// read twice from its slot (the sum of the residual goes back into it where the row is
-// aligned, and is formed again where it is not): once for its
+// read twice from its slot, where it is kept (with the residual, and aligned): once for its
 // squares, once for its codes, four chunks of 256 features at a time, whose eight
 // groups' maxima a halving exchange leaves in a lane each.
 template <bool ALIGNED>
@@ -464,18 +510,43 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
     }
     uint64_t sum2 = 0;
     const int off_x = row_off<ALIGNED>(a.x + t * a.ldx), off_r = a.residual ? row_off<ALIGNED>(a.residual + t * a.ldr) : 0;
+    auto keep = [&](int k, const uint4& h) {
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(from + 2u * (uint32_t)k), "r"(h.x), "r"(h.y), "r"(h.z),
+                   "r"(h.w)
+                   : "memory");
+    };
+    if constexpr (ALIGNED) {
 #pragma unroll 4
-    for (int k = kVec * (32 * sub + lane); k < K; k += 32 * kVec * size) {
-      uint4 h = lds_row8<ALIGNED>(from, off_x, k, K);
-      if (a.residual) {
-        h = add8(h, lds_row8<ALIGNED>(from + space, off_r, k, K));
-        store_row8<ALIGNED>(a.h + t * a.ldh, k, K, h);
-        if (ALIGNED)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(from + 2u * (uint32_t)k), "r"(h.x), "r"(h.y), "r"(h.z),
-                       "r"(h.w)
-                       : "memory");
+      for (int k = kVec * (32 * sub + lane); k < K; k += 32 * kVec * size) {
+        uint4 h = lds_v4(from + 2u * (uint32_t)k);
+        if (a.residual) {
+          h = add8(h, lds_v4(from + space + 2u * (uint32_t)k));
+          *reinterpret_cast<uint4*>(a.h + t * a.ldh + k) = h;
+          keep(k, h);
+        }
+        sum2 = squares8(h, sum2);
       }
-      sum2 = squares8(h, sum2);
+    } else {
+      // 1024 features a warp and step; a step's blocks, which reach into the next step's first one, are read by the whole
+      // team before they are written
+      for (int k00 = 0; k00 < K; k00 += 4 * 32 * kVec * size) {
+        const int k0 = k00 + 4 * 32 * kVec * sub;
+        uint4 h[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int k = k0 + kVec * (32 * u + lane);
+          h[u] = lds_row8<false>(from, off_x, k, K);
+          if (a.residual) h[u] = add8(h[u], lds_row8<false>(from + space, off_r, k, K));
+          sum2 = squares8(h[u], sum2);
+        }
+        if (a.residual && k0 < K) store_run<false>(a.h + t * a.ldh, k0, K, h);
+        team_sync();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int k = k0 + kVec * (32 * u + lane);
+          if (k < K) keep(k, h[u]);
+        }
+      }
     }
     float sum = f2_sum(sum2);
 #pragma unroll
@@ -497,14 +568,14 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
           const int k = k0 + kVec * (32 * u + lane);
           uint64_t w[4];
           staged_weight8(weights, a.weight_f32, k, K, w);
-          uint4 h = lds_row8<ALIGNED>(from, off_x, k, K);
-          if (!ALIGNED && a.residual) h = add8(h, lds_row8<ALIGNED>(from + space, off_r, k, K));
-          times8(h, w, v[u]);
+          times8(lds_row8<true>(from, 0, k, K), w, v[u]);
           am[u] = amax8(v[u]);
         }
         if (a.y) {
+          uint4 y[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) store_row8<ALIGNED>(a.y + t * a.ldy, k0 + kVec * (32 * u + lane), K, scaled_bf16(v[u], r));
+          for (int u = 0; u < 4; ++u) y[u] = scaled_bf16(v[u], r);
+          store_run<ALIGNED>(a.y + t * a.ldy, k0, K, y);
         }
         if (a.q_row) {
           // lane l: chunk u = (l & 8 ? 2 : 0) + (l & 4 ? 1 : 0), group l / 16 of it
@@ -637,10 +708,12 @@ __global__ void __launch_bounds__(256, 4) rms_norm_cols_kernel(const NormArgs a)
 // (rows loaded into registers where they are used: a training step's norm, forward
 // and backward, of 16384 x 4096 265 us, so 236; with two CTAs an SM for rows up to
 // 8192, where three spilled registers, 219).
-template <int VPT, bool ALIGNED>
-__global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdArgs a) {
+constexpr int bwd_ctas(int threads, int vpt) { return threads > 256 ? 1 : vpt <= 1 ? 3 : 2; }  // that an SM holds
+template <int THREADS, int VPT, bool ALIGNED>
+__global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS, VPT)) rms_norm_bwd_kernel(const NormBwdArgs a) {
+  constexpr bool kKeep = VPT <= 2;  // a thread's weights stay in registers
   extern __shared__ __align__(128) uint8_t s_ring[];  // weights, then [stages][dy, h, dh][rows of an iteration][K]
-  __shared__ float s_slots[2][8];
+  __shared__ float s_slots[2][THREADS / 32];
   __shared__ uint64_t s_full[kBwdMaxStages];
   __shared__ int s_abort, s_asked[kBwdMaxStages];  // iterations that a stage was asked to take
   const Team team = team_of(a.team);
@@ -682,6 +755,19 @@ __global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
       if ((int64_t)blockIdx.x + (int64_t)i * gridDim.x < iterations) issue((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
   stage_weights(a.weight, a.weight_f32, K, weights);
   __syncthreads();
+  uint64_t kept[kKeep ? VPT : 1][4];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) staged_weight8(weights, a.weight_f32, kVec * (u * team.size + lane), K, kept[u]);
+  }
+  auto weights8 = [&](int u, uint64_t (&w)[4]) {
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = kept[u][i];
+    } else {
+      staged_weight8(weights, a.weight_f32, kVec * (u * team.size + lane), K, w);
+    }
+  };
   float dw[VPT][8] = {};
   int turn = 0, st = 0;
   uint32_t parity = 0;
@@ -712,7 +798,7 @@ __global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
       uint64_t n[4], d[4], w[4];
       row_times(hv[u], r, n);
       pairs8(dv[u], d);
-      staged_weight8(weights, a.weight_f32, kVec * (u * team.size + lane), K, w);
+      weights8(u, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f2_unpack(f2_fma(d[i], n[i], f2_pack(dw[u][2 * i], dw[u][2 * i + 1])), dw[u][2 * i], dw[u][2 * i + 1]);
@@ -734,7 +820,7 @@ __global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
         row_times(hv[u], r, n);
         pairs8(dv[u], d);
         pairs8(rv[u], e);
-        staged_weight8(weights, a.weight_f32, k, K, w);
+        weights8(u, w);
         uint32_t out[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -742,6 +828,8 @@ __global__ void __launch_bounds__(256, VPT <= 1 ? 3 : VPT <= 4 ? 2 : 1) rms_norm
           f2_unpack(f2_add(f2_fma(c2, n[i], f2_mul(r2, f2_mul(d[i], w[i]))), e[i]), lo, hi);
           out[i] = pack_bf16x2(lo, hi);
         }
+        // (element by element where it is not aligned: store_run's two ends cost a chunk of 256 more than its blocks save,
+        // 36.7 us for 33.0 at 5003 x 2001)
         store_row8<ALIGNED>(a.dx + t * a.lddx, k, K, make_uint4(out[0], out[1], out[2], out[3]));
       }
     }
@@ -772,12 +860,13 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* partial,
     sum = to;
   };
   if (k < K) {
-    for (int64_t i = warp; i < teams; i += 8 * 32) {  // (eight loads in flight)
-      float v[8];
+    constexpr int kLoads = 15;  // in flight: all of three CTAs an SM on 152
+    for (int64_t i = warp; i < teams; i += kLoads * 32) {
+      float v[kLoads];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = i + 32 * j < teams ? partial[(i + 32 * j) * K + k] : 0.0f;
+      for (int j = 0; j < kLoads; ++j) v[j] = i + 32 * j < teams ? partial[(i + 32 * j) * K + k] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) add(v[j]);
+      for (int j = 0; j < kLoads; ++j) add(v[j]);
     }
   }
   s[warp][lane] = sum + lost;
@@ -823,8 +912,11 @@ static cudaError_t run_norm_ring(NormArgs a, int num_sms, cudaStream_t st) {
   if (attr_err != cudaSuccess) return attr_err;
   const int64_t weights = staged_bytes((int)a.K, a.weight_f32), slot = (int64_t)row_space((int)a.K, ALIGNED) * (a.residual ? 2 : 1);
   const int64_t fit = (most - weights) / slot;  // (two of the largest rows)
-  a.team = a.K <= 4096 ? 1 : a.K <= 8192 ? 2 : 4;
   a.slots = (int)(fit < kNormMaxSlots ? fit : kNormMaxSlots);
+  // A warp a row where that keeps every warp busy, else four, or two where rows are short of that by little (16384 x 4096
+  // with residual, 12 slots: one warp 83.1 us, two 86.3, four 81.3; 4096 x 8192, 5 slots: two 56.7, four 46.4; without
+  // residual, 11: two 30.7, four 32.3).
+  a.team = a.slots >= kNormWarps ? 1 : a.slots >= kNormWarps / 2 && !a.residual ? 2 : 4;
   return launch_pdl(rms_norm_ring_kernel<ALIGNED>, (unsigned)(a.T < num_sms ? a.T : num_sms), 32 * kNormWarps,
                     (size_t)(weights + a.slots * slot), st, a);
 }
@@ -868,9 +960,10 @@ cudaError_t norm_read_errors(uint32_t* out) {
 
 NormBwdGeom norm_bwd_geom(int64_t T, int64_t K, int num_sms) {
   NormBwdGeom g;
-  g.vpt = K <= 2048 ? 1 : K <= 4096 ? 2 : K <= 8192 ? 4 : 8;
-  g.team = team_size(K, g.vpt, 256);
-  const int64_t per = 256 / g.team, most = (int64_t)num_sms * (g.vpt <= 1 ? 3 : g.vpt <= 4 ? 2 : 1);
+  g.threads = K <= 4096 ? 256 : 512;
+  g.vpt = K <= 2048 ? 1 : K <= 8192 ? 2 : 4;
+  g.team = team_size(K, g.vpt, g.threads);
+  const int64_t per = g.threads / g.team, most = (int64_t)num_sms * bwd_ctas(g.threads, g.vpt);
   const int64_t ctas = cdiv(T, per * 8);  // eight rows a team at least: each writes a row of sums
   g.grid = ctas < most ? ctas : most;
   g.teams = g.grid * per;
@@ -884,27 +977,31 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& args, int num_sms, cudaStream
   if (a.T > 0) {
     const bool vec = a.K % 8 == 0 && vec_ok(a.dy, a.lddy) && vec_ok(a.h, a.ldh) && vec_ok(a.dh, a.lddh) &&
                      vec_ok(a.dx, a.lddx) && vec_ok(a.weight, 0);
-    auto run = [&](auto vpt, auto aligned) {
-      constexpr int V = decltype(vpt)::value;
+    auto run = [&](auto threads, auto vpt, auto aligned) {
+      constexpr int N = decltype(threads)::value, V = decltype(vpt)::value;
       constexpr bool A = decltype(aligned)::value;
       // the ring: what the CTAs that an SM holds leave each other (one stage of the largest rows)
-      constexpr int64_t most = 220 * 1024 / (V <= 1 ? 3 : V <= 4 ? 2 : 1) - 1024;
+      constexpr int64_t most = 220 * 1024 / bwd_ctas(N, V) - 1024;
       static std::once_flag once;
       static cudaError_t attr_err = cudaSuccess;
       std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(rms_norm_bwd_kernel<V, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        attr_err = cudaFuncSetAttribute(rms_norm_bwd_kernel<N, V, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
       });
       if (attr_err != cudaSuccess) return attr_err;
       const int64_t weights = staged_bytes((int)a.K, a.weight_f32);
-      const int64_t stage = 256 / g.team * (int64_t)row_space((int)a.K, A) * (a.dh ? 3 : 2), fit = (most - weights) / stage;
+      const int64_t stage = N / g.team * (int64_t)row_space((int)a.K, A) * (a.dh ? 3 : 2), fit = (most - weights) / stage;
       a.stages = (int)(fit < kBwdMaxStages ? fit : kBwdMaxStages);
-      return launch_pdl(rms_norm_bwd_kernel<V, A>, (unsigned)g.grid, 256, (size_t)(weights + a.stages * stage), st, a);
+      return launch_pdl(rms_norm_bwd_kernel<N, V, A>, (unsigned)g.grid, N, (size_t)(weights + a.stages * stage), st, a);
     };
-    auto go = [&](auto vpt) { return vec ? run(vpt, std::true_type{}) : run(vpt, std::false_type{}); };
-    const cudaError_t e = g.vpt == 1   ? go(std::integral_constant<int, 1>{})
-                          : g.vpt == 2 ? go(std::integral_constant<int, 2>{})
-                          : g.vpt == 4 ? go(std::integral_constant<int, 4>{})
-                                       : go(std::integral_constant<int, 8>{});
+    auto go = [&](auto threads, auto vpt) {
+      return vec ? run(threads, vpt, std::true_type{}) : run(threads, vpt, std::false_type{});
+    };
+    constexpr std::integral_constant<int, 256> n256;
+    constexpr std::integral_constant<int, 512> n512;
+    const cudaError_t e = g.vpt == 1   ? go(n256, std::integral_constant<int, 1>{})
+                          : g.vpt == 4 ? go(n512, std::integral_constant<int, 4>{})
+                          : g.threads == 256 ? go(n256, std::integral_constant<int, 2>{})
+                                       : go(n512, std::integral_constant<int, 2>{});
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(rms_norm_dw_kernel, (unsigned)cdiv(a.K, 32), 1024, 0, st, (const float*)a.partial, g.teams, (int)a.K, a.dweight);
