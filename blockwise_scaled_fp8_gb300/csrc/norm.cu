@@ -273,13 +273,14 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   return cvt_e4m3x2(a, b) | cvt_e4m3x2(c, d) << 16;
 }
 // The codes of v m at feature k of a row of codes.
+template <bool WHOLE = false>
 __device__ __forceinline__ void store_codes8(uint8_t* row, int k, int K, const uint64_t (&v)[4], float m) {
-  if (k >= K) return;
+  if (!WHOLE && k >= K) return;
   float f[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) f2_unpack(f2_mul(v[i], f2_pack(m, m)), f[2 * i], f[2 * i + 1]);
   const uint32_t lo = codes4(f[0], f[1], f[2], f[3]), hi = codes4(f[4], f[5], f[6], f[7]);
-  if (k + kVec <= K) {
+  if (WHOLE || k + kVec <= K) {
     *reinterpret_cast<uint2*>(row + k) = make_uint2(lo, hi);
   } else {
 #pragma unroll
@@ -298,40 +299,23 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
 __device__ __forceinline__ void lds_2x64(uint32_t addr, uint64_t& a, uint64_t& b) {
   asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
 }
-// The weights, kept in shared memory as they come (zeros up to a whole chunk), and eight of them from feature k on (zeros
-// past the end).
-__host__ __device__ __forceinline__ uint32_t staged_bytes(int K, int f32) {
-  return ((uint32_t)(K + kVec - 1) / kVec * kVec * (f32 ? 4u : 2u) + 127u) / 128u * 128u;
-}
+// The weights in shared memory, in fp32 (zeros up to a whole chunk), and eight of them from feature k on, k below that.
+__host__ __device__ __forceinline__ uint32_t staged_bytes(int K) { return ((uint32_t)K * 4u + 127u) / 128u * 128u; }
 __device__ __forceinline__ void stage_weights(const void* w, int f32, int K, uint32_t to) {
   const int padded = (K + kVec - 1) / kVec * kVec;
-  if (K == padded && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
-    for (uint32_t i = 16u * threadIdx.x; i < (uint32_t)K * (f32 ? 4u : 2u); i += 16u * blockDim.x) {
+  if (f32 && K == padded && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {
+    for (uint32_t i = 16u * threadIdx.x; i < (uint32_t)K * 4u; i += 16u * blockDim.x) {
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(w) + i));
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + i), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
     }
   } else {
-    for (int i = (int)threadIdx.x; i < padded; i += (int)blockDim.x) {
-      if (f32) {
-        const float v = i < K ? __ldg(static_cast<const float*>(w) + i) : 0.0f;
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + 4u * (uint32_t)i), "f"(v) : "memory");
-      } else {
-        const uint16_t v = i < K ? __ldg(static_cast<const uint16_t*>(w) + i) : (uint16_t)0;
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 2u * (uint32_t)i), "h"(v) : "memory");
-      }
-    }
+    for (int i = (int)threadIdx.x; i < padded; i += (int)blockDim.x)
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + 4u * (uint32_t)i), "f"(i < K ? weight_at(w, f32, i) : 0.0f) : "memory");
   }
 }
-__device__ __forceinline__ void staged_weight8(uint32_t from, int f32, int k, int K, uint64_t (&w)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = 0;
-  if (k >= K) return;
-  if (f32) {
-    lds_2x64(from + 4u * (uint32_t)k, w[0], w[1]);
-    lds_2x64(from + 4u * (uint32_t)k + 16u, w[2], w[3]);
-  } else {
-    pairs8(lds_v4(from + 2u * (uint32_t)k), w);
-  }
+__device__ __forceinline__ void staged_weight8(uint32_t from, int k, uint64_t (&w)[4]) {
+  lds_2x64(from + 4u * (uint32_t)k, w[0], w[1]);
+  lds_2x64(from + 4u * (uint32_t)k + 16u, w[2], w[3]);
 }
 // A row in shared memory as bulk copies bring it: the 16-byte blocks that hold it, its first element `off` bytes into them
 // (0 where it is aligned).  Each block holds a byte of the row, so no copy leaves the tensor's own 16-byte blocks.
@@ -468,7 +452,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
   const int K = (int)a.K, tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31, slots = a.slots;
   const int size = a.team, teams = min(slots, kNormWarps / size), team = warp / size, sub = warp % size;
   const uint32_t space = row_space(K, ALIGNED), slot_bytes = space * (a.residual ? 2u : 1u);
-  const uint32_t weights = smem_u32(s_ring), ring = weights + staged_bytes(K, a.weight_f32), full = smem_u32(s_full);
+  const uint32_t weights = smem_u32(s_ring), ring = weights + staged_bytes(K), full = smem_u32(s_full);
   const int64_t rows = a.T > blockIdx.x ? cdiv(a.T - blockIdx.x, (int64_t)gridDim.x) : 0;  // of this CTA: every grid-th
   volatile int* abort_flag = &s_abort;
   pdl_launch_dependents();
@@ -516,8 +500,8 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
                    : "memory");
     };
     if constexpr (ALIGNED) {
-#pragma unroll 4
-      for (int k = kVec * (32 * sub + lane); k < K; k += 32 * kVec * size) {
+      const int step = 32 * kVec * size;
+      auto take = [&](int k) {
         uint4 h = lds_v4(from + 2u * (uint32_t)k);
         if (a.residual) {
           h = add8(h, lds_v4(from + space + 2u * (uint32_t)k));
@@ -525,7 +509,13 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
           keep(k, h);
         }
         sum2 = squares8(h, sum2);
+      };
+      int k = kVec * (32 * sub + lane);
+      for (; k + 3 * step < K; k += 4 * step) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) take(k + u * step);
       }
+      for (; k < K; k += step) take(k);
     } else {
       // 1024 features a warp and step; a step's blocks, which reach into the next step's first one, are read by the whole
       // team before they are written
@@ -559,41 +549,53 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
     }
     const float r = rstd_of(sum, K, a.eps);
     if (sub == 0 && lane == 0) a.rstd[t] = r;
-    if (a.q_row || a.y) {
-      for (int k0 = 4 * 32 * kVec * sub; k0 < K; k0 += 4 * 32 * kVec * size) {
-        uint64_t v[4][4];
-        float am[4];
+    // Codes of the 1024 features from k0 on; `whole`: all of them are there.
+    auto codes = [&](int k0, auto whole) {
+      constexpr bool W = decltype(whole)::value;
+      uint64_t v[4][4];
+      float am[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + kVec * (32 * u + lane);
+        if (W || k < K) {
+          uint64_t w[4];
+          staged_weight8(weights, k, w);
+          times8(lds_v4(from + 2u * (uint32_t)k), w, v[u]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] = 0;
+        }
+        am[u] = amax8(v[u]);
+      }
+      if (a.y) {
+        uint4 y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) y[u] = scaled_bf16(v[u], r);
+        store_run<ALIGNED>(a.y + t * a.ldy, k0, K, y);
+      }
+      if (a.q_row) {
+        // lane l: chunk u = (l & 8 ? 2 : 0) + (l & 4 ? 1 : 0), group l / 16 of it
+        const bool up8 = (lane & 8) != 0, up4 = (lane & 4) != 0;
+        float m0 = fmaxf(up8 ? am[2] : am[0], __shfl_xor_sync(kAll, up8 ? am[0] : am[2], 8));
+        float m1 = fmaxf(up8 ? am[3] : am[1], __shfl_xor_sync(kAll, up8 ? am[1] : am[3], 8));
+        float m = fmaxf(up4 ? m1 : m0, __shfl_xor_sync(kAll, up4 ? m0 : m1, 4));
+        m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
+        m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
+        const float s = group_scale(m * r), mul = __fdiv_rn(r, s);
+        const int g = k0 / kBlock + (up8 ? 4 : 0) + (up4 ? 2 : 0) + (lane >> 4);
+        if ((lane & 3) == 0 && (W || g * kBlock < K)) a.s_row[(int64_t)g * a.lds_row + t] = s;
+        uint8_t* q = a.q_row + t * a.ldq_row;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int k = k0 + kVec * (32 * u + lane);
-          uint64_t w[4];
-          staged_weight8(weights, a.weight_f32, k, K, w);
-          times8(lds_row8<true>(from, 0, k, K), w, v[u]);
-          am[u] = amax8(v[u]);
+          const float mu = __shfl_sync(kAll, mul, (lane & 16) | (u & 2 ? 8 : 0) | (u & 1 ? 4 : 0));
+          store_codes8<W>(q, k0 + kVec * (32 * u + lane), K, v[u], mu);
         }
-        if (a.y) {
-          uint4 y[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) y[u] = scaled_bf16(v[u], r);
-          store_run<ALIGNED>(a.y + t * a.ldy, k0, K, y);
-        }
-        if (a.q_row) {
-          // lane l: chunk u = (l & 8 ? 2 : 0) + (l & 4 ? 1 : 0), group l / 16 of it
-          const bool up8 = (lane & 8) != 0, up4 = (lane & 4) != 0;
-          float m0 = fmaxf(up8 ? am[2] : am[0], __shfl_xor_sync(kAll, up8 ? am[0] : am[2], 8));
-          float m1 = fmaxf(up8 ? am[3] : am[1], __shfl_xor_sync(kAll, up8 ? am[1] : am[3], 8));
-          float m = fmaxf(up4 ? m1 : m0, __shfl_xor_sync(kAll, up4 ? m0 : m1, 4));
-          m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
-          m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
-          const float s = group_scale(m * r), mul = __fdiv_rn(r, s);
-          const int g = k0 / kBlock + (up8 ? 4 : 0) + (up4 ? 2 : 0) + (lane >> 4);
-          if ((lane & 3) == 0 && g * kBlock < K) a.s_row[(int64_t)g * a.lds_row + t] = s;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float mu = __shfl_sync(kAll, mul, (lane & 16) | (u & 2 ? 8 : 0) | (u & 1 ? 4 : 0));
-            store_codes8(a.q_row + t * a.ldq_row, k0 + kVec * (32 * u + lane), K, v[u], mu);
-          }
-        }
+      }
+    };
+    if (a.q_row || a.y) {
+      for (int k0 = 4 * 32 * kVec * sub; k0 < K; k0 += 4 * 32 * kVec * size) {
+        if (k0 + 4 * 32 * kVec <= K) codes(k0, std::true_type{});
+        else codes(k0, std::false_type{});
       }
     }
     fence_proxy_async_shared();  // this row's reads and writes of the slot, before the copy that takes it
@@ -718,7 +720,7 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS, VPT)) rms_norm_bwd_
   __shared__ int s_abort, s_asked[kBwdMaxStages];  // iterations that a stage was asked to take
   const Team team = team_of(a.team);
   const int K = (int)a.K, lane = team.lane, tid = (int)threadIdx.x, stages = a.stages;
-  const uint32_t weights = smem_u32(s_ring), ring = weights + staged_bytes(K, a.weight_f32), full = smem_u32(s_full);
+  const uint32_t weights = smem_u32(s_ring), ring = weights + (kKeep ? 0u : staged_bytes(K)), full = smem_u32(s_full);
   const uint32_t space = row_space(K, ALIGNED), part_bytes = (uint32_t)team.count * space, parts = a.dh ? 3 : 2;
   const int64_t iterations = cdiv(a.T, team.count);
   volatile int* abort_flag = &s_abort;
@@ -753,19 +755,23 @@ __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS, VPT)) rms_norm_bwd_
   if (tid < 32)
     for (int i = 0; i < stages; ++i)
       if ((int64_t)blockIdx.x + (int64_t)i * gridDim.x < iterations) issue((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
-  stage_weights(a.weight, a.weight_f32, K, weights);
-  __syncthreads();
   uint64_t kept[kKeep ? VPT : 1][4];
   if constexpr (kKeep) {
 #pragma unroll
-    for (int u = 0; u < VPT; ++u) staged_weight8(weights, a.weight_f32, kVec * (u * team.size + lane), K, kept[u]);
+    for (int u = 0; u < VPT; ++u) load_weight8<ALIGNED>(a.weight, a.weight_f32, kVec * (u * team.size + lane), K, kept[u]);
+  } else {
+    stage_weights(a.weight, a.weight_f32, K, weights);
+    __syncthreads();
   }
   auto weights8 = [&](int u, uint64_t (&w)[4]) {
     if constexpr (kKeep) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = kept[u][i];
     } else {
-      staged_weight8(weights, a.weight_f32, kVec * (u * team.size + lane), K, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = 0;
+      const int k = kVec * (u * team.size + lane);
+      if (k < K) staged_weight8(weights, k, w);
     }
   };
   float dw[VPT][8] = {};
@@ -910,7 +916,7 @@ static cudaError_t run_norm_ring(NormArgs a, int num_sms, cudaStream_t st) {
     attr_err = cudaFuncSetAttribute(rms_norm_ring_kernel<ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  const int64_t weights = staged_bytes((int)a.K, a.weight_f32), slot = (int64_t)row_space((int)a.K, ALIGNED) * (a.residual ? 2 : 1);
+  const int64_t weights = staged_bytes((int)a.K), slot = (int64_t)row_space((int)a.K, ALIGNED) * (a.residual ? 2 : 1);
   const int64_t fit = (most - weights) / slot;  // (two of the largest rows)
   a.slots = (int)(fit < kNormMaxSlots ? fit : kNormMaxSlots);
   // A warp a row where that keeps every warp busy, else four, or two where rows are short of that by little (16384 x 4096
@@ -988,7 +994,7 @@ cudaError_t launch_rms_norm_bwd(const NormBwdArgs& args, int num_sms, cudaStream
         attr_err = cudaFuncSetAttribute(rms_norm_bwd_kernel<N, V, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
       });
       if (attr_err != cudaSuccess) return attr_err;
-      const int64_t weights = staged_bytes((int)a.K, a.weight_f32);
+      const int64_t weights = V <= 2 ? 0 : staged_bytes((int)a.K);  // (kept in registers, or staged)
       const int64_t stage = N / g.team * (int64_t)row_space((int)a.K, A) * (a.dh ? 3 : 2), fit = (most - weights) / stage;
       a.stages = (int)(fit < kBwdMaxStages ? fit : kBwdMaxStages);
       return launch_pdl(rms_norm_bwd_kernel<N, V, A>, (unsigned)g.grid, N, (size_t)(weights + a.stages * stage), st, a);
