@@ -952,25 +952,26 @@ _grad_types = None
 
 
 def _grad_list(tensors, name):
-    """Types, addresses and (all contiguous or not) of a list of tensors.  (Whole lists at a time: a call's host time is
-    what its tensors' attributes cost.)"""
+    """Types, addresses and (all contiguous or not) of a list of tensors.  (Whole lists at a time, by unbound methods: a
+    call's host time is what its tensors' attributes cost.)"""
     global _grad_types
     torch = _torch()
     if _grad_types is None:
         _grad_types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     here = _here() if tensors else 0
     kinds = [_grad_types.get(t.dtype, -1) for t in tensors]
-    if -1 in kinds or {t.get_device() for t in tensors} - {here}:
+    T = torch.Tensor
+    if -1 in kinds or {*map(T.get_device, tensors)} - {here}:
         for i, t in enumerate(tensors):
             if kinds[i] < 0 or t.get_device() != here:
                 raise ValueError(f"{name}[{i}] must be a bf16, fp16 or float32 tensor on the current device cuda:{here}, got "
                                  f"{t.dtype} on {t.device}")
-    packed = all([t.is_contiguous() for t in tensors])
+    packed = all(map(T.is_contiguous, tensors))
     if not packed:
         for i, t in enumerate(tensors):
             if not (t.is_contiguous() or _dense(t)):
                 raise ValueError(f"{name}[{i}] has gaps or repeats (shape {tuple(t.shape)}, strides {t.stride()})")
-    return array("i", kinds), array("q", [t.data_ptr() for t in tensors]), packed
+    return array("i", kinds), array("q", [*map(T.data_ptr, tensors)]), packed
 
 
 def _dense(t):
@@ -995,7 +996,7 @@ def grad_norm(tensors):
     tensors = list(tensors)
     n = len(tensors)
     kinds, at, _ = _grad_list(tensors, "tensors")
-    numel = array("q", [t.numel() for t in tensors])
+    numel = array("q", [*map(_torch().Tensor.numel, tensors)])
     norm, ws, size = _grad_scratch(n, tensors[0].device if n else "cuda")
     st = lib().bfp8_grad_norm(_at(at), _at(numel), _at(kinds), n, norm.data_ptr(), ws.data_ptr(), size, _stream())
     if st:
@@ -1023,7 +1024,7 @@ def clip_grads(tensors, max_norm: float, out=None):
                 if t.shape != o.shape or not (t.is_contiguous() and o.is_contiguous() or t.stride() == o.stride()):
                     raise ValueError(f"out[{i}] must have the shape and strides of tensors[{i}], {tuple(t.shape)} "
                                      f"{t.stride()}, got {tuple(o.shape)} {o.stride()}")
-    numel = array("q", [t.numel() for t in tensors])
+    numel = array("q", [*map(_torch().Tensor.numel, tensors)])
     norm, ws, size = _grad_scratch(n, tensors[0].device if n else "cuda")
     st = lib().bfp8_clip_grads(_at(at), _at(numel), _at(kinds), n, max_norm, _at(to), _at(to_kinds), norm.data_ptr(),
                                ws.data_ptr(), size, _stream())
