@@ -19,9 +19,9 @@
 // a second pass reads h again (10 bytes an element for 8).  One launch instead (a
 // cluster of CTAs for 128 rows, which reads them again from L2 once its sums of
 // squares are joined) took 203 us for both codes of 16384 x 4096 with residual; the
-// two passes take 122: the rows' codes 83 (5.6 TB/s), the columns' 38 (5.3).  The
-// gradient takes 100 (5.4 TB/s) and the sum of its partial dw 7; a plain copy of
-// such sizes moves 6.2-6.7 TB/s.
+// two passes take 116: the rows' codes 78 (6.0 TB/s), the columns' 38 (5.3).  The
+// gradient with the sum of its partial dw takes 90 (6.0 TB/s); a plain copy of such
+// sizes moves 6.2-6.7 TB/s.
 #include <mutex>
 #include <type_traits>
 
@@ -706,10 +706,13 @@ __global__ void __launch_bounds__(256, 4) rms_norm_cols_kernel(const NormArgs a)
 
 // Gradient of every teams-th row, by teams of threads (chunks as above); the teams'
 // sums for the weight go to partial[team of the launch][K].  The rows of dy, h and dh
-// arrive by bulk copies, iterations ahead, and the weights lie in shared memory
-// (rows loaded into registers where they are used: a training step's norm, forward
-// and backward, of 16384 x 4096 265 us, so 236; with two CTAs an SM for rows up to
-// 8192, where three spilled registers, 219).
+// arrive by bulk copies, iterations ahead (rows loaded into registers where they are
+// used: a training step's norm, forward and backward, of 16384 x 4096 265 us, so 236),
+// two CTAs an SM for 2048 < K <= 4096 (three spilled registers: 229 us, two 219).  A
+// thread's weights stay in its registers up to 8192 features (from shared memory,
+// twice a row, they took more of its bandwidth than the rows: 98 us the gradient, so
+// 91); from 4096 on 512 threads a row rather than longer threads (4096 x 8192: 72 us
+// with 256, 57 with 512).
 constexpr int bwd_ctas(int threads, int vpt) { return threads > 256 ? 1 : vpt <= 1 ? 3 : 2; }  // that an SM holds
 template <int THREADS, int VPT, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS, bwd_ctas(THREADS, VPT)) rms_norm_bwd_kernel(const NormBwdArgs a) {

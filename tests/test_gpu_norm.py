@@ -80,7 +80,9 @@ def test_forward(T, K, residual, wdtype):
 
 
 @pytest.mark.parametrize("T,K,off,ld", [(200, 1024, 1, 1031), (200, 1024, 8, 1032), (180, 130, 3, 140), (1, 4096, 5, 5000),
-                                        (170, 5120, 2, 5122)])
+                                        (170, 5120, 2, 5122), (400, 2001, 7, 2011), (350, 4001, 1, 4003),
+                                        (300, 7003, 5, 7003), (200, 16383, 3, 16384), (5000, 513, 3, 513),
+                                        (1200, 1024, 4, 1024), (700, 1026, 6, 1027)])
 def test_parts_of_larger_buffers(T, K, off, ld):
     """Rows inside larger buffers: what lies around them is neither read as data (NaN there) nor written."""
     g = gen(T + K)
@@ -112,7 +114,7 @@ def test_parts_of_larger_buffers(T, K, off, ld):
     check_backward(dyp, h, w, o.rstd, dhp)
 
 
-@pytest.mark.parametrize("K", [1000, 1003])
+@pytest.mark.parametrize("K", [1000, 1003, 4101, 9001])
 @pytest.mark.parametrize("which", ["x", "residual"])
 def test_sum_in_place(K, which):
     x, r, w = make(400, K, 3, True)
