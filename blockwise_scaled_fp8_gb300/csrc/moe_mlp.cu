@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
       mbar_init(tempty0 + 8 * i, 4);
     }
     for (int i = 0; i < kMlpMaxBuffers; ++i) {
-      mbar_init(hfull0 + 8 * i, kCoders);
+      mbar_init(hfull0 + 8 * i, 32 * kCoders);
       mbar_init(hempty0 + 8 * i, 4);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
       for (int r = 0; r < experts2 && ok; ++r) {
         ok = __all_sync(kAll, mbar_wait_bounded(hfull0 + 8 * h.at, h.parity, 2 * kWaitLimitNs, abort_flag));
         if (!ok && lane == 0) fail(4u);
+        fence_proxy_async_shared();  // (codes that cp.async brought: no thread waited for them but by the barrier)
         for (int j = 0; j < items2 && ok; ++j, ++n)
           if (n % kIssuers == me) issue(area + (uint32_t)((h.at * Ib + j * blocks2) * NT * kAtom), idesc2);
         h.step(1, a.buffers);
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
           const float s = code8(p, q, lo, hi);
           if (in) {
             *reinterpret_cast<uint2*>(a.codes + (int64_t)g * kBlock + 8 * l16) = make_uint2(lo, hi);
-            if (l16 == 0) a.scales[g] = s;
+            if (l16 == 0) a.scales[g] = s * s_weight[slot];  // (the promotion wants the product)
           }
         }
         named_sync(3, 32 * kCoders);
@@ -702,40 +703,22 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
           return false;
         };
         const int first = s_start[r], of_expert = __popc(mask) * Ib;
-        const int turn0 = (coder % size) * 32 + lane;
         if (shared_codes) {
-          // codes as they are: 16 bytes a lane, eight lanes a group
-          for (int i0 = 0; i0 < 8 * of_expert; i0 += kActBatch * 32 * size) {
-            uint4 v[kActBatch];
-#pragma unroll
-            for (int i = 0; i < kActBatch; ++i) {
-              const int n = i0 + i * 32 * size + turn0, g = n >> 3, c = g / Ib;
-              if (g < of_expert)
-                v[i] = __ldcg(reinterpret_cast<const uint4*>(
-                    a.codes + ((int64_t)(s_slot[first + c] & 0xFFFF) * Ib + (g - c * Ib)) * kBlock + 16 * (n & 7)));
-            }
-            // and a group's scale a lane: as many groups a batch as the team has lanes
-            static_assert(kActBatch == 8, "a lane a group");
-            const int gs = i0 / 8 + turn0, cs = gs / Ib;
-            float sc = 0.0f;
-            int slot_s = 0;
-            if (gs < of_expert) {
-              slot_s = s_slot[first + cs];
-              sc = __ldcg(a.scales + (int64_t)(slot_s & 0xFFFF) * Ib + (gs - cs * Ib)) * s_weight[slot_s & 0xFFFF];
-            }
-            if (i0 == 0 && !(ok = buffer_free())) break;
-#pragma unroll
-            for (int i = 0; i < kActBatch; ++i) {
-              const int n = i0 + i * 32 * size + turn0, g = n >> 3, c = g / Ib, blk = g - c * Ib;
-              if (g < of_expert) {
-                const int t = s_slot[first + c] >> 16;
-                const uint32_t to = codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 + (((n & 7) ^ (t & 7)) << 4));
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
-                             : "memory");
-              }
-            }
-            if (gs < of_expert) scales[(gs - cs * Ib) * NC + (slot_s >> 16)] = sc;
+          // Codes as they are: 16 bytes a lane, eight lanes a group, and its scale.  They pass no registers and nobody waits
+          // for them here, so a team's next expert is under way while they land.
+          if (!(ok = buffer_free())) break;
+          const int sub = lane & 7;
+          int c = 0, blk = 4 * (coder % size) + (lane >> 3);  // of the next group: token of the expert, K-block
+          for (;; blk += 4 * size) {
+            while (blk >= Ib) blk -= Ib, ++c;
+            if (c * Ib + blk >= of_expert) break;
+            const int slot = s_slot[first + c], t = slot >> 16, g = (slot & 0xFFFF) * Ib + blk;
+            cp_async_16(codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 + ((sub ^ (t & 7)) << 4)),
+                        a.codes + (int64_t)g * kBlock + 16 * sub, 16u);
+            if (sub == 0) cp_async_4(smem_u32(scales + blk * NC + t), a.scales + g, 4u);
           }
+          __syncwarp();
+          for (int i = 0; i < kCoders / size; ++i) cp_async_mbar_arrive(hfull0 + 8 * at.at);
         } else {
           int c = h / Ib, blk = h - c * Ib;  // of the half's next group: token of the expert, K-block
           for (int g0 = 0; g0 < of_expert; g0 += kActBatch * halves) {
@@ -773,13 +756,13 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
               }
             }
           }
+          if (!ok) break;
+          fence_proxy_async_shared();
+          for (int i = 0; i < kCoders / size; ++i) mbar_arrive(hfull0 + 8 * at.at);  // as many a team, whatever its size
         }
-        if (!ok) break;
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane < kCoders / size) mbar_arrive(hfull0 + 8 * at.at);  // as many arrivals a team, whatever its size
         for (int i = 0; i < teams; ++i) at.step(1, a.buffers);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
   __syncwarp();
