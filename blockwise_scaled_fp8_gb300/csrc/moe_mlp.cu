@@ -74,11 +74,6 @@ constexpr int kMlpThreads = 512;
 constexpr int kProducers = 3;       // warps 0, 14, 15
 constexpr int kIssuers = 2;         // warps 1, 3
 constexpr int kCoders = 6;          // warps 8-13
-constexpr int kActBatch = 8;        // groups of 128 activations that half a warp of them loads at once
-// Groups a CTA from which on the CTAs share the coding.  Shared / each for itself, us: 64 experts of 3 x 2048 x 4096, 8 a token:
-// 2 tokens (1.7 groups a CTA) 72.8 / 71.8, 3 tokens 91.3 / 93.2, 4 tokens 110.5 / 114.5, 8 tokens 151 / 175, 16 tokens 211 / 251;
-// 128 of 3 x 704 x 1920, 6 a token: 5 tokens (1.2) 36.1 / 38.0, 16 tokens 77 / 87.
-constexpr int kSharedGroups = 1;
 constexpr int kStageBytes = 128 * kBlock;
 constexpr int kPairs = 16;          // gate (and up) rows of a unit
 constexpr int kUnitRows = 2 * kPairs, kUnitBlocks = 128 / kUnitRows;  // K-blocks of a stage of the first part
@@ -330,7 +325,6 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
   const int group = a.group, blocks2 = 128 / group;                         // `group` rows of `blocks2` K-blocks a stage
   const int items2 = (int)cdiv(Ib, blocks2);
   const int experts2 = n0 < a.N ? reached : 0;
-  const bool shared_codes = slots * Ib >= kSharedGroups * grid;             // the CTAs share the activations' coding
   auto fail = [&](uint32_t code) {
     if (!*abort_flag) atomicOr(&g_mlp_error, code);
     *abort_flag = 1;
@@ -644,15 +638,13 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
             a.y[(int64_t)t * a.ldy + n0 + i] = (uint16_t)(pack_bf16x2(sum, 0.0f) & 0xFFFFu);
           }
       }
-    } else if (experts2 > 0 || (shared_codes && reached > 0)) {
+    } else if (reached > 0) {
       // ------------------------------------------------------------ the activations' codes
-      // Teams of the six warps take an expert each, in turn: six teams, three where an expert's tokens have more groups
-      // than a warp loads at once, and no more teams than buffers (a team that is a whole turn of the
-      // buffers ahead of another could not tell the phases of their barriers apart).
+      // Teams of the six warps take an expert each, in turn: six teams or three, but no more of them than buffers (a team
+      // that is a whole turn of the buffers ahead of another could not tell the phases of their barriers apart), and all
+      // six warps an expert where there are two buffers or one (16 tokens of 64 experts: 213.3 us with two teams, 211.5).
       const int coder = warp - 8;
-      const int want = slots * Ib > 2 * kActBatch * reached ? 3 : 6, most = min(want, a.buffers);
-      const int teams = most >= 6 ? 6 : min(most, 3), size = kCoders / teams;
-      const int h = 2 * (coder % size) + (lane >> 4), halves = 2 * size;
+      const int teams = a.buffers <= 2 ? 1 : a.buffers < kCoders ? 3 : kCoders, size = kCoders / teams;
       bool ok = true;
       // until every CTA has arrived (one warp asks: more of them hold the arrivals up)
       auto wait_arrived = [&](const uint32_t* count) {
@@ -664,32 +656,30 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
       if (coder == 0 && !wait_arrived(a.arrived) && lane == 0) fail(16u);
       named_sync(3, 32 * kCoders);
       ok = !*abort_flag;
-      if (shared_codes) {
-        // this CTA's share of the groups: every (grid x 2 kCoders)-th, half a warp each
-        for (int g0 = 0; g0 < slots * Ib; g0 += grid * 2 * kCoders) {
-          const int g = g0 + (2 * coder + (lane >> 4)) * grid + cta, slot = g / Ib, blk = g - slot * Ib, k = blk * kBlock + 8 * l16;
-          float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q = p;
-          const bool in = ok && g < slots * Ib;
-          if (in && k < a.I) {  // (a slot without an expert: whatever was there, and not read)
-            const float4* from = reinterpret_cast<const float4*>(a.act + (int64_t)slot * a.I + k);
-            p = __ldcg(from);
-            q = __ldcg(from + 1);
-          }
-          uint32_t lo, hi;
-          const float s = code8(p, q, lo, hi);
-          if (in) {
-            *reinterpret_cast<uint2*>(a.codes + (int64_t)g * kBlock + 8 * l16) = make_uint2(lo, hi);
-            if (l16 == 0) a.scales[g] = s * s_weight[slot];  // (the promotion wants the product)
-          }
+      // this CTA's share of the groups: every (grid x 2 kCoders)-th, half a warp each
+      for (int g0 = 0; g0 < slots * Ib; g0 += grid * 2 * kCoders) {
+        const int g = g0 + (2 * coder + (lane >> 4)) * grid + cta, slot = g / Ib, blk = g - slot * Ib, k = blk * kBlock + 8 * l16;
+        float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q = p;
+        const bool in = ok && g < slots * Ib;
+        if (in && k < a.I) {  // (a slot without an expert: whatever was there, and not read)
+          const float4* from = reinterpret_cast<const float4*>(a.act + (int64_t)slot * a.I + k);
+          p = __ldcg(from);
+          q = __ldcg(from + 1);
         }
-        named_sync(3, 32 * kCoders);
-        if (coder == 0) {
-          if (lane == 0 && ok) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.arrived + 1) : "memory");
-          if (!wait_arrived(a.arrived + 1) && lane == 0) fail(16u);
+        uint32_t lo, hi;
+        const float s = code8(p, q, lo, hi);
+        if (in) {
+          *reinterpret_cast<uint2*>(a.codes + (int64_t)g * kBlock + 8 * l16) = make_uint2(lo, hi);
+          if (l16 == 0) a.scales[g] = s * s_weight[slot];  // (the promotion wants the product)
         }
-        named_sync(3, 32 * kCoders);
-        ok = !*abort_flag;
       }
+      named_sync(3, 32 * kCoders);
+      if (coder == 0) {
+        if (lane == 0 && ok) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.arrived + 1) : "memory");
+        if (!wait_arrived(a.arrived + 1) && lane == 0) fail(16u);
+      }
+      named_sync(3, 32 * kCoders);
+      ok = !*abort_flag;
       Ring at{0, 0};  // expert r's buffer
       int r = coder / size;
       for (int i = 0; i < r; ++i) at.step(1, a.buffers);
@@ -703,63 +693,21 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
           return false;
         };
         const int first = s_start[r], of_expert = __popc(mask) * Ib;
-        if (shared_codes) {
-          // Codes as they are: 16 bytes a lane, eight lanes a group, and its scale.  They pass no registers and nobody waits
-          // for them here, so a team's next expert is under way while they land.
-          if (!(ok = buffer_free())) break;
-          const int sub = lane & 7;
-          int c = 0, blk = 4 * (coder % size) + (lane >> 3);  // of the next group: token of the expert, K-block
-          for (;; blk += 4 * size) {
-            while (blk >= Ib) blk -= Ib, ++c;
-            if (c * Ib + blk >= of_expert) break;
-            const int slot = s_slot[first + c], t = slot >> 16, g = (slot & 0xFFFF) * Ib + blk;
-            cp_async_16(codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 + ((sub ^ (t & 7)) << 4)),
-                        a.codes + (int64_t)g * kBlock + 16 * sub, 16u);
-            if (sub == 0) cp_async_4(smem_u32(scales + blk * NC + t), a.scales + g, 4u);
-          }
-          __syncwarp();
-          for (int i = 0; i < kCoders / size; ++i) cp_async_mbar_arrive(hfull0 + 8 * at.at);
-        } else {
-          int c = h / Ib, blk = h - c * Ib;  // of the half's next group: token of the expert, K-block
-          for (int g0 = 0; g0 < of_expert; g0 += kActBatch * halves) {
-            float4 v[kActBatch][2];
-            const int c0 = c, blk0 = blk;
-#pragma unroll
-            for (int i = 0; i < kActBatch; ++i) {
-              if (g0 + i * halves < of_expert) {  // (of some half of the team)
-                const int k = blk * kBlock + 8 * l16;
-                v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (g0 + i * halves + h < of_expert && k < a.I) {
-                  const float4* p = reinterpret_cast<const float4*>(a.act + (int64_t)(s_slot[first + c] & 0xFFFF) * a.I + k);
-                  v[i][0] = __ldcg(p);
-                  v[i][1] = __ldcg(p + 1);
-                }
-                for (blk += halves; blk >= Ib; blk -= Ib) ++c;
-              }
-            }
-            if (g0 == 0 && !(ok = buffer_free())) break;  // the values are on their way when the buffer is asked for
-            c = c0, blk = blk0;
-#pragma unroll
-            for (int i = 0; i < kActBatch; ++i) {
-              if (g0 + i * halves < of_expert) {
-                const float4 p = v[i][0], q = v[i][1];
-                uint32_t lo, hi;
-                const float s = code8(p, q, lo, hi);
-                if (g0 + i * halves + h < of_expert) {
-                  const int slot = s_slot[first + c], t = slot >> 16;
-                  const uint32_t to = codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 +
-                                                         (((l16 >> 1) ^ (t & 7)) << 4) + 8 * (l16 & 1));
-                  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(to), "r"(lo), "r"(hi) : "memory");
-                  if (l16 == 0) scales[blk * NC + t] = s * s_weight[slot & 0xFFFF];
-                }
-                for (blk += halves; blk >= Ib; blk -= Ib) ++c;
-              }
-            }
-          }
-          if (!ok) break;
-          fence_proxy_async_shared();
-          for (int i = 0; i < kCoders / size; ++i) mbar_arrive(hfull0 + 8 * at.at);  // as many a team, whatever its size
+        // Codes as they are: 16 bytes a lane, eight lanes a group, and its scale.  They pass no registers and nobody waits
+        // for them here, so a team's next expert is under way while they land.
+        if (!(ok = buffer_free())) break;
+        const int sub = lane & 7;
+        int c = 0, blk = 4 * (coder % size) + (lane >> 3);  // of the next group: token of the expert, K-block
+        for (;; blk += 4 * size) {
+          while (blk >= Ib) blk -= Ib, ++c;
+          if (c * Ib + blk >= of_expert) break;
+          const int slot = s_slot[first + c], t = slot >> 16, g = (slot & 0xFFFF) * Ib + blk;
+          cp_async_16(codes + (uint32_t)((blk * NT + (t >> 3)) * kAtom + (t & 7) * 128 + ((sub ^ (t & 7)) << 4)),
+                      a.codes + (int64_t)g * kBlock + 16 * sub, 16u);
+          if (sub == 0) cp_async_4(smem_u32(scales + blk * NC + t), a.scales + g, 4u);
         }
+        __syncwarp();
+        for (int i = 0; i < kCoders / size; ++i) cp_async_mbar_arrive(hfull0 + 8 * at.at);
         for (int i = 0; i < teams; ++i) at.step(1, a.buffers);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
