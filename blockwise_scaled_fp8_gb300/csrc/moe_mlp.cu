@@ -12,12 +12,14 @@
 //     that holds most of shared memory, first its share of the gate and up rows,
 //     then of the down rows;
 //   - the exchange of the activations between the two (every CTA needs all of
-//     them) is a barrier over the grid that only the warps behind the ring wait
-//     for: the down weights do not depend on it and fill the ring meanwhile.  The
-//     activations pass in fp32 and each CTA codes them for itself; where they are
-//     many, each CTA codes its share, and a second barrier hands out the codes (16
-//     tokens, 8 of 64 experts: coding all of them took a CTA as long as reading its
-//     weights, 251 us in all).
+//     them) is two barriers over the grid that only the warps behind the ring wait
+//     for: the down weights do not depend on them and fill the ring meanwhile.  The
+//     activations pass in fp32; each CTA codes its share behind the first barrier,
+//     and takes everyone's codes behind the second, by cp.async straight into the
+//     operand's place (each CTA coding all of them for itself, with one barrier: one
+//     token 43.5 us against 43.8, but 16 tokens of 64 experts 248 against 213, whose
+//     coding took a CTA as long as reading its weights; codes by way of registers:
+//     16 tokens of 128 narrow experts 76 us against 64).
 //
 // First part: a unit is 16 gate rows and the 16 up rows of the same features; the
 // units of all reached experts are shared evenly.  Second part: CTA c takes the
@@ -40,16 +42,17 @@
 //   warp 2         the weights' scales, into slots ahead of the products (loaded where
 //                  they are used they cost a trip to L2 a stage)
 //   warps 4-7      promotion: lane l of warp w is row 32 w + l of the 128
-//   warps 8-13     the activations' codes, experts ahead of the products: one to six
-//                  warps an expert, as many experts at once as there are buffers
+//   warps 8-13     the activations' codes: this CTA's share of their coding, then each
+//                  expert's into its buffer, ahead of the products: one, two or all
+//                  six warps an expert, no more experts at once than buffers
 // Producers and issuers are whole warps that stay together, of which an elected lane
 // issues: a lane that left the others took 326 cycles for the four MMAs and two commits
 // of a stage, an elected one 252.
 //
 // Measured (with the router's launch; the floor is the reached experts' codes at the
-// rate of a plain copy): 64 experts of 3 x 2048 x 4096, 8 a token: one token 45 us
-// (floor 30), 4 tokens 111 (99), 16 tokens 212 (212); 128 of 3 x 704 x 1920, 6 a
-// token, 5 tokens 36 (16.5).  What is left at few tokens does not grow with the
+// rate of a plain copy): 64 experts of 3 x 2048 x 4096, 8 a token: one token 44 us
+// (floor 30), 4 tokens 109 (99), 16 tokens 213 (212); 128 of 3 x 704 x 1920, 6 a
+// token, 5 tokens 34 (16.5).  What is left at few tokens does not grow with the
 // weights: the router's launch, the plan, the tokens' codes and the exchange of the
 // activations.
 //

@@ -408,8 +408,7 @@ BFP8_API bfp8_status bfp8_gemm_routed_1x128_128x128(const void *qa, int64_t lda,
  *   ws  device, bfp8_moe_mlp_workspace_size(T, k, I) bytes, 16-byte aligned:
  *       one call's at a time
  * The second launch is a cooperative one: its CTAs, one a multiprocessor, wait
- * for one another once, or twice where the activations are many.  Every wait is
- * bounded (bfp8_check_device_errors).
+ * for one another twice.  Every wait is bounded (bfp8_check_device_errors).
  */
 BFP8_API size_t bfp8_moe_mlp_workspace_size(int64_t T, int64_t k, int64_t I);
 BFP8_API bfp8_status bfp8_moe_mlp_decode(const void *x, int64_t T, int64_t K, int64_t ldx, const void *logits,
