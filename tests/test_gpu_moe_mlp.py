@@ -190,6 +190,19 @@ def test_near_the_five_launches():
     assert float((y.float() - z.float()).norm() / z.float().norm()) < 0.03
 
 
+@pytest.mark.parametrize("T,E,k,K,I,N", [(1, 16, 8, 1024, 512, 1024), (16, 64, 8, 1024, 512, 1024), (16, 8, 2, 2048, 2048, 2048),
+                                         (5, 64, 6, 1920, 704, 1920), (12, 8, 2, 512, 4096, 512), (7, 32, 4, 384, 192, 4096)])
+def test_many_runs_in_a_row(T, E, k, K, I, N):
+    """The same bits of calls that follow one another without a pause, on inputs in turn."""
+    layer = Layer(E, K, I, N)
+    sets = [layer.inputs(T) for _ in range(3)]
+    first = [layer(x, logits, k) for x, logits in sets]
+    got = [layer(*sets[i % 3], k) for i in range(90)]
+    B.check_device_errors()
+    assert all(torch.equal(y, first[i % 3]) for i, y in enumerate(got))
+    assert all(bool(torch.isfinite(y.float()).all()) and float(y.float().abs().max()) > 0 for y in first)
+
+
 def test_captured_replayed_and_concurrent():
     layer, other = Layer(16, 512, 256, 512), Layer(8, 256, 128, 256, seed=3)
     x, logits = layer.inputs(4)
