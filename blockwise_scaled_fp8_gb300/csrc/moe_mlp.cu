@@ -77,6 +77,10 @@ constexpr int kMlpThreads = 512;
 constexpr int kProducers = 3;       // warps 0, 14, 15
 constexpr int kIssuers = 2;         // warps 1, 3
 constexpr int kCoders = 6;          // warps 8-13
+// Warps that wait for a buffer of activations, all of which have seen its codes before it is coded again: promotion's, and
+// both issuers, also where an expert is one stage and so one issuer's alone (the other could find the barrier two phases
+// on, whose parity is that of codes that are not there yet, and wait for good).
+constexpr int kBufferReaders = 4 + kIssuers;
 constexpr int kStageBytes = 128 * kBlock;
 constexpr int kPairs = 16;          // gate (and up) rows of a unit
 constexpr int kUnitRows = 2 * kPairs, kUnitBlocks = 128 / kUnitRows;  // K-blocks of a stage of the first part
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
     }
     for (int i = 0; i < kMlpMaxBuffers; ++i) {
       mbar_init(hfull0 + 8 * i, 32 * kCoders);
-      mbar_init(hempty0 + 8 * i, 4);
+      mbar_init(hempty0 + 8 * i, kBufferReaders);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(sfull0 + 8 * i, 32);  // one cp.async arrival a lane
@@ -419,6 +423,7 @@ __global__ void __launch_bounds__(kMlpThreads, 1)
         ok = __all_sync(kAll, mbar_wait_bounded(hfull0 + 8 * h.at, h.parity, 2 * kWaitLimitNs, abort_flag));
         if (!ok && lane == 0) fail(4u);
         fence_proxy_async_shared();  // (codes that cp.async brought: no thread waited for them but by the barrier)
+        if (ok && lead) mbar_arrive(hempty0 + 8 * h.at);  // seen (promotion's arrivals wait for the products)
         for (int j = 0; j < items2 && ok; ++j, ++n)
           if (n % kIssuers == me) issue(area + (uint32_t)((h.at * Ib + j * blocks2) * NT * kAtom), idesc2);
         h.step(1, a.buffers);
