@@ -145,8 +145,9 @@ __device__ __forceinline__ float code8(const float4& p, const float4& q, uint32_
 #pragma unroll
   for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
   const float s = scale_near(m), y = recip_rn(s);
-  lo = cvt_e4m3x2(p.x * y, p.y * y) | cvt_e4m3x2(p.z * y, p.w * y) << 16;
-  hi = cvt_e4m3x2(q.x * y, q.y * y) | cvt_e4m3x2(q.z * y, q.w * y) << 16;
+  // (quotients, not products with y: those take the other code of a tie for one in nine of the values next to it)
+  lo = cvt_e4m3x2(quotient(p.x, s, y), quotient(p.y, s, y)) | cvt_e4m3x2(quotient(p.z, s, y), quotient(p.w, s, y)) << 16;
+  hi = cvt_e4m3x2(quotient(q.x, s, y), quotient(q.y, s, y)) | cvt_e4m3x2(quotient(q.z, s, y), quotient(q.w, s, y)) << 16;
   return s;
 }
 // C consecutive 32-bit columns of this warp's 32 lanes of tensor memory.

@@ -393,9 +393,10 @@ BFP8_API bfp8_status bfp8_gemm_routed_1x128_128x128(const void *qa, int64_t lda,
  *   a[t,j] = silu(G_e q(x[t])) * (U_e q(x[t]))       e = idx[t,j], fp32
  *   y[t]   = sum over j of w[t,j] D_e q(a[t,j])      (a slot with idx -1 adds nothing)
  * q quantises in 1x128 groups, q(a) from fp32 values that were not rounded
- * before; its scale is the product max(amax, 1e-12) * fl(1/448), within an ulp
- * of bfp8_quant_lhs's quotient (codes of x/s that lie at a tie of two codes for
- * one of the two scales may differ), its codes RNE_e4m3(x/s).  The products are those of
+ * before.  The scale of both is the product max(amax, 1e-12) * fl(1/448), within
+ * an ulp of bfp8_quant_lhs's quotient (a value that lies at a tie of two codes for
+ * one of the two scales may get the other code: of normally distributed bf16 tokens
+ * about one in 850), the codes are RNE_e4m3(x/s), x/s rounded to fp32.  The products are those of
  * bfp8_gemm_1x128_128x128 with fp32 results, and y is rounded once.  The same
  * inputs give the same bits.
  *   x   device bf16 [T,K], 0 <= T <= 16, ldx >= K;  y device bf16 [T,N], ldy >= N
