@@ -878,7 +878,8 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* partial,
       for (int j = 0; j < kLoads; ++j) add(v[j]);
     }
   }
-  s[warp][lane] = sum + lost;
+  // (where the sum became infinite, what was lost is a difference of infinities: NaN)
+  s[warp][lane] = fabsf(sum) < INFINITY ? sum + lost : sum;
   __syncthreads();
   float v = s[lane][warp];  // column `warp` of the CTA, over its 32 sums
 #pragma unroll
