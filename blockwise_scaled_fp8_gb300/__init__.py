@@ -839,6 +839,12 @@ def _here():
     return _torch()._C._cuda_getDevice()
 
 
+def _written(*tensors):
+    """Counts a write in place for autograd (kernels write through addresses, which torch does not see): a graph that saved
+    one of the tensors refuses to go backward."""
+    _torch().autograd.graph.increment_version(tensors)
+
+
 def _rows(t, name, shape, here):
     """The row stride of a bf16 tensor of that shape on device `here`, rows apart from one another."""
     n, k = shape
@@ -868,7 +874,8 @@ def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, rows: bool = Tru
     [T, K], residual bf16, weight [K] bf16 or fp32), quantised in 1x128 groups
     (``rows``) and 128x1 groups (``cols``), or in bf16 (``out``), from one pass;
     y is not rounded before its quantisation.  ``h`` (default: a new tensor) takes
-    the sum; it may be x or residual.  See bfp8_rms_norm_quant."""
+    the sum; it may be x or residual, and counts as written in place for autograd.  See
+    bfp8_rms_norm_quant."""
     torch = _torch()
     if x.dim() != 2:
         raise ValueError(f"x must be a 2-D tensor, got shape {tuple(x.shape)}")
@@ -879,17 +886,18 @@ def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, rows: bool = Tru
     f32 = _norm_weight(weight, K, here)
     dev, u8, fp, bf = x.device, torch.uint8, torch.float32, torch.bfloat16
     empty = torch.empty
+    given = h is not None
     at_r = at_h = at_q = at_s = at_qc = at_sc = at_y = None
     ldr = ldh = ldq = ldqc = ldsc = 0
     q = s = qc = sc = y = None
     if residual is not None:
         ldr, at_r = _rows(residual, "residual", shape, here), residual.data_ptr()
-        if h is None:
-            h, ldh = empty(shape, dtype=bf, device=dev), max(K, 1)
-        else:
+        if given:
             ldh = _rows(h, "h", shape, here)
+        else:
+            h, ldh = empty(shape, dtype=bf, device=dev), max(K, 1)
         at_h = h.data_ptr()
-    elif h is not None:
+    elif given:
         raise ValueError("h takes x + residual: it needs a residual")
     else:
         h = x
@@ -911,6 +919,8 @@ def rms_norm_quant(x, weight, residual=None, eps: float = 1e-6, rows: bool = Tru
                                    rstd.data_ptr(), at_q, ldq, at_s, max(T, 1), at_qc, ldqc, at_sc, ldsc, at_y, K, _stream())
     if st:
         _check(st)
+    if given:
+        _written(h)
     return NormOut(h, rstd, q, s, qc, sc, y)
 
 
@@ -1007,7 +1017,8 @@ def grad_norm(tensors):
 def clip_grads(tensors, max_norm: float, out=None):
     """Scales the tensors by min(1, max_norm / (norm + 1e-6)) with their
     grad_norm, in place or into the tensors ``out`` (bf16, fp16 or fp32, of the
-    same shapes and strides: an optimizer's own buffers).  Returns the norm
+    same shapes and strides: an optimizer's own buffers); what it writes counts as
+    written in place for autograd, also where the factor is 1.  Returns the norm
     before, an fp32 scalar on the device; nothing waits for it."""
     tensors = list(tensors)
     n = len(tensors)
@@ -1030,6 +1041,7 @@ def clip_grads(tensors, max_norm: float, out=None):
                                ws.data_ptr(), size, _stream())
     if st:
         _check(st)
+    _written(*(tensors if out is None else out))
     return norm
 
 
