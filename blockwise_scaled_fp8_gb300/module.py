@@ -89,6 +89,12 @@ class Float8BlockwiseLinear(torch.nn.Module):
         return f"in_features={self.in_features}, out_features={self.out_features}, bias=False"
 
 
+def _packed(t: torch.Tensor) -> torch.Tensor:
+    """t [T, C] with its rows one after another, also where a size is 0 or 1, for which torch calls any strides contiguous
+    (an expanded gradient's are 0)."""
+    return t if t.stride() == (t.shape[1], 1) else t.clone(memory_format=torch.contiguous_format)
+
+
 class _BlockwiseFp8NormLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, norm_weight, residual, eps):
@@ -104,10 +110,12 @@ class _BlockwiseFp8NormLinear(torch.autograd.Function):
     def backward(ctx, dy, dh=None):
         q_col, s_col, qwt, sw, h, rstd, norm_weight = ctx.saved_tensors
         T, N = dy.shape
-        qd, sd, qdt, sdt = quant_dual(dy.to(torch.bfloat16).contiguous())
+        qd, sd, qdt, sdt = quant_dual(_packed(dy.to(torch.bfloat16)))
         dn = gemm_1x128_128x128(qd, sd, qwt, sw, N, sb_transposed=True)
-        dw = gemm_1x128_128x1(qdt, sdt, q_col, s_col, T) if ctx.needs_input_grad[1] else None
-        dx, dnorm = rms_norm_bwd(dn, h, norm_weight, rstd, dh=None if dh is None else dh.to(torch.bfloat16).contiguous())
+        dw = None
+        if ctx.needs_input_grad[1]:  # (no rows: no product, whose operands are empty)
+            dw = gemm_1x128_128x1(qdt, sdt, q_col, s_col, T) if T else h.new_zeros(N, h.shape[1])
+        dx, dnorm = rms_norm_bwd(dn, h, norm_weight, rstd, dh=None if dh is None else _packed(dh.to(torch.bfloat16)))
         return dx, dw, dnorm.to(norm_weight.dtype), dx if ctx.streams else None, None
 
 
@@ -123,12 +131,12 @@ def blockwise_fp8_norm_linear(x: torch.Tensor, weight: torch.Tensor, norm_weight
             (residual is not None and residual.shape != x.shape):
         raise ValueError(f"blockwise_fp8_norm_linear: x is {tuple(x.shape)}, weight {tuple(weight.shape)}, norm_weight "
                          f"{tuple(norm_weight.shape)}, residual {None if residual is None else tuple(residual.shape)}")
-    x2 = x.reshape(-1, K).contiguous()
+    x2 = _packed(x.reshape(-1, K))
     if residual is None:
         y = _BlockwiseFp8NormLinear.apply(x2, weight.contiguous(), norm_weight.contiguous(), None, eps)
         return y.reshape(*lead, weight.shape[0]), x
     y, h = _BlockwiseFp8NormLinear.apply(x2, weight.contiguous(), norm_weight.contiguous(),
-                                         residual.reshape(-1, K).contiguous(), eps)
+                                         _packed(residual.reshape(-1, K)), eps)
     return y.reshape(*lead, weight.shape[0]), h.reshape(x.shape)
 
 
