@@ -404,8 +404,8 @@ __device__ __forceinline__ void finish_row(const NormArgs& a, const Team& team, 
 }
 
 // One row a team of threads, each thread VPT chunks of eight features (chunk u of a
-// thread starts at feature 8 (u size + lane)): few rows, and rows that are not
-// 16-byte aligned.
+// thread starts at feature 8 (u size + lane)): no more rows than SMs, or fewer than
+// 512 features.
 template <int THREADS, int VPT, bool VEC>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 4 : THREADS <= 512 ? 2 : 1) rms_norm_kernel(const NormArgs a) {
   __shared__ float s_slots[THREADS / 32];
@@ -912,7 +912,7 @@ static cudaError_t run_norm(const NormArgs& a, int64_t grid, cudaStream_t st) {
 }
 
 template <bool ALIGNED>
-static cudaError_t run_norm_ring(NormArgs a, int num_sms, cudaStream_t st) {
+static cudaError_t run_norm_ring(NormArgs a, int num_sms, cudaStream_t st) {  // more rows than SMs
   constexpr int64_t most = 220 * 1024;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
@@ -927,7 +927,7 @@ static cudaError_t run_norm_ring(NormArgs a, int num_sms, cudaStream_t st) {
   // with residual, 12 slots: one warp 83.1 us, two 86.3, four 81.3; 4096 x 8192, 5 slots: two 56.7, four 46.4; without
   // residual, 11: two 30.7, four 32.3).
   a.team = a.slots >= kNormWarps ? 1 : a.slots >= kNormWarps / 2 && !a.residual ? 2 : 4;
-  return launch_pdl(rms_norm_ring_kernel<ALIGNED>, (unsigned)(a.T < num_sms ? a.T : num_sms), 32 * kNormWarps,
+  return launch_pdl(rms_norm_ring_kernel<ALIGNED>, (unsigned)num_sms, 32 * kNormWarps,
                     (size_t)(weights + a.slots * slot), st, a);
 }
 
@@ -942,15 +942,8 @@ static cudaError_t norm_rows(NormArgs a, int num_sms, cudaStream_t st) {
     return K <= 8192 ? run_norm<1024, 1>(a, a.T, st) : run_norm<1024, 2>(a, a.T, st);
   }
   if (K >= 512 && a.T > num_sms) return norm_vec(a) ? run_norm_ring<true>(a, num_sms, st) : run_norm_ring<false>(a, num_sms, st);
-  auto go = [&](auto threads, auto vpt) {
-    constexpr int N = decltype(threads)::value, V = decltype(vpt)::value;
-    a.team = team_size(K, V, N);
-    return run_norm<N, V>(a, cdiv(a.T, N / a.team), st);
-  };
-  if (K <= 2048) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-  if (K <= 4096) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (K <= 8192) return go(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
-  return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+  a.team = team_size(K, 1, 256);  // several rows a CTA: K <= 2048
+  return run_norm<256, 1>(a, cdiv(a.T, 256 / a.team), st);
 }
 
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t st) {
