@@ -20,8 +20,9 @@
 // What bounds it is memory: every element is read for the norm, and read again
 // and written for the clipping, since the norm has to be known first.  The
 // second pass walks each run backwards: what the first one read last is still
-// in L2.  1.2e9 bf16 elements: 1.10 ms for 7.2 GB, 6.5 TB/s; the norm alone of 150M
-// mixed ones 65 us, 6.1 TB/s; 2M elements in 40 tensors 16 us.
+// in L2 (50 MB of 600 at 300M bf16 elements).  1.2e9 bf16 elements: 1.10 ms for
+// 7.2 GB, 6.5 TB/s; the norm alone of 150M mixed ones 65 us, 6.1 TB/s; 2M elements
+// in 40 tensors 16 us.
 #include <string.h>
 
 #include "common.cuh"

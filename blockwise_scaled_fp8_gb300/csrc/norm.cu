@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(32 * kNormWarps, 1) rms_norm_ring_kernel(const
 
 // Codes along the columns, from h and rstd: a CTA a 128 x 128 tile, a thread eight
 // columns of 2 x 4 rows.  The row blocks are taken last first: what the rows' pass
-// wrote last is still in L2.
+// wrote last is still in L2 (30 MB of the 134 of 16384 x 4096).
 template <bool VEC>
 __global__ void __launch_bounds__(256, 4) rms_norm_cols_kernel(const NormArgs a) {
   __shared__ float s_max[8][kBlock], s_mul[kBlock], s_r[kBlock];

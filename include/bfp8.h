@@ -436,7 +436,7 @@ BFP8_API bfp8_status bfp8_moe_mlp_decode(const void *x, int64_t T, int64_t K, in
  *   (weight_f32 != 0) [K]; rstd device fp32 [T], gets r; codes, scales, strides
  *   as bfp8_quant_dual's; y device bf16 [T,K], no memory of x, residual or h.
  *   K <= 16384.  Rows that are 16-byte aligned (K and strides multiples of 8)
- *   are fastest; any others are allowed.
+ *   are fastest; any others are allowed.  T == 0 or K == 0 writes nothing.
  */
 BFP8_API bfp8_status bfp8_rms_norm_quant(const void *x, int64_t T, int64_t K, int64_t ldx, const void *residual,
                                          int64_t ldr, const void *weight, int weight_f32, float eps, void *h,
